@@ -305,7 +305,8 @@ def _run_own(s):
         return dict(table=s["table"], left=s["left"], cu=s["cu"], pos=s["pos"], seq=s["rseq"], slots=s["slots"])
     pool = kvr.Kv4Layout(s["data"], s["table"])
     if op == "decode":
-        return kvr.full_attn_decode_kv4(s["q"], s["pos"], s["seq"], pool, s["rope"], SCALE, s["max_ctx"])
+        most = min(s["max_ctx"], pool.max_blocks * pool.block_size)  # ragged: the longest drawn may be shorter than the range's end
+        return kvr.full_attn_decode_kv4(s["q"], s["pos"], s["seq"], pool, s["rope"], SCALE, most)
     if op == "append":
         T, hkv = s["k"].shape[:2]
         rows = kvr.LinearLayout.empty(T, hkv)
