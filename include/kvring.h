@@ -71,6 +71,7 @@ enum {
 #define KVR_DEV_TIMEOUT 8u    /* a kernel gave up waiting on its own pipeline (bounded wait) and returned */
 #define KVR_DEV_BAD_ROWS 16u  /* varlen: cu_rows not non-decreasing within [0, T]; that chunk is skipped */
 #define KVR_DEV_FREE_FULL 32u /* kv_pages_release_window: the free list could not take the released ids */
+#define KVR_DEV_NO_BLOCKS 64u /* kv_pages_grow: the free list holds fewer blocks than the step needs */
 
 /* KV storage kinds. */
 enum {
@@ -114,6 +115,39 @@ typedef struct kvr_kv_layout {
   int32_t num_blocks;          /* PAGED */
   int64_t num_rows;            /* LINEAR */
 } kvr_kv_layout;
+
+/*
+ * A full layer's pool in 4 bits: 182 bytes per (position, KV head) where the
+ * bf16 pages take 640 (no counterpart on the pages: Xiaomi section 1.2 has
+ * decode bound by the KV bytes read, and this reads fewer).  K (RoPE applied)
+ * and V (value scale applied) are kept as 4-bit codes u in groups of 64 dims
+ * -- K's dims 0..63 (the rotary ones), 64..127, 128..191; V's 0..63, 64..127
+ * -- each group with an fp16 scale s and minimum m: its values are m + s * u.
+ *   data [num_blocks][Hkv][block_size / 16][2912] bytes, 16-byte aligned: one
+ *   tile of 2912 bytes per 16 consecutive positions of a KV head, position r
+ *   of the tile (r = position % 16) at
+ *     K codes   byte    0 + 512 g + 64 (r % 8) + 16 t + 8 (r / 8) + i / 2:
+ *               dim 64 g + 16 t + i (i < 16), even dims in the low half
+ *     V codes   byte 1536 + 512 g + 64 a + 16 ((r / 2) % 4) + 8 (r / 8)
+ *               + 4 w + 2 (r % 2) + i / 2: dim 64 g + 8 a + 4 w + i (i < 4)
+ *     K scales  fp16 at byte 2560 + 32 g + 2 c, c = 4 ((r / 2) % 4) + 2 (r / 8) + r % 2
+ *     V scales  fp16 at byte 2656 + 32 g + 2 c
+ *     V minima  fp16 at byte 2720 + 32 g + 2 c
+ *     K minima  fp16 at byte 2784 + 8 r + 2 g (the fourth is zero);
+ *   block_table [num_seqs][max_blocks] int32: position p of sequence s lies in
+ *   block block_table[s][p / block_size], at p % block_size.
+ * block_size is a multiple of 16 in [16, 1024].  The data needs no
+ * initialisation: what no append wrote is never used.
+ */
+typedef struct kvr_kv4_layout {
+  int32_t num_kv_heads;
+  int32_t num_seqs;
+  int32_t max_blocks;
+  int32_t block_size;
+  int32_t num_blocks;
+  uint8_t *data;
+  const int32_t *block_table;
+} kvr_kv4_layout;
 
 /*
  * Every call that launches work looks up, on its first use on a device (and
@@ -453,6 +487,101 @@ kvr_status swa_sink_prefill_varlen(const kvr_bf16 *q, const int32_t *cu_rows, co
                                    const float *sinks, const float *rope_cos_sin, int64_t max_pos,
                                    float softmax_scale, void *workspace, size_t workspace_bytes,
                                    kvr_bf16 *out, void *stream);
+
+/*
+ * Page growth: the block tables and slot maps of a batch's next step, built
+ * on the device from the requests' lengths (Xiaomi "Full-Pipeline Inference
+ * Optimization", section 2.1: the Full pool grows on demand), the other half
+ * of kv_pages_release_window.  Request i (i < n) is sequence seqs[i], holds
+ * lens[i] positions and gains add[i] >= 0 tokens at positions lens[i] .. .
+ *   block_table [num_seqs][max_blocks] int32 (read and written): entries bi
+ *     with ceil(lens/block_size) <= bi < ceil((lens + add)/block_size) get new
+ *     blocks; the entries below them are read, no other is touched;
+ *   free_ids [free_cap], free_count_in [1] int32: the free list.  The k-th
+ *     block the call takes, in (request, entry) order, is
+ *     free_ids[*free_count_in - 1 - k]; *free_count_out [1] receives the
+ *     remaining count and may be the same word (free_ids is left as it is).
+ * and, for the step's own calls, with rows in request order:
+ *   cu_rows [n+1] int32: request i owns rows cu_rows[i] .. cu_rows[i+1]-1 (as
+ *     the varlen calls and kv4_unpack take them, with lens as their P0);
+ *   pos [T] int64, row_seq [T] int32, slots [T] int64: each row's position,
+ *     sequence, and slot = block id * block_size + position % block_size (what
+ *     kv4_append_rope takes).  Rows past the last token get -1 in all three, so
+ *     a captured step of T rows serves any batch of at most T tokens.
+ * A request with a sequence id outside [0, num_seqs) (KVR_DEV_BAD_SEQ), or
+ * with lens or add negative or lens + add past max_blocks*block_size
+ * (KVR_DEV_BAD_POS), gets no rows and no blocks.  A free id or a table entry
+ * in use that is no block id of the pool sets KVR_DEV_BAD_BLOCK: its table
+ * entry becomes -1 (a new one) and its rows' slots are -1.  If the batch has
+ * more than T rows (KVR_DEV_BAD_ROWS) or needs more blocks than are free
+ * (KVR_DEV_NO_BLOCKS), the step is empty: cu_rows is all zero, every row -1,
+ * the table and the count are unchanged.  No two requests may name the same
+ * sequence.  n <= 8192 (KVR_EUNSUPPORTED).  One launch; block_size >= 1.
+ */
+kvr_status kv_pages_grow(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, const int32_t *seqs, const int64_t *lens, const int32_t *add, int32_t n,
+                         const int32_t *free_ids, const int32_t *free_count_in, int32_t *free_count_out,
+                         int32_t free_cap, int32_t *cu_rows, int64_t *pos, int32_t *row_seq, int64_t *slots, int64_t T,
+                         void *stream);
+
+/*
+ * kv_ring_append_rope into a 4-bit pool: RoPE on k's first 64 dims and the
+ * value scale on v in fp32 (each product and sum rounded), then, per group of
+ * 64 dims with fp32 values x,
+ *   m = min x rounded down to fp16, s = (max x - m) / 15 rounded up to fp16,
+ *   u = clamp(rint((x - m) / s), 0, 15), ties to even; s = 0 gives u = 0.
+ * m and s saturate at +-65504.  A group holding a NaN or an infinity is
+ * stored with m = s = NaN: every read of it gives NaN.
+ * Where token t goes is named either by seq [T] int32 and the pool's block
+ * table (slots NULL), or by slots [T] int64 (seq NULL): block id * block_size
+ * + row, as kv_pages_grow makes them.  seq[t] = -1, or a negative slot, marks
+ * padding: the token is skipped and nothing is flagged.  A position outside
+ * the table (KVR_DEV_BAD_POS), a sequence id outside the layout
+ * (KVR_DEV_BAD_SEQ), a table entry or slot outside the pool
+ * (KVR_DEV_BAD_BLOCK): the token is skipped.  Two tokens of one call must not
+ * go to the same place.  T = 0 is a no-op.
+ */
+kvr_status kv4_append_rope(const kvr_bf16 *k, const kvr_bf16 *v, const int64_t *pos, const int32_t *seq,
+                           const int64_t *slots, int32_t T, int32_t Hkv, const float *rope_cos_sin, int64_t max_pos,
+                           float value_scale, const kvr_kv4_layout *dst, void *stream);
+
+/* Workspace bytes for full_attn_decode_kv4 (0 on bad arguments). */
+size_t full_attn_decode_kv4_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int64_t max_ctx);
+
+/*
+ * full_attn_decode over a 4-bit pool: the token at pos[b] of sequence seq[b]
+ * attends positions 0..pos[b], whose values are the ones the codes stand for.
+ * Arguments, bounds, flags and results as full_attn_decode (q is rotated in
+ * fp32 and not rounded to bf16; a block outside the pool masks its keys).
+ * Several rows of one call may name the same sequence: the C draft tokens of a
+ * verification are B * C rows with their own positions, once all of them are
+ * appended.  workspace: full_attn_decode_kv4_workspace_size(B, Hq, Hkv,
+ * max_ctx) bytes, 16-byte aligned, no initialisation; calls that may overlap
+ * on the GPU need workspaces of their own.
+ */
+kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
+                                const kvr_kv4_layout *pool, const float *rope_cos_sin, int64_t max_pos,
+                                float softmax_scale, int64_t max_ctx, void *workspace, size_t workspace_bytes,
+                                kvr_bf16 *out, void *stream);
+
+/*
+ * Positions of a 4-bit pool as bf16 (one rounding of m + s * u), into pages or
+ * rows: with them full_attn_prefill_chunk and full_attn_prefill_varlen go on
+ * from a prefix kept in 4 bits.  Entry i (i < n) is positions lo[i] ..
+ * lo[i] + cu_rows[i+1] - cu_rows[i] - 1 of sequence src_seqs[i], written to
+ *   PAGED   the same positions of sequence dst_seqs[i] of dst;
+ *   LINEAR  rows cu_rows[i] .. cu_rows[i+1]-1 (dst_seqs may be NULL,
+ *           dst->num_rows >= T).
+ * src_seqs [n] int32, lo [n] int64, cu_rows [n+1] int32, dst_seqs [n] int32
+ * are device arrays; cu_rows must be non-decreasing within [0, T] (an entry
+ * that is not is skipped with KVR_DEV_BAD_ROWS, and entries after it may be
+ * skipped too).  Positions that cannot be read (KVR_DEV_BAD_POS,
+ * KVR_DEV_BAD_SEQ, KVR_DEV_BAD_BLOCK) are written as zeros, except that a
+ * negative or too large lo writes no page; a destination that cannot be
+ * addressed is flagged and not written.  n = 0 or T = 0 is a no-op.
+ */
+kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                      int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);
 
 #ifdef __cplusplus
 }

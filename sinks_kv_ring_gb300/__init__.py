@@ -17,6 +17,16 @@ gaudi-cookbook "MiMo-V2.6-Flash on Gaudi 2", "What was built"):
 and the batched forms of the two prefill calls, ``swa_sink_prefill_varlen``
 and ``full_attn_prefill_varlen``: n chunks of different lengths in one call
 (multi-token-prediction draft verification, mixed prefill/decode batches).
+
+A full layer's pool may be kept in 4 bits (``Kv4Layout``):
+
+  kv4_append_rope         the KV write into it
+  full_attn_decode_kv4    one token over it
+  kv4_unpack              positions of it back to bf16 pages or rows
+
+and ``kv_pages_grow`` builds a step's block tables and slot map on the device
+from the requests' lengths, taking blocks from the free list that
+``kv_pages_release_window`` fills.
 """
 from __future__ import annotations
 
@@ -33,12 +43,16 @@ __all__ = [
     "kv_ring_snapshot", "kv_ring_restore", "ring_snapshot_alloc",
     "full_attn_prefill_varlen", "swa_sink_prefill_varlen", "full_attn_prefill_varlen_workspace_size",
     "swa_sink_prefill_varlen_workspace_size",
+    "Kv4Layout", "kv4_append_rope", "full_attn_decode_kv4", "full_attn_decode_kv4_workspace_size", "kv4_unpack",
+    "kv_pages_grow",
     "DQK", "DV", "DROT", "WINDOW",
 ]
 
 DQK, DV, DROT, WINDOW = 192, 128, 64, 128
 LAYOUT_RING, LAYOUT_PAGED, LAYOUT_LINEAR = 1, 2, 3
 DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_BLOCK, DEV_TIMEOUT, DEV_BAD_ROWS, DEV_FREE_FULL = 1, 2, 4, 8, 16, 32
+DEV_NO_BLOCKS = 64
+KV4_TILE = 2912  # bytes of 16 positions of one KV head in a 4-bit pool
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvring.so")
@@ -65,6 +79,18 @@ class _Layout(ctypes.Structure):
         ("block_size", ctypes.c_int32),
         ("num_blocks", ctypes.c_int32),
         ("num_rows", ctypes.c_int64),
+    ]
+
+
+class _Layout4(ctypes.Structure):
+    _fields_ = [
+        ("num_kv_heads", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
     ]
 
 
@@ -118,6 +144,16 @@ def lib():
                 L.kv_pages_release_window.argtypes = [p, i32, i32, i32, i32, p, p, p, i32, i32, p, p, i32, p]
                 L.kv_ring_gather_pages.restype = ctypes.c_int
                 L.kv_ring_gather_pages.argtypes = [p, p, p, p, p, i32, p]
+                L.kv_pages_grow.restype = ctypes.c_int
+                L.kv_pages_grow.argtypes = [p, i32, i32, i32, i32, p, p, p, i32, p, p, p, i32, p, p, p, p, i64, p]
+                L.kv4_append_rope.restype = ctypes.c_int
+                L.kv4_append_rope.argtypes = [p, p, p, p, p, i32, i32, p, i64, f32, p, p]
+                L.full_attn_decode_kv4_workspace_size.restype = ctypes.c_size_t
+                L.full_attn_decode_kv4_workspace_size.argtypes = [i32, i32, i32, i64]
+                L.full_attn_decode_kv4.restype = ctypes.c_int
+                L.full_attn_decode_kv4.argtypes = [p, p, p, i32, i32, p, p, i64, f32, i64, p, ctypes.c_size_t, p, p]
+                L.kv4_unpack.restype = ctypes.c_int
+                L.kv4_unpack.argtypes = [p, p, p, p, i32, i64, p, p, p]
                 _lib = L
     return _lib
 
@@ -289,6 +325,46 @@ class LinearLayout:
     def c(self):
         return _Layout(LAYOUT_LINEAR, self.num_kv_heads, self.k.data_ptr(), self.v.data_ptr(), None, None,
                        0, 0, 0, 0, self.num_rows)
+
+
+class Kv4Layout:
+    """Full pool of one layer in 4 bits: data [nblk, Hkv, Bsz / 16, 2912]
+    uint8 (tiles of 16 positions, see kvr_kv4_layout in kvring.h), block_table
+    [S, max_blocks] int32."""
+
+    def __init__(self, data, block_table):
+        _want(data, "pool.data", torch.uint8, 4)
+        _want(block_table, "pool.block_table", torch.int32, 2)
+        nb, H, tiles, nbytes = data.shape
+        if nbytes != KV4_TILE:
+            raise ValueError(f"pool.data must be [blocks, Hkv, block_size / 16, {KV4_TILE}], got {tuple(data.shape)}")
+        self.data, self.block_table = data, block_table
+        self.num_blocks, self.num_kv_heads, self.block_size = nb, H, 16 * tiles
+        self.num_seqs, self.max_blocks = block_table.shape
+
+    def tensors(self):
+        return self.data, self.block_table
+
+    @classmethod
+    def contiguous(cls, num_seqs, num_kv_heads, max_ctx, block_size=64, device="cuda", zero=True):
+        """A pool where sequence s owns blocks s*mb .. s*mb+mb-1 in order."""
+        if block_size % 16:
+            raise ValueError(f"block_size {block_size} is not a multiple of 16")
+        mb = (max_ctx + block_size - 1) // block_size
+        nb = num_seqs * mb
+        alloc = torch.zeros if zero else torch.empty
+        data = alloc(nb, num_kv_heads, block_size // 16, KV4_TILE, dtype=torch.uint8, device=device)
+        bt = torch.arange(nb, dtype=torch.int32, device=device).reshape(num_seqs, mb)
+        return cls(data, bt)
+
+    @staticmethod
+    def bytes_per_token(num_kv_heads):
+        """Pool bytes one token adds per layer."""
+        return num_kv_heads * KV4_TILE // 16
+
+    def c(self):
+        return _Layout4(self.num_kv_heads, self.num_seqs, self.max_blocks, self.block_size, self.num_blocks,
+                        self.data.data_ptr(), self.block_table.data_ptr())
 
 
 def rope_table(theta: float, max_pos: int, device="cuda", nthreads: int = 0) -> torch.Tensor:
@@ -546,6 +622,128 @@ def kv_ring_gather_pages(pages, ring, src_seqs, dst_seqs, end, stream=None):
     pc, rc = pages.c(), ring.c()
     _check(lib().kv_ring_gather_pages(ctypes.byref(pc), ctypes.byref(rc), _ptr(src_seqs), _ptr(dst_seqs), _ptr(end),
                                       n, _stream(stream)))
+
+
+def kv_pages_grow(block_table, num_blocks, block_size, seqs, lens, add, free_ids, free_count, cu_rows, pos, row_seq,
+                  slots, free_count_out=None, stream=None):
+    """The block tables and slot map of a step in which request i (sequence
+    seqs[i], int32 [n]) holds lens[i] (int64) positions and gains add[i]
+    (int32) tokens: the blocks they need are taken from the end of the free
+    list (free_ids int32 [cap], free_count int32 [1]) and written to
+    block_table (int32 [num_seqs, max_blocks]); cu_rows (int32 [n + 1]) and the
+    rows' pos (int64 [T]), row_seq (int32 [T]) and slots (int64 [T]) are filled
+    (-1 past the last token).  The remaining count goes to free_count_out
+    (default: free_count itself).  Everything stays on the device."""
+    _want(block_table, "block_table", torch.int32, 2)
+    _want(seqs, "seqs", torch.int32, 1)
+    _want(lens, "lens", torch.int64, 1)
+    _want(add, "add", torch.int32, 1)
+    _want(free_ids, "free_ids", torch.int32, 1)
+    _want(free_count, "free_count", torch.int32, 1)
+    _want(cu_rows, "cu_rows", torch.int32, 1)
+    _want(pos, "pos", torch.int64, 1)
+    _want(row_seq, "row_seq", torch.int32, 1)
+    _want(slots, "slots", torch.int64, 1)
+    if free_count_out is None:
+        free_count_out = free_count
+    _want(free_count_out, "free_count_out", torch.int32, 1)
+    S, mb = block_table.shape
+    n, T = seqs.shape[0], pos.shape[0]
+    _want_len(lens, "lens", n)
+    _want_len(add, "add", n)
+    _want_len(cu_rows, "cu_rows", n + 1)
+    _want_len(row_seq, "row_seq", T)
+    _want_len(slots, "slots", T)
+    _want_len(free_count, "free_count", 1)
+    _want_len(free_count_out, "free_count_out", 1)
+    _same_device(block_table, seqs, lens, add, free_ids, free_count, free_count_out, cu_rows, pos, row_seq, slots)
+    _check(lib().kv_pages_grow(_ptr(block_table), S, mb, int(block_size), int(num_blocks), _ptr(seqs), _ptr(lens),
+                               _ptr(add), n, _ptr(free_ids), _ptr(free_count), _ptr(free_count_out),
+                               free_ids.shape[0], _ptr(cu_rows), _ptr(pos), _ptr(row_seq), _ptr(slots), T,
+                               _stream(stream)))
+
+
+def kv4_append_rope(k, v, pos, seq, table, value_scale, dst, slots=None, stream=None):
+    """kv_ring_append_rope into a 4-bit pool (Kv4Layout).  Token t goes to
+    position pos[t] of sequence seq[t], or, with seq None, to slot slots[t]
+    (block id * block_size + row, int64, as kv_pages_grow makes them).  seq -1
+    or a negative slot marks padding."""
+    _want(k, "k", torch.bfloat16, 3)
+    _want(v, "v", torch.bfloat16, 3)
+    _want(pos, "pos", torch.int64, 1)
+    if (seq is None) == (slots is None):
+        raise ValueError("exactly one of seq and slots names where the tokens go")
+    if seq is not None:
+        _want(seq, "seq", torch.int32, 1)
+        _want_len(seq, "seq", k.shape[0])
+    else:
+        _want(slots, "slots", torch.int64, 1)
+        _want_len(slots, "slots", k.shape[0])
+    _want_table(table)
+    T, H = k.shape[0], k.shape[1]
+    if tuple(k.shape) != (T, H, DQK) or tuple(v.shape) != (T, H, DV) or pos.shape[0] != T:
+        raise ValueError("k/v/pos shapes disagree")
+    _same_device(k, v, pos, seq, slots, table, *dst.tensors())
+    c = dst.c()
+    _check(lib().kv4_append_rope(_ptr(k), _ptr(v), _ptr(pos), _ptr(seq), _ptr(slots), T, H, _ptr(table),
+                                 table.shape[0], float(value_scale), ctypes.byref(c), _stream(stream)))
+
+
+def full_attn_decode_kv4_workspace_size(B, Hq, Hkv, max_ctx) -> int:
+    return int(lib().full_attn_decode_kv4_workspace_size(int(B), int(Hq), int(Hkv), int(max_ctx)))
+
+
+def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, workspace=None, out=None, stream=None):
+    """full_attn_decode over a 4-bit pool (Kv4Layout).  Rows may share a
+    sequence (draft tokens at their own positions)."""
+    _want_q(q)
+    _want(pos, "pos", torch.int64, 1)
+    _want(seq, "seq", torch.int32, 1)
+    _want_table(table)
+    B, Hq, _ = q.shape
+    _want_len(pos, "pos", B)
+    _want_len(seq, "seq", B)
+    if workspace is None:
+        n = full_attn_decode_kv4_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    _want(workspace, "workspace", torch.uint8, 1)
+    out = _out(out, B, Hq, q)
+    _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
+    c = pool.c()
+    _check(lib().full_attn_decode_kv4(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),
+                                      table.shape[0], float(softmax_scale), int(max_ctx), _ptr(workspace),
+                                      workspace.numel(), _ptr(out), _stream(stream)))
+    return out
+
+
+def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=None):
+    """Positions lo[i] .. lo[i] + cu_rows[i+1] - cu_rows[i] - 1 of sequence
+src_seqs[i] of a 4-bit pool as bf16: into the same positions of sequence
+    dst_seqs[i] of a PagedLayout, or into rows cu_rows[i] .. of a LinearLayout.
+    T bounds the rows of the call (cu_rows' last entry; the launch is sized by
+    it); by default it is all that dst holds."""
+    _want(src_seqs, "src_seqs", torch.int32, 1)
+    _want(lo, "lo", torch.int64, 1)
+    _want(cu_rows, "cu_rows", torch.int32, 1)
+    n = src_seqs.shape[0]
+    _want_len(lo, "lo", n)
+    _want_len(cu_rows, "cu_rows", n + 1)
+    if isinstance(dst, LinearLayout):
+        most = dst.num_rows
+    elif isinstance(dst, PagedLayout):
+        if dst_seqs is None:
+            raise ValueError("dst_seqs names the sequences of a PagedLayout")
+        most = min(dst.num_seqs * dst.max_blocks * dst.block_size, 2 ** 31 - 1)
+    else:
+        raise TypeError("dst must be a PagedLayout or a LinearLayout")
+    T = most if T is None else int(T)
+    if dst_seqs is not None:
+        _want(dst_seqs, "dst_seqs", torch.int32, 1)
+        _want_len(dst_seqs, "dst_seqs", n)
+    _same_device(src_seqs, lo, cu_rows, dst_seqs, *src.tensors(), *dst.tensors())
+    sc, dc = src.c(), dst.c()
+    _check(lib().kv4_unpack(ctypes.byref(sc), _ptr(src_seqs), _ptr(lo), _ptr(cu_rows), n, T, _ptr(dst_seqs),
+                            ctypes.byref(dc), _stream(stream)))
 
 
 def debug_stall_next(launches: int, limit_ns: int) -> None:

@@ -187,6 +187,30 @@ kvr_status check_layout(const kvr_kv_layout *L, int want_kind, const char *name)
   return KVR_OK;
 }
 
+kvr::Kv4View view4(const kvr_kv4_layout &L) {
+  kvr::Kv4View v;
+  v.data = L.data;
+  v.block_table = L.block_table;
+  v.hkv = L.num_kv_heads;
+  v.num_seqs = L.num_seqs;
+  v.max_blocks = L.max_blocks;
+  v.block_size = L.block_size;
+  v.num_blocks = L.num_blocks;
+  return v;
+}
+
+kvr_status check_kv4(const kvr_kv4_layout *L, const char *name) {
+  if (!L) return fail(KVR_EINVAL, "%s: layout is NULL", name);
+  if (L->num_kv_heads < 1) return fail(KVR_EINVAL, "%s: num_kv_heads %d", name, L->num_kv_heads);
+  if (!L->data || !L->block_table) return fail(KVR_EINVAL, "%s: data/block_table is NULL", name);
+  if (!aligned16(L->data)) return fail(KVR_EINVAL, "%s: data not 16-byte aligned", name);
+  if (L->num_seqs < 1 || L->max_blocks < 1 || L->num_blocks < 1)
+    return fail(KVR_EINVAL, "%s: num_seqs/max_blocks/num_blocks must be >= 1", name);
+  if (L->block_size < 16 || L->block_size > 1024 || L->block_size % 16)
+    return fail(KVR_EUNSUPPORTED, "%s: block_size %d (needs a multiple of 16 in [16, 1024])", name, L->block_size);
+  return KVR_OK;
+}
+
 kvr_status check_table(const float *table, int64_t max_pos) {
   if (!table) return fail(KVR_EINVAL, "rope_cos_sin is NULL");
   if (!aligned16(table)) return fail(KVR_EINVAL, "rope_cos_sin not 16-byte aligned");
@@ -224,7 +248,7 @@ unsigned long long take_stall() {
 }
 
 namespace {
-constexpr int MAX_KSLOT = 16;
+constexpr int MAX_KSLOT = 24;
 unsigned char g_smem_done[MAX_DEV][MAX_KSLOT];
 void *g_smem_ctx[MAX_DEV];  // the context g_smem_done[dev] is for
 }  // namespace
@@ -584,6 +608,112 @@ kvr_status kv_ring_gather_pages(const kvr_kv_layout *pages, const kvr_kv_layout 
   if (e != cudaSuccess) return state_fail(e, "kv_ring_gather_pages");
   e = kvr::launch_ring_gather(view(*pages), view(*ring), src_seqs, dst_seqs, end, n, st, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_ring_gather_pages launch");
+  return ok();
+}
+
+kvr_status kv_pages_grow(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, const int32_t *seqs, const int64_t *lens, const int32_t *add, int32_t n,
+                         const int32_t *free_ids, const int32_t *free_count_in, int32_t *free_count_out,
+                         int32_t free_cap, int32_t *cu_rows, int64_t *pos, int32_t *row_seq, int64_t *slots, int64_t T,
+                         void *stream) {
+  const char *who = "kv_pages_grow";
+  if (n < 0 || T < 0 || T > INT32_MAX) return fail(KVR_EINVAL, "%s: n %d, T %lld", who, n, (long long)T);
+  if (num_seqs < 1 || max_blocks < 1 || num_blocks < 1 || block_size < 1)
+    return fail(KVR_EINVAL, "%s: num_seqs/max_blocks/num_blocks/block_size must be >= 1", who);
+  if (free_cap < 0) return fail(KVR_EINVAL, "%s: free_cap %d", who, free_cap);
+  if (!block_table || !free_count_in || !free_count_out || !cu_rows)
+    return fail(KVR_EINVAL, "%s: block_table/free_count_in/free_count_out/cu_rows is NULL", who);
+  if (n > kvr::GROW_MAX_N) return fail(KVR_EUNSUPPORTED, "%s: n %d > %d", who, n, kvr::GROW_MAX_N);
+  if (n > 0 && (!seqs || !lens || !add)) return fail(KVR_EINVAL, "%s: seqs/lens/add is NULL", who);
+  if (free_cap > 0 && !free_ids) return fail(KVR_EINVAL, "%s: free_ids is NULL", who);
+  if (T > 0 && (!pos || !row_seq || !slots)) return fail(KVR_EINVAL, "%s: pos/row_seq/slots is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_pages_grow(block_table, num_seqs, max_blocks, block_size, num_blocks, seqs, lens, add, n, free_ids,
+                             free_count_in, free_count_out, free_cap, cu_rows, pos, row_seq, slots, T, st,
+                             as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_pages_grow launch");
+  return ok();
+}
+
+kvr_status kv4_append_rope(const kvr_bf16 *k, const kvr_bf16 *v, const int64_t *pos, const int32_t *seq,
+                           const int64_t *slots, int32_t T, int32_t Hkv, const float *rope_cos_sin, int64_t max_pos,
+                           float value_scale, const kvr_kv4_layout *dst, void *stream) {
+  if (T < 0) return fail(KVR_EINVAL, "T %d", T);
+  kvr_status s = check_kv4(dst, "dst");
+  if (s) return s;
+  if (Hkv != dst->num_kv_heads) return fail(KVR_EINVAL, "Hkv %d != dst->num_kv_heads %d", Hkv, dst->num_kv_heads);
+  if ((s = check_table(rope_cos_sin, max_pos))) return s;
+  if (T == 0) return ok();
+  if (!k || !v || !pos) return fail(KVR_EINVAL, "k/v/pos is NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(KVR_EINVAL, "k/v not 16-byte aligned");
+  if (!seq == !slots) return fail(KVR_EINVAL, "exactly one of seq and slots names where the tokens go");
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, "kv4_append_rope");
+  e = kvr::launch_kv4_append(k, v, pos, seq, slots, T, rope_cos_sin, max_pos, value_scale, view4(*dst), st,
+                             as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_append_rope launch");
+  return ok();
+}
+
+size_t full_attn_decode_kv4_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int64_t max_ctx) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_ctx < 1) return 0;
+  return kvr::kv4_decode_workspace(B, Hq, Hkv, max_ctx);
+}
+
+kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
+                                const kvr_kv4_layout *pool, const float *rope_cos_sin, int64_t max_pos,
+                                float softmax_scale, int64_t max_ctx, void *workspace, size_t workspace_bytes,
+                                kvr_bf16 *out, void *stream) {
+  if (B < 0) return fail(KVR_EINVAL, "B %d", B);
+  kvr_status s = check_kv4(pool, "pool");
+  if (s) return s;
+  if ((s = check_heads(Hq, pool->num_kv_heads, 16))) return s;
+  if ((s = check_table(rope_cos_sin, max_pos))) return s;
+  if (max_ctx < 1 || max_ctx > max_pos)
+    return fail(KVR_ERANGE, "max_ctx %lld outside [1, max_pos=%lld]", (long long)max_ctx, (long long)max_pos);
+  if (max_ctx > (int64_t)pool->max_blocks * pool->block_size)
+    return fail(KVR_ERANGE, "max_ctx %lld exceeds max_blocks*block_size = %lld", (long long)max_ctx,
+                (long long)pool->max_blocks * pool->block_size);
+  if (B == 0) return ok();
+  if (!q || !pos || !seq || !out) return fail(KVR_EINVAL, "q/pos/seq/out is NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(KVR_EINVAL, "q/out not 16-byte aligned");
+  const size_t need = kvr::kv4_decode_workspace(B, Hq, pool->num_kv_heads, max_ctx);
+  if (!workspace || workspace_bytes < need)
+    return fail(KVR_EWORKSPACE, "workspace %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, need);
+  if (!aligned16(workspace)) return fail(KVR_EINVAL, "workspace not 16-byte aligned");
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, "full_attn_decode_kv4");
+  e = kvr::launch_kv4_decode(q, pos, seq, B, Hq, view4(*pool), rope_cos_sin, max_pos, softmax_scale, max_ctx,
+                             workspace, out, st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "full_attn_decode_kv4 launch");
+  return ok();
+}
+
+kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                      int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream) {
+  const char *who = "kv4_unpack";
+  kvr_status s = check_kv4(src, "src");
+  if (s) return s;
+  if ((s = check_layout(dst, 0, "dst"))) return s;
+  if (dst->kind != KVR_LAYOUT_PAGED && dst->kind != KVR_LAYOUT_LINEAR)
+    return fail(KVR_EINVAL, "dst: layout kind %d, expected PAGED or LINEAR", dst->kind);
+  if (src->num_kv_heads != dst->num_kv_heads)
+    return fail(KVR_EINVAL, "src has %d KV heads, dst %d", src->num_kv_heads, dst->num_kv_heads);
+  if (n < 0 || T < 0 || T > INT32_MAX) return fail(KVR_EINVAL, "%s: n %d, T %lld", who, n, (long long)T);
+  if (dst->kind == KVR_LAYOUT_LINEAR && dst->num_rows < T)
+    return fail(KVR_EINVAL, "LINEAR dst has %lld rows, T = %lld", (long long)dst->num_rows, (long long)T);
+  if (n == 0 || T == 0) return ok();
+  if (!src_seqs || !lo || !cu_rows) return fail(KVR_EINVAL, "%s: src_seqs/lo/cu_rows is NULL", who);
+  if (dst->kind == KVR_LAYOUT_PAGED && !dst_seqs) return fail(KVR_EINVAL, "%s: dst_seqs is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_kv4_unpack(view4(*src), src_seqs, lo, cu_rows, n, T, dst_seqs, view(*dst), st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv4_unpack launch");
   return ok();
 }
 

@@ -23,6 +23,7 @@ constexpr unsigned ST_BAD_SEQ = 2u;
 constexpr unsigned ST_BAD_BLOCK = 4u;
 constexpr unsigned ST_BAD_ROWS = 16u;
 constexpr unsigned ST_FREE_FULL = 32u;
+constexpr unsigned ST_NO_BLOCKS = 64u;
 
 // Programmatic dependent launch (kernels launched through launch_pdl).
 // pdl_wait returns once the kernel before this one on the stream has

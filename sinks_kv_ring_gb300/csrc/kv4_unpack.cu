@@ -1,0 +1,157 @@
+// kv4_unpack.cu -- positions of a 4-bit pool back to bf16, into pages or
+// rows: what the prefill and varlen calls read when a sequence kept in 4 bits
+// goes on.
+//
+// Value = m + s * u: the product is exact in fp32, the sum is rounded once to
+// fp32 and once to bf16.  Entry i of the call is cu_rows[i+1] - cu_rows[i]
+// positions from lo[i] on.  A work unit is one tile of 16 positions of one KV
+// head, taken by one warp; entry i owns units cu_rows[i] / 16 + 2i onwards
+// (an entry of n rows touches at most n / 16 + 2 tiles), so a unit finds its
+// entry by a search over cu_rows and no plan is made first.  180 bytes in,
+// 640 bytes out per (position, KV head): the stores bound it, and every lane
+// writes 16 or 32 bytes at a time, whole sectors.
+#include "kv4.cuh"
+#include "launch.h"
+
+namespace kvr {
+namespace {
+
+constexpr int K4U_WARPS = 8;
+constexpr unsigned FULLW = 0xffffffffu;
+
+// bf16 pair of two codes' values
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t a, uint32_t b, float s, float m) {
+  return pack_bf16(fmaf((float)a, s, m), fmaf((float)b, s, m));
+}
+// the 8 values of a word of codes (dim i in nibble i)
+__device__ __forceinline__ uint4 kv4_word(uint32_t w, float s, float m) {
+  return make_uint4(kv4_pair(w & 15u, (w >> 4) & 15u, s, m), kv4_pair((w >> 8) & 15u, (w >> 12) & 15u, s, m),
+                    kv4_pair((w >> 16) & 15u, (w >> 20) & 15u, s, m), kv4_pair((w >> 24) & 15u, w >> 28, s, m));
+}
+
+__global__ void __launch_bounds__(K4U_WARPS * 32)
+    kv4_unpack_kernel(Kv4View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
+                      const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
+                      KvView dst, long long units, unsigned *status) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * K4U_WARPS + (threadIdx.x >> 5);
+  const long long unit = w / src.hkv;
+  const int h = (int)(w - unit * src.hkv);
+  if (unit >= units) return;
+  // the last entry whose first unit is not past this one
+  int i = 0, hi = n;
+  while (hi - i > 1) {
+    const int mid = (i + hi) >> 1;
+    if ((long long)(cu_rows[mid] >> 4) + 2LL * mid <= unit) i = mid; else hi = mid;
+  }
+  const int c0 = cu_rows[i], c1 = cu_rows[i + 1];
+  if (c0 < 0 || c1 < c0 || c1 > T) {
+    if (lane == 0) flag(status, ST_BAD_ROWS);
+    return;
+  }
+  long long a = lo[i];
+  const int s = src_seqs[i];
+  const bool mine = lane == 0 && h == 0;
+  const long long u = unit - ((c0 >> 4) + 2LL * i);
+  if (u < 0 || c1 == c0) return;
+  // an entry that names no source has its rows written as zeros
+  bool ok = true;
+  if (a < 0 || a > (long long)src.max_blocks * src.block_size) {
+    if (mine) flag(status, ST_BAD_POS);
+    if (dst.kind != 3) return;  // (no position: no page either)
+    a = 0;
+    ok = false;
+  }
+  if (s < 0 || s >= src.num_seqs) {
+    if (mine) flag(status, ST_BAD_SEQ);
+    ok = false;
+  }
+  const long long p0 = ((a >> 4) + u) << 4;  // the first position of the unit's tile
+  const long long end = a + (c1 - c0);
+  if (p0 >= end) return;
+
+  const long long sbi = p0 / src.block_size;
+  int sblk = 0;
+  if (ok) {
+    sblk = sbi < src.max_blocks ? src.block_table[(long long)s * src.max_blocks + sbi] : -1;
+    ok = sblk >= 0 && sblk < src.num_blocks;
+    if (!ok && mine) flag(status, ST_BAD_BLOCK);
+  }
+  // destination head-row of position p0 + j: rows of a tile are `step` apart
+  long long drow;
+  long long step = 1;
+  if (dst.kind == 3) {
+    drow = ((long long)c0 + (p0 - a)) * dst.hkv + h;  // may start below the entry's first row: those positions are not written
+    step = dst.hkv;
+  } else {
+    const int ds = dst_seqs[i];
+    if (ds < 0 || ds >= dst.num_seqs) {
+      if (mine) flag(status, ST_BAD_SEQ);
+      return;
+    }
+    const long long dbi = p0 / dst.block_size;  // block sizes are multiples of 16: a tile lies in one block
+    const int dblk = dbi < dst.max_blocks ? dst.block_table[(long long)ds * dst.max_blocks + dbi] : -1;
+    if (dblk < 0 || dblk >= dst.num_blocks) {
+      if (mine) flag(status, ST_BAD_BLOCK);
+      return;
+    }
+    drow = ((long long)dblk * dst.hkv + h) * dst.block_size + (p0 - dbi * dst.block_size);
+  }
+
+  const uint8_t *tile = src.data + (ok ? kv4_tile(src, sblk, h, (int)(p0 - sbi * src.block_size)) : 0);
+  uint4 kc[KV4_KG], vc[KV4_VG];
+#pragma unroll
+  for (int g = 0; g < KV4_KG; ++g)
+    kc[g] = ok ? *reinterpret_cast<const uint4 *>(tile + g * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int g = 0; g < KV4_VG; ++g)
+    vc[g] = ok ? *reinterpret_cast<const uint4 *>(tile + KV4_OFF_V + g * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
+  auto half_at = [&](int off) -> float {
+    return ok ? __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(tile + off))) : 0.f;
+  };
+  const int q = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {  // K: positions q and q + 8, dims 16t .. of each group
+    const int r = q + 8 * nt;
+    const long long p = p0 + r;
+    if (p < a || p >= end) continue;
+    uint16_t *kd = dst.k + (drow + r * step) * DQK + 16 * t;
+#pragma unroll
+    for (int g = 0; g < KV4_KG; ++g) {
+      const float sc = half_at(KV4_OFF_KS + (g * 16 + kv4_quad(r)) * 2), mn = half_at(KV4_OFF_KM + r * 8 + g * 2);
+      uint4 *o = reinterpret_cast<uint4 *>(kd + 64 * g);
+      o[0] = kv4_word(nt ? kc[g].z : kc[g].x, sc, mn);
+      o[1] = kv4_word(nt ? kc[g].w : kc[g].y, sc, mn);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // V: positions 2t + (j & 1) + 8 (j >> 1), dims 8q .. of each group
+    const int e = j & 1, nt = j >> 1, r = 8 * nt + 2 * t + e;
+    const long long p = p0 + r;
+    if (p < a || p >= end) continue;
+    uint16_t *vd = dst.v + (drow + r * step) * DV + 8 * q;
+#pragma unroll
+    for (int g = 0; g < KV4_VG; ++g) {
+      const float sc = half_at(KV4_OFF_VS + (g * 16 + kv4_quad(r)) * 2);
+      const float mn = half_at(KV4_OFF_VM + (g * 16 + kv4_quad(r)) * 2);
+      const uint32_t w0 = nt ? vc[g].z : vc[g].x, w1 = nt ? vc[g].w : vc[g].y;
+      *reinterpret_cast<uint4 *>(vd + 64 * g) = kv4_word(__byte_perm(w0, w1, e ? 0x7632 : 0x5410), sc, mn);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_unpack(const Kv4View &src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                              int n, long long T, const int32_t *dst_seqs, const KvView &dst, unsigned *status,
+                              cudaStream_t st) {
+  const long long units = (T >> 4) + 2LL * n;
+  const long long blocks = (units * src.hkv + K4U_WARPS - 1) / K4U_WARPS;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(kv4_unpack_kernel, dim3((unsigned)blocks), dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows,
+                    n, T, dst_seqs, dst, units, status);
+}
+
+}  // namespace kvr

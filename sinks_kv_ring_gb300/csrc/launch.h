@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "kv4.cuh"
 
 namespace kvr {
 
@@ -173,6 +174,25 @@ cudaError_t launch_pages_release(int32_t *table, int num_seqs, int max_blocks, i
 cudaError_t launch_ring_gather(const KvView &pages, const KvView &ring, const int32_t *src_seqs,
                                const int32_t *dst_seqs, const int64_t *end, int n, unsigned *status,
                                cudaStream_t st);
+
+// The 4-bit pool: KV write, decode, and back to bf16 (PAGED or LINEAR dst).
+cudaError_t launch_kv4_append(const uint16_t *k, const uint16_t *v, const int64_t *pos, const int32_t *seq,
+                              const int64_t *slots, int T, const float *table, int64_t max_pos, float value_scale,
+                              const Kv4View &dst, unsigned *status, cudaStream_t st);
+size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx);
+cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
+                              const Kv4View &pool, const float *table, int64_t max_pos, float softmax_scale,
+                              long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st);
+cudaError_t launch_kv4_unpack(const Kv4View &src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                              int n, long long T, const int32_t *dst_seqs, const KvView &dst, unsigned *status,
+                              cudaStream_t st);
+
+constexpr int GROW_MAX_N = 8192;  // requests of one kv_pages_grow call (their prefix sums lie in shared memory)
+cudaError_t launch_pages_grow(int32_t *table, int num_seqs, int max_blocks, int block_size, int num_blocks,
+                              const int32_t *seqs, const int64_t *lens, const int32_t *add, int n,
+                              const int32_t *free_ids, const int32_t *count_in, int32_t *count_out, int free_cap,
+                              int32_t *cu_rows, int64_t *pos, int32_t *row_seq, int64_t *slots, long long T,
+                              unsigned *status, cudaStream_t st);
 
 int num_sms();
 
