@@ -1,132 +1,649 @@
 // kv4_decode.cu -- one-token decode over a full-attention layer kept in 4
-// bits.
+// bits: split-K with a log-sum-exp merge, as the bf16 decode.
 //
-// A key's score takes its scales out of the product,
-//   s = scale * sum_g (s_g (q_g . u_g) + m_g sum(q_g)),
-// and the values theirs: o = sum_j p_j (s_j u_j + m_j) / sum_j p_j.
+// Mathematics.  With values m + s u, a key's score takes its scales out of
+// the product, and the values theirs:
+//   score_j = sum_g s_jg (q_g . u_jg) + sum_g m_jg sum(q_g)
+//   o       = sum_j (p_j s_jg) u_jg + sum_j p_j m_jg
+// so the tensor cores multiply codes, and a scale costs one multiply per
+// (head, key, group), not one per element.  All products are m16n8k16 f16
+// with fp32 accumulators, the G query heads of one KV head as the 16 rows:
+//   * Codes as operands.  A code u masked out of a word in place, w &
+//     0x000f000f, is the pair of fp16 numbers u 2^-24 (subnormal, exact in the
+//     product), and w & 0x00f000f0 is 16 u 2^-24: two instructions give two
+//     operand registers and one shift serves the next two, 5 per 8 codes, with
+//     no conversion, no bias and no rounding.  The factor 16 of every other
+//     dim is divided out of q beforehand (K) or of the sums afterwards (V).
+//   * Queries are rotated, scaled by softmax_scale log2(e), brought by a power
+//     of two to a largest magnitude in [2^14, 2^15) per head, and rounded once
+//     to fp16 (2^-12 of a value, where the bf16 decode rounds to 2^-9).
+//   * The minima enter as one more k = 8 product, of the stored fp16 minima
+//     with sum(q_g) in two fp16 parts (22 bits), which starts the score.
+//   * Weights p 2^10 are fp16 (at most 2^14, so 2^-34 of the largest is still
+//     above fp16's least number: a long flat tail keeps its mass); p s is one
+//     packed fp16 multiply, with s brought below 2 by a power of two that
+//     follows the largest scale seen.  Both roundings are 2^-12 of a weight,
+//     eight times finer than the bf16 weights of the other decode.
+//   * sum p m and sum p come out of one more product whose columns are the
+//     two groups' minima and ones.
+// The running maximum is a reference that moves (with a rescale of the sums)
+// only when a score passes it by more than 4: the check is one vote per 32
+// keys.
 //
-// First form: one CTA per (sequence, KV head) walks the tiles of 16
-// positions; each tile's values go to shared memory in fp32, then scores,
-// online softmax and the weighted sum run on the fp32 units.
+// What bounds it.  180 bytes and 2 (192 + 128) G flops per key and KV head:
+// at G = 16 the m16n8k16 rate (600 TFLOP/s measured, 8 cycles per product and
+// SM quarter) takes 0.7 of the time the bytes take, and the masks, loads and
+// softmax of a quarter about as many issue slots, so the warps have to keep
+// both busy: each warp streams its own 32-key units through its own ring of
+// bulk copies (one copy brings a tile's codes and scales), with no barrier
+// between warps inside an item.
+#include "decode_plan.cuh"
 #include "kv4.cuh"
 #include "launch.h"
+#include "tc_ptx.cuh"
+#include "warp_attn.cuh"
 
 namespace kvr {
 namespace {
 
-constexpr int K4D_THREADS = 128;
+constexpr unsigned FULLW = 0xffffffffu;
+constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
+constexpr int K4_WARPS = 4;
+constexpr int K4_CTAS = 3;           // per SM
+constexpr int K4_STAGES = 2;
+constexpr int K4_STAGE = 2 * KV4_TILE;
+constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
+constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
+// split plan: an item's fixed cost in keys and the longest split
+constexpr long long K4_ITEM_KEYS = 700;
+constexpr long long K4_MAX_LEN = 16384 + 256;
+constexpr int K4_INLINE_MAX = 128;   // batches the split kernel plans itself
+// shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
+constexpr int K4_OFF_QX = 12 * 512;
+constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
+constexpr int K4_OFF_BAR = K4_OFF_ROW + 64;
+constexpr int K4_OFF_ABORT = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;
+constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
+constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 3) * 4 / 16 * 16 + 16;
+constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
+constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
+static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16) * 4, "merge area");
+static_assert(K4_CTAS * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
-__global__ void __launch_bounds__(K4D_THREADS)
-    kv4_decode_kernel(const uint16_t *__restrict__ q, const int64_t *__restrict__ pos, const int32_t *__restrict__ seq,
-                      int hq, int G, Kv4View pool, const float *__restrict__ table, int64_t max_pos, float scale_log2,
-                      long long max_ctx, uint16_t *__restrict__ out, unsigned *status) {
-  __shared__ float sQ[16][DQK];
-  __shared__ float sK[16][DQK + 1];
-  __shared__ float sV[16][DV];
-  __shared__ float sS[16][17];
-  __shared__ float sM[16], sL[16], sC[16];
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The query operands of one item: thread (row r, eighth c) rotates and scales
+// 24 dims of head r, the row's eight threads share its power of two and its
+// group sums.  Operand order: step 4g + j holds, for lane 4a + t, the halves
+// of dims 64 g + 16 t + 8 (j / 2) + 2 (j % 2) + {0, 4} (registers 0, 1: rows a
+// and a + 8) and + {1, 5}, divided by 16 (registers 2, 3): what masking word
+// j / 2, shifted by 8 (j % 2), leaves.
+__device__ __forceinline__ void kv4_query(const uint16_t *__restrict__ qh, int G, const float *__restrict__ cs_row,
+                                          float scale_log2, uint8_t *smem, int tid) {
+  const int r = tid >> 3, c = tid & 7;
+  float y[24];
+#pragma unroll
+  for (int i = 0; i < 24; ++i) y[i] = 0.f;
+  if (r < G) {
+    const uint16_t *qr = qh + r * DQK;
+    const uint2 lo = *reinterpret_cast<const uint2 *>(qr + 4 * c), hi = *reinterpret_cast<const uint2 *>(qr + 32 + 4 * c);
+    const uint4 g1 = *reinterpret_cast<const uint4 *>(qr + 64 + 8 * c), g2 = *reinterpret_cast<const uint4 *>(qr + 128 + 8 * c);
+    const float4 t0 = *reinterpret_cast<const float4 *>(cs_row + 8 * c), t1 = *reinterpret_cast<const float4 *>(cs_row + 8 * c + 4);
+    const float cs[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+    const uint16_t *a = reinterpret_cast<const uint16_t *>(&lo), *b = reinterpret_cast<const uint16_t *>(&hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v1 = bf2f(a[i]), v2 = bf2f(b[i]);
+      y[i] = (v1 * cs[2 * i] - v2 * cs[2 * i + 1]) * scale_log2;
+      y[4 + i] = (v2 * cs[2 * i] + v1 * cs[2 * i + 1]) * scale_log2;
+    }
+    const uint16_t *e1 = reinterpret_cast<const uint16_t *>(&g1), *e2 = reinterpret_cast<const uint16_t *>(&g2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[8 + i] = bf2f(e1[i]) * scale_log2;
+      y[16 + i] = bf2f(e2[i]) * scale_log2;
+    }
+  }
+  uint32_t mx = 0;  // largest magnitude's bits (NaN and infinity above all)
+#pragma unroll
+  for (int i = 0; i < 24; ++i) mx = max(mx, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(FULLW, mx, o));
+  // y 2^a has its largest magnitude in [2^14, 2^15); not finite, or zero: as it is
+  const int ex = (int)(mx >> 23);
+  int a = (ex == 255 || mx == 0) ? 0 : 14 + 127 - ex;
+  a = a > 126 ? 126 : a;  // (values below 2^-112 stay smaller than that)
+  const float up = __uint_as_float((uint32_t)(127 + (a > 0 ? a : 0)) << 23);   // 2^max(a, 0)
+  const float dn = a < 0 ? __uint_as_float((uint32_t)max(127 + a, 1) << 23) : 1.f;  // 2^min(a, 0)  (a >= -113)
+  float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 24; ++i) {
+    const int g = i >> 3;
+    // the thread's dims of a group: for group 0 4c..4c+3 and 32+4c.., else 8c..8c+7
+    const int d = g == 0 ? ((i & 4) ? 32 + 4 * c + (i & 3) : 4 * c + (i & 3)) : 8 * c + (i & 7);
+    const int nib = d & 7, j = ((d >> 3) & 1) * 2 + ((nib >> 1) & 1);
+    const float v = y[i] * up * dn;
+    const __half h = __float2half_rn((nib & 1) ? v * 0.0625f : v);
+    sum[g] += __half2float(h) * ((nib & 1) ? 16.f : 1.f);
+    const int at = ((g * 4 + j) * 32 + (r & 7) * 4 + (d >> 4)) * 16 + ((nib & 1) * 2 + (r >> 3)) * 4 + (nib >> 2) * 2;
+    *reinterpret_cast<__half *>(smem + at) = h;
+  }
+#pragma unroll
+  for (int g = 0; g < 3; ++g)
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum[g] += __shfl_xor_sync(FULLW, sum[g], o);
+  if (c < 4) {  // k = 2c, 2c + 1 of the minima's product: (s0, s1), (s2, 0), and the low parts of both
+    __half2 w;
+    const float s0 = (c & 1) ? sum[2] * 0x1p-24f : sum[0] * 0x1p-24f, s1 = (c & 1) ? 0.f : sum[1] * 0x1p-24f;
+    __half h0 = __float2half_rn(s0), h1 = __float2half_rn(s1);
+    if (c >= 2) {
+      h0 = __float2half_rn(s0 - __half2float(h0));
+      h1 = __float2half_rn(s1 - __half2float(h1));
+    }
+    w = __halves2half2(h0, h1);
+    *reinterpret_cast<__half2 *>(smem + K4_OFF_QX + ((r & 7) * 4 + c) * 8 + (r >> 3) * 4) = w;
+  }
+  // a score's unit: the sums hold (y . k) 2^(a - 24)
+  if (c == 0) {
+    const int e = 24 - a;  // >= -102
+    *reinterpret_cast<float *>(smem + K4_OFF_ROW + 4 * r) = __uint_as_float((uint32_t)min(max(127 + e, 1), 254) << 23);
+  }
+}
+
+struct K4Args {
+  const uint16_t *q;
+  const int64_t *pos;
+  const int32_t *seq;
+  int B, hq, G;
+  Kv4View pool;
+  const float *table;
+  int64_t max_pos;
+  float scale_log2;
+  long long max_ctx;
+  int32_t *plan;
+  float *part_ml;
+  float *part_o;
+  unsigned *status;
+  unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
+};
+
+__global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(const K4Args A) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hkv = A.pool.hkv, G = A.G;
+  const uint32_t sBase = smem_u32(smem);
+  const uint32_t sBar = sBase + K4_OFF_BAR + 8 * K4_STAGES * warp;
+  volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + K4_OFF_ABORT);
+  const uint32_t sStage = sBase + K4_OFF_STAGE + warp * K4_STAGES * K4_STAGE;
+  int32_t *sPrefix = reinterpret_cast<int32_t *>(smem + K4_OFF_PLAN);
+  if (lane == 0) {
+    for (int j = 0; j < K4_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
+    if (warp == 0) *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  const int b = blockIdx.x / pool.hkv, kv = blockIdx.x % pool.hkv;
-  uint16_t *o = out + ((long long)b * hq + (long long)kv * G) * DV;
-  const long long p = pos[b];
-  const int s = seq[b];
-  const bool bad_pos = p < 0 || p >= max_pos || p + 1 > max_ctx, bad_seq = s < 0 || s >= pool.num_seqs;
-  if (bad_pos || bad_seq) {
-    if (kv == 0 && tid == 0) flag(status, (bad_pos ? ST_BAD_POS : 0u) | (bad_seq ? ST_BAD_SEQ : 0u));
-    for (int e = tid; e < G * DV; e += K4D_THREADS) o[e] = 0;
-    return;
-  }
-  for (int e = tid; e < 16 * DQK; e += K4D_THREADS) {
-    const int g = e / DQK, d = e % DQK;
-    float x = 0.f;
-    if (g < G) {
-      const uint16_t *qr = q + ((long long)b * hq + (long long)kv * G + g) * DQK;
-      x = bf2f(qr[d]);
-      if (d < DROT) {
-        const float c = table[p * 64 + 2 * (d & 31)], sn = table[p * 64 + 2 * (d & 31) + 1];
-        x = d < HALF ? x * c - bf2f(qr[d + HALF]) * sn : x * c + bf2f(qr[d - HALF]) * sn;
-      }
-    }
-    sQ[g][d] = x * scale_log2;
-  }
-  if (tid < 16) {
-    sM[tid] = -INFINITY;
-    sL[tid] = 0.f;
-  }
-  float O[16];
-#pragma unroll
-  for (int g = 0; g < 16; ++g) O[g] = 0.f;
-  for (long long p0 = 0; p0 <= p; p0 += 16) {
-    const int blk = pool.block_table[(long long)s * pool.max_blocks + p0 / pool.block_size];
-    if (blk < 0 || blk >= pool.num_blocks) {
-      if (tid == 0) flag(status, ST_BAD_BLOCK);
-      continue;
-    }
-    const uint8_t *tile = pool.data + kv4_tile(pool, blk, kv, (int)(p0 % pool.block_size));
-    auto half_at = [&](int off) -> float {
-      return __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(tile + off)));
-    };
-    __syncthreads();
-    for (int e = tid; e < 16 * DQK; e += K4D_THREADS) {
-      const int r = e / DQK, d = e % DQK, g = d / 64, i = d % 64;
-      const int u = tile[kv4_k_at(g, r, i / 16) + (i % 16) / 2] >> (4 * (i & 1)) & 15;
-      sK[r][d] = fmaf((float)u, half_at(KV4_OFF_KS + (g * 16 + kv4_quad(r)) * 2), half_at(KV4_OFF_KM + r * 8 + g * 2));
-    }
-    for (int e = tid; e < 16 * DV; e += K4D_THREADS) {
-      const int r = e / DV, d = e % DV, g = d / 64, i = d % 64;
-      const int u = tile[kv4_v_at(g, r, i / 8, i % 8 / 4) + (i % 4) / 2] >> (4 * (i & 1)) & 15;
-      const float x = fmaf((float)u, half_at(KV4_OFF_VS + (g * 16 + kv4_quad(r)) * 2),
-                           half_at(KV4_OFF_VM + (g * 16 + kv4_quad(r)) * 2));
-      sV[r][d] = p0 + r <= p ? x : 0.f;
-    }
-    __syncthreads();
-    for (int e = tid; e < 256; e += K4D_THREADS) {
-      const int g = e >> 4, r = e & 15;
-      float x = 0.f;
-      for (int d = 0; d < DQK; ++d) x = fmaf(sQ[g][d], sK[r][d], x);
-      sS[g][r] = p0 + r <= p ? x : -INFINITY;
-    }
-    __syncthreads();
-    if (tid < 16) {
-      float m = sM[tid];
-      for (int r = 0; r < 16; ++r) m = fmaxf(m, sS[tid][r]);
-      const float base = m == -INFINITY ? 0.f : m;
-      const float c = ex2(sM[tid] - base);
-      float l = sL[tid] * c;
-      for (int r = 0; r < 16; ++r) {
-        const float w = ex2(sS[tid][r] - base);
-        sS[tid][r] = w;
-        l += w;
-      }
-      sM[tid] = m;
-      sL[tid] = l;
-      sC[tid] = c;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int g = 0; g < 16; ++g) {
-      float x = O[g] * sC[g];
-      for (int r = 0; r < 16; ++r) x = fmaf(sS[g][r], sV[r][tid], x);
-      O[g] = x;
-    }
-  }
   __syncthreads();
+
+  // the plan (see full_decode_kernel): every CTA makes it for small batches,
+  // CTA 0 stores it for the merge
+  const int32_t *prefix = A.plan + DECODE_PLAN_PREFIX;
+  int split_len, nitems;
+  if (A.B <= K4_INLINE_MAX) {
+    unsigned *st = blockIdx.x == 0 ? A.status : nullptr;
+    if (A.B <= 32) {
+      if (warp == 0) {
+        long long p = 0;
+        int s = 0;
+        if (lane < A.B) {
+          p = A.pos[lane];
+          s = A.seq[lane];
+        }
+        decode_plan_warp<K4_ITEM_KEYS, K4_MAX_LEN>(p, s, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x,
+                                                   sPrefix, st);
+      }
+      __syncthreads();
+      split_len = sPrefix[A.B + 1];
+      nitems = sPrefix[A.B + 2];
+    } else {
+      split_len = decode_plan_block<K4_WARPS * 32, K4_ITEM_KEYS, K4_MAX_LEN>(
+          A.pos, A.seq, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, &nitems, st);
+    }
+    if (blockIdx.x == 0) {
+      for (int b = tid; b <= A.B; b += blockDim.x) A.plan[DECODE_PLAN_PREFIX + b] = sPrefix[b];
+      if (tid == 0) {
+        A.plan[0] = split_len;
+        A.plan[1] = nitems;
+      }
+    }
+    prefix = sPrefix;
+  } else {
+    split_len = A.plan[0];
+    nitems = A.plan[1];
+  }
+
+  const int tpb = A.pool.block_size >> 4;
+  const int t = lane & 3, gr = lane >> 2;
+  uint32_t seen = 0;  // this warp's loads waited for so far: stage seen % K4_STAGES, phase (seen / K4_STAGES) & 1
+  uint32_t sent = 0;  // and issued
+  bool gave_up = false;
+
+  for (int w = blockIdx.x; w < nitems; w += gridDim.x) {
+    const int b = plan_find(prefix, A.B, w);
+    const int local = w - prefix[b], split = local / hkv, kv = local - split * hkv;
+    const long long p = A.pos[b];
+    const int s = A.seq[b];  // (a sequence with items has a valid position and id)
+    const int key_lo = split * split_len, key_hi = (int)min((long long)key_lo + split_len, p + 1);
+    const int nunit = (key_hi - key_lo + 31) >> 5;
+    const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
+    const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
+    if (__syncthreads_or(*abort_flag != 0)) break;  // the last item's merge area (over the stages) is free again
+    tc::fence_proxy_async_smem();
+
+    // pool tile of the tiles ahead: lane l holds tile (l & 1) of unit
+    // base + (l >> 1); -1 past the keys, -2 in a block that is none of the pool's
+    int ids = -1;
+    auto fetch_ids = [&](int base) {
+      const int key = key_lo + 32 * (warp + (base + (lane >> 1)) * K4_WARPS) + 16 * (lane & 1);
+      ids = -1;
+      if (key < key_hi) {
+        const unsigned tile = (unsigned)key >> 4, bi = (unsigned)((tile * A.tpb_mul) >> 36);
+        const int blk = bt[bi];
+        ids = -2;
+        if (blk >= 0 && blk < A.pool.num_blocks)
+          ids = (blk * hkv + kv) * tpb + (int)(tile - bi * tpb);
+        else
+          flag(A.status, ST_BAD_BLOCK);
+      }
+    };
+    auto issue = [&](int i) {
+      if ((i & 15) == 0) fetch_ids(i);
+      const int a = __shfl_sync(FULLW, ids, 2 * (i & 15)), c = __shfl_sync(FULLW, ids, 2 * (i & 15) + 1);
+      const uint32_t st = sent % K4_STAGES, bar = sBar + 8 * st, dst = sStage + st * K4_STAGE;
+      ++sent;
+      tc::mbar_expect_tx_elect(bar, ((a >= 0) + (c >= 0)) * KV4_TILE);
+      if (a >= 0) tc::bulk_load_elect(dst, A.pool.data + (long long)a * KV4_TILE, KV4_TILE, bar);
+      if (c >= 0) tc::bulk_load_elect(dst + KV4_TILE, A.pool.data + (long long)c * KV4_TILE, KV4_TILE, bar);
+      return (a >= 0 ? 1 : 0) | (c >= 0 ? 2 : 0);
+    };
+    int live[K4_STAGES];  // which tiles of a stage were loaded
 #pragma unroll
-  for (int g = 0; g < 16; ++g)
-    if (g < G) o[g * DV + tid] = f2bf(sL[g] == 0.f ? 0.f : O[g] / sL[g]);
+    for (int i = 0; i < K4_STAGES; ++i) live[i] = 0;
+#pragma unroll
+    for (int i = 0; i < K4_STAGES - 1; ++i)
+      if (i < my_n) live[i] = issue(i);
+
+    kv4_query(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, A.scale_log2, smem, tid);
+    __syncthreads();
+    const float crow0 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * gr);
+    const float crow1 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * (gr + 8));
+    const uint2 qx = lds64(sBase + K4_OFF_QX + lane * 8);
+
+    float O[16][4], E[4];
+#pragma unroll
+    for (int n = 0; n < 16; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
+    E[0] = E[1] = E[2] = E[3] = 0.f;
+    float mb0 = NEG_INF, mb1 = NEG_INF;  // the reference maximum less K4_PBIAS; -inf before the first keys
+    __half2 f2 = __float2half2_rn(32768.f);  // the power of two on the value scales
+
+    for (int i = 0; i < my_n; ++i) {
+      const int lv = live[0];
+#pragma unroll
+      for (int k = 0; k + 1 < K4_STAGES; ++k) live[k] = live[k + 1];
+      if (i + K4_STAGES - 1 < my_n) live[K4_STAGES - 2] = issue(i + K4_STAGES - 1);
+      const uint32_t st = seen % K4_STAGES;
+      const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
+      if (!got) {
+        gave_up = true;
+        break;
+      }
+      ++seen;
+      const int key0 = key_lo + 32 * (warp + i * K4_WARPS);
+      if (lv == 0) continue;  // no block of the pool
+      const uint32_t sT = sStage + st * K4_STAGE;
+
+      // scores
+      float S[4][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+        mma_f16_k8(S[nt], qx.x, qx.y, lds32(sT + (nt >> 1) * KV4_TILE + KV4_OFF_KM + (gr + 8 * (nt & 1)) * 8 + (t & 1) * 4));
+      }
+#pragma unroll
+      for (int g = 0; g < KV4_KG; ++g) {
+        uint4 kw[2];
+        kw[0] = lds128(sT + g * 512 + lane * 16);
+        kw[1] = lds128(sT + KV4_TILE + g * 512 + lane * 16);
+        float acc[4][4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 a = lds128(sBase + (g * 4 + j) * 512 + lane * 16);
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint4 &kk = kw[nt >> 1];
+            uint32_t x = (nt & 1) ? ((j >> 1) ? kk.w : kk.z) : ((j >> 1) ? kk.y : kk.x);
+            if (j & 1) x >>= 8;
+            mma_f16(acc[nt], a.x, a.y, a.z, a.w, x & 0x000f000fu, x & 0x00f000f0u);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 sc = lds64(sT + h * KV4_TILE + KV4_OFF_KS + g * 32 + t * 8);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float2 f = __half22float2(u32_as_h2(n ? sc.y : sc.x));
+            float(&Sn)[4] = S[2 * h + n];
+            const float(&an)[4] = acc[2 * h + n];
+            const uint64_t ff = f32x2(f.x, f.y);
+            f32x2_split(fma_f32x2(f32x2(an[0], an[1]), ff, f32x2(Sn[0], Sn[1])), Sn[0], Sn[1]);
+            f32x2_split(fma_f32x2(f32x2(an[2], an[3]), ff, f32x2(Sn[2], Sn[3])), Sn[2], Sn[3]);
+          }
+        }
+      }
+      // value scales and minima of this lane's keys (2t, 2t+1, 2t+8, 2t+9 of both tiles)
+      uint32_t sv[2][4], vm[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = sT + h * KV4_TILE;
+#pragma unroll
+        for (int g = 0; g < KV4_VG; ++g) {
+          const uint2 x = lds64(at + KV4_OFF_VS + g * 32 + t * 8);
+          sv[g][2 * h] = x.x;
+          sv[g][2 * h + 1] = x.y;
+        }
+        // columns of the sums' product: group 0's minima, group 1's, ones, nothing
+        const uint2 x = lds64(at + KV4_OFF_VM + (gr & 1) * 32 + t * 8);
+        vm[2 * h] = gr < 2 ? x.x : gr == 2 ? 0x3c003c00u : 0u;
+        vm[2 * h + 1] = gr < 2 ? x.y : gr == 2 ? 0x3c003c00u : 0u;
+      }
+      if (lv != 3 || key0 + 32 > key_hi) {
+        // keys past the range or of a bad block: what lies there (any bits) must not be met
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          const int k = key0 + 8 * nt + 2 * t;
+          const bool in = (lv >> (nt >> 1)) & 1;
+          const bool v0 = in && k < key_hi, v1 = in && k + 1 < key_hi;
+          if (!v0) S[nt][0] = S[nt][2] = NEG_INF;
+          if (!v1) S[nt][1] = S[nt][3] = NEG_INF;
+          const uint32_t keep = (v0 ? 0xffffu : 0u) | (v1 ? 0xffff0000u : 0u);
+          sv[0][nt] &= keep;
+          sv[1][nt] &= keep;
+          vm[nt] &= keep;
+        }
+      }
+      // scores less the reference, base 2; does one pass it, or a value scale its bound?
+      const float r0 = mb0 == NEG_INF ? 0.f : mb0, r1 = mb1 == NEG_INF ? 0.f : mb1;
+      float X[4][4];
+      float top0 = NEG_INF, top1 = NEG_INF;
+      __half2 big = __float2half2_rn(0.f);
+      uint32_t sf[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        X[nt][0] = fmaf(S[nt][0], crow0, -r0);
+        X[nt][1] = fmaf(S[nt][1], crow0, -r0);
+        X[nt][2] = fmaf(S[nt][2], crow1, -r1);
+        X[nt][3] = fmaf(S[nt][3], crow1, -r1);
+        top0 = fmax3(top0, X[nt][0], X[nt][1]);
+        top1 = fmax3(top1, X[nt][2], X[nt][3]);
+#pragma unroll
+        for (int g = 0; g < KV4_VG; ++g) {
+          const __half2 x = __hmul2(u32_as_h2(sv[g][nt]), f2);
+          sf[g][nt] = h2_as_u32(x);
+          big = __hmax2(big, x);
+        }
+      }
+      const bool move = top0 > K4_PBIAS + K4_SLACK || top1 > K4_PBIAS + K4_SLACK || mb0 == NEG_INF || mb1 == NEG_INF ||
+                        __low2float(big) >= 2.f || __high2float(big) >= 2.f;
+      if (__any_sync(FULLW, move)) {
+        // new reference per row: the larger of the old one and this unit's maximum
+        float t0 = top0 + r0, t1 = top1 + r1;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
+          t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
+        }
+        // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
+        const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - K4_PBIAS);
+        const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - K4_PBIAS);
+        const float c0 = mb0 == NEG_INF ? 0.f : ex2(mb0 - n0), c1 = mb1 == NEG_INF ? 0.f : ex2(mb1 - n1);
+        mb0 = n0;
+        mb1 = n1;
+        // power of two that brings the largest value scale below 2 (NaN scales aside: __hmax2 passes them by)
+        uint32_t hb = 0;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int g = 0; g < KV4_VG; ++g) {
+            const uint32_t x = sv[g][nt];
+            const uint32_t lo = x & 0xffffu, hi = x >> 16;
+            hb = max(hb, lo > 0x7c00u ? 0u : lo);
+            hb = max(hb, hi > 0x7c00u ? 0u : hi);
+          }
+        hb = __reduce_max_sync(FULLW, hb);
+        const int old = (int)(__half_as_ushort(__low2half(f2)) >> 10);   // exponent field: f = 2^(old - 15)
+        int nw = 30 - (int)(hb >> 10);                                    // 2^-(exponent of the scale): field 30 - e
+        nw = nw < 1 ? 1 : nw;
+        nw = nw > old ? old : nw;
+        const float cf = __uint_as_float((uint32_t)(127 + nw - old) << 23);
+        f2 = u32_as_h2((uint32_t)(nw << 10) * 0x10001u);
+        const float o0 = c0 * cf, o1 = c1 * cf;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          O[n][0] *= o0;
+          O[n][1] *= o0;
+          O[n][2] *= o1;
+          O[n][3] *= o1;
+        }
+        E[0] *= c0;
+        E[1] *= c0;
+        E[2] *= c1;
+        E[3] *= c1;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          X[nt][0] = fmaf(S[nt][0], crow0, -n0);
+          X[nt][1] = fmaf(S[nt][1], crow0, -n0);
+          X[nt][2] = fmaf(S[nt][2], crow1, -n1);
+          X[nt][3] = fmaf(S[nt][3], crow1, -n1);
+#pragma unroll
+          for (int g = 0; g < KV4_VG; ++g) sf[g][nt] = h2_as_u32(__hmul2(u32_as_h2(sv[g][nt]), f2));
+        }
+      }
+      // weights
+      uint32_t P[4][2];  // [8 keys][row gr, row gr + 8]
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
+        P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
+      }
+      // sums
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!((lv >> h) & 1)) continue;
+        const uint32_t at = sT + h * KV4_TILE + KV4_OFF_V;
+        const uint32_t *p0 = P[2 * h], *p1 = P[2 * h + 1];
+        mma_f16(E, p0[0], p0[1], p1[0], p1[1], vm[2 * h], vm[2 * h + 1]);
+#pragma unroll
+        for (int g = 0; g < KV4_VG; ++g) {
+          const uint4 x = lds128(at + g * 512 + lane * 16);
+          const __half2 s0 = u32_as_h2(sf[g][2 * h]), s1 = u32_as_h2(sf[g][2 * h + 1]);
+          const uint32_t a0 = h2_as_u32(__hmul2(u32_as_h2(p0[0]), s0)), a1 = h2_as_u32(__hmul2(u32_as_h2(p0[1]), s0));
+          const uint32_t a2 = h2_as_u32(__hmul2(u32_as_h2(p1[0]), s1)), a3 = h2_as_u32(__hmul2(u32_as_h2(p1[1]), s1));
+#pragma unroll
+          for (int ww = 0; ww < 2; ++ww) {
+            uint32_t y0 = ww ? x.y : x.x, y1 = ww ? x.w : x.z;
+            float(*On)[4] = &O[g * 8 + ww * 4];
+            mma_f16(On[0], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
+            mma_f16(On[1], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
+            y0 >>= 8;
+            y1 >>= 8;
+            mma_f16(On[2], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
+            mma_f16(On[3], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
+          }
+        }
+      }
+      __syncwarp();  // the stage is read: the next copy into it may go out
+    }
+    __syncthreads();  // all warps done with their stages: reuse them as the merge area
+
+    // per warp: reference and sum per row, numerators in true units (times 2^K4_PBIAS, as the sums)
+    float *mml = reinterpret_cast<float *>(smem + K4_OFF_STAGE);  // [4][16][2]
+    float *mo = mml + K4_WARPS * 16 * 2;                          // [4][16][MO_STRIDE]
+    {
+      const int src = lane & ~3;
+      const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);  // sum p m, groups 0, 1
+      const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
+      if (t == 1) {
+        float *m = mml + warp * 32;
+        m[gr * 2] = mb0;
+        m[gr * 2 + 1] = E[0];
+        m[(gr + 8) * 2] = mb1;
+        m[(gr + 8) * 2 + 1] = E[2];
+      }
+      // 2^24 over the power of two on the scales; odd dims carry 16 more
+      const int fe = (int)(__half_as_ushort(__low2half(f2)) >> 10);
+      const float un = __uint_as_float((uint32_t)(127 + 24 + 15 - fe) << 23), un16 = un * 0.0625f;
+      float *o = mo + warp * 16 * MO_STRIDE;
+#pragma unroll
+      for (int g = 0; g < KV4_VG; ++g)
+#pragma unroll
+        for (int ww = 0; ww < 2; ++ww)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float(*On)[4] = &O[g * 8 + ww * 4];
+            const float m0 = g ? g01 : g00, m1 = g ? g11 : g10;
+            const int d = 64 * g + 8 * (2 * t + c) + 4 * ww;
+            *reinterpret_cast<float4 *>(o + gr * MO_STRIDE + d) =
+                make_float4(fmaf(On[0][c], un, m0), fmaf(On[1][c], un16, m0), fmaf(On[2][c], un, m0), fmaf(On[3][c], un16, m0));
+            *reinterpret_cast<float4 *>(o + (gr + 8) * MO_STRIDE + d) =
+                make_float4(fmaf(On[0][2 + c], un, m1), fmaf(On[1][2 + c], un16, m1), fmaf(On[2][2 + c], un, m1),
+                            fmaf(On[3][2 + c], un16, m1));
+          }
+    }
+    __syncthreads();
+    float *fac = mo + K4_WARPS * 16 * MO_STRIDE;  // [4 warps][16 heads]
+    if (tid < G) {
+      float M = NEG_INF;
+#pragma unroll
+      for (int ww = 0; ww < K4_WARPS; ++ww) M = fmaxf(M, mml[ww * 32 + tid * 2]);
+      const float base = M == NEG_INF ? 0.f : M;
+      float L = 0.f;
+#pragma unroll
+      for (int ww = 0; ww < K4_WARPS; ++ww) {
+        const float mw = mml[ww * 32 + tid * 2];
+        const float f = mw == NEG_INF ? 0.f : ex2(mw - base);
+        fac[ww * 16 + tid] = f;
+        L += mml[ww * 32 + tid * 2 + 1] * f;
+      }
+      float *pml = A.part_ml + (long long)w * G * 2;
+      pml[tid * 2] = M;
+      pml[tid * 2 + 1] = L;
+    }
+    __syncthreads();
+    for (int idx = tid; idx < G * (DV / 4); idx += blockDim.x) {
+      const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int ww = 0; ww < K4_WARPS; ++ww) {
+        const float f = fac[ww * 16 + g];
+        const float4 x = *reinterpret_cast<const float4 *>(mo + (ww * 16 + g) * MO_STRIDE + d4);
+        acc.x += x.x * f;
+        acc.y += x.y * f;
+        acc.z += x.z * f;
+        acc.w += x.w * f;
+      }
+      *reinterpret_cast<float4 *>(A.part_o + ((long long)w * G + g) * DV + d4) = acc;
+    }
+  }
+  if (gave_up && lane == 0) flag(A.status, ST_TIMEOUT);
+  // leave no copy in flight: only a wait that gave up left any (bounded again)
+  uint32_t never = 0;
+  for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K4_STAGES), (seen / K4_STAGES) & 1u, &never);
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+size_t plan_bytes(int B) { return align256(((size_t)DECODE_PLAN_PREFIX + B + 1) * 4); }
+
+// Most items a device plan can give (see decode_plan_block): about k <= 8 items
+// per resident CTA and one partial split per (sequence, KV head), or the splits
+// that the longest split forces.
+long long items_cap(int B, int hkv, long long max_ctx) {
+  const long long R = (long long)K4_CTAS * num_sms(), units = (long long)B * hkv;
+  const long long a = 8 * R + units, c = units * ((max_ctx + K4_MAX_LEN - 1) / K4_MAX_LEN);
+  return a > c ? a : c;
 }
 
 }  // namespace
 
-size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) { return full_decode_workspace(B, hq, hkv, max_ctx); }
+size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
+  const size_t items = (size_t)items_cap(B, hkv, max_ctx), G = (size_t)(hq / hkv);
+  return plan_bytes(B) + align256(items * G * 2 * sizeof(float)) + align256(items * G * DV * sizeof(float));
+}
 
 cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
                               const Kv4View &pool, const float *table, int64_t max_pos, float softmax_scale,
-                              long long max_ctx, void *, uint16_t *out, unsigned *status, cudaStream_t st) {
-  return launch_pdl(kv4_decode_kernel, dim3((unsigned)(B * pool.hkv)), dim3(K4D_THREADS), 0, st, q, pos, seq, hq,
-                    hq / pool.hkv, pool, table, max_pos, softmax_scale * LOG2E, max_ctx, out, status);
+                              long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st) {
+  cudaError_t e = ensure_smem_limit(17, (const void *)kv4_decode_kernel, K4_SMEM, true);
+  if (e != cudaSuccess) return e;
+  const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
+  const size_t items = (size_t)items_cap(B, hkv, max_ctx);
+  K4Args A;
+  A.q = q;
+  A.pos = pos;
+  A.seq = seq;
+  A.B = B;
+  A.hq = hq;
+  A.G = G;
+  A.pool = pool;
+  A.table = table;
+  A.max_pos = max_pos;
+  A.scale_log2 = softmax_scale * LOG2E;
+  A.max_ctx = max_ctx;
+  A.plan = reinterpret_cast<int32_t *>(ws);
+  uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + plan_bytes(B);
+  A.part_ml = reinterpret_cast<float *>(w8);
+  A.part_o = reinterpret_cast<float *>(w8 + align256(items * G * 2 * sizeof(float)));
+  A.status = status;
+  const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
+  A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
+  if (B > K4_INLINE_MAX) {
+    e = launch_pdl(decode_plan_kernel<K4_ITEM_KEYS, K4_MAX_LEN>, dim3(1), dim3(DP_THREADS), 0, st, pos, seq, B, hkv,
+                   pool.num_seqs, max_pos, max_ctx, R, A.plan, status);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_pdl(kv4_decode_kernel, dim3((unsigned)R), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)B * hkv;
+  const int est = (int)((R + units - 1) / units);
+  return launch_full_combine(pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, A.plan, est, A.part_ml, A.part_o,
+                             out, st);
 }
 
 }  // namespace kvr
