@@ -164,13 +164,13 @@ def _check(rc: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the raw handle: a Stream object costs as much as the rest of a small call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _want(t, name, dtype, dim=None, cuda=True):
@@ -218,8 +218,14 @@ def _out(out, rows, hq, like):
 def _same_device(first, *rest):
     """The library launches on the current CUDA device and reads every pointer
     of a call there, so all of the call's tensors must live on that device."""
-    dev = first.device
     cur = torch.cuda.current_device()
+    for t in rest:
+        if t is not None and t.get_device() != cur:
+            break
+    else:
+        if first.get_device() == cur:
+            return
+    dev = first.device
     if dev.index != cur:
         raise ValueError(f"the call's tensors are on {dev} but the current device is cuda:{cur} "
                          "(make it current with torch.cuda.device)")

@@ -50,8 +50,11 @@ constexpr unsigned FULLW = 0xffffffffu;
 constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K4_WARPS = 4;
 constexpr int K4_CTAS = 3;           // per SM
+constexpr int K4_TILES = 2;          // tiles of a unit
+constexpr int K4_UNIT = 16 * K4_TILES;
+constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
 constexpr int K4_STAGES = 2;
-constexpr int K4_STAGE = 2 * KV4_TILE;
+constexpr int K4_STAGE = K4_TILES * KV4_TILE;
 constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
 // split plan: an item's fixed cost in keys and the longest split
@@ -72,31 +75,18 @@ static_assert(K4_CTAS * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(b0));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_cast<const uint4 *>(a); }
+__device__ __forceinline__ uint2 lds64(const uint8_t *a) { return *reinterpret_cast<const uint2 *>(a); }
+__device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
 
 // The query operands of one item: thread (row r, eighth c) rotates and scales
 // 24 dims of head r, the row's eight threads share its power of two and its
@@ -200,7 +190,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   const uint32_t sBase = smem_u32(smem);
   const uint32_t sBar = sBase + K4_OFF_BAR + 8 * K4_STAGES * warp;
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + K4_OFF_ABORT);
-  const uint32_t sStage = sBase + K4_OFF_STAGE + warp * K4_STAGES * K4_STAGE;
+  uint8_t *const sStage = smem + K4_OFF_STAGE + warp * K4_STAGES * K4_STAGE;
   int32_t *sPrefix = reinterpret_cast<int32_t *>(smem + K4_OFF_PLAN);
   if (lane == 0) {
     for (int j = 0; j < K4_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
@@ -260,50 +250,65 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
     const long long p = A.pos[b];
     const int s = A.seq[b];  // (a sequence with items has a valid position and id)
     const int key_lo = split * split_len, key_hi = (int)min((long long)key_lo + split_len, p + 1);
-    const int nunit = (key_hi - key_lo + 31) >> 5;
+    const int nunit = (key_hi - key_lo + K4_UNIT - 1) / K4_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
     if (__syncthreads_or(*abort_flag != 0)) break;  // the last item's merge area (over the stages) is free again
     tc::fence_proxy_async_smem();
 
-    // pool tile of the tiles ahead: lane l holds tile (l & 1) of unit
-    // base + (l >> 1); -1 past the keys, -2 in a block that is none of the pool's
-    int ids = -1;
+    // Units go out 32 at a time: lane l looks up unit base + l's tiles (a
+    // block that is none of the pool's gives -1) and issues its copies when
+    // its turn comes; `ok` has the warp's units with every tile in range.
+    int ids[K4_TILES];
+    uint32_t ok[K4_TILES], next_ok[K4_TILES];
+#pragma unroll
+    for (int k = 0; k < K4_TILES; ++k) ok[k] = next_ok[k] = 0;
     auto fetch_ids = [&](int base) {
-      const int key = key_lo + 32 * (warp + (base + (lane >> 1)) * K4_WARPS) + 16 * (lane & 1);
-      ids = -1;
-      if (key < key_hi) {
-        const unsigned tile = (unsigned)key >> 4, bi = (unsigned)((tile * A.tpb_mul) >> 36);
-        const int blk = bt[bi];
-        ids = -2;
-        if (blk >= 0 && blk < A.pool.num_blocks)
-          ids = (blk * hkv + kv) * tpb + (int)(tile - bi * tpb);
-        else
-          flag(A.status, ST_BAD_BLOCK);
+#pragma unroll
+      for (int k = 0; k < K4_TILES; ++k) {
+        const int key = key_lo + K4_UNIT * (warp + (base + lane) * K4_WARPS) + 16 * k;
+        ids[k] = -1;
+        if (base + lane < my_n && key < key_hi) {
+          const unsigned tile = (unsigned)key >> 4, bi = (unsigned)((tile * A.tpb_mul) >> 36);
+          const int blk = bt[bi];
+          if (blk >= 0 && blk < A.pool.num_blocks)
+            ids[k] = (blk * hkv + kv) * tpb + (int)(tile - bi * tpb);
+          else
+            flag(A.status, ST_BAD_BLOCK);
+        }
+        next_ok[k] = __ballot_sync(FULLW, ids[k] >= 0);
       }
     };
     auto issue = [&](int i) {
-      if ((i & 15) == 0) fetch_ids(i);
-      const int a = __shfl_sync(FULLW, ids, 2 * (i & 15)), c = __shfl_sync(FULLW, ids, 2 * (i & 15) + 1);
-      const uint32_t st = sent % K4_STAGES, bar = sBar + 8 * st, dst = sStage + st * K4_STAGE;
+      if ((i & 31) == 0) fetch_ids(i);
+      const uint32_t st = sent % K4_STAGES;
       ++sent;
-      tc::mbar_expect_tx_elect(bar, ((a >= 0) + (c >= 0)) * KV4_TILE);
-      if (a >= 0) tc::bulk_load_elect(dst, A.pool.data + (long long)a * KV4_TILE, KV4_TILE, bar);
-      if (c >= 0) tc::bulk_load_elect(dst + KV4_TILE, A.pool.data + (long long)c * KV4_TILE, KV4_TILE, bar);
-      return (a >= 0 ? 1 : 0) | (c >= 0 ? 2 : 0);
-    };
-    int live[K4_STAGES];  // which tiles of a stage were loaded
+      if (lane == (i & 31)) {
+        const uint32_t bar = sBar + 8 * st, dst = smem_u32(sStage + st * K4_STAGE);
+        if (K4_TILES == 2 && ids[0] >= 0 && ids[K4_TILES - 1] == ids[0] + 1) {
+          tc::mbar_expect_tx(bar, 2 * KV4_TILE);
+          tc::bulk_load(dst, A.pool.data + (long long)ids[0] * KV4_TILE, 2 * KV4_TILE, bar);
+        } else {
+          int n = 0;
 #pragma unroll
-    for (int i = 0; i < K4_STAGES; ++i) live[i] = 0;
+          for (int k = 0; k < K4_TILES; ++k) n += ids[k] >= 0;
+          tc::mbar_expect_tx(bar, n * KV4_TILE);
+#pragma unroll
+          for (int k = 0; k < K4_TILES; ++k)
+            if (ids[k] >= 0)
+              tc::bulk_load(dst + k * KV4_TILE, A.pool.data + (long long)ids[k] * KV4_TILE, KV4_TILE, bar);
+        }
+      }
+    };
 #pragma unroll
     for (int i = 0; i < K4_STAGES - 1; ++i)
-      if (i < my_n) live[i] = issue(i);
+      if (i < my_n) issue(i);
 
     kv4_query(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, A.scale_log2, smem, tid);
     __syncthreads();
     const float crow0 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * gr);
     const float crow1 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * (gr + 8));
-    const uint2 qx = lds64(sBase + K4_OFF_QX + lane * 8);
+    const uint2 qx = lds64(smem + K4_OFF_QX + lane * 8);
 
     float O[16][4], E[4];
 #pragma unroll
@@ -313,10 +318,11 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
     __half2 f2 = __float2half2_rn(32768.f);  // the power of two on the value scales
 
     for (int i = 0; i < my_n; ++i) {
-      const int lv = live[0];
+      if ((i & 31) == 0) {  // (the units of this round were looked up no later than with their first)
 #pragma unroll
-      for (int k = 0; k + 1 < K4_STAGES; ++k) live[k] = live[k + 1];
-      if (i + K4_STAGES - 1 < my_n) live[K4_STAGES - 2] = issue(i + K4_STAGES - 1);
+        for (int k = 0; k < K4_TILES; ++k) ok[k] = next_ok[k];
+      }
+      if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
       const uint32_t st = seen % K4_STAGES;
       const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
       if (!got) {
@@ -324,30 +330,33 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         break;
       }
       ++seen;
-      const int key0 = key_lo + 32 * (warp + i * K4_WARPS);
+      const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
+      int lv = 0;
+#pragma unroll
+      for (int k = 0; k < K4_TILES; ++k) lv |= ((ok[k] >> (i & 31)) & 1) << k;
       if (lv == 0) continue;  // no block of the pool
-      const uint32_t sT = sStage + st * K4_STAGE;
+      const uint8_t *sT = sStage + st * K4_STAGE;
 
       // scores
-      float S[4][4];
+      float S[K4_NT][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < K4_NT; ++nt) {
         S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
         mma_f16_k8(S[nt], qx.x, qx.y, lds32(sT + (nt >> 1) * KV4_TILE + KV4_OFF_KM + (gr + 8 * (nt & 1)) * 8 + (t & 1) * 4));
       }
 #pragma unroll
       for (int g = 0; g < KV4_KG; ++g) {
-        uint4 kw[2];
-        kw[0] = lds128(sT + g * 512 + lane * 16);
-        kw[1] = lds128(sT + KV4_TILE + g * 512 + lane * 16);
-        float acc[4][4];
+        uint4 kw[K4_TILES];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        for (int k = 0; k < K4_TILES; ++k) kw[k] = lds128(sT + k * KV4_TILE + g * 512 + lane * 16);
+        float acc[K4_NT][4];
+#pragma unroll
+        for (int nt = 0; nt < K4_NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 a = lds128(sBase + (g * 4 + j) * 512 + lane * 16);
+          const uint4 a = lds128(smem + (g * 4 + j) * 512 + lane * 16);
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
+          for (int nt = 0; nt < K4_NT; ++nt) {
             const uint4 &kk = kw[nt >> 1];
             uint32_t x = (nt & 1) ? ((j >> 1) ? kk.w : kk.z) : ((j >> 1) ? kk.y : kk.x);
             if (j & 1) x >>= 8;
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
           }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < K4_TILES; ++h) {
           const uint2 sc = lds64(sT + h * KV4_TILE + KV4_OFF_KS + g * 32 + t * 8);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
@@ -369,10 +378,10 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         }
       }
       // value scales and minima of this lane's keys (2t, 2t+1, 2t+8, 2t+9 of both tiles)
-      uint32_t sv[2][4], vm[4];
+      uint32_t sv[2][K4_NT], vm[K4_NT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = sT + h * KV4_TILE;
+      for (int h = 0; h < K4_TILES; ++h) {
+        const uint8_t *at = sT + h * KV4_TILE;
 #pragma unroll
         for (int g = 0; g < KV4_VG; ++g) {
           const uint2 x = lds64(at + KV4_OFF_VS + g * 32 + t * 8);
@@ -384,10 +393,10 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         vm[2 * h] = gr < 2 ? x.x : gr == 2 ? 0x3c003c00u : 0u;
         vm[2 * h + 1] = gr < 2 ? x.y : gr == 2 ? 0x3c003c00u : 0u;
       }
-      if (lv != 3 || key0 + 32 > key_hi) {
+      if (lv != (1 << K4_TILES) - 1 || key0 + K4_UNIT > key_hi) {
         // keys past the range or of a bad block: what lies there (any bits) must not be met
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < K4_NT; ++nt) {
           const int k = key0 + 8 * nt + 2 * t;
           const bool in = (lv >> (nt >> 1)) & 1;
           const bool v0 = in && k < key_hi, v1 = in && k + 1 < key_hi;
@@ -401,12 +410,12 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
       }
       // scores less the reference, base 2; does one pass it, or a value scale its bound?
       const float r0 = mb0 == NEG_INF ? 0.f : mb0, r1 = mb1 == NEG_INF ? 0.f : mb1;
-      float X[4][4];
+      float X[K4_NT][4];
       float top0 = NEG_INF, top1 = NEG_INF;
       __half2 big = __float2half2_rn(0.f);
-      uint32_t sf[2][4];
+      uint32_t sf[2][K4_NT];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < K4_NT; ++nt) {
         X[nt][0] = fmaf(S[nt][0], crow0, -r0);
         X[nt][1] = fmaf(S[nt][1], crow0, -r0);
         X[nt][2] = fmaf(S[nt][2], crow1, -r1);
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         // power of two that brings the largest value scale below 2 (NaN scales aside: __hmax2 passes them by)
         uint32_t hb = 0;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < K4_NT; ++nt)
 #pragma unroll
           for (int g = 0; g < KV4_VG; ++g) {
             const uint32_t x = sv[g][nt];
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         E[2] *= c1;
         E[3] *= c1;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < K4_NT; ++nt) {
           X[nt][0] = fmaf(S[nt][0], crow0, -n0);
           X[nt][1] = fmaf(S[nt][1], crow0, -n0);
           X[nt][2] = fmaf(S[nt][2], crow1, -n1);
@@ -477,17 +486,17 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         }
       }
       // weights
-      uint32_t P[4][2];  // [8 keys][row gr, row gr + 8]
+      uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < K4_NT; ++nt) {
         P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
         P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
       }
       // sums
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < K4_TILES; ++h) {
         if (!((lv >> h) & 1)) continue;
-        const uint32_t at = sT + h * KV4_TILE + KV4_OFF_V;
+        const uint8_t *at = sT + h * KV4_TILE + KV4_OFF_V;
         const uint32_t *p0 = P[2 * h], *p1 = P[2 * h + 1];
         mma_f16(E, p0[0], p0[1], p1[0], p1[1], vm[2 * h], vm[2 * h + 1]);
 #pragma unroll
@@ -592,11 +601,13 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t plan_bytes(int B) { return align256(((size_t)DECODE_PLAN_PREFIX + B + 1) * 4); }
 
 // Most items a device plan can give (see decode_plan_block): about k <= 8 items
-// per resident CTA and one partial split per (sequence, KV head), or the splits
-// that the longest split forces.
+// per resident CTA and one partial split per (sequence, KV head), but none
+// shorter than 64 keys; or the splits that the longest split forces.
 long long items_cap(int B, int hkv, long long max_ctx) {
   const long long R = (long long)K4_CTAS * num_sms(), units = (long long)B * hkv;
-  const long long a = 8 * R + units, c = units * ((max_ctx + K4_MAX_LEN - 1) / K4_MAX_LEN);
+  long long a = 8 * R + units;
+  const long long most = units * ((max_ctx + 63) / 64), c = units * ((max_ctx + K4_MAX_LEN - 1) / K4_MAX_LEN);
+  if (a > most) a = most;
   return a > c ? a : c;
 }
 
