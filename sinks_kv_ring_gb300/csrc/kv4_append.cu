@@ -12,184 +12,321 @@
 // group instead of 64 divisions, and exact ties round to even as they should
 // (bf16 keys meet them often).
 //
-// A warp takes four (token, KV head) items: lane 8i + c holds dims 8c..8c+7
-// of a group of item i, five groups in turn, so the group's extrema are three
-// shuffles away and a 16-byte load brings a lane's values.  All five loads
-// are in flight before the destination is looked up.
+// A warp takes four tokens of one KV head: lane 8i + c holds dims 8c..8c+7 of
+// a group of token i, five groups in turn, so the group's extrema are three
+// shuffles away and a 16-byte load brings a lane's values, all five in flight
+// at once.
+//
+// A position's V codes are 32 pieces of 2 bytes, so writing tokens one by one
+// is bound by the stores' sectors, not by their bytes.  A CTA therefore owns
+// the runs of tokens (consecutive in the call and in one tile) that start
+// among its 16: when one of them is a whole tile, as all but the first and
+// last of a chunk are, the tile is put together in shared memory and leaves as
+// 16-byte stores of whole sectors.
 #include "kv4.cuh"
 #include "launch.h"
 
 namespace kvr {
 namespace {
 
-constexpr int K4A_WARPS = 8;
-constexpr int K4A_ITEMS = 4;
+constexpr int K4A_WARPS = 4;
+constexpr int K4A_ITEMS = 4;                       // tokens of a warp
+constexpr int K4A_TOKENS = K4A_WARPS * K4A_ITEMS;  // and of a CTA
+static_assert(K4A_TOKENS == 16, "a CTA's tokens are as many as a tile's");
 constexpr unsigned FULLW = 0xffffffffu;
 
-// Codes of a lane's 8 values (dim i in nibble i) and the group's scale and
-// minimum; the 8 lanes of the group call together.
-__device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], int lane, uint16_t &s16, uint16_t &m16) {
-  float lo = x[0], hi = x[0], odd = 0.f;
+// min and max that hand a NaN on
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// Least and greatest of a group's 64 bf16 values over its eight lanes: in
+// packed pairs, the greatest as the least of the negated ones.
+__device__ __forceinline__ void extrema_bf16(const uint4 &x, float &lo, float &hi) {
+  const uint32_t a = min_nan_bf16x2(min_nan_bf16x2(x.x, x.y), min_nan_bf16x2(x.z, x.w));
+  const uint32_t b = max_nan_bf16x2(max_nan_bf16x2(x.x, x.y), max_nan_bf16x2(x.z, x.w)) ^ 0x80008000u;
+  uint32_t m = min_nan_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // (least, -greatest)
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) odd = fmaf(x[i], 0.f, odd);  // NaN when a value is infinite or NaN
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(FULLW, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(FULLW, hi, o));
-  }
-  const bool bad = (__ballot_sync(FULLW, odd != odd) >> (lane & 24)) & 0xffu;
+  for (int o = 1; o < 8; o <<= 1) m = min_nan_bf16x2(m, __shfl_xor_sync(FULLW, m, o));
+  lo = __uint_as_float(m << 16);
+  hi = -__uint_as_float(m & 0xffff0000u);
+}
+
+// Scale and minimum of a group (packed, scale in the low half) and the
+// reciprocal of the scale; the reciprocal is -1 where values lie past fp16
+// (their codes need a clamp) and -2 where one is not finite.
+__device__ __forceinline__ void kv4_scale(float lo, float hi, uint32_t &sm, float &r) {
   const __half m = __float2half_rd(fminf(fmaxf(lo, -65504.f), 65504.f));
   const float mf = __half2float(m);
   const __half s = __float2half_ru(fminf(__fdiv_rn(__fsub_rn(hi, mf), 15.f), 65504.f));
   const float sf = __half2float(s);
-  const float r = sf > 0.f ? __frcp_rn(sf) : 0.f;
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = __fsub_rn(x[i], mf);
-    const float q0 = __fmul_rn(d, r);
-    const float q = fmaf(fmaf(-sf, q0, d), r, q0);
-    w |= (uint32_t)__float2int_rn(fminf(fmaxf(q, 0.f), 15.f)) << (4 * i);
+  sm = __half_as_ushort(s) | ((uint32_t)__half_as_ushort(m) << 16);
+  r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  if (!(lo >= -65504.f && hi <= 65504.f)) {  // (so for a NaN)
+    r = -1.f;
+    if (!(lo >= -3.4028235e38f && hi <= 3.4028235e38f)) {
+      sm = 0x7fff7fffu;
+      r = -2.f;
+    }
   }
-  s16 = bad ? 0x7fff : __half_as_ushort(s);
-  m16 = bad ? 0x7fff : __half_as_ushort(m);
-  return bad ? 0u : w;
 }
 
+// Codes of a lane's 8 values (dim i in nibble i) under scale, minimum and
+// reciprocal.  The quotient lies in [0, 15] and is rounded by adding 1.5 2^23,
+// which leaves it in the low bits; multiply-adds join the nibbles.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], uint32_t sm, float r) {
+  const float sf = __half2float(__ushort_as_half((uint16_t)sm)), mf = __half2float(__ushort_as_half((uint16_t)(sm >> 16)));
+  uint32_t w = 0;
+  if (r >= 0.f) {  // (the group's eight lanes agree)
+    const uint64_t nm = f32x2(-mf, -mf), ns = f32x2(-sf, -sf), rr = f32x2(r, r), magic = f32x2(12582912.f, 12582912.f);
+#pragma unroll
+    for (int i = 6; i >= 0; i -= 2) {
+      const uint64_t d = add_f32x2(f32x2(x[i], x[i + 1]), nm);
+      const uint64_t q0 = mul_f32x2(d, rr);
+      float a, b;
+      f32x2_split(add_f32x2(fma_f32x2(fma_f32x2(ns, q0, d), rr, q0), magic), a, b);
+      w = (w * 16u + __float_as_uint(b)) * 16u + __float_as_uint(a);
+    }
+    return w - 0x4b400000u * 0x11111111u;  // less the eight exponents
+  }
+  if (r == -1.f) {  // values past fp16
+    r = sf > 0.f ? __frcp_rn(sf) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = __fsub_rn(x[i], mf);
+      const float q0 = __fmul_rn(d, r);
+      const float q = fmaf(fmaf(-sf, q0, d), r, q0);
+      w |= (uint32_t)__float2int_rn(fminf(fmaxf(q, 0.f), 15.f)) << (4 * i);
+    }
+  }
+  return w;
+}
+
+__device__ __forceinline__ void load_token(const uint16_t *k, const uint16_t *v, size_t item, int c, uint4 (&raw)[5]) {
+  const uint4 *k4 = reinterpret_cast<const uint4 *>(k) + item * (DQK / 8);
+  const uint4 *v4 = reinterpret_cast<const uint4 *>(v) + item * (DV / 8);
+#pragma unroll
+  for (int g = 0; g < KV4_KG; ++g) raw[g] = k4[g * 8 + c];
+#pragma unroll
+  for (int g = 0; g < KV4_VG; ++g) raw[KV4_KG + g] = v4[g * 8 + c];
+}
+
+// early: load the CTA's own 16 tokens ahead of the look-up (they are the ones
+// it takes unless a run reaches into them: worth it when latency is all)
 __global__ void __launch_bounds__(K4A_WARPS * 32)
     kv4_append_kernel(const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, const int64_t *__restrict__ pos,
-                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, long long total,
-                      const float *__restrict__ table, int64_t max_pos, float vscale, Kv4View dst, unsigned *status) {
+                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, int T,
+                      const float *__restrict__ table, int64_t max_pos, float vscale, Kv4View dst, int early,
+                      unsigned *status) {
+  constexpr int LOOK = 2 * K4A_TOKENS + 1;  // tokens looked up: one before the CTA's, and as many behind
+  __shared__ __align__(16) uint8_t s_img[KV4_TILE];
+  __shared__ int s_blk[LOOK], s_row[LOOK], s_pos[LOOK];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, c = lane & 7;
-  const long long item =
-      ((long long)blockIdx.x * K4A_WARPS + (threadIdx.x >> 5)) * K4A_ITEMS + (lane >> 3);
-  const bool have = item < total;
-
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7;
+  const int h = (int)(blockIdx.x % (unsigned)dst.hkv), t0 = (int)(blockIdx.x / (unsigned)dst.hkv) * K4A_TOKENS;
   uint4 raw[5];
 #pragma unroll
   for (int g = 0; g < 5; ++g) raw[g] = make_uint4(0, 0, 0, 0);
-  if (have) {
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(k) + item * (DQK / 8);
-    const uint4 *v4 = reinterpret_cast<const uint4 *>(v) + item * (DV / 8);
-#pragma unroll
-    for (int g = 0; g < KV4_KG; ++g) raw[g] = k4[g * 8 + c];
-#pragma unroll
-    for (int g = 0; g < KV4_VG; ++g) raw[KV4_KG + g] = v4[g * 8 + c];
+  if (early) {
+    const int t = t0 + warp * K4A_ITEMS + (lane >> 3);
+    if (t < T) load_token(k, v, (size_t)t * dst.hkv + h, c, raw);
   }
 
-  // where the item goes: the tile's first byte and the position within it
-  // (every lane of the item the same; lane c = 0 flags)
-  uint8_t *tile = nullptr;
-  int r = 0;
-  long long p = 0;
-  unsigned bad = 0;
-  if (have) {
-    const long long t = item / dst.hkv;
-    const int h = (int)(item - t * dst.hkv);
-    p = pos[t];
-    long long slot = -1;
-    const int s = slots ? 0 : seq[t];
-    if (slots) {
-      slot = slots[t];
-      if (slot >= (long long)dst.num_blocks * dst.block_size) {
-        bad = ST_BAD_BLOCK;
-        slot = -1;
-      }
-    }
-    const bool skip = slots ? slot < 0 : s == -1;  // padding
-    if (!skip && !bad) {
-      if (p < 0 || p >= max_pos) {
-        bad = ST_BAD_POS;
-      } else if (!slots) {
-        if (s < 0 || s >= dst.num_seqs) {
-          bad = ST_BAD_SEQ;
-        } else {
-          const long long bi = p / dst.block_size;
-          const int blk = bi < dst.max_blocks ? dst.block_table[(long long)s * dst.max_blocks + bi] : -1;
-          if (blk < 0 || blk >= dst.num_blocks)
+  // 1. where the tokens go: block (-1: nowhere) and row in it
+  if (threadIdx.x < LOOK) {
+    const int t = t0 - 1 + (int)threadIdx.x;
+    int blk = -1;
+    unsigned row = 0, bad = 0;
+    long long p = 0;
+    if (t >= 0 && t < T) {
+      p = pos[t];
+      const int s = slots ? 0 : seq[t];
+      bool pad = s == -1;
+      if (slots) {
+        const long long slot = slots[t];
+        pad = slot < 0;
+        if (!pad) {
+          if (slot < (long long)dst.num_blocks * dst.block_size) {
+            // (a pool of 2^32 positions would be 781 GB)
+            blk = (int)((unsigned)slot / (unsigned)dst.block_size);
+            row = (unsigned)slot - (unsigned)blk * (unsigned)dst.block_size;
+          } else {
             bad = ST_BAD_BLOCK;
-          else
-            slot = (long long)blk * dst.block_size + (p - bi * dst.block_size);
+          }
         }
       }
+      if (!pad && !bad) {
+        if (p < 0 || p >= max_pos) {
+          bad = ST_BAD_POS;
+        } else if (!slots) {
+          if (s < 0 || s >= dst.num_seqs) {
+            bad = ST_BAD_SEQ;
+          } else {
+            const unsigned bi = (unsigned)p / (unsigned)dst.block_size;  // (max_pos < 2^31)
+            blk = bi < (unsigned)dst.max_blocks ? dst.block_table[(long long)s * dst.max_blocks + bi] : -1;
+            row = (unsigned)p - bi * (unsigned)dst.block_size;
+            if (blk < 0 || blk >= dst.num_blocks) bad = ST_BAD_BLOCK;
+          }
+        }
+      }
+      if (bad) {
+        blk = -1;
+        if (h == 0 && threadIdx.x >= 1 && threadIdx.x <= K4A_TOKENS) flag(status, bad);
+      }
     }
-    if (bad) {
-      if (c == 0 && h == 0) flag(status, bad);
-    } else if (slot >= 0) {
-      const int blk = (int)(slot / dst.block_size), row = (int)(slot % dst.block_size);
-      tile = dst.data + kv4_tile(dst, blk, h, row);
-      r = row & 15;
-    }
+    s_blk[threadIdx.x] = blk;
+    s_row[threadIdx.x] = (int)row;
+    s_pos[threadIdx.x] = (int)p;
   }
-  if (!__any_sync(FULLW, tile != nullptr)) return;
-
-  // RoPE row: frequencies 8(c & 3) .. +7
-  float cs[16];
-  if (tile) {
-    const float4 *tr = reinterpret_cast<const float4 *>(table + p * 64 + 16 * (c & 3));
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 f = tr[u];
-      cs[4 * u] = f.x; cs[4 * u + 1] = f.y; cs[4 * u + 2] = f.z; cs[4 * u + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < 16; ++u) cs[u] = 0.f;
+  __syncthreads();
+  // 2. runs: entry j (token t0 - 1 + j) goes on with the one before it when
+  // both go to the same tile and its row is the next.  Bit j - 1 of `starts`
+  // is set where entry j does not.
+  uint32_t starts, heads;
+  {
+    const int j = lane + 1, blk = s_blk[j], row = s_row[j];
+    starts = __ballot_sync(FULLW, !(blk >= 0 && blk == s_blk[j - 1] && row == s_row[j - 1] + 1 && (row & 15)));
+    heads = __ballot_sync(FULLW, blk >= 0 && !(row & 15));  // entries at a tile's first row
   }
+  // the CTA's tokens: from the first run that starts among its 16 to the first that starts behind them (a run has at
+  // most 16 tokens, so there is one)
+  const uint32_t own = starts & 0xffffu, after = starts & 0xffff0000u;
+  const int first = own ? __ffs(own) : LOOK;
+  int end = after ? __ffs(after) : LOOK;
+  if (end > T - t0 + 1) end = T - t0 + 1;
+  if (first >= end) return;
+  // the whole tile among them, if there is one: its first entry, followed by 15 that go on
+  uint32_t on = ~starts >> 1;  // bit j - 1: entry j + 1 goes on
+  on &= on >> 1;
+  on &= on >> 2;
+  on &= on >> 4;               // eight in a row
+  on &= on >> 7;               // fifteen
+  const uint32_t whole = own & heads & on;
+  const int full = whole && __ffs(whole) + 16 <= end ? __ffs(whole) : -1;
 
+  for (int j0 = first; j0 < end; j0 += K4A_TOKENS) {
+    const int j = j0 + warp * K4A_ITEMS + (lane >> 3);
+    uint8_t *tile = nullptr;
+    int r = 0, p = 0;
+    if (j < end && s_blk[j] >= 0) {
+      if (!early || j0 != 1) load_token(k, v, (size_t)(t0 - 1 + j) * dst.hkv + h, c, raw);
+      p = s_pos[j];
+      r = s_row[j] & 15;
+      tile = full >= 0 && j >= full && j < full + 16 ? s_img : dst.data + kv4_tile(dst, s_blk[j], h, s_row[j]);
+    }
+
+    // group 0: rotate.  The other half of the pair lies four lanes away;
+    // products and sum are rounded one by one, so the result does not hang on
+    // contraction.
+    float x0[8];
+    {
+      float cs[16];
+      const float4 *tr = reinterpret_cast<const float4 *>(table + (long long)p * 64 + 16 * (c & 3));
 #pragma unroll
-  for (int g = 0; g < 5; ++g) {
-    const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[g]);
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bf2f(e[i]);
-    if (g == 0) {
-      // the other half of the rotated pair lies four lanes away; products and
-      // sum are rounded one by one, so the result does not hang on contraction
+      for (int u = 0; u < 4; ++u) {
+        const float4 f = tr[u];
+        cs[4 * u] = f.x; cs[4 * u + 1] = f.y; cs[4 * u + 2] = f.z; cs[4 * u + 3] = f.w;
+      }
       uint4 o;
       o.x = __shfl_xor_sync(FULLW, raw[0].x, 4);
       o.y = __shfl_xor_sync(FULLW, raw[0].y, 4);
       o.z = __shfl_xor_sync(FULLW, raw[0].z, 4);
       o.w = __shfl_xor_sync(FULLW, raw[0].w, 4);
-      const uint16_t *oe = reinterpret_cast<const uint16_t *>(&o);
+      const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[0]), *oe = reinterpret_cast<const uint16_t *>(&o);
+      const uint32_t neg = c < 4 ? 0x80000000u : 0u;  // a - b, or a + b
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float a = __fmul_rn(x[i], cs[2 * i]), b = __fmul_rn(bf2f(oe[i]), cs[2 * i + 1]);
-        x[i] = c < 4 ? __fsub_rn(a, b) : __fadd_rn(a, b);
+        const float a = __fmul_rn(bf2f(e[i]), cs[2 * i]), b = __fmul_rn(bf2f(oe[i]), cs[2 * i + 1]);
+        x0[i] = __fadd_rn(a, __uint_as_float(__float_as_uint(b) ^ neg));
       }
-    } else if (g >= KV4_KG) {
+    }
+    // extrema of all groups, then lane g of the token's eight takes group g's
+    // scale (the divisions are most of a group's cost) and hands it round
+    float lo[5], hi[5];
+    lo[0] = hi[0] = x0[0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], vscale);
+    for (int i = 1; i < 8; ++i) {
+      lo[0] = min_nan(lo[0], x0[i]);
+      hi[0] = max_nan(hi[0], x0[i]);
     }
-    uint16_t s16, m16;
-    const uint32_t w = kv4_quantise(x, lane, s16, m16);
-    if (tile) {
-      if (g < KV4_KG) {
-        *reinterpret_cast<uint32_t *>(tile + kv4_k_at(g, r, c >> 1) + (c & 1) * 4) = w;
-        if (c == 0) {
-          *reinterpret_cast<uint16_t *>(tile + KV4_OFF_KS + (g * 16 + kv4_quad(r)) * 2) = s16;
-          if (g < 2)
-            *reinterpret_cast<uint16_t *>(tile + KV4_OFF_KM + r * 8 + g * 2) = m16;
-          else
-            *reinterpret_cast<uint32_t *>(tile + KV4_OFF_KM + r * 8 + 4) = m16;  // and the row's zero
-        }
-      } else {
-        const int vg = g - KV4_KG;
-        *reinterpret_cast<uint16_t *>(tile + kv4_v_at(vg, r, c, 0)) = (uint16_t)w;
-        *reinterpret_cast<uint16_t *>(tile + kv4_v_at(vg, r, c, 1)) = (uint16_t)(w >> 16);
-        if (c == 0) {
-          *reinterpret_cast<uint16_t *>(tile + KV4_OFF_VS + (vg * 16 + kv4_quad(r)) * 2) = s16;
-          *reinterpret_cast<uint16_t *>(tile + KV4_OFF_VM + (vg * 16 + kv4_quad(r)) * 2) = m16;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      lo[0] = min_nan(lo[0], __shfl_xor_sync(FULLW, lo[0], o));
+      hi[0] = max_nan(hi[0], __shfl_xor_sync(FULLW, hi[0], o));
+    }
+#pragma unroll
+    for (int g = 1; g < 5; ++g) {
+      extrema_bf16(raw[g], lo[g], hi[g]);
+      if (g >= KV4_KG) {  // the scaled values' extrema are the extrema's products (swapped under a negative scale)
+        const float a = __fmul_rn(lo[g], vscale), b = __fmul_rn(hi[g], vscale);
+        lo[g] = min_nan(a, b);
+        hi[g] = max_nan(a, b);
+      }
+    }
+    float mylo = lo[0], myhi = hi[0];
+#pragma unroll
+    for (int g = 1; g < 5; ++g) {
+      mylo = c == g ? lo[g] : mylo;
+      myhi = c == g ? hi[g] : myhi;
+    }
+    uint32_t mysm;
+    float myr;
+    kv4_scale(mylo, myhi, mysm, myr);
+    if (tile && c < 5) {  // lane c writes group c's scale and minimum
+      const int q = kv4_quad(r);
+      const int at_s = c < KV4_KG ? KV4_OFF_KS + c * 32 + q * 2 : KV4_OFF_VS + (c - KV4_KG) * 32 + q * 2;
+      const int at_m = c < KV4_KG ? KV4_OFF_KM + r * 8 + c * 2 : KV4_OFF_VM + (c - KV4_KG) * 32 + q * 2;
+      *reinterpret_cast<uint16_t *>(tile + at_s) = (uint16_t)mysm;
+      *reinterpret_cast<uint16_t *>(tile + at_m) = (uint16_t)(mysm >> 16);
+    } else if (tile && c == 5) {
+      *reinterpret_cast<uint16_t *>(tile + KV4_OFF_KM + r * 8 + 6) = 0;
+    }
+#pragma unroll
+    for (int g = 0; g < 5; ++g) {
+      const uint32_t sm = __shfl_sync(FULLW, mysm, (lane & 24) + g);
+      const float rc = __shfl_sync(FULLW, myr, (lane & 24) + g);
+      float x[8];
+      const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[g]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = g == 0 ? x0[i] : g < KV4_KG ? bf2f(e[i]) : __fmul_rn(bf2f(e[i]), vscale);
+      const uint32_t w = kv4_codes(x, sm, rc);
+      if (tile) {
+        if (g < KV4_KG) {
+          *reinterpret_cast<uint32_t *>(tile + kv4_k_at(g, r, c >> 1) + (c & 1) * 4) = w;
+        } else {
+          *reinterpret_cast<uint16_t *>(tile + kv4_v_at(g - KV4_KG, r, c, 0)) = (uint16_t)w;
+          *reinterpret_cast<uint16_t *>(tile + kv4_v_at(g - KV4_KG, r, c, 1)) = (uint16_t)(w >> 16);
         }
       }
     }
+  }
+  if (full >= 0) {  // (the same for the whole CTA)
+    __syncthreads();
+    uint4 *o = reinterpret_cast<uint4 *>(dst.data + kv4_tile(dst, s_blk[full], h, s_row[full]));
+    for (int i = threadIdx.x; i < KV4_TILE / 16; i += K4A_WARPS * 32) o[i] = reinterpret_cast<const uint4 *>(s_img)[i];
   }
 }
 
@@ -198,12 +335,10 @@ __global__ void __launch_bounds__(K4A_WARPS * 32)
 cudaError_t launch_kv4_append(const uint16_t *k, const uint16_t *v, const int64_t *pos, const int32_t *seq,
                               const int64_t *slots, int T, const float *table, int64_t max_pos, float value_scale,
                               const Kv4View &dst, unsigned *status, cudaStream_t st) {
-  const long long items = (long long)T * dst.hkv;
-  const long long per_block = (long long)K4A_WARPS * K4A_ITEMS;
-  const long long blocks = (items + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(kv4_append_kernel, dim3((unsigned)blocks), dim3(K4A_WARPS * 32), 0, st, k, v, pos, seq, slots,
-                    items, table, max_pos, value_scale, dst, status);
+  const long long ctas = (long long)((T + (long long)K4A_TOKENS - 1) / K4A_TOKENS) * dst.hkv;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(kv4_append_kernel, dim3((unsigned)ctas), dim3(K4A_WARPS * 32), 0, st, k, v, pos, seq, slots, T,
+                    table, max_pos, value_scale, dst, ctas <= 4 * num_sms() ? 1 : 0, status);
 }
 
 }  // namespace kvr

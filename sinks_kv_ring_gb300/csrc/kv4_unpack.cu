@@ -19,14 +19,19 @@ namespace {
 constexpr int K4U_WARPS = 8;
 constexpr unsigned FULLW = 0xffffffffu;
 
-// bf16 pair of two codes' values
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t a, uint32_t b, float s, float m) {
-  return pack_bf16(fmaf((float)a, s, m), fmaf((float)b, s, m));
+// The values of a word of codes (dim i in nibble i) as bf16.  A code masked
+// out of the word in place is the fp16 number u 2^-24 (or 16 u 2^-24), so the
+// conversion to fp32 is the fp16 one and the power of two goes into the scale
+// (exactly): s24 = s 2^24, s20 = s 2^20.
+__device__ __forceinline__ uint4 kv4_word(uint32_t w, float s24, float s20, float m) {
+  const uint32_t w8 = w >> 8;
+  const float2 a = __half22float2(u32_as_h2(w & 0x000f000fu)), b = __half22float2(u32_as_h2(w & 0x00f000f0u));
+  const float2 c = __half22float2(u32_as_h2(w8 & 0x000f000fu)), d = __half22float2(u32_as_h2(w8 & 0x00f000f0u));
+  return make_uint4(pack_bf16(fmaf(a.x, s24, m), fmaf(b.x, s20, m)), pack_bf16(fmaf(c.x, s24, m), fmaf(d.x, s20, m)),
+                    pack_bf16(fmaf(a.y, s24, m), fmaf(b.y, s20, m)), pack_bf16(fmaf(c.y, s24, m), fmaf(d.y, s20, m)));
 }
-// the 8 values of a word of codes (dim i in nibble i)
-__device__ __forceinline__ uint4 kv4_word(uint32_t w, float s, float m) {
-  return make_uint4(kv4_pair(w & 15u, (w >> 4) & 15u, s, m), kv4_pair((w >> 8) & 15u, (w >> 12) & 15u, s, m),
-                    kv4_pair((w >> 16) & 15u, (w >> 20) & 15u, s, m), kv4_pair((w >> 24) & 15u, w >> 28, s, m));
+__device__ __forceinline__ float kv4_half(uint32_t w, int hi) {
+  return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w)));
 }
 
 __global__ void __launch_bounds__(K4U_WARPS * 32)
@@ -108,10 +113,25 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
 #pragma unroll
   for (int g = 0; g < KV4_VG; ++g)
     vc[g] = ok ? *reinterpret_cast<const uint4 *>(tile + KV4_OFF_V + g * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
-  auto half_at = [&](int off) -> float {
-    return ok ? __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(tile + off))) : 0.f;
-  };
   const int q = lane >> 2, t = lane & 3;
+  // K minima of positions q and q + 8 (three and a zero), K scales of the same
+  uint2 km[2];
+  uint16_t ks[2][KV4_KG];
+  // V scales and minima of positions 2t, 2t + 1, 2t + 8, 2t + 9
+  uint2 vs[KV4_VG], vm[KV4_VG];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    const int r = q + 8 * nt;
+    km[nt] = ok ? *reinterpret_cast<const uint2 *>(tile + KV4_OFF_KM + r * 8) : make_uint2(0, 0);
+#pragma unroll
+    for (int g = 0; g < KV4_KG; ++g)
+      ks[nt][g] = ok ? *reinterpret_cast<const uint16_t *>(tile + KV4_OFF_KS + (g * 16 + kv4_quad(r)) * 2) : (uint16_t)0;
+  }
+#pragma unroll
+  for (int g = 0; g < KV4_VG; ++g) {
+    vs[g] = ok ? *reinterpret_cast<const uint2 *>(tile + KV4_OFF_VS + g * 32 + t * 8) : make_uint2(0, 0);
+    vm[g] = ok ? *reinterpret_cast<const uint2 *>(tile + KV4_OFF_VM + g * 32 + t * 8) : make_uint2(0, 0);
+  }
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) {  // K: positions q and q + 8, dims 16t .. of each group
     const int r = q + 8 * nt;
@@ -120,10 +140,11 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
     uint16_t *kd = dst.k + (drow + r * step) * DQK + 16 * t;
 #pragma unroll
     for (int g = 0; g < KV4_KG; ++g) {
-      const float sc = half_at(KV4_OFF_KS + (g * 16 + kv4_quad(r)) * 2), mn = half_at(KV4_OFF_KM + r * 8 + g * 2);
+      const float sc = __half2float(__ushort_as_half(ks[nt][g])), mn = kv4_half(g == 2 ? km[nt].y : km[nt].x, g & 1);
+      const float s24 = sc * 0x1p24f, s20 = sc * 0x1p20f;
       uint4 *o = reinterpret_cast<uint4 *>(kd + 64 * g);
-      o[0] = kv4_word(nt ? kc[g].z : kc[g].x, sc, mn);
-      o[1] = kv4_word(nt ? kc[g].w : kc[g].y, sc, mn);
+      o[0] = kv4_word(nt ? kc[g].z : kc[g].x, s24, s20, mn);
+      o[1] = kv4_word(nt ? kc[g].w : kc[g].y, s24, s20, mn);
     }
   }
 #pragma unroll
@@ -134,10 +155,9 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
     uint16_t *vd = dst.v + (drow + r * step) * DV + 8 * q;
 #pragma unroll
     for (int g = 0; g < KV4_VG; ++g) {
-      const float sc = half_at(KV4_OFF_VS + (g * 16 + kv4_quad(r)) * 2);
-      const float mn = half_at(KV4_OFF_VM + (g * 16 + kv4_quad(r)) * 2);
+      const float sc = kv4_half(nt ? vs[g].y : vs[g].x, e), mn = kv4_half(nt ? vm[g].y : vm[g].x, e);
       const uint32_t w0 = nt ? vc[g].z : vc[g].x, w1 = nt ? vc[g].w : vc[g].y;
-      *reinterpret_cast<uint4 *>(vd + 64 * g) = kv4_word(__byte_perm(w0, w1, e ? 0x7632 : 0x5410), sc, mn);
+      *reinterpret_cast<uint4 *>(vd + 64 * g) = kv4_word(__byte_perm(w0, w1, e ? 0x7632 : 0x5410), sc * 0x1p24f, sc * 0x1p20f, mn);
     }
   }
 }

@@ -9,10 +9,12 @@
 // the table) or one of those ids, so no row waits for a table write and the
 // whole step is one launch.
 //
-// One cluster of GROW_CTAS CTAs: every CTA takes the same prefix sums over
-// the requests (rows and blocks) into shared memory, then its share of the
-// rows and of the new table entries.  The cluster's barrier stands between
-// the last read of the free count and its update, which may be in place.
+// Clusters of GROW_CTAS CTAs: every CTA takes the same prefix sums over the
+// requests (rows and blocks) into shared memory.  The first cluster then fills
+// the batch's rows and the new table entries; its barrier stands between the
+// last read of the free count and its update, which may be in place.  The
+// other clusters, as many as the row arrays ask for, write the -1 of the rows
+// behind the last token, which depend on no count.
 #include <cooperative_groups.h>
 
 #include "launch.h"
@@ -55,6 +57,7 @@ __global__ void __cluster_dims__(GROW_CTAS, 1, 1) __launch_bounds__(GROW_THREADS
   pdl_trigger();
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   const int rank = (int)cluster.block_rank();
+  const int part = (int)(blockIdx.x / GROW_CTAS), parts = (int)(gridDim.x / GROW_CTAS);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = A.block_size;
   const long long cap_pos = (long long)A.max_blocks * bs;
@@ -63,7 +66,7 @@ __global__ void __cluster_dims__(GROW_CTAS, 1, 1) __launch_bounds__(GROW_THREADS
     s_over = 0;
   }
   __syncthreads();
-  const int count = *A.count_in;
+  const int count = part == 0 ? *A.count_in : 0;
 
   // rows and new blocks of request i (none where it cannot be served)
   auto want = [&](int i, int &rows, int &blks) -> unsigned {
@@ -124,6 +127,17 @@ __global__ void __cluster_dims__(GROW_CTAS, 1, 1) __launch_bounds__(GROW_THREADS
     s_blk[A.n] = need;
   }
   __syncthreads();
+  if (part > 0) {  // rows past the last token (none when there are more tokens than rows)
+    if (s_over || total >= A.T) return;
+    const long long step = (long long)(parts - 1) * GROW_CTAS * GROW_THREADS;
+    for (long long r = total + ((long long)(part - 1) * GROW_CTAS + rank) * GROW_THREADS + tid; r < A.T; r += step) {
+      A.pos[r] = -1;
+      A.row_seq[r] = -1;
+      A.slots[r] = -1;
+    }
+    return;
+  }
+  const long long mine = parts > 1 && !s_over && total < A.T ? total : A.T;  // rows of this cluster
   // all or nothing: too many rows, or too few free blocks, make an empty step
   const bool rows_over = s_over || total > A.T;
   const bool short_of = !rows_over && (count < 0 || count > A.free_cap || need > count);
@@ -155,7 +169,7 @@ __global__ void __cluster_dims__(GROW_CTAS, 1, 1) __launch_bounds__(GROW_THREADS
       A.table[(long long)A.seqs[lo] * A.max_blocks + bi] = id;
     }
   }
-  for (long long r = me; r < A.T; r += stride) {
+  for (long long r = me; r < mine; r += stride) {
     long long p = -1, slot = -1;
     int s = -1;
     if (!none && r < total) {
@@ -200,7 +214,11 @@ cudaError_t launch_pages_grow(int32_t *table, int num_seqs, int max_blocks, int 
   const size_t smem = 2 * sizeof(int32_t) * ((size_t)GROW_MAX_N + 1);
   cudaError_t e = ensure_smem_limit(16, (const void *)pages_grow_kernel, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(pages_grow_kernel, dim3(GROW_CTAS), dim3(GROW_THREADS),
+  // one cluster writes 16K rows about as fast as the launch itself takes; beyond, more of them up to the GPU's SMs
+  long long parts = 1 + T / 16384;
+  const long long most = num_sms() / GROW_CTAS;
+  if (parts > most) parts = most > 1 ? most : 1;
+  return launch_pdl(pages_grow_kernel, dim3((unsigned)(GROW_CTAS * parts)), dim3(GROW_THREADS),
                     2 * sizeof(int32_t) * ((size_t)n + 1), st, A, status);
 }
 

@@ -633,3 +633,36 @@ def test_a_run_of_them_together(table):
     kvr.kv_pages_release_window(bt, nb, bs, seqs[:1].contiguous(), _ints([mb * bs], torch.int64), free, count, window=1)
     assert int(count) == nb - sum(-(-h // bs) for h in held[1:]) and (bt[2] == -1).all()
     assert kvr.device_status() == 0
+
+
+@pytest.mark.parametrize("by_slot", [False, True])
+@pytest.mark.parametrize("bs", [16, 48, 64])
+def test_append_runs(table, bs, by_slot):
+    """Runs of every kind in one call: whole tiles at every offset of the call, chunks that start and end inside a tile,
+    runs cut by padding, backwards and repeated order, neighbours in memory that are not neighbours in a sequence."""
+    gen = _gen(300 + bs)
+    hkv, S = 2, 8
+    pool = _pool(gen, S, hkv, 1024, bs, fill=0xEE)
+    runs = [(0, 0, 16), (1, 5, 11), (1, 16, 16), (1, 32, 37), (2, 3, 1), (0, 16, 100), (3, 1, 15), (4, 15, 1), (4, 16, 17),
+            (5, 500, 33), (None, 0, 7), (5, 533, 11), (6, 0, 15), (None, 0, 1), (6, 15, 1), (6, 16, 16), (7, 64, 64),
+            (2, 128, 64), (0, 116, 12), (3, 16, 16), (3, 32, 3)]
+    seq, pos = [], []
+    for s, lo, n in runs:
+        seq += [-1 if s is None else s] * n
+        pos += [-1] * n if s is None else list(range(lo, lo + n))
+    back = list(range(700, 732))[::-1]
+    seq += [7] * 32
+    pos += back
+    T = len(seq)
+    k, v = _kv(gen, T, hkv, 1.0)
+    seq_t, pos_t = _ints(seq, torch.int32), _ints(pos, torch.int64)
+    bt = pool.block_table.cpu().numpy()
+    places = [None if s < 0 else (int(bt[s, p // bs]), p % bs) for s, p in zip(seq, pos)]
+    want = _want_bytes(pool, k, v, places, pos_t, table)
+    if by_slot:
+        slots = _ints([-1 if pl is None else pl[0] * bs + pl[1] for pl in places], torch.int64)
+        kvr.kv4_append_rope(k, v, pos_t, None, table, VS, pool, slots=slots)
+    else:
+        kvr.kv4_append_rope(k, v, pos_t, seq_t, table, VS, pool)
+    assert np.array_equal(pool.data.cpu().numpy(), want)
+    assert kvr.device_status() == 0
