@@ -18,7 +18,6 @@
 // sink in the denominator (colibri "What the engine implements").
 #include <cuda.h>
 
-#include "decode_plan.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
 #include "warp_attn.cuh"
@@ -56,12 +55,12 @@ constexpr int FDW_SMEM = FD_HEAD + 1024 + FDW_SUBS * FD_STAGE;
 // a window's keys (at most WIN + 15 from its 16-key aligned start) over
 // blocks of at least 16 keys
 static_assert((WIN + 15 + 15) / 16 + 1 <= FDW_NB, "block ids of one window");
-// split plan (see decode_plan_kernel): the fixed cost of an item in keys,
+// split plan (see full_decode_plan_kernel): the fixed cost of an item in keys,
 // the longest split, and where the per-sequence item prefix starts in the
 // plan (after L and the item count, 256-byte aligned)
 constexpr long long FD_ITEM_KEYS = 300;
 constexpr long long FD_MAX_LEN = 8192 + 256;
-constexpr int DPLAN_PREFIX = DECODE_PLAN_PREFIX;
+constexpr int DPLAN_PREFIX = 64;
 
 // Full layer, phase 0: the split plan, from the batch's own contexts (one
 // CTA).  The split kernel is persistent with R = 2 CTAs per SM taking items
@@ -74,8 +73,217 @@ constexpr int DPLAN_PREFIX = DECODE_PLAN_PREFIX;
 // real item count (ties: fewer items), then writes L, the item count and the
 // per-sequence item prefix.  Sequences with a bad position or id get no items
 // (flagged here; the merge zeroes their rows).
+constexpr int DP_CANDS = 16;
 constexpr int DP_INLINE_MAX = 4096;
 constexpr int FD_EARLY_KEYS = 256;   // keys of a CTA's first item prefetched before the wait (B <= 32)  // batches the split kernel plans itself (prefix in shared memory)
+
+// The plan by one CTA of NT threads: the split length (returned), the item
+// count (*nitems) and the per-sequence item prefix (prefix[0..B]).  Flags bad
+// entries when `status` is not null.
+template <int NT>
+__device__ int decode_plan_block(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv,
+                                 int num_seqs, int64_t max_pos, long long max_ctx, int R, int32_t *prefix,
+                                 int *nitems, unsigned *status) {
+  constexpr int NW = NT / 32;
+  __shared__ long long s_tot[NW], s_mx[NW];
+  __shared__ int s_cnt[NW][DP_CANDS];
+  __shared__ int s_scan[NW];
+  __shared__ int s_L;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto ctx_of = [&](int b) -> long long {
+    const long long p = pos[b];
+    const int s = seq[b];
+    return (p >= 0 && p < max_pos && p + 1 <= max_ctx && s >= 0 && s < num_seqs) ? p + 1 : 0;
+  };
+  // 1. total keys, longest context, bad entries
+  long long tot = 0, mx = 0;
+  unsigned bad = 0;
+  for (int b = tid; b < B; b += NT) {
+    const long long p = pos[b];
+    const int s = seq[b];
+    const bool bp = p < 0 || p >= max_pos || p + 1 > max_ctx, bs = s < 0 || s >= num_seqs;
+    if (bp || bs) {
+      bad |= (bp ? ST_BAD_POS : 0u) | (bs ? ST_BAD_SEQ : 0u);
+    } else {
+      tot += p + 1;
+      mx = p + 1 > mx ? p + 1 : mx;
+    }
+  }
+  if (bad && status) flag(status, bad);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    const long long y = __shfl_xor_sync(0xffffffffu, mx, o);
+    mx = y > mx ? y : mx;
+  }
+  if (lane == 0) {
+    s_tot[warp] = tot;
+    s_mx[warp] = mx;
+  }
+  __syncthreads();
+  tot = 0;
+  mx = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    tot += s_tot[i];
+    mx = s_mx[i] > mx ? s_mx[i] : mx;
+  }
+  // 2. candidate split lengths: lane c of every warp derives candidate c and
+  // the warp shares them by shuffles (GB300's FP64 rate is a small fraction of
+  // its integer rate, so no double arithmetic here; one 64-bit division per
+  // lane, the rest in 32 bits as contexts and split lengths fit)
+  unsigned mine_L;
+  {
+    const unsigned k = lane % 8 + 1;
+    unsigned L;
+    if (lane < 8) {  // about k items per resident CTA for the longest context
+      unsigned n = k * (unsigned)R / ((unsigned)B * (unsigned)hkv);
+      if (n < 1) n = 1;
+      L = ((unsigned)mx + n - 1) / n;
+    } else {         // ... for the batch's total keys
+      const unsigned long long d = (unsigned long long)k * (unsigned)R;
+      const unsigned long long l = ((unsigned long long)tot * (unsigned)hkv + d - 1) / d;
+      L = l > (unsigned long long)FD_MAX_LEN ? (unsigned)FD_MAX_LEN : (unsigned)l;
+    }
+    L = (L + 63) / 64 * 64;
+    mine_L = L < 64 ? 64u : (L > (unsigned)FD_MAX_LEN ? (unsigned)FD_MAX_LEN : L);
+  }
+  unsigned cand[DP_CANDS];
+#pragma unroll
+  for (int c = 0; c < DP_CANDS; ++c) cand[c] = __shfl_sync(0xffffffffu, mine_L, c);
+  // 3. items of every candidate, one combined reduction
+  int cnt[DP_CANDS];
+#pragma unroll
+  for (int c = 0; c < DP_CANDS; ++c) cnt[c] = 0;
+  for (int b = tid; b < B; b += NT) {
+    const unsigned ctx = (unsigned)ctx_of(b);
+#pragma unroll
+    for (int c = 0; c < DP_CANDS; ++c) cnt[c] += (int)((ctx + cand[c] - 1) / cand[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < DP_CANDS; ++c) cnt[c] = __reduce_add_sync(0xffffffffu, cnt[c]);
+  if (lane == 0) {
+#pragma unroll
+    for (int c = 0; c < DP_CANDS; ++c) s_cnt[warp][c] = cnt[c];
+  }
+  __syncthreads();
+  // 4. choose: the least cost, ties to fewer items (one thread: measured
+  // quicker here than a warp-wide argmin)
+  if (tid == 0) {
+    unsigned best_L = (unsigned)FD_MAX_LEN, best_items = 0;
+    long long best_cost = -1;
+    for (int c = 0; c < DP_CANDS; ++c) {
+      unsigned items = 0;
+      for (int i = 0; i < NW; ++i) items += (unsigned)s_cnt[i][c];
+      items *= (unsigned)hkv;
+      const long long cost = (long long)((items + (unsigned)R - 1) / (unsigned)R) * (cand[c] + FD_ITEM_KEYS);
+      if (best_cost < 0 || cost < best_cost || (cost == best_cost && items < best_items)) {
+        best_cost = cost;
+        best_L = cand[c];
+        best_items = items;
+      }
+    }
+    s_L = (int)best_L;
+  }
+  __syncthreads();
+  const unsigned L = (unsigned)s_L;
+  // 5. per-sequence item prefix (exclusive scan, NT sequences at a time)
+  int running = 0;
+  for (int b0 = 0; b0 < B; b0 += NT) {
+    const int b = b0 + tid;
+    const int mine = b < B ? (int)(((unsigned)ctx_of(b) + L - 1) / L) * hkv : 0;
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      before += i < warp ? s_scan[i] : 0;
+      all += s_scan[i];
+    }
+    if (b < B) prefix[b] = running + before + x - mine;
+    running += all;
+    __syncthreads();  // s_scan is rewritten by the next round
+  }
+  if (tid == 0) prefix[B] = running;
+  *nitems = running;
+  return (int)L;
+}
+
+// The same plan made by one warp for a batch of at most 32 sequences (lane b
+// is sequence b): warp reductions and shuffles only, no block barrier.  Ties
+// between candidates of equal cost go to the lower candidate index.  The
+// split length and the item count go to prefix[B + 1] and prefix[B + 2].
+// Lane b < B passes sequence b's position p and id s (the other lanes
+// anything).
+__device__ void decode_plan_warp(long long p, int s, int B, int hkv,
+                                 int num_seqs, int64_t max_pos, long long max_ctx, int R, int32_t *prefix,
+                                 unsigned *status) {
+  constexpr unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  unsigned ctx = 0, bad = 0;
+  if (lane < B) {
+    const bool bp = p < 0 || p >= max_pos || p + 1 > max_ctx, bs = s < 0 || s >= num_seqs;
+    if (bp || bs)
+      bad = (bp ? ST_BAD_POS : 0u) | (bs ? ST_BAD_SEQ : 0u);
+    else
+      ctx = (unsigned)(p + 1);
+  }
+  if (bad && status) flag(status, bad);
+  const unsigned mx = __reduce_max_sync(FULL, ctx);
+  const unsigned long long tot = ((unsigned long long)__reduce_add_sync(FULL, ctx >> 16) << 16) +
+                                 __reduce_add_sync(FULL, ctx & 0xffffu);
+  // candidate `lane` (lanes 0 .. 15), as in decode_plan_block
+  unsigned mine_L;
+  {
+    const unsigned k = lane % 8 + 1;
+    unsigned L;
+    if (lane < 8) {
+      unsigned n = k * (unsigned)R / ((unsigned)B * (unsigned)hkv);
+      if (n < 1) n = 1;
+      L = (mx + n - 1) / n;
+    } else {
+      const unsigned long long d = (unsigned long long)k * (unsigned)R;
+      const unsigned long long l = (tot * (unsigned)hkv + d - 1) / d;
+      L = l > (unsigned long long)FD_MAX_LEN ? (unsigned)FD_MAX_LEN : (unsigned)l;
+    }
+    L = (L + 63) / 64 * 64;
+    mine_L = L < 64 ? 64u : (L > (unsigned)FD_MAX_LEN ? (unsigned)FD_MAX_LEN : L);
+  }
+  unsigned items_mine = 0;  // items of candidate `lane`
+#pragma unroll
+  for (int c = 0; c < DP_CANDS; ++c) {
+    const unsigned L = __shfl_sync(FULL, mine_L, c);
+    const unsigned n = __reduce_add_sync(FULL, (ctx + L - 1) / L);
+    if (lane == c) items_mine = n * (unsigned)hkv;
+  }
+  unsigned key = FULL;
+  if (lane < DP_CANDS) {
+    unsigned cost = (items_mine + (unsigned)R - 1) / (unsigned)R * (mine_L + FD_ITEM_KEYS);
+    cost = cost > 0x7ffffffu ? 0x7ffffffu : cost;
+    key = (cost << 4) | (unsigned)lane;
+  }
+  const unsigned L = __shfl_sync(FULL, mine_L, (int)(__reduce_min_sync(FULL, key) & 15u));
+  // per-sequence item prefix
+  const int mine = lane < B ? (int)((ctx + L - 1) / L) * hkv : 0;
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane < B) prefix[lane] = x - mine;
+  if (lane == 31) {
+    prefix[B] = x;
+    prefix[B + 1] = (int)L;
+    prefix[B + 2] = x;
+  }
+}
 
 static_assert(FD_WARPS * FD_STAGES * FD_STAGE >= (FD_WARPS * 16 * (MO_STRIDE + 2) + FD_WARPS * 16) * 4, "merge area");
 static_assert(FDW_SUBS * FD_STAGE >= (FD_WARPS * 16 * (MO_STRIDE + 2) + FD_WARPS * 16) * 4, "merge area");
@@ -109,7 +317,7 @@ __global__ void __launch_bounds__(FD_WARPS * 32, 2)
       pe = ld_early_s64(pos + lane);
       se = ld_early_s32(seq + lane);
     }
-    decode_plan_warp<FD_ITEM_KEYS, FD_MAX_LEN>(pe, se, B, pool.hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x, sPrefix, nullptr);
+    decode_plan_warp(pe, se, B, pool.hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x, sPrefix, nullptr);
     __syncwarp();
     const int L = sPrefix[B + 1];
     if ((int)blockIdx.x < sPrefix[B + 2]) {
@@ -151,7 +359,7 @@ __global__ void __launch_bounds__(FD_WARPS * 32, 2)
   // Windowed layer: one item per (sequence, KV head).
   // A batch of up to DP_INLINE_MAX sequences is planned by every CTA itself
   // (the same inputs give every CTA the same plan; CTA 0 stores it for the
-  // merge); a larger one by decode_plan_kernel before this kernel.
+  // merge); a larger one by full_decode_plan_kernel before this kernel.
   long long nitems = (long long)B * hkv;
   // windowed layer: bit j of ph is the parity of stage j's next phase, bit j
   // of pend marks a load into stage j not yet seen complete (this warp's
@@ -178,8 +386,8 @@ __global__ void __launch_bounds__(FD_WARPS * 32, 2)
             sq = seq[lane];
           }
           if (!__all_sync(0xffffffffu, p == pe && sq == se)) {
-            decode_plan_warp<FD_ITEM_KEYS, FD_MAX_LEN>(p, sq, B, hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x,
-                                                       sPrefix, blockIdx.x == 0 ? status : nullptr);
+            decode_plan_warp(p, sq, B, hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x, sPrefix,
+                             blockIdx.x == 0 ? status : nullptr);
           } else if (blockIdx.x == 0 && lane < B) {  // the early plan stands; its bad entries flagged here
             const bool bp = p < 0 || p >= max_pos || p + 1 > max_ctx, bs = sq < 0 || sq >= pool.num_seqs;
             if (bp || bs) flag(status, (bp ? ST_BAD_POS : 0u) | (bs ? ST_BAD_SEQ : 0u));
@@ -189,9 +397,8 @@ __global__ void __launch_bounds__(FD_WARPS * 32, 2)
         split_len = sPrefix[B + 1];
         n = sPrefix[B + 2];
       } else {
-        split_len = decode_plan_block<FD_WARPS * 32, FD_ITEM_KEYS, FD_MAX_LEN>(
-            pos, seq, B, hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x, sPrefix, &n,
-            blockIdx.x == 0 ? status : nullptr);
+        split_len = decode_plan_block<FD_WARPS * 32>(pos, seq, B, hkv, pool.num_seqs, max_pos, max_ctx, gridDim.x,
+                                                     sPrefix, &n, blockIdx.x == 0 ? status : nullptr);
       }
       nitems = n;
       if (blockIdx.x == 0) {
@@ -508,6 +715,25 @@ __global__ void __launch_bounds__(FD_WARPS * 32, 2)
   }
 }
 
+// Batches past DP_INLINE_MAX sequences: the plan by a kernel of its own,
+// written to the workspace for the split and merge kernels.
+constexpr int DP_THREADS = 256;
+
+__global__ void __launch_bounds__(DP_THREADS)
+    full_decode_plan_kernel(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv,
+                            int num_seqs, int64_t max_pos, long long max_ctx, int R, int32_t *__restrict__ plan,
+                            unsigned *status) {
+  pdl_wait();
+  pdl_trigger();
+  int nitems;
+  const int L = decode_plan_block<DP_THREADS>(pos, seq, B, hkv, num_seqs, max_pos, max_ctx, R,
+                                              plan + DPLAN_PREFIX, &nitems, status);
+  if (threadIdx.x == 0) {
+    plan[0] = L;
+    plan[1] = nitems;
+  }
+}
+
 // Full layer, phase 2: merge the splits of each (sequence, KV head, q head)
 // row by log-sum-exp and normalise.  NW warps per row (NW in {1, 2, 4, 8,
 // 16}, from the expected split count) fold interleaved subsets of the splits
@@ -629,7 +855,7 @@ __global__ void __launch_bounds__(FC_WARPS * 32)
 // ---------------------------------------------------------------------------
 
 // Uniform-batch estimate of the split plan (every sequence at max_ctx): the
-// first eight candidates of decode_plan_kernel.  The merge kernel sizes
+// first eight candidates of full_decode_plan_kernel.  The merge kernel sizes
 // its warps per row from it.  Measured with the plan taken this way: at batch
 // 1 and 4 one item per CTA beats eight short ones by 1.5x; at batch 16, four
 // per CTA beat an uneven 1.05; a cap of 8192 keys against 16K / 32K: the
@@ -698,7 +924,7 @@ cudaError_t launch_full_decode(const uint16_t *q, const int64_t *pos, const int3
   if (B <= DP_INLINE_MAX) {
     smem += ((B + 3) * 4 + 15) / 16 * 16;  // prefix[B + 1] and a split length and item count
   } else {
-    e = launch_pdl(decode_plan_kernel<FD_ITEM_KEYS, FD_MAX_LEN>, dim3(1), dim3(DP_THREADS), 0, st, pos, seq, B, hkv, pool.num_seqs, max_pos,
+    e = launch_pdl(full_decode_plan_kernel, dim3(1), dim3(DP_THREADS), 0, st, pos, seq, B, hkv, pool.num_seqs, max_pos,
                    max_ctx, R, plan, status);
     if (e != cudaSuccess) return e;
   }
@@ -707,23 +933,16 @@ cudaError_t launch_full_decode(const uint16_t *q, const int64_t *pos, const int3
                  pos, seq, B, hq, G, pool, table, max_pos, softmax_scale * LOG2E, max_ctx, (const int32_t *)plan, 0,
                  part_ml, part_o, status, 0, (const float *)nullptr, (uint16_t *)nullptr);
   if (e != cudaSuccess) return e;
-  const DecodePlan est = full_decode_plan(B, hkv, max_ctx);
-  return launch_full_combine(pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, plan, est.splits, part_ml, part_o,
-                             out, st);
-}
-
-cudaError_t launch_full_combine(const int64_t *pos, const int32_t *seq, int B, int hq, int hkv, int num_seqs,
-                                int64_t max_pos, long long max_ctx, const int32_t *plan, int est_splits,
-                                const float *part_ml, const float *part_o, uint16_t *out, cudaStream_t st) {
-  const int G = hq / hkv;
   // warps per merged row: about four splits each, at most sixteen
+  const DecodePlan est = full_decode_plan(B, hkv, max_ctx);
   int nw = 1;
-  while (nw < FC_WARPS && nw * 4 < est_splits) nw *= 2;
+  while (nw < FC_WARPS && nw * 4 < est.splits) nw *= 2;
   const long long rows = (long long)B * hkv * G;
   const long long ctas = (rows + FC_WARPS / nw - 1) / (FC_WARPS / nw);
   // a programmatic dependent of the split kernel (see full_combine_kernel)
   return launch_pdl(full_combine_kernel, dim3((unsigned)ctas), dim3(FC_WARPS * 32), 0, st, pos, seq, B, hq, G, hkv,
-                    num_seqs, max_pos, max_ctx, plan, nw, part_ml, part_o, out);
+                    pool.num_seqs, max_pos, max_ctx, (const int32_t *)plan, nw, (const float *)part_ml,
+                    (const float *)part_o, out);
 }
 
 cudaError_t launch_swa_decode_paged(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,

@@ -13,16 +13,18 @@
 // (bf16 keys meet them often).
 //
 // A warp takes four tokens of one KV head: lane 8i + c holds dims 8c..8c+7 of
-// a group of token i, five groups in turn, so the group's extrema are three
-// shuffles away and a 16-byte load brings a lane's values, all five in flight
-// at once.
+// a group of token i, so the group's extrema are three shuffles away and a
+// 16-byte load brings a lane's values, all five in flight before the
+// destination is looked up.
 //
-// A position's V codes are 32 pieces of 2 bytes, so writing tokens one by one
-// is bound by the stores' sectors, not by their bytes.  A CTA therefore owns
-// the runs of tokens (consecutive in the call and in one tile) that start
-// among its 16: when one of them is a whole tile, as all but the first and
-// last of a chunk are, the tile is put together in shared memory and leaves as
-// 16-byte stores of whole sectors.
+// What bounds it: about 650 instructions per four tokens (unpacking,
+// extrema, the exact quotient), 64 us for 302,216 (token, KV head) pairs where
+// their 820 bytes each take 37 us at the copy rate.  The scales of a token's
+// five groups are taken by five of its lanes at once (2 divisions instead of
+// 10 per lane), the codes in packed pairs.  The stores are 2 and 4 bytes wide
+// (a position's V codes lie apart) and merge in L2; putting whole tiles
+// together in shared memory first, for full-sector stores, measured slower
+// (73 us against 64): they are not what bounds it.
 #include "kv4.cuh"
 #include "launch.h"
 
@@ -30,9 +32,6 @@ namespace kvr {
 namespace {
 
 constexpr int K4A_WARPS = 4;
-constexpr int K4A_ITEMS = 4;                       // tokens of a warp
-constexpr int K4A_TOKENS = K4A_WARPS * K4A_ITEMS;  // and of a CTA
-static_assert(K4A_TOKENS == 16, "a CTA's tokens are as many as a tile's");
 constexpr unsigned FULLW = 0xffffffffu;
 
 // min and max that hand a NaN on
@@ -124,210 +123,167 @@ __device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], uint32_t sm, 
   return w;
 }
 
-__device__ __forceinline__ void load_token(const uint16_t *k, const uint16_t *v, size_t item, int c, uint4 (&raw)[5]) {
-  const uint4 *k4 = reinterpret_cast<const uint4 *>(k) + item * (DQK / 8);
-  const uint4 *v4 = reinterpret_cast<const uint4 *>(v) + item * (DV / 8);
-#pragma unroll
-  for (int g = 0; g < KV4_KG; ++g) raw[g] = k4[g * 8 + c];
-#pragma unroll
-  for (int g = 0; g < KV4_VG; ++g) raw[KV4_KG + g] = v4[g * 8 + c];
+// Where token t goes: block (-1: nowhere) and row in it; flags a token that
+// cannot be written where `say` is set.
+__device__ __forceinline__ void look_up(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq,
+                                        const int64_t *__restrict__ slots, long long t, int T, int64_t max_pos,
+                                        const Kv4View &dst, bool say, unsigned *status, int &blk, int &row, int &p) {
+  blk = -1;
+  row = p = 0;
+  if (t >= T) return;
+  const long long pp = pos[t];
+  const int s = slots ? 0 : seq[t];
+  unsigned bad = 0;
+  bool pad = s == -1;
+  if (slots) {
+    const long long slot = slots[t];
+    pad = slot < 0;
+    if (!pad) {
+      if (slot < (long long)dst.num_blocks * dst.block_size) {
+        // (a pool of 2^32 positions would be 781 GB)
+        blk = (int)((unsigned)slot / (unsigned)dst.block_size);
+        row = (int)((unsigned)slot - (unsigned)blk * (unsigned)dst.block_size);
+      } else {
+        bad = ST_BAD_BLOCK;
+      }
+    }
+  }
+  if (!pad && !bad) {
+    if (pp < 0 || pp >= max_pos) {
+      bad = ST_BAD_POS;
+    } else if (!slots) {
+      if (s < 0 || s >= dst.num_seqs) {
+        bad = ST_BAD_SEQ;
+      } else {
+        const unsigned bi = (unsigned)pp / (unsigned)dst.block_size;  // (max_pos < 2^31)
+        blk = bi < (unsigned)dst.max_blocks ? dst.block_table[(long long)s * dst.max_blocks + bi] : -1;
+        row = (int)((unsigned)pp - bi * (unsigned)dst.block_size);
+        if (blk < 0 || blk >= dst.num_blocks) bad = ST_BAD_BLOCK;
+      }
+    }
+  }
+  if (bad) {
+    blk = -1;
+    if (say) flag(status, bad);
+  } else {
+    p = (int)pp;
+  }
 }
 
-// early: load the CTA's own 16 tokens ahead of the look-up (they are the ones
-// it takes unless a run reaches into them: worth it when latency is all)
+// One token of four (lane 8i + c: token i): rotate, quantise and store to
+// position r of `tile` (null: nothing); p is its position.
+__device__ __forceinline__ void put_token(const uint4 (&raw)[5], const float *__restrict__ table, int p, float vscale,
+                                          uint8_t *tile, int r, int lane) {
+  const int c = lane & 7;
+  // group 0: rotate.  The other half of the pair lies four lanes away;
+  // products and sum are rounded one by one, so the result does not hang on
+  // contraction.
+  float x0[8];
+  {
+    float cs[16];
+    const float4 *tr = reinterpret_cast<const float4 *>(table + (long long)p * 64 + 16 * (c & 3));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4 f = tr[u];
+      cs[4 * u] = f.x; cs[4 * u + 1] = f.y; cs[4 * u + 2] = f.z; cs[4 * u + 3] = f.w;
+    }
+    uint4 o;
+    o.x = __shfl_xor_sync(FULLW, raw[0].x, 4);
+    o.y = __shfl_xor_sync(FULLW, raw[0].y, 4);
+    o.z = __shfl_xor_sync(FULLW, raw[0].z, 4);
+    o.w = __shfl_xor_sync(FULLW, raw[0].w, 4);
+    const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[0]), *oe = reinterpret_cast<const uint16_t *>(&o);
+    const uint32_t neg = c < 4 ? 0x80000000u : 0u;  // a - b, or a + b
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = __fmul_rn(bf2f(e[i]), cs[2 * i]), b = __fmul_rn(bf2f(oe[i]), cs[2 * i + 1]);
+      x0[i] = __fadd_rn(a, __uint_as_float(__float_as_uint(b) ^ neg));
+    }
+  }
+  // extrema of all groups, then lane g of the token's eight takes group g's
+  // scale (the divisions are most of a group's cost) and hands it round
+  float lo = x0[0], hi = x0[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = min_nan(lo, x0[i]);
+    hi = max_nan(hi, x0[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(FULLW, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(FULLW, hi, o));
+  }
+#pragma unroll
+  for (int g = 1; g < 5; ++g) {
+    float a, b;
+    extrema_bf16(raw[g], a, b);
+    lo = c == g ? a : lo;
+    hi = c == g ? b : hi;
+  }
+  if (c >= KV4_KG) {  // the scaled values' extrema are the extrema's products (swapped under a negative scale)
+    const float a = __fmul_rn(lo, vscale), b = __fmul_rn(hi, vscale);
+    lo = min_nan(a, b);
+    hi = max_nan(a, b);
+  }
+  uint32_t mysm;
+  float myr;
+  kv4_scale(lo, hi, mysm, myr);
+  if (tile && c < 5) {  // lane c writes group c's scale and minimum
+    const int q = kv4_quad(r) * 2;
+    const int at_s = c < KV4_KG ? KV4_OFF_KS + c * 32 + q : KV4_OFF_VS + (c - KV4_KG) * 32 + q;
+    const int at_m = c < KV4_KG ? KV4_OFF_KM + r * 8 + c * 2 : KV4_OFF_VM + (c - KV4_KG) * 32 + q;
+    *reinterpret_cast<uint16_t *>(tile + at_s) = (uint16_t)mysm;
+    *reinterpret_cast<uint16_t *>(tile + at_m) = (uint16_t)(mysm >> 16);
+  } else if (tile && c == 5) {
+    *reinterpret_cast<uint16_t *>(tile + KV4_OFF_KM + r * 8 + 6) = 0;
+  }
+  uint8_t *kd = tile + kv4_k_at(0, r, c >> 1) + (c & 1) * 4, *vd = tile + kv4_v_at(0, r, c, 0);
+#pragma unroll
+  for (int g = 0; g < 5; ++g) {
+    const uint32_t sm = __shfl_sync(FULLW, mysm, (lane & 24) + g);
+    const float rc = __shfl_sync(FULLW, myr, (lane & 24) + g);
+    float x[8];
+    const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[g]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = g == 0 ? x0[i] : g < KV4_KG ? bf2f(e[i]) : __fmul_rn(bf2f(e[i]), vscale);
+    const uint32_t w = kv4_codes(x, sm, rc);
+    if (tile) {
+      if (g < KV4_KG) {
+        *reinterpret_cast<uint32_t *>(kd + 512 * g) = w;
+      } else {
+        *reinterpret_cast<uint16_t *>(vd + 512 * (g - KV4_KG)) = (uint16_t)w;
+        *reinterpret_cast<uint16_t *>(vd + 512 * (g - KV4_KG) + 4) = (uint16_t)(w >> 16);
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(K4A_WARPS * 32)
     kv4_append_kernel(const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, const int64_t *__restrict__ pos,
-                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, int T,
-                      const float *__restrict__ table, int64_t max_pos, float vscale, Kv4View dst, int early,
-                      unsigned *status) {
-  constexpr int LOOK = 2 * K4A_TOKENS + 1;  // tokens looked up: one before the CTA's, and as many behind
-  __shared__ __align__(16) uint8_t s_img[KV4_TILE];
-  __shared__ int s_blk[LOOK], s_row[LOOK], s_pos[LOOK];
+                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, int T, long long warps,
+                      const float *__restrict__ table, int64_t max_pos, float vscale, Kv4View dst, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7;
-  const int h = (int)(blockIdx.x % (unsigned)dst.hkv), t0 = (int)(blockIdx.x / (unsigned)dst.hkv) * K4A_TOKENS;
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const long long w = (long long)blockIdx.x * K4A_WARPS + (threadIdx.x >> 5);
+  if (w >= warps) return;
+  const int h = (int)(w % dst.hkv);
+  const long long t = w / dst.hkv * 4 + (lane >> 3);
   uint4 raw[5];
 #pragma unroll
   for (int g = 0; g < 5; ++g) raw[g] = make_uint4(0, 0, 0, 0);
-  if (early) {
-    const int t = t0 + warp * K4A_ITEMS + (lane >> 3);
-    if (t < T) load_token(k, v, (size_t)t * dst.hkv + h, c, raw);
+  if (t < T) {
+    const size_t item = (size_t)t * dst.hkv + h;
+    const uint4 *k4 = reinterpret_cast<const uint4 *>(k) + item * (DQK / 8);
+    const uint4 *v4 = reinterpret_cast<const uint4 *>(v) + item * (DV / 8);
+#pragma unroll
+    for (int g = 0; g < KV4_KG; ++g) raw[g] = k4[g * 8 + c];
+#pragma unroll
+    for (int g = 0; g < KV4_VG; ++g) raw[KV4_KG + g] = v4[g * 8 + c];
   }
-
-  // 1. where the tokens go: block (-1: nowhere) and row in it
-  if (threadIdx.x < LOOK) {
-    const int t = t0 - 1 + (int)threadIdx.x;
-    int blk = -1;
-    unsigned row = 0, bad = 0;
-    long long p = 0;
-    if (t >= 0 && t < T) {
-      p = pos[t];
-      const int s = slots ? 0 : seq[t];
-      bool pad = s == -1;
-      if (slots) {
-        const long long slot = slots[t];
-        pad = slot < 0;
-        if (!pad) {
-          if (slot < (long long)dst.num_blocks * dst.block_size) {
-            // (a pool of 2^32 positions would be 781 GB)
-            blk = (int)((unsigned)slot / (unsigned)dst.block_size);
-            row = (unsigned)slot - (unsigned)blk * (unsigned)dst.block_size;
-          } else {
-            bad = ST_BAD_BLOCK;
-          }
-        }
-      }
-      if (!pad && !bad) {
-        if (p < 0 || p >= max_pos) {
-          bad = ST_BAD_POS;
-        } else if (!slots) {
-          if (s < 0 || s >= dst.num_seqs) {
-            bad = ST_BAD_SEQ;
-          } else {
-            const unsigned bi = (unsigned)p / (unsigned)dst.block_size;  // (max_pos < 2^31)
-            blk = bi < (unsigned)dst.max_blocks ? dst.block_table[(long long)s * dst.max_blocks + bi] : -1;
-            row = (unsigned)p - bi * (unsigned)dst.block_size;
-            if (blk < 0 || blk >= dst.num_blocks) bad = ST_BAD_BLOCK;
-          }
-        }
-      }
-      if (bad) {
-        blk = -1;
-        if (h == 0 && threadIdx.x >= 1 && threadIdx.x <= K4A_TOKENS) flag(status, bad);
-      }
-    }
-    s_blk[threadIdx.x] = blk;
-    s_row[threadIdx.x] = (int)row;
-    s_pos[threadIdx.x] = (int)p;
-  }
-  __syncthreads();
-  // 2. runs: entry j (token t0 - 1 + j) goes on with the one before it when
-  // both go to the same tile and its row is the next.  Bit j - 1 of `starts`
-  // is set where entry j does not.
-  uint32_t starts, heads;
-  {
-    const int j = lane + 1, blk = s_blk[j], row = s_row[j];
-    starts = __ballot_sync(FULLW, !(blk >= 0 && blk == s_blk[j - 1] && row == s_row[j - 1] + 1 && (row & 15)));
-    heads = __ballot_sync(FULLW, blk >= 0 && !(row & 15));  // entries at a tile's first row
-  }
-  // the CTA's tokens: from the first run that starts among its 16 to the first that starts behind them (a run has at
-  // most 16 tokens, so there is one)
-  const uint32_t own = starts & 0xffffu, after = starts & 0xffff0000u;
-  const int first = own ? __ffs(own) : LOOK;
-  int end = after ? __ffs(after) : LOOK;
-  if (end > T - t0 + 1) end = T - t0 + 1;
-  if (first >= end) return;
-  // the whole tile among them, if there is one: its first entry, followed by 15 that go on
-  uint32_t on = ~starts >> 1;  // bit j - 1: entry j + 1 goes on
-  on &= on >> 1;
-  on &= on >> 2;
-  on &= on >> 4;               // eight in a row
-  on &= on >> 7;               // fifteen
-  const uint32_t whole = own & heads & on;
-  const int full = whole && __ffs(whole) + 16 <= end ? __ffs(whole) : -1;
-
-  for (int j0 = first; j0 < end; j0 += K4A_TOKENS) {
-    const int j = j0 + warp * K4A_ITEMS + (lane >> 3);
-    uint8_t *tile = nullptr;
-    int r = 0, p = 0;
-    if (j < end && s_blk[j] >= 0) {
-      if (!early || j0 != 1) load_token(k, v, (size_t)(t0 - 1 + j) * dst.hkv + h, c, raw);
-      p = s_pos[j];
-      r = s_row[j] & 15;
-      tile = full >= 0 && j >= full && j < full + 16 ? s_img : dst.data + kv4_tile(dst, s_blk[j], h, s_row[j]);
-    }
-
-    // group 0: rotate.  The other half of the pair lies four lanes away;
-    // products and sum are rounded one by one, so the result does not hang on
-    // contraction.
-    float x0[8];
-    {
-      float cs[16];
-      const float4 *tr = reinterpret_cast<const float4 *>(table + (long long)p * 64 + 16 * (c & 3));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float4 f = tr[u];
-        cs[4 * u] = f.x; cs[4 * u + 1] = f.y; cs[4 * u + 2] = f.z; cs[4 * u + 3] = f.w;
-      }
-      uint4 o;
-      o.x = __shfl_xor_sync(FULLW, raw[0].x, 4);
-      o.y = __shfl_xor_sync(FULLW, raw[0].y, 4);
-      o.z = __shfl_xor_sync(FULLW, raw[0].z, 4);
-      o.w = __shfl_xor_sync(FULLW, raw[0].w, 4);
-      const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[0]), *oe = reinterpret_cast<const uint16_t *>(&o);
-      const uint32_t neg = c < 4 ? 0x80000000u : 0u;  // a - b, or a + b
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = __fmul_rn(bf2f(e[i]), cs[2 * i]), b = __fmul_rn(bf2f(oe[i]), cs[2 * i + 1]);
-        x0[i] = __fadd_rn(a, __uint_as_float(__float_as_uint(b) ^ neg));
-      }
-    }
-    // extrema of all groups, then lane g of the token's eight takes group g's
-    // scale (the divisions are most of a group's cost) and hands it round
-    float lo[5], hi[5];
-    lo[0] = hi[0] = x0[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      lo[0] = min_nan(lo[0], x0[i]);
-      hi[0] = max_nan(hi[0], x0[i]);
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      lo[0] = min_nan(lo[0], __shfl_xor_sync(FULLW, lo[0], o));
-      hi[0] = max_nan(hi[0], __shfl_xor_sync(FULLW, hi[0], o));
-    }
-#pragma unroll
-    for (int g = 1; g < 5; ++g) {
-      extrema_bf16(raw[g], lo[g], hi[g]);
-      if (g >= KV4_KG) {  // the scaled values' extrema are the extrema's products (swapped under a negative scale)
-        const float a = __fmul_rn(lo[g], vscale), b = __fmul_rn(hi[g], vscale);
-        lo[g] = min_nan(a, b);
-        hi[g] = max_nan(a, b);
-      }
-    }
-    float mylo = lo[0], myhi = hi[0];
-#pragma unroll
-    for (int g = 1; g < 5; ++g) {
-      mylo = c == g ? lo[g] : mylo;
-      myhi = c == g ? hi[g] : myhi;
-    }
-    uint32_t mysm;
-    float myr;
-    kv4_scale(mylo, myhi, mysm, myr);
-    if (tile && c < 5) {  // lane c writes group c's scale and minimum
-      const int q = kv4_quad(r);
-      const int at_s = c < KV4_KG ? KV4_OFF_KS + c * 32 + q * 2 : KV4_OFF_VS + (c - KV4_KG) * 32 + q * 2;
-      const int at_m = c < KV4_KG ? KV4_OFF_KM + r * 8 + c * 2 : KV4_OFF_VM + (c - KV4_KG) * 32 + q * 2;
-      *reinterpret_cast<uint16_t *>(tile + at_s) = (uint16_t)mysm;
-      *reinterpret_cast<uint16_t *>(tile + at_m) = (uint16_t)(mysm >> 16);
-    } else if (tile && c == 5) {
-      *reinterpret_cast<uint16_t *>(tile + KV4_OFF_KM + r * 8 + 6) = 0;
-    }
-#pragma unroll
-    for (int g = 0; g < 5; ++g) {
-      const uint32_t sm = __shfl_sync(FULLW, mysm, (lane & 24) + g);
-      const float rc = __shfl_sync(FULLW, myr, (lane & 24) + g);
-      float x[8];
-      const uint16_t *e = reinterpret_cast<const uint16_t *>(&raw[g]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = g == 0 ? x0[i] : g < KV4_KG ? bf2f(e[i]) : __fmul_rn(bf2f(e[i]), vscale);
-      const uint32_t w = kv4_codes(x, sm, rc);
-      if (tile) {
-        if (g < KV4_KG) {
-          *reinterpret_cast<uint32_t *>(tile + kv4_k_at(g, r, c >> 1) + (c & 1) * 4) = w;
-        } else {
-          *reinterpret_cast<uint16_t *>(tile + kv4_v_at(g - KV4_KG, r, c, 0)) = (uint16_t)w;
-          *reinterpret_cast<uint16_t *>(tile + kv4_v_at(g - KV4_KG, r, c, 1)) = (uint16_t)(w >> 16);
-        }
-      }
-    }
-  }
-  if (full >= 0) {  // (the same for the whole CTA)
-    __syncthreads();
-    uint4 *o = reinterpret_cast<uint4 *>(dst.data + kv4_tile(dst, s_blk[full], h, s_row[full]));
-    for (int i = threadIdx.x; i < KV4_TILE / 16; i += K4A_WARPS * 32) o[i] = reinterpret_cast<const uint4 *>(s_img)[i];
-  }
+  int blk, row, p;
+  look_up(pos, seq, slots, t, T, max_pos, dst, h == 0 && c == 0, status, blk, row, p);
+  put_token(raw, table, p, vscale, blk >= 0 ? dst.data + kv4_tile(dst, blk, h, row) : nullptr, row & 15, lane);
 }
 
 }  // namespace
@@ -335,10 +291,10 @@ __global__ void __launch_bounds__(K4A_WARPS * 32)
 cudaError_t launch_kv4_append(const uint16_t *k, const uint16_t *v, const int64_t *pos, const int32_t *seq,
                               const int64_t *slots, int T, const float *table, int64_t max_pos, float value_scale,
                               const Kv4View &dst, unsigned *status, cudaStream_t st) {
-  const long long ctas = (long long)((T + (long long)K4A_TOKENS - 1) / K4A_TOKENS) * dst.hkv;
+  const long long warps = ((long long)T + 3) / 4 * dst.hkv, ctas = (warps + K4A_WARPS - 1) / K4A_WARPS;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(kv4_append_kernel, dim3((unsigned)ctas), dim3(K4A_WARPS * 32), 0, st, k, v, pos, seq, slots, T,
-                    table, max_pos, value_scale, dst, ctas <= 4 * num_sms() ? 1 : 0, status);
+                    warps, table, max_pos, value_scale, dst, status);
 }
 
 }  // namespace kvr

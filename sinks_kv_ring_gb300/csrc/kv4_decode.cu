@@ -37,7 +37,6 @@
 // both busy: each warp streams its own 32-key units through its own ring of
 // bulk copies (one copy brings a tile's codes and scales), with no barrier
 // between warps inside an item.
-#include "decode_plan.cuh"
 #include "kv4.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
@@ -57,17 +56,23 @@ constexpr int K4_STAGES = 2;
 constexpr int K4_STAGE = K4_TILES * KV4_TILE;
 constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
-// split plan: an item's fixed cost in keys and the longest split
-constexpr long long K4_ITEM_KEYS = 700;
-constexpr long long K4_MAX_LEN = 16384 + 256;
-constexpr int K4_INLINE_MAX = 128;   // batches the split kernel plans itself
+// The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW
+// units of set-up and then its keys in units of K4_UNIT; CTA c takes units
+// c L .. (c + 1) L - 1 of the line, L = total / CTAs (at least one unit per
+// warp), so all CTAs end together whatever the contexts are, and a row is cut
+// only where a CTA's share ends.  The part of row r in CTA c is piece c + r:
+// no two pieces share a number, and a row's are consecutive.
+constexpr int K4_ROW = 16;           // a row's set-up and merge, in units (48 ragged rows: 8 -> 58 us, 16 -> 53, 32 -> 57)
+constexpr int K4_MIN = K4_WARPS;     // least share (twice that costs 0.9 us at 513 keys)
+constexpr int K4_PLAN = 32;          // int64 words of the plan ahead of the rows' prefix: L
+constexpr int K4_INLINE_MAX = 512;   // batches the split kernel plans itself
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
 constexpr int K4_OFF_QX = 12 * 512;
 constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
 constexpr int K4_OFF_BAR = K4_OFF_ROW + 64;
 constexpr int K4_OFF_ABORT = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;
 constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
-constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 3) * 4 / 16 * 16 + 16;
+constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
 static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16) * 4, "merge area");
@@ -166,6 +171,80 @@ __device__ __forceinline__ void kv4_query(const uint16_t *__restrict__ qh, int G
   }
 }
 
+// Units of keys of sequence b; 0 (flagged once) where its position or id is
+// out of range: such a row has no part of the line, and the merge writes zeros.
+__device__ __forceinline__ int kv4_units(long long p, int s, int num_seqs, int64_t max_pos, long long max_ctx,
+                                         unsigned *status) {
+  const bool bp = p < 0 || p >= max_pos || p + 1 > max_ctx, bs = s < 0 || s >= num_seqs;
+  if (bp || bs) {
+    if (status) flag(status, (bp ? ST_BAD_POS : 0u) | (bs ? ST_BAD_SEQ : 0u));
+    return 0;
+  }
+  return (int)((p + K4_UNIT) / K4_UNIT);
+}
+
+// The line's prefix over the sequences (prefix[b]: units ahead of sequence b)
+// by NT threads; returns L.
+template <int NT>
+__device__ long long kv4_plan(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv,
+                              int num_seqs, int64_t max_pos, long long max_ctx, int ctas, int64_t *prefix,
+                              unsigned *status) {
+  __shared__ long long s_sum[NT / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long base = 0;
+  for (int b0 = 0; b0 < B; b0 += NT) {
+    const int b = b0 + tid;
+    long long x = 0;
+    if (b < B) {
+      const int u = kv4_units(pos[b], seq[b], num_seqs, max_pos, max_ctx, status);
+      x = u ? (long long)hkv * (u + K4_ROW) : 0;
+    }
+    const long long mine = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(FULLW, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    long long before = base;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+      before += i < warp ? s_sum[i] : 0;
+      base += s_sum[i];
+    }
+    if (b < B) prefix[b] = before + x - mine;
+    __syncthreads();  // s_sum is rewritten by the next round
+  }
+  if (tid == 0) prefix[B] = base;
+  __syncthreads();
+  const long long L = (base + ctas - 1) / ctas;
+  return L < K4_MIN ? K4_MIN : L;
+}
+
+// Sequence of unit x of the line: the last b with prefix[b] <= x whose part is not empty (x < prefix[B]).
+__device__ __forceinline__ int kv4_find(const int64_t *prefix, int B, long long x) {
+  int lo = 0, hi = B;  // prefix[lo] <= x < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+constexpr int K4P_THREADS = 256;
+
+// Batches past K4_INLINE_MAX rows: the plan by a kernel of its own.
+__global__ void __launch_bounds__(K4P_THREADS)
+    kv4_plan_kernel(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv, int num_seqs,
+                    int64_t max_pos, long long max_ctx, int ctas, int64_t *__restrict__ plan, unsigned *status) {
+  pdl_wait();
+  pdl_trigger();
+  const long long L =
+      kv4_plan<K4P_THREADS>(pos, seq, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + K4_PLAN, status);
+  if (threadIdx.x == 0) plan[0] = L;
+}
+
 struct K4Args {
   const uint16_t *q;
   const int64_t *pos;
@@ -176,7 +255,7 @@ struct K4Args {
   int64_t max_pos;
   float scale_log2;
   long long max_ctx;
-  int32_t *plan;
+  int64_t *plan;
   float *part_ml;
   float *part_o;
   unsigned *status;
@@ -191,7 +270,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   const uint32_t sBar = sBase + K4_OFF_BAR + 8 * K4_STAGES * warp;
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + K4_OFF_ABORT);
   uint8_t *const sStage = smem + K4_OFF_STAGE + warp * K4_STAGES * K4_STAGE;
-  int32_t *sPrefix = reinterpret_cast<int32_t *>(smem + K4_OFF_PLAN);
+  int64_t *sPrefix = reinterpret_cast<int64_t *>(smem + K4_OFF_PLAN);
   if (lane == 0) {
     for (int j = 0; j < K4_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
     if (warp == 0) *abort_flag = 0;
@@ -201,41 +280,19 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   pdl_trigger();
   __syncthreads();
 
-  // the plan (see full_decode_kernel): every CTA makes it for small batches,
-  // CTA 0 stores it for the merge
-  const int32_t *prefix = A.plan + DECODE_PLAN_PREFIX;
-  int split_len, nitems;
+  // the plan: every CTA makes it for small batches, CTA 0 stores it for the merge
+  const int64_t *prefix = A.plan + K4_PLAN;
+  long long L;
   if (A.B <= K4_INLINE_MAX) {
-    unsigned *st = blockIdx.x == 0 ? A.status : nullptr;
-    if (A.B <= 32) {
-      if (warp == 0) {
-        long long p = 0;
-        int s = 0;
-        if (lane < A.B) {
-          p = A.pos[lane];
-          s = A.seq[lane];
-        }
-        decode_plan_warp<K4_ITEM_KEYS, K4_MAX_LEN>(p, s, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x,
-                                                   sPrefix, st);
-      }
-      __syncthreads();
-      split_len = sPrefix[A.B + 1];
-      nitems = sPrefix[A.B + 2];
-    } else {
-      split_len = decode_plan_block<K4_WARPS * 32, K4_ITEM_KEYS, K4_MAX_LEN>(
-          A.pos, A.seq, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, &nitems, st);
-    }
+    L = kv4_plan<K4_WARPS * 32>(A.pos, A.seq, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix,
+                                blockIdx.x == 0 ? A.status : nullptr);
     if (blockIdx.x == 0) {
-      for (int b = tid; b <= A.B; b += blockDim.x) A.plan[DECODE_PLAN_PREFIX + b] = sPrefix[b];
-      if (tid == 0) {
-        A.plan[0] = split_len;
-        A.plan[1] = nitems;
-      }
+      for (int b = tid; b <= A.B; b += blockDim.x) A.plan[K4_PLAN + b] = sPrefix[b];
+      if (tid == 0) A.plan[0] = L;
     }
     prefix = sPrefix;
   } else {
-    split_len = A.plan[0];
-    nitems = A.plan[1];
+    L = A.plan[0];
   }
 
   const int tpb = A.pool.block_size >> 4;
@@ -244,12 +301,18 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   uint32_t sent = 0;  // and issued
   bool gave_up = false;
 
-  for (int w = blockIdx.x; w < nitems; w += gridDim.x) {
-    const int b = plan_find(prefix, A.B, w);
-    const int local = w - prefix[b], split = local / hkv, kv = local - split * hkv;
+  const long long line_end = min((blockIdx.x + 1) * L, (long long)prefix[A.B]);
+  for (long long x = blockIdx.x * L; x < line_end;) {
+    const int b = kv4_find(prefix, A.B, x);
+    const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
+    const int kv = (int)((x - prefix[b]) / rowlen), off = (int)(x - prefix[b] - (long long)kv * rowlen);
+    const int stop = (int)min((long long)rowlen, off + (line_end - x));
+    x += stop - off;
+    if (stop <= K4_ROW) continue;  // set-up alone: no piece
+    const int w = (int)blockIdx.x + b * hkv + kv;
     const long long p = A.pos[b];
-    const int s = A.seq[b];  // (a sequence with items has a valid position and id)
-    const int key_lo = split * split_len, key_hi = (int)min((long long)key_lo + split_len, p + 1);
+    const int s = A.seq[b];  // (a sequence on the line has a valid position and id)
+    const int key_lo = max(off - K4_ROW, 0) * K4_UNIT, key_hi = (int)min((long long)(stop - K4_ROW) * K4_UNIT, p + 1);
     const int nunit = (key_hi - key_lo + K4_UNIT - 1) / K4_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
@@ -597,25 +660,118 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K4_STAGES), (seen / K4_STAGES) & 1u, &never);
 }
 
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-size_t plan_bytes(int B) { return align256(((size_t)DECODE_PLAN_PREFIX + B + 1) * 4); }
+// Merge of a row's pieces by log-sum-exp, and normalisation: NW warps per
+// (sequence, KV head, q head) fold interleaved pieces, lane l the value dims
+// 4l..4l+3, K4M_K pieces' loads in flight at a time; the row's first warp
+// joins them.
+constexpr int K4M_WARPS = 16;
+constexpr int K4M_K = 8;
 
-// Most items a device plan can give (see decode_plan_block): about k <= 8 items
-// per resident CTA and one partial split per (sequence, KV head), but none
-// shorter than 64 keys; or the splits that the longest split forces.
-long long items_cap(int B, int hkv, long long max_ctx) {
-  const long long R = (long long)K4_CTAS * num_sms(), units = (long long)B * hkv;
-  long long a = 8 * R + units;
-  const long long most = units * ((max_ctx + 63) / 64), c = units * ((max_ctx + K4_MAX_LEN - 1) / K4_MAX_LEN);
-  if (a > most) a = most;
-  return a > c ? a : c;
+__global__ void __launch_bounds__(K4M_WARPS * 32)
+    kv4_merge_kernel(int B, int hq, int G, int hkv,
+                     const int64_t *__restrict__ plan, int nw, const float *__restrict__ part_ml,
+                     const float *__restrict__ part_o, uint16_t *__restrict__ out) {
+  __shared__ float s_ml[K4M_WARPS][2];
+  __shared__ float4 s_acc[K4M_WARPS][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % nw;
+  const long long row = (long long)blockIdx.x * (K4M_WARPS / nw) + warp / nw;  // (b hkv + kv) G + g
+  const bool have = row < (long long)B * hq;
+  const int g = have ? (int)(row % G) : 0, pair = have ? (int)(row / G) : 0, b = pair / hkv, kv = pair - b * hkv;
+  pdl_wait();
+  pdl_trigger();
+  const long long L = plan[0], at = have ? plan[K4_PLAN + b] : 0;
+  const long long len = have ? (plan[K4_PLAN + b + 1] - at) / hkv : 0;  // 0: nothing to attend to
+  long long c0 = 0;
+  int n = 0;
+  if (len > 0) {
+    c0 = (at + kv * len + K4_ROW) / L;
+    n = (int)((at + kv * len + len - 1) / L - c0) + 1;
+  }
+  float M = NEG_INF, S = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = sub; i0 < n; i0 += K4M_K * nw) {
+    float2 ml[K4M_K];
+    float4 o[K4M_K];
+#pragma unroll
+    for (int k = 0; k < K4M_K; ++k) {
+      const int i = i0 + k * nw;
+      ml[k] = make_float2(NEG_INF, 0.f);
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const long long r = (c0 + i + pair) * G + g;
+        ml[k] = *reinterpret_cast<const float2 *>(part_ml + r * 2);
+        o[k] = *reinterpret_cast<const float4 *>(part_o + r * DV + 4 * lane);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int k = 0; k < K4M_K; ++k) Mn = fmaxf(Mn, ml[k].x);
+    if (Mn == NEG_INF) continue;  // nothing yet (pieces without a block of the pool)
+    const float c = ex2(M - Mn);  // M = -inf gives 0
+    S *= c;
+    acc.x *= c;
+    acc.y *= c;
+    acc.z *= c;
+    acc.w *= c;
+#pragma unroll
+    for (int k = 0; k < K4M_K; ++k) {
+      const float f = ex2(ml[k].x - Mn);
+      S += ml[k].y * f;
+      acc.x += o[k].x * f;
+      acc.y += o[k].y * f;
+      acc.z += o[k].z * f;
+      acc.w += o[k].w * f;
+    }
+    M = Mn;
+  }
+  if (nw > 1) {
+    if (lane == 0) {
+      s_ml[warp][0] = M;
+      s_ml[warp][1] = S;
+    }
+    s_acc[warp][lane] = acc;
+    __syncthreads();
+    if (sub == 0) {
+      float Mt = NEG_INF;
+      for (int u = 0; u < nw; ++u) Mt = fmaxf(Mt, s_ml[warp + u][0]);
+      S = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (Mt != NEG_INF) {
+        for (int u = 0; u < nw; ++u) {
+          const float mu = s_ml[warp + u][0];
+          if (mu == NEG_INF) continue;
+          const float f = ex2(mu - Mt);
+          const float4 o = s_acc[warp + u][lane];
+          S += s_ml[warp + u][1] * f;
+          acc.x += o.x * f;
+          acc.y += o.y * f;
+          acc.z += o.z * f;
+          acc.w += o.w * f;
+        }
+      }
+    }
+  }
+  if (!have || sub != 0) return;
+  const float inv = S == 0.f ? 0.f : 1.f / S;  // (a NaN sum stays one)
+  *reinterpret_cast<uint2 *>(out + ((long long)b * hq + (long long)kv * G + g) * DV + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+size_t plan_bytes(int B) { return align256(((size_t)K4_PLAN + B + 1) * 8); }
+
+// Piece numbers: one per CTA that can have a share (of K4_MIN units at least) and one per row.
+size_t pieces_cap(int B, int hkv, long long max_ctx) {
+  const long long rows = (long long)B * hkv, R = (long long)K4_CTAS * num_sms();
+  const long long most = (rows * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW) + K4_MIN - 1) / K4_MIN;
+  return (size_t)(rows + (most < R ? most : R));
 }
 
 }  // namespace
 
 size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
-  const size_t items = (size_t)items_cap(B, hkv, max_ctx), G = (size_t)(hq / hkv);
-  return plan_bytes(B) + align256(items * G * 2 * sizeof(float)) + align256(items * G * DV * sizeof(float));
+  const size_t n = pieces_cap(B, hkv, max_ctx), G = (size_t)(hq / hkv);
+  return plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
 }
 
 cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
@@ -624,7 +780,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   cudaError_t e = ensure_smem_limit(17, (const void *)kv4_decode_kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
   const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
-  const size_t items = (size_t)items_cap(B, hkv, max_ctx);
+  const size_t pieces = pieces_cap(B, hkv, max_ctx);
   K4Args A;
   A.q = q;
   A.pos = pos;
@@ -637,24 +793,29 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   A.max_pos = max_pos;
   A.scale_log2 = softmax_scale * LOG2E;
   A.max_ctx = max_ctx;
-  A.plan = reinterpret_cast<int32_t *>(ws);
+  A.plan = reinterpret_cast<int64_t *>(ws);
   uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + plan_bytes(B);
   A.part_ml = reinterpret_cast<float *>(w8);
-  A.part_o = reinterpret_cast<float *>(w8 + align256(items * G * 2 * sizeof(float)));
+  A.part_o = reinterpret_cast<float *>(w8 + align256(pieces * G * 2 * sizeof(float)));
   A.status = status;
   const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
   A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
+  // (a CTA whose share would lie past the line has nothing to do)
+  const int ctas = (int)(pieces - (size_t)B * hkv);
   if (B > K4_INLINE_MAX) {
-    e = launch_pdl(decode_plan_kernel<K4_ITEM_KEYS, K4_MAX_LEN>, dim3(1), dim3(DP_THREADS), 0, st, pos, seq, B, hkv,
-                   pool.num_seqs, max_pos, max_ctx, R, A.plan, status);
+    e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(K4P_THREADS), 0, st, pos, seq, B, hkv, pool.num_seqs, max_pos,
+                   max_ctx, ctas, A.plan, status);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(kv4_decode_kernel, dim3((unsigned)R), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
+  e = launch_pdl(kv4_decode_kernel, dim3((unsigned)ctas), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
   if (e != cudaSuccess) return e;
-  const long long units = (long long)B * hkv;
-  const int est = (int)((R + units - 1) / units);
-  return launch_full_combine(pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, A.plan, est, A.part_ml, A.part_o,
-                             out, st);
+  // warps per merged row: about four pieces each
+  const int est = (int)(R / ((long long)B * hkv)) + 1;
+  int nw = 1;
+  while (nw < K4M_WARPS && nw * 4 < est) nw *= 2;
+  const long long blocks = ((long long)B * hq + K4M_WARPS / nw - 1) / (K4M_WARPS / nw);
+  return launch_pdl(kv4_merge_kernel, dim3((unsigned)blocks), dim3(K4M_WARPS * 32), 0, st, B, hq, G, hkv,
+                    (const int64_t *)A.plan, nw, (const float *)A.part_ml, (const float *)A.part_o, out);
 }
 
 }  // namespace kvr

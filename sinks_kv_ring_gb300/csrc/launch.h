@@ -90,12 +90,6 @@ cudaError_t launch_full_decode(const uint16_t *q, const int64_t *pos, const int3
                                float softmax_scale, long long max_ctx, void *ws, uint16_t *out,
                                unsigned *status, cudaStream_t st);
 
-// Merge of a split decode's partials by log-sum-exp (fp32 (m, l) and numerators per item and q head), launched as a
-// programmatic dependent of the split kernel; est_splits: about how many splits a row has.
-cudaError_t launch_full_combine(const int64_t *pos, const int32_t *seq, int B, int hq, int hkv, int num_seqs,
-                                int64_t max_pos, long long max_ctx, const int32_t *plan, int est_splits,
-                                const float *part_ml, const float *part_o, uint16_t *out, cudaStream_t st);
-
 cudaError_t launch_full_prefill(const uint16_t *q, int64_t P0, int C, int seq, int hq, const KvView &pool,
                                 const float *table, int64_t max_pos, float softmax_scale, uint16_t *out,
                                 unsigned *status, cudaStream_t st);
