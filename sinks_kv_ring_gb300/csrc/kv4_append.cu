@@ -165,9 +165,8 @@ __device__ __forceinline__ void look_up(const int64_t *__restrict__ pos, const i
   if (bad) {
     blk = -1;
     if (say) flag(status, bad);
-  } else {
-    p = (int)pp;
   }
+  if (blk >= 0) p = (int)pp;  // (a token that goes nowhere rotates by row 0: its position may be anything)
 }
 
 // One token of four (lane 8i + c: token i): rotate, quantise and store to
