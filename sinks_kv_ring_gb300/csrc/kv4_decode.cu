@@ -55,7 +55,9 @@ constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
 constexpr int K4_STAGES = 2;
 constexpr int K4_STAGE = K4_TILES * KV4_TILE;
 constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
+constexpr int K4_FOLD = 16;          // units between foldings of the minima's sum (1 us of 292 at batch 64; 4 costs 4)
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
+constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the bias as it is: below 2, times 2^14
 // The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW
 // units of set-up and then its keys in units of K4_UNIT; CTA c takes units
 // c L .. (c + 1) L - 1 of the line, L = total / CTAs (at least one unit per
@@ -69,7 +71,8 @@ constexpr int K4_INLINE_MAX = 512;   // batches the split kernel plans itself
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
 constexpr int K4_OFF_QX = 12 * 512;
 constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
-constexpr int K4_OFF_BAR = K4_OFF_ROW + 64;
+constexpr int K4_OFF_ONES = K4_OFF_ROW + 64;  // four fp16 ones, four zeros
+constexpr int K4_OFF_BAR = K4_OFF_ONES + 16;
 constexpr int K4_OFF_ABORT = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;
 constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
 constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + K4_OFF_ABORT);
   uint8_t *const sStage = smem + K4_OFF_STAGE + warp * K4_STAGES * K4_STAGE;
   int64_t *sPrefix = reinterpret_cast<int64_t *>(smem + K4_OFF_PLAN);
+  if (tid < 4) *reinterpret_cast<uint32_t *>(smem + K4_OFF_ONES + 4 * tid) = tid < 2 ? 0x3c003c00u : 0u;
   if (lane == 0) {
     for (int j = 0; j < K4_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
     if (warp == 0) *abort_flag = 0;
@@ -322,14 +326,13 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
     // Units go out 32 at a time: lane l looks up unit base + l's tiles (a
     // block that is none of the pool's gives -1) and issues its copies when
     // its turn comes; `ok` has the warp's units with every tile in range.
-    int ids[K4_TILES];
-    uint32_t ok[K4_TILES], next_ok[K4_TILES];
-#pragma unroll
-    for (int k = 0; k < K4_TILES; ++k) ok[k] = next_ok[k] = 0;
+    int ids[2];
+    uint3 ok = make_uint3(0, 0, 0), next_ok = ok;  // x: whole units; y, z: units with their first, second tile
     auto fetch_ids = [&](int base) {
+      const int key0 = key_lo + K4_UNIT * (warp + (base + lane) * K4_WARPS);
 #pragma unroll
-      for (int k = 0; k < K4_TILES; ++k) {
-        const int key = key_lo + K4_UNIT * (warp + (base + lane) * K4_WARPS) + 16 * k;
+      for (int k = 0; k < 2; ++k) {
+        const int key = key0 + 16 * k;
         ids[k] = -1;
         if (base + lane < my_n && key < key_hi) {
           const unsigned tile = (unsigned)key >> 4, bi = (unsigned)((tile * A.tpb_mul) >> 36);
@@ -339,8 +342,10 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
           else
             flag(A.status, ST_BAD_BLOCK);
         }
-        next_ok[k] = __ballot_sync(FULLW, ids[k] >= 0);
       }
+      next_ok.x = __ballot_sync(FULLW, ids[0] >= 0 && ids[1] >= 0 && key0 + K4_UNIT <= key_hi);
+      next_ok.y = __ballot_sync(FULLW, ids[0] >= 0);
+      next_ok.z = __ballot_sync(FULLW, ids[1] >= 0);
     };
     auto issue = [&](int i) {
       if ((i & 31) == 0) fetch_ids(i);
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
       ++sent;
       if (lane == (i & 31)) {
         const uint32_t bar = sBar + 8 * st, dst = smem_u32(sStage + st * K4_STAGE);
-        if (K4_TILES == 2 && ids[0] >= 0 && ids[K4_TILES - 1] == ids[0] + 1) {
+        if (ids[0] >= 0 && ids[1] == ids[0] + 1) {
           tc::mbar_expect_tx(bar, 2 * KV4_TILE);
           tc::bulk_load(dst, A.pool.data + (long long)ids[0] * KV4_TILE, 2 * KV4_TILE, bar);
         } else {
@@ -377,14 +382,35 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
 #pragma unroll
     for (int n = 0; n < 16; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
     E[0] = E[1] = E[2] = E[3] = 0.f;
-    float mb0 = NEG_INF, mb1 = NEG_INF;  // the reference maximum less K4_PBIAS; -inf before the first keys
-    __half2 f2 = __float2half2_rn(32768.f);  // the power of two on the value scales
+    // per row, the exponent that a weight is counted from (its maximum so far
+    // less the bias); -inf, and 0 in its place, before the first keys
+    float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;
+    float limit = NEG_INF;                   // how large a score less r may get before the reference moves
+    float bias = K4_PBIAS;                   // lowered by the value scales' size, so that weight times scale stays in fp16
+    __half2 lim2 = __float2half2_rn(K4_VLIM);  // the largest value scale that the bias leaves room for
 
-    for (int i = 0; i < my_n; ++i) {
-      if ((i & 31) == 0) {  // (the units of this round were looked up no later than with their first)
+    // The sums of codes (all positive) and of minima grow together and cancel
+    // in the end, while the tensor cores cut every sum off below its last bit:
+    // every K4_FOLD units the minima's sum goes into the codes' (rounded to
+    // nearest), so neither gets large.  Without it the output of 18,000 keys a
+    // CTA was off by 0.3%, twice its rounding.
+    auto fold = [&]() {
+      const int src = lane & ~3;
+      const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);
+      const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
+      if (t == 0) E[0] = E[1] = E[2] = E[3] = 0.f;
+      constexpr float un = 0x1p-24f, un16 = 0x1p-20f;  // even and odd dims' units
 #pragma unroll
-        for (int k = 0; k < K4_TILES; ++k) ok[k] = next_ok[k];
+      for (int n = 0; n < 16; ++n) {
+        const float k = (n & 1) ? un16 : un, m0 = n < 8 ? g00 : g01, m1 = n < 8 ? g10 : g11;
+        O[n][0] = fmaf(m0, k, O[n][0]);
+        O[n][1] = fmaf(m0, k, O[n][1]);
+        O[n][2] = fmaf(m1, k, O[n][2]);
+        O[n][3] = fmaf(m1, k, O[n][3]);
       }
+    };
+    for (int i = 0; i < my_n; ++i) {
+      if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
       if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
       const uint32_t st = seen % K4_STAGES;
       const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
@@ -393,12 +419,9 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         break;
       }
       ++seen;
-      const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
-      int lv = 0;
-#pragma unroll
-      for (int k = 0; k < K4_TILES; ++k) lv |= ((ok[k] >> (i & 31)) & 1) << k;
-      if (lv == 0) continue;  // no block of the pool
       const uint8_t *sT = sStage + st * K4_STAGE;
+      const bool whole = (ok.x >> (i & 31)) & 1;  // both tiles there, every key in range
+      if (!whole && !(((ok.y | ok.z) >> (i & 31)) & 1)) continue;  // no block of the pool
 
       // scores
       float S[K4_NT][4];
@@ -441,7 +464,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         }
       }
       // value scales and minima of this lane's keys (2t, 2t+1, 2t+8, 2t+9 of both tiles)
-      uint32_t sv[2][K4_NT], vm[K4_NT];
+      uint32_t sv[KV4_VG][K4_NT], vm[K4_NT];
 #pragma unroll
       for (int h = 0; h < K4_TILES; ++h) {
         const uint8_t *at = sT + h * KV4_TILE;
@@ -452,16 +475,17 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
           sv[g][2 * h + 1] = x.y;
         }
         // columns of the sums' product: group 0's minima, group 1's, ones, nothing
-        const uint2 x = lds64(at + KV4_OFF_VM + (gr & 1) * 32 + t * 8);
-        vm[2 * h] = gr < 2 ? x.x : gr == 2 ? 0x3c003c00u : 0u;
-        vm[2 * h + 1] = gr < 2 ? x.y : gr == 2 ? 0x3c003c00u : 0u;
+        const uint2 x = lds64(gr < 2 ? at + KV4_OFF_VM + gr * 32 + t * 8 : smem + K4_OFF_ONES + (gr == 2 ? 0 : 8));
+        vm[2 * h] = x.x;
+        vm[2 * h + 1] = x.y;
       }
-      if (lv != (1 << K4_TILES) - 1 || key0 + K4_UNIT > key_hi) {
+      if (!whole) {
         // keys past the range or of a bad block: what lies there (any bits) must not be met
+        const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
 #pragma unroll
         for (int nt = 0; nt < K4_NT; ++nt) {
           const int k = key0 + 8 * nt + 2 * t;
-          const bool in = (lv >> (nt >> 1)) & 1;
+          const bool in = ((nt >> 1 ? ok.z : ok.y) >> (i & 31)) & 1;
           const bool v0 = in && k < key_hi, v1 = in && k + 1 < key_hi;
           if (!v0) S[nt][0] = S[nt][2] = NEG_INF;
           if (!v1) S[nt][1] = S[nt][3] = NEG_INF;
@@ -472,28 +496,25 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         }
       }
       // scores less the reference, base 2; does one pass it, or a value scale its bound?
-      const float r0 = mb0 == NEG_INF ? 0.f : mb0, r1 = mb1 == NEG_INF ? 0.f : mb1;
       float X[K4_NT][4];
       float top0 = NEG_INF, top1 = NEG_INF;
-      __half2 big = __float2half2_rn(0.f);
-      uint32_t sf[2][K4_NT];
 #pragma unroll
       for (int nt = 0; nt < K4_NT; ++nt) {
-        X[nt][0] = fmaf(S[nt][0], crow0, -r0);
-        X[nt][1] = fmaf(S[nt][1], crow0, -r0);
-        X[nt][2] = fmaf(S[nt][2], crow1, -r1);
-        X[nt][3] = fmaf(S[nt][3], crow1, -r1);
+        f32x2_split(fma_f32x2(f32x2(S[nt][0], S[nt][1]), f32x2(crow0, crow0), f32x2(-r0, -r0)), X[nt][0], X[nt][1]);
+        f32x2_split(fma_f32x2(f32x2(S[nt][2], S[nt][3]), f32x2(crow1, crow1), f32x2(-r1, -r1)), X[nt][2], X[nt][3]);
         top0 = fmax3(top0, X[nt][0], X[nt][1]);
         top1 = fmax3(top1, X[nt][2], X[nt][3]);
-#pragma unroll
-        for (int g = 0; g < KV4_VG; ++g) {
-          const __half2 x = __hmul2(u32_as_h2(sv[g][nt]), f2);
-          sf[g][nt] = h2_as_u32(x);
-          big = __hmax2(big, x);
-        }
       }
-      const bool move = top0 > K4_PBIAS + K4_SLACK || top1 > K4_PBIAS + K4_SLACK || mb0 == NEG_INF || mb1 == NEG_INF ||
-                        __low2float(big) >= 2.f || __high2float(big) >= 2.f;
+      // (each lane looks at two of the unit's 64 value scales; a stale or masked one costs a needless move at worst)
+      const __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
+      const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
+      // weights, taken before the vote on them is in
+      uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
+#pragma unroll
+      for (int nt = 0; nt < K4_NT; ++nt) {
+        P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
+        P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
+      }
       if (__any_sync(FULLW, move)) {
         // new reference per row: the larger of the old one and this unit's maximum
         float t0 = top0 + r0, t1 = top1 + r1;
@@ -502,13 +523,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
           t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
           t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
         }
-        // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
-        const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - K4_PBIAS);
-        const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - K4_PBIAS);
-        const float c0 = mb0 == NEG_INF ? 0.f : ex2(mb0 - n0), c1 = mb1 == NEG_INF ? 0.f : ex2(mb1 - n1);
-        mb0 = n0;
-        mb1 = n1;
-        // power of two that brings the largest value scale below 2 (NaN scales aside: __hmax2 passes them by)
+        // the largest value scale lowers the bias (NaN scales aside): the
+        // least power of two above it, times 2^(bias + slack), fits fp16
         uint32_t hb = 0;
 #pragma unroll
         for (int nt = 0; nt < K4_NT; ++nt)
@@ -519,20 +535,28 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
             hb = max(hb, lo > 0x7c00u ? 0u : lo);
             hb = max(hb, hi > 0x7c00u ? 0u : hi);
           }
-        hb = __reduce_max_sync(FULLW, hb);
-        const int old = (int)(__half_as_ushort(__low2half(f2)) >> 10);   // exponent field: f = 2^(old - 15)
-        int nw = 30 - (int)(hb >> 10);                                    // 2^-(exponent of the scale): field 30 - e
-        nw = nw < 1 ? 1 : nw;
-        nw = nw > old ? old : nw;
-        const float cf = __uint_as_float((uint32_t)(127 + nw - old) << 23);
-        f2 = u32_as_h2((uint32_t)(nw << 10) * 0x10001u);
-        const float o0 = c0 * cf, o1 = c1 * cf;
+        hb = __reduce_max_sync(FULLW, hb) >> 10;  // its exponent field: below 2^(hb - 14)
+        const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
+        if (room < bias) {
+          mb0 += bias - room;  // (-inf stays)
+          mb1 += bias - room;
+          bias = room;
+          lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
+        }
+        // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
+        const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
+        const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
+        const bool fresh = limit == NEG_INF;  // the first keys: nothing to scale yet
+        const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
+        mb0 = r0 = n0;
+        mb1 = r1 = n1;
+        limit = bias + K4_SLACK;
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          O[n][0] *= o0;
-          O[n][1] *= o0;
-          O[n][2] *= o1;
-          O[n][3] *= o1;
+          O[n][0] *= c0;
+          O[n][1] *= c0;
+          O[n][2] *= c1;
+          O[n][3] *= c1;
         }
         E[0] *= c0;
         E[1] *= c0;
@@ -544,28 +568,21 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
           X[nt][1] = fmaf(S[nt][1], crow0, -n0);
           X[nt][2] = fmaf(S[nt][2], crow1, -n1);
           X[nt][3] = fmaf(S[nt][3], crow1, -n1);
-#pragma unroll
-          for (int g = 0; g < KV4_VG; ++g) sf[g][nt] = h2_as_u32(__hmul2(u32_as_h2(sv[g][nt]), f2));
+          P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
+          P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
         }
-      }
-      // weights
-      uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
-#pragma unroll
-      for (int nt = 0; nt < K4_NT; ++nt) {
-        P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
-        P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
       }
       // sums
 #pragma unroll
       for (int h = 0; h < K4_TILES; ++h) {
-        if (!((lv >> h) & 1)) continue;
+        // (a tile that is not there has no weight, and any code is a finite operand)
         const uint8_t *at = sT + h * KV4_TILE + KV4_OFF_V;
         const uint32_t *p0 = P[2 * h], *p1 = P[2 * h + 1];
         mma_f16(E, p0[0], p0[1], p1[0], p1[1], vm[2 * h], vm[2 * h + 1]);
 #pragma unroll
         for (int g = 0; g < KV4_VG; ++g) {
           const uint4 x = lds128(at + g * 512 + lane * 16);
-          const __half2 s0 = u32_as_h2(sf[g][2 * h]), s1 = u32_as_h2(sf[g][2 * h + 1]);
+          const __half2 s0 = u32_as_h2(sv[g][2 * h]), s1 = u32_as_h2(sv[g][2 * h + 1]);
           const uint32_t a0 = h2_as_u32(__hmul2(u32_as_h2(p0[0]), s0)), a1 = h2_as_u32(__hmul2(u32_as_h2(p0[1]), s0));
           const uint32_t a2 = h2_as_u32(__hmul2(u32_as_h2(p1[0]), s1)), a3 = h2_as_u32(__hmul2(u32_as_h2(p1[1]), s1));
 #pragma unroll
@@ -582,6 +599,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         }
       }
       __syncwarp();  // the stage is read: the next copy into it may go out
+      if ((i & (K4_FOLD - 1)) == K4_FOLD - 1) fold();
     }
     __syncthreads();  // all warps done with their stages: reuse them as the merge area
 
@@ -599,9 +617,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
         m[(gr + 8) * 2] = mb1;
         m[(gr + 8) * 2 + 1] = E[2];
       }
-      // 2^24 over the power of two on the scales; odd dims carry 16 more
-      const int fe = (int)(__half_as_ushort(__low2half(f2)) >> 10);
-      const float un = __uint_as_float((uint32_t)(127 + 24 + 15 - fe) << 23), un16 = un * 0.0625f;
+      constexpr float un = 0x1p24f, un16 = 0x1p20f;  // even and odd dims' units
       float *o = mo + warp * 16 * MO_STRIDE;
 #pragma unroll
       for (int g = 0; g < KV4_VG; ++g)

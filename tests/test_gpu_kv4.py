@@ -666,3 +666,36 @@ def test_append_runs(table, bs, by_slot):
         kvr.kv4_append_rope(k, v, pos_t, seq_t, table, VS, pool)
     assert np.array_equal(pool.data.cpu().numpy(), want)
     assert kvr.device_status() == 0
+
+
+def test_decode_long_shares_keep_their_digits(table):
+    """Long shares per CTA (18,000 keys): the codes' sums (all positive) and the minima's cancel to a hundredth of their
+    size, so a sum cut off below its last bit at every product would show.  The output's own rounding is at most 2^-8 of
+    a value, 2^-8 / sqrt(3) in the mean square; everything else (weights and scaled weights rounded to fp16, 2^-11 each
+    and independent from key to key) is held to 2^-11."""
+    gen = _gen(211)
+    B, ctx, hkv, G = 32, 65537, 4, 16
+    pool = kvr.Kv4Layout.contiguous(B, hkv, ctx, zero=False)
+    for s in range(B):
+        _append(pool, *_kv(gen, ctx, hkv, 0.5), s, 0, table)
+    q = torch.randn(B, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    pos = torch.full((B,), ctx - 1, dtype=torch.int64, device=DEV)
+    out = kvr.full_attn_decode_kv4(q, pos, torch.arange(B, dtype=torch.int32, device=DEV), pool, table, SCALE, ctx)
+    pl = [o4.places(r) for r in range(16)]
+    at = [torch.tensor(np.array([p[i] for p in pl]), device=DEV) for i in range(6)]
+    hi = (torch.arange(192, device=DEV) % 2 * 4).to(torch.uint8)
+
+    def group(tiles, codes, scales, minima, n):
+        half = lambda a: torch.stack([tiles[:, a], tiles[:, a + 1]], -1).contiguous().view(torch.float16)[..., 0].double()
+        u = ((tiles[:, codes] >> hi[:n]) & 15).double()
+        return (half(minima).repeat_interleave(64, -1) + half(scales).repeat_interleave(64, -1) * u).flatten(0, 1)
+
+    cs = table[ctx - 1].double()
+    for b, h in ((0, 0), (17, 3), (31, 1)):
+        tiles = pool.data[pool.block_table[b].long(), h].flatten(0, 1)
+        K, V = group(tiles, at[0], at[2], at[5], 192)[:ctx], group(tiles, at[1], at[3], at[4], 128)[:ctx]
+        x = q[b, h * G:(h + 1) * G].double()
+        x = torch.cat([x[:, :32] * cs[:, 0] - x[:, 32:64] * cs[:, 1], x[:, 32:64] * cs[:, 0] + x[:, :32] * cs[:, 1], x[:, 64:]], 1)
+        want = torch.softmax(x @ K.T * SCALE, -1) @ V
+        err = (out[b, h * G:(h + 1) * G].double() - want).norm(dim=-1) / want.norm(dim=-1)
+        assert float(err.max()) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11, float(err.max())
