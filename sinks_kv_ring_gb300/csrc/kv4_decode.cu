@@ -49,6 +49,7 @@ constexpr unsigned FULLW = 0xffffffffu;
 constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K4_WARPS = 4;
 constexpr int K4_CTAS = 3;           // per SM
+constexpr int K4_CTAS8 = 4;          // per SM, groups of up to 8 heads
 constexpr int K4_TILES = 2;          // tiles of a unit
 constexpr int K4_UNIT = 16 * K4_TILES;
 constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
@@ -67,7 +68,7 @@ constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the b
 constexpr int K4_ROW = 16;           // a row's set-up and merge, in units (48 ragged rows: 8 -> 58 us, 16 -> 53, 32 -> 57)
 constexpr int K4_MIN = K4_WARPS;     // least share (twice that costs 0.9 us at 513 keys)
 constexpr int K4_PLAN = 32;          // int64 words of the plan ahead of the rows' prefix: L
-constexpr int K4_INLINE_MAX = 512;   // batches the split kernel plans itself
+constexpr int K4_INLINE_MAX = 256;   // batches the split kernel plans itself
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
 constexpr int K4_OFF_QX = 12 * 512;
 constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
@@ -79,7 +80,7 @@ constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
 static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16) * 4, "merge area");
-static_assert(K4_CTAS * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
+static_assert(K4_CTAS8 * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -91,6 +92,12 @@ __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t 
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(b0));
+}
+// the transpose of an 8 x 8 matrix of 16-bit elements held as an MMA fragment
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_cast<const uint4 *>(a); }
 __device__ __forceinline__ uint2 lds64(const uint8_t *a) { return *reinterpret_cast<const uint2 *>(a); }
@@ -265,7 +272,13 @@ struct K4Args {
   unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
 };
 
-__global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(const K4Args A) {
+// SMALL: groups of up to 8 query heads.  The keys are then the 16 rows of the
+// products and the heads their 8 columns (scores K Q^T, sums V^T P^T): half
+// the products, and half the registers for the sums, so four CTAs fit an SM.
+// The codes' operands are the same registers; a weight's row and column change
+// places between the two products by an 8 x 8 transposition (movmatrix).
+template <bool SMALL>
+__global__ void __launch_bounds__(K4_WARPS * 32, SMALL ? K4_CTAS8 : K4_CTAS) kv4_decode_kernel(K4Args A) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = A.pool.hkv, G = A.G;
@@ -320,8 +333,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
     const int nunit = (key_hi - key_lo + K4_UNIT - 1) / K4_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
-    if (__syncthreads_or(*abort_flag != 0)) break;  // the last item's merge area (over the stages) is free again
-    tc::fence_proxy_async_smem();
+    tc::fence_proxy_async_smem();                   // the last piece's merge area lies over the stages:
+    if (__syncthreads_or(*abort_flag != 0)) break;  // it is free again, its accesses ahead of the copies'
 
     // Units go out 32 at a time: lane l looks up unit base + l's tiles (a
     // block that is none of the pool's gives -1) and issues its copies when
@@ -374,266 +387,487 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(cons
 
     kv4_query(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, A.scale_log2, smem, tid);
     __syncthreads();
-    const float crow0 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * gr);
-    const float crow1 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * (gr + 8));
-    const uint2 qx = lds64(smem + K4_OFF_QX + lane * 8);
+    // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators
+    // in true units (times 2 to the bias, as the sums)
+    float *mml = reinterpret_cast<float *>(smem + K4_OFF_STAGE);  // [4][16][2]
+    float *mo = mml + K4_WARPS * 16 * 2;                          // [4][16][MO_STRIDE]
+    if constexpr (!SMALL) {
+      const float crow0 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * gr);
+      const float crow1 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 4 * (gr + 8));
+      const uint2 qx = lds64(smem + K4_OFF_QX + lane * 8);
 
-    float O[16][4], E[4];
+      float O[16][4], E[4];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
-    E[0] = E[1] = E[2] = E[3] = 0.f;
-    // per row, the exponent that a weight is counted from (its maximum so far
-    // less the bias); -inf, and 0 in its place, before the first keys
-    float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;
-    float limit = NEG_INF;                   // how large a score less r may get before the reference moves
-    float bias = K4_PBIAS;                   // lowered by the value scales' size, so that weight times scale stays in fp16
-    __half2 lim2 = __float2half2_rn(K4_VLIM);  // the largest value scale that the bias leaves room for
+      for (int n = 0; n < 16; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
+      E[0] = E[1] = E[2] = E[3] = 0.f;
+      // per row, the exponent that a weight is counted from (its maximum so far
+      // less the bias); -inf, and 0 in its place, before the first keys
+      float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;
+      float limit = NEG_INF;                   // how large a score less r may get before the reference moves
+      float bias = K4_PBIAS;                   // lowered by the value scales' size, so that weight times scale stays in fp16
+      __half2 lim2 = __float2half2_rn(K4_VLIM);  // the largest value scale that the bias leaves room for
 
-    // The sums of codes (all positive) and of minima grow together and cancel
-    // in the end, while the tensor cores cut every sum off below its last bit:
-    // every K4_FOLD units the minima's sum goes into the codes' (rounded to
-    // nearest), so neither gets large.  Without it the output of 18,000 keys a
-    // CTA was off by 0.3%, twice its rounding.
-    auto fold = [&]() {
-      const int src = lane & ~3;
-      const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);
-      const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
-      if (t == 0) E[0] = E[1] = E[2] = E[3] = 0.f;
-      constexpr float un = 0x1p-24f, un16 = 0x1p-20f;  // even and odd dims' units
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const float k = (n & 1) ? un16 : un, m0 = n < 8 ? g00 : g01, m1 = n < 8 ? g10 : g11;
-        O[n][0] = fmaf(m0, k, O[n][0]);
-        O[n][1] = fmaf(m0, k, O[n][1]);
-        O[n][2] = fmaf(m1, k, O[n][2]);
-        O[n][3] = fmaf(m1, k, O[n][3]);
-      }
-    };
-    for (int i = 0; i < my_n; ++i) {
-      if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
-      if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
-      const uint32_t st = seen % K4_STAGES;
-      const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
-      if (!got) {
-        gave_up = true;
-        break;
-      }
-      ++seen;
-      const uint8_t *sT = sStage + st * K4_STAGE;
-      const bool whole = (ok.x >> (i & 31)) & 1;  // both tiles there, every key in range
-      if (!whole && !(((ok.y | ok.z) >> (i & 31)) & 1)) continue;  // no block of the pool
-
-      // scores
-      float S[K4_NT][4];
-#pragma unroll
-      for (int nt = 0; nt < K4_NT; ++nt) {
-        S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
-        mma_f16_k8(S[nt], qx.x, qx.y, lds32(sT + (nt >> 1) * KV4_TILE + KV4_OFF_KM + (gr + 8 * (nt & 1)) * 8 + (t & 1) * 4));
-      }
-#pragma unroll
-      for (int g = 0; g < KV4_KG; ++g) {
-        uint4 kw[K4_TILES];
-#pragma unroll
-        for (int k = 0; k < K4_TILES; ++k) kw[k] = lds128(sT + k * KV4_TILE + g * 512 + lane * 16);
-        float acc[K4_NT][4];
-#pragma unroll
-        for (int nt = 0; nt < K4_NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 a = lds128(smem + (g * 4 + j) * 512 + lane * 16);
-#pragma unroll
-          for (int nt = 0; nt < K4_NT; ++nt) {
-            const uint4 &kk = kw[nt >> 1];
-            uint32_t x = (nt & 1) ? ((j >> 1) ? kk.w : kk.z) : ((j >> 1) ? kk.y : kk.x);
-            if (j & 1) x >>= 8;
-            mma_f16(acc[nt], a.x, a.y, a.z, a.w, x & 0x000f000fu, x & 0x00f000f0u);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < K4_TILES; ++h) {
-          const uint2 sc = lds64(sT + h * KV4_TILE + KV4_OFF_KS + g * 32 + t * 8);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float2 f = __half22float2(u32_as_h2(n ? sc.y : sc.x));
-            float(&Sn)[4] = S[2 * h + n];
-            const float(&an)[4] = acc[2 * h + n];
-            const uint64_t ff = f32x2(f.x, f.y);
-            f32x2_split(fma_f32x2(f32x2(an[0], an[1]), ff, f32x2(Sn[0], Sn[1])), Sn[0], Sn[1]);
-            f32x2_split(fma_f32x2(f32x2(an[2], an[3]), ff, f32x2(Sn[2], Sn[3])), Sn[2], Sn[3]);
-          }
-        }
-      }
-      // value scales and minima of this lane's keys (2t, 2t+1, 2t+8, 2t+9 of both tiles)
-      uint32_t sv[KV4_VG][K4_NT], vm[K4_NT];
-#pragma unroll
-      for (int h = 0; h < K4_TILES; ++h) {
-        const uint8_t *at = sT + h * KV4_TILE;
-#pragma unroll
-        for (int g = 0; g < KV4_VG; ++g) {
-          const uint2 x = lds64(at + KV4_OFF_VS + g * 32 + t * 8);
-          sv[g][2 * h] = x.x;
-          sv[g][2 * h + 1] = x.y;
-        }
-        // columns of the sums' product: group 0's minima, group 1's, ones, nothing
-        const uint2 x = lds64(gr < 2 ? at + KV4_OFF_VM + gr * 32 + t * 8 : smem + K4_OFF_ONES + (gr == 2 ? 0 : 8));
-        vm[2 * h] = x.x;
-        vm[2 * h + 1] = x.y;
-      }
-      if (!whole) {
-        // keys past the range or of a bad block: what lies there (any bits) must not be met
-        const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
-#pragma unroll
-        for (int nt = 0; nt < K4_NT; ++nt) {
-          const int k = key0 + 8 * nt + 2 * t;
-          const bool in = ((nt >> 1 ? ok.z : ok.y) >> (i & 31)) & 1;
-          const bool v0 = in && k < key_hi, v1 = in && k + 1 < key_hi;
-          if (!v0) S[nt][0] = S[nt][2] = NEG_INF;
-          if (!v1) S[nt][1] = S[nt][3] = NEG_INF;
-          const uint32_t keep = (v0 ? 0xffffu : 0u) | (v1 ? 0xffff0000u : 0u);
-          sv[0][nt] &= keep;
-          sv[1][nt] &= keep;
-          vm[nt] &= keep;
-        }
-      }
-      // scores less the reference, base 2; does one pass it, or a value scale its bound?
-      float X[K4_NT][4];
-      float top0 = NEG_INF, top1 = NEG_INF;
-#pragma unroll
-      for (int nt = 0; nt < K4_NT; ++nt) {
-        f32x2_split(fma_f32x2(f32x2(S[nt][0], S[nt][1]), f32x2(crow0, crow0), f32x2(-r0, -r0)), X[nt][0], X[nt][1]);
-        f32x2_split(fma_f32x2(f32x2(S[nt][2], S[nt][3]), f32x2(crow1, crow1), f32x2(-r1, -r1)), X[nt][2], X[nt][3]);
-        top0 = fmax3(top0, X[nt][0], X[nt][1]);
-        top1 = fmax3(top1, X[nt][2], X[nt][3]);
-      }
-      // (each lane looks at two of the unit's 64 value scales; a stale or masked one costs a needless move at worst)
-      const __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
-      const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
-      // weights, taken before the vote on them is in
-      uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
-#pragma unroll
-      for (int nt = 0; nt < K4_NT; ++nt) {
-        P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
-        P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
-      }
-      if (__any_sync(FULLW, move)) {
-        // new reference per row: the larger of the old one and this unit's maximum
-        float t0 = top0 + r0, t1 = top1 + r1;
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
-          t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
-        }
-        // the largest value scale lowers the bias (NaN scales aside): the
-        // least power of two above it, times 2^(bias + slack), fits fp16
-        uint32_t hb = 0;
-#pragma unroll
-        for (int nt = 0; nt < K4_NT; ++nt)
-#pragma unroll
-          for (int g = 0; g < KV4_VG; ++g) {
-            const uint32_t x = sv[g][nt];
-            const uint32_t lo = x & 0xffffu, hi = x >> 16;
-            hb = max(hb, lo > 0x7c00u ? 0u : lo);
-            hb = max(hb, hi > 0x7c00u ? 0u : hi);
-          }
-        hb = __reduce_max_sync(FULLW, hb) >> 10;  // its exponent field: below 2^(hb - 14)
-        const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
-        if (room < bias) {
-          mb0 += bias - room;  // (-inf stays)
-          mb1 += bias - room;
-          bias = room;
-          lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
-        }
-        // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
-        const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
-        const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
-        const bool fresh = limit == NEG_INF;  // the first keys: nothing to scale yet
-        const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
-        mb0 = r0 = n0;
-        mb1 = r1 = n1;
-        limit = bias + K4_SLACK;
+      // The sums of codes (all positive) and of minima grow together and cancel
+      // in the end, while the tensor cores cut every sum off below its last bit:
+      // every K4_FOLD units the minima's sum goes into the codes' (rounded to
+      // nearest), so neither gets large.  Without it the output of 18,000 keys a
+      // CTA was off by 0.3%, twice its rounding.
+      auto fold = [&]() {
+        const int src = lane & ~3;
+        const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);
+        const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
+        if (t == 0) E[0] = E[1] = E[2] = E[3] = 0.f;
+        constexpr float un = 0x1p-24f, un16 = 0x1p-20f;  // even and odd dims' units
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          O[n][0] *= c0;
-          O[n][1] *= c0;
-          O[n][2] *= c1;
-          O[n][3] *= c1;
+          const float k = (n & 1) ? un16 : un, m0 = n < 8 ? g00 : g01, m1 = n < 8 ? g10 : g11;
+          O[n][0] = fmaf(m0, k, O[n][0]);
+          O[n][1] = fmaf(m0, k, O[n][1]);
+          O[n][2] = fmaf(m1, k, O[n][2]);
+          O[n][3] = fmaf(m1, k, O[n][3]);
         }
-        E[0] *= c0;
-        E[1] *= c0;
-        E[2] *= c1;
-        E[3] *= c1;
+      };
+      for (int i = 0; i < my_n; ++i) {
+        if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
+        if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
+        const uint32_t st = seen % K4_STAGES;
+        const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
+        if (!got) {
+          gave_up = true;
+          break;
+        }
+        ++seen;
+        const uint8_t *sT = sStage + st * K4_STAGE;
+        const bool whole = (ok.x >> (i & 31)) & 1;  // both tiles there, every key in range
+        if (!whole && !(((ok.y | ok.z) >> (i & 31)) & 1)) continue;  // no block of the pool
+
+        // scores
+        float S[K4_NT][4];
 #pragma unroll
         for (int nt = 0; nt < K4_NT; ++nt) {
-          X[nt][0] = fmaf(S[nt][0], crow0, -n0);
-          X[nt][1] = fmaf(S[nt][1], crow0, -n0);
-          X[nt][2] = fmaf(S[nt][2], crow1, -n1);
-          X[nt][3] = fmaf(S[nt][3], crow1, -n1);
+          S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+          mma_f16_k8(S[nt], qx.x, qx.y, lds32(sT + (nt >> 1) * KV4_TILE + KV4_OFF_KM + (gr + 8 * (nt & 1)) * 8 + (t & 1) * 4));
+        }
+#pragma unroll
+        for (int g = 0; g < KV4_KG; ++g) {
+          uint4 kw[K4_TILES];
+#pragma unroll
+          for (int k = 0; k < K4_TILES; ++k) kw[k] = lds128(sT + k * KV4_TILE + g * 512 + lane * 16);
+          float acc[K4_NT][4];
+#pragma unroll
+          for (int nt = 0; nt < K4_NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 a = lds128(smem + (g * 4 + j) * 512 + lane * 16);
+#pragma unroll
+            for (int nt = 0; nt < K4_NT; ++nt) {
+              const uint4 &kk = kw[nt >> 1];
+              uint32_t x = (nt & 1) ? ((j >> 1) ? kk.w : kk.z) : ((j >> 1) ? kk.y : kk.x);
+              if (j & 1) x >>= 8;
+              mma_f16(acc[nt], a.x, a.y, a.z, a.w, x & 0x000f000fu, x & 0x00f000f0u);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < K4_TILES; ++h) {
+            const uint2 sc = lds64(sT + h * KV4_TILE + KV4_OFF_KS + g * 32 + t * 8);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float2 f = __half22float2(u32_as_h2(n ? sc.y : sc.x));
+              float(&Sn)[4] = S[2 * h + n];
+              const float(&an)[4] = acc[2 * h + n];
+              const uint64_t ff = f32x2(f.x, f.y);
+              f32x2_split(fma_f32x2(f32x2(an[0], an[1]), ff, f32x2(Sn[0], Sn[1])), Sn[0], Sn[1]);
+              f32x2_split(fma_f32x2(f32x2(an[2], an[3]), ff, f32x2(Sn[2], Sn[3])), Sn[2], Sn[3]);
+            }
+          }
+        }
+        // value scales and minima of this lane's keys (2t, 2t+1, 2t+8, 2t+9 of both tiles)
+        uint32_t sv[KV4_VG][K4_NT], vm[K4_NT];
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          const uint8_t *at = sT + h * KV4_TILE;
+#pragma unroll
+          for (int g = 0; g < KV4_VG; ++g) {
+            const uint2 x = lds64(at + KV4_OFF_VS + g * 32 + t * 8);
+            sv[g][2 * h] = x.x;
+            sv[g][2 * h + 1] = x.y;
+          }
+          // columns of the sums' product: group 0's minima, group 1's, ones, nothing
+          const uint2 x = lds64(gr < 2 ? at + KV4_OFF_VM + gr * 32 + t * 8 : smem + K4_OFF_ONES + (gr == 2 ? 0 : 8));
+          vm[2 * h] = x.x;
+          vm[2 * h + 1] = x.y;
+        }
+        // each lane looks at two of the unit's 64 value scales (of the ones it
+        // keeps where some are masked: those may be anything)
+        __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
+        if (!whole) {
+          // keys past the range or of a bad block: what lies there (any bits) must not be met
+          const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
+#pragma unroll
+          for (int nt = 0; nt < K4_NT; ++nt) {
+            const int k = key0 + 8 * nt + 2 * t;
+            const bool in = ((nt >> 1 ? ok.z : ok.y) >> (i & 31)) & 1;
+            const bool v0 = in && k < key_hi, v1 = in && k + 1 < key_hi;
+            if (!v0) S[nt][0] = S[nt][2] = NEG_INF;
+            if (!v1) S[nt][1] = S[nt][3] = NEG_INF;
+            const uint32_t keep = (v0 ? 0xffffu : 0u) | (v1 ? 0xffff0000u : 0u);
+            sv[0][nt] &= keep;
+            sv[1][nt] &= keep;
+            vm[nt] &= keep;
+            big = nt ? __hmax2(big, u32_as_h2(sv[0][nt])) : u32_as_h2(sv[0][0]);
+            big = __hmax2(big, u32_as_h2(sv[1][nt]));
+          }
+        }
+        // scores less the reference, base 2; does one pass it, or a value scale its bound?
+        float X[K4_NT][4];
+        float top0 = NEG_INF, top1 = NEG_INF;
+#pragma unroll
+        for (int nt = 0; nt < K4_NT; ++nt) {
+          f32x2_split(fma_f32x2(f32x2(S[nt][0], S[nt][1]), f32x2(crow0, crow0), f32x2(-r0, -r0)), X[nt][0], X[nt][1]);
+          f32x2_split(fma_f32x2(f32x2(S[nt][2], S[nt][3]), f32x2(crow1, crow1), f32x2(-r1, -r1)), X[nt][2], X[nt][3]);
+          top0 = fmax3(top0, X[nt][0], X[nt][1]);
+          top1 = fmax3(top1, X[nt][2], X[nt][3]);
+        }
+        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
+        // weights, taken before the vote on them is in
+        uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
+#pragma unroll
+        for (int nt = 0; nt < K4_NT; ++nt) {
           P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
           P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
         }
-      }
-      // sums
+        if (__any_sync(FULLW, move)) {
+          // new reference per row: the larger of the old one and this unit's maximum
+          float t0 = top0 + r0, t1 = top1 + r1;
 #pragma unroll
-      for (int h = 0; h < K4_TILES; ++h) {
-        // (a tile that is not there has no weight, and any code is a finite operand)
-        const uint8_t *at = sT + h * KV4_TILE + KV4_OFF_V;
-        const uint32_t *p0 = P[2 * h], *p1 = P[2 * h + 1];
-        mma_f16(E, p0[0], p0[1], p1[0], p1[1], vm[2 * h], vm[2 * h + 1]);
+          for (int o = 1; o < 4; o <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
+            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
+          }
+          // the largest value scale lowers the bias (NaN scales aside): the
+          // least power of two above it, times 2^(bias + slack), fits fp16
+          uint32_t hb = 0;
 #pragma unroll
-        for (int g = 0; g < KV4_VG; ++g) {
-          const uint4 x = lds128(at + g * 512 + lane * 16);
-          const __half2 s0 = u32_as_h2(sv[g][2 * h]), s1 = u32_as_h2(sv[g][2 * h + 1]);
-          const uint32_t a0 = h2_as_u32(__hmul2(u32_as_h2(p0[0]), s0)), a1 = h2_as_u32(__hmul2(u32_as_h2(p0[1]), s0));
-          const uint32_t a2 = h2_as_u32(__hmul2(u32_as_h2(p1[0]), s1)), a3 = h2_as_u32(__hmul2(u32_as_h2(p1[1]), s1));
+          for (int nt = 0; nt < K4_NT; ++nt)
 #pragma unroll
-          for (int ww = 0; ww < 2; ++ww) {
-            uint32_t y0 = ww ? x.y : x.x, y1 = ww ? x.w : x.z;
-            float(*On)[4] = &O[g * 8 + ww * 4];
-            mma_f16(On[0], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
-            mma_f16(On[1], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
-            y0 >>= 8;
-            y1 >>= 8;
-            mma_f16(On[2], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
-            mma_f16(On[3], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
+            for (int g = 0; g < KV4_VG; ++g) {
+              const uint32_t x = sv[g][nt];
+              const uint32_t lo = x & 0xffffu, hi = x >> 16;
+              hb = max(hb, lo > 0x7c00u ? 0u : lo);
+              hb = max(hb, hi > 0x7c00u ? 0u : hi);
+            }
+          hb = __reduce_max_sync(FULLW, hb) >> 10;  // its exponent field: below 2^(hb - 14)
+          const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
+          if (room < bias) {
+            mb0 += bias - room;  // (-inf stays)
+            mb1 += bias - room;
+            bias = room;
+            lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
+          }
+          // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
+          const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
+          const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
+          const bool fresh = limit == NEG_INF;  // the first keys: nothing to scale yet
+          const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
+          mb0 = r0 = n0;
+          mb1 = r1 = n1;
+          limit = bias + K4_SLACK;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            O[n][0] *= c0;
+            O[n][1] *= c0;
+            O[n][2] *= c1;
+            O[n][3] *= c1;
+          }
+          E[0] *= c0;
+          E[1] *= c0;
+          E[2] *= c1;
+          E[3] *= c1;
+#pragma unroll
+          for (int nt = 0; nt < K4_NT; ++nt) {
+            X[nt][0] = fmaf(S[nt][0], crow0, -n0);
+            X[nt][1] = fmaf(S[nt][1], crow0, -n0);
+            X[nt][2] = fmaf(S[nt][2], crow1, -n1);
+            X[nt][3] = fmaf(S[nt][3], crow1, -n1);
+            P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
+            P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
           }
         }
-      }
-      __syncwarp();  // the stage is read: the next copy into it may go out
-      if ((i & (K4_FOLD - 1)) == K4_FOLD - 1) fold();
-    }
-    __syncthreads();  // all warps done with their stages: reuse them as the merge area
-
-    // per warp: reference and sum per row, numerators in true units (times 2^K4_PBIAS, as the sums)
-    float *mml = reinterpret_cast<float *>(smem + K4_OFF_STAGE);  // [4][16][2]
-    float *mo = mml + K4_WARPS * 16 * 2;                          // [4][16][MO_STRIDE]
-    {
-      const int src = lane & ~3;
-      const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);  // sum p m, groups 0, 1
-      const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
-      if (t == 1) {
-        float *m = mml + warp * 32;
-        m[gr * 2] = mb0;
-        m[gr * 2 + 1] = E[0];
-        m[(gr + 8) * 2] = mb1;
-        m[(gr + 8) * 2 + 1] = E[2];
-      }
-      constexpr float un = 0x1p24f, un16 = 0x1p20f;  // even and odd dims' units
-      float *o = mo + warp * 16 * MO_STRIDE;
+        // sums
 #pragma unroll
-      for (int g = 0; g < KV4_VG; ++g)
+        for (int h = 0; h < K4_TILES; ++h) {
+          // (a tile that is not there has no weight, and any code is a finite operand)
+          const uint8_t *at = sT + h * KV4_TILE + KV4_OFF_V;
+          const uint32_t *p0 = P[2 * h], *p1 = P[2 * h + 1];
+          mma_f16(E, p0[0], p0[1], p1[0], p1[1], vm[2 * h], vm[2 * h + 1]);
 #pragma unroll
-        for (int ww = 0; ww < 2; ++ww)
+          for (int g = 0; g < KV4_VG; ++g) {
+            const uint4 x = lds128(at + g * 512 + lane * 16);
+            const __half2 s0 = u32_as_h2(sv[g][2 * h]), s1 = u32_as_h2(sv[g][2 * h + 1]);
+            const uint32_t a0 = h2_as_u32(__hmul2(u32_as_h2(p0[0]), s0)), a1 = h2_as_u32(__hmul2(u32_as_h2(p0[1]), s0));
+            const uint32_t a2 = h2_as_u32(__hmul2(u32_as_h2(p1[0]), s1)), a3 = h2_as_u32(__hmul2(u32_as_h2(p1[1]), s1));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float(*On)[4] = &O[g * 8 + ww * 4];
-            const float m0 = g ? g01 : g00, m1 = g ? g11 : g10;
-            const int d = 64 * g + 8 * (2 * t + c) + 4 * ww;
-            *reinterpret_cast<float4 *>(o + gr * MO_STRIDE + d) =
-                make_float4(fmaf(On[0][c], un, m0), fmaf(On[1][c], un16, m0), fmaf(On[2][c], un, m0), fmaf(On[3][c], un16, m0));
-            *reinterpret_cast<float4 *>(o + (gr + 8) * MO_STRIDE + d) =
-                make_float4(fmaf(On[0][2 + c], un, m1), fmaf(On[1][2 + c], un16, m1), fmaf(On[2][2 + c], un, m1),
-                            fmaf(On[3][2 + c], un16, m1));
+            for (int ww = 0; ww < 2; ++ww) {
+              uint32_t y0 = ww ? x.y : x.x, y1 = ww ? x.w : x.z;
+              float(*On)[4] = &O[g * 8 + ww * 4];
+              mma_f16(On[0], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
+              mma_f16(On[1], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
+              y0 >>= 8;
+              y1 >>= 8;
+              mma_f16(On[2], a0, a1, a2, a3, y0 & 0x000f000fu, y1 & 0x000f000fu);
+              mma_f16(On[3], a0, a1, a2, a3, y0 & 0x00f000f0u, y1 & 0x00f000f0u);
+            }
           }
+        }
+        __syncwarp();  // the stage is read: the next copy into it may go out
+        if ((i & (K4_FOLD - 1)) == K4_FOLD - 1) fold();
+      }
+      __syncthreads();  // all warps done with their stages: reuse them as the merge area
+
+      {
+        const int src = lane & ~3;
+        const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);  // sum p m, groups 0, 1
+        const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
+        if (t == 1) {
+          float *m = mml + warp * 32;
+          m[gr * 2] = mb0;
+          m[gr * 2 + 1] = E[0];
+          m[(gr + 8) * 2] = mb1;
+          m[(gr + 8) * 2 + 1] = E[2];
+        }
+        constexpr float un = 0x1p24f, un16 = 0x1p20f;  // even and odd dims' units
+        float *o = mo + warp * 16 * MO_STRIDE;
+#pragma unroll
+        for (int g = 0; g < KV4_VG; ++g)
+#pragma unroll
+          for (int ww = 0; ww < 2; ++ww)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float(*On)[4] = &O[g * 8 + ww * 4];
+              const float m0 = g ? g01 : g00, m1 = g ? g11 : g10;
+              const int d = 64 * g + 8 * (2 * t + c) + 4 * ww;
+              *reinterpret_cast<float4 *>(o + gr * MO_STRIDE + d) =
+                  make_float4(fmaf(On[0][c], un, m0), fmaf(On[1][c], un16, m0), fmaf(On[2][c], un, m0), fmaf(On[3][c], un16, m0));
+              *reinterpret_cast<float4 *>(o + (gr + 8) * MO_STRIDE + d) =
+                  make_float4(fmaf(On[0][2 + c], un, m1), fmaf(On[1][2 + c], un16, m1), fmaf(On[2][2 + c], un, m1),
+                              fmaf(On[3][2 + c], un16, m1));
+            }
+      }
+    } else {
+      // a head's column: this lane has heads 2t and 2t + 1
+      const float crow0 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 8 * t);
+      const float crow1 = *reinterpret_cast<const float *>(smem + K4_OFF_ROW + 8 * t + 4);
+      const uint32_t qx = lds32(smem + K4_OFF_QX + lane * 8);
+      uint2 qb[12];
+#pragma unroll
+      for (int j = 0; j < 12; ++j) qb[j] = make_uint2(lds32(smem + j * 512 + lane * 16), lds32(smem + j * 512 + lane * 16 + 8));
+
+      float O[8][4], E[4];  // O[4g + i]: dims 64g + 8 gr + i (rows gr) and + 4 (rows gr + 8)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
+      E[0] = E[1] = E[2] = E[3] = 0.f;
+      float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;  // of the two heads (see the other form)
+      float limit = NEG_INF, bias = K4_PBIAS;
+      __half2 lim2 = __float2half2_rn(K4_VLIM);
+      // which scales of a 4-position word are this lane's keys gr and gr + 8
+      const uint32_t pick = (gr & 1) ? 0x7632u : 0x5410u;
+
+      auto fold = [&]() {
+        const float m00 = __shfl_sync(FULLW, E[0], t), m01 = __shfl_sync(FULLW, E[1], t);          // group 0, both heads
+        const float m10 = __shfl_sync(FULLW, E[0], 4 + t), m11 = __shfl_sync(FULLW, E[1], 4 + t);  // group 1
+        if (gr < 2) E[0] = E[1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float k = (n & 1) ? 0x1p-20f : 0x1p-24f, m0 = n < 4 ? m00 : m10, m1 = n < 4 ? m01 : m11;
+          O[n][0] = fmaf(m0, k, O[n][0]);
+          O[n][1] = fmaf(m1, k, O[n][1]);
+          O[n][2] = fmaf(m0, k, O[n][2]);
+          O[n][3] = fmaf(m1, k, O[n][3]);
+        }
+      };
+      for (int i = 0; i < my_n; ++i) {
+        if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
+        if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
+        const uint32_t st = seen % K4_STAGES;
+        const bool got = __all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K4_STAGES) & 1u, abort_flag));
+        if (!got) {
+          gave_up = true;
+          break;
+        }
+        ++seen;
+        const uint8_t *sT = sStage + st * K4_STAGE;
+        const bool whole = (ok.x >> (i & 31)) & 1;  // both tiles there, every key in range
+        if (!whole && !(((ok.y | ok.z) >> (i & 31)) & 1)) continue;  // no block of the pool
+
+        // scores: rows keys gr and gr + 8 of each tile, columns heads 2t, 2t + 1
+        float S[K4_TILES][4];
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          const uint8_t *at = sT + h * KV4_TILE;
+          S[h][0] = S[h][1] = S[h][2] = S[h][3] = 0.f;
+          mma_f16_k8(S[h], lds32(at + KV4_OFF_KM + gr * 8 + (t & 1) * 4), lds32(at + KV4_OFF_KM + (gr + 8) * 8 + (t & 1) * 4), qx);
+        }
+#pragma unroll
+        for (int g = 0; g < KV4_KG; ++g)
+#pragma unroll
+          for (int h = 0; h < K4_TILES; ++h) {
+            const uint4 kw = lds128(sT + h * KV4_TILE + g * 512 + lane * 16);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t lo = (j >> 1) ? kw.y : kw.x, hi = (j >> 1) ? kw.w : kw.z;
+              if (j & 1) {
+                lo >>= 8;
+                hi >>= 8;
+              }
+              mma_f16(acc, lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, qb[g * 4 + j].x, qb[g * 4 + j].y);
+            }
+            const uint2 sc4 = lds64(sT + h * KV4_TILE + KV4_OFF_KS + g * 32 + (gr >> 1) * 8);
+            const float2 sc = __half22float2(u32_as_h2(__byte_perm(sc4.x, sc4.y, pick)));
+            S[h][0] = fmaf(acc[0], sc.x, S[h][0]);
+            S[h][1] = fmaf(acc[1], sc.x, S[h][1]);
+            S[h][2] = fmaf(acc[2], sc.y, S[h][2]);
+            S[h][3] = fmaf(acc[3], sc.y, S[h][3]);
+          }
+        // value scales of keys 2t, 2t+1, 2t+8, 2t+9, and the rows of the sums' product (minima of both groups, ones)
+        uint32_t sv[KV4_VG][K4_NT], vm[K4_NT];
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          const uint8_t *at = sT + h * KV4_TILE;
+#pragma unroll
+          for (int g = 0; g < KV4_VG; ++g) {
+            const uint2 x = lds64(at + KV4_OFF_VS + g * 32 + t * 8);
+            sv[g][2 * h] = x.x;
+            sv[g][2 * h + 1] = x.y;
+          }
+          const uint2 x = lds64(gr < 2 ? at + KV4_OFF_VM + gr * 32 + t * 8 : smem + K4_OFF_ONES + (gr == 2 ? 0 : 8));
+          vm[2 * h] = x.x;
+          vm[2 * h + 1] = x.y;
+        }
+        // each lane looks at two of the unit's 64 value scales (of the ones it
+        // keeps where some are masked: those may be anything)
+        __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
+        if (!whole) {  // (see the other form)
+          const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
+#pragma unroll
+          for (int nt = 0; nt < K4_NT; ++nt) {
+            const bool in = ((nt >> 1 ? ok.z : ok.y) >> (i & 31)) & 1;
+            if (!in || key0 + 8 * nt + gr >= key_hi) S[nt >> 1][2 * (nt & 1)] = S[nt >> 1][2 * (nt & 1) + 1] = NEG_INF;
+            const int k = key0 + 8 * nt + 2 * t;
+            const uint32_t keep = (in && k < key_hi ? 0xffffu : 0u) | (in && k + 1 < key_hi ? 0xffff0000u : 0u);
+            sv[0][nt] &= keep;
+            sv[1][nt] &= keep;
+            vm[nt] &= keep;
+            big = nt ? __hmax2(big, u32_as_h2(sv[0][nt])) : u32_as_h2(sv[0][0]);
+            big = __hmax2(big, u32_as_h2(sv[1][nt]));
+          }
+        }
+        float top0 = NEG_INF, top1 = NEG_INF;
+        float X[K4_TILES][4];
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          f32x2_split(fma_f32x2(f32x2(S[h][0], S[h][1]), f32x2(crow0, crow1), f32x2(-r0, -r1)), X[h][0], X[h][1]);
+          f32x2_split(fma_f32x2(f32x2(S[h][2], S[h][3]), f32x2(crow0, crow1), f32x2(-r0, -r1)), X[h][2], X[h][3]);
+          top0 = fmax3(top0, X[h][0], X[h][2]);
+          top1 = fmax3(top1, X[h][1], X[h][3]);
+        }
+        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
+        if (__any_sync(FULLW, move)) {
+          float t0 = top0 + r0, t1 = top1 + r1;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
+            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
+          }
+          uint32_t hb = 0;
+#pragma unroll
+          for (int nt = 0; nt < K4_NT; ++nt)
+#pragma unroll
+            for (int g = 0; g < KV4_VG; ++g) {
+              const uint32_t x = sv[g][nt];
+              const uint32_t lo = x & 0xffffu, hi = x >> 16;
+              hb = max(hb, lo > 0x7c00u ? 0u : lo);
+              hb = max(hb, hi > 0x7c00u ? 0u : hi);
+            }
+          hb = __reduce_max_sync(FULLW, hb) >> 10;
+          const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
+          if (room < bias) {
+            mb0 += bias - room;
+            mb1 += bias - room;
+            bias = room;
+            lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
+          }
+          const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
+          const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
+          const bool fresh = limit == NEG_INF;
+          const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
+          mb0 = r0 = n0;
+          mb1 = r1 = n1;
+          limit = bias + K4_SLACK;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            O[n][0] *= c0;
+            O[n][1] *= c1;
+            O[n][2] *= c0;
+            O[n][3] *= c1;
+          }
+          E[0] *= c0;
+          E[1] *= c1;
+#pragma unroll
+          for (int h = 0; h < K4_TILES; ++h) {
+            X[h][0] = fmaf(S[h][0], crow0, -n0);
+            X[h][1] = fmaf(S[h][1], crow1, -n1);
+            X[h][2] = fmaf(S[h][2], crow0, -n0);
+            X[h][3] = fmaf(S[h][3], crow1, -n1);
+          }
+        }
+        // weights: row head gr, columns keys 2t, 2t + 1 (nt even: of the tile's first eight, odd: of the others)
+        uint32_t P[K4_NT];
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          P[2 * h] = transpose8(h2_as_u32(__floats2half2_rn(ex2(X[h][0]), ex2(X[h][1]))));
+          P[2 * h + 1] = transpose8(h2_as_u32(__floats2half2_rn(ex2(X[h][2]), ex2(X[h][3]))));
+        }
+#pragma unroll
+        for (int h = 0; h < K4_TILES; ++h) {
+          const uint8_t *at = sT + h * KV4_TILE + KV4_OFF_V;
+          mma_f16(E, vm[2 * h], 0u, vm[2 * h + 1], 0u, P[2 * h], P[2 * h + 1]);
+#pragma unroll
+          for (int g = 0; g < KV4_VG; ++g) {
+            const uint4 x = lds128(at + g * 512 + lane * 16);
+            const uint32_t b0 = h2_as_u32(__hmul2(u32_as_h2(P[2 * h]), u32_as_h2(sv[g][2 * h])));
+            const uint32_t b1 = h2_as_u32(__hmul2(u32_as_h2(P[2 * h + 1]), u32_as_h2(sv[g][2 * h + 1])));
+            mma_f16(O[4 * g], x.x & 0x000f000fu, x.y & 0x000f000fu, x.z & 0x000f000fu, x.w & 0x000f000fu, b0, b1);
+            mma_f16(O[4 * g + 1], x.x & 0x00f000f0u, x.y & 0x00f000f0u, x.z & 0x00f000f0u, x.w & 0x00f000f0u, b0, b1);
+            const uint32_t y0 = x.x >> 8, y1 = x.y >> 8, y2 = x.z >> 8, y3 = x.w >> 8;
+            mma_f16(O[4 * g + 2], y0 & 0x000f000fu, y1 & 0x000f000fu, y2 & 0x000f000fu, y3 & 0x000f000fu, b0, b1);
+            mma_f16(O[4 * g + 3], y0 & 0x00f000f0u, y1 & 0x00f000f0u, y2 & 0x00f000f0u, y3 & 0x00f000f0u, b0, b1);
+          }
+        }
+        __syncwarp();  // the stage is read: the next copy into it may go out
+        if ((i & (K4_FOLD - 1)) == K4_FOLD - 1) fold();
+      }
+      __syncthreads();  // all warps done with their stages: reuse them as the merge area
+      {
+        const float m00 = __shfl_sync(FULLW, E[0], t), m01 = __shfl_sync(FULLW, E[1], t);
+        const float m10 = __shfl_sync(FULLW, E[0], 4 + t), m11 = __shfl_sync(FULLW, E[1], 4 + t);
+        if (gr == 2) {  // the ones' row: sums of weights
+          *reinterpret_cast<float4 *>(mml + warp * 32 + 4 * t) = make_float4(mb0, E[0], mb1, E[1]);
+        }
+        float *o = mo + warp * 16 * MO_STRIDE + 2 * t * MO_STRIDE + 8 * gr;
+#pragma unroll
+        for (int g = 0; g < KV4_VG; ++g)
+#pragma unroll
+          for (int ww = 0; ww < 2; ++ww)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float m = c ? (g ? m11 : m01) : (g ? m10 : m00);
+              const int e = 2 * ww + c;
+              *reinterpret_cast<float4 *>(o + c * MO_STRIDE + 64 * g + 4 * ww) =
+                  make_float4(fmaf(O[4 * g][e], 0x1p24f, m), fmaf(O[4 * g + 1][e], 0x1p20f, m),
+                              fmaf(O[4 * g + 2][e], 0x1p24f, m), fmaf(O[4 * g + 3][e], 0x1p20f, m));
+            }
+      }
     }
     __syncthreads();
     float *fac = mo + K4_WARPS * 16 * MO_STRIDE;  // [4 warps][16 heads]
@@ -777,8 +1011,8 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t plan_bytes(int B) { return align256(((size_t)K4_PLAN + B + 1) * 8); }
 
 // Piece numbers: one per CTA that can have a share (of K4_MIN units at least) and one per row.
-size_t pieces_cap(int B, int hkv, long long max_ctx) {
-  const long long rows = (long long)B * hkv, R = (long long)K4_CTAS * num_sms();
+size_t pieces_cap(int B, int G, int hkv, long long max_ctx) {
+  const long long rows = (long long)B * hkv, R = (long long)(G <= 8 ? K4_CTAS8 : K4_CTAS) * num_sms();
   const long long most = (rows * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW) + K4_MIN - 1) / K4_MIN;
   return (size_t)(rows + (most < R ? most : R));
 }
@@ -786,17 +1020,18 @@ size_t pieces_cap(int B, int hkv, long long max_ctx) {
 }  // namespace
 
 size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
-  const size_t n = pieces_cap(B, hkv, max_ctx), G = (size_t)(hq / hkv);
+  const size_t G = (size_t)(hq / hkv), n = pieces_cap(B, hq / hkv, hkv, max_ctx);
   return plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
 }
 
 cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
                               const Kv4View &pool, const float *table, int64_t max_pos, float softmax_scale,
                               long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st) {
-  cudaError_t e = ensure_smem_limit(17, (const void *)kv4_decode_kernel, K4_SMEM, true);
+  const int hkv = pool.hkv, G = hq / hkv, R = (G <= 8 ? K4_CTAS8 : K4_CTAS) * num_sms();
+  void (*const kernel)(K4Args) = G <= 8 ? kv4_decode_kernel<true> : kv4_decode_kernel<false>;
+  cudaError_t e = ensure_smem_limit(G <= 8 ? 18 : 17, (const void *)kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
-  const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
-  const size_t pieces = pieces_cap(B, hkv, max_ctx);
+  const size_t pieces = pieces_cap(B, G, hkv, max_ctx);
   K4Args A;
   A.q = q;
   A.pos = pos;
@@ -823,7 +1058,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
                    max_ctx, ctas, A.plan, status);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(kv4_decode_kernel, dim3((unsigned)ctas), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
+  e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
   if (e != cudaSuccess) return e;
   // warps per merged row: about four pieces each
   const int est = (int)(R / ((long long)B * hkv)) + 1;

@@ -699,3 +699,26 @@ def test_decode_long_shares_keep_their_digits(table):
         want = torch.softmax(x @ K.T * SCALE, -1) @ V
         err = (out[b, h * G:(h + 1) * G].double() - want).norm(dim=-1) / want.norm(dim=-1)
         assert float(err.max()) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11, float(err.max())
+
+
+@pytest.mark.parametrize("G", [3, 8, 16])
+def test_decode_ragged_rows_share_ctas(table, G):
+    """Many short and some long rows, several to a CTA, rows cut at a CTA's share: bit for bit the same in every run, and
+    right in a sample of rows of every length."""
+    gen = _gen(307 + G)
+    B, hkv, most = 150, 4, 6000
+    lens = torch.exp(torch.rand(B, generator=gen, device=DEV) * np.log(most)).long().clamp(1, most).tolist()
+    pool = _pool(gen, B, hkv, most, 48)
+    k, v = _kv(gen, sum(lens), hkv, 1.0)
+    seq = torch.arange(B, device=DEV).repeat_interleave(torch.tensor(lens, device=DEV)).to(torch.int32)
+    kvr.kv4_append_rope(k, v, torch.cat([torch.arange(m, device=DEV) for m in lens]), seq, table, VS, pool)
+    q = torch.randn(B, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    pos, ids = _ints([m - 1 for m in lens], torch.int64), torch.arange(B, dtype=torch.int32, device=DEV)
+    n = kvr.full_attn_decode_kv4_workspace_size(B, hkv * G, hkv, most)
+    outs = []
+    for i in range(12):
+        ws = torch.full((n,), 0xFF if i % 2 else 0, dtype=torch.uint8, device=DEV)  # no initialisation is relied on
+        outs.append(kvr.full_attn_decode_kv4(q, pos, ids, pool, table, SCALE, most, workspace=ws))
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    some = sorted(range(B), key=lambda b: lens[b])[::5]
+    _check_decode(outs[0][some], q[some], [lens[b] - 1 for b in some], some, pool, table)
