@@ -259,15 +259,16 @@ __device__ __forceinline__ void put_token(const uint4 (&raw)[5], const float *__
 
 __global__ void __launch_bounds__(K4A_WARPS * 32)
     kv4_append_kernel(const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, const int64_t *__restrict__ pos,
-                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, int T, long long warps,
+                      const int32_t *__restrict__ seq, const int64_t *__restrict__ slots, int T, unsigned warps,
                       const float *__restrict__ table, int64_t max_pos, float vscale, Kv4View dst, unsigned *status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = lane & 7;
-  const long long w = (long long)blockIdx.x * K4A_WARPS + (threadIdx.x >> 5);
+  const unsigned w = blockIdx.x * K4A_WARPS + (threadIdx.x >> 5);
   if (w >= warps) return;
-  const int h = (int)(w % dst.hkv);
-  const long long t = w / dst.hkv * 4 + (lane >> 3);
+  const unsigned four = w / (unsigned)dst.hkv;
+  const int h = (int)(w - four * (unsigned)dst.hkv);
+  const long long t = 4LL * four + (lane >> 3);
   uint4 raw[5];
 #pragma unroll
   for (int g = 0; g < 5; ++g) raw[g] = make_uint4(0, 0, 0, 0);
@@ -291,9 +292,9 @@ cudaError_t launch_kv4_append(const uint16_t *k, const uint16_t *v, const int64_
                               const int64_t *slots, int T, const float *table, int64_t max_pos, float value_scale,
                               const Kv4View &dst, unsigned *status, cudaStream_t st) {
   const long long warps = ((long long)T + 3) / 4 * dst.hkv, ctas = (warps + K4A_WARPS - 1) / K4A_WARPS;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(kv4_append_kernel, dim3((unsigned)ctas), dim3(K4A_WARPS * 32), 0, st, k, v, pos, seq, slots, T,
-                    warps, table, max_pos, value_scale, dst, status);
+                    (unsigned)warps, table, max_pos, value_scale, dst, status);
 }
 
 }  // namespace kvr

@@ -49,7 +49,6 @@ constexpr unsigned FULLW = 0xffffffffu;
 constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K4_WARPS = 4;
 constexpr int K4_CTAS = 3;           // per SM
-constexpr int K4_CTAS8 = 4;          // per SM, groups of up to 8 heads
 constexpr int K4_TILES = 2;          // tiles of a unit
 constexpr int K4_UNIT = 16 * K4_TILES;
 constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
@@ -80,7 +79,7 @@ constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
 static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16) * 4, "merge area");
-static_assert(K4_CTAS8 * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
+static_assert(K4_CTAS * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -274,11 +273,13 @@ struct K4Args {
 
 // SMALL: groups of up to 8 query heads.  The keys are then the 16 rows of the
 // products and the heads their 8 columns (scores K Q^T, sums V^T P^T): half
-// the products, and half the registers for the sums, so four CTAs fit an SM.
+// the products, and half the registers for the sums (four CTAs an SM, at 128
+// registers, measured slower than three: 241 us against 230 at batch 64 and 8
+// heads).
 // The codes' operands are the same registers; a weight's row and column change
 // places between the two products by an 8 x 8 transposition (movmatrix).
 template <bool SMALL>
-__global__ void __launch_bounds__(K4_WARPS * 32, SMALL ? K4_CTAS8 : K4_CTAS) kv4_decode_kernel(K4Args A) {
+__global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Args A) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = A.pool.hkv, G = A.G;
@@ -1011,8 +1012,8 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t plan_bytes(int B) { return align256(((size_t)K4_PLAN + B + 1) * 8); }
 
 // Piece numbers: one per CTA that can have a share (of K4_MIN units at least) and one per row.
-size_t pieces_cap(int B, int G, int hkv, long long max_ctx) {
-  const long long rows = (long long)B * hkv, R = (long long)(G <= 8 ? K4_CTAS8 : K4_CTAS) * num_sms();
+size_t pieces_cap(int B, int hkv, long long max_ctx) {
+  const long long rows = (long long)B * hkv, R = (long long)K4_CTAS * num_sms();
   const long long most = (rows * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW) + K4_MIN - 1) / K4_MIN;
   return (size_t)(rows + (most < R ? most : R));
 }
@@ -1020,18 +1021,18 @@ size_t pieces_cap(int B, int G, int hkv, long long max_ctx) {
 }  // namespace
 
 size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
-  const size_t G = (size_t)(hq / hkv), n = pieces_cap(B, hq / hkv, hkv, max_ctx);
+  const size_t G = (size_t)(hq / hkv), n = pieces_cap(B, hkv, max_ctx);
   return plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
 }
 
 cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
                               const Kv4View &pool, const float *table, int64_t max_pos, float softmax_scale,
                               long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st) {
-  const int hkv = pool.hkv, G = hq / hkv, R = (G <= 8 ? K4_CTAS8 : K4_CTAS) * num_sms();
+  const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
   void (*const kernel)(K4Args) = G <= 8 ? kv4_decode_kernel<true> : kv4_decode_kernel<false>;
   cudaError_t e = ensure_smem_limit(G <= 8 ? 18 : 17, (const void *)kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
-  const size_t pieces = pieces_cap(B, G, hkv, max_ctx);
+  const size_t pieces = pieces_cap(B, hkv, max_ctx);
   K4Args A;
   A.q = q;
   A.pos = pos;

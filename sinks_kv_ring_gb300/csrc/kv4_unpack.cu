@@ -41,9 +41,10 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * K4U_WARPS + (threadIdx.x >> 5);
-  const long long unit = w / src.hkv;
-  const int h = (int)(w - unit * src.hkv);
+  const unsigned w = blockIdx.x * K4U_WARPS + (threadIdx.x >> 5);
+  const unsigned unit32 = w / (unsigned)src.hkv;
+  const int h = (int)(w - unit32 * (unsigned)src.hkv);
+  const long long unit = unit32;
   if (unit >= units) return;
   // the last entry whose first unit is not past this one
   int i = 0, hi = n;
@@ -77,10 +78,11 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
   const long long end = a + (c1 - c0);
   if (p0 >= end) return;
 
-  const long long sbi = p0 / src.block_size;
+  // (positions in tiles, which 32 bits hold: a table of 2^36 positions would be 4 GB of entries at the least)
+  const unsigned tile0 = (unsigned)(p0 >> 4), stb = (unsigned)src.block_size >> 4, sbi = tile0 / stb;
   int sblk = 0;
   if (ok) {
-    sblk = sbi < src.max_blocks ? src.block_table[(long long)s * src.max_blocks + sbi] : -1;
+    sblk = sbi < (unsigned)src.max_blocks ? src.block_table[(long long)s * src.max_blocks + sbi] : -1;
     ok = sblk >= 0 && sblk < src.num_blocks;
     if (!ok && mine) flag(status, ST_BAD_BLOCK);
   }
@@ -96,16 +98,16 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
       if (mine) flag(status, ST_BAD_SEQ);
       return;
     }
-    const long long dbi = p0 / dst.block_size;  // block sizes are multiples of 16: a tile lies in one block
-    const int dblk = dbi < dst.max_blocks ? dst.block_table[(long long)ds * dst.max_blocks + dbi] : -1;
+    const unsigned dtb = (unsigned)dst.block_size >> 4, dbi = tile0 / dtb;  // a tile lies in one block
+    const int dblk = dbi < (unsigned)dst.max_blocks ? dst.block_table[(long long)ds * dst.max_blocks + dbi] : -1;
     if (dblk < 0 || dblk >= dst.num_blocks) {
       if (mine) flag(status, ST_BAD_BLOCK);
       return;
     }
-    drow = ((long long)dblk * dst.hkv + h) * dst.block_size + (p0 - dbi * dst.block_size);
+    drow = ((long long)dblk * dst.hkv + h) * dst.block_size + 16 * (tile0 - dbi * dtb);
   }
 
-  const uint8_t *tile = src.data + (ok ? kv4_tile(src, sblk, h, (int)(p0 - sbi * src.block_size)) : 0);
+  const uint8_t *tile = src.data + (ok ? kv4_tile(src, sblk, h, (int)(16 * (tile0 - sbi * stb))) : 0);
   uint4 kc[KV4_KG], vc[KV4_VG];
 #pragma unroll
   for (int g = 0; g < KV4_KG; ++g)
@@ -169,7 +171,7 @@ cudaError_t launch_kv4_unpack(const Kv4View &src, const int32_t *src_seqs, const
                               cudaStream_t st) {
   const long long units = (T >> 4) + 2LL * n;
   const long long blocks = (units * src.hkv + K4U_WARPS - 1) / K4U_WARPS;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (units * src.hkv > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(kv4_unpack_kernel, dim3((unsigned)blocks), dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows,
                     n, T, dst_seqs, dst, units, status);
 }
