@@ -37,6 +37,8 @@
 // both busy: each warp streams its own 32-key units through its own ring of
 // bulk copies (one copy brings a tile's codes and scales), with no barrier
 // between warps inside an item.
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
@@ -78,7 +80,8 @@ constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
 constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
-static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16) * 4, "merge area");
+static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16 + 32 + 16 * DV) * 4,
+              "merge area");
 static_assert(K4_CTAS * (K4_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -268,6 +271,8 @@ struct K4Args {
   float *part_ml;
   float *part_o;
   unsigned *status;
+  uint16_t *out;               // DIRECT
+  int cs;                      // DIRECT: CTAs of a row
   unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
 };
 
@@ -278,7 +283,12 @@ struct K4Args {
 // heads).
 // The codes' operands are the same registers; a weight's row and column change
 // places between the two products by an 8 x 8 transposition (movmatrix).
-template <bool SMALL>
+//
+// DIRECT: short contexts of few rows, where a launch costs more than the work.
+// A cluster of A.cs CTAs takes one row, each an equal share of its units, and
+// the CTAs merge their parts through each other's shared memory: one launch,
+// no plan and no workspace.
+template <bool SMALL, bool DIRECT>
 __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Args A) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -300,8 +310,9 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
 
   // the plan: every CTA makes it for small batches, CTA 0 stores it for the merge
   const int64_t *prefix = A.plan + K4_PLAN;
-  long long L;
-  if (A.B <= K4_INLINE_MAX) {
+  long long L = 0;
+  if (DIRECT) {
+  } else if (A.B <= K4_INLINE_MAX) {
     L = kv4_plan<K4_WARPS * 32>(A.pos, A.seq, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix,
                                 blockIdx.x == 0 ? A.status : nullptr);
     if (blockIdx.x == 0) {
@@ -319,18 +330,41 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   uint32_t sent = 0;  // and issued
   bool gave_up = false;
 
-  const long long line_end = min((blockIdx.x + 1) * L, (long long)prefix[A.B]);
-  for (long long x = blockIdx.x * L; x < line_end;) {
-    const int b = kv4_find(prefix, A.B, x);
-    const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
-    const int kv = (int)((x - prefix[b]) / rowlen), off = (int)(x - prefix[b] - (long long)kv * rowlen);
-    const int stop = (int)min((long long)rowlen, off + (line_end - x));
-    x += stop - off;
-    if (stop <= K4_ROW) continue;  // set-up alone: no piece
-    const int w = (int)blockIdx.x + b * hkv + kv;
-    const long long p = A.pos[b];
-    const int s = A.seq[b];  // (a sequence on the line has a valid position and id)
-    const int key_lo = max(off - K4_ROW, 0) * K4_UNIT, key_hi = (int)min((long long)(stop - K4_ROW) * K4_UNIT, p + 1);
+  const long long line_end = DIRECT ? 1 : min((blockIdx.x + 1) * L, (long long)prefix[A.B]);
+  for (long long x = DIRECT ? 0 : blockIdx.x * L; x < line_end;) {
+    int b, kv, w = 0, key_lo, key_hi;
+    long long p;
+    if (DIRECT) {
+      const int row = (int)blockIdx.x / A.cs, rank = (int)blockIdx.x - row * A.cs;
+      b = row / hkv;
+      kv = row - b * hkv;
+      x = 1;
+      p = A.pos[b];
+      const int units = kv4_units(p, A.seq[b], A.pool.num_seqs, A.max_pos, A.max_ctx,
+                                  kv == 0 && rank == 0 && tid == 0 ? A.status : nullptr);
+      if (units == 0) {  // (so for the whole cluster)
+        uint16_t *o = A.out + ((long long)b * A.hq + (long long)kv * G) * DV;
+        for (int i = rank * (K4_WARPS * 32) + tid; i < G * DV; i += A.cs * (K4_WARPS * 32)) o[i] = 0;
+        return;
+      }
+      const int each = (units + A.cs - 1) / A.cs;
+      key_lo = min(rank * each, units) * K4_UNIT;
+      key_hi = (int)min((long long)min((rank + 1) * each, units) * K4_UNIT, p + 1);
+      if (key_hi < key_lo) key_hi = key_lo;
+    } else {
+      b = kv4_find(prefix, A.B, x);
+      const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
+      kv = (int)((x - prefix[b]) / rowlen);
+      const int off = (int)(x - prefix[b] - (long long)kv * rowlen);
+      const int stop = (int)min((long long)rowlen, off + (line_end - x));
+      x += stop - off;
+      if (stop <= K4_ROW) continue;  // set-up alone: no piece
+      w = (int)blockIdx.x + b * hkv + kv;
+      p = A.pos[b];
+      key_lo = max(off - K4_ROW, 0) * K4_UNIT;
+      key_hi = (int)min((long long)(stop - K4_ROW) * K4_UNIT, p + 1);
+    }
+    const int s = A.seq[b];  // (a row that gets here has a valid position and id)
     const int nunit = (key_hi - key_lo + K4_UNIT - 1) / K4_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
@@ -872,6 +906,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     }
     __syncthreads();
     float *fac = mo + K4_WARPS * 16 * MO_STRIDE;  // [4 warps][16 heads]
+    float *own_ml = fac + K4_WARPS * 16;          // DIRECT: the CTA's merged part, [16][2] and [16][128]
+    float *own_o = own_ml + 32;
     if (tid < G) {
       float M = NEG_INF;
 #pragma unroll
@@ -885,7 +921,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
         fac[ww * 16 + tid] = f;
         L += mml[ww * 32 + tid * 2 + 1] * f;
       }
-      float *pml = A.part_ml + (long long)w * G * 2;
+      float *pml = DIRECT ? own_ml : A.part_ml + (long long)w * G * 2;
       pml[tid * 2] = M;
       pml[tid * 2 + 1] = L;
     }
@@ -902,7 +938,33 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
         acc.z += x.z * f;
         acc.w += x.w * f;
       }
-      *reinterpret_cast<float4 *>(A.part_o + ((long long)w * G + g) * DV + d4) = acc;
+      *reinterpret_cast<float4 *>(DIRECT ? own_o + g * DV + d4 : A.part_o + ((long long)w * G + g) * DV + d4) = acc;
+    }
+    if constexpr (DIRECT) {
+      cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+      const int rank = (int)cl.block_rank();
+      cl.sync();
+      for (int idx = rank * (K4_WARPS * 32) + tid; idx < G * (DV / 4); idx += A.cs * (K4_WARPS * 32)) {
+        const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
+        float M = NEG_INF, S = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < A.cs; ++c) M = fmaxf(M, cl.map_shared_rank(own_ml, c)[2 * g]);
+        for (int c = 0; c < A.cs; ++c) {
+          const float2 ml = *reinterpret_cast<const float2 *>(cl.map_shared_rank(own_ml, c) + 2 * g);
+          if (ml.x == NEG_INF) continue;
+          const float f = ex2(ml.x - M);
+          const float4 o = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own_o, c) + g * DV + d4);
+          S += ml.y * f;
+          acc.x += o.x * f;
+          acc.y += o.y * f;
+          acc.z += o.z * f;
+          acc.w += o.w * f;
+        }
+        const float inv = S == 0.f ? 0.f : 1.f / S;
+        *reinterpret_cast<uint2 *>(A.out + ((long long)b * A.hq + (long long)kv * G + g) * DV + d4) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      }
+      cl.sync();  // no CTA leaves while another reads its part
     }
   }
   if (gave_up && lane == 0) flag(A.status, ST_TIMEOUT);
@@ -1029,8 +1091,16 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
                               const Kv4View &pool, const float *table, int64_t max_pos, float softmax_scale,
                               long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st) {
   const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
-  void (*const kernel)(K4Args) = G <= 8 ? kv4_decode_kernel<true> : kv4_decode_kernel<false>;
-  cudaError_t e = ensure_smem_limit(G <= 8 ? 18 : 17, (const void *)kernel, K4_SMEM, true);
+  const long long rows = (long long)B * hkv, units = (max_ctx + K4_UNIT - 1) / K4_UNIT;
+  // Short contexts go by clusters in one launch.  Measured at max_ctx 1024
+  // (one launch against the work line's two): 1 x 2 KV heads at 4 query heads
+  // each 5.7 us against 7.1, 16 x 4 at 16 11.1 / 13.2, 64 x 4 23.0 / 24.3, 600
+  // x 4 121 / 156; at 2048 8 x 4 11.3 / 12.5 but 64 x 4 38.1 / 34.4: a row then
+  // needs its eight CTAs.
+  const bool direct = units <= (8 * rows <= R ? 64 : 32);
+  void (*const kernel)(K4Args) = G <= 8 ? (direct ? kv4_decode_kernel<true, true> : kv4_decode_kernel<true, false>)
+                                        : (direct ? kv4_decode_kernel<false, true> : kv4_decode_kernel<false, false>);
+  cudaError_t e = ensure_smem_limit(17 + 2 * (G <= 8) + direct, (const void *)kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
   const size_t pieces = pieces_cap(B, hkv, max_ctx);
   K4Args A;
@@ -1052,6 +1122,14 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   A.status = status;
   const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
   A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
+  A.out = out;
+  A.cs = 1;
+  if (direct) {
+    // as many CTAs a row as the longest row gives every warp a unit, as a
+    // cluster may have, and as the GPU holds of all rows at once
+    while (A.cs < 8 && A.cs * K4_WARPS < units && 2 * A.cs * rows <= R) A.cs *= 2;
+    return launch_pdl_cluster(kernel, dim3((unsigned)(rows * A.cs)), dim3(K4_WARPS * 32), (size_t)K4_SMEM, A.cs, st, A);
+  }
   // (a CTA whose share would lie past the line has nothing to do)
   const int ctas = (int)(pieces - (size_t)B * hkv);
   if (B > K4_INLINE_MAX) {

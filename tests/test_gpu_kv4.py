@@ -722,3 +722,49 @@ def test_decode_ragged_rows_share_ctas(table, G):
     assert all(torch.equal(o, outs[0]) for o in outs)
     some = sorted(range(B), key=lambda b: lens[b])[::5]
     _check_decode(outs[0][some], q[some], [lens[b] - 1 for b in some], some, pool, table)
+
+
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("B,hkv,max_ctx", [(1, 1, 1), (1, 2, 2048), (9, 1, 2048), (14, 4, 2049), (50, 4, 1024), (120, 8, 1000),
+                                           (300, 2, 64)])
+def test_decode_short_contexts(table, G, B, hkv, max_ctx):
+    """Batches around the sizes where a row is taken by a cluster of CTAs in one launch: contexts from one token to the
+    bound, rows that cannot be served among them, a captured run replayed with other lengths."""
+    gen = _gen(401 + B + G)
+    lens = torch.randint(1, max_ctx + 1, (B,), generator=gen, device=DEV).tolist()
+    lens[0] = max_ctx
+    if B > 3:
+        lens[1], lens[2] = 1, min(33, max_ctx)
+    pool = _pool(gen, B, hkv, max_ctx, 32)
+    k, v = _kv(gen, sum(lens), hkv, 1.0)
+    seq = torch.arange(B, device=DEV).repeat_interleave(torch.tensor(lens, device=DEV)).to(torch.int32)
+    kvr.kv4_append_rope(k, v, torch.cat([torch.arange(m, device=DEV) for m in lens]), seq, table, VS, pool)
+    q = torch.randn(B, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    pos, ids = _ints([m - 1 for m in lens], torch.int64), torch.arange(B, dtype=torch.int32, device=DEV)
+    bad = 3 if B > 3 else None
+    if bad is not None:
+        pos[bad] = max_ctx
+    out = torch.full((B, hkv * G, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(kvr.full_attn_decode_kv4_workspace_size(B, hkv * G, hkv, max_ctx), dtype=torch.uint8, device=DEV)
+    call = lambda: kvr.full_attn_decode_kv4(q, pos, ids, pool, table, SCALE, max_ctx, workspace=ws, out=out)
+    call()
+    assert kvr.device_status() == (kvr.DEV_BAD_POS if bad is not None else 0)
+    good = [b for b in range(B) if b != bad]
+    some = good if B <= 20 else good[::7] + [0, 1, 2]
+    if bad is not None:
+        assert not out[bad].any()
+    _check_decode(out[some], q[some], [lens[b] - 1 for b in some], some, pool, table)
+    first = out.clone()
+    call()
+    assert torch.equal(out, first)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        call()
+    half = [max(1, m // 2) for m in lens]
+    pos.copy_(_ints([m - 1 for m in half], torch.int64))
+    g.replay()
+    torch.cuda.synchronize()
+    kvr.device_status()
+    _check_decode(out[some], q[some], [half[b] - 1 for b in some], some, pool, table)
