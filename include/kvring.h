@@ -171,8 +171,8 @@ kvr_status kvr_device_status(uint32_t *flags, int reset);
  * `launches` kernels started by swa_sink_decode (over a RING layout, or over
  * a PAGED one with up to 8 q heads per KV head), by the short-chunk part of
  * swa_sink_prefill_varlen, by full_attn_prefill_chunk, by
- * kv_ring_gather_pages or by kv_ring_snapshot / kv_ring_restore, in this
- * process, stall on purpose: once their loads are in flight (and, for the
+ * full_attn_decode_kv4, by kv_ring_gather_pages or by kv_ring_snapshot /
+ * kv_ring_restore, in this process, stall on purpose: once their loads are in flight (and, for the
  * prefill, with its tensor memory held), one warp group (for the copies: the
  * first CTA) waits on an internal barrier that nothing completes, with a
  * time limit of limit_ns nanoseconds.  When the limit passes the kernel takes
@@ -557,7 +557,10 @@ size_t full_attn_decode_kv4_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, i
  * verification are B * C rows with their own positions, once all of them are
  * appended.  workspace: full_attn_decode_kv4_workspace_size(B, Hq, Hkv,
  * max_ctx) bytes, 16-byte aligned, no initialisation; calls that may overlap
- * on the GPU need workspaces of their own.
+ * on the GPU need workspaces of their own.  max_ctx <= 2^30
+ * (KVR_EUNSUPPORTED).  The same inputs give the same bits in every call.  A
+ * query, key or value that is not finite makes NaN of exactly the outputs it
+ * enters; what lies in the pool behind a context is never used.
  */
 kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
                                 const kvr_kv4_layout *pool, const float *rope_cos_sin, int64_t max_pos,

@@ -197,7 +197,7 @@ def _want_q(q):
 
 def _want_table(table):
     _want(table, "table", torch.float32, 3)
-    if tuple(table.shape[1:]) != (DROT // 2, 2):
+    if table.shape[1:] != (DROT // 2, 2):
         raise ValueError(f"table must be [max_pos, {DROT // 2}, 2] (cos, sin), got shape {tuple(table.shape)}")
 
 
@@ -210,7 +210,7 @@ def _out(out, rows, hq, like):
     if out is None:
         return torch.empty(rows, hq, DV, dtype=torch.bfloat16, device=like.device)
     _want(out, "out", torch.bfloat16, 3)
-    if tuple(out.shape) != (rows, hq, DV):
+    if out.shape != (rows, hq, DV):
         raise ValueError(f"out must be [{rows}, {hq}, {DV}], got shape {tuple(out.shape)}")
     return out
 
@@ -315,7 +315,7 @@ class LinearLayout:
         _want(k, "linear.k", torch.bfloat16, 3)
         _want(v, "linear.v", torch.bfloat16, 3)
         T, H, D = k.shape
-        if D != DQK or tuple(v.shape) != (T, H, DV):
+        if D != DQK or v.shape != (T, H, DV):
             raise ValueError("linear tensors have inconsistent shapes")
         self.k, self.v = k, v
         self.num_rows, self.num_kv_heads = T, H
@@ -347,6 +347,7 @@ class Kv4Layout:
         self.data, self.block_table = data, block_table
         self.num_blocks, self.num_kv_heads, self.block_size = nb, H, 16 * tiles
         self.num_seqs, self.max_blocks = block_table.shape
+        self._c = _Layout4(H, self.num_seqs, self.max_blocks, 16 * tiles, nb)
 
     def tensors(self):
         return self.data, self.block_table
@@ -369,8 +370,8 @@ class Kv4Layout:
         return num_kv_heads * KV4_TILE // 16
 
     def c(self):
-        return _Layout4(self.num_kv_heads, self.num_seqs, self.max_blocks, self.block_size, self.num_blocks,
-                        self.data.data_ptr(), self.block_table.data_ptr())
+        self._c.data, self._c.block_table = self.data.data_ptr(), self.block_table.data_ptr()
+        return self._c
 
 
 def rope_table(theta: float, max_pos: int, device="cuda", nthreads: int = 0) -> torch.Tensor:
@@ -686,8 +687,8 @@ def kv4_append_rope(k, v, pos, seq, table, value_scale, dst, slots=None, stream=
         _want(slots, "slots", torch.int64, 1)
         _want_len(slots, "slots", k.shape[0])
     _want_table(table)
-    T, H = k.shape[0], k.shape[1]
-    if tuple(k.shape) != (T, H, DQK) or tuple(v.shape) != (T, H, DV) or pos.shape[0] != T:
+    T, H = k.shape[:2]
+    if k.shape[2] != DQK or v.shape != (T, H, DV) or pos.shape[0] != T:
         raise ValueError("k/v/pos shapes disagree")
     _same_device(k, v, pos, seq, slots, table, *dst.tensors())
     c = dst.c()
@@ -712,6 +713,8 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
     if workspace is None:
         n = full_attn_decode_kv4_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)  # (the allocator may hand it on while that stream still works)
     _want(workspace, "workspace", torch.uint8, 1)
     out = _out(out, B, Hq, q)
     _same_device(q, pos, seq, table, workspace, out, *pool.tensors())

@@ -75,7 +75,8 @@ constexpr int K4_OFF_QX = 12 * 512;
 constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
 constexpr int K4_OFF_ONES = K4_OFF_ROW + 64;  // four fp16 ones, four zeros
 constexpr int K4_OFF_BAR = K4_OFF_ONES + 16;
-constexpr int K4_OFF_ABORT = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;
+constexpr int K4_OFF_STALL = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;  // a barrier that nothing completes (test hook)
+constexpr int K4_OFF_ABORT = K4_OFF_STALL + 8;
 constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
 constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
@@ -271,6 +272,7 @@ struct K4Args {
   float *part_ml;
   float *part_o;
   unsigned *status;
+  unsigned long long stall_ns;  // test hook: warp 0's first wait is on a barrier that nothing completes (0: no stall)
   uint16_t *out;               // DIRECT
   int cs;                      // DIRECT: CTAs of a row
   unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
@@ -301,7 +303,10 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   if (tid < 4) *reinterpret_cast<uint32_t *>(smem + K4_OFF_ONES + 4 * tid) = tid < 2 ? 0x3c003c00u : 0u;
   if (lane == 0) {
     for (int j = 0; j < K4_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
-    if (warp == 0) *abort_flag = 0;
+    if (warp == 0) {
+      tc::mbar_init(sBase + K4_OFF_STALL, 1);
+      *abort_flag = 0;
+    }
     tc::fence_mbar_init();
   }
   pdl_wait();
@@ -422,6 +427,11 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
 
     kv4_query(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, A.scale_log2, smem, tid);
     __syncthreads();
+    int run_n = my_n;
+    if (A.stall_ns && warp == 0 && !gave_up && !tc::mbar_wait(sBase + K4_OFF_STALL, 0, abort_flag, A.stall_ns)) {
+      gave_up = true;
+      run_n = 0;
+    }
     // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators
     // in true units (times 2 to the bias, as the sums)
     float *mml = reinterpret_cast<float *>(smem + K4_OFF_STAGE);  // [4][16][2]
@@ -462,7 +472,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           O[n][3] = fmaf(m1, k, O[n][3]);
         }
       };
-      for (int i = 0; i < my_n; ++i) {
+      for (int i = 0; i < run_n; ++i) {
         if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
         if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
         const uint32_t st = seen % K4_STAGES;
@@ -720,7 +730,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           O[n][3] = fmaf(m1, k, O[n][3]);
         }
       };
-      for (int i = 0; i < my_n; ++i) {
+      for (int i = 0; i < run_n; ++i) {
         if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
         if (i + K4_STAGES - 1 < my_n) issue(i + K4_STAGES - 1);
         const uint32_t st = seen % K4_STAGES;
@@ -1092,6 +1102,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
                               long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st) {
   const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
   const long long rows = (long long)B * hkv, units = (max_ctx + K4_UNIT - 1) / K4_UNIT;
+  if (rows > 0x7ffffffLL) return cudaErrorInvalidValue;  // (its queries alone would fill the GPU)
   // Short contexts go by clusters in one launch.  Measured at max_ctx 1024
   // (one launch against the work line's two): 1 x 2 KV heads at 4 query heads
   // each 5.7 us against 7.1, 16 x 4 at 16 11.1 / 13.2, 64 x 4 23.0 / 24.3, 600
@@ -1120,6 +1131,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   A.part_ml = reinterpret_cast<float *>(w8);
   A.part_o = reinterpret_cast<float *>(w8 + align256(pieces * G * 2 * sizeof(float)));
   A.status = status;
+  A.stall_ns = take_stall();
   const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
   A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
   A.out = out;

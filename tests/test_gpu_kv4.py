@@ -768,3 +768,55 @@ def test_decode_short_contexts(table, G, B, hkv, max_ctx):
     torch.cuda.synchronize()
     kvr.device_status()
     _check_decode(out[some], q[some], [half[b] - 1 for b in some], some, pool, table)
+
+
+def test_unpack_rows_at_any_aligned_address(table):
+    """Destinations whose rows start 16 but not 32 bytes on (the store width goes by it)."""
+    gen = _gen(73)
+    hkv, n = 2, 70
+    pool = _filled(gen, [n], hkv, 16, table)
+    args = (_ints([0], torch.int32), _ints([0], torch.int64), _ints([0, n], torch.int32))
+    want = _want_unpacked(pool, 0, 0, n)
+    for shift in (0, 8):
+        kb = torch.full((n * hkv * 192 + 64,), 9.0, dtype=torch.bfloat16, device=DEV)
+        vb = torch.full((n * hkv * 128 + 64,), 9.0, dtype=torch.bfloat16, device=DEV)
+        k = kb[shift:shift + n * hkv * 192].view(n, hkv, 192)
+        v = vb[shift:shift + n * hkv * 128].view(n, hkv, 128)
+        kvr.kv4_unpack(pool, *args, kvr.LinearLayout(k, v))
+        assert torch.equal(k.cpu(), want[0]) and torch.equal(v.cpu(), want[1])
+        assert (kb[shift + k.numel():] == 9).all() and (kb[:shift] == 9).all()
+
+
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("ctx", [700, 20000])
+def test_decode_stalled_wait_leaves_in_time(table, ctx, G):
+    """A wait that nothing completes runs into its limit: the kernel leaves with the timeout bit (the cluster form for the
+    short context, the work line for the long one), and the next call is right again."""
+    gen = _gen(503 + ctx + G)
+    pool = _filled(gen, [ctx, 40], 2, 64, table)
+    q = torch.randn(2, 2 * G, 192, generator=gen, device=DEV).bfloat16()
+    pos, ids = _ints([ctx - 1, 39], torch.int64), _ints([0, 1], torch.int32)
+    call = lambda: kvr.full_attn_decode_kv4(q, pos, ids, pool, table, SCALE, ctx)
+    want = call()
+    assert kvr.device_status() == 0
+    kvr.debug_stall_next(1, 2_000_000)
+    call()
+    assert kvr.device_status() & kvr.DEV_TIMEOUT
+    assert torch.equal(call(), want)
+    assert kvr.device_status() == 0
+    kvr.debug_stall_next(0, 1000)
+
+
+def test_decode_on_another_stream(table):
+    gen = _gen(509)
+    pool = _filled(gen, [900, 3000], 2, 64, table)
+    q = torch.randn(2, 16, 192, generator=gen, device=DEV).bfloat16()
+    pos, ids = _ints([899, 2999], torch.int64), _ints([0, 1], torch.int32)
+    want = kvr.full_attn_decode_kv4(q, pos, ids, pool, table, SCALE, 3000)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    outs = [kvr.full_attn_decode_kv4(q, pos, ids, pool, table, SCALE, 3000, stream=st) for _ in range(20)]
+    junk = [torch.randn(1 << 20, device=DEV) for _ in range(20)]  # the current stream goes on allocating meanwhile
+    st.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and len(junk) == 20
