@@ -7,36 +7,48 @@
 //   o       = sum_j (p_j s_jg) u_jg + sum_j p_j m_jg
 // so the tensor cores multiply codes, and a scale costs one multiply per
 // (head, key, group), not one per element.  All products are m16n8k16 f16
-// with fp32 accumulators, the G query heads of one KV head as the 16 rows:
+// with fp32 accumulators; groups of more than 8 query heads per KV head put
+// the heads in the 16 rows, smaller ones in the 8 columns (SMALL, below):
 //   * Codes as operands.  A code u masked out of a word in place, w &
 //     0x000f000f, is the pair of fp16 numbers u 2^-24 (subnormal, exact in the
 //     product), and w & 0x00f000f0 is 16 u 2^-24: two instructions give two
 //     operand registers and one shift serves the next two, 5 per 8 codes, with
 //     no conversion, no bias and no rounding.  The factor 16 of every other
 //     dim is divided out of q beforehand (K) or of the sums afterwards (V).
+//     (e4m3 operands would take 3 per 8 codes, but their m16n8k32 product runs
+//     at 20 cycles here: 470 us at batch 64 where this takes 288.)
 //   * Queries are rotated, scaled by softmax_scale log2(e), brought by a power
 //     of two to a largest magnitude in [2^14, 2^15) per head, and rounded once
-//     to fp16 (2^-12 of a value, where the bf16 decode rounds to 2^-9).
+//     to fp16 (2^-11 of a value, where the bf16 decode rounds to 2^-8).
 //   * The minima enter as one more k = 8 product, of the stored fp16 minima
 //     with sum(q_g) in two fp16 parts (22 bits), which starts the score.
-//   * Weights p 2^10 are fp16 (at most 2^14, so 2^-34 of the largest is still
-//     above fp16's least number: a long flat tail keeps its mass); p s is one
-//     packed fp16 multiply, with s brought below 2 by a power of two that
-//     follows the largest scale seen.  Both roundings are 2^-12 of a weight,
-//     eight times finer than the bf16 weights of the other decode.
-//   * sum p m and sum p come out of one more product whose columns are the
-//     two groups' minima and ones.
+//   * Weights p 2^bias are fp16, with bias + 4 = 14 as long as the value scales
+//     stay below 2 and less by the scales' exponent beyond: weight times scale
+//     (one packed fp16 multiply) stays in range, and a weight 2^-34 of the
+//     largest is still above fp16's least number, so a long flat tail keeps its
+//     mass.  Both roundings are 2^-11 of a weight, eight times finer than the
+//     bf16 weights of the other decode.
+//   * sum p m and sum p come out of one more product, with the two groups'
+//     minima and ones as its other operand.
 // The running maximum is a reference that moves (with a rescale of the sums)
 // only when a score passes it by more than 4: the check is one vote per 32
 // keys.
 //
-// What bounds it.  180 bytes and 2 (192 + 128) G flops per key and KV head:
-// at G = 16 the m16n8k16 rate (600 TFLOP/s measured, 8 cycles per product and
-// SM quarter) takes 0.7 of the time the bytes take, and the masks, loads and
-// softmax of a quarter about as many issue slots, so the warps have to keep
-// both busy: each warp streams its own 32-key units through its own ring of
-// bulk copies (one copy brings a tile's codes and scales), with no barrier
-// between warps inside an item.
+// Work.  Each warp streams its own 32-key units through its own ring of bulk
+// copies (one copy brings two tiles' codes and scales), with no barrier
+// between warps inside a piece; 12 warps an SM, three CTAs, hold the sums in
+// registers.
+//
+// What bounds it.  180 bytes and 2 (192 + 128) G flops per key and KV head.
+// Up to 8 heads: HBM (batch 64 at 32769 keys, 4 x 8 heads: 230 us, 6.55 TB/s,
+// 0.97 of the copy rate).  At 16 heads the products alone take 153 us (86 of
+// them per unit at 8.2 cycles an SM quarter) and every other instruction of a
+// quarter about 0.75 cycles on top, as masks, loads and softmax share its
+// register ports with them: 287 us (5.26 TB/s, 0.78), where the same pipeline
+// without any arithmetic takes 240.  Measured and left out: two CTAs of 255
+// registers (322 us), 16-key units with four CTAs (335), scores of one unit
+// interleaved with the sums of the one before (323), queries held in registers
+// (327).
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -57,7 +69,7 @@ constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
 constexpr int K4_STAGES = 2;
 constexpr int K4_STAGE = K4_TILES * KV4_TILE;
 constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
-constexpr int K4_FOLD = 16;          // units between foldings of the minima's sum (1 us of 292 at batch 64; 4 costs 4)
+constexpr int K4_FOLD = 16;          // units between foldings of the minima's sum (1 us at batch 64; 4 units: 4 us)
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
 constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the bias as it is: below 2, times 2^14
 // The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW

@@ -165,11 +165,12 @@ def test_append_padding_and_flags(table):
 # -- decode --------------------------------------------------------------------------------------------------------------
 
 def _check_decode(got, q, pos, seq, pool, table, what=""):
-    """Every row against fp64.  Rounding of the output is half a bf16 step, 2^-9 |o|.  A score moves by what rounding
-    the rotated q to fp16 does, 2^-11 of sum |q||k| at most (2^-12 for the rounding, the same again for the fp32 sums,
-    the group sums and the scales' products), which moves a weight by twice that; a weight is rounded twice to fp16
-    (2^-12 each, its step included), and so are the sums' terms: 2^-10 together, of sum p |v|, where |v| counts the
-    code part and the minimum apart: at most 3 |v|_max of the group.  And the bar of the bf16 decode, per row."""
+    """Every row against fp64.  The output is rounded by half a bf16 step, 2^-8 |o| at most.  A score moves by at most
+    2^-11 sum |q||k| for the rounding of the rotated q to fp16, and by less than as much again for everything held in
+    fp32 or in two fp16 parts: 2^-10 sum |q||k|, which moves a weight by twice that at most (its own score's and the
+    sum's part).  A weight is rounded to fp16 twice, 2^-11 each, and their sum with the minima once: 2^-10 of sum p |v|,
+    where |v| counts the code part and the minimum apart, at most 3 |v|_max of the group.  And the bar of the bf16
+    decode, per row."""
     data, bt = pool.data.cpu().numpy(), pool.block_table.cpu().numpy()
     cs = table.cpu().numpy()
     G = q.shape[1] // pool.num_kv_heads
@@ -185,7 +186,7 @@ def _check_decode(got, q, pos, seq, pool, table, what=""):
             want, a, w = o4.attend(qf[b, hs], p, K, V, ok, cs[p], SCALE)
             err = np.abs(g[b, hs] - want)
             vmax = np.abs(V[:p + 1][ok[:p + 1]]).max() if ok[:p + 1].any() else 0.0
-            tol = 2.0 ** -9 * np.abs(want) + 2 * 2.0 ** -11 * a[:, None] * w + 2.0 ** -10 * (w + 3 * vmax)
+            tol = 2.0 ** -8 * np.abs(want) + 2 * 2.0 ** -10 * a[:, None] * w + 2.0 ** -10 * (w + 3 * vmax)
             assert np.all(err <= tol), f"{what} row {b} head {h}: {np.max(err - tol):.3e} over"
             rel = np.sqrt((err ** 2).mean(1) / np.maximum((want ** 2).mean(1), 1e-30))
             assert rel.max() <= 1e-2, f"{what} row {b} head {h}: rel RMS {rel.max():.3e}"
@@ -282,12 +283,13 @@ def test_decode_scores_rise_and_fall(table):
         _append(pool, k, v, 0, 0, table)
         q = (torch.randn(1, G, 192, generator=gen, device=DEV) * 0.1 + u * 14).bfloat16()
         out = kvr.full_attn_decode_kv4(q, _ints([n - 1], torch.int64), _ints([0], torch.int32), pool, table, SCALE, n)
-        # scores of hundreds carry the fp16 rounding of q: 2^-11 of sum |q||k| is up to 0.3, so the bound of
-        # _check_decode is wide here, and the rel RMS bar does not apply: check the bound alone
+        # scores of hundreds carry the fp16 rounding of q: 2^-10 of sum |q||k| is up to 0.6, so the bound of
+        # _check_decode is wide here (the weights' change taken as the exponential it is, of values that differ by at
+        # most 2 |v|_max), and the rel RMS bar does not apply: check the bound alone
         K, V, ok = o4.sequence(pool.data.cpu().numpy(), pool.block_table[0].cpu().numpy(), 0, n)
         want, a, w = o4.attend(q[0].float().cpu().numpy(), n - 1, K, V, ok, table[n - 1].cpu().numpy(), SCALE)
         err = np.abs(out[0].double().cpu().numpy() - want)
-        tol = 2.0 ** -9 * np.abs(want) + (np.exp(2 * 2.0 ** -11 * a[:, None]) - 1) * 2 * np.abs(V).max() + 2.0 ** -10 * (w + 3 * np.abs(V).max())
+        tol = 2.0 ** -8 * np.abs(want) + (np.exp(2 * 2.0 ** -10 * a[:, None]) - 1) * 2 * np.abs(V).max() + 2.0 ** -10 * (w + 3 * np.abs(V).max())
         assert np.all(err <= tol)
 
 
