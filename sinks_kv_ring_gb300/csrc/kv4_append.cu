@@ -17,14 +17,15 @@
 // 16-byte load brings a lane's values, all five in flight before the
 // destination is looked up.
 //
-// What bounds it: about 650 instructions per four tokens (unpacking,
-// extrema, the exact quotient), 64 us for 302,216 (token, KV head) pairs where
-// their 820 bytes each take 37 us at the copy rate.  The scales of a token's
-// five groups are taken by five of its lanes at once (2 divisions instead of
-// 10 per lane), the codes in packed pairs.  The stores are 2 and 4 bytes wide
-// (a position's V codes lie apart) and merge in L2; putting whole tiles
-// together in shared memory first, for full-sector stores, measured slower
-// (73 us against 64): they are not what bounds it.
+// What bounds it: instructions, about 750 per four tokens (unpacking, extrema,
+// the exact quotient; the schedulers issue in 75% of the cycles): 302,216
+// (token, KV head) pairs take 64 us where their 820 bytes each take 37 us at
+// the copy rate.  The scales of a token's five groups are taken by five of its
+// lanes at once (2 divisions instead of 10 per lane), the codes in packed
+// pairs.  The stores are 2 and 4 bytes wide (a position's V codes lie apart)
+// and merge in L2; putting whole tiles together in shared memory first, for
+// full-sector stores, measured slower (73 us against 64): they are not what
+// bounds it.
 #include "kv4.cuh"
 #include "launch.h"
 
