@@ -130,6 +130,46 @@ def test_append_corner_groups(table):
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("hkv,by_slot,scale", [(1, False, VS), (2, True, VS), (3, False, -VS), (5, True, -1.0), (8, False, VS)])
+def test_append_many_as_few(table, hkv, by_slot, scale):
+    """A call of many (token, KV head) pairs writes the bytes that calls of a few tokens write, and says the same of the
+    tokens it cannot write."""
+    gen = _gen(300 + hkv)
+    T, bs, S = 66001 // hkv + 1, 48, 4
+    mb = -(-T // (S * bs)) + 1
+    pools = [_pool(_gen(5), S, hkv, mb * bs, bs, fill=0x3C) for _ in range(2)]
+    k, v = _kv(gen, T, hkv, 2.0)
+    hit = torch.randint(0, T, (60,), generator=gen, device=DEV)
+    k[hit[:10], :, 3] = float("nan")
+    k[hit[10:20], -1, 70] = float("inf")
+    k[hit[20:30], 0, 64:128] *= 1e30
+    k[hit[30:35]] = 1.5
+    v[hit[35:45], -1] *= 1e6
+    v[hit[45:50], 0, 127] = float("-inf")
+    v[hit[50:60]] = 0.0
+    pick = torch.randperm(S * mb * bs, generator=gen, device=DEV)[:T]
+    seq, pos = (pick // (mb * bs)).to(torch.int32), pick % (mb * bs)
+    slots = pools[0].block_table[seq.long(), pos // bs].long() * bs + pos % bs
+    off = torch.randint(0, T, (40,), generator=gen, device=DEV)
+    seq[off[:10]], slots[off[:10]] = -1, -1
+    seq[off[10:20]], slots[off[10:20]] = S, 1 << 40
+    pos[off[20:30]] = 1 << 17
+    pos[off[30:]] = -7
+    step = 997
+
+    def run(pool, lo, hi):
+        kvr.kv4_append_rope(k[lo:hi], v[lo:hi], pos[lo:hi], None if by_slot else seq[lo:hi], table, scale, pool,
+                            slots=slots[lo:hi] if by_slot else None)
+
+    run(pools[0], 0, T)
+    status = kvr.device_status()
+    for lo in range(0, T, step):
+        run(pools[1], lo, min(lo + step, T))
+    assert kvr.device_status() == status == kvr.DEV_BAD_POS | (kvr.DEV_BAD_BLOCK if by_slot else kvr.DEV_BAD_SEQ)
+    assert torch.equal(pools[0].block_table, pools[1].block_table)
+    assert torch.equal(pools[0].data, pools[1].data)
+
+
 def test_append_padding_and_flags(table):
     gen = _gen(8)
     T, hkv, bs = 8, 2, 32
