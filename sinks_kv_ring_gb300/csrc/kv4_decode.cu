@@ -16,7 +16,7 @@
 //     no conversion, no bias and no rounding.  The factor 16 of every other
 //     dim is divided out of q beforehand (K) or of the sums afterwards (V).
 //     (e4m3 operands would take 3 per 8 codes, but their m16n8k32 product runs
-//     at 20 cycles here: 470 us at batch 64 where this takes 288.)
+//     at 20 cycles here: 470 us at batch 64 where this takes 285.)
 //   * Queries are rotated, scaled by softmax_scale log2(e), brought by a power
 //     of two to a largest magnitude in [2^14, 2^15) per head, and rounded once
 //     to fp16 (2^-11 of a value, where the bf16 decode rounds to 2^-8).
@@ -40,15 +40,20 @@
 // registers.
 //
 // What bounds it.  180 bytes and 2 (192 + 128) G flops per key and KV head.
-// Up to 8 heads: HBM (batch 64 at 32769 keys, 4 x 8 heads: 230 us, 6.55 TB/s,
-// 0.97 of the copy rate).  At 16 heads the products alone take 153 us (86 of
+// Up to 8 heads: HBM (batch 64 at 32769 keys, 4 x 8 heads: 227 us, 6.65 TB/s,
+// 0.98 of the copy rate).  At 16 heads the products alone take 153 us (86 of
 // them per unit at 8.2 cycles an SM quarter) and every other instruction of a
 // quarter about 0.75 cycles on top, as masks, loads and softmax share its
-// register ports with them: 287 us (5.26 TB/s, 0.78), where the same pipeline
+// register ports with them: 285 us (5.30 TB/s, 0.78), where the same pipeline
 // without any arithmetic takes 240.  Measured and left out: two CTAs of 255
 // registers (322 us), 16-key units with four CTAs (335), scores of one unit
 // interleaved with the sums of the one before (323), queries held in registers
-// (327).
+// (327).  A single row at 32769 keys, 4 x 16 heads, takes 13.3 us: about 2 of
+// launch, 2.5 until the first tile is there, 5 of products, 1 of joining the
+// CTA's warps and 3 of merging 114 pieces a row.  The plan made before the wait
+// for the kernel ahead and in the merge kernel while the split kernel ends took
+// 1.4 us off that and 1 to 2 off ragged batches; requesting the first tiles
+// into L2 before the wait changed nothing.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -124,26 +129,41 @@ __device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpre
 // of dims 64 g + 16 t + 8 (j / 2) + 2 (j % 2) + {0, 4} (registers 0, 1: rows a
 // and a + 8) and + {1, 5}, divided by 16 (registers 2, 3): what masking word
 // j / 2, shifted by 8 (j % 2), leaves.
-__device__ __forceinline__ void kv4_query(const uint16_t *__restrict__ qh, int G, const float *__restrict__ cs_row,
-                                          float scale_log2, uint8_t *smem, int tid) {
+struct K4Query {
+  uint2 lo, hi;
+  uint4 g1, g2;
+  float4 t0, t1;
+};
+__device__ __forceinline__ K4Query kv4_query_load(const uint16_t *__restrict__ qh, int G,
+                                                  const float *__restrict__ cs_row, int tid) {
+  const int r = tid >> 3, c = tid & 7;
+  K4Query Q = {};
+  if (r < G) {
+    const uint16_t *qr = qh + r * DQK;
+    Q.lo = *reinterpret_cast<const uint2 *>(qr + 4 * c);
+    Q.hi = *reinterpret_cast<const uint2 *>(qr + 32 + 4 * c);
+    Q.g1 = *reinterpret_cast<const uint4 *>(qr + 64 + 8 * c);
+    Q.g2 = *reinterpret_cast<const uint4 *>(qr + 128 + 8 * c);
+    Q.t0 = *reinterpret_cast<const float4 *>(cs_row + 8 * c);
+    Q.t1 = *reinterpret_cast<const float4 *>(cs_row + 8 * c + 4);
+  }
+  return Q;
+}
+__device__ __forceinline__ void kv4_query(const K4Query &Q, int G, float scale_log2, uint8_t *smem, int tid) {
   const int r = tid >> 3, c = tid & 7;
   float y[24];
 #pragma unroll
   for (int i = 0; i < 24; ++i) y[i] = 0.f;
   if (r < G) {
-    const uint16_t *qr = qh + r * DQK;
-    const uint2 lo = *reinterpret_cast<const uint2 *>(qr + 4 * c), hi = *reinterpret_cast<const uint2 *>(qr + 32 + 4 * c);
-    const uint4 g1 = *reinterpret_cast<const uint4 *>(qr + 64 + 8 * c), g2 = *reinterpret_cast<const uint4 *>(qr + 128 + 8 * c);
-    const float4 t0 = *reinterpret_cast<const float4 *>(cs_row + 8 * c), t1 = *reinterpret_cast<const float4 *>(cs_row + 8 * c + 4);
-    const float cs[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
-    const uint16_t *a = reinterpret_cast<const uint16_t *>(&lo), *b = reinterpret_cast<const uint16_t *>(&hi);
+    const float cs[8] = {Q.t0.x, Q.t0.y, Q.t0.z, Q.t0.w, Q.t1.x, Q.t1.y, Q.t1.z, Q.t1.w};
+    const uint16_t *a = reinterpret_cast<const uint16_t *>(&Q.lo), *b = reinterpret_cast<const uint16_t *>(&Q.hi);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float v1 = bf2f(a[i]), v2 = bf2f(b[i]);
       y[i] = (v1 * cs[2 * i] - v2 * cs[2 * i + 1]) * scale_log2;
       y[4 + i] = (v2 * cs[2 * i] + v1 * cs[2 * i + 1]) * scale_log2;
     }
-    const uint16_t *e1 = reinterpret_cast<const uint16_t *>(&g1), *e2 = reinterpret_cast<const uint16_t *>(&g2);
+    const uint16_t *e1 = reinterpret_cast<const uint16_t *>(&Q.g1), *e2 = reinterpret_cast<const uint16_t *>(&Q.g2);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       y[8 + i] = bf2f(e1[i]) * scale_log2;
@@ -162,6 +182,7 @@ __device__ __forceinline__ void kv4_query(const uint16_t *__restrict__ qh, int G
   const float up = __uint_as_float((uint32_t)(127 + (a > 0 ? a : 0)) << 23);   // 2^max(a, 0)
   const float dn = a < 0 ? __uint_as_float((uint32_t)max(127 + a, 1) << 23) : 1.f;  // 2^min(a, 0)  (a >= -113)
   float sum[3] = {0.f, 0.f, 0.f};
+  __half hs[24];
 #pragma unroll
   for (int i = 0; i < 24; ++i) {
     const int g = i >> 3;
@@ -172,7 +193,9 @@ __device__ __forceinline__ void kv4_query(const uint16_t *__restrict__ qh, int G
     const __half h = __float2half_rn((nib & 1) ? v * 0.0625f : v);
     sum[g] += __half2float(h) * ((nib & 1) ? 16.f : 1.f);
     const int at = ((g * 4 + j) * 32 + (r & 7) * 4 + (d >> 4)) * 16 + ((nib & 1) * 2 + (r >> 3)) * 4 + (nib >> 2) * 2;
-    *reinterpret_cast<__half *>(smem + at) = h;
+    hs[i] = h;
+    if (g == 0) *reinterpret_cast<__half *>(smem + at) = h;
+    else if (nib >= 4) *reinterpret_cast<__half2 *>(smem + at - 2) = __halves2half2(hs[i - 4], h);
   }
 #pragma unroll
   for (int g = 0; g < 3; ++g)
@@ -209,11 +232,10 @@ __device__ __forceinline__ int kv4_units(long long p, int s, int num_seqs, int64
 }
 
 // The line's prefix over the sequences (prefix[b]: units ahead of sequence b)
-// by NT threads; returns L.
-template <int NT>
-__device__ long long kv4_plan(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv,
-                              int num_seqs, int64_t max_pos, long long max_ctx, int ctas, int64_t *prefix,
-                              unsigned *status) {
+// by NT threads, `get(b, p, s)` giving sequence b's position and id; returns L.
+template <int NT, typename Get>
+__device__ __forceinline__ long long kv4_plan(Get get, int B, int hkv, int num_seqs, int64_t max_pos, long long max_ctx,
+                                              int ctas, int64_t *prefix, unsigned *status) {
   __shared__ long long s_sum[NT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long base = 0;
@@ -221,7 +243,10 @@ __device__ long long kv4_plan(const int64_t *__restrict__ pos, const int32_t *__
     const int b = b0 + tid;
     long long x = 0;
     if (b < B) {
-      const int u = kv4_units(pos[b], seq[b], num_seqs, max_pos, max_ctx, status);
+      long long p;
+      int q;
+      get(b, p, q);
+      const int u = kv4_units(p, q, num_seqs, max_pos, max_ctx, status);
       x = u ? (long long)hkv * (u + K4_ROW) : 0;
     }
     const long long mine = x;
@@ -265,8 +290,8 @@ __global__ void __launch_bounds__(K4P_THREADS)
                     int64_t max_pos, long long max_ctx, int ctas, int64_t *__restrict__ plan, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  const long long L =
-      kv4_plan<K4P_THREADS>(pos, seq, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + K4_PLAN, status);
+  const auto get = [&](int b, long long &p, int &s) { p = pos[b], s = seq[b]; };
+  const long long L = kv4_plan<K4P_THREADS>(get, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + K4_PLAN, status);
   if (threadIdx.x == 0) plan[0] = L;
 }
 
@@ -285,10 +310,24 @@ struct K4Args {
   float *part_o;
   unsigned *status;
   unsigned long long stall_ns;  // test hook: warp 0's first wait is on a barrier that nothing completes (0: no stall)
-  uint16_t *out;               // DIRECT
+  uint16_t *out;
   int cs;                      // DIRECT: CTAs of a row
   unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
 };
+
+// CTA's part of the line from unit x on: row (b, kv), units [lo, hi) of its
+// keys (none where hi <= lo: set-up alone); x moves behind it.
+__device__ __forceinline__ void kv4_part(const int64_t *prefix, int B, int hkv, long long line_end, long long &x, int &b,
+                                         int &kv, int &lo, int &hi) {
+  b = kv4_find(prefix, B, x);
+  const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
+  kv = (int)((x - prefix[b]) / rowlen);
+  const int off = (int)(x - prefix[b] - (long long)kv * rowlen);
+  const int stop = (int)min((long long)rowlen, off + (line_end - x));
+  x += stop - off;
+  lo = max(off - K4_ROW, 0);
+  hi = stop - K4_ROW;
+}
 
 // SMALL: groups of up to 8 query heads.  The keys are then the 16 rows of the
 // products and the heads their 8 columns (scores K Q^T, sums V^T P^T): half
@@ -321,25 +360,45 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     }
     tc::fence_mbar_init();
   }
+  // The plan: every CTA makes it for small batches.  For up to a sequence a
+  // thread it is made before the wait for the kernel ahead, with the CTA's
+  // first part, from positions and ids read early (ld_early_s32); after the
+  // wait it stands if they read the same, else it is made again.
+  const bool early = !DIRECT && A.B <= K4_WARPS * 32;
+  const int64_t *prefix = A.B <= K4_INLINE_MAX ? sPrefix : A.plan + K4_PLAN;
+  long long x = 0, line_end = 0, early_p = 0;
+  int b = 0, kv = 0, lo = 0, hi = 0, early_s = 0;
+  bool ready = DIRECT;  // b, kv, lo, hi hold the next part
+  auto plan = [&](auto get, unsigned *status) {
+    return kv4_plan<K4_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status);
+  };
+  auto share = [&](long long L) {
+    x = blockIdx.x * L;
+    line_end = min(x + L, (long long)prefix[A.B]);
+    ready = x < line_end;
+    if (ready) kv4_part(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
+  };
+  if (early) {
+    if (tid < A.B) {
+      early_p = ld_early_s64(A.pos + tid);
+      early_s = ld_early_s32(A.seq + tid);
+    }
+    share(plan([&](int, long long &p, int &s) { p = early_p, s = early_s; }, nullptr));
+  }
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
-
-  // the plan: every CTA makes it for small batches, CTA 0 stores it for the merge
-  const int64_t *prefix = A.plan + K4_PLAN;
-  long long L = 0;
-  if (DIRECT) {
-  } else if (A.B <= K4_INLINE_MAX) {
-    L = kv4_plan<K4_WARPS * 32>(A.pos, A.seq, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix,
-                                blockIdx.x == 0 ? A.status : nullptr);
-    if (blockIdx.x == 0) {
-      for (int b = tid; b <= A.B; b += blockDim.x) A.plan[K4_PLAN + b] = sPrefix[b];
-      if (tid == 0) A.plan[0] = L;
-    }
-    prefix = sPrefix;
-  } else {
-    L = A.plan[0];
+  bool same = early;
+  if (early && tid < A.B) {
+    const long long p = A.pos[tid];
+    const int s = A.seq[tid];
+    same = p == early_p && s == early_s;
+    if (blockIdx.x == 0) kv4_units(p, s, A.pool.num_seqs, A.max_pos, A.max_ctx, A.status);
   }
+  same = __syncthreads_and(same);
+  if (!DIRECT && !same)
+    share(A.B <= K4_INLINE_MAX
+              ? plan([&](int i, long long &p, int &s) { p = A.pos[i], s = A.seq[i]; }, blockIdx.x == 0 ? A.status : nullptr)
+              : A.plan[0]);
 
   const int tpb = A.pool.block_size >> 4;
   const int t = lane & 3, gr = lane >> 2;
@@ -347,15 +406,14 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   uint32_t sent = 0;  // and issued
   bool gave_up = false;
 
-  const long long line_end = DIRECT ? 1 : min((blockIdx.x + 1) * L, (long long)prefix[A.B]);
-  for (long long x = DIRECT ? 0 : blockIdx.x * L; x < line_end;) {
-    int b, kv, w = 0, key_lo, key_hi;
+  while (ready || x < line_end) {
+    int w = 0, key_lo, key_hi;
     long long p;
     if (DIRECT) {
+      ready = false;
       const int row = (int)blockIdx.x / A.cs, rank = (int)blockIdx.x - row * A.cs;
       b = row / hkv;
       kv = row - b * hkv;
-      x = 1;
       p = A.pos[b];
       const int units = kv4_units(p, A.seq[b], A.pool.num_seqs, A.max_pos, A.max_ctx,
                                   kv == 0 && rank == 0 && tid == 0 ? A.status : nullptr);
@@ -369,22 +427,19 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       key_hi = (int)min((long long)min((rank + 1) * each, units) * K4_UNIT, p + 1);
       if (key_hi < key_lo) key_hi = key_lo;
     } else {
-      b = kv4_find(prefix, A.B, x);
-      const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
-      kv = (int)((x - prefix[b]) / rowlen);
-      const int off = (int)(x - prefix[b] - (long long)kv * rowlen);
-      const int stop = (int)min((long long)rowlen, off + (line_end - x));
-      x += stop - off;
-      if (stop <= K4_ROW) continue;  // set-up alone: no piece
+      if (!ready) kv4_part(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
+      ready = false;
+      if (hi <= 0) continue;  // set-up alone: no piece
       w = (int)blockIdx.x + b * hkv + kv;
       p = A.pos[b];
-      key_lo = max(off - K4_ROW, 0) * K4_UNIT;
-      key_hi = (int)min((long long)(stop - K4_ROW) * K4_UNIT, p + 1);
+      key_lo = lo * K4_UNIT;
+      key_hi = (int)min((long long)hi * K4_UNIT, p + 1);
     }
     const int s = A.seq[b];  // (a row that gets here has a valid position and id)
     const int nunit = (key_hi - key_lo + K4_UNIT - 1) / K4_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K4_WARPS - 1) / K4_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
+    const K4Query Q = kv4_query_load(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, tid);
     tc::fence_proxy_async_smem();                   // the last piece's merge area lies over the stages:
     if (__syncthreads_or(*abort_flag != 0)) break;  // it is free again, its accesses ahead of the copies'
 
@@ -437,7 +492,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     for (int i = 0; i < K4_STAGES - 1; ++i)
       if (i < my_n) issue(i);
 
-    kv4_query(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, A.scale_log2, smem, tid);
+    kv4_query(Q, G, A.scale_log2, smem, tid);
     __syncthreads();
     int run_n = my_n;
     if (A.stall_ns && warp == 0 && !gave_up && !tc::mbar_wait(sBase + K4_OFF_STALL, 0, abort_flag, A.stall_ns)) {
@@ -1003,25 +1058,37 @@ constexpr int K4M_WARPS = 16;
 constexpr int K4M_K = 8;
 
 __global__ void __launch_bounds__(K4M_WARPS * 32)
-    kv4_merge_kernel(int B, int hq, int G, int hkv,
-                     const int64_t *__restrict__ plan, int nw, const float *__restrict__ part_ml,
-                     const float *__restrict__ part_o, uint16_t *__restrict__ out) {
+    kv4_merge_kernel(K4Args A, int ctas, int nw) {
   __shared__ float s_ml[K4M_WARPS][2];
   __shared__ float4 s_acc[K4M_WARPS][32];
+  __shared__ int64_t s_prefix[K4_INLINE_MAX + 1];
+  const int G = A.G, hkv = A.pool.hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % nw;
   const long long row = (long long)blockIdx.x * (K4M_WARPS / nw) + warp / nw;  // (b hkv + kv) G + g
-  const bool have = row < (long long)B * hq;
+  const bool have = row < (long long)A.B * A.hq;
   const int g = have ? (int)(row % G) : 0, pair = have ? (int)(row / G) : 0, b = pair / hkv, kv = pair - b * hkv;
-  pdl_wait();
-  pdl_trigger();
-  const long long L = plan[0], at = have ? plan[K4_PLAN + b] : 0;
-  const long long len = have ? (plan[K4_PLAN + b + 1] - at) / hkv : 0;  // 0: nothing to attend to
+  // The plan, while the split kernel still runs: that kernel let this one start
+  // after its own wait, so the batch (and the plan kernel's plan) are there.
+  long long L, at, next;
+  if (A.B <= K4_INLINE_MAX) {
+    const auto get = [&](int i, long long &p, int &s) { p = ld_early_s64(A.pos + i), s = ld_early_s32(A.seq + i); };
+    L = kv4_plan<K4M_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, ctas, s_prefix, nullptr);
+    at = s_prefix[b];
+    next = s_prefix[b + 1];
+  } else {
+    L = ld_early_s64(A.plan);
+    at = ld_early_s64(A.plan + K4_PLAN + b);
+    next = ld_early_s64(A.plan + K4_PLAN + b + 1);
+  }
+  const long long len = have ? (next - at) / hkv : 0;  // 0: nothing to attend to
   long long c0 = 0;
   int n = 0;
   if (len > 0) {
     c0 = (at + kv * len + K4_ROW) / L;
     n = (int)((at + kv * len + len - 1) / L - c0) + 1;
   }
+  pdl_wait();
+  pdl_trigger();
   float M = NEG_INF, S = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = sub; i0 < n; i0 += K4M_K * nw) {
@@ -1034,8 +1101,8 @@ __global__ void __launch_bounds__(K4M_WARPS * 32)
       o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
         const long long r = (c0 + i + pair) * G + g;
-        ml[k] = *reinterpret_cast<const float2 *>(part_ml + r * 2);
-        o[k] = *reinterpret_cast<const float4 *>(part_o + r * DV + 4 * lane);
+        ml[k] = *reinterpret_cast<const float2 *>(A.part_ml + r * 2);
+        o[k] = *reinterpret_cast<const float4 *>(A.part_o + r * DV + 4 * lane);
       }
     }
     float Mn = M;
@@ -1088,7 +1155,7 @@ __global__ void __launch_bounds__(K4M_WARPS * 32)
   }
   if (!have || sub != 0) return;
   const float inv = S == 0.f ? 0.f : 1.f / S;  // (a NaN sum stays one)
-  *reinterpret_cast<uint2 *>(out + ((long long)b * hq + (long long)kv * G + g) * DV + 4 * lane) =
+  *reinterpret_cast<uint2 *>(A.out + ((long long)b * A.hq + (long long)kv * G + g) * DV + 4 * lane) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
@@ -1168,8 +1235,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   int nw = 1;
   while (nw < K4M_WARPS && nw * 4 < est) nw *= 2;
   const long long blocks = ((long long)B * hq + K4M_WARPS / nw - 1) / (K4M_WARPS / nw);
-  return launch_pdl(kv4_merge_kernel, dim3((unsigned)blocks), dim3(K4M_WARPS * 32), 0, st, B, hq, G, hkv,
-                    (const int64_t *)A.plan, nw, (const float *)A.part_ml, (const float *)A.part_o, out);
+  return launch_pdl(kv4_merge_kernel, dim3((unsigned)blocks), dim3(K4M_WARPS * 32), 0, st, A, ctas, nw);
 }
 
 }  // namespace kvr

@@ -414,6 +414,40 @@ def test_decode_repeats_bit_for_bit_and_in_graphs(table):
     _check_decode(runs[1][2], q, [40, 3, 799], [0, 1, 2], pool, table)
 
 
+@pytest.mark.parametrize("B", [3, 128, 150, 300])
+def test_decode_of_positions_written_right_before(table, B):
+    """Positions and ids come from the kernel launched just ahead, other ones each time: what a decode reads of the batch
+    before that kernel is done never counts."""
+    gen = _gen(70 + B)
+    hkv, G, ctx, bs = 2, 16, 4096, 64
+    pool = _filled(gen, [ctx, ctx, ctx], hkv, bs, table, max_ctx=ctx)
+    pool = kvr.Kv4Layout(pool.data, pool.block_table[torch.arange(B, device=DEV) % 3].contiguous())
+    q = torch.randn(B, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    own = torch.zeros(B, ctx // bs, dtype=torch.int32, device=DEV)
+    free, left = torch.zeros(B, dtype=torch.int32, device=DEV), _ints([B], torch.int32)
+    cu, count = torch.empty(B + 1, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    pos, slots = torch.zeros(B, dtype=torch.int64, device=DEV), torch.empty(B, dtype=torch.int64, device=DEV)
+    seq, add = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+    ws = torch.empty(kvr.full_attn_decode_kv4_workspace_size(B, hkv * G, hkv, ctx), dtype=torch.uint8, device=DEV)
+    steps = []
+    for _ in range(12):
+        lens = torch.randint(0, 200, (B,), generator=gen, device=DEV)
+        lens[torch.randint(0, B, (2,), generator=gen, device=DEV)] = torch.randint(0, ctx, (2,), generator=gen, device=DEV)
+        steps.append((lens, torch.randperm(B, generator=gen, device=DEV).to(torch.int32),
+                      torch.empty(B, hkv * G, 128, dtype=torch.bfloat16, device=DEV)))
+    torch.cuda.synchronize()
+    for lens, ids, out in steps:
+        kvr.kv_pages_grow(own, 1, bs, ids, lens, add, free, left, cu, pos, seq, slots, free_count_out=count)
+        kvr.full_attn_decode_kv4(q, pos, seq, pool, table, SCALE, ctx, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    for lens, ids, out in steps:
+        assert torch.equal(out, kvr.full_attn_decode_kv4(q, lens, ids, pool, table, SCALE, ctx))
+    assert kvr.device_status() == 0
+    lens, ids, out = steps[-1]
+    few = [0, 1, 2] if B > 3 else list(range(B))
+    _check_decode(out[few], q[few], lens[few].tolist(), ids[few].tolist(), pool, table)
+
+
 @pytest.mark.parametrize("B", [33, 130, 700])
 def test_decode_many_sequences(table, B):
     gen = _gen(B)
