@@ -545,7 +545,10 @@ kvr_status kv4_append_rope(const kvr_bf16 *k, const kvr_bf16 *v, const int64_t *
                            const int64_t *slots, int32_t T, int32_t Hkv, const float *rope_cos_sin, int64_t max_pos,
                            float value_scale, const kvr_kv4_layout *dst, void *stream);
 
-/* Workspace bytes for full_attn_decode_kv4 (0 on bad arguments). */
+/*
+ * Workspace bytes for full_attn_decode_kv4: 0 on bad arguments, and where the
+ * call needs none (short contexts; workspace may then be NULL).
+ */
 size_t full_attn_decode_kv4_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int64_t max_ctx);
 
 /*

@@ -712,16 +712,18 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
     _want_len(seq, "seq", B)
     if workspace is None:
         n = full_attn_decode_kv4_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)  # (the allocator may hand it on while that stream still works)
-    _want(workspace, "workspace", torch.uint8, 1)
+        if n:  # (short contexts need none)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            if stream is not None:
+                workspace.record_stream(stream)  # (the allocator may hand it on while that stream still works)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1)
     out = _out(out, B, Hq, q)
     _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_decode_kv4(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),
                                       table.shape[0], float(softmax_scale), int(max_ctx), _ptr(workspace),
-                                      workspace.numel(), _ptr(out), _stream(stream)))
+                                      0 if workspace is None else workspace.numel(), _ptr(out), _stream(stream)))
     return out
 
 

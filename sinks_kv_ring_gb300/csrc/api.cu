@@ -682,7 +682,7 @@ kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int
   if (!aligned16(q) || !aligned16(out)) return fail(KVR_EINVAL, "q/out not 16-byte aligned");
   if (max_ctx > (1 << 30)) return fail(KVR_EUNSUPPORTED, "max_ctx %lld > 2^30", (long long)max_ctx);
   const size_t need = kvr::kv4_decode_workspace(B, Hq, pool->num_kv_heads, max_ctx);
-  if (!workspace || workspace_bytes < need)
+  if (need && (!workspace || workspace_bytes < need))
     return fail(KVR_EWORKSPACE, "workspace %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, need);
   if (!aligned16(workspace)) return fail(KVR_EINVAL, "workspace not 16-byte aligned");
   unsigned *st = nullptr;

@@ -1169,9 +1169,20 @@ size_t pieces_cap(int B, int hkv, long long max_ctx) {
   return (size_t)(rows + (most < R ? most : R));
 }
 
+// Short contexts go by clusters in one launch.  Measured at max_ctx 1024
+// (one launch against the work line's two): 1 x 2 KV heads at 4 query heads
+// each 5.7 us against 7.1, 16 x 4 at 16 11.1 / 13.2, 64 x 4 23.0 / 24.3, 600
+// x 4 121 / 156; at 2048 8 x 4 11.3 / 12.5 but 64 x 4 38.1 / 34.4: a row then
+// needs its eight CTAs.
+bool one_launch(int B, int hkv, long long max_ctx) {
+  const long long R = (long long)K4_CTAS * num_sms(), units = (max_ctx + K4_UNIT - 1) / K4_UNIT;
+  return units <= (8LL * B * hkv <= R ? 64 : 32);
+}
+
 }  // namespace
 
 size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
+  if (one_launch(B, hkv, max_ctx)) return 0;
   const size_t G = (size_t)(hq / hkv), n = pieces_cap(B, hkv, max_ctx);
   return plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
 }
@@ -1182,12 +1193,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   const int hkv = pool.hkv, G = hq / hkv, R = K4_CTAS * num_sms();
   const long long rows = (long long)B * hkv, units = (max_ctx + K4_UNIT - 1) / K4_UNIT;
   if (rows > 0x7ffffffLL) return cudaErrorInvalidValue;  // (its queries alone would fill the GPU)
-  // Short contexts go by clusters in one launch.  Measured at max_ctx 1024
-  // (one launch against the work line's two): 1 x 2 KV heads at 4 query heads
-  // each 5.7 us against 7.1, 16 x 4 at 16 11.1 / 13.2, 64 x 4 23.0 / 24.3, 600
-  // x 4 121 / 156; at 2048 8 x 4 11.3 / 12.5 but 64 x 4 38.1 / 34.4: a row then
-  // needs its eight CTAs.
-  const bool direct = units <= (8 * rows <= R ? 64 : 32);
+  const bool direct = one_launch(B, hkv, max_ctx);
   void (*const kernel)(K4Args) = G <= 8 ? (direct ? kv4_decode_kernel<true, true> : kv4_decode_kernel<true, false>)
                                         : (direct ? kv4_decode_kernel<false, true> : kv4_decode_kernel<false, false>);
   cudaError_t e = ensure_smem_limit(17 + 2 * (G <= 8) + direct, (const void *)kernel, K4_SMEM, true);

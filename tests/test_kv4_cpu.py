@@ -124,10 +124,12 @@ def test_kv4_host_validation_codes(L):
     assert app(None, None, None, None, None, 0, 4, P, 1000, 0.7, R(pool), None) == 0
 
     dec, size = L.full_attn_decode_kv4, L.full_attn_decode_kv4_workspace_size
-    need = size(2, 64, 4, 1000)
-    assert need > 0 and size(2, 62, 4, 1000) == 0 and size(0, 64, 4, 1000) == 0 and size(2, 64, 4, 0) == 0
-    assert dec(P, P, P, 2, 64, R(pool), P, 1000, 0.1, 1000, P, need - 1, P, None) == -3
-    assert dec(P, P, P, 2, 64, R(pool), P, 1000, 0.1, 1000, None, need, P, None) == -3
+    need = size(2, 64, 4, 10000)
+    assert need > 0 and size(2, 62, 4, 10000) == 0 and size(0, 64, 4, 10000) == 0 and size(2, 64, 4, 0) == 0
+    assert size(2, 64, 4, 1000) == 0                                                  # short contexts need none
+    long = _pool(max_blocks=200)
+    assert dec(P, P, P, 2, 64, R(long), P, 10000, 0.1, 10000, P, need - 1, P, None) == -3
+    assert dec(P, P, P, 2, 64, R(long), P, 10000, 0.1, 10000, None, need, P, None) == -3
     assert dec(P, P, P, 2, 64, R(pool), P, 1000, 0.1, 1001, P, 1 << 40, P, None) == -2
     assert dec(P, P, P, 2, 64, R(pool), P, 5000, 0.1, 1025, P, 1 << 40, P, None) == -2
     assert dec(P, P, P, 2, 62, R(pool), P, 1000, 0.1, 100, P, 1 << 40, P, None) == -1
