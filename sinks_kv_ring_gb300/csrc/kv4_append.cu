@@ -17,17 +17,17 @@
 // away and a 16-byte load brings a lane's values, all five in flight before
 // the destination is looked up.
 //
-// What bounds it: instructions (unpacking, extrema, the exact quotient),
-// 52 us for 302,216 (token, KV head) pairs where their 820 bytes each take
-// 37 us at the copy rate.  The extrema of the five groups go through one
-// butterfly that halves what a lane carries at each step, a group's scale is
-// taken by one lane of its token (2 divisions instead of 10 per lane) and the
-// codes come in packed pairs.  Loading the next head's values ahead of their
-// use, into registers or shared memory, gained nothing (58 us or more): 32
-// warps an SM cover the loads.  The stores are 2 and 4 bytes wide (a position's
-// V codes lie apart) and merge in L2; putting whole tiles together in shared
-// memory first, for full-sector stores, measured slower (73 us against 64 at
-// the time): they are not what bounds it.
+// What bounds it: instructions, some 480 per four tokens of a head (unpacking,
+// extrema, the exact quotient), issued in 64% of the cycles: 52 us for 302,216
+// (token, KV head) pairs where their 820 bytes each take 37 us at the copy
+// rate.  The extrema of the five groups go through one butterfly that halves
+// what a lane carries at each step, a group's scale is taken by one lane of its
+// token (2 divisions instead of 10 per lane) and the codes come in packed
+// pairs.  Loading the next head's values ahead of their use, into registers or
+// shared memory, gained nothing (54 us or more).  The stores are 2 and 4 bytes
+// wide (a position's V codes lie apart) and merge in L2; putting whole tiles
+// together in shared memory first, for full-sector stores, measured slower (73
+// us against 64 at the time): they are not what bounds it.
 #include "kv4.cuh"
 #include "launch.h"
 
