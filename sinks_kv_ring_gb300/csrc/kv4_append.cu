@@ -199,7 +199,6 @@ __device__ __forceinline__ uint64_t bf16x2_f32x2(uint32_t x) {
 template <bool ANY>
 __device__ __forceinline__ void put_codes(const uint64_t (&x0)[4], const uint4 (&raw)[5], float vscale, uint32_t mysm,
                                           float myr, uint8_t *kd, uint8_t *vd, bool put, int lane) {
-  const uint64_t vs = f32x2(vscale, vscale);
 #pragma unroll
   for (int g = 0; g < 5; ++g) {
     const int from = (lane & 24) + (g == 0 ? 1 : 2 * g - 2);
@@ -209,8 +208,11 @@ __device__ __forceinline__ void put_codes(const uint64_t (&x0)[4], const uint4 (
     const uint32_t e[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = g == 0 ? x0[i] : bf16x2_f32x2(e[i]);
-      if (g >= KV4_KG) x[i] = mul_f32x2(x[i], vs);
+      if (g < KV4_KG) {
+        x[i] = g == 0 ? x0[i] : bf16x2_f32x2(e[i]);
+      } else {  // (a packed product would be joined with the subtraction that follows, and not be rounded)
+        x[i] = f32x2(__fmul_rn(__uint_as_float(e[i] << 16), vscale), __fmul_rn(__uint_as_float(e[i] & 0xffff0000u), vscale));
+      }
     }
     const uint32_t w = ANY ? kv4_codes_any(x, sm, rc) : kv4_codes(x, sm, rc);
     if (put) {
@@ -235,21 +237,23 @@ __device__ __forceinline__ void put_token(const uint4 (&raw)[5], const float *tr
   // contraction.
   uint64_t x0[4];
   {
-    uint64_t cs[8];  // (cos, sin) of the lane's dims; not kept across heads: 16 registers
+    float cs[16];  // (cos, sin) of the lane's dims; not kept across heads: 16 registers
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      asm volatile("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(cs[2 * u]), "=l"(cs[2 * u + 1]) : "l"(tr + 4 * u));
+      asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(cs[4 * u]), "=f"(cs[4 * u + 1]), "=f"(cs[4 * u + 2]), "=f"(cs[4 * u + 3])
+                   : "l"(tr + 4 * u));
     }
     const uint32_t neg = c < 4 ? 0x80008000u : 0u;  // a - b, or a + b
     const uint32_t e[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t o = __shfl_xor_sync(FULLW, e[i], 4) ^ neg;
-      float a, b, a1, b1;
-      f32x2_split(mul_f32x2(f32x2(__uint_as_float(e[i] << 16), __uint_as_float(o << 16)), cs[2 * i]), a, b);
-      f32x2_split(mul_f32x2(f32x2(__uint_as_float(e[i] & 0xffff0000u), __uint_as_float(o & 0xffff0000u)), cs[2 * i + 1]),
-                  a1, b1);
-      x0[i] = f32x2(__fadd_rn(a, b), __fadd_rn(a1, b1));
+      const float a0 = __fmul_rn(__uint_as_float(e[i] << 16), cs[4 * i]);
+      const float b0 = __fmul_rn(__uint_as_float(o << 16), cs[4 * i + 1]);
+      const float a1 = __fmul_rn(__uint_as_float(e[i] & 0xffff0000u), cs[4 * i + 2]);
+      const float b1 = __fmul_rn(__uint_as_float(o & 0xffff0000u), cs[4 * i + 3]);
+      x0[i] = f32x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
     }
   }
   // Extrema.  Each step of a butterfly over the token's eight lanes halves

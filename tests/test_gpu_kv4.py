@@ -130,6 +130,44 @@ def test_append_corner_groups(table):
     assert np.array_equal(got, want)
 
 
+def test_append_value_products_are_rounded(table):
+    """Values whose code hangs on the rounding of value times value scale: a product added without it falls on the other
+    side of a half step."""
+    rng = np.random.default_rng(1)
+    vs = np.float32(VS)
+
+    def bf16(x):
+        return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).bfloat16().float().numpy()
+
+    n = 400000
+    x = np.zeros((n, 64), np.float32)
+    x[:, 0], x[:, 1] = bf16(-1 - 3 * rng.random(n)), bf16(1 + 3 * rng.random(n))
+    with np.errstate(divide="ignore", invalid="ignore"):
+        _, s, m = (a.astype(np.float32) if a.dtype != np.uint8 else a for a in o4.quantise(x * vs))
+        v = bf16((m + s * (np.arange(15, dtype=np.float32) + np.float32(0.5))) / vs)
+        rounded = (v * vs - m) / s
+        fused = (v.astype(np.float64) * np.float64(vs) - m).astype(np.float32) / s
+    hit = (np.rint(rounded) != np.rint(fused)) & (v > x[:, :1]) & (v < x[:, 1:2])
+    rows = np.flatnonzero(hit.any(1))
+    assert len(rows) >= 16
+    rows = rows[:16]
+    x[rows, 2:17] = np.where(hit[rows], v[rows], 0)
+    vals = torch.from_numpy(x[rows]).bfloat16().to(DEV)                     # [16, 64]
+    v1 = torch.cat([vals, vals.flip(1)], 1)[:, None].expand(16, 2, 128).contiguous()
+    k1, _ = _kv(_gen(9), 16, 2)
+    small = _pool(_gen(4), 1, 2, 16, 16, fill=0)
+    pos = torch.arange(16, device=DEV)
+    want = _want_bytes(small, k1, v1, [(int(small.block_table[0, 0]), t) for t in range(16)], pos, table)
+    _append(small, k1, v1, 0, 0, table)
+    assert np.array_equal(small.data.cpu().numpy(), want)
+    many = 2200                                                             # 70,400 pairs: the same values 2200 times
+    big = _pool(_gen(4), many, 2, 16, 16, fill=0)
+    kvr.kv4_append_rope(k1.repeat(many, 1, 1), v1.repeat(many, 1, 1), pos.repeat(many),
+                        torch.arange(many, device=DEV).repeat_interleave(16).to(torch.int32), table, VS, big)
+    tile = small.data[small.block_table[0, 0].long()]
+    assert torch.equal(big.data[big.block_table[:, 0].long()], tile.expand(many, *tile.shape))
+
+
 @pytest.mark.parametrize("hkv,by_slot,scale", [(1, False, VS), (2, True, VS), (3, False, -VS), (5, True, -1.0), (8, False, VS)])
 def test_append_many_as_few(table, hkv, by_slot, scale):
     """A call of many (token, KV head) pairs writes the bytes that calls of a few tokens write, and says the same of the
