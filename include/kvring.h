@@ -136,8 +136,9 @@ typedef struct kvr_kv_layout {
  *     K minima  fp16 at byte 2784 + 8 r + 2 g (the fourth is zero);
  *   block_table [num_seqs][max_blocks] int32: position p of sequence s lies in
  *   block block_table[s][p / block_size], at p % block_size.
- * block_size is a multiple of 16 in [16, 1024].  The data needs no
- * initialisation: what no append wrote is never used.
+ * block_size is a multiple of 16 in [16, 1024], max_blocks * block_size at
+ * most 2^35.  The data needs no initialisation: what no append wrote is never
+ * used.
  */
 typedef struct kvr_kv4_layout {
   int32_t num_kv_heads;
@@ -172,9 +173,10 @@ kvr_status kvr_device_status(uint32_t *flags, int reset);
  * a PAGED one with up to 8 q heads per KV head), by the short-chunk part of
  * swa_sink_prefill_varlen, by full_attn_prefill_chunk, by
  * full_attn_decode_kv4, by kv_ring_gather_pages or by kv_ring_snapshot /
- * kv_ring_restore, in this process, stall on purpose: once their loads are in flight (and, for the
- * prefill, with its tensor memory held), one warp group (for the copies: the
- * first CTA) waits on an internal barrier that nothing completes, with a
+ * kv_ring_restore, in this process, stall on purpose: once their loads are in
+ * flight (and, for the prefill, with its tensor memory held), one warp group
+ * (for the copies: the first CTA; for full_attn_decode_kv4: one warp of each
+ * CTA) waits on an internal barrier that nothing completes, with a
  * time limit of limit_ns nanoseconds.  When the limit passes the kernel takes
  * the exit a real stall would take -- the other warps see the abort, the
  * loads and products already issued finish, tensor memory is freed, a copy

@@ -729,7 +729,7 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
 
 def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=None):
     """Positions lo[i] .. lo[i] + cu_rows[i+1] - cu_rows[i] - 1 of sequence
-src_seqs[i] of a 4-bit pool as bf16: into the same positions of sequence
+    src_seqs[i] of a 4-bit pool as bf16: into the same positions of sequence
     dst_seqs[i] of a PagedLayout, or into rows cu_rows[i] .. of a LinearLayout.
     T bounds the rows of the call (cu_rows' last entry; the launch is sized by
     it); by default it is all that dst holds."""
@@ -758,9 +758,9 @@ src_seqs[i] of a 4-bit pool as bf16: into the same positions of sequence
 
 
 def debug_stall_next(launches: int, limit_ns: int) -> None:
-    """Test hook: the next `launches` windowed decodes (ring layout) or
-    single-chunk full-attention prefills stall on purpose and leave by their
-    bounded-wait exit after limit_ns, setting DEV_TIMEOUT (kvr_debug_stall_next)."""
+    """Test hook: the next `launches` windowed decodes (ring layout), 4-bit
+    decodes or single-chunk full-attention prefills stall on purpose and leave
+    by their bounded-wait exit after limit_ns, setting DEV_TIMEOUT (kvr_debug_stall_next)."""
     _check(lib().kvr_debug_stall_next(int(launches), int(limit_ns)))
 
 

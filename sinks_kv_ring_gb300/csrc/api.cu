@@ -208,6 +208,8 @@ kvr_status check_kv4(const kvr_kv4_layout *L, const char *name) {
     return fail(KVR_EINVAL, "%s: num_seqs/max_blocks/num_blocks must be >= 1", name);
   if (L->block_size < 16 || L->block_size > 1024 || L->block_size % 16)
     return fail(KVR_EUNSUPPORTED, "%s: block_size %d (needs a multiple of 16 in [16, 1024])", name, L->block_size);
+  if ((int64_t)L->max_blocks * L->block_size > (1LL << 35))  // (32 bits count the kernels' tiles)
+    return fail(KVR_EUNSUPPORTED, "%s: max_blocks*block_size %lld > 2^35", name, (long long)L->max_blocks * L->block_size);
   return KVR_OK;
 }
 

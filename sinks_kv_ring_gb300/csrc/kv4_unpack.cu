@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
   const long long end = a + (c1 - c0);
   if (p0 >= end) return;
 
-  // (positions in tiles, which 32 bits hold: a table of 2^36 positions would be 4 GB of entries at the least)
+  // (in tiles, which 32 bits hold: a sequence has at most 2^35 positions, an entry 2^31)
   const unsigned tile0 = (unsigned)(p0 >> 4), stb = (unsigned)src.block_size >> 4, sbi = tile0 / stb;
   int sblk = 0;
   if (ok) {

@@ -120,6 +120,8 @@ def test_kv4_host_validation_codes(L):
     assert app(P, P, P, P, None, 8, 4, P, 1000, 0.7, R(_pool(block_table=None)), None) == -1
     assert app(P, P, P, P, None, 8, 4, P, 1000, 0.7, R(_pool(block_size=40)), None) == -4
     assert app(P, P, P, P, None, 8, 4, P, 1000, 0.7, R(_pool(block_size=2048)), None) == -4
+    far = _pool(max_blocks=(1 << 25) + 1, block_size=1024)                            # past 2^35 positions a sequence
+    assert app(P, P, P, P, None, 8, 4, P, 1000, 0.7, R(far), None) == -4
     assert app(P, P, P, P, None, 8, 4, P, 0, 0.7, R(pool), None) == -2
     assert app(None, None, None, None, None, 0, 4, P, 1000, 0.7, R(pool), None) == 0
 
