@@ -934,3 +934,37 @@ def test_decode_on_another_stream(table):
     st.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs) and len(junk) == 20
+
+
+def test_pools_past_4_gb(table):
+    """Blocks whose bytes lie past 32 bits, in the 4-bit pool and in the bf16 pages they are unpacked to, give what a
+    pool of three blocks gives."""
+    gen = _gen(95)
+    n, bs, G, nb = 2100, 1024, 16, 24000                                    # 4.5 GB of tiles
+    k, v = _kv(gen, n, 1)
+    q = torch.randn(2, G, 192, generator=gen, device=DEV).bfloat16()
+    pos, seq = _ints([n - 1, 1500], torch.int64), _ints([0, 0], torch.int32)
+    got = []
+    for blocks, ids in ((3, [2, 0, 1]), (nb, [nb - 1, 0, nb - 2])):
+        pool = kvr.Kv4Layout(torch.empty(blocks, 1, bs // 16, kvr.KV4_TILE, dtype=torch.uint8, device=DEV),
+                             _ints([ids], torch.int32))
+        _append(pool, k, v, 0, 0, table)
+        out = kvr.full_attn_decode_kv4(q, pos, seq, pool, table, SCALE, 3 * bs)
+        at = pool.block_table[0].long()
+        slots = (at[torch.arange(n, device=DEV) // bs] * bs + torch.arange(n, device=DEV) % bs)
+        tiles = pool.data[at].clone()
+        tiles[2, :, 3:] = 0                                                 # (positions behind the last token)
+        pool.data[at] = 0
+        kvr.kv4_append_rope(k, v, torch.arange(n, device=DEV), None, table, VS, pool, slots=slots)
+        pages = kvr.PagedLayout(torch.empty(blocks // 2 + 2, 1, bs, 192, dtype=torch.bfloat16, device=DEV),
+                                torch.empty(blocks // 2 + 2, 1, bs, 128, dtype=torch.bfloat16, device=DEV),
+                                _ints([[blocks // 2 + 1, 0, 1]], torch.int32))
+        kvr.kv4_unpack(pool, seq[:1], _ints([0], torch.int64), _ints([0, n], torch.int32), pages, seq[:1], T=n)
+        again = pool.data[at].clone()
+        r = pages.block_table[0].long()
+        got.append((out, tiles[:2], again, pages.k[r].reshape(-1, 192)[:n].clone(), pages.v[r].reshape(-1, 128)[:n].clone()))
+        assert torch.equal(tiles[:2], again[:2])
+        del pool, pages
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert kvr.device_status() == 0
