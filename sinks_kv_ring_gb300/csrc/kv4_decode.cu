@@ -83,8 +83,10 @@ constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the b
 // warp), so all CTAs end together whatever the contexts are, and a row is cut
 // only where a CTA's share ends.  The part of row r in CTA c is piece c + r:
 // no two pieces share a number, and a row's are consecutive.
-constexpr int K4_ROW = 16;           // a row's set-up and merge, in units (48 ragged rows: 8 -> 58 us, 16 -> 53, 32 -> 57)
-constexpr int K4_MIN = K4_WARPS;     // least share (twice that costs 0.9 us at 513 keys)
+// A row's set-up and merge, in units (48 ragged rows, 8 heads a group: 8 -> 49
+// us, 12 -> 43, 16 -> 41, 24 -> 42; 16 heads: 59, 53, 53, 55).
+constexpr int K4_ROW = 16;
+constexpr int K4_MIN = K4_WARPS;     // least share: a unit a warp (8 and 12 units measured the same)
 constexpr int K4_PLAN = 32;          // int64 words of the plan ahead of the rows' prefix: L
 constexpr int K4_INLINE_MAX = 256;   // batches the split kernel plans itself
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
