@@ -44,15 +44,17 @@
 // 0.98 of the copy rate).  At 16 heads the products alone take 153 us (86 of
 // them per unit at 8.2 cycles an SM quarter) and every other instruction of a
 // quarter about 0.75 cycles on top, as masks, loads and softmax share its
-// register ports with them: 285 us (5.30 TB/s, 0.78).  Measured and left out: two CTAs of 255
-// registers (322 us), 16-key units with four CTAs (335), scores of one unit
-// interleaved with the sums of the one before (323), queries held in registers
-// (327).  A single row at 32769 keys, 4 x 16 heads, takes 13.3 us: about 2 of
-// launch, 2.5 until the first tile is there, 5 of products, 1 of joining the
-// CTA's warps and 3 of merging 114 pieces a row.  The plan made before the wait
-// for the kernel ahead and in the merge kernel while the split kernel ends took
-// 1.4 us off that and 1 to 2 off ragged batches; requesting the first tiles
-// into L2 before the wait changed nothing.
+// register ports with them: 285 us (5.30 TB/s, 0.78).  Measured and left out:
+// two CTAs of 255 registers (322 us), 16-key units with four CTAs (335), scores
+// of one unit interleaved with the sums of the one before (323), queries held
+// in registers (327).
+//
+// A single row at 32769 keys, 4 x 16 heads, takes 13.3 us: about 2 of launch,
+// 2.5 until the first tile is there, 5 of products, 1 of joining the CTA's
+// warps and 3 of merging 114 pieces a row.  The plan made before the wait for
+// the kernel ahead and in the merge kernel while the split kernel ends took 1.4
+// us off that and 1 to 2 off ragged batches; requesting the first tiles into L2
+// before the wait changed nothing.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
