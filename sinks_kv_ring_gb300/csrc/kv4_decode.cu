@@ -79,15 +79,21 @@ constexpr int K4_FOLD = 16;          // units between foldings of the minima's s
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
 constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the bias as it is: below 2, times 2^14
 // The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW
-// units of set-up and then its keys in units of K4_UNIT; CTA c takes units
+// units of set-up and then its keys in units of K4_UNIT; share c is units
 // c L .. (c + 1) L - 1 of the line, L = total / CTAs (at least one unit per
-// warp), so all CTAs end together whatever the contexts are, and a row is cut
-// only where a CTA's share ends.  The part of row r in CTA c is piece c + r:
-// no two pieces share a number, and a row's are consecutive.
+// warp), and CTA c takes it, so all CTAs end together whatever the contexts
+// are, and a row is cut only where a share ends.  The part of row r in share c
+// is piece c + r: no two pieces share a number, and a row's are consecutive.
+// A share is at most K4_MOST units: a longer line is cut into a multiple of the
+// CTAs' number of shares, and CTA c takes c, c + CTAs, ...  The tensor cores cut
+// a sum off below its last bit at every product (2^-23 of it as measured: rows
+// of 2^24 keys, one a CTA, came out 3% too large), two a unit; at K4_MOST, 1024
+// units a warp, that is 2^-12 of the sum, a sixteenth of the output's half step.
 // A row's set-up and merge, in units (48 ragged rows, 8 heads a group: 8 -> 49
 // us, 12 -> 43, 16 -> 41, 24 -> 42; 16 heads: 59, 53, 53, 55).
 constexpr int K4_ROW = 16;
 constexpr int K4_MIN = K4_WARPS;     // least share: a unit a warp (8 and 12 units measured the same)
+constexpr int K4_MOST = 1024 * K4_WARPS;  // greatest share
 constexpr int K4_PLAN = 32;          // int64 words of the plan ahead of the rows' prefix: L
 constexpr int K4_INLINE_MAX = 256;   // batches the split kernel plans itself
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
@@ -97,7 +103,8 @@ constexpr int K4_OFF_ONES = K4_OFF_ROW + 64;  // four fp16 ones, four zeros
 constexpr int K4_OFF_BAR = K4_OFF_ONES + 16;
 constexpr int K4_OFF_STALL = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;  // a barrier that nothing completes (test hook)
 constexpr int K4_OFF_ABORT = K4_OFF_STALL + 8;
-constexpr int K4_OFF_PLAN = (K4_OFF_ABORT + 4 + 15) / 16 * 16;
+constexpr int K4_OFF_L = (K4_OFF_ABORT + 4 + 7) / 8 * 8;
+constexpr int K4_OFF_PLAN = (K4_OFF_L + 8 + 15) / 16 * 16;
 constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
@@ -234,6 +241,16 @@ __device__ __forceinline__ int kv4_units(long long p, int s, int num_seqs, int64
   return (int)((p + K4_UNIT) / K4_UNIT);
 }
 
+// Units of a share for a line of `total` units.
+__device__ __forceinline__ long long kv4_share(long long total, long long ctas) {
+  long long L = (total + ctas - 1) / ctas;
+  if (L > K4_MOST) {
+    const long long turns = (L + K4_MOST - 1) / K4_MOST;
+    L = (total + ctas * turns - 1) / (ctas * turns);
+  }
+  return L < K4_MIN ? K4_MIN : L;
+}
+
 // The line's prefix over the sequences (prefix[b]: units ahead of sequence b)
 // by NT threads, `get(b, p, s)` giving sequence b's position and id; returns L.
 template <int NT, typename Get>
@@ -271,8 +288,7 @@ __device__ __forceinline__ long long kv4_plan(Get get, int B, int hkv, int num_s
   }
   if (tid == 0) prefix[B] = base;
   __syncthreads();
-  const long long L = (base + ctas - 1) / ctas;
-  return L < K4_MIN ? K4_MIN : L;
+  return kv4_share(base, ctas);
 }
 
 // Sequence of unit x of the line: the last b with prefix[b] <= x whose part is not empty (x < prefix[B]).
@@ -340,12 +356,16 @@ __device__ __forceinline__ void kv4_part(const int64_t *prefix, int B, int hkv, 
 // The codes' operands are the same registers; a weight's row and column change
 // places between the two products by an 8 x 8 transposition (movmatrix).
 //
-// DIRECT: short contexts of few rows, where a launch costs more than the work.
-// A cluster of A.cs CTAs takes one row, each an equal share of its units, and
-// the CTAs merge their parts through each other's shared memory: one launch,
-// no plan and no workspace.
-template <bool SMALL, bool DIRECT>
+// FORM: the work line, a share a CTA (K4_LINE) or several (K4_TURNS: the loop
+// over them costs the line 0.5%, so batches that cannot need it go without);
+// or DIRECT: short contexts of few rows, where a launch costs more than the
+// work.  A cluster of A.cs CTAs takes one row, each an equal share of its units,
+// and the CTAs merge their parts through each other's shared memory: one
+// launch, no plan and no workspace.
+enum K4Form { K4_LINE, K4_TURNS, K4_DIRECT };
+template <bool SMALL, K4Form FORM>
 __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Args A) {
+  constexpr bool DIRECT = FORM == K4_DIRECT, TURNS = FORM == K4_TURNS;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = A.pool.hkv, G = A.G;
@@ -375,10 +395,13 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   auto plan = [&](auto get, unsigned *status) {
     return kv4_plan<K4_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status);
   };
+  long long *const sL = reinterpret_cast<long long *>(smem + K4_OFF_L);  // TURNS: L, for the shares after the first
+  int turn = 0;                                                          // and the shares done
   auto share = [&](long long L) {
     x = blockIdx.x * L;
     line_end = min(x + L, (long long)prefix[A.B]);
     ready = x < line_end;
+    if (TURNS && tid == 0) *sL = L;  // (a barrier follows each call)
     if (ready) kv4_part(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
   };
   if (early) {
@@ -398,10 +421,12 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     if (blockIdx.x == 0) kv4_units(p, s, A.pool.num_seqs, A.max_pos, A.max_ctx, A.status);
   }
   same = __syncthreads_and(same);
-  if (!DIRECT && !same)
+  if (!DIRECT && !same) {
     share(A.B <= K4_INLINE_MAX
               ? plan([&](int i, long long &p, int &s) { p = A.pos[i], s = A.seq[i]; }, blockIdx.x == 0 ? A.status : nullptr)
               : A.plan[0]);
+    if (TURNS) __syncthreads();  // *sL
+  }
 
   const int tpb = A.pool.block_size >> 4;
   const int t = lane & 3, gr = lane >> 2;
@@ -409,7 +434,16 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   uint32_t sent = 0;  // and issued
   bool gave_up = false;
 
-  while (ready || x < line_end) {
+  while (TURNS || ready || x < line_end) {
+    if (TURNS && !ready && x >= line_end) {  // the share is done: the next one lies gridDim.x shares on
+      const long long total = prefix[A.B];
+      if (line_end >= total) break;
+      const long long L = *sL;
+      x = line_end + (gridDim.x - 1) * L;
+      if (x >= total) break;
+      line_end = min(x + L, total);
+      ++turn;
+    }
     int w = 0, key_lo, key_hi;
     long long p;
     if (DIRECT) {
@@ -434,6 +468,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       ready = false;
       if (hi <= 0) continue;  // set-up alone: no piece
       w = (int)blockIdx.x + b * hkv + kv;
+      if (TURNS) w += turn * (int)gridDim.x;
       p = A.pos[b];
       key_lo = lo * K4_UNIT;
       key_hi = (int)min((long long)hi * K4_UNIT, p + 1);
@@ -1165,11 +1200,21 @@ __global__ void __launch_bounds__(K4M_WARPS * 32)
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t plan_bytes(int B) { return align256(((size_t)K4_PLAN + B + 1) * 8); }
 
-// Piece numbers: one per CTA that can have a share (of K4_MIN units at least) and one per row.
+// CTAs: as many as the GPU holds at once and as can have a share (of K4_MIN units at least).
+int line_ctas(int B, int hkv, long long max_ctx) {
+  const long long units = (long long)B * hkv * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW);
+  const long long R = (long long)K4_CTAS * num_sms(), most = (units + K4_MIN - 1) / K4_MIN;
+  return (int)(most < R ? most : R);
+}
+// Shares of a CTA on the longest line.
+long long line_turns(int B, int hkv, long long max_ctx) {
+  const long long units = (long long)B * hkv * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW);
+  const long long most = (long long)line_ctas(B, hkv, max_ctx) * K4_MOST;
+  return (units + most - 1) / most;
+}
+// Piece numbers: one per share of the longest line and one per row.
 size_t pieces_cap(int B, int hkv, long long max_ctx) {
-  const long long rows = (long long)B * hkv, R = (long long)K4_CTAS * num_sms();
-  const long long most = (rows * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW) + K4_MIN - 1) / K4_MIN;
-  return (size_t)(rows + (most < R ? most : R));
+  return (size_t)((long long)B * hkv + line_ctas(B, hkv, max_ctx) * line_turns(B, hkv, max_ctx));
 }
 
 // Short contexts go by clusters in one launch.  Measured at max_ctx 1024
@@ -1197,9 +1242,12 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   const long long rows = (long long)B * hkv, units = (max_ctx + K4_UNIT - 1) / K4_UNIT;
   if (rows > 0x7ffffffLL) return cudaErrorInvalidValue;  // (its queries alone would fill the GPU)
   const bool direct = one_launch(B, hkv, max_ctx);
-  void (*const kernel)(K4Args) = G <= 8 ? (direct ? kv4_decode_kernel<true, true> : kv4_decode_kernel<true, false>)
-                                        : (direct ? kv4_decode_kernel<false, true> : kv4_decode_kernel<false, false>);
-  cudaError_t e = ensure_smem_limit(17 + 2 * (G <= 8) + direct, (const void *)kernel, K4_SMEM, true);
+  static void (*const kernels[2][3])(K4Args) = {
+      {kv4_decode_kernel<false, K4_LINE>, kv4_decode_kernel<false, K4_TURNS>, kv4_decode_kernel<false, K4_DIRECT>},
+      {kv4_decode_kernel<true, K4_LINE>, kv4_decode_kernel<true, K4_TURNS>, kv4_decode_kernel<true, K4_DIRECT>}};
+  const int form = direct ? K4_DIRECT : line_turns(B, hkv, max_ctx) > 1 ? K4_TURNS : K4_LINE;
+  void (*const kernel)(K4Args) = kernels[G <= 8][form];
+  cudaError_t e = ensure_smem_limit(17 + 3 * (G <= 8) + form, (const void *)kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
   const size_t pieces = pieces_cap(B, hkv, max_ctx);
   K4Args A;
@@ -1230,8 +1278,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
     while (A.cs < 8 && A.cs * K4_WARPS < units && 2 * A.cs * rows <= R) A.cs *= 2;
     return launch_pdl_cluster(kernel, dim3((unsigned)(rows * A.cs)), dim3(K4_WARPS * 32), (size_t)K4_SMEM, A.cs, st, A);
   }
-  // (a CTA whose share would lie past the line has nothing to do)
-  const int ctas = (int)(pieces - (size_t)B * hkv);
+  const int ctas = line_ctas(B, hkv, max_ctx);  // (a CTA whose share would lie past the line has nothing to do)
   if (B > K4_INLINE_MAX) {
     e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(K4P_THREADS), 0, st, pos, seq, B, hkv, pool.num_seqs, max_pos,
                    max_ctx, ctas, A.plan, status);
