@@ -23,11 +23,13 @@
 //   * The minima enter as one more k = 8 product, of the stored fp16 minima
 //     with sum(q_g) in two fp16 parts (22 bits), which starts the score.
 //   * Weights p 2^bias are fp16, with bias + 4 = 14 as long as the value scales
-//     stay below 2 and less by the scales' exponent beyond: weight times scale
-//     (one packed fp16 multiply) stays in range, and a weight 2^-34 of the
-//     largest is still above fp16's least number, so a long flat tail keeps its
-//     mass.  Both roundings are 2^-11 of a weight, eight times finer than the
-//     bf16 weights of the other decode.
+//     stay below 2 and less by the scales' exponent beyond; a group's scales that
+//     are all below 2^-9 are brought up by a power of two.  So weight times scale
+//     (one packed fp16 multiply) stays in range at both ends: it is above fp16's
+//     least number for weights down to 2^-26 of the largest, and the 2^15 keys
+//     that a warp has at most are 2^-11 together below that.  A long flat tail
+//     keeps its mass.  Both roundings are 2^-11 of a weight, eight times finer
+//     than the bf16 weights of the other decode.
 //   * sum p m and sum p come out of one more product, with the two groups'
 //     minima and ones as its other operand.
 // The running maximum is a reference that moves (with a rescale of the sums)
@@ -74,10 +76,9 @@ constexpr int K4_UNIT = 16 * K4_TILES;
 constexpr int K4_NT = 2 * K4_TILES;  // its 8-key column tiles
 constexpr int K4_STAGES = 2;
 constexpr int K4_STAGE = K4_TILES * KV4_TILE;
-constexpr float K4_PBIAS = 10.f;     // weights are p 2^10
+constexpr float K4_PBIAS = 10.f;     // weights are p 2^10 as long as the value scales are below 2 (times 2^14: fp16's end)
 constexpr int K4_FOLD = 16;          // units between foldings of the minima's sum (1 us at batch 64; 4 units: 4 us)
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
-constexpr float K4_VLIM = 1.9990234375f;  // value scales up to here leave the bias as it is: below 2, times 2^14
 // The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW
 // units of set-up and then its keys in units of K4_UNIT; share c is units
 // c L .. (c + 1) L - 1 of the line, L = total / CTAs (at least one unit per
@@ -348,6 +349,54 @@ __device__ __forceinline__ void kv4_part(const int64_t *prefix, int B, int hkv, 
   hi = stop - K4_ROW;
 }
 
+// The size of the value scales, seen from both ends of fp16.  A weight times a
+// scale has to stay in range: above, the weights' exponent bias gives way (the
+// scales of both groups together); below, the scales of a group whose largest so
+// far is under 2^-9 are multiplied by a power of two that brings it to [1, 2),
+// and the group's sums count in that (a weight of 2^-17 beside a scale of 2^-18
+// was below fp16's least number, and a batch's 8,000 such keys a warp, 5% of a
+// row, were lost).  Both only ever move one way, as larger scales turn up.  Costs
+// 0.1% at batch 64 and 16 heads, 0.4% at 8, 0.9% on 48 ragged rows.
+constexpr uint32_t K4_PLAIN = 15;  // e of a group whose scales are used as they are
+constexpr uint32_t K4_TINY = 6;    // fp16's exponent field of 2^-9
+struct K4Scales {
+  uint32_t e;     // of group 0 (low half) and 1: scales are multiplied by 2^(15 - e); 0 before the first keys
+  __half2 limit;  // the largest scale that this lane's share of the check may meet
+};
+__device__ __forceinline__ bool kv4_plain(const K4Scales &k) { return k.e == (K4_PLAIN << 16 | K4_PLAIN); }
+__device__ __forceinline__ uint32_t kv4_e(const K4Scales &k, int g) { return g ? k.e >> 16 : k.e & 0xffffu; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// Takes in a unit's scales (`big`: this lane's two, zeros where they do not
+// count; lanes 0..7 and 16..23 hold group 0's; NaN ones aside): lowers `bias`,
+// updates `k`, and leaves in r[g] what group g's sums are multiplied by.
+__device__ __forceinline__ void kv4_take_scales(__half2 big, int lane, float &bias, K4Scales &k, float (&r)[KV4_VG]) {
+  const uint32_t lo = h2_as_u32(big) & 0xffffu, hi = h2_as_u32(big) >> 16;
+  const uint32_t x = max(lo > 0x7c00u ? 0u : lo, hi > 0x7c00u ? 0u : hi);
+  // exponent field of a group's largest: it is below 2^(hb - 14)
+  const uint32_t hb[KV4_VG] = {__reduce_max_sync(FULLW, (lane & 8) ? 0u : x) >> 10,
+                               __reduce_max_sync(FULLW, (lane & 8) ? x : 0u) >> 10};
+  // the least power of two above the largest scale, times 2^(bias + slack), fits fp16
+  bias = fminf(bias, 15.f - K4_SLACK - (float)((int)max(hb[0], hb[1]) - 14));
+  uint32_t e[KV4_VG];
+#pragma unroll
+  for (int g = 0; g < KV4_VG; ++g) {
+    e[g] = max(kv4_e(k, g), hb[g] < K4_TINY ? hb[g] : K4_PLAIN);
+    r[g] = pow2((int)kv4_e(k, g) - (int)e[g]);
+  }
+  k.e = e[1] << 16 | e[0];
+  const uint32_t mine = (lane & 8) ? e[1] : e[0];
+  k.limit = u32_as_h2((((mine < K4_PLAIN ? mine : 25u - (uint32_t)(int)bias) << 10) + 0x3ffu) * 0x10001u);
+}
+// A unit's scales times their groups' powers of two (exact: the largest is below 2).
+__device__ __forceinline__ void kv4_raise(uint32_t (&sv)[KV4_VG][K4_NT], const K4Scales &k) {
+#pragma unroll
+  for (int g = 0; g < KV4_VG; ++g) {
+    const __half2 b = u32_as_h2(((30u - kv4_e(k, g)) << 10) * 0x10001u);
+#pragma unroll
+    for (int nt = 0; nt < K4_NT; ++nt) sv[g][nt] = h2_as_u32(__hmul2(u32_as_h2(sv[g][nt]), b));
+  }
+}
+
 // SMALL: groups of up to 8 query heads.  The keys are then the 16 rows of the
 // products and the heads their 8 columns (scores K Q^T, sums V^T P^T): half
 // the products, and half the registers for the sums (four CTAs an SM, at 128
@@ -537,6 +586,12 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       gave_up = true;
       run_n = 0;
     }
+    // of a masked unit from key0 on: which of this lane's two value scales of the check count
+    auto kept_of = [&](int i, int key0) {
+      const int k = key0 + 16 * (lane >> 4) + 2 * ((lane & 7) >> 1) + 8 * (lane & 1);
+      const bool in = ((lane >> 4 ? ok.z : ok.y) >> (i & 31)) & 1;
+      return (in && k < key_hi ? 0xffffu : 0u) | (in && k + 1 < key_hi ? 0xffff0000u : 0u);
+    };
     // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators
     // in true units (times 2 to the bias, as the sums)
     float *mml = reinterpret_cast<float *>(smem + K4_OFF_STAGE);  // [4][16][2]
@@ -553,9 +608,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       // per row, the exponent that a weight is counted from (its maximum so far
       // less the bias); -inf, and 0 in its place, before the first keys
       float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;
-      float limit = NEG_INF;                   // how large a score less r may get before the reference moves
-      float bias = K4_PBIAS;                   // lowered by the value scales' size, so that weight times scale stays in fp16
-      __half2 lim2 = __float2half2_rn(K4_VLIM);  // the largest value scale that the bias leaves room for
+      float limit = NEG_INF;                   // how large a score less r may get before the reference moves (bias + slack)
+      K4Scales vs = {0u, __float2half2_rn(0.f)};
 
       // The sums of codes (all positive) and of minima grow together and cancel
       // in the end, while the tensor cores cut every sum off below its last bit:
@@ -567,10 +621,9 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
         const float g00 = __shfl_sync(FULLW, E[0], src), g01 = __shfl_sync(FULLW, E[1], src);
         const float g10 = __shfl_sync(FULLW, E[2], src), g11 = __shfl_sync(FULLW, E[3], src);
         if (t == 0) E[0] = E[1] = E[2] = E[3] = 0.f;
-        constexpr float un = 0x1p-24f, un16 = 0x1p-20f;  // even and odd dims' units
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const float k = (n & 1) ? un16 : un, m0 = n < 8 ? g00 : g01, m1 = n < 8 ? g10 : g11;
+          const float k = pow2(((n & 1) ? -5 : -9) - (int)kv4_e(vs, n >> 3)), m0 = n < 8 ? g00 : g01, m1 = n < 8 ? g10 : g11;
           O[n][0] = fmaf(m0, k, O[n][0]);
           O[n][1] = fmaf(m0, k, O[n][1]);
           O[n][2] = fmaf(m1, k, O[n][2]);
@@ -647,8 +700,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           vm[2 * h] = x.x;
           vm[2 * h + 1] = x.y;
         }
-        // each lane looks at two of the unit's 64 value scales (of the ones it
-        // keeps where some are masked: those may be anything)
+        // each lane looks at two of the unit's 64 value scales (masked ones,
+        // which may be anything, left out)
         __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
         if (!whole) {
           // keys past the range or of a bad block: what lies there (any bits) must not be met
@@ -664,9 +717,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
             sv[0][nt] &= keep;
             sv[1][nt] &= keep;
             vm[nt] &= keep;
-            big = nt ? __hmax2(big, u32_as_h2(sv[0][nt])) : u32_as_h2(sv[0][0]);
-            big = __hmax2(big, u32_as_h2(sv[1][nt]));
           }
+          big = u32_as_h2(h2_as_u32(big) & kept_of(i, key0));
         }
         // scores less the reference, base 2; does one pass it, or a value scale its bound?
         float X[K4_NT][4];
@@ -678,7 +730,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           top0 = fmax3(top0, X[nt][0], X[nt][1]);
           top1 = fmax3(top1, X[nt][2], X[nt][3]);
         }
-        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
+        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, vs.limit) != 0u || limit == NEG_INF;
+        const bool rare = move || !kv4_plain(vs);
         // weights, taken before the vote on them is in
         uint32_t P[K4_NT][2];  // [8 keys][row gr, row gr + 8]
 #pragma unroll
@@ -686,62 +739,50 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
           P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
         }
-        if (__any_sync(FULLW, move)) {
-          // new reference per row: the larger of the old one and this unit's maximum
-          float t0 = top0 + r0, t1 = top1 + r1;
+        if (__any_sync(FULLW, rare)) {
+          if (__any_sync(FULLW, move)) {
+            // new reference per row: the larger of the old one and this unit's maximum
+            float t0 = top0 + r0, t1 = top1 + r1;
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
-            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
-          }
-          // the largest value scale lowers the bias (NaN scales aside): the
-          // least power of two above it, times 2^(bias + slack), fits fp16
-          uint32_t hb = 0;
-#pragma unroll
-          for (int nt = 0; nt < K4_NT; ++nt)
-#pragma unroll
-            for (int g = 0; g < KV4_VG; ++g) {
-              const uint32_t x = sv[g][nt];
-              const uint32_t lo = x & 0xffffu, hi = x >> 16;
-              hb = max(hb, lo > 0x7c00u ? 0u : lo);
-              hb = max(hb, hi > 0x7c00u ? 0u : hi);
+            for (int o = 1; o < 4; o <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
+              t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
             }
-          hb = __reduce_max_sync(FULLW, hb) >> 10;  // its exponent field: below 2^(hb - 14)
-          const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
-          if (room < bias) {
-            mb0 += bias - room;  // (-inf stays)
-            mb1 += bias - room;
-            bias = room;
-            lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
-          }
-          // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
-          const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
-          const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
-          const bool fresh = limit == NEG_INF;  // the first keys: nothing to scale yet
-          const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
-          mb0 = r0 = n0;
-          mb1 = r1 = n1;
-          limit = bias + K4_SLACK;
+            const bool fresh = limit == NEG_INF;  // the first keys: nothing to scale yet
+            const float was = fresh ? K4_PBIAS : limit - K4_SLACK;
+            float bias = was, rv[KV4_VG];
+            kv4_take_scales(big, lane, bias, vs, rv);
+            mb0 += was - bias;  // (-inf stays)
+            mb1 += was - bias;
+            // (a unit has a key in range: no maximum means that its scores are NaN, and the row will be)
+            const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
+            const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
+            const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
+            mb0 = r0 = n0;
+            mb1 = r1 = n1;
+            limit = bias + K4_SLACK;
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            O[n][0] *= c0;
-            O[n][1] *= c0;
-            O[n][2] *= c1;
-            O[n][3] *= c1;
-          }
-          E[0] *= c0;
-          E[1] *= c0;
-          E[2] *= c1;
-          E[3] *= c1;
+            for (int n = 0; n < 16; ++n) {
+              O[n][0] *= c0 * rv[n >> 3];
+              O[n][1] *= c0 * rv[n >> 3];
+              O[n][2] *= c1 * rv[n >> 3];
+              O[n][3] *= c1 * rv[n >> 3];
+            }
+            E[0] *= c0;
+            E[1] *= c0;
+            E[2] *= c1;
+            E[3] *= c1;
 #pragma unroll
-          for (int nt = 0; nt < K4_NT; ++nt) {
-            X[nt][0] = fmaf(S[nt][0], crow0, -n0);
-            X[nt][1] = fmaf(S[nt][1], crow0, -n0);
-            X[nt][2] = fmaf(S[nt][2], crow1, -n1);
-            X[nt][3] = fmaf(S[nt][3], crow1, -n1);
-            P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
-            P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
+            for (int nt = 0; nt < K4_NT; ++nt) {
+              X[nt][0] = fmaf(S[nt][0], crow0, -n0);
+              X[nt][1] = fmaf(S[nt][1], crow0, -n0);
+              X[nt][2] = fmaf(S[nt][2], crow1, -n1);
+              X[nt][3] = fmaf(S[nt][3], crow1, -n1);
+              P[nt][0] = h2_as_u32(__floats2half2_rn(ex2(X[nt][0]), ex2(X[nt][1])));
+              P[nt][1] = h2_as_u32(__floats2half2_rn(ex2(X[nt][2]), ex2(X[nt][3])));
+            }
           }
+          if (!kv4_plain(vs)) kv4_raise(sv, vs);
         }
         // sums
 #pragma unroll
@@ -785,7 +826,6 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           m[(gr + 8) * 2] = mb1;
           m[(gr + 8) * 2 + 1] = E[2];
         }
-        constexpr float un = 0x1p24f, un16 = 0x1p20f;  // even and odd dims' units
         float *o = mo + warp * 16 * MO_STRIDE;
 #pragma unroll
         for (int g = 0; g < KV4_VG; ++g)
@@ -795,6 +835,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
             for (int c = 0; c < 2; ++c) {
               const float(*On)[4] = &O[g * 8 + ww * 4];
               const float m0 = g ? g01 : g00, m1 = g ? g11 : g10;
+              const float un = pow2(9 + (int)kv4_e(vs, g)), un16 = pow2(5 + (int)kv4_e(vs, g));  // even and odd dims' units
               const int d = 64 * g + 8 * (2 * t + c) + 4 * ww;
               *reinterpret_cast<float4 *>(o + gr * MO_STRIDE + d) =
                   make_float4(fmaf(On[0][c], un, m0), fmaf(On[1][c], un16, m0), fmaf(On[2][c], un, m0), fmaf(On[3][c], un16, m0));
@@ -817,8 +858,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       for (int n = 0; n < 8; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
       E[0] = E[1] = E[2] = E[3] = 0.f;
       float mb0 = NEG_INF, mb1 = NEG_INF, r0 = 0.f, r1 = 0.f;  // of the two heads (see the other form)
-      float limit = NEG_INF, bias = K4_PBIAS;
-      __half2 lim2 = __float2half2_rn(K4_VLIM);
+      float limit = NEG_INF;
+      K4Scales vs = {0u, __float2half2_rn(0.f)};
       // which scales of a 4-position word are this lane's keys gr and gr + 8
       const uint32_t pick = (gr & 1) ? 0x7632u : 0x5410u;
 
@@ -828,7 +869,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
         if (gr < 2) E[0] = E[1] = 0.f;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          const float k = (n & 1) ? 0x1p-20f : 0x1p-24f, m0 = n < 4 ? m00 : m10, m1 = n < 4 ? m01 : m11;
+          const float k = pow2(((n & 1) ? -5 : -9) - (int)kv4_e(vs, n >> 2)), m0 = n < 4 ? m00 : m10, m1 = n < 4 ? m01 : m11;
           O[n][0] = fmaf(m0, k, O[n][0]);
           O[n][1] = fmaf(m1, k, O[n][1]);
           O[n][2] = fmaf(m0, k, O[n][2]);
@@ -894,8 +935,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           vm[2 * h] = x.x;
           vm[2 * h + 1] = x.y;
         }
-        // each lane looks at two of the unit's 64 value scales (of the ones it
-        // keeps where some are masked: those may be anything)
+        // each lane looks at two of the unit's 64 value scales (masked ones,
+        // which may be anything, left out)
         __half2 big = u32_as_h2(lds32(sT + (lane >> 4) * KV4_TILE + KV4_OFF_VS + (lane & 15) * 4));
         if (!whole) {  // (see the other form)
           const int key0 = key_lo + K4_UNIT * (warp + i * K4_WARPS);
@@ -908,9 +949,8 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
             sv[0][nt] &= keep;
             sv[1][nt] &= keep;
             vm[nt] &= keep;
-            big = nt ? __hmax2(big, u32_as_h2(sv[0][nt])) : u32_as_h2(sv[0][0]);
-            big = __hmax2(big, u32_as_h2(sv[1][nt]));
           }
+          big = u32_as_h2(h2_as_u32(big) & kept_of(i, key0));
         }
         float top0 = NEG_INF, top1 = NEG_INF;
         float X[K4_TILES][4];
@@ -921,55 +961,46 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
           top0 = fmax3(top0, X[h][0], X[h][2]);
           top1 = fmax3(top1, X[h][1], X[h][3]);
         }
-        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, lim2) != 0u || limit == NEG_INF;
-        if (__any_sync(FULLW, move)) {
-          float t0 = top0 + r0, t1 = top1 + r1;
+        const bool move = fmaxf(top0, top1) > limit || __hgt2_mask(big, vs.limit) != 0u || limit == NEG_INF;
+        const bool rare = move || !kv4_plain(vs);
+        if (__any_sync(FULLW, rare)) {
+          if (__any_sync(FULLW, move)) {
+            float t0 = top0 + r0, t1 = top1 + r1;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
-            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
-          }
-          uint32_t hb = 0;
-#pragma unroll
-          for (int nt = 0; nt < K4_NT; ++nt)
-#pragma unroll
-            for (int g = 0; g < KV4_VG; ++g) {
-              const uint32_t x = sv[g][nt];
-              const uint32_t lo = x & 0xffffu, hi = x >> 16;
-              hb = max(hb, lo > 0x7c00u ? 0u : lo);
-              hb = max(hb, hi > 0x7c00u ? 0u : hi);
+            for (int o = 4; o < 32; o <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
+              t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
             }
-          hb = __reduce_max_sync(FULLW, hb) >> 10;
-          const float room = fminf(K4_PBIAS, 15.f - K4_SLACK - (float)((int)hb - 14));
-          if (room < bias) {
-            mb0 += bias - room;
-            mb1 += bias - room;
-            bias = room;
-            lim2 = u32_as_h2(((hb << 10) + 0x3ffu) * 0x10001u);
-          }
-          const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
-          const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
-          const bool fresh = limit == NEG_INF;
-          const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
-          mb0 = r0 = n0;
-          mb1 = r1 = n1;
-          limit = bias + K4_SLACK;
+            const bool fresh = limit == NEG_INF;
+            const float was = fresh ? K4_PBIAS : limit - K4_SLACK;
+            float bias = was, rv[KV4_VG];
+            kv4_take_scales(big, lane, bias, vs, rv);
+            mb0 += was - bias;
+            mb1 += was - bias;
+            const float n0 = fmaxf(mb0, (t0 == NEG_INF ? 0.f : t0) - bias);
+            const float n1 = fmaxf(mb1, (t1 == NEG_INF ? 0.f : t1) - bias);
+            const float c0 = fresh ? 0.f : ex2(r0 - n0), c1 = fresh ? 0.f : ex2(r1 - n1);
+            mb0 = r0 = n0;
+            mb1 = r1 = n1;
+            limit = bias + K4_SLACK;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            O[n][0] *= c0;
-            O[n][1] *= c1;
-            O[n][2] *= c0;
-            O[n][3] *= c1;
-          }
-          E[0] *= c0;
-          E[1] *= c1;
+            for (int n = 0; n < 8; ++n) {
+              O[n][0] *= c0 * rv[n >> 2];
+              O[n][1] *= c1 * rv[n >> 2];
+              O[n][2] *= c0 * rv[n >> 2];
+              O[n][3] *= c1 * rv[n >> 2];
+            }
+            E[0] *= c0;
+            E[1] *= c1;
 #pragma unroll
-          for (int h = 0; h < K4_TILES; ++h) {
-            X[h][0] = fmaf(S[h][0], crow0, -n0);
-            X[h][1] = fmaf(S[h][1], crow1, -n1);
-            X[h][2] = fmaf(S[h][2], crow0, -n0);
-            X[h][3] = fmaf(S[h][3], crow1, -n1);
+            for (int h = 0; h < K4_TILES; ++h) {
+              X[h][0] = fmaf(S[h][0], crow0, -n0);
+              X[h][1] = fmaf(S[h][1], crow1, -n1);
+              X[h][2] = fmaf(S[h][2], crow0, -n0);
+              X[h][3] = fmaf(S[h][3], crow1, -n1);
+            }
           }
+          if (!kv4_plain(vs)) kv4_raise(sv, vs);
         }
         // weights: row head gr, columns keys 2t, 2t + 1 (nt even: of the tile's first eight, odd: of the others)
         uint32_t P[K4_NT];
@@ -1012,10 +1043,11 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float m = c ? (g ? m11 : m01) : (g ? m10 : m00);
+              const float un = pow2(9 + (int)kv4_e(vs, g)), un16 = pow2(5 + (int)kv4_e(vs, g));
               const int e = 2 * ww + c;
               *reinterpret_cast<float4 *>(o + c * MO_STRIDE + 64 * g + 4 * ww) =
-                  make_float4(fmaf(O[4 * g][e], 0x1p24f, m), fmaf(O[4 * g + 1][e], 0x1p20f, m),
-                              fmaf(O[4 * g + 2][e], 0x1p24f, m), fmaf(O[4 * g + 3][e], 0x1p20f, m));
+                  make_float4(fmaf(O[4 * g][e], un, m), fmaf(O[4 * g + 1][e], un16, m), fmaf(O[4 * g + 2][e], un, m),
+                              fmaf(O[4 * g + 3][e], un16, m));
             }
       }
     }

@@ -1,4 +1,5 @@
-"""Values of the 4-bit decode over very long contexts: sums over long pieces, and lines of several shares a CTA.
+"""Values of the 4-bit decode over very long contexts: sums over long pieces, lines of several shares a
+CTA, and values so small that their scales are fp16 subnormals.
 
 The oracle is fp64 on the GPU over the values that the codes stand for, from the format's byte offsets alone."""
 import math
@@ -83,6 +84,23 @@ def _rotated(q, cs):
     return torch.cat([q[:, :32] * c - q[:, 32:64] * s, q[:, 32:64] * c + q[:, :32] * s, q[:, 64:]], 1)
 
 
+def _check(got, q, p, cs, K, V, what="", rel_bar=True):
+    """One row's heads of one KV head against fp64, by the bound of the decode's own tests: half a bf16 step of the
+    output; 2^-10 sum |q||k| of a score (the rotated q rounded to fp16), which moves a weight by twice that; two
+    roundings of a weight and one of their sum, 2^-10 of sum p |v| with code part and minimum counted apart (at most
+    3 |v|_max of the group of 64 dims)."""
+    x = _rotated(q, cs)
+    w = torch.softmax(x @ K.T * SCALE, -1)
+    want, wv = w @ V, w @ V.abs()
+    a = (x.abs() @ K.abs().T).amax(1, keepdim=True) * SCALE
+    vmax = V.abs().unflatten(1, (2, 64)).amax((0, 2)).repeat_interleave(64)
+    err = (got.double() - want).abs()
+    tol = 2.0 ** -8 * want.abs() + 2 * 2.0 ** -10 * a * wv + 2.0 ** -10 * (wv + 3 * vmax)
+    assert torch.all(err <= tol), f"{what}: {float((err - tol).max()):.3e} over, {float((err / tol).max()):.2f} of the bound"
+    rel = float((err.norm(dim=-1) / want.norm(dim=-1)).max())
+    assert not rel_bar or rel <= 1e-2, f"{what}: rel RMS {rel:.3e}"
+
+
 # -- sums and weights at the ends of their range -------------------------------------------------------------------------
 
 @pytest.mark.parametrize("G", [2, 9])
@@ -148,3 +166,32 @@ def test_long_ragged_rows_in_turns(table, tiles, B, long, G):
         tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * (w @ V.abs()) + 3 * 2.0 ** -10 * (w * w @ (V * V)).sqrt()
         err = (out[b].double() - want).abs()
         assert torch.all(err <= tol), f"row {b} ({p + 1} keys): {float((err / tol).max()):.2f} of the bound"
+
+
+@pytest.mark.parametrize("G", [8, 16])
+@pytest.mark.parametrize("small,large", [(1e-5, 1e-5), (2e-6, 2e-6), (1e-5, 1.0), (1e-5, 3e3)])
+def test_light_keys_of_small_values_count(table, tiles, G, small, large):
+    """A few keys that weigh 2^17 times as much as each of the many others, all of whose values are small (in one group
+    of dims or both): the others' part, a few percent of the output, has to be there.  A weight of 2^-17 times a value
+    scale of 2^-18 is below fp16."""
+    gen = _gen(601 + G)
+    B, n = 456, 32768
+    u = torch.zeros(192, device=DEV)
+    u[64:] = _randn(gen, 128)
+    u /= u.norm()
+    lead = math.sqrt(17.3 * math.log(2) / SCALE)
+    k = _randn(gen, n, 1, 192) * 0.02
+    k[:, 0, :64] = 0
+    k[torch.arange(4, device=DEV) * 32, 0] = lead * u                            # one in each warp's first unit
+    v = _randn(gen, n, 1, 128)
+    v[..., :64] *= small
+    v[..., 64:] *= large
+    pool = kvr.Kv4Layout.contiguous(1, 1, n)
+    _append(pool, k.bfloat16(), v.bfloat16(), 0, table, vscale=1.0)
+    q = (u * lead).expand(B, G, 192).bfloat16().contiguous()
+    pos = torch.full((B,), n - 1, dtype=torch.int64, device=DEV)
+    out = kvr.full_attn_decode_kv4(q, pos, torch.zeros(B, dtype=torch.int32, device=DEV), pool, table, SCALE, n)
+    K, V, _, _ = tiles.keys(pool, 0, 0, n)
+    for b in (0, 311, 455):
+        _check(out[b], q[b], n - 1, table[n - 1], K, V, f"row {b}")
+    assert kvr.device_status() == 0
