@@ -206,9 +206,20 @@ def _want_len(t, name, n):
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
 
 
-def _out(out, rows, hq, like):
+def _empty(shape, dtype, like, stream):
+    """Memory of a call's own, from the stream that the call runs on: a block that the current stream handed back may
+    still be in use there.  The current stream, which is where the caller goes on, may use it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _out(out, rows, hq, like, stream):
     if out is None:
-        return torch.empty(rows, hq, DV, dtype=torch.bfloat16, device=like.device)
+        return _empty((rows, hq, DV), torch.bfloat16, like, stream)
     _want(out, "out", torch.bfloat16, 3)
     if out.shape != (rows, hq, DV):
         raise ValueError(f"out must be [{rows}, {hq}, {DV}], got shape {tuple(out.shape)}")
@@ -410,7 +421,7 @@ def swa_sink_decode(q, pos, seq, ring, sinks, table, softmax_scale, out=None, st
     _want_len(pos, "pos", B)
     _want_len(seq, "seq", B)
     _want_len(sinks, "sinks", Hq)
-    out = _out(out, B, Hq, q)
+    out = _out(out, B, Hq, q, stream)
     _same_device(q, pos, seq, sinks, table, out, *ring.tensors())
     c = ring.c()
     _check(lib().swa_sink_decode(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(sinks),
@@ -432,9 +443,9 @@ def full_attn_decode(q, pos, seq, pool, table, softmax_scale, max_ctx, workspace
     _want_len(seq, "seq", B)
     if workspace is None:
         n = full_attn_decode_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(n, 1), torch.uint8, q, stream)
     _want(workspace, "workspace", torch.uint8, 1)
-    out = _out(out, B, Hq, q)
+    out = _out(out, B, Hq, q, stream)
     _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_decode(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),
@@ -459,7 +470,7 @@ def full_attn_decode_noalloc(q, pos, seq, pool, table, softmax_scale, max_ctx, o
     B, Hq, _ = q.shape
     _want_len(pos, "pos", B)
     _want_len(seq, "seq", B)
-    out = _out(out, B, Hq, q)
+    out = _out(out, B, Hq, q, stream)
     _same_device(q, pos, seq, table, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_decode_noalloc(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),
@@ -474,7 +485,7 @@ def swa_sink_prefill_chunk(q, P0, seq, chunk_kv, ring, sinks, table, softmax_sca
     _want_table(table)
     C, Hq, _ = q.shape
     _want_len(sinks, "sinks", Hq)
-    out = _out(out, C, Hq, q)
+    out = _out(out, C, Hq, q, stream)
     _same_device(q, sinks, table, out, *chunk_kv.tensors(), *ring.tensors())
     cc, rc = chunk_kv.c(), ring.c()
     _check(lib().swa_sink_prefill_chunk(_ptr(q), int(P0), C, int(seq), Hq, ctypes.byref(cc), ctypes.byref(rc),
@@ -487,7 +498,7 @@ def full_attn_prefill_chunk(q, P0, seq, pool, table, softmax_scale, out=None, st
     _want_q(q)
     _want_table(table)
     C, Hq, _ = q.shape
-    out = _out(out, C, Hq, q)
+    out = _out(out, C, Hq, q, stream)
     _same_device(q, table, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_prefill_chunk(_ptr(q), int(P0), C, int(seq), Hq, ctypes.byref(c), _ptr(table),
@@ -524,9 +535,9 @@ def full_attn_prefill_varlen(q, cu_rows, P0, seq, pool, table, softmax_scale, ma
     T, Hq, _ = q.shape
     if workspace is None:
         nb = full_attn_prefill_varlen_workspace_size(n, T, Hq, pool.num_kv_heads, max_ctx)
-        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nb, 1), torch.uint8, q, stream)
     _want(workspace, "workspace", torch.uint8, 1)
-    out = _out(out, T, Hq, q)
+    out = _out(out, T, Hq, q, stream)
     _same_device(q, cu_rows, P0, seq, table, workspace, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_prefill_varlen(_ptr(q), _ptr(cu_rows), _ptr(P0), _ptr(seq), n, T, Hq, ctypes.byref(c),
@@ -546,9 +557,9 @@ def swa_sink_prefill_varlen(q, cu_rows, P0, seq, chunk_kv, ring, sinks, table, s
     _want_len(sinks, "sinks", Hq)
     if workspace is None:
         nb = swa_sink_prefill_varlen_workspace_size(n)
-        workspace = torch.empty(max(nb, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nb, 1), torch.uint8, q, stream)
     _want(workspace, "workspace", torch.uint8, 1)
-    out = _out(out, T, Hq, q)
+    out = _out(out, T, Hq, q, stream)
     _same_device(q, cu_rows, P0, seq, sinks, table, workspace, out, *chunk_kv.tensors(), *ring.tensors())
     cc, rc = chunk_kv.c(), ring.c()
     _check(lib().swa_sink_prefill_varlen(_ptr(q), _ptr(cu_rows), _ptr(P0), _ptr(seq), n, T, Hq, ctypes.byref(cc),
@@ -713,12 +724,10 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
     if workspace is None:
         n = full_attn_decode_kv4_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
         if n:  # (short contexts need none)
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)  # (the allocator may hand it on while that stream still works)
+            workspace = _empty(n, torch.uint8, q, stream)
     else:
         _want(workspace, "workspace", torch.uint8, 1)
-    out = _out(out, B, Hq, q)
+    out = _out(out, B, Hq, q, stream)
     _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
     c = pool.c()
     _check(lib().full_attn_decode_kv4(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),

@@ -162,3 +162,54 @@ def test_pool_calls_check_devices_and_reach_the_library(rec):
         with pytest.raises(ValueError):
             case()
         assert rec.calls == [], i
+
+
+def test_memory_of_a_call_comes_from_its_stream(rec, monkeypatch):
+    """Workspace and output that a call allocates for itself are taken while the stream that it was given is the current
+    one (a block freed on the caller's stream may still be in use there), and the caller's stream is recorded on them."""
+    stack, made, recorded = ["caller's"], [], []
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            stack.append(self.stream)
+
+        def __exit__(self, *a):
+            stack.pop()
+
+    empty = torch.empty
+
+    def spy(*a, **kw):
+        t = empty(*a, **kw)
+        made.append(stack[-1])
+        return t
+
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stack[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append(s))
+    monkeypatch.setattr(torch, "empty", spy)
+    ring, pool, stage = _layouts()
+    pool4 = kvr.Kv4Layout.contiguous(4, HKV, 256, block_size=64, device="cpu")
+    q, pos, seq = _decode_args()
+    table, sinks, qc = _f32(300, 32, 2), _f32(HQ), _bf(8, HQ, 192)
+    cu, P0, sq = torch.tensor([0, 5, 8], dtype=torch.int32), _i64(2), _i32(2)
+    calls = [
+        (2, lambda st: kvr.full_attn_decode_kv4(q, pos, seq, pool4, table, 0.1, 256, stream=st)),
+        (2, lambda st: kvr.full_attn_decode(q, pos, seq, pool, table, 0.1, 256, stream=st)),
+        (1, lambda st: kvr.full_attn_decode_noalloc(q, pos, seq, pool, table, 0.1, 256, stream=st)),
+        (1, lambda st: kvr.swa_sink_decode(q, pos, seq, ring, sinks, table, 0.1, stream=st)),
+        (1, lambda st: kvr.swa_sink_prefill_chunk(qc, 100, 1, stage, ring, sinks, table, 0.1, stream=st)),
+        (1, lambda st: kvr.full_attn_prefill_chunk(qc, 100, 1, pool, table, 0.1, stream=st)),
+        (2, lambda st: kvr.full_attn_prefill_varlen(qc, cu, P0, sq, pool, table, 0.1, 256, stream=st)),
+        (2, lambda st: kvr.swa_sink_prefill_varlen(qc, cu, P0, sq, stage, ring, sinks, table, 0.1, stream=st)),
+    ]
+    for i, (n, call) in enumerate(calls):
+        for given in (None, "another"):
+            made.clear()
+            recorded.clear()
+            call(given)
+            assert made == [given or "caller's"] * n, i
+            assert recorded == (["caller's"] * n if given else []), i
+        assert stack == ["caller's"]

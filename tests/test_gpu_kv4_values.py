@@ -1,4 +1,4 @@
-"""Values of the 4-bit decode over very long contexts: sums over long pieces, lines of several shares a
+"""The 4-bit decode over very long contexts and on two streams at once: sums over long pieces, lines of several shares a
 CTA, and values so small that their scales are fp16 subnormals.
 
 The oracle is fp64 on the GPU over the values that the codes stand for, from the format's byte offsets alone."""
@@ -194,4 +194,27 @@ def test_light_keys_of_small_values_count(table, tiles, G, small, large):
     K, V, _, _ = tiles.keys(pool, 0, 0, n)
     for b in (0, 311, 455):
         _check(out[b], q[b], n - 1, table[n - 1], K, V, f"row {b}")
+    assert kvr.device_status() == 0
+
+
+# -- two streams ---------------------------------------------------------------------------------------------------------
+
+def test_calls_on_two_streams_at_once(table):
+    """Calls that allocate for themselves, in turn on the current stream and on another, with nothing between them: each
+    gives what it gives alone."""
+    gen = _gen(907)
+    n, hkv = 30000, 4
+    pool = kvr.Kv4Layout.contiguous(2, hkv, n)
+    for s in range(2):
+        _append(pool, _randn(gen, n, hkv, 192).bfloat16(), _randn(gen, n, hkv, 128).bfloat16(), s, table)
+    qs = [_randn(gen, 8, 16 * hkv, 192).bfloat16() for _ in range(2)]
+    pos = [_ints([n - 1 - 900 * i for i in range(8)], torch.int64), _ints([n - 1 - 2100 * i for i in range(8)], torch.int64)]
+    seq = _ints([0, 1] * 4, torch.int32)
+    call = lambda i, st: kvr.full_attn_decode_kv4(qs[i], pos[i], seq, pool, table, SCALE, n, stream=st)
+    want = [call(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    outs = [(i, call(i, other if i else None)) for _ in range(30) for i in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in outs)
     assert kvr.device_status() == 0
