@@ -740,8 +740,8 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
     """Positions lo[i] .. lo[i] + cu_rows[i+1] - cu_rows[i] - 1 of sequence
     src_seqs[i] of a 4-bit pool as bf16: into the same positions of sequence
     dst_seqs[i] of a PagedLayout, or into rows cu_rows[i] .. of a LinearLayout.
-    T bounds the rows of the call (cu_rows' last entry; the launch is sized by
-    it); by default it is all that dst holds."""
+    T bounds the rows of the call (cu_rows' last entry); by default it is all
+    that dst, or its block table, can name."""
     _want(src_seqs, "src_seqs", torch.int32, 1)
     _want(lo, "lo", torch.int64, 1)
     _want(cu_rows, "cu_rows", torch.int32, 1)

@@ -7,7 +7,10 @@
 // positions from lo[i] on.  A work unit is one tile of 16 positions of one KV
 // head, taken by one warp; entry i owns units cu_rows[i] / 16 + 2i onwards
 // (an entry of n rows touches at most n / 16 + 2 tiles), so a unit finds its
-// entry by a search over cu_rows and no plan is made first.
+// entry by a search over cu_rows and no plan is made first.  A call of more than
+// K4U_ONCE CTAs goes round with fewer of them instead, and a warp stops behind
+// the last entry's rows: a T far above the rows there are (all that a block
+// table spans) costs neither CTAs nor searches.
 //
 // What bounds it: HBM, 180 bytes in and 640 out per (position, KV head), as
 // long as every store fills its sectors: 122,880 positions of 4 KV heads take
@@ -20,6 +23,11 @@ namespace kvr {
 namespace {
 
 constexpr int K4U_WARPS = 8;
+// Going round takes 16 registers more a thread (600,002 positions of 4 KV heads:
+// 293 us at once, 300 in rounds).  1000 rows of 4 KV heads: 4.6 us with T = 1000,
+// 21 with T = 2^19 and 79 with 2^21 (empty CTAs), 9.5 beyond (in rounds).
+constexpr int K4U_ONCE = 1 << 16;
+constexpr int K4U_CTAS = 32;  // CTAs per SM of a call that goes round
 
 // The values of a word of codes (dim i in nibble i) as bf16.  A code masked
 // out of the word in place is the fp16 number u 2^-24 (or 16 u 2^-24), so the
@@ -48,39 +56,37 @@ __device__ __forceinline__ float kv4_half(uint32_t w, int hi) {
   return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w)));
 }
 
-__global__ void __launch_bounds__(K4U_WARPS * 32)
-    kv4_unpack_kernel(Kv4View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
-                      const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
-                      KvView dst, long long units, unsigned *status) {
-  pdl_wait();
-  pdl_trigger();
+// Unit `unit` of KV head h, by a warp.  False when it lies behind all rows of
+// the call, as every later one does: the entry found does not come earlier for
+// a later unit (even where cu_rows is out of order), and the last one's rows
+// have ended or are none.
+__device__ __forceinline__ bool unpack_unit(const Kv4View &src, const int32_t *__restrict__ src_seqs,
+                                            const int64_t *__restrict__ lo, const int32_t *__restrict__ cu_rows, int n,
+                                            long long T, const int32_t *__restrict__ dst_seqs, const KvView &dst,
+                                            long long unit, int h, unsigned *status) {
   const int lane = threadIdx.x & 31;
-  const unsigned w = blockIdx.x * K4U_WARPS + (threadIdx.x >> 5);
-  const unsigned unit32 = w / (unsigned)src.hkv;
-  const int h = (int)(w - unit32 * (unsigned)src.hkv);
-  const long long unit = unit32;
-  if (unit >= units) return;
   // the last entry whose first unit is not past this one
   int i = 0, hi = n;
   while (hi - i > 1) {
-    const int mid = (i + hi) >> 1;
+    const int mid = i + ((hi - i) >> 1);
     if ((long long)(cu_rows[mid] >> 4) + 2LL * mid <= unit) i = mid; else hi = mid;
   }
   const int c0 = cu_rows[i], c1 = cu_rows[i + 1];
   if (c0 < 0 || c1 < c0 || c1 > T) {
     if (lane == 0) flag(status, ST_BAD_ROWS);
-    return;
+    return i < n - 1;
   }
   long long a = lo[i];
   const int s = src_seqs[i];
   const bool mine = lane == 0 && h == 0;
   const long long u = unit - ((c0 >> 4) + 2LL * i);
-  if (u < 0 || c1 == c0) return;
+  if (u < 0) return true;
+  if (c1 == c0) return i < n - 1;
   // an entry that names no source has its rows written as zeros
   bool ok = true;
   if (a < 0 || a > (long long)src.max_blocks * src.block_size) {
     if (mine) flag(status, ST_BAD_POS);
-    if (dst.kind != 3) return;  // (no position: no page either)
+    if (dst.kind != 3) return i < n - 1;  // (no position: no page either)
     a = 0;
     ok = false;
   }
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
   }
   const long long p0 = ((a >> 4) + u) << 4;  // the first position of the unit's tile
   const long long end = a + (c1 - c0);
-  if (p0 >= end) return;
+  if (p0 >= end) return i < n - 1;
 
   // (in tiles, which 32 bits hold: a sequence has at most 2^35 positions, an entry 2^31)
   const unsigned tile0 = (unsigned)(p0 >> 4), stb = (unsigned)src.block_size >> 4, sbi = tile0 / stb;
@@ -110,13 +116,13 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
     const int ds = dst_seqs[i];
     if (ds < 0 || ds >= dst.num_seqs) {
       if (mine) flag(status, ST_BAD_SEQ);
-      return;
+      return true;
     }
     const unsigned dtb = (unsigned)dst.block_size >> 4, dbi = tile0 / dtb;  // a tile lies in one block
     const int dblk = dbi < (unsigned)dst.max_blocks ? dst.block_table[(long long)ds * dst.max_blocks + dbi] : -1;
     if (dblk < 0 || dblk >= dst.num_blocks) {
       if (mine) flag(status, ST_BAD_BLOCK);
-      return;
+      return true;
     }
     drow = ((long long)dblk * dst.hkv + h) * dst.block_size + 16 * (tile0 - dbi * dtb);
   }
@@ -176,6 +182,29 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
       *reinterpret_cast<uint4 *>(vd + 64 * g) = kv4_word(__byte_perm(w0, w1, e ? 0x7632 : 0x5410), sc * 0x1p24f, sc * 0x1p20f, mn);
     }
   }
+  return true;
+}
+
+template <bool ROUND>
+__global__ void __launch_bounds__(K4U_WARPS * 32)
+    kv4_unpack_kernel(Kv4View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
+                      const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
+                      KvView dst, long long units, unsigned *status) {
+  pdl_wait();
+  pdl_trigger();
+  const unsigned w = blockIdx.x * K4U_WARPS + (threadIdx.x >> 5), first = w / (unsigned)src.hkv;
+  int h = (int)(w - first * (unsigned)src.hkv);
+  for (long long unit = first; unit < units;) {
+    if (!unpack_unit(src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
+    // on by gridDim.x * K4U_WARPS (unit, head) pairs
+    const unsigned step = gridDim.x * K4U_WARPS, su = step / (unsigned)src.hkv;
+    unit += su;
+    h += (int)(step - su * (unsigned)src.hkv);
+    if (h >= src.hkv) {
+      h -= src.hkv;
+      ++unit;
+    }
+  }
 }
 
 }  // namespace
@@ -184,10 +213,12 @@ cudaError_t launch_kv4_unpack(const Kv4View &src, const int32_t *src_seqs, const
                               int n, long long T, const int32_t *dst_seqs, const KvView &dst, unsigned *status,
                               cudaStream_t st) {
   const long long units = (T >> 4) + 2LL * n;
-  const long long blocks = (units * src.hkv + K4U_WARPS - 1) / K4U_WARPS;
-  if (units * src.hkv > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(kv4_unpack_kernel, dim3((unsigned)blocks), dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows,
-                    n, T, dst_seqs, dst, units, status);
+  long long blocks = (units * src.hkv + K4U_WARPS - 1) / K4U_WARPS;  // (units < 2^33)
+  if (src.hkv > (1 << 24)) return cudaErrorInvalidValue;  // (a position alone would be 3 GB)
+  const bool round = blocks > K4U_ONCE;
+  if (round) blocks = (long long)K4U_CTAS * num_sms();
+  return launch_pdl(round ? kv4_unpack_kernel<true> : kv4_unpack_kernel<false>, dim3((unsigned)blocks),
+                    dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, units, status);
 }
 
 }  // namespace kvr
