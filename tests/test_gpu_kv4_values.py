@@ -1,5 +1,7 @@
-"""The 4-bit decode over very long contexts and on two streams at once: sums over long pieces, lines of several shares a
-CTA, and values so small that their scales are fp16 subnormals.
+"""Values of the 4-bit decode where bounds elsewhere are wide or no other test goes: scores that rise and fall by
+hundreds, queries so large that one key takes everything, long shares of small head groups, draft rows on long
+contexts, a million keys, sums over very long pieces, several shares a CTA, values so small that their scales are fp16
+subnormals, and calls on two streams at once.
 
 The oracle is fp64 on the GPU over the values that the codes stand for, from the format's byte offsets alone."""
 import math
@@ -99,6 +101,174 @@ def _check(got, q, p, cs, K, V, what="", rel_bar=True):
     assert torch.all(err <= tol), f"{what}: {float((err - tol).max()):.3e} over, {float((err / tol).max()):.2f} of the bound"
     rel = float((err.norm(dim=-1) / want.norm(dim=-1)).max())
     assert not rel_bar or rel <= 1e-2, f"{what}: rel RMS {rel:.3e}"
+
+
+# -- scores far apart ----------------------------------------------------------------------------------------------------
+
+def _as_held(q):
+    """The query as the kernel holds it, for queries whose rotary dims are zero: q * scale * log2(e) in fp32, times the
+    power of two that brings a head's largest magnitude to [2^14, 2^15), to fp16 (odd dims after a division by 16).
+    In units of log2, fp64."""
+    y = q.float() * float(np.float32(SCALE) * np.float32(1.4426950408889634))
+    up = torch.exp2(14 - torch.floor(torch.log2(y.abs().amax(-1, keepdim=True).double()))).float()
+    div = torch.where(torch.arange(192, device=DEV) % 2 == 1, 16.0, 1.0)
+    return (y * up / div).half().double() * div / up.double()
+
+
+def _check_held(out, q, K, V, km, ks):
+    """One row's heads of one KV head against attention with the query as the kernel holds it.  What is left of a score's
+    error is fp32: every product of a sum of at most 14 cuts off below 2^-23 of what it adds up (A: codes and minima
+    counted apart), and a group's query sum is held to max|y| 2^-15 beside its minimum.  Returns answer and bound."""
+    y = _as_held(q)
+    S = y @ K.T
+    w = torch.exp2(S - S.amax(1, keepdim=True))
+    w /= w.sum(1, keepdim=True)
+    want, wv = w @ V, w @ V.abs()
+    yg = y.abs().unflatten(1, (3, 64)).sum(-1)                                     # [G, 3]
+    A = (yg @ (15 * ks + km.abs()).T).amax(1, keepdim=True)
+    d = 14 * 2.0 ** -23 * A + 2.0 ** -15 * y.abs().amax(1, keepdim=True) * km.abs().sum(1).amax()
+    assert float(d.max()) < 0.02
+    tol = 2.0 ** -8 * want.abs() + (torch.exp2(2 * d) - 1) * (wv + want.abs()) + 2.0 ** -10 * (wv + 3 * V.abs().max())
+    err = (out.double() - want).abs()
+    assert torch.all(err <= tol), f"{float((err - tol).max()):.3e} over"
+    return want, tol
+
+
+@pytest.mark.parametrize("G", [8, 16])
+@pytest.mark.parametrize("n", [1500, 6000])
+@pytest.mark.parametrize("kind", ["rise", "fall", "first", "last", "saw"])
+def test_scores_rise_and_fall_with_their_values(table, tiles, kind, n, G):
+    """Scores that climb along the keys (every unit moves the reference), fall by hundreds, stand out at one end or go up
+    and down, over one row's pieces (6000 keys: the work line; 1500: a cluster)."""
+    gen = _gen(1000 + n + G)
+    t = torch.linspace(-1, 1, n, device=DEV)
+    ramp = {"rise": 300 * t, "fall": -300 * t, "first": 400.0 * (t == t[0]), "last": 400.0 * (t == t[-1]),
+            "saw": 100 * torch.sin(t * 40)}[kind]
+    u = torch.zeros(192, device=DEV)
+    u[64:] = _randn(gen, 128)
+    u /= u.norm()
+    k = (_randn(gen, n, 1, 192) * 0.05 + ramp[:, None, None] * u * 0.5).bfloat16()
+    v = _randn(gen, n, 1, 128).bfloat16()
+    pool = kvr.Kv4Layout.contiguous(1, 1, n)
+    _append(pool, k, v, 0, table)
+    q = (_randn(gen, 1, G, 192) * 0.1 + u * 14)
+    q[..., :64] = 0
+    q = q.bfloat16()
+    out = kvr.full_attn_decode_kv4(q, _ints([n - 1], torch.int64), _ints([0], torch.int32), pool, table, SCALE, n)
+    K, V, km, ks = tiles.keys(pool, 0, 0, n)
+    want, tol = _check_held(out[0], q[0], K, V, km, ks)
+    # the bound can fail: neither zeros nor the keys' mean nor the answer's negative pass it
+    for wrong in (torch.zeros_like(want), V.mean(0).expand_as(want), -want):
+        assert torch.any((wrong - want).abs() > 4 * tol)
+    assert kvr.device_status() == 0
+
+
+@pytest.mark.parametrize("G", [8, 16])
+def test_minima_far_from_zero_under_cancelling_queries(table, tiles, G):
+    """Keys around +40 in every dim under queries whose dims of a group add up to next to nothing: the minima's product
+    is a large number times a small one."""
+    gen = _gen(77 + G)
+    n = 5000
+    k = _randn(gen, n, 1, 192) + 40
+    pool = kvr.Kv4Layout.contiguous(1, 1, n)
+    _append(pool, k.bfloat16(), _randn(gen, n, 1, 128).bfloat16(), 0, table)
+    q = _randn(gen, 1, G, 192).bfloat16().float()
+    q[..., :64] = 0
+    for lo in (64, 128):  # bf16 values that cancel in pairs, but for one dim
+        q[..., lo + 33:lo + 64] = -q[..., lo + 1:lo + 32].flip(-1)
+    q = q.bfloat16()
+    out = kvr.full_attn_decode_kv4(q, _ints([n - 1], torch.int64), _ints([0], torch.int32), pool, table, SCALE, n)
+    _check_held(out[0], q[0], *tiles.keys(pool, 0, 0, n))
+    assert kvr.device_status() == 0
+
+
+@pytest.mark.parametrize("G", [4, 16])
+def test_one_key_takes_everything(table, tiles, G):
+    """Queries of magnitude 1e4: the best key's logit leads by hundreds (asserted), so its value is the answer, in every
+    KV head."""
+    gen = _gen(43 + G)
+    n, hkv = 200, 2
+    pool = kvr.Kv4Layout.contiguous(1, hkv, n)
+    _append(pool, _randn(gen, n, hkv, 192).bfloat16(), _randn(gen, n, hkv, 128).bfloat16(), 0, table)
+    q = (_randn(gen, 1, hkv * G, 192) * 1e4).bfloat16()
+    out = kvr.full_attn_decode_kv4(q, _ints([n - 1], torch.int64), _ints([0], torch.int32), pool, table, SCALE, n)
+    for h in range(hkv):
+        K, V, _, _ = tiles.keys(pool, 0, h, n)
+        x = _rotated(q[0, h * G:(h + 1) * G], table[n - 1])
+        top = (x @ K.T * SCALE).topk(2, -1)
+        # a score is known to 2^-10 sum |q||k|: the lead has to be out of its reach
+        lead = top.values[:, 0] - top.values[:, 1]
+        reach = 2 * 2.0 ** -10 * (x.abs() @ K.abs().T).amax(1) * SCALE
+        sure = lead > reach + 20
+        assert int(sure.sum()) >= G // 2
+        want = V[top.indices[:, 0]]
+        # one weight, rounded to fp16 in numerator (twice) and sum, and the output's half step; the value's code part
+        # and minimum counted apart
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -10 * 4 * V.abs().max()
+        err = (out[0, h * G:(h + 1) * G].double() - want).abs()
+        assert torch.all((err <= tol)[sure])
+    assert kvr.device_status() == 0
+
+
+# -- forms that long contexts reach --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("G", [2, 8])
+def test_long_shares_of_small_groups_keep_their_digits(table, tiles, G):
+    """Shares of 18,000 keys a CTA in the form for up to 8 heads: sums of codes and minima cancel to a hundredth of their
+    size.  The output's own rounding is 2^-8 / sqrt(3) in the mean square at most, everything else is held to 2^-11."""
+    gen = _gen(213)
+    B, ctx, hkv = 32, 65537, 4
+    pool = kvr.Kv4Layout.contiguous(B, hkv, ctx, zero=False)
+    for s in range(B):
+        k, v = _randn(gen, ctx, hkv, 192), _randn(gen, ctx, hkv, 128)
+        k[..., 64:] += 0.5 * _randn(gen, 1, hkv, 128)
+        _append(pool, k.bfloat16(), v.bfloat16(), s, table)
+    q = _randn(gen, B, hkv * G, 192).bfloat16()
+    pos = torch.full((B,), ctx - 1, dtype=torch.int64, device=DEV)
+    out = kvr.full_attn_decode_kv4(q, pos, torch.arange(B, dtype=torch.int32, device=DEV), pool, table, SCALE, ctx)
+    for b, h in ((0, 0), (13, 2), (31, 1)):
+        K, V, _, _ = tiles.keys(pool, b, h, ctx)
+        want = torch.softmax(_rotated(q[b, h * G:(h + 1) * G], table[ctx - 1]) @ K.T * SCALE, -1) @ V
+        err = (out[b, h * G:(h + 1) * G].double() - want).norm(dim=-1) / want.norm(dim=-1)
+        assert float(err.max()) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -11, float(err.max())
+
+
+@pytest.mark.parametrize("G", [5, 16])
+def test_draft_rows_on_long_contexts(table, tiles, G):
+    gen = _gen(31 + G)
+    lens, C, hkv = [70, 3000, 9001], 4, 2
+    pool = kvr.Kv4Layout.contiguous(3, hkv, max(lens), block_size=32)
+    for s, n in enumerate(lens):
+        _append(pool, _randn(gen, n, hkv, 192).bfloat16(), _randn(gen, n, hkv, 128).bfloat16(), s, table)
+    pos = [n - C + c for n in lens for c in range(C)]
+    seq = [s for s in range(len(lens)) for _ in range(C)]
+    q = _randn(gen, len(pos), hkv * G, 192).bfloat16()
+    assert kvr.full_attn_decode_kv4_workspace_size(len(pos), hkv * G, hkv, max(lens)) > 0  # (not the one-launch form)
+    out = kvr.full_attn_decode_kv4(q, _ints(pos, torch.int64), _ints(seq, torch.int32), pool, table, SCALE, max(lens))
+    for b, (p, s) in enumerate(zip(pos, seq)):
+        for h in range(hkv):
+            K, V, _, _ = tiles.keys(pool, s, h, p + 1)
+            _check(out[b, h * G:(h + 1) * G], q[b, h * G:(h + 1) * G], p, table[p], K, V, f"row {b} head {h}")
+    assert kvr.device_status() == 0
+
+
+@pytest.mark.parametrize("G", [8, 16])
+def test_a_million_keys(table, tiles, G):
+    gen = _gen(101 + G)
+    ctx, hkv, bs, step = 1000003, 1, 48, 1 << 18
+    mb = -(-ctx // bs)
+    ids = torch.randperm(mb, generator=gen, device=DEV).to(torch.int32)[None].contiguous()
+    pool = kvr.Kv4Layout(torch.empty(mb, hkv, bs // 16, kvr.KV4_TILE, dtype=torch.uint8, device=DEV), ids)
+    for lo in range(0, ctx, step):
+        m = min(step, ctx - lo)
+        _append(pool, _randn(gen, m, hkv, 192).bfloat16(), _randn(gen, m, hkv, 128).bfloat16(), 0, table, lo)
+    q = (_randn(gen, 3, hkv * G, 192) * 2).bfloat16()
+    pos = [ctx - 1, ctx // 3, 131073]
+    out = kvr.full_attn_decode_kv4(q, _ints(pos, torch.int64), _ints([0, 0, 0], torch.int32), pool, table, SCALE, ctx)
+    K, V, _, _ = tiles.keys(pool, 0, 0, ctx)
+    for b, p in enumerate(pos):
+        _check(out[b], q[b], p, table[p], K[:p + 1], V[:p + 1], f"row {b}")
+    assert kvr.device_status() == 0
 
 
 # -- sums and weights at the ends of their range -------------------------------------------------------------------------
