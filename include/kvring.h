@@ -22,8 +22,9 @@
  *    work.  Calls on one stream execute in order.  The decode-path kernels
  *    are launched with programmatic stream serialisation: one may be
  *    scheduled while the kernel before it on the stream is still running,
- *    but touches no global memory until that kernel has completed and its
- *    writes are visible, so stream order holds as for a plain launch.
+ *    but writes no global memory, and computes with nothing that the work
+ *    before its call writes, until that work has completed and its writes
+ *    are visible, so stream order holds as for a plain launch.
  *  - Arguments are validated on the host before anything is launched; a bad
  *    argument returns a negative kvr_status and launches nothing.  A launch
  *    failure returns KVR_ECUDA.  kvr_last_error() gives a message (thread
@@ -586,7 +587,8 @@ kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int
  * skipped too).  Positions that cannot be read (KVR_DEV_BAD_POS,
  * KVR_DEV_BAD_SEQ, KVR_DEV_BAD_BLOCK) are written as zeros, except that a
  * negative or too large lo writes no page; a destination that cannot be
- * addressed is flagged and not written.  n = 0 or T = 0 is a no-op.
+ * addressed is flagged and not written.  n = 0 or T = 0 is a no-op.  T may be
+ * far above cu_rows[n]: the rows there are decide what a call costs.
  */
 kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
                       int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);

@@ -35,13 +35,20 @@ constexpr unsigned ST_NO_BLOCKS = 64u;
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// Prefetch ahead of pdl_wait.  A kernel may read, before its pdl_wait, an
-// index that the kernel ahead of it could still be writing, and use it only
-// to choose bytes to bring into L2: such a read may see an old value, which
-// costs nothing but a useless prefetch, since every value the kernel computes
-// with is read again after pdl_wait.  The early read bypasses L1 (.cg), so no
-// stale line stays there for the later one.  The prefetch itself is
-// prefetch_l2 below.
+// Reads ahead of pdl_wait.  A kernel may read, before its pdl_wait, an index
+// that the kernel ahead of it could still be writing, in one of three ways:
+//   * to choose bytes to bring into L2 (prefetch_l2 below): an old value costs
+//     nothing but a useless prefetch, since every value the kernel computes with
+//     is read again after pdl_wait;
+//   * to prepare work that is checked after pdl_wait against the same values
+//     read again, and made again where they differ (kv4_decode_kernel's plan);
+//   * as a value that the kernel ahead does not write and that was there before
+//     that kernel let this one start: a kernel that triggers only after its own
+//     pdl_wait, as all here do, starts its dependent no earlier than its
+//     predecessors are complete (kv4_merge_kernel's positions and plan, behind
+//     kv4_decode_kernel).
+// The early read bypasses L1 (.cg), so no stale line stays there for the later
+// one.
 __device__ __forceinline__ int ld_early_s32(const int32_t *p) {
   int v;
   asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");

@@ -17,10 +17,11 @@
 // away and a 16-byte load brings a lane's values, all five in flight before
 // the destination is looked up.
 //
-// What bounds it: instructions, some 480 per four tokens of a head (unpacking,
-// extrema, the exact quotient), issued in 64% of the cycles: 52 us for 302,216
-// (token, KV head) pairs where their 820 bytes each take 37 us at the copy
-// rate.  The extrema of the five groups go through one butterfly that halves
+// What bounds it: a warp's own chain (loads, the RoPE row, some 480 instructions
+// per four tokens of a head, stores), with too few warps an SM to fill either
+// side: 52 us for 302,216 (token, KV head) pairs, 0.70 of what their 820 bytes
+// each take at the copy rate, 64% of the issue slots, and waits for loads the
+// largest of the stalls.  The extrema of the five groups go through one butterfly that halves
 // what a lane carries at each step, a group's scale is taken by one lane of its
 // token (2 divisions instead of 10 per lane) and the codes come in packed
 // pairs.  Loading the next head's values ahead of their use, into registers or

@@ -21,14 +21,17 @@
 //     of two to a largest magnitude in [2^14, 2^15) per head, and rounded once
 //     to fp16 (2^-11 of a value, where the bf16 decode rounds to 2^-8).
 //   * The minima enter as one more k = 8 product, of the stored fp16 minima
-//     with sum(q_g) in two fp16 parts (22 bits), which starts the score.
+//     with sum(q_g) in two fp16 parts, which starts the score.  The sum is stored
+//     times 2^-24, below 2^-3, so the low part ends at fp16's least step: off by
+//     2^-25 at most, max|q| 2^-15 of the sum, far less than the rounding of q to
+//     fp16 moves the same product.
 //   * Weights p 2^bias are fp16, with bias + 4 = 14 as long as the value scales
 //     stay below 2 and less by the scales' exponent beyond; a group's scales that
 //     are all below 2^-9 are brought up by a power of two.  So weight times scale
-//     (one packed fp16 multiply) stays in range at both ends: it is above fp16's
-//     least number for weights down to 2^-26 of the largest, and the 2^15 keys
-//     that a warp has at most are 2^-11 together below that.  A long flat tail
-//     keeps its mass.  Both roundings are 2^-11 of a weight, eight times finer
+//     (one packed fp16 multiply) stays in range at both ends: beside scales up to
+//     2^9, as a group's largest are, it is above fp16's least number for weights
+//     down to 2^-26 of the largest, and what the 2^15 keys that a warp has at
+//     most weigh below that is 2^-11 together.  A long flat tail keeps its mass.  Both roundings are 2^-11 of a weight, eight times finer
 //     than the bf16 weights of the other decode.
 //   * sum p m and sum p come out of one more product, with the two groups'
 //     minima and ones as its other operand.
@@ -42,18 +45,18 @@
 // registers.
 //
 // What bounds it.  180 bytes and 2 (192 + 128) G flops per key and KV head.
-// Up to 8 heads: HBM (batch 64 at 32769 keys, 4 x 8 heads: 227 us, 6.65 TB/s,
-// 0.98 of the copy rate).  At 16 heads the products alone take 153 us (86 of
+// Up to 8 heads: HBM (batch 64 at 32769 keys, 4 x 8 heads: 229 us, 6.60 TB/s,
+// 0.97 of the copy rate).  At 16 heads the products alone take 153 us (86 of
 // them per unit at 8.2 cycles an SM quarter) and every other instruction of a
 // quarter about 0.75 cycles on top, as masks, loads and softmax share its
-// register ports with them: 285 us (5.30 TB/s, 0.78).  Measured and left out:
+// register ports with them: 287 us (5.27 TB/s, 0.78).  Measured and left out:
 // two CTAs of 255 registers (322 us), 16-key units with four CTAs (335), scores
 // of one unit interleaved with the sums of the one before (323), queries held
 // in registers (327).
 //
-// A single row at 32769 keys, 4 x 16 heads, takes 13.3 us: about 2 of launch,
+// A single row at 32769 keys, 4 x 16 heads, takes 13.5 us: about 2 of launch,
 // 2.5 until the first tile is there, 5 of products, 1 of joining the CTA's
-// warps and 3 of merging 114 pieces a row.  The plan made before the wait for
+// warps and 3 of merging 104 pieces a row (shares of 10 units).  The plan made before the wait for
 // the kernel ahead and in the merge kernel while the split kernel ends took 1.4
 // us off that and 1 to 2 off ragged batches; requesting the first tiles into L2
 // before the wait changed nothing.
