@@ -209,11 +209,14 @@ def _want_len(t, name, n):
 def _empty(shape, dtype, like, stream):
     """Memory of a call's own, from the stream that the call runs on: a block that the current stream handed back may
     still be in use there.  The current stream, which is where the caller goes on, may use it as well."""
-    if stream is None:
+    cur = None if stream is None else torch.cuda.current_stream()
+    if stream == cur:
         return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(getattr(stream, "cuda_stream", None), int) and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=like.device)  # (a handle is all the calls ask for)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=like.device)
-    t.record_stream(torch.cuda.current_stream())
+    t.record_stream(cur)
     return t
 
 

@@ -213,3 +213,35 @@ def test_memory_of_a_call_comes_from_its_stream(rec, monkeypatch):
             assert made == [given or "caller's"] * n, i
             assert recorded == (["caller's"] * n if given else []), i
         assert stack == ["caller's"]
+
+
+def test_any_object_with_a_stream_handle_is_taken(rec, monkeypatch):
+    """The calls ask a stream for its cuda_stream alone; the one that is current is used as it is."""
+    class Handle:
+        cuda_stream = 1234
+
+    entered = []
+
+    class Use:
+        def __init__(self, stream):
+            entered.append(stream)
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            pass
+
+    handle = Handle()
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: ("external", h))
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    _, pool, _ = _layouts()
+    q, pos, seq = _decode_args()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: "caller's")
+    kvr.full_attn_decode(q, pos, seq, pool, _f32(300, 32, 2), 0.1, 256, stream=handle)
+    assert entered == [("external", 1234)] * 2
+    entered.clear()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: handle)
+    kvr.full_attn_decode(q, pos, seq, pool, _f32(300, 32, 2), 0.1, 256, stream=handle)
+    assert entered == []
