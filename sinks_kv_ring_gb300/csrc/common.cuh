@@ -45,8 +45,8 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 //   * as a value that the kernel ahead does not write and that was there before
 //     that kernel let this one start: a kernel that triggers only after its own
 //     pdl_wait, as all here do, starts its dependent no earlier than its
-//     predecessors are complete (kv4_merge_kernel's positions and plan, behind
-//     kv4_decode_kernel).
+//     predecessors are complete (line_merge_kernel's positions and plan, behind
+//     the split kernel).
 // The early read bypasses L1 (.cg), so no stale line stays there for the later
 // one.
 __device__ __forceinline__ int ld_early_s32(const int32_t *p) {

@@ -63,14 +63,12 @@
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
-#include "launch.h"
+#include "line.cuh"
 #include "tc_ptx.cuh"
-#include "warp_attn.cuh"
 
 namespace kvr {
 namespace {
 
-constexpr unsigned FULLW = 0xffffffffu;
 constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K4_WARPS = 4;
 constexpr int K4_CTAS = 3;           // per SM
@@ -82,24 +80,16 @@ constexpr int K4_STAGE = K4_TILES * KV4_TILE;
 constexpr float K4_PBIAS = 10.f;     // weights are p 2^10 as long as the value scales are below 2 (times 2^14: fp16's end)
 constexpr int K4_FOLD = 16;          // units between foldings of the minima's sum (1 us at batch 64; 4 units: 4 us)
 constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference maximum
-// The work line.  Every (sequence, KV head) row is laid end to end, K4_ROW
-// units of set-up and then its keys in units of K4_UNIT; share c is units
-// c L .. (c + 1) L - 1 of the line, L = total / CTAs (at least one unit per
-// warp), and CTA c takes it, so all CTAs end together whatever the contexts
-// are, and a row is cut only where a share ends.  The part of row r in share c
-// is piece c + r: no two pieces share a number, and a row's are consecutive.
-// A share is at most K4_MOST units: a longer line is cut into a multiple of the
-// CTAs' number of shares, and CTA c takes c, c + CTAs, ...  The tensor cores cut
-// a sum off below its last bit at every product (2^-23 of it as measured: rows
-// of 2^24 keys, one a CTA, came out 3% too large), two a unit; at K4_MOST, 1024
-// units a warp, that is 2^-12 of the sum, a sixteenth of the output's half step.
-// A row's set-up and merge, in units (48 ragged rows, 8 heads a group: 8 -> 49
-// us, 12 -> 43, 16 -> 41, 24 -> 42; 16 heads: 59, 53, 53, 55).
-constexpr int K4_ROW = 16;
-constexpr int K4_MIN = K4_WARPS;     // least share: a unit a warp (8 and 12 units measured the same)
-constexpr int K4_MOST = 1024 * K4_WARPS;  // greatest share
-constexpr int K4_PLAN = 32;          // int64 words of the plan ahead of the rows' prefix: L
-constexpr int K4_INLINE_MAX = 256;   // batches the split kernel plans itself
+// The work line (line.cuh) in units of K4_UNIT keys.  A row's set-up and merge,
+// in units (48 ragged rows, 8 heads a group: 8 -> 49 us, 12 -> 43, 16 -> 41, 24
+// -> 42; 16 heads: 59, 53, 53, 55); the least share is a unit a warp (8 and 12
+// units measured the same).  The greatest: the tensor cores cut a sum off below
+// its last bit at every product (2^-23 of it as measured: rows of 2^24 keys, one
+// a CTA, came out 3% too large), two a unit; at 1024 units a warp that is 2^-12
+// of the sum, a sixteenth of the output's half step.
+struct K4Line {
+  static constexpr int UNIT = K4_UNIT, ROW = 16, MIN = K4_WARPS, MOST = 1024 * K4_WARPS, CTAS = K4_CTAS;
+};
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
 constexpr int K4_OFF_QX = 12 * 512;
 constexpr int K4_OFF_ROW = K4_OFF_QX + 256;
@@ -109,7 +99,7 @@ constexpr int K4_OFF_STALL = K4_OFF_BAR + 8 * K4_WARPS * K4_STAGES;  // a barrie
 constexpr int K4_OFF_ABORT = K4_OFF_STALL + 8;
 constexpr int K4_OFF_L = (K4_OFF_ABORT + 4 + 7) / 8 * 8;
 constexpr int K4_OFF_PLAN = (K4_OFF_L + 8 + 15) / 16 * 16;
-constexpr int K4_PLAN_BYTES = (K4_INLINE_MAX + 2) * 8;
+constexpr int K4_PLAN_BYTES = (LINE_INLINE_MAX + 2) * 8;
 constexpr int K4_OFF_STAGE = (K4_OFF_PLAN + K4_PLAN_BYTES + 127) / 128 * 128;
 constexpr int K4_SMEM = K4_OFF_STAGE + K4_WARPS * K4_STAGES * K4_STAGE;
 static_assert(K4_WARPS * K4_STAGES * K4_STAGE >= (K4_WARPS * 16 * (MO_STRIDE + 2) + K4_WARPS * 16 + 32 + 16 * DV) * 4,
@@ -233,124 +223,16 @@ __device__ __forceinline__ void kv4_query(const K4Query &Q, int G, float scale_l
   }
 }
 
-// Units of keys of sequence b; 0 (flagged once) where its position or id is
-// out of range: such a row has no part of the line, and the merge writes zeros.
-__device__ __forceinline__ int kv4_units(long long p, int s, int num_seqs, int64_t max_pos, long long max_ctx,
-                                         unsigned *status) {
-  const bool bp = p < 0 || p >= max_pos || p + 1 > max_ctx, bs = s < 0 || s >= num_seqs;
-  if (bp || bs) {
-    if (status) flag(status, (bp ? ST_BAD_POS : 0u) | (bs ? ST_BAD_SEQ : 0u));
-    return 0;
-  }
-  return (int)((p + K4_UNIT) / K4_UNIT);
-}
-
-// Units of a share for a line of `total` units.
-__device__ __forceinline__ long long kv4_share(long long total, long long ctas) {
-  long long L = (total + ctas - 1) / ctas;
-  if (L > K4_MOST) {
-    const long long turns = (L + K4_MOST - 1) / K4_MOST;
-    L = (total + ctas * turns - 1) / (ctas * turns);
-  }
-  return L < K4_MIN ? K4_MIN : L;
-}
-
-// The line's prefix over the sequences (prefix[b]: units ahead of sequence b)
-// by NT threads, `get(b, p, s)` giving sequence b's position and id; returns L.
-template <int NT, typename Get>
-__device__ __forceinline__ long long kv4_plan(Get get, int B, int hkv, int num_seqs, int64_t max_pos, long long max_ctx,
-                                              int ctas, int64_t *prefix, unsigned *status) {
-  __shared__ long long s_sum[NT / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long base = 0;
-  for (int b0 = 0; b0 < B; b0 += NT) {
-    const int b = b0 + tid;
-    long long x = 0;
-    if (b < B) {
-      long long p;
-      int q;
-      get(b, p, q);
-      const int u = kv4_units(p, q, num_seqs, max_pos, max_ctx, status);
-      x = u ? (long long)hkv * (u + K4_ROW) : 0;
-    }
-    const long long mine = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(FULLW, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_sum[warp] = x;
-    __syncthreads();
-    long long before = base;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-      before += i < warp ? s_sum[i] : 0;
-      base += s_sum[i];
-    }
-    if (b < B) prefix[b] = before + x - mine;
-    __syncthreads();  // s_sum is rewritten by the next round
-  }
-  if (tid == 0) prefix[B] = base;
-  __syncthreads();
-  return kv4_share(base, ctas);
-}
-
-// Sequence of unit x of the line: the last b with prefix[b] <= x whose part is not empty (x < prefix[B]).
-__device__ __forceinline__ int kv4_find(const int64_t *prefix, int B, long long x) {
-  int lo = 0, hi = B;  // prefix[lo] <= x < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
-constexpr int K4P_THREADS = 256;
-
-// Batches past K4_INLINE_MAX rows: the plan by a kernel of its own.
-__global__ void __launch_bounds__(K4P_THREADS)
-    kv4_plan_kernel(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv, int num_seqs,
-                    int64_t max_pos, long long max_ctx, int ctas, int64_t *__restrict__ plan, unsigned *status) {
-  pdl_wait();
-  pdl_trigger();
-  const auto get = [&](int b, long long &p, int &s) { p = pos[b], s = seq[b]; };
-  const long long L = kv4_plan<K4P_THREADS>(get, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + K4_PLAN, status);
-  if (threadIdx.x == 0) plan[0] = L;
-}
-
-struct K4Args {
+struct K4Args : LineArgs {
   const uint16_t *q;
-  const int64_t *pos;
-  const int32_t *seq;
-  int B, hq, G;
   Kv4View pool;
   const float *table;
-  int64_t max_pos;
   float scale_log2;
-  long long max_ctx;
-  int64_t *plan;
-  float *part_ml;
-  float *part_o;
   unsigned *status;
   unsigned long long stall_ns;  // test hook: warp 0's first wait is on a barrier that nothing completes (0: no stall)
-  uint16_t *out;
   int cs;                      // DIRECT: CTAs of a row
   unsigned long long tpb_mul;  // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
 };
-
-// CTA's part of the line from unit x on: row (b, kv), units [lo, hi) of its
-// keys (none where hi <= lo: set-up alone); x moves behind it.
-__device__ __forceinline__ void kv4_part(const int64_t *prefix, int B, int hkv, long long line_end, long long &x, int &b,
-                                         int &kv, int &lo, int &hi) {
-  b = kv4_find(prefix, B, x);
-  const int rowlen = (int)((prefix[b + 1] - prefix[b]) / hkv);
-  kv = (int)((x - prefix[b]) / rowlen);
-  const int off = (int)(x - prefix[b] - (long long)kv * rowlen);
-  const int stop = (int)min((long long)rowlen, off + (line_end - x));
-  x += stop - off;
-  lo = max(off - K4_ROW, 0);
-  hi = stop - K4_ROW;
-}
 
 // The size of the value scales, seen from both ends of fp16.  A weight times a
 // scale has to stay in range: above, the weights' exponent bias gives way (the
@@ -440,12 +322,12 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   // first part, from positions and ids read early (ld_early_s32); after the
   // wait it stands if they read the same, else it is made again.
   const bool early = !DIRECT && A.B <= K4_WARPS * 32;
-  const int64_t *prefix = A.B <= K4_INLINE_MAX ? sPrefix : A.plan + K4_PLAN;
+  const int64_t *prefix = A.B <= LINE_INLINE_MAX ? sPrefix : A.plan + LINE_PLAN;
   long long x = 0, line_end = 0, early_p = 0;
   int b = 0, kv = 0, lo = 0, hi = 0, early_s = 0;
   bool ready = DIRECT;  // b, kv, lo, hi hold the next part
   auto plan = [&](auto get, unsigned *status) {
-    return kv4_plan<K4_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status);
+    return line_plan<K4Line, K4_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status);
   };
   long long *const sL = reinterpret_cast<long long *>(smem + K4_OFF_L);  // TURNS: L, for the shares after the first
   int turn = 0;                                                          // and the shares done
@@ -454,7 +336,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     line_end = min(x + L, (long long)prefix[A.B]);
     ready = x < line_end;
     if (TURNS && tid == 0) *sL = L;  // (a barrier follows each call)
-    if (ready) kv4_part(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
+    if (ready) line_part<K4Line>(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
   };
   if (early) {
     if (tid < A.B) {
@@ -470,11 +352,11 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
     const long long p = A.pos[tid];
     const int s = A.seq[tid];
     same = p == early_p && s == early_s;
-    if (blockIdx.x == 0) kv4_units(p, s, A.pool.num_seqs, A.max_pos, A.max_ctx, A.status);
+    if (blockIdx.x == 0) line_units<K4Line>(p, s, A.pool.num_seqs, A.max_pos, A.max_ctx, A.status);
   }
   same = __syncthreads_and(same);
   if (!DIRECT && !same) {
-    share(A.B <= K4_INLINE_MAX
+    share(A.B <= LINE_INLINE_MAX
               ? plan([&](int i, long long &p, int &s) { p = A.pos[i], s = A.seq[i]; }, blockIdx.x == 0 ? A.status : nullptr)
               : A.plan[0]);
     if (TURNS) __syncthreads();  // *sL
@@ -504,7 +386,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       b = row / hkv;
       kv = row - b * hkv;
       p = A.pos[b];
-      const int units = kv4_units(p, A.seq[b], A.pool.num_seqs, A.max_pos, A.max_ctx,
+      const int units = line_units<K4Line>(p, A.seq[b], A.pool.num_seqs, A.max_pos, A.max_ctx,
                                   kv == 0 && rank == 0 && tid == 0 ? A.status : nullptr);
       if (units == 0) {  // (so for the whole cluster)
         uint16_t *o = A.out + ((long long)b * A.hq + (long long)kv * G) * DV;
@@ -516,7 +398,7 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
       key_hi = (int)min((long long)min((rank + 1) * each, units) * K4_UNIT, p + 1);
       if (key_hi < key_lo) key_hi = key_lo;
     } else {
-      if (!ready) kv4_part(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
+      if (!ready) line_part<K4Line>(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
       ready = false;
       if (hi <= 0) continue;  // set-up alone: no piece
       w = (int)blockIdx.x + b * hkv + kv;
@@ -1123,135 +1005,6 @@ __global__ void __launch_bounds__(K4_WARPS * 32, K4_CTAS) kv4_decode_kernel(K4Ar
   for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K4_STAGES), (seen / K4_STAGES) & 1u, &never);
 }
 
-// Merge of a row's pieces by log-sum-exp, and normalisation: NW warps per
-// (sequence, KV head, q head) fold interleaved pieces, lane l the value dims
-// 4l..4l+3, K4M_K pieces' loads in flight at a time; the row's first warp
-// joins them.
-constexpr int K4M_WARPS = 16;
-constexpr int K4M_K = 8;
-
-__global__ void __launch_bounds__(K4M_WARPS * 32)
-    kv4_merge_kernel(K4Args A, int ctas, int nw) {
-  __shared__ float s_ml[K4M_WARPS][2];
-  __shared__ float4 s_acc[K4M_WARPS][32];
-  __shared__ int64_t s_prefix[K4_INLINE_MAX + 1];
-  const int G = A.G, hkv = A.pool.hkv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % nw;
-  const long long row = (long long)blockIdx.x * (K4M_WARPS / nw) + warp / nw;  // (b hkv + kv) G + g
-  const bool have = row < (long long)A.B * A.hq;
-  const int g = have ? (int)(row % G) : 0, pair = have ? (int)(row / G) : 0, b = pair / hkv, kv = pair - b * hkv;
-  // The plan, while the split kernel still runs: that kernel let this one start
-  // after its own wait, so the batch (and the plan kernel's plan) are there.
-  long long L, at, next;
-  if (A.B <= K4_INLINE_MAX) {
-    const auto get = [&](int i, long long &p, int &s) { p = ld_early_s64(A.pos + i), s = ld_early_s32(A.seq + i); };
-    L = kv4_plan<K4M_WARPS * 32>(get, A.B, hkv, A.pool.num_seqs, A.max_pos, A.max_ctx, ctas, s_prefix, nullptr);
-    at = s_prefix[b];
-    next = s_prefix[b + 1];
-  } else {
-    L = ld_early_s64(A.plan);
-    at = ld_early_s64(A.plan + K4_PLAN + b);
-    next = ld_early_s64(A.plan + K4_PLAN + b + 1);
-  }
-  const long long len = have ? (next - at) / hkv : 0;  // 0: nothing to attend to
-  long long c0 = 0;
-  int n = 0;
-  if (len > 0) {
-    c0 = (at + kv * len + K4_ROW) / L;
-    n = (int)((at + kv * len + len - 1) / L - c0) + 1;
-  }
-  pdl_wait();
-  pdl_trigger();
-  float M = NEG_INF, S = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = sub; i0 < n; i0 += K4M_K * nw) {
-    float2 ml[K4M_K];
-    float4 o[K4M_K];
-#pragma unroll
-    for (int k = 0; k < K4M_K; ++k) {
-      const int i = i0 + k * nw;
-      ml[k] = make_float2(NEG_INF, 0.f);
-      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n) {
-        const long long r = (c0 + i + pair) * G + g;
-        ml[k] = *reinterpret_cast<const float2 *>(A.part_ml + r * 2);
-        o[k] = *reinterpret_cast<const float4 *>(A.part_o + r * DV + 4 * lane);
-      }
-    }
-    float Mn = M;
-#pragma unroll
-    for (int k = 0; k < K4M_K; ++k) Mn = fmaxf(Mn, ml[k].x);
-    if (Mn == NEG_INF) continue;  // nothing yet (pieces without a block of the pool)
-    const float c = ex2(M - Mn);  // M = -inf gives 0
-    S *= c;
-    acc.x *= c;
-    acc.y *= c;
-    acc.z *= c;
-    acc.w *= c;
-#pragma unroll
-    for (int k = 0; k < K4M_K; ++k) {
-      const float f = ex2(ml[k].x - Mn);
-      S += ml[k].y * f;
-      acc.x += o[k].x * f;
-      acc.y += o[k].y * f;
-      acc.z += o[k].z * f;
-      acc.w += o[k].w * f;
-    }
-    M = Mn;
-  }
-  if (nw > 1) {
-    if (lane == 0) {
-      s_ml[warp][0] = M;
-      s_ml[warp][1] = S;
-    }
-    s_acc[warp][lane] = acc;
-    __syncthreads();
-    if (sub == 0) {
-      float Mt = NEG_INF;
-      for (int u = 0; u < nw; ++u) Mt = fmaxf(Mt, s_ml[warp + u][0]);
-      S = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (Mt != NEG_INF) {
-        for (int u = 0; u < nw; ++u) {
-          const float mu = s_ml[warp + u][0];
-          if (mu == NEG_INF) continue;
-          const float f = ex2(mu - Mt);
-          const float4 o = s_acc[warp + u][lane];
-          S += s_ml[warp + u][1] * f;
-          acc.x += o.x * f;
-          acc.y += o.y * f;
-          acc.z += o.z * f;
-          acc.w += o.w * f;
-        }
-      }
-    }
-  }
-  if (!have || sub != 0) return;
-  const float inv = S == 0.f ? 0.f : 1.f / S;  // (a NaN sum stays one)
-  *reinterpret_cast<uint2 *>(A.out + ((long long)b * A.hq + (long long)kv * G + g) * DV + 4 * lane) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-}
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-size_t plan_bytes(int B) { return align256(((size_t)K4_PLAN + B + 1) * 8); }
-
-// CTAs: as many as the GPU holds at once and as can have a share (of K4_MIN units at least).
-int line_ctas(int B, int hkv, long long max_ctx) {
-  const long long units = (long long)B * hkv * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW);
-  const long long R = (long long)K4_CTAS * num_sms(), most = (units + K4_MIN - 1) / K4_MIN;
-  return (int)(most < R ? most : R);
-}
-// Shares of a CTA on the longest line.
-long long line_turns(int B, int hkv, long long max_ctx) {
-  const long long units = (long long)B * hkv * ((max_ctx + K4_UNIT - 1) / K4_UNIT + K4_ROW);
-  const long long most = (long long)line_ctas(B, hkv, max_ctx) * K4_MOST;
-  return (units + most - 1) / most;
-}
-// Piece numbers: one per share of the longest line and one per row.
-size_t pieces_cap(int B, int hkv, long long max_ctx) {
-  return (size_t)((long long)B * hkv + line_ctas(B, hkv, max_ctx) * line_turns(B, hkv, max_ctx));
-}
-
 // Short contexts go by clusters in one launch.  Measured at max_ctx 1024
 // (one launch against the work line's two): 1 x 2 KV heads at 4 query heads
 // each 5.7 us against 7.1, 16 x 4 at 16 11.1 / 13.2, 64 x 4 23.0 / 24.3, 600
@@ -1266,8 +1019,7 @@ bool one_launch(int B, int hkv, long long max_ctx) {
 
 size_t kv4_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
   if (one_launch(B, hkv, max_ctx)) return 0;
-  const size_t G = (size_t)(hq / hkv), n = pieces_cap(B, hkv, max_ctx);
-  return plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
+  return line_workspace<K4Line>(B, hq, hkv, max_ctx);
 }
 
 cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
@@ -1280,32 +1032,20 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
   static void (*const kernels[2][3])(K4Args) = {
       {kv4_decode_kernel<false, K4_LINE>, kv4_decode_kernel<false, K4_TURNS>, kv4_decode_kernel<false, K4_DIRECT>},
       {kv4_decode_kernel<true, K4_LINE>, kv4_decode_kernel<true, K4_TURNS>, kv4_decode_kernel<true, K4_DIRECT>}};
-  const int form = direct ? K4_DIRECT : line_turns(B, hkv, max_ctx) > 1 ? K4_TURNS : K4_LINE;
+  const int form = direct ? K4_DIRECT : line_turns<K4Line>(B, hkv, max_ctx) > 1 ? K4_TURNS : K4_LINE;
   void (*const kernel)(K4Args) = kernels[G <= 8][form];
   cudaError_t e = ensure_smem_limit(17 + 3 * (G <= 8) + form, (const void *)kernel, K4_SMEM, true);
   if (e != cudaSuccess) return e;
-  const size_t pieces = pieces_cap(B, hkv, max_ctx);
   K4Args A;
+  line_args<K4Line>(A, pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, ws, out);
   A.q = q;
-  A.pos = pos;
-  A.seq = seq;
-  A.B = B;
-  A.hq = hq;
-  A.G = G;
   A.pool = pool;
   A.table = table;
-  A.max_pos = max_pos;
   A.scale_log2 = softmax_scale * LOG2E;
-  A.max_ctx = max_ctx;
-  A.plan = reinterpret_cast<int64_t *>(ws);
-  uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + plan_bytes(B);
-  A.part_ml = reinterpret_cast<float *>(w8);
-  A.part_o = reinterpret_cast<float *>(w8 + align256(pieces * G * 2 * sizeof(float)));
   A.status = status;
   A.stall_ns = take_stall();
   const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
   A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
-  A.out = out;
   A.cs = 1;
   if (direct) {
     // as many CTAs a row as the longest row gives every warp a unit, as a
@@ -1313,20 +1053,7 @@ cudaError_t launch_kv4_decode(const uint16_t *q, const int64_t *pos, const int32
     while (A.cs < 8 && A.cs * K4_WARPS < units && 2 * A.cs * rows <= R) A.cs *= 2;
     return launch_pdl_cluster(kernel, dim3((unsigned)(rows * A.cs)), dim3(K4_WARPS * 32), (size_t)K4_SMEM, A.cs, st, A);
   }
-  const int ctas = line_ctas(B, hkv, max_ctx);  // (a CTA whose share would lie past the line has nothing to do)
-  if (B > K4_INLINE_MAX) {
-    e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(K4P_THREADS), 0, st, pos, seq, B, hkv, pool.num_seqs, max_pos,
-                   max_ctx, ctas, A.plan, status);
-    if (e != cudaSuccess) return e;
-  }
-  e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(K4_WARPS * 32), (size_t)K4_SMEM, st, A);
-  if (e != cudaSuccess) return e;
-  // warps per merged row: about four pieces each
-  const int est = (int)(R / ((long long)B * hkv)) + 1;
-  int nw = 1;
-  while (nw < K4M_WARPS && nw * 4 < est) nw *= 2;
-  const long long blocks = ((long long)B * hq + K4M_WARPS / nw - 1) / (K4M_WARPS / nw);
-  return launch_pdl(kv4_merge_kernel, dim3((unsigned)blocks), dim3(K4M_WARPS * 32), 0, st, A, ctas, nw);
+  return line_launch<K4Line>(kernel, K4_WARPS * 32, (size_t)K4_SMEM, A, status, st);
 }
 
 }  // namespace kvr
