@@ -152,6 +152,38 @@ typedef struct kvr_kv4_layout {
 } kvr_kv4_layout;
 
 /*
+ * A full layer's pool in 8 bits: 321 bytes per (position, KV head) where the
+ * bf16 pages take 640 and the 4-bit pool 182.  K (RoPE applied) and V (value
+ * scale applied) are signed codes u in -127..127, stored as u + 128, with one
+ * scale for the K and one for the V of 16 consecutive positions of a KV head:
+ * value = s * u.
+ *   data [num_blocks][Hkv][block_size / 16][5136] bytes, 16-byte aligned: one
+ *   tile of 5136 bytes per 16 consecutive positions, position r of the tile
+ *   (r = position % 16) at
+ *     K codes   byte 1024 g + 64 r + i: dim 64 g + i (i < 64)
+ *     V codes   byte 3072 + 512 g + 64 a + 16 ((r / 2) % 4) + 4 i + 2 (r / 8)
+ *               + r % 2: dim 32 g + 4 a + i (i < 4)
+ *     scales    fp32 at byte 5120 (K) and 5124 (V), bf16 numbers
+ *     masks     16 bits at byte 5128 (K) and 5130 (V): bit r is set where the
+ *               position's row is not finite (it reads as NaN; its codes are 0)
+ *     zero      bytes 5132..5135;
+ *   block_table [num_seqs][max_blocks] int32: position p of sequence s lies in
+ *   block block_table[s][p / block_size], at p % block_size.
+ * block_size is a multiple of 16 in [16, 1024], max_blocks * block_size at
+ * most 2^35.  The data needs no initialisation: what no append wrote is never
+ * used.
+ */
+typedef struct kvr_kv8_layout {
+  int32_t num_kv_heads;
+  int32_t num_seqs;
+  int32_t max_blocks;
+  int32_t block_size;
+  int32_t num_blocks;
+  uint8_t *data;
+  const int32_t *block_table;
+} kvr_kv8_layout;
+
+/*
  * Every call that launches work looks up, on its first use on a device (and
  * again after cudaDeviceReset), the device address of the library's status
  * word; that first call must not run while its stream is being captured
@@ -173,11 +205,11 @@ kvr_status kvr_device_status(uint32_t *flags, int reset);
  * `launches` kernels started by swa_sink_decode (over a RING layout, or over
  * a PAGED one with up to 8 q heads per KV head), by the short-chunk part of
  * swa_sink_prefill_varlen, by full_attn_prefill_chunk, by
- * full_attn_decode_kv4, by kv_ring_gather_pages or by kv_ring_snapshot /
- * kv_ring_restore, in this process, stall on purpose: once their loads are in
- * flight (and, for the prefill, with its tensor memory held), one warp group
- * (for the copies: the first CTA; for full_attn_decode_kv4: one warp of each
- * CTA) waits on an internal barrier that nothing completes, with a
+ * full_attn_decode_kv4 or full_attn_decode_kv8, by kv_ring_gather_pages or by
+ * kv_ring_snapshot / kv_ring_restore, in this process, stall on purpose: once
+ * their loads are in flight (and, for the prefill, with its tensor memory
+ * held), one warp group (for the copies: the first CTA; for the decodes over
+ * quantised pools: one warp of each CTA) waits on an internal barrier that nothing completes, with a
  * time limit of limit_ns nanoseconds.  When the limit passes the kernel takes
  * the exit a real stall would take -- the other warps see the abort, the
  * loads and products already issued finish, tensor memory is freed, a copy
@@ -592,6 +624,159 @@ kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int
  */
 kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
                       int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);
+
+/*
+ * KV write of a batch of chunks into an 8-bit pool: RoPE on k's first 64 dims
+ * and the value scale on v in fp32 (each product and sum rounded), then codes.
+ * Chunk i (i < n) is rows cu_rows[i] .. cu_rows[i+1]-1 of k [T][Hkv][192] and
+ * v [T][Hkv][128], at positions P0[i] .. of sequence seqs[i] (as the varlen
+ * calls and kv_pages_grow name them; a decode step is chunks of one row).
+ * Per tile of 16 positions and KV head, for the K rows x of the chunk and, apart
+ * from them, its V rows:
+ *   s = the least bf16 number with 127 s >= |x| for all of them, but no less
+ *       than the tile's scale where the chunk starts behind the tile's first
+ *       position; u = rint(x / s), ties to even; s = 0 gives u = 0;
+ *   the tile's rows ahead of the chunk, under a scale that grew from s_old:
+ *       u = rint(u s_old / s).
+ * So positions are written in order: those ahead of P0[i] in its tile have been
+ * appended before, and those behind the chunk in its last tile mean nothing
+ * afterwards (a draft that was turned down is written over by going on from its
+ * first position; a scale that it raised stays).  A row (K or V of one token and
+ * head) holding a NaN or an infinity reads as NaN and counts for no scale.
+ * cu_rows [n+1] int32, P0 [n] int64, seqs [n] int32 are device arrays; cu_rows
+ * must be non-decreasing within [0, T] (an entry that is not is skipped with
+ * KVR_DEV_BAD_ROWS, and entries after it may be skipped too).  seqs[i] = -1
+ * marks padding: the chunk is skipped and nothing is flagged.  A chunk with a
+ * sequence id outside the layout (KVR_DEV_BAD_SEQ), or with P0 < 0 or rows past
+ * the RoPE table or the block table (KVR_DEV_BAD_POS), is skipped; a tile whose
+ * table entry is outside the pool (KVR_DEV_BAD_BLOCK) is.  No two chunks of one
+ * call may name the same sequence, nor sequences that share the block they
+ * write (kv_pages_fork gives each its own).  n = 0 or T = 0 is a no-op.
+ */
+kvr_status kv8_append_rope(const kvr_bf16 *k, const kvr_bf16 *v, const int32_t *cu_rows, const int64_t *P0,
+                           const int32_t *seqs, int32_t n, int64_t T, int32_t Hkv, const float *rope_cos_sin,
+                           int64_t max_pos, float value_scale, const kvr_kv8_layout *dst, void *stream);
+
+/*
+ * Workspace bytes for full_attn_decode_kv8: 0 on bad arguments, and where the
+ * call needs none (short contexts; workspace may then be NULL).
+ */
+size_t full_attn_decode_kv8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int64_t max_ctx);
+
+/*
+ * full_attn_decode over an 8-bit pool: the token at pos[b] of sequence seq[b]
+ * attends positions 0..pos[b], whose values are the ones the codes stand for.
+ * Arguments, bounds, flags, workspace and results as full_attn_decode_kv4.
+ */
+kvr_status full_attn_decode_kv8(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
+                                const kvr_kv8_layout *pool, const float *rope_cos_sin, int64_t max_pos,
+                                float softmax_scale, int64_t max_ctx, void *workspace, size_t workspace_bytes,
+                                kvr_bf16 *out, void *stream);
+
+/*
+ * Positions of an 8-bit pool as bf16 (one rounding of s * u), into pages or
+ * rows.  Arguments, flags and results as kv4_unpack.
+ */
+kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                      int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);
+
+/*
+ * Pages held by more than one sequence (the Full pool of Xiaomi "Full-Pipeline
+ * Inference Optimization", section 2.1, with prefixes that are kept and shared).
+ * The calls work on a block table, whatever the pools behind it hold (bf16, 4
+ * or 8 bits, several layers).
+ *   refs [num_blocks] int32 (device): the holders of a block beyond the first;
+ *   all zero for a pool without sharing, and 0 for a free block.
+ *   kv_pages_grow needs no refs: blocks that it takes have one holder.
+ *   kv_pages_release_window is for sequences that share nothing; kv_pages_free
+ *   with keep_lo is its form for the others.
+ *   free_ids [free_cap], free_count [1] int32 (device): the free list, as
+ *   kv_pages_grow takes from it.
+ * num_blocks <= 2^30 (KVR_EUNSUPPORTED).
+ *
+ * kv_pages_free gives up the blocks of sequences seqs[0..n-1] (int32, device):
+ * all of them where keep_hi is NULL, else those that hold no position of
+ * [keep_lo[i], keep_hi[i]) (int64 [n], device; keep_lo NULL: 0): the end of a
+ * request, a sequence cut to keep_hi positions, a window that has moved on.
+ * Their table entries become -1 and each loses one holder; the blocks that
+ * nobody holds any more are added to the free list in ascending order (in one
+ * call, and the same whichever of the holders came first).  A sequence that the
+ * call names twice gives up once.  Entries of -1 are skipped; ids >= num_blocks are
+ * left in place (KVR_DEV_BAD_BLOCK); a sequence id outside the table is skipped
+ * (KVR_DEV_BAD_SEQ).  If the blocks do not fit in free_cap (KVR_DEV_FREE_FULL)
+ * none is added, and the next call with room for them adds them (their refs are
+ * -1 until then).  n = 0 is a no-op.
+ */
+kvr_status kv_pages_free(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, int32_t *refs, const int32_t *seqs, const int64_t *keep_lo,
+                         const int64_t *keep_hi, int32_t n, int32_t *free_ids, int32_t *free_count, int32_t free_cap,
+                         void *stream);
+
+/*
+ * kv_pages_fork: sequence dst_seqs[i] receives the first lens[i] positions of
+ * src_seqs[i] (int32, int32, int64 [n], device): parallel samples of a prompt,
+ * the beams of a step, a prompt that starts with a kept one.  Whole blocks are
+ * shared (the same id in both rows of the table, one holder more); for a last
+ * block that is filled in part, the call takes a new one from the free list, so
+ * that each sequence may append to its own: the k-th of the call, in order of
+ * the entries, is free_ids[*free_count_in - 1 - k], and copy_src[k] -> copy_dst[k]
+ * (int32 [n]) is the copy to be made in every pool (kv_pages_copy), copy_count
+ * [1] their number.  *free_count_out receives the remaining count and may be the
+ * same word.
+ * Entries of dst's row behind those are left as they are; what the row held
+ * before is to be given up first (kv_pages_free).  Several entries may name one
+ * src; no dst may be named twice, nor be a src of the call.  An entry with a
+ * sequence id outside the table or src = dst (KVR_DEV_BAD_SEQ) or a length
+ * outside it (KVR_DEV_BAD_POS) is skipped; an entry of src's row, or a free id,
+ * that is no block of the pool sets KVR_DEV_BAD_BLOCK: dst's entry becomes -1 (a
+ * new last block is kept without a copy, its pair is -1).  If the list holds too
+ * few blocks (KVR_DEV_NO_BLOCKS) nothing changes and copy_count is 0.  n <= 8192
+ * (KVR_EUNSUPPORTED).
+ */
+kvr_status kv_pages_fork(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, int32_t *refs, const int32_t *src_seqs, const int32_t *dst_seqs,
+                         const int64_t *lens, int32_t n, const int32_t *free_ids, const int32_t *free_count_in,
+                         int32_t *free_count_out, int32_t free_cap, int32_t *copy_src, int32_t *copy_dst,
+                         int32_t *copy_count, void *stream);
+
+/* Workspace bytes for kv_pages_compact (0 on bad arguments). */
+size_t kv_pages_compact_workspace_size(int32_t num_blocks);
+
+/*
+ * kv_pages_compact: the pool's used blocks (those that are not in the free list)
+ * are brought below `limit`, so that it can end there; limit = 0 means as low as
+ * they fit, their number.  The k-th used block at or past the limit, in ascending
+ * order, moves to the k-th free one below it: copy_src[k] -> copy_dst[k] (int32
+ * [num_blocks / 2]) is the copy to be made in every pool (kv_pages_copy),
+ * copy_count [1] their number.  block_table_out receives the table with the new
+ * ids (entries that name a free block become -1, others that are no block of the
+ * pool are kept), refs_out the counts, free_ids_out the free list in descending
+ * order, so that the lowest ids are taken first (*free_count stays); each may be
+ * the array it is made from.  A limit below the number of used blocks
+ * (KVR_DEV_NO_BLOCKS), or a free list that names a block twice or none of the
+ * pool's (KVR_DEV_BAD_BLOCK), moves nothing: the outputs are the inputs and
+ * copy_count is 0.  workspace: kv_pages_compact_workspace_size(num_blocks) bytes,
+ * 16-byte aligned, no initialisation.
+ */
+kvr_status kv_pages_compact(const int32_t *block_table, int32_t *block_table_out, int32_t num_seqs, int32_t max_blocks,
+                            int32_t num_blocks, int32_t limit, const int32_t *refs, int32_t *refs_out,
+                            const int32_t *free_ids, const int32_t *free_count, int32_t *free_ids_out, int32_t free_cap,
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * kv_pages_copy: block copy_src[k] is copied to copy_dst[k] for k < min(*copy_count,
+ * n) (device arrays of n entries, and a device count: the host need not know it),
+ * in each of num_planes arrays of num_blocks equal blocks: planes and block_bytes
+ * are HOST arrays, of device pointers (16-byte aligned) and of a block's bytes (a
+ * multiple of 16) -- the k and v of a bf16 pool are two planes, the data of a
+ * quantised one is one, and all layers that share a block table go in one call.
+ * No destination may be named twice or be a source.  A pair with an id outside the
+ * pool is skipped (KVR_DEV_BAD_BLOCK).  n = 0 or num_planes = 0 is a no-op.
+ */
+kvr_status kv_pages_copy(void *const *planes, const int64_t *block_bytes, int32_t num_planes, int32_t num_blocks,
+                         const int32_t *copy_src, const int32_t *copy_dst, const int32_t *copy_count, int32_t n,
+                         void *stream);
 
 #ifdef __cplusplus
 }

@@ -24,9 +24,15 @@ A full layer's pool may be kept in 4 bits (``Kv4Layout``):
   full_attn_decode_kv4    one token over it
   kv4_unpack              positions of it back to bf16 pages or rows
 
-and ``kv_pages_grow`` builds a step's block tables and slot map on the device
-from the requests' lengths, taking blocks from the free list that
-``kv_pages_release_window`` fills.
+or in 8 bits (``Kv8Layout``: ``kv8_append_rope``, ``full_attn_decode_kv8``,
+``kv8_unpack``), and ``kv_pages_grow`` builds a step's block tables and slot map
+on the device from the requests' lengths, taking blocks from the free list that
+``kv_pages_release_window`` fills.  Pages may be shared:
+
+  kv_pages_fork           a sequence starts with another's positions
+  kv_pages_free           a sequence, or a part of one, gives its blocks up
+  kv_pages_compact        the used blocks move together at the pool's start
+  kv_pages_copy           the block copies of either, in any pools
 """
 from __future__ import annotations
 
@@ -45,6 +51,8 @@ __all__ = [
     "swa_sink_prefill_varlen_workspace_size",
     "Kv4Layout", "kv4_append_rope", "full_attn_decode_kv4", "full_attn_decode_kv4_workspace_size", "kv4_unpack",
     "kv_pages_grow",
+    "Kv8Layout", "kv8_append_rope", "full_attn_decode_kv8", "full_attn_decode_kv8_workspace_size", "kv8_unpack",
+    "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_compact_workspace_size", "kv_pages_copy",
     "DQK", "DV", "DROT", "WINDOW",
 ]
 
@@ -53,6 +61,7 @@ LAYOUT_RING, LAYOUT_PAGED, LAYOUT_LINEAR = 1, 2, 3
 DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_BLOCK, DEV_TIMEOUT, DEV_BAD_ROWS, DEV_FREE_FULL = 1, 2, 4, 8, 16, 32
 DEV_NO_BLOCKS = 64
 KV4_TILE = 2912  # bytes of 16 positions of one KV head in a 4-bit pool
+KV8_TILE = 5136  # the same in an 8-bit pool
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvring.so")
@@ -82,7 +91,7 @@ class _Layout(ctypes.Structure):
     ]
 
 
-class _Layout4(ctypes.Structure):
+class _Layout4(ctypes.Structure):  # (and that of an 8-bit pool: the same fields)
     _fields_ = [
         ("num_kv_heads", ctypes.c_int32),
         ("num_seqs", ctypes.c_int32),
@@ -154,6 +163,25 @@ def lib():
                 L.full_attn_decode_kv4.argtypes = [p, p, p, i32, i32, p, p, i64, f32, i64, p, ctypes.c_size_t, p, p]
                 L.kv4_unpack.restype = ctypes.c_int
                 L.kv4_unpack.argtypes = [p, p, p, p, i32, i64, p, p, p]
+                L.kv8_append_rope.restype = ctypes.c_int
+                L.kv8_append_rope.argtypes = [p, p, p, p, p, i32, i64, i32, p, i64, f32, p, p]
+                L.full_attn_decode_kv8_workspace_size.restype = ctypes.c_size_t
+                L.full_attn_decode_kv8_workspace_size.argtypes = [i32, i32, i32, i64]
+                L.full_attn_decode_kv8.restype = ctypes.c_int
+                L.full_attn_decode_kv8.argtypes = [p, p, p, i32, i32, p, p, i64, f32, i64, p, ctypes.c_size_t, p, p]
+                L.kv8_unpack.restype = ctypes.c_int
+                L.kv8_unpack.argtypes = [p, p, p, p, i32, i64, p, p, p]
+                L.kv_pages_free.restype = ctypes.c_int
+                L.kv_pages_free.argtypes = [p, i32, i32, i32, i32, p, p, p, p, i32, p, p, i32, p]
+                L.kv_pages_fork.restype = ctypes.c_int
+                L.kv_pages_fork.argtypes = [p, i32, i32, i32, i32, p, p, p, p, i32, p, p, p, i32, p, p, p, p]
+                L.kv_pages_compact_workspace_size.restype = ctypes.c_size_t
+                L.kv_pages_compact_workspace_size.argtypes = [i32]
+                L.kv_pages_compact.restype = ctypes.c_int
+                L.kv_pages_compact.argtypes = [p, p, i32, i32, i32, i32, p, p, p, p, p, i32, p, p, p, p,
+                                               ctypes.c_size_t, p]
+                L.kv_pages_copy.restype = ctypes.c_int
+                L.kv_pages_copy.argtypes = [p, p, i32, i32, p, p, p, i32, p]
                 _lib = L
     return _lib
 
@@ -347,17 +375,18 @@ class LinearLayout:
                        0, 0, 0, 0, self.num_rows)
 
 
-class Kv4Layout:
-    """Full pool of one layer in 4 bits: data [nblk, Hkv, Bsz / 16, 2912]
-    uint8 (tiles of 16 positions, see kvr_kv4_layout in kvring.h), block_table
+class _TileLayout:
+    """A pool of tiles of 16 positions of one KV head: data [nblk, Hkv, Bsz / 16, TILE] uint8, block_table
     [S, max_blocks] int32."""
+
+    TILE = 0
 
     def __init__(self, data, block_table):
         _want(data, "pool.data", torch.uint8, 4)
         _want(block_table, "pool.block_table", torch.int32, 2)
         nb, H, tiles, nbytes = data.shape
-        if nbytes != KV4_TILE:
-            raise ValueError(f"pool.data must be [blocks, Hkv, block_size / 16, {KV4_TILE}], got {tuple(data.shape)}")
+        if nbytes != self.TILE:
+            raise ValueError(f"pool.data must be [blocks, Hkv, block_size / 16, {self.TILE}], got {tuple(data.shape)}")
         self.data, self.block_table = data, block_table
         self.num_blocks, self.num_kv_heads, self.block_size = nb, H, 16 * tiles
         self.num_seqs, self.max_blocks = block_table.shape
@@ -374,18 +403,34 @@ class Kv4Layout:
         mb = (max_ctx + block_size - 1) // block_size
         nb = num_seqs * mb
         alloc = torch.zeros if zero else torch.empty
-        data = alloc(nb, num_kv_heads, block_size // 16, KV4_TILE, dtype=torch.uint8, device=device)
+        data = alloc(nb, num_kv_heads, block_size // 16, cls.TILE, dtype=torch.uint8, device=device)
         bt = torch.arange(nb, dtype=torch.int32, device=device).reshape(num_seqs, mb)
         return cls(data, bt)
 
-    @staticmethod
-    def bytes_per_token(num_kv_heads):
+    @classmethod
+    def bytes_per_token(cls, num_kv_heads):
         """Pool bytes one token adds per layer."""
-        return num_kv_heads * KV4_TILE // 16
+        return num_kv_heads * cls.TILE // 16
 
     def c(self):
         self._c.data, self._c.block_table = self.data.data_ptr(), self.block_table.data_ptr()
         return self._c
+
+
+class Kv4Layout(_TileLayout):
+    """Full pool of one layer in 4 bits: data [nblk, Hkv, Bsz / 16, 2912]
+    uint8 (tiles of 16 positions, see kvr_kv4_layout in kvring.h), block_table
+    [S, max_blocks] int32."""
+
+    TILE = KV4_TILE
+
+
+class Kv8Layout(_TileLayout):
+    """Full pool of one layer in 8 bits: data [nblk, Hkv, Bsz / 16, 5136]
+    uint8 (tiles of 16 positions, see kvr_kv8_layout in kvring.h), block_table
+    [S, max_blocks] int32."""
+
+    TILE = KV8_TILE
 
 
 def rope_table(theta: float, max_pos: int, device="cuda", nthreads: int = 0) -> torch.Tensor:
@@ -717,6 +762,12 @@ def full_attn_decode_kv4_workspace_size(B, Hq, Hkv, max_ctx) -> int:
 def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, workspace=None, out=None, stream=None):
     """full_attn_decode over a 4-bit pool (Kv4Layout).  Rows may share a
     sequence (draft tokens at their own positions)."""
+    return _decode_tiles(Kv4Layout, lib().full_attn_decode_kv4, full_attn_decode_kv4_workspace_size, q, pos, seq, pool,
+                         table, softmax_scale, max_ctx, workspace, out, stream)
+
+
+def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_ctx, workspace, out, stream):
+    _want_pool(pool, kind)
     _want_q(q)
     _want(pos, "pos", torch.int64, 1)
     _want(seq, "seq", torch.int32, 1)
@@ -725,7 +776,7 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
     _want_len(pos, "pos", B)
     _want_len(seq, "seq", B)
     if workspace is None:
-        n = full_attn_decode_kv4_workspace_size(B, Hq, pool.num_kv_heads, max_ctx)
+        n = size(B, Hq, pool.num_kv_heads, max_ctx)
         if n:  # (short contexts need none)
             workspace = _empty(n, torch.uint8, q, stream)
     else:
@@ -733,10 +784,14 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
     out = _out(out, B, Hq, q, stream)
     _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
     c = pool.c()
-    _check(lib().full_attn_decode_kv4(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table),
-                                      table.shape[0], float(softmax_scale), int(max_ctx), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _ptr(out), _stream(stream)))
+    _check(fn(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table), table.shape[0], float(softmax_scale),
+              int(max_ctx), _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(out), _stream(stream)))
     return out
+
+
+def _want_pool(pool, kind):
+    if getattr(pool, "TILE", None) != kind.TILE:  # (the layouts' structs look alike to the library)
+        raise TypeError(f"a {kind.__name__} is wanted, got {type(pool).__name__}")
 
 
 def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=None):
@@ -745,6 +800,11 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
     dst_seqs[i] of a PagedLayout, or into rows cu_rows[i] .. of a LinearLayout.
     T bounds the rows of the call (cu_rows' last entry); by default it is all
     that dst, or its block table, can name."""
+    _unpack_tiles(Kv4Layout, lib().kv4_unpack, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream)
+
+
+def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream):
+    _want_pool(src, kind)
     _want(src_seqs, "src_seqs", torch.int32, 1)
     _want(lo, "lo", torch.int64, 1)
     _want(cu_rows, "cu_rows", torch.int32, 1)
@@ -765,13 +825,190 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
         _want_len(dst_seqs, "dst_seqs", n)
     _same_device(src_seqs, lo, cu_rows, dst_seqs, *src.tensors(), *dst.tensors())
     sc, dc = src.c(), dst.c()
-    _check(lib().kv4_unpack(ctypes.byref(sc), _ptr(src_seqs), _ptr(lo), _ptr(cu_rows), n, T, _ptr(dst_seqs),
-                            ctypes.byref(dc), _stream(stream)))
+    _check(fn(ctypes.byref(sc), _ptr(src_seqs), _ptr(lo), _ptr(cu_rows), n, T, _ptr(dst_seqs), ctypes.byref(dc),
+              _stream(stream)))
+
+
+def kv8_append_rope(k, v, cu_rows, P0, seqs, table, value_scale, dst, stream=None):
+    """KV write into an 8-bit pool (Kv8Layout) of a batch of chunks: rows
+    cu_rows[i] .. cu_rows[i+1]-1 of k and v (int32 [n + 1]) go to positions
+    P0[i] .. (int64) of sequence seqs[i] (int32; -1 marks padding).  Positions are
+    written in order: those ahead of P0[i] in its tile of 16 are there already,
+    those behind the chunk in its last tile mean nothing afterwards."""
+    _want_pool(dst, Kv8Layout)
+    _want(k, "k", torch.bfloat16, 3)
+    _want(v, "v", torch.bfloat16, 3)
+    _want(cu_rows, "cu_rows", torch.int32, 1)
+    _want(P0, "P0", torch.int64, 1)
+    _want(seqs, "seqs", torch.int32, 1)
+    _want_table(table)
+    T, H = k.shape[:2]
+    n = seqs.shape[0]
+    if k.shape[2] != DQK or v.shape != (T, H, DV):
+        raise ValueError("k/v shapes disagree")
+    _want_len(cu_rows, "cu_rows", n + 1)
+    _want_len(P0, "P0", n)
+    _same_device(k, v, cu_rows, P0, seqs, table, *dst.tensors())
+    c = dst.c()
+    _check(lib().kv8_append_rope(_ptr(k), _ptr(v), _ptr(cu_rows), _ptr(P0), _ptr(seqs), n, T, H, _ptr(table),
+                                 table.shape[0], float(value_scale), ctypes.byref(c), _stream(stream)))
+
+
+def full_attn_decode_kv8_workspace_size(B, Hq, Hkv, max_ctx) -> int:
+    return int(lib().full_attn_decode_kv8_workspace_size(int(B), int(Hq), int(Hkv), int(max_ctx)))
+
+
+def full_attn_decode_kv8(q, pos, seq, pool, table, softmax_scale, max_ctx, workspace=None, out=None, stream=None):
+    """full_attn_decode over an 8-bit pool (Kv8Layout).  Rows may share a
+    sequence (draft tokens at their own positions)."""
+    return _decode_tiles(Kv8Layout, lib().full_attn_decode_kv8, full_attn_decode_kv8_workspace_size, q, pos, seq, pool,
+                         table, softmax_scale, max_ctx, workspace, out, stream)
+
+
+def kv8_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=None):
+    """kv4_unpack from an 8-bit pool (Kv8Layout)."""
+    _unpack_tiles(Kv8Layout, lib().kv8_unpack, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream)
+
+
+def _want_free_list(free_ids, free_count, refs, num_blocks):
+    _want(free_ids, "free_ids", torch.int32, 1)
+    _want(free_count, "free_count", torch.int32, 1)
+    _want_len(free_count, "free_count", 1)
+    _want(refs, "refs", torch.int32, 1)
+    _want_len(refs, "refs", int(num_blocks))
+
+
+def _want_pairs(copy_src, copy_dst, copy_count, least):
+    _want(copy_src, "copy_src", torch.int32, 1)
+    _want(copy_dst, "copy_dst", torch.int32, 1)
+    _want(copy_count, "copy_count", torch.int32, 1)
+    _want_len(copy_count, "copy_count", 1)
+    if copy_src.shape[0] < least or copy_dst.shape[0] < least:
+        raise ValueError(f"copy_src and copy_dst must have {least} entries, got {copy_src.shape[0]} and {copy_dst.shape[0]}")
+
+
+def kv_pages_free(block_table, num_blocks, block_size, refs, seqs, free_ids, free_count, keep_lo=None, keep_hi=None,
+                  stream=None):
+    """Sequences seqs[i] (int32 [n]) give up their blocks -- all of them, or with
+    keep_hi (and keep_lo, default 0; int64 [n]) those without a position of
+    [keep_lo[i], keep_hi[i]): the entries of block_table (int32 [num_seqs,
+    max_blocks]) become -1, refs (int32 [num_blocks], the holders of a block
+    beyond the first) goes down, and the blocks that nobody holds are added to the
+    free list (free_ids int32 [cap], free_count int32 [1]) in ascending order."""
+    _want(block_table, "block_table", torch.int32, 2)
+    _want(seqs, "seqs", torch.int32, 1)
+    _want_free_list(free_ids, free_count, refs, num_blocks)
+    S, mb = block_table.shape
+    n = seqs.shape[0]
+    for t, name in ((keep_lo, "keep_lo"), (keep_hi, "keep_hi")):
+        if t is not None:
+            _want(t, name, torch.int64, 1)
+            _want_len(t, name, n)
+    _same_device(block_table, refs, seqs, free_ids, free_count, keep_lo, keep_hi)
+    _check(lib().kv_pages_free(_ptr(block_table), S, mb, int(block_size), int(num_blocks), _ptr(refs), _ptr(seqs),
+                               _ptr(keep_lo), _ptr(keep_hi), n, _ptr(free_ids), _ptr(free_count), free_ids.shape[0],
+                               _stream(stream)))
+
+
+def kv_pages_fork(block_table, num_blocks, block_size, refs, src_seqs, dst_seqs, lens, free_ids, free_count, copy_src,
+                  copy_dst, copy_count, free_count_out=None, stream=None):
+    """Sequence dst_seqs[i] (int32 [n]) receives the first lens[i] (int64)
+    positions of src_seqs[i]: whole blocks are shared (refs goes up), a last block
+    that is filled in part gets a new one from the end of the free list, and the
+    copies to be made (kv_pages_copy) are copy_src[k] -> copy_dst[k] (int32, n
+    entries), copy_count (int32 [1]) of them.  The remaining count goes to
+    free_count_out (default: free_count itself).  Everything stays on the
+    device."""
+    _want(block_table, "block_table", torch.int32, 2)
+    _want(src_seqs, "src_seqs", torch.int32, 1)
+    _want(dst_seqs, "dst_seqs", torch.int32, 1)
+    _want(lens, "lens", torch.int64, 1)
+    _want_free_list(free_ids, free_count, refs, num_blocks)
+    if free_count_out is None:
+        free_count_out = free_count
+    _want(free_count_out, "free_count_out", torch.int32, 1)
+    _want_len(free_count_out, "free_count_out", 1)
+    S, mb = block_table.shape
+    n = src_seqs.shape[0]
+    _want_len(dst_seqs, "dst_seqs", n)
+    _want_len(lens, "lens", n)
+    _want_pairs(copy_src, copy_dst, copy_count, n)
+    _same_device(block_table, refs, src_seqs, dst_seqs, lens, free_ids, free_count, free_count_out, copy_src, copy_dst,
+                 copy_count)
+    _check(lib().kv_pages_fork(_ptr(block_table), S, mb, int(block_size), int(num_blocks), _ptr(refs), _ptr(src_seqs),
+                               _ptr(dst_seqs), _ptr(lens), n, _ptr(free_ids), _ptr(free_count), _ptr(free_count_out),
+                               free_ids.shape[0], _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream)))
+
+
+def kv_pages_compact_workspace_size(num_blocks) -> int:
+    return int(lib().kv_pages_compact_workspace_size(int(num_blocks)))
+
+
+def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_src, copy_dst, copy_count, limit=0,
+                     table_out=None, refs_out=None, free_ids_out=None, workspace=None, stream=None):
+    """The pool's used blocks move below `limit` (0: as low as they fit): the
+    copies to be made (kv_pages_copy) are copy_src[k] -> copy_dst[k] (int32,
+    num_blocks // 2 entries), copy_count (int32 [1]) of them; block_table, refs
+    and the free list (then in descending order) name the new places, in
+    table_out, refs_out and free_ids_out (default: the arrays themselves).
+    Everything stays on the device."""
+    _want(block_table, "block_table", torch.int32, 2)
+    _want_free_list(free_ids, free_count, refs, num_blocks)
+    _want_pairs(copy_src, copy_dst, copy_count, int(num_blocks) // 2)
+    outs = []
+    for t, src, name in ((table_out, block_table, "table_out"), (refs_out, refs, "refs_out"),
+                         (free_ids_out, free_ids, "free_ids_out")):
+        if t is None:
+            t = src
+        else:
+            _want(t, name, torch.int32, src.dim())
+            if t.shape != src.shape:
+                raise ValueError(f"{name} must have the shape {tuple(src.shape)}, got {tuple(t.shape)}")
+        outs.append(t)
+    if workspace is None:
+        workspace = _empty(max(kv_pages_compact_workspace_size(num_blocks), 1), torch.uint8, refs, stream)
+    else:
+        _want(workspace, "workspace", torch.uint8, 1)
+    S, mb = block_table.shape
+    _same_device(block_table, refs, free_ids, free_count, copy_src, copy_dst, copy_count, workspace, *outs)
+    _check(lib().kv_pages_compact(_ptr(block_table), _ptr(outs[0]), S, mb, int(num_blocks), int(limit), _ptr(refs),
+                                  _ptr(outs[1]), _ptr(free_ids), _ptr(free_count), _ptr(outs[2]), free_ids.shape[0],
+                                  _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)))
+
+
+def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):
+    """Copy block copy_src[k] to copy_dst[k], k < copy_count, in every pool of
+    `pools` (one PagedLayout, Kv4Layout or Kv8Layout, or a list of them: the
+    layers that share a block table), in one launch."""
+    if isinstance(pools, (PagedLayout, _TileLayout)):
+        pools = [pools]
+    planes = []
+    for p in pools:
+        if isinstance(p, PagedLayout):
+            planes += [p.k, p.v]
+        elif isinstance(p, _TileLayout):
+            planes.append(p.data)
+        else:
+            raise TypeError(f"pools must be PagedLayout, Kv4Layout or Kv8Layout, got {type(p).__name__}")
+    if not planes:
+        return
+    nb = planes[0].shape[0]
+    for t in planes:
+        if t.shape[0] != nb:
+            raise ValueError(f"the pools have {nb} and {t.shape[0]} blocks: they do not share a block table")
+    _want_pairs(copy_src, copy_dst, copy_count, 0)
+    _same_device(copy_src, copy_dst, copy_count, *planes)
+    n = len(planes)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in planes])
+    sizes = (ctypes.c_int64 * n)(*[t.stride(0) * t.element_size() for t in planes])
+    _check(lib().kv_pages_copy(ptrs, sizes, n, nb, _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count),
+                               min(copy_src.shape[0], copy_dst.shape[0]), _stream(stream)))
 
 
 def debug_stall_next(launches: int, limit_ns: int) -> None:
-    """Test hook: the next `launches` windowed decodes (ring layout), 4-bit
-    decodes or single-chunk full-attention prefills stall on purpose and leave
+    """Test hook: the next `launches` windowed decodes (ring layout), 4-bit and
+    8-bit decodes or single-chunk full-attention prefills stall on purpose and leave
     by their bounded-wait exit after limit_ns, setting DEV_TIMEOUT (kvr_debug_stall_next)."""
     _check(lib().kvr_debug_stall_next(int(launches), int(limit_ns)))
 

@@ -187,8 +187,10 @@ kvr_status check_layout(const kvr_kv_layout *L, int want_kind, const char *name)
   return KVR_OK;
 }
 
-kvr::Kv4View view4(const kvr_kv4_layout &L) {
-  kvr::Kv4View v;
+// The 4-bit and 8-bit pools' layouts have the same fields.
+template <class View, class Layout>
+View pool_view(const Layout &L) {
+  View v;
   v.data = L.data;
   v.block_table = L.block_table;
   v.hkv = L.num_kv_heads;
@@ -198,8 +200,11 @@ kvr::Kv4View view4(const kvr_kv4_layout &L) {
   v.num_blocks = L.num_blocks;
   return v;
 }
+kvr::Kv4View view4(const kvr_kv4_layout &L) { return pool_view<kvr::Kv4View>(L); }
+kvr::Kv8View view8(const kvr_kv8_layout &L) { return pool_view<kvr::Kv8View>(L); }
 
-kvr_status check_kv4(const kvr_kv4_layout *L, const char *name) {
+template <class Layout>
+kvr_status check_pool(const Layout *L, const char *name) {
   if (!L) return fail(KVR_EINVAL, "%s: layout is NULL", name);
   if (L->num_kv_heads < 1) return fail(KVR_EINVAL, "%s: num_kv_heads %d", name, L->num_kv_heads);
   if (!L->data || !L->block_table) return fail(KVR_EINVAL, "%s: data/block_table is NULL", name);
@@ -212,6 +217,8 @@ kvr_status check_kv4(const kvr_kv4_layout *L, const char *name) {
     return fail(KVR_EUNSUPPORTED, "%s: max_blocks*block_size %lld > 2^35", name, (long long)L->max_blocks * L->block_size);
   return KVR_OK;
 }
+kvr_status check_kv4(const kvr_kv4_layout *L, const char *name) { return check_pool(L, name); }
+kvr_status check_kv8(const kvr_kv8_layout *L, const char *name) { return check_pool(L, name); }
 
 kvr_status check_table(const float *table, int64_t max_pos) {
   if (!table) return fail(KVR_EINVAL, "rope_cos_sin is NULL");
@@ -250,7 +257,7 @@ unsigned long long take_stall() {
 }
 
 namespace {
-constexpr int MAX_KSLOT = 24;
+constexpr int MAX_KSLOT = 32;
 unsigned char g_smem_done[MAX_DEV][MAX_KSLOT];
 void *g_smem_ctx[MAX_DEV];  // the context g_smem_done[dev] is for
 }  // namespace
@@ -717,6 +724,196 @@ kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const 
   if (e != cudaSuccess) return state_fail(e, who);
   e = kvr::launch_kv4_unpack(view4(*src), src_seqs, lo, cu_rows, n, T, dst_seqs, view(*dst), st, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv4_unpack launch");
+  return ok();
+}
+
+kvr_status kv8_append_rope(const kvr_bf16 *k, const kvr_bf16 *v, const int32_t *cu_rows, const int64_t *P0,
+                           const int32_t *seqs, int32_t n, int64_t T, int32_t Hkv, const float *rope_cos_sin,
+                           int64_t max_pos, float value_scale, const kvr_kv8_layout *dst, void *stream) {
+  const char *who = "kv8_append_rope";
+  kvr_status s = check_kv8(dst, "dst");
+  if (s) return s;
+  if (Hkv != dst->num_kv_heads) return fail(KVR_EINVAL, "Hkv %d != dst->num_kv_heads %d", Hkv, dst->num_kv_heads);
+  if ((s = check_table(rope_cos_sin, max_pos))) return s;
+  if (n < 0 || T < 0 || T > INT32_MAX) return fail(KVR_EINVAL, "%s: n %d, T %lld", who, n, (long long)T);
+  if (n == 0 || T == 0) return ok();
+  if (!k || !v || !cu_rows || !P0 || !seqs) return fail(KVR_EINVAL, "%s: k/v/cu_rows/P0/seqs is NULL", who);
+  if (!aligned16(k) || !aligned16(v)) return fail(KVR_EINVAL, "k/v not 16-byte aligned");
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_kv8_append(k, v, cu_rows, P0, seqs, n, T, rope_cos_sin, max_pos, value_scale, view8(*dst), st,
+                             as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8_append_rope launch");
+  return ok();
+}
+
+size_t full_attn_decode_kv8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int64_t max_ctx) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_ctx < 1) return 0;
+  return kvr::kv8_decode_workspace(B, Hq, Hkv, max_ctx);
+}
+
+kvr_status full_attn_decode_kv8(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
+                                const kvr_kv8_layout *pool, const float *rope_cos_sin, int64_t max_pos,
+                                float softmax_scale, int64_t max_ctx, void *workspace, size_t workspace_bytes,
+                                kvr_bf16 *out, void *stream) {
+  if (B < 0) return fail(KVR_EINVAL, "B %d", B);
+  kvr_status s = check_kv8(pool, "pool");
+  if (s) return s;
+  if ((s = check_heads(Hq, pool->num_kv_heads, 16))) return s;
+  if ((s = check_table(rope_cos_sin, max_pos))) return s;
+  if (max_ctx < 1 || max_ctx > max_pos)
+    return fail(KVR_ERANGE, "max_ctx %lld outside [1, max_pos=%lld]", (long long)max_ctx, (long long)max_pos);
+  if (max_ctx > (int64_t)pool->max_blocks * pool->block_size)
+    return fail(KVR_ERANGE, "max_ctx %lld exceeds max_blocks*block_size = %lld", (long long)max_ctx,
+                (long long)pool->max_blocks * pool->block_size);
+  if (B == 0) return ok();
+  if (!q || !pos || !seq || !out) return fail(KVR_EINVAL, "q/pos/seq/out is NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(KVR_EINVAL, "q/out not 16-byte aligned");
+  if (max_ctx > (1 << 30)) return fail(KVR_EUNSUPPORTED, "max_ctx %lld > 2^30", (long long)max_ctx);
+  const size_t need = kvr::kv8_decode_workspace(B, Hq, pool->num_kv_heads, max_ctx);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(KVR_EWORKSPACE, "workspace %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, need);
+  if (!aligned16(workspace)) return fail(KVR_EINVAL, "workspace not 16-byte aligned");
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, "full_attn_decode_kv8");
+  e = kvr::launch_kv8_decode(q, pos, seq, B, Hq, view8(*pool), rope_cos_sin, max_pos, softmax_scale, max_ctx,
+                             workspace, out, st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "full_attn_decode_kv8 launch");
+  return ok();
+}
+
+kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                      int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream) {
+  const char *who = "kv8_unpack";
+  kvr_status s = check_kv8(src, "src");
+  if (s) return s;
+  if ((s = check_layout(dst, 0, "dst"))) return s;
+  if (dst->kind != KVR_LAYOUT_PAGED && dst->kind != KVR_LAYOUT_LINEAR)
+    return fail(KVR_EINVAL, "dst: layout kind %d, expected PAGED or LINEAR", dst->kind);
+  if (src->num_kv_heads != dst->num_kv_heads)
+    return fail(KVR_EINVAL, "src has %d KV heads, dst %d", src->num_kv_heads, dst->num_kv_heads);
+  if (n < 0 || T < 0 || T > INT32_MAX) return fail(KVR_EINVAL, "%s: n %d, T %lld", who, n, (long long)T);
+  if (dst->kind == KVR_LAYOUT_LINEAR && dst->num_rows < T)
+    return fail(KVR_EINVAL, "LINEAR dst has %lld rows, T = %lld", (long long)dst->num_rows, (long long)T);
+  if (n == 0 || T == 0) return ok();
+  if (!src_seqs || !lo || !cu_rows) return fail(KVR_EINVAL, "%s: src_seqs/lo/cu_rows is NULL", who);
+  if (dst->kind == KVR_LAYOUT_PAGED && !dst_seqs) return fail(KVR_EINVAL, "%s: dst_seqs is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_kv8_unpack(view8(*src), src_seqs, lo, cu_rows, n, T, dst_seqs, view(*dst), st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv8_unpack launch");
+  return ok();
+}
+
+// Sizes and the arrays that every call on shared pages has.
+static kvr_status check_pages(const char *who, const int32_t *block_table, int32_t num_seqs, int32_t max_blocks,
+                              int32_t num_blocks, const int32_t *refs, const int32_t *free_ids,
+                              const int32_t *free_count, int32_t free_cap) {
+  if (num_seqs < 1 || max_blocks < 1 || num_blocks < 1)
+    return fail(KVR_EINVAL, "%s: num_seqs/max_blocks/num_blocks must be >= 1", who);
+  if (num_blocks > kvr::PAGES_MAX_BLOCKS) return fail(KVR_EUNSUPPORTED, "%s: num_blocks %d > 2^30", who, num_blocks);
+  if (free_cap < 0) return fail(KVR_EINVAL, "%s: free_cap %d", who, free_cap);
+  if (!block_table || !refs || !free_count) return fail(KVR_EINVAL, "%s: block_table/refs/free_count is NULL", who);
+  if (free_cap > 0 && !free_ids) return fail(KVR_EINVAL, "%s: free_ids is NULL", who);
+  return KVR_OK;
+}
+
+kvr_status kv_pages_free(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, int32_t *refs, const int32_t *seqs, const int64_t *keep_lo,
+                         const int64_t *keep_hi, int32_t n, int32_t *free_ids, int32_t *free_count, int32_t free_cap,
+                         void *stream) {
+  const char *who = "kv_pages_free";
+  if (n < 0 || block_size < 1) return fail(KVR_EINVAL, "%s: n %d, block_size %d", who, n, block_size);
+  kvr_status s = check_pages(who, block_table, num_seqs, max_blocks, num_blocks, refs, free_ids, free_count, free_cap);
+  if (s) return s;
+  if (keep_lo && !keep_hi) return fail(KVR_EINVAL, "%s: keep_lo without keep_hi", who);
+  if (n == 0) return ok();
+  if (!seqs) return fail(KVR_EINVAL, "%s: seqs is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_pages_free(block_table, num_seqs, max_blocks, block_size, num_blocks, refs, seqs, keep_lo, keep_hi, n,
+                             free_ids, free_count, free_cap, st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_pages_free launch");
+  return ok();
+}
+
+kvr_status kv_pages_fork(int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t block_size,
+                         int32_t num_blocks, int32_t *refs, const int32_t *src_seqs, const int32_t *dst_seqs,
+                         const int64_t *lens, int32_t n, const int32_t *free_ids, const int32_t *free_count_in,
+                         int32_t *free_count_out, int32_t free_cap, int32_t *copy_src, int32_t *copy_dst,
+                         int32_t *copy_count, void *stream) {
+  const char *who = "kv_pages_fork";
+  if (n < 0 || block_size < 1) return fail(KVR_EINVAL, "%s: n %d, block_size %d", who, n, block_size);
+  kvr_status s = check_pages(who, block_table, num_seqs, max_blocks, num_blocks, refs, free_ids, free_count_in, free_cap);
+  if (s) return s;
+  if (!free_count_out || !copy_count) return fail(KVR_EINVAL, "%s: free_count_out/copy_count is NULL", who);
+  if (n > kvr::FORK_MAX_N) return fail(KVR_EUNSUPPORTED, "%s: n %d > %d", who, n, kvr::FORK_MAX_N);
+  if (n > 0 && (!src_seqs || !dst_seqs || !lens || !copy_src || !copy_dst))
+    return fail(KVR_EINVAL, "%s: src_seqs/dst_seqs/lens/copy_src/copy_dst is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_pages_fork(block_table, num_seqs, max_blocks, block_size, num_blocks, refs, src_seqs, dst_seqs, lens,
+                             n, free_ids, free_count_in, free_count_out, free_cap, copy_src, copy_dst, copy_count, st,
+                             as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_pages_fork launch");
+  return ok();
+}
+
+size_t kv_pages_compact_workspace_size(int32_t num_blocks) { return num_blocks < 1 ? 0 : sizeof(int32_t) * (size_t)num_blocks; }
+
+kvr_status kv_pages_compact(const int32_t *block_table, int32_t *block_table_out, int32_t num_seqs, int32_t max_blocks,
+                            int32_t num_blocks, int32_t limit, const int32_t *refs, int32_t *refs_out,
+                            const int32_t *free_ids, const int32_t *free_count, int32_t *free_ids_out, int32_t free_cap,
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+  const char *who = "kv_pages_compact";
+  kvr_status s = check_pages(who, block_table, num_seqs, max_blocks, num_blocks, refs, free_ids, free_count, free_cap);
+  if (s) return s;
+  if (limit < 0) return fail(KVR_EINVAL, "%s: limit %d", who, limit);
+  if (!block_table_out || !refs_out || !copy_src || !copy_dst || !copy_count || (free_cap > 0 && !free_ids_out))
+    return fail(KVR_EINVAL, "%s: block_table_out/refs_out/free_ids_out/copy_src/copy_dst/copy_count is NULL", who);
+  const size_t need = kv_pages_compact_workspace_size(num_blocks);
+  if (!workspace || workspace_bytes < need)
+    return fail(KVR_EWORKSPACE, "workspace %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, need);
+  if (!aligned16(workspace)) return fail(KVR_EINVAL, "workspace not 16-byte aligned");
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  e = kvr::launch_pages_compact(block_table, block_table_out, (long long)num_seqs * max_blocks, num_blocks, limit, refs,
+                                refs_out, free_ids, free_count, free_ids_out, free_cap, copy_src, copy_dst, copy_count,
+                                static_cast<int32_t *>(workspace), st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_pages_compact launch");
+  return ok();
+}
+
+kvr_status kv_pages_copy(void *const *planes, const int64_t *block_bytes, int32_t num_planes, int32_t num_blocks,
+                         const int32_t *copy_src, const int32_t *copy_dst, const int32_t *copy_count, int32_t n,
+                         void *stream) {
+  const char *who = "kv_pages_copy";
+  if (num_planes < 0 || num_blocks < 1 || n < 0)
+    return fail(KVR_EINVAL, "%s: num_planes %d, num_blocks %d, n %d", who, num_planes, num_blocks, n);
+  if (num_planes > 0 && (!planes || !block_bytes)) return fail(KVR_EINVAL, "%s: planes/block_bytes is NULL", who);
+  for (int32_t p = 0; p < num_planes; ++p) {
+    if (!planes[p] || !aligned16(planes[p])) return fail(KVR_EINVAL, "%s: plane %d is NULL or not 16-byte aligned", who, p);
+    if (block_bytes[p] < 16 || block_bytes[p] % 16 || block_bytes[p] > (1LL << 40))
+      return fail(KVR_EINVAL, "%s: plane %d: blocks of %lld bytes (needs a multiple of 16 up to 2^40)", who, p,
+                  (long long)block_bytes[p]);
+  }
+  if (!copy_count) return fail(KVR_EINVAL, "%s: copy_count is NULL", who);
+  if (n == 0 || num_planes == 0) return ok();
+  if (!copy_src || !copy_dst) return fail(KVR_EINVAL, "%s: copy_src/copy_dst is NULL", who);
+  unsigned *st = nullptr;
+  cudaError_t e = status_ptr(&st, stream);
+  if (e != cudaSuccess) return state_fail(e, who);
+  static_assert(sizeof(long long) == sizeof(int64_t), "block_bytes is handed on");
+  e = kvr::launch_pages_copy(reinterpret_cast<uint8_t *const *>(planes), reinterpret_cast<const long long *>(block_bytes),
+                             num_planes, num_blocks, copy_src, copy_dst, copy_count, n, st, as_stream(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_pages_copy launch");
   return ok();
 }
 

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kv4.cuh"
+#include "kv8.cuh"
 
 namespace kvr {
 
@@ -214,6 +215,39 @@ cudaError_t launch_pages_grow(int32_t *table, int num_seqs, int max_blocks, int 
                               const int32_t *free_ids, const int32_t *count_in, int32_t *count_out, int free_cap,
                               int32_t *cu_rows, int64_t *pos, int32_t *row_seq, int64_t *slots, long long T,
                               unsigned *status, cudaStream_t st);
+
+// The 8-bit pool: KV write of a batch of chunks, decode, and back to bf16.
+cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, const int32_t *cu_rows, const int64_t *P0,
+                              const int32_t *seqs, int n, long long T, const float *table, int64_t max_pos,
+                              float value_scale, const Kv8View &dst, unsigned *status, cudaStream_t st);
+size_t kv8_decode_workspace(int B, int hq, int hkv, long long max_ctx);
+cudaError_t launch_kv8_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
+                              const Kv8View &pool, const float *table, int64_t max_pos, float softmax_scale,
+                              long long max_ctx, void *ws, uint16_t *out, unsigned *status, cudaStream_t st);
+cudaError_t launch_kv8_unpack(const Kv8View &src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
+                              int n, long long T, const int32_t *dst_seqs, const KvView &dst, unsigned *status,
+                              cudaStream_t st);
+
+// Shared pages (pages_share.cu) and the copies that follow (pages_copy.cu).
+constexpr int FORK_MAX_N = 8192;         // entries of one kv_pages_fork call (their places lie in shared memory)
+constexpr int PAGES_MAX_BLOCKS = 1 << 30;
+constexpr int PAGES_COPY_PLANES = 96;    // arrays of one copy launch (more take more launches)
+cudaError_t launch_pages_free(int32_t *table, int num_seqs, int max_blocks, int block_size, int num_blocks, int32_t *refs,
+                              const int32_t *seqs, const int64_t *keep_lo, const int64_t *keep_hi, int n,
+                              int32_t *free_ids, int32_t *free_count, int free_cap, unsigned *status, cudaStream_t st);
+cudaError_t launch_pages_fork(int32_t *table, int num_seqs, int max_blocks, int block_size, int num_blocks, int32_t *refs,
+                              const int32_t *src_seqs, const int32_t *dst_seqs, const int64_t *lens, int n,
+                              const int32_t *free_ids, const int32_t *count_in, int32_t *count_out, int free_cap,
+                              int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, unsigned *status,
+                              cudaStream_t st);
+cudaError_t launch_pages_compact(const int32_t *table, int32_t *table_out, long long entries, int num_blocks, int limit,
+                                 const int32_t *refs, int32_t *refs_out, const int32_t *free_ids,
+                                 const int32_t *free_count, int32_t *free_out, int free_cap, int32_t *copy_src,
+                                 int32_t *copy_dst, int32_t *copy_count, int32_t *map, unsigned *status,
+                                 cudaStream_t st);
+cudaError_t launch_pages_copy(uint8_t *const *data, const long long *bytes, int planes, int num_blocks,
+                              const int32_t *src, const int32_t *dst, const int32_t *count, int n, unsigned *status,
+                              cudaStream_t st);
 
 int num_sms();
 
