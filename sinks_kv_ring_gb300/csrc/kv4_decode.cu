@@ -89,6 +89,7 @@ constexpr float K4_SLACK = 4.f;      // how far a score may pass the reference m
 // of the sum, a sixteenth of the output's half step.
 struct K4Line {
   static constexpr int UNIT = K4_UNIT, ROW = 16, MIN = K4_WARPS, MOST = 1024 * K4_WARPS, CTAS = K4_CTAS;
+  static constexpr bool SHARE = false;
 };
 // shared memory: query operands (12 steps), their group sums, row factors, barriers, abort flag, stages
 constexpr int K4_OFF_QX = 12 * 512;

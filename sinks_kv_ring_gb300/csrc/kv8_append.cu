@@ -25,10 +25,10 @@
 namespace kvr {
 namespace {
 
-constexpr int K8A_WARPS = 8;
+constexpr int K8A_WARPS = 4;
 constexpr unsigned FULLW = 0xffffffffu;
 
-__device__ __forceinline__ float abs_bits(uint32_t m) { return __uint_as_float(m); }
+__device__ __forceinline__ void prefetch_line(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The least bf16 number s with 127 s >= a (a finite, >= 0): the quotient
 // rounded up to bf16, one step more where fp32 rounded it down onto it.
@@ -38,41 +38,66 @@ __device__ __forceinline__ float kv8_scale(float a) {
   return __uint_as_float(b);
 }
 
-// Stored codes (u + 128) of four values: rint(x / s) by the residual step,
-// rounded by adding 1.5 2^23, which leaves it in the low bits.  s = 0 has r = 0.
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// A scale, and what the quotients by it are made with.
 struct Kv8Div {
-  float s, r;
-  bool slow;  // a scale so small that its reciprocal or the residual leaves fp32
+  uint64_t ns, r;  // minus the scale, and its reciprocal (0 for a scale of 0), in both halves
+  bool tiny;       // so small that the reciprocal leaves fp32: then of 2^64 times the scale, for values times 2^64
 };
 __device__ __forceinline__ Kv8Div kv8_div(float s) {
   Kv8Div D;
-  D.s = s;
-  D.slow = s < 0x1p-100f && s > 0.f;
-  D.r = s > 0.f && !D.slow ? __frcp_rn(s) : 0.f;
+  D.tiny = s < 0x1p-100f && s > 0.f;
+  if (D.tiny) s *= 0x1p64f;
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  D.ns = f32x2(-s, -s);
+  D.r = f32x2(r, r);
   return D;
 }
-__device__ __forceinline__ uint32_t kv8_codes(const float (&x)[4], const Kv8Div &D) {
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float q0 = __fmul_rn(x[i], D.r);
-    float v = fmaf(fmaf(-D.s, q0, x[i]), D.r, q0);
-    if (D.slow) v = __fdiv_rn(x[i], D.s);
-    q[i] = __float_as_uint(__fadd_rn(v, 12582912.f));
+// Stored codes (u + 128) of four values in two pairs: the quotients are rounded by
+// adding 1.5 2^23 and the 128 (an even number: halves go to even as without it),
+// which leaves them in the low bytes.
+template <bool TINY>
+__device__ __forceinline__ uint32_t kv8_codes(uint64_t a, uint64_t b, const Kv8Div &D) {
+  const uint64_t magic = f32x2(12583040.f, 12583040.f);
+  if (TINY) {
+    a = mul_f32x2(a, f32x2(0x1p64f, 0x1p64f));
+    b = mul_f32x2(b, f32x2(0x1p64f, 0x1p64f));
   }
-  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410) ^ 0x80808080u;
+  const uint64_t qa = mul_f32x2(a, D.r), qb = mul_f32x2(b, D.r);
+  float x, y, z, w;
+  f32x2_split(add_f32x2(fma_f32x2(fma_f32x2(D.ns, qa, a), D.r, qa), magic), x, y);
+  f32x2_split(add_f32x2(fma_f32x2(fma_f32x2(D.ns, qb, b), D.r, qb), magic), z, w);
+  return __byte_perm(__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x0040),
+                     __byte_perm(__float_as_uint(z), __float_as_uint(w), 0x0040), 0x5410);
 }
 // Stored codes under a larger scale: the values that they stand for, quantised again.
+template <bool TINY>
 __device__ __forceinline__ uint32_t kv8_again(uint32_t w, float s_old, const Kv8Div &D) {
-  float x[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = __fmul_rn((float)((int)((w >> (8 * i)) & 255u) - 128), s_old);
-  return kv8_codes(x, D);
+  const float2 a = __half22float2(bits_half2(kv8_pair<0>(w))), b = __half22float2(bits_half2(kv8_pair<1>(w)));
+  const uint64_t s = f32x2(s_old, s_old);
+  return kv8_codes<TINY>(mul_f32x2(f32x2(a.x, a.y), s), mul_f32x2(f32x2(b.x, b.y), s), D);
 }
 
-__device__ __forceinline__ void unpack_bf16(uint32_t w, float &lo, float &hi) {
-  lo = __uint_as_float(w << 16);
-  hi = __uint_as_float(w & 0xffff0000u);
+__device__ __forceinline__ uint64_t bf16_f32x2(uint32_t w) {
+  return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t word4(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// 32 bytes of input, in one load where its rows are 32-byte aligned (a lane's
+// quarter of a 128-byte line: half the requests).
+__device__ __forceinline__ void load32(const void *p, bool wide, uint4 &a, uint4 &b) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+  } else {
+    a = reinterpret_cast<const uint4 *>(p)[0];
+    b = reinterpret_cast<const uint4 *>(p)[1];
+  }
 }
 // Largest magnitudes of a packed pair of bf16, kept apart in the two halves.
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
@@ -94,50 +119,104 @@ struct Kv8Append {
 
 // Where a warp's tile lies and which of its rows are new.
 struct Kv8Item {
-  uint8_t *tile;
+  int blk;         // its block (any number: checked before the tile is touched)
+  int row;         // first row of the tile in its block
   long long row0;  // k/v row of the tile's position 0 (may lie ahead of the chunk's first)
   int r0, r1;      // new rows [r0, r1); rows below r0 are there already
   long long p;     // position of the tile's row 0
 };
+// The tile, or null where its block is none of the pool's.
+__device__ __forceinline__ uint8_t *tile_of(const Kv8Append &A, const Kv8Item &I, int h) {
+  return I.blk < 0 || I.blk >= A.dst.num_blocks ? nullptr : A.dst.data + kv8_tile(A.dst, I.blk, h, I.row);
+}
+
+// K rows of a lane under their scale: rows gr + 8 e, dims 16t .. of the groups of 64 that are not rotated, and 8t .. and
+// 32 + 8t .. of the rotary one.
+template <bool TINY>
+__device__ __forceinline__ void put_k(const uint64_t (&x0)[2][8], const uint4 (&raw)[2][2][2], const bool (&is_new)[2],
+                                      bool grow, float s_old, const Kv8Div &D, const Kv8Item &I, uint8_t *tile, int gr, int lane) {
+  const int t = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint8_t *at = tile + e * 512 + lane * 16;
+    if (is_new[e]) {
+      uint8_t *rot = tile + e * 512 + gr * 64 + 8 * t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint2 *>(rot + 32 * i) = make_uint2(kv8_codes<TINY>(x0[e][4 * i], x0[e][4 * i + 1], D),
+                                                              kv8_codes<TINY>(x0[e][4 * i + 2], x0[e][4 * i + 3], D));
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // four dims each
+          const uint4 &w = raw[e][g][j >> 1];
+          c[j] = kv8_codes<TINY>(bf16_f32x2(j & 1 ? w.z : w.x), bf16_f32x2(j & 1 ? w.w : w.y), D);
+        }
+        *reinterpret_cast<uint4 *>(at + 1024 + 1024 * g) = make_uint4(c[0], c[1], c[2], c[3]);
+      }
+    } else if (grow && gr + 8 * e < I.r0) {
+      uint4 w[3];
+#pragma unroll
+      for (int g = 0; g < 3; ++g) w[g] = *reinterpret_cast<const uint4 *>(at + 1024 * g);
+#pragma unroll
+      for (int g = 0; g < 3; ++g)
+        *reinterpret_cast<uint4 *>(at + 1024 * g) =
+            make_uint4(kv8_again<TINY>(w[g].x, s_old, D), kv8_again<TINY>(w[g].y, s_old, D),
+                       kv8_again<TINY>(w[g].z, s_old, D), kv8_again<TINY>(w[g].w, s_old, D));
+    }
+  }
+}
 
 __device__ __forceinline__ void kv8_append_k(const Kv8Append &A, const Kv8Item &I, int h, int lane) {
   const int t = lane & 3, gr = lane >> 2, H = A.dst.hkv;
-  // rows gr and gr + 8, dims 16t .. 16t + 15 of each group of 64; and of the rotary group the other half of the pairs
-  uint4 raw[2][3][2], mate[2][2];
-  float4 cs[2][8];
+  const bool wide = (reinterpret_cast<uintptr_t>(A.k) & 31u) == 0, wide_t = (reinterpret_cast<uintptr_t>(A.table) & 31u) == 0;
+  uint4 raw[2][2][2];  // rows gr + 8 e, dims 16t .. 16t + 15 of the groups of 64 that are not rotated
+  uint64_t x0[2][8];   // dims 8t .. and 32 + 8t .. of the rotary one, in pairs
+  uint4 a[2], b[2], cs[2][4];
   bool is_new[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = gr + 8 * e;
     is_new[e] = r >= I.r0 && r < I.r1;
-    const uint16_t *src = A.k + ((I.row0 + r) * H + h) * DQK + 16 * t;
-    const float *tr = A.table + (I.p + r) * 64 + 32 * (t & 1);
+    a[e] = b[e] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int g = 0; g < 3; ++g)
+    for (int i = 0; i < 4; ++i) cs[e][i] = raw[e][i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+    if (is_new[e]) {
+      const uint16_t *src = A.k + ((I.row0 + r) * H + h) * DQK;
+      const float *tr = A.table + (I.p + r) * 64 + 16 * t;
+      a[e] = *reinterpret_cast<const uint4 *>(src + 8 * t);
+      b[e] = *reinterpret_cast<const uint4 *>(src + 32 + 8 * t);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) raw[e][g][i] = is_new[e] ? reinterpret_cast<const uint4 *>(src + 64 * g)[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      mate[e][i] = is_new[e] ? reinterpret_cast<const uint4 *>(src + (t < 2 ? 32 : -32))[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[e][i] = is_new[e] ? reinterpret_cast<const float4 *>(tr)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < 2; ++i) {
+        load32(tr + 8 * i, wide_t, cs[e][2 * i], cs[e][2 * i + 1]);
+        load32(src + 64 + 64 * i + 16 * t, wide, raw[e][i][0], raw[e][i][1]);
+      }
+    }
   }
-  const uint4 tail = I.r0 > 0 ? *reinterpret_cast<const uint4 *>(I.tile + KV8_OFF_TAIL) : make_uint4(0, 0, 0, 0);
-  // the rotary group: products and sum rounded one by one, so the result does not hang on contraction
-  float x0[2][16];
-  const float sign = t < 2 ? -1.f : 1.f;  // a c - b s, or b c + a s
+  uint8_t *const tile = tile_of(A, I, h);
+  if (!tile) return;
+  uint4 tail = make_uint4(0, 0, 0, 0);
+  if (I.r0 > 0) {
+    tail = *reinterpret_cast<const uint4 *>(tile + KV8_OFF_TAIL);
+    if (lane < 24) prefetch_line(tile + 128 * lane);  // rows ahead in the tile, in case the scale grows
+  }
+  // the rotary group: products and sums rounded one by one, so the result does not hang on contraction
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 &w4 = raw[e][0][i >> 2], &m4 = mate[e][i >> 2];
-      const uint32_t w = (i & 3) == 0 ? w4.x : (i & 3) == 1 ? w4.y : (i & 3) == 2 ? w4.z : w4.w;
-      const uint32_t m = (i & 3) == 0 ? m4.x : (i & 3) == 1 ? m4.y : (i & 3) == 2 ? m4.z : m4.w;
-      float a, b, c, d;
-      unpack_bf16(w, a, b);
-      unpack_bf16(m, c, d);
-      x0[e][2 * i] = __fadd_rn(__fmul_rn(a, cs[e][i].x), sign * __fmul_rn(c, cs[e][i].y));
-      x0[e][2 * i + 1] = __fadd_rn(__fmul_rn(b, cs[e][i].z), sign * __fmul_rn(d, cs[e][i].w));
+    for (int i = 0; i < 4; ++i) {  // two pairs (d, d + 32)
+      float x[2], y[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t wa = word4(a[e], i), wb = word4(b[e], i);
+        const float va = __uint_as_float(u ? wa & 0xffff0000u : wa << 16), vb = __uint_as_float(u ? wb & 0xffff0000u : wb << 16);
+        const float c = __uint_as_float(u ? cs[e][i].z : cs[e][i].x), sn = __uint_as_float(u ? cs[e][i].w : cs[e][i].y);
+        x[u] = __fsub_rn(__fmul_rn(va, c), __fmul_rn(vb, sn));
+        y[u] = __fadd_rn(__fmul_rn(vb, c), __fmul_rn(va, sn));
+      }
+      x0[e][i] = f32x2(x[0], x[1]);
+      x0[e][4 + i] = f32x2(y[0], y[1]);
     }
   // a row's largest magnitude (as bits: infinities and NaN above all), the rows that are not finite, the tile's largest
   uint32_t top = 0, bad = 0;
@@ -145,72 +224,81 @@ __device__ __forceinline__ void kv8_append_k(const Kv8Append &A, const Kv8Item &
   for (int e = 0; e < 2; ++e) {
     uint32_t m2 = 0, m = 0;
 #pragma unroll
-    for (int g = 1; g < 3; ++g)
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint4 &w = raw[e][g][i];
         m2 = abs_max2(abs_max2(abs_max2(abs_max2(m2, w.x), w.y), w.z), w.w);
       }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x0[e][i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) {
+      float x, y;
+      f32x2_split(x0[e][i], x, y);
+      m = max(max(m, __float_as_uint(x) & 0x7fffffffu), __float_as_uint(y) & 0x7fffffffu);
+    }
     m = max(m, max(m2 << 16, m2 & 0xffff0000u));
     m = max(m, __shfl_xor_sync(FULLW, m, 1));
     m = max(m, __shfl_xor_sync(FULLW, m, 2));
     const bool odd = m >= 0x7f800000u;
     const unsigned rows = __ballot_sync(FULLW, odd && t == 0);  // bit 4 gr
+    if (rows) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= (rows >> (4 * i) & 1u) << (i + 8 * e);
-    if (odd) {
+      for (int i = 0; i < 8; ++i) bad |= (rows >> (4 * i) & 1u) << (i + 8 * e);
+      if (odd) {
+        m = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x0[e][i] = 0.f;
+        for (int i = 0; i < 8; ++i) x0[e][i] = 0;
 #pragma unroll
-      for (int g = 1; g < 3; ++g) raw[e][g][0] = raw[e][g][1] = make_uint4(0, 0, 0, 0);
-    } else {
-      top = max(top, m);
+        for (int g = 0; g < 2; ++g) raw[e][g][0] = raw[e][g][1] = make_uint4(0, 0, 0, 0);
+      }
     }
+    top = max(top, m);
   }
   top = __reduce_max_sync(FULLW, top);
-  const float s_old = __uint_as_float(tail.x), s_need = kv8_scale(abs_bits(top));
+  const float s_old = __uint_as_float(tail.x), s_need = kv8_scale(__uint_as_float(top));
   const bool grow = I.r0 > 0 && s_need > s_old;
   const float s = I.r0 > 0 && !grow ? s_old : s_need;
   const Kv8Div D = kv8_div(s);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = gr + 8 * e;
-    uint8_t *at = I.tile + e * 512 + lane * 16;
-    if (is_new[e]) {
-#pragma unroll
-      for (int g = 0; g < 3; ++g) {
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // four dims each
-          float x[4];
-          if (g == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = x0[e][4 * j + i];
-          } else {
-            const uint4 &w = raw[e][g][j >> 1];
-            unpack_bf16(j & 1 ? w.z : w.x, x[0], x[1]);
-            unpack_bf16(j & 1 ? w.w : w.y, x[2], x[3]);
-          }
-          c[j] = kv8_codes(x, D);
-        }
-        *reinterpret_cast<uint4 *>(at + 1024 * g) = make_uint4(c[0], c[1], c[2], c[3]);
-      }
-    } else if (grow && r < I.r0) {
-      uint4 w[3];
-#pragma unroll
-      for (int g = 0; g < 3; ++g) w[g] = *reinterpret_cast<const uint4 *>(at + 1024 * g);
-#pragma unroll
-      for (int g = 0; g < 3; ++g)
-        *reinterpret_cast<uint4 *>(at + 1024 * g) = make_uint4(kv8_again(w[g].x, s_old, D), kv8_again(w[g].y, s_old, D),
-                                                               kv8_again(w[g].z, s_old, D), kv8_again(w[g].w, s_old, D));
-    }
-  }
+  if (D.tiny) put_k<true>(x0, raw, is_new, grow, s_old, D, I, tile, gr, lane);
+  else put_k<false>(x0, raw, is_new, grow, s_old, D, I, tile, gr, lane);
   if (lane == 0) {
-    *reinterpret_cast<float *>(I.tile + KV8_OFF_TAIL) = s;
-    *reinterpret_cast<uint16_t *>(I.tile + KV8_OFF_TAIL + 8) = (uint16_t)((tail.z & ((1u << I.r0) - 1u)) | bad);
-    *reinterpret_cast<uint32_t *>(I.tile + KV8_OFF_TAIL + 12) = 0u;
+    *reinterpret_cast<float *>(tile + KV8_OFF_TAIL) = s;
+    *reinterpret_cast<uint16_t *>(tile + KV8_OFF_TAIL + 8) = (uint16_t)((tail.z & ((1u << I.r0) - 1u)) | bad);
+    *reinterpret_cast<uint32_t *>(tile + KV8_OFF_TAIL + 12) = 0u;
+  }
+}
+
+// V of a lane under its scale: positions 2t, 2t + 1, 2t + 8, 2t + 9, dims 4 gr .. of each group of 32.
+template <bool TINY>
+__device__ __forceinline__ void put_v(const uint2 (&raw)[4][4], const uint4 (&old)[4], float vscale, bool grow, float s_old,
+                                      const Kv8Div &D, const Kv8Item &I, uint8_t *tile, int t, int lane) {
+  const uint64_t vs = f32x2(vscale, vscale);
+  uint32_t keep = 0;  // bytes of positions that are there already
+#pragma unroll
+  for (int j = 0; j < 4; ++j) keep |= 2 * t + (j & 1) + 8 * (j >> 1) < I.r0 ? 0xffu << (8 * j) : 0u;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t c[4];  // of position j: four dims
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = kv8_codes<TINY>(mul_f32x2(bf16_f32x2(raw[j][g].x), vs), mul_f32x2(bf16_f32x2(raw[j][g].y), vs), D);
+    // to a word per dim: positions in its bytes
+    uint32_t w[4];
+    const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);  // dims 0, 1 of both
+    const uint32_t e = __byte_perm(c[0], c[1], 0x7362), f = __byte_perm(c[2], c[3], 0x7362);  // dims 2, 3
+    w[0] = __byte_perm(a, b, 0x5410);
+    w[1] = __byte_perm(a, b, 0x7632);
+    w[2] = __byte_perm(e, f, 0x5410);
+    w[3] = __byte_perm(e, f, 0x7632);
+    if (I.r0 > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o = word4(old[g], i);
+        if (grow) o = kv8_again<TINY>(o, s_old, D);
+        w[i] = (o & keep) | (w[i] & ~keep);
+      }
+    }
+    *reinterpret_cast<uint4 *>(tile + KV8_OFF_V + 512 * g + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -228,15 +316,15 @@ __device__ __forceinline__ void kv8_append_v(const Kv8Append &A, const Kv8Item &
 #pragma unroll
     for (int g = 0; g < 4; ++g) raw[j][g] = is_new[j] ? *reinterpret_cast<const uint2 *>(src + 32 * g) : make_uint2(0, 0);
   }
-  const bool any_old = I.r0 > 0;
+  uint8_t *const tile = tile_of(A, I, h);
+  if (!tile) return;
   uint4 tail = make_uint4(0, 0, 0, 0);
-  if (any_old) {
-    tail = *reinterpret_cast<const uint4 *>(I.tile + KV8_OFF_TAIL);
+  if (I.r0 > 0) {
+    tail = *reinterpret_cast<const uint4 *>(tile + KV8_OFF_TAIL);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) old[g] = *reinterpret_cast<const uint4 *>(I.tile + KV8_OFF_V + 512 * g + 16 * lane);
+    for (int g = 0; g < 4; ++g) old[g] = *reinterpret_cast<const uint4 *>(tile + KV8_OFF_V + 512 * g + 16 * lane);
   }
   uint32_t top = 0, bad = 0;
-  bool odd[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t m2 = 0;
@@ -247,60 +335,34 @@ __device__ __forceinline__ void kv8_append_v(const Kv8Append &A, const Kv8Item &
     m = max(m, __shfl_xor_sync(FULLW, m, 8));
     m = max(m, __shfl_xor_sync(FULLW, m, 16));
     // the largest of the scaled values is the largest's product (a NaN stays one)
-    const uint32_t y = __float_as_uint(__fmul_rn(__uint_as_float(m), A.vscale)) & 0x7fffffffu;
-    odd[j] = m >= 0x7f800000u || y >= 0x7f800000u;
-    if (is_new[j]) {
-      if (!odd[j]) top = max(top, y);
-    }
-    const unsigned rows = __ballot_sync(FULLW, is_new[j] && odd[j] && gr == 0);  // bits t
+    uint32_t y = __float_as_uint(__fmul_rn(__uint_as_float(m), A.vscale)) & 0x7fffffffu;
+    const bool odd = is_new[j] && y >= 0x7f800000u;
+    const unsigned rows = __ballot_sync(FULLW, odd && gr == 0);  // bits t
+    if (rows) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= (rows >> i & 1u) << (2 * i + (j & 1) + 8 * (j >> 1));
-  }
-  top = __reduce_max_sync(FULLW, top);
-  const float s_old = __uint_as_float(tail.y), s_need = kv8_scale(abs_bits(top));
-  const bool grow = any_old && s_need > s_old;
-  const float s = any_old && !grow ? s_old : s_need;
-  const Kv8Div D = kv8_div(s);
+      for (int i = 0; i < 4; ++i) bad |= (rows >> i & 1u) << (2 * i + (j & 1) + 8 * (j >> 1));
+      if (odd) {
+        y = 0;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t c[4];  // of position j: four dims
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x[4];
-      unpack_bf16(raw[j][g].x, x[0], x[1]);
-      unpack_bf16(raw[j][g].y, x[2], x[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = odd[j] ? 0.f : __fmul_rn(x[i], A.vscale);
-      c[j] = kv8_codes(x, D);
-    }
-    // to a word per dim: positions in its bytes
-    uint32_t w[4];
-    const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);  // dims 0, 1 of both
-    const uint32_t e = __byte_perm(c[0], c[1], 0x7362), f = __byte_perm(c[2], c[3], 0x7362);  // dims 2, 3
-    w[0] = __byte_perm(a, b, 0x5410);
-    w[1] = __byte_perm(a, b, 0x7632);
-    w[2] = __byte_perm(e, f, 0x5410);
-    w[3] = __byte_perm(e, f, 0x7632);
-    if (any_old) {
-      uint32_t keep = 0;  // bytes of positions that are there already
-#pragma unroll
-      for (int j = 0; j < 4; ++j) keep |= 2 * t + (j & 1) + 8 * (j >> 1) < I.r0 ? 0xffu << (8 * j) : 0u;
-      uint32_t o[4] = {old[g].x, old[g].y, old[g].z, old[g].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (grow) o[i] = kv8_again(o[i], s_old, D);
-        w[i] = (o[i] & keep) | (w[i] & ~keep);
+        for (int g = 0; g < 4; ++g) raw[j][g] = make_uint2(0, 0);
       }
     }
-    *reinterpret_cast<uint4 *>(I.tile + KV8_OFF_V + 512 * g + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    top = max(top, is_new[j] ? y : 0u);
   }
+  top = __reduce_max_sync(FULLW, top);
+  const float s_old = __uint_as_float(tail.y), s_need = kv8_scale(__uint_as_float(top));
+  const bool grow = I.r0 > 0 && s_need > s_old;
+  const float s = I.r0 > 0 && !grow ? s_old : s_need;
+  const Kv8Div D = kv8_div(s);
+  if (D.tiny) put_v<true>(raw, old, A.vscale, grow, s_old, D, I, tile, t, lane);
+  else put_v<false>(raw, old, A.vscale, grow, s_old, D, I, tile, t, lane);
   if (lane == 0) {
-    *reinterpret_cast<float *>(I.tile + KV8_OFF_TAIL + 4) = s;
-    *reinterpret_cast<uint16_t *>(I.tile + KV8_OFF_TAIL + 10) = (uint16_t)(((tail.z >> 16) & ((1u << I.r0) - 1u)) | bad);
+    *reinterpret_cast<float *>(tile + KV8_OFF_TAIL + 4) = s;
+    *reinterpret_cast<uint16_t *>(tile + KV8_OFF_TAIL + 10) = (uint16_t)(((tail.z >> 16) & ((1u << I.r0) - 1u)) | bad);
   }
 }
 
-__global__ void __launch_bounds__(K8A_WARPS * 32) kv8_append_kernel(Kv8Append A) {
+__global__ void __launch_bounds__(K8A_WARPS * 32, 5) kv8_append_kernel(Kv8Append A) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, per = 2 * A.dst.hkv;
@@ -309,9 +371,9 @@ __global__ void __launch_bounds__(K8A_WARPS * 32) kv8_append_kernel(Kv8Append A)
   const long long unit = w / per;
   const int part = (int)(w - unit * per), h = part >> 1;
   const bool say = lane == 0 && part == 0;
-  const int i = kv8_chunk(A.cu_rows, A.n, unit);
-  const int c0 = A.cu_rows[i], c1 = A.cu_rows[i + 1], s = A.seqs[i];
-  const long long a = A.P0[i];
+  const Kv8Chunk C = kv8_chunk(A.cu_rows, A.P0, A.seqs, A.n, unit);
+  const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
+  const long long a = C.pos;
   if (c0 < 0 || c1 < c0 || c1 > A.T) {
     if (say) flag(A.status, ST_BAD_ROWS);
     return;
@@ -333,13 +395,10 @@ __global__ void __launch_bounds__(K8A_WARPS * 32) kv8_append_kernel(Kv8Append A)
   I.r1 = (int)min(end - I.p, 16LL);
   I.row0 = c0 + (I.p - a);
   const unsigned tile = (unsigned)(I.p >> 4), per_block = (unsigned)A.dst.block_size >> 4, bi = tile / per_block;
-  const int blk = A.dst.block_table[(long long)s * A.dst.max_blocks + bi];
-  if (blk < 0 || blk >= A.dst.num_blocks) {
-    if (say) flag(A.status, ST_BAD_BLOCK);
-    return;
-  }
-  I.tile = A.dst.data + kv8_tile(A.dst, blk, h, (int)(16 * (tile - bi * per_block)));
+  I.blk = A.dst.block_table[(long long)s * A.dst.max_blocks + bi];
+  I.row = (int)(16 * (tile - bi * per_block));
   if (part & 1) kv8_append_v(A, I, h, lane); else kv8_append_k(A, I, h, lane);
+  if (say && (I.blk < 0 || I.blk >= A.dst.num_blocks)) flag(A.status, ST_BAD_BLOCK);
 }
 
 }  // namespace

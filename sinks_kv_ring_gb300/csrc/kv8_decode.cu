@@ -27,6 +27,7 @@
 // copies (one copy brings codes and scales), with no barrier between warps
 // inside a piece; 12 warps an SM, three CTAs, hold the sums in registers.
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "line.cuh"
@@ -37,9 +38,11 @@ namespace {
 
 constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K8_WARPS = 4;
-constexpr int K8_CTAS = 3;           // per SM
+constexpr int K8_CTAS = 2;           // per SM
 constexpr int K8_UNIT = 16;          // keys: one tile
-constexpr int K8_STAGES = 3;
+constexpr int K8_STAGES = 4;
+constexpr int K8_MT = 2;
+constexpr int K8_ROWS = 16 * K8_MT;  // query rows of a part: those of up to 4 batch rows of one sequence
 constexpr float K8_PBIAS = 11.f;     // weights are 2^11 where they equal the reference
 constexpr float K8_SLACK = 4.f;      // how far a score or weight may pass its reference
 constexpr float K8_NONE = -1e30f;    // a reference before the first keys
@@ -49,17 +52,24 @@ constexpr float K8_NONE = -1e30f;    // a reference before the first keys
 // sum at most, a sixteenth of the output's half step.
 struct K8Line {
   static constexpr int UNIT = K8_UNIT, ROW = 24, MIN = K8_WARPS, MOST = 2048 * K8_WARPS, CTAS = K8_CTAS;
+  static constexpr bool SHARE = true;
 };
-// shared memory: query operands (12 steps), row factors, barriers, abort flag, plan, stages
-constexpr int K8_OFF_ROW = 12 * 512;
-constexpr int K8_OFF_BAR = K8_OFF_ROW + 64;
+// Batch rows that may go together: as many as their heads fit in K8_ROWS query rows, up to the four of a draft.
+int rows_together(int G) { return K8_ROWS / G >= 4 ? 4 : K8_ROWS / G >= 2 ? 2 : 1; }
+// shared memory: query operands (12 steps, twice), row factors and key counts, barriers, abort flag, plan, stages
+constexpr int K8_OFF_ROW = K8_MT * 12 * 512;
+constexpr int K8_OFF_KEYS = K8_OFF_ROW + 4 * K8_ROWS;
+constexpr int K8_OFF_BAR = K8_OFF_KEYS + 4 * K8_ROWS;
 constexpr int K8_OFF_STALL = K8_OFF_BAR + 8 * K8_WARPS * K8_STAGES;  // a barrier that nothing completes (test hook)
 constexpr int K8_OFF_ABORT = K8_OFF_STALL + 8;
 constexpr int K8_OFF_L = (K8_OFF_ABORT + 4 + 7) / 8 * 8;
 constexpr int K8_OFF_PLAN = (K8_OFF_L + 8 + 15) / 16 * 16;
-constexpr int K8_OFF_STAGE = (K8_OFF_PLAN + (LINE_INLINE_MAX + 2) * 8 + 127) / 128 * 128;
+constexpr int K8_OFF_EARLY = K8_OFF_PLAN + (LINE_INLINE_MAX + 2) * 8;  // positions and ids of a batch of up to a row a thread
+constexpr int K8_OFF_INFO = K8_OFF_EARLY + K8_WARPS * 32 * 12;
+constexpr int K8_OFF_STAGE = (K8_OFF_INFO + LINE_INLINE_MAX + 127) / 128 * 128;
 constexpr int K8_SMEM = K8_OFF_STAGE + K8_WARPS * K8_STAGES * KV8_TILE;
-static_assert(K8_WARPS * K8_STAGES * KV8_TILE >= (K8_WARPS * 16 * (MO_STRIDE + 2) + K8_WARPS * 16 + 32 + 16 * DV) * 4,
+static_assert(K8_WARPS * K8_STAGES * KV8_TILE >=
+                  (K8_WARPS * 16 * (MO_STRIDE + 2) + K8_WARPS * 16 + K8_ROWS * (2 + DV)) * 4,
               "merge area");
 static_assert(K8_CTAS * (K8_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
 
@@ -85,22 +95,20 @@ __device__ __forceinline__ float lg2(float x) {
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return half2_bits(__floats2half2_rn(lo, hi)); }
 
-// The query operands of one row: thread (head r, eighth c) rotates and scales 24
-// dims of head r, and the head's eight threads share its power of two.  Operand
-// order: step 4g + w holds, for lane 4a + t, dims 64 g + 16 t + 4 w + {0, 1}
-// (registers 0, 1: heads a and a + 8) and + {2, 3} (registers 2, 3), as word w of
-// a lane's K codes has them.
+// The query operands of 16 of a part's rows (row r is head r % G of batch row r / G
+// of the part): thread (row, eighth c) rotates and scales 24 dims of its row, and
+// the row's eight threads share its power of two.  Operand order: step 4g + w
+// holds, for lane 4a + t, dims 64 g + 16 t + 4 w + {0, 1} (registers 0, 1: rows a
+// and a + 8) and + {2, 3} (registers 2, 3), as word w of a lane's K codes has them.
 struct K8Query {
   uint2 lo, hi;
   uint4 g1, g2;
   float4 t0, t1;
 };
-__device__ __forceinline__ K8Query kv8_query_load(const uint16_t *__restrict__ qh, int G,
-                                                  const float *__restrict__ cs_row, int tid) {
-  const int r = tid >> 3, c = tid & 7;
+__device__ __forceinline__ K8Query kv8_query_load(const uint16_t *__restrict__ qr, const float *__restrict__ cs_row, int c,
+                                                  bool have) {
   K8Query Q = {};
-  if (r < G) {
-    const uint16_t *qr = qh + r * DQK;
+  if (have) {
     Q.lo = *reinterpret_cast<const uint2 *>(qr + 4 * c);
     Q.hi = *reinterpret_cast<const uint2 *>(qr + 32 + 4 * c);
     Q.g1 = *reinterpret_cast<const uint4 *>(qr + 64 + 8 * c);
@@ -110,12 +118,11 @@ __device__ __forceinline__ K8Query kv8_query_load(const uint16_t *__restrict__ q
   }
   return Q;
 }
-__device__ __forceinline__ void kv8_query(const K8Query &Q, int G, float scale_log2, uint8_t *smem, int tid) {
+// (Q is all zeros for a row that is not there); ops, factor: the 16 rows' operands and row factors
+__device__ __forceinline__ void kv8_query(const K8Query &Q, float scale_log2, uint8_t *ops, float *factor, int tid) {
   const int r = tid >> 3, c = tid & 7;
   float y[24];
-#pragma unroll
-  for (int i = 0; i < 24; ++i) y[i] = 0.f;
-  if (r < G) {
+  {
     const float cs[8] = {Q.t0.x, Q.t0.y, Q.t0.z, Q.t0.w, Q.t1.x, Q.t1.y, Q.t1.z, Q.t1.w};
     const uint16_t *a = reinterpret_cast<const uint16_t *>(&Q.lo), *b = reinterpret_cast<const uint16_t *>(&Q.hi);
 #pragma unroll
@@ -147,13 +154,12 @@ __device__ __forceinline__ void kv8_query(const K8Query &Q, int G, float scale_l
     const int g = i >> 3;
     const int d = g == 0 ? ((i & 4) ? 32 + 4 * c : 4 * c) : 8 * c + (i & 7);
     const int at = ((g * 4 + (d >> 2 & 3)) * 32 + (r & 7) * 4 + (d >> 4)) * 16 + (r >> 3) * 4;
-    *reinterpret_cast<uint32_t *>(smem + at) = pack_h2(y[i] * up * dn, y[i + 1] * up * dn);
-    *reinterpret_cast<uint32_t *>(smem + at + 8) = pack_h2(y[i + 2] * up * dn, y[i + 3] * up * dn);
+    *reinterpret_cast<uint32_t *>(ops + at) = pack_h2(y[i] * up * dn, y[i + 1] * up * dn);
+    *reinterpret_cast<uint32_t *>(ops + at + 8) = pack_h2(y[i + 2] * up * dn, y[i + 3] * up * dn);
   }
   // a score's unit per K scale: the sums hold (y . u) 2^a.  A query that is not finite has none: its row is NaN
   if (c == 0)
-    *reinterpret_cast<float *>(smem + K8_OFF_ROW + 4 * r) =
-        mx >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)min(max(127 - a, 1), 254) << 23);
+    factor[r] = mx >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)min(max(127 - a, 1), 254) << 23);
 }
 
 struct K8Args : LineArgs {
@@ -164,14 +170,18 @@ struct K8Args : LineArgs {
   unsigned *status;
   unsigned long long stall_ns;  // test hook: warp 0's first wait is on a barrier that nothing completes (0: no stall)
   int cs;                       // DIRECT: CTAs of a row
+  uint32_t g_mul;               // ceil(2^16 / G): r / G = r * g_mul >> 16 (r < 32)
   unsigned long long tpb_mul;   // ceil(2^36 / tiles per block): tile / tiles per block = tile * tpb_mul >> 36 (tile < 2^28)
 };
 
-// SMALL: groups of up to 8 query heads.  The keys are then the 16 rows of the
-// products and the heads their 8 columns (scores K Q^T, sums V^T P^T): half the
-// products, and half the registers for the sums.  The codes' operands are the
-// same registers; a weight's row and column change places between the two
-// products by an 8 x 8 transposition (movmatrix).
+// A part's query rows are the G heads of a batch row, or of up to rmax of them that
+// share a sequence.  Up to 8 rows: the keys are the 16 rows of the products and the
+// query rows their 8 columns (scores K Q^T, sums V^T P^T): half the products of the
+// other form, and a quarter of the registers for the sums; the codes' operands are
+// the same registers, and a weight's row and column change places between the two
+// products by an 8 x 8 transposition (movmatrix).  Up to 16, or 32: the query rows
+// are the rows of one, or two, products, and a tile's codes are converted once for
+// both.
 //
 // FORM: the work line, a share a CTA (K8_LINE) or several (K8_TURNS); or DIRECT:
 // short contexts of few rows, where a launch costs more than the work.  A cluster
@@ -179,7 +189,7 @@ struct K8Args : LineArgs {
 // merge their parts through each other's shared memory: one launch, no plan and
 // no workspace.
 enum K8Form { K8_LINE, K8_TURNS, K8_DIRECT };
-template <bool SMALL, K8Form FORM>
+template <K8Form FORM>
 __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Args A) {
   constexpr bool DIRECT = FORM == K8_DIRECT, TURNS = FORM == K8_TURNS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -204,11 +214,13 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
   // wait it stands if they read the same, else it is made again.
   const bool early = !DIRECT && A.B <= K8_WARPS * 32;
   const int64_t *prefix = A.B <= LINE_INLINE_MAX ? sPrefix : A.plan + LINE_PLAN;
+  const uint8_t *info = A.B <= LINE_INLINE_MAX ? smem + K8_OFF_INFO : reinterpret_cast<uint8_t *>(A.plan + LINE_PLAN + A.B + 1);
   long long x = 0, line_end = 0, early_p = 0;
   int b = 0, kv = 0, lo = 0, hi = 0, early_s = 0;
   bool ready = DIRECT;  // b, kv, lo, hi hold the next part
   auto plan = [&](auto get, unsigned *status) {
-    return line_plan<K8Line, K8_WARPS * 32>(get, A.B, hkv, A.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status);
+    return line_plan<K8Line, K8_WARPS * 32>(get, A.B, hkv, A.num_seqs, A.max_pos, A.max_ctx, gridDim.x, sPrefix, status,
+                                               A.rmax, smem + K8_OFF_INFO);
   };
   long long *const sL = reinterpret_cast<long long *>(smem + K8_OFF_L);  // TURNS: L, for the shares after the first
   int turn = 0;                                                          // and the shares done
@@ -219,10 +231,12 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
     if (TURNS && tid == 0) *sL = L;  // (a barrier follows each call)
     if (ready) line_part<K8Line>(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
   };
+  int64_t *const sPos = reinterpret_cast<int64_t *>(smem + K8_OFF_EARLY);
+  int32_t *const sSeq = reinterpret_cast<int32_t *>(smem + K8_OFF_EARLY + K8_WARPS * 32 * 8);
   if (early) {
     if (tid < A.B) {
-      early_p = ld_early_s64(A.pos + tid);
-      early_s = ld_early_s32(A.seq + tid);
+      sPos[tid] = early_p = ld_early_s64(A.pos + tid);
+      sSeq[tid] = early_s = ld_early_s32(A.seq + tid);
     }
     share(plan([&](int, long long &p, int &s) { p = early_p, s = early_s; }, nullptr));
   }
@@ -243,6 +257,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
     if (TURNS) __syncthreads();  // *sL
   }
 
+  int *const sKeys = reinterpret_cast<int *>(smem + K8_OFF_KEYS);
   const int tpb = A.pool.block_size >> 4;
   const int t = lane & 3, gr = lane >> 2;
   uint32_t seen = 0;  // this warp's loads waited for so far: stage seen % K8_STAGES, phase (seen / K8_STAGES) & 1
@@ -259,24 +274,39 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       line_end = min(x + L, total);
       ++turn;
     }
-    int w = 0, key_lo, key_hi;
-    long long p;
+    int w = 0, key_lo, key_hi, rows;  // rows: of the batch, from b on
+    long long at[4], top = -1;        // their positions, and the largest
+    auto positions = [&]() {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        at[c] = c < rows ? (same ? sPos[b + c] : A.pos[b + c]) : -1;
+        top = max(top, at[c]);
+      }
+    };
     if (DIRECT) {
       ready = false;
       const int row = (int)blockIdx.x / A.cs, rank = (int)blockIdx.x - row * A.cs;
       b = row / hkv;
       kv = row - b * hkv;
-      p = A.pos[b];
-      const int units = line_units<K8Line>(p, A.seq[b], A.num_seqs, A.max_pos, A.max_ctx,
-                                           kv == 0 && rank == 0 && tid == 0 ? A.status : nullptr);
-      if (units == 0) {  // (so for the whole cluster)
+      // the rows that go together (as the plan has it), by every warp
+      const int base = b & ~(A.rmax - 1), in = b - base;
+      long long pl = -1;
+      int sl = -1;
+      if (lane < A.rmax && base + lane < A.B) pl = A.pos[base + lane], sl = A.seq[base + lane];
+      const bool say = kv == 0 && rank == 0 && warp == 0 && lane == in;
+      const int mine = line_units<K8Line>(pl, sl, A.num_seqs, A.max_pos, A.max_ctx, say ? A.status : nullptr);
+      const uint8_t told = line_info(line_joined(mine > 0, sl, lane, A.rmax), in);
+      if (__shfl_sync(FULLW, mine, in) == 0) {  // (so for the whole cluster)
         uint16_t *o = A.out + ((long long)b * A.hq + (long long)kv * G) * DV;
         for (int i = rank * (K8_WARPS * 32) + tid; i < G * DV; i += A.cs * (K8_WARPS * 32)) o[i] = 0;
         return;
       }
-      const int each = (units + A.cs - 1) / A.cs;
+      if (line_lead(told)) return;  // (the whole cluster: the row's leader has one)
+      rows = line_rows(told);
+      positions();
+      const int units = (int)((top + K8_UNIT) / K8_UNIT), each = (units + A.cs - 1) / A.cs;
       key_lo = min(rank * each, units) * K8_UNIT;
-      key_hi = (int)min((long long)min((rank + 1) * each, units) * K8_UNIT, p + 1);
+      key_hi = (int)min((long long)min((rank + 1) * each, units) * K8_UNIT, top + 1);
       if (key_hi < key_lo) key_hi = key_lo;
     } else {
       if (!ready) line_part<K8Line>(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
@@ -284,15 +314,27 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       if (hi <= 0) continue;  // set-up alone: no piece
       w = (int)blockIdx.x + b * hkv + kv;
       if (TURNS) w += turn * (int)gridDim.x;
-      p = A.pos[b];
+      rows = line_rows(info[b]);
+      positions();
       key_lo = lo * K8_UNIT;
-      key_hi = (int)min((long long)hi * K8_UNIT, p + 1);
+      key_hi = (int)min((long long)hi * K8_UNIT, top + 1);
     }
-    const int s = A.seq[b];  // (a row that gets here has a valid position and id)
+    const int s = same ? sSeq[b] : A.seq[b];  // (a row that gets here has a valid position and id)
     const int nunit = (key_hi - key_lo + K8_UNIT - 1) / K8_UNIT;
     const int my_n = nunit > warp ? (nunit - warp + K8_WARPS - 1) / K8_WARPS : 0;
     const int32_t *bt = A.pool.block_table + (long long)s * A.pool.max_blocks;
-    const K8Query Q = kv8_query_load(A.q + ((long long)b * A.hq + (long long)kv * G) * DQK, G, A.table + p * 64, tid);
+    const int nq = rows * G;  // query rows
+    K8Query Q[K8_MT];
+#pragma unroll
+    for (int m = 0; m < K8_MT; ++m) {
+      const int r = 16 * m + (tid >> 3), c = (int)((uint32_t)r * A.g_mul >> 16);
+      const bool have = r < nq;
+      const long long pr = c == 0 ? at[0] : c == 1 ? at[1] : c == 2 ? at[2] : at[3];
+      if (m == 0 || nq > 16)
+        Q[m] = kv8_query_load(A.q + ((long long)(b + c) * A.hq + (long long)kv * G + (r - c * G)) * DQK, A.table + pr * 64,
+                              tid & 7, have);
+      if ((tid & 7) == 0 && have) sKeys[r] = (int)pr + 1;  // keys that the row may see
+    }
     tc::fence_proxy_async_smem();                   // the last piece's merge area lies over the stages:
     if (__syncthreads_or(*abort_flag != 0)) break;  // it is free again, its accesses ahead of the copies'
 
@@ -329,7 +371,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
     for (int i = 0; i < K8_STAGES - 1; ++i)
       if (i < my_n) issue(i);
 
-    kv8_query(Q, G, A.scale_log2, smem, tid);
+    kv8_query(Q[0], A.scale_log2, smem, reinterpret_cast<float *>(smem + K8_OFF_ROW), tid);
+    if (nq > 16) kv8_query(Q[K8_MT - 1], A.scale_log2, smem + 12 * 512, reinterpret_cast<float *>(smem + K8_OFF_ROW) + 16, tid);
     __syncthreads();
     int run_n = my_n;
     if (A.stall_ns && warp == 0 && !gave_up && !tc::mbar_wait(sBase + K8_OFF_STALL, 0, abort_flag, A.stall_ns)) {
@@ -348,158 +391,259 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       ++seen;
       return (ok >> (i & 31)) & 1 ? sStage + st * KV8_TILE : nullptr;
     };
-    // references of the scores (r) and of the weights (R, less the bias) of this
-    // lane's two rows or columns, and the sums of exp2(score - r)
-    float r0 = K8_NONE, r1 = K8_NONE, R0 = K8_NONE, R1 = K8_NONE, l0 = 0.f, l1 = 0.f;
-    bool any = false;  // a tile was there
-    // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators
+    // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators,
+    // of 16 rows at a time; behind it the CTA's merged part of all rows (DIRECT)
     float *mml = reinterpret_cast<float *>(smem + K8_OFF_STAGE);  // [4][16][2]
     float *mo = mml + K8_WARPS * 16 * 2;                          // [4][16][MO_STRIDE]
-    if constexpr (!SMALL) {
-      const float crow0 = *reinterpret_cast<const float *>(smem + K8_OFF_ROW + 4 * gr);
-      const float crow1 = *reinterpret_cast<const float *>(smem + K8_OFF_ROW + 4 * (gr + 8));
-      float O[16][4];  // O[4g + i]: dims 32 g + 4 c + i of column c
+    float *fac = mo + K8_WARPS * 16 * MO_STRIDE;                  // [4 warps][16]
+    float *own_ml = fac + K8_WARPS * 16;                          // [32][2]
+    float *own_o = own_ml + 2 * K8_ROWS;                          // [32][128]
+    // the CTA's four parts of rows 16 m .. joined
+    auto join = [&](int m) {
+      __syncthreads();
+      const int n = min(nq - 16 * m, 16);
+      if (tid < n) {
+        float M = NEG_INF;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
+        for (int ww = 0; ww < K8_WARPS; ++ww) M = fmaxf(M, mml[ww * 32 + tid * 2]);
+        const float base = M == NEG_INF ? 0.f : M;
+        float L = 0.f;
+#pragma unroll
+        for (int ww = 0; ww < K8_WARPS; ++ww) {
+          const float mw = mml[ww * 32 + tid * 2];
+          const float f = mw == NEG_INF ? 0.f : ex2(mw - base);
+          fac[ww * 16 + tid] = f;
+          L += mml[ww * 32 + tid * 2 + 1] * f;
+        }
+        float *pml = DIRECT ? own_ml + 32 * m : A.part_ml + ((long long)w * (A.rmax * G) + 16 * m) * 2;
+        pml[tid * 2] = M;
+        pml[tid * 2 + 1] = L;
+      }
+      __syncthreads();
+      float *po = DIRECT ? own_o + 16 * m * DV : A.part_o + ((long long)w * (A.rmax * G) + 16 * m) * DV;
+      for (int idx = tid; idx < n * (DV / 4); idx += blockDim.x) {
+        const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int ww = 0; ww < K8_WARPS; ++ww) {
+          const float f = fac[ww * 16 + g];
+          const float4 x = *reinterpret_cast<const float4 *>(mo + (ww * 16 + g) * MO_STRIDE + d4);
+          acc.x += x.x * f;
+          acc.y += x.y * f;
+          acc.z += x.z * f;
+          acc.w += x.w * f;
+        }
+        *reinterpret_cast<float4 *>(po + g * DV + d4) = acc;
+      }
+    };
+    // A warp's reference of a row for the merge: none (-inf) where it saw no key of the row's, 0 where no score was a
+    // number (the row will not be one either).
+    auto ref = [](float r, float l) { return r != K8_NONE ? r : l == 0.f ? NEG_INF : 0.f; };
+    const float *sFac = reinterpret_cast<const float *>(smem + K8_OFF_ROW);
+
+    // MT x 16 query rows as rows of the products; this lane has rows gr and gr + 8 (index e) of each
+    auto wide = [&](auto mt) {
+      constexpr int MT = decltype(mt)::value;
+      float f[MT][2], O[MT][16][4];              // O[m][4g + i]: dims 32 g + 4 c + i of column c
+      float rr[MT][2], RR[MT][2], ll[MT][2];     // references of the scores and (less the bias) of the weights; sums
+      int keys[MT][2], least = 0x7fffffff;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) O[m][n][0] = O[m][n][1] = O[m][n][2] = O[m][n][3] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * m + gr + 8 * e;
+          f[m][e] = sFac[r];
+          keys[m][e] = r < nq ? sKeys[r] : 0x7fffffff;
+          least = min(least, keys[m][e]);
+          rr[m][e] = RR[m][e] = K8_NONE;
+          ll[m][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) least = min(least, __shfl_xor_sync(FULLW, least, o));
+      least = min(least, key_hi);  // keys that every row sees
       for (int i = 0; i < run_n; ++i) {
         const uint8_t *sT = next_tile(i);
         if (!sT) {
           if (gave_up) break;
           continue;
         }
-        any = true;
-        // scores: rows heads gr and gr + 8, columns keys 2t, 2t + 1 (nt = 0) and + 8
-        float S[2][4];
+        // scores: columns keys 2t, 2t + 1 (nt = 0) and + 8
+        float S[MT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) S[m][nt][0] = S[m][nt][1] = S[m][nt][2] = S[m][nt][3] = 0.f;
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
           const uint4 ka = lds128(sT + g * 1024 + lane * 16), kb = lds128(sT + g * 1024 + 512 + lane * 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 a = lds128(smem + (g * 4 + j) * 512 + lane * 16);
-            mma_f16(S[0], a.x, a.y, a.z, a.w, kv8_pair<0>(word(ka, j)), kv8_pair<1>(word(ka, j)));
-            mma_f16(S[1], a.x, a.y, a.z, a.w, kv8_pair<0>(word(kb, j)), kv8_pair<1>(word(kb, j)));
+            const uint32_t a0 = kv8_pair<0>(word(ka, j)), a1 = kv8_pair<1>(word(ka, j));
+            const uint32_t b0 = kv8_pair<0>(word(kb, j)), b1 = kv8_pair<1>(word(kb, j));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const uint4 q = lds128(smem + m * 12 * 512 + (g * 4 + j) * 512 + lane * 16);
+              mma_f16(S[m][0], q.x, q.y, q.z, q.w, a0, a1);
+              mma_f16(S[m][1], q.x, q.y, q.z, q.w, b0, b1);
+            }
           }
         }
         const uint4 tail = lds128(sT + KV8_OFF_TAIL);
-        const int left = key_hi - (key_lo + K8_UNIT * (warp + i * K8_WARPS));  // keys of the tile in range
-        if (left < 16 || tail.z != 0) {
+        const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS);
+        const bool plain = key0 + 16 <= least && tail.z == 0;  // every row sees all 16 keys, and all rows of the tile are finite
+        if (!plain) {
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = 8 * nt + 2 * t + e;
-              if (k >= left) S[nt][e] = S[nt][2 + e] = NEG_INF;
-              else if (tail.z >> k & 1) S[nt][e] = S[nt][2 + e] = __uint_as_float(0x7fffffffu);  // a K row that is not finite
-            }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int k = 8 * (u >> 1) + 2 * t + (u & 1);
+                float &x = S[m][u >> 1][2 * e + (u & 1)];
+                if (key0 + k >= min(keys[m][e], key_hi)) x = NEG_INF;
+                else if (tail.z >> k & 1) x = __uint_as_float(0x7fffffffu);  // a K row that is not finite
+              }
         }
-        // (the least number keeps a factor of zero from making NaN of a masked score)
-        const float ks = __uint_as_float(tail.x), f0 = fmaf(ks, crow0, 0x1p-126f), f1 = fmaf(ks, crow1, 0x1p-126f);
+        const float ks = __uint_as_float(tail.x);
         const float lv = lg2(__uint_as_float(tail.y));  // -inf for a scale of 0: no weight
-        const float top0 = fmaxf(fmax3(S[0][0], S[0][1], S[1][0]), S[1][1]) * f0;
-        const float top1 = fmaxf(fmax3(S[0][2], S[0][3], S[1][2]), S[1][3]) * f1;
-        const bool move = fmaxf(top0 - r0, top1 - r1) > K8_SLACK || lv + fmaxf(top0 - R0, top1 - R1) > K8_SLACK + K8_PBIAS;
+        float fs[MT][2], top[MT][2];
+        bool move = false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // (the least number keeps a factor of zero from making NaN of a masked score)
+            fs[m][e] = fmaf(ks, f[m][e], 0x1p-126f);
+            top[m][e] = fmaxf(fmax3(S[m][0][2 * e], S[m][0][2 * e + 1], S[m][1][2 * e]), S[m][1][2 * e + 1]) * fs[m][e];
+            move |= top[m][e] - rr[m][e] > K8_SLACK || lv + (top[m][e] - RR[m][e]) > K8_SLACK + K8_PBIAS;
+          }
         if (__any_sync(FULLW, move)) {
           // new references per row: the larger of the old one and this tile's maximum
-          float t0 = top0, t1 = top1;
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
-            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
-          }
-          const float n0 = fmaxf(r0, t0), n1 = fmaxf(r1, t1);
-          l0 *= ex2(r0 - n0);
-          l1 *= ex2(r1 - n1);
-          r0 = n0;
-          r1 = n1;
-          const float N0 = fmaxf(R0, t0 + lv - K8_PBIAS), N1 = fmaxf(R1, t1 + lv - K8_PBIAS);
-          const float c0 = ex2(R0 - N0), c1 = ex2(R1 - N1);
-          R0 = N0;
-          R1 = N1;
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            O[n][0] *= c0;
-            O[n][1] *= c0;
-            O[n][2] *= c1;
-            O[n][3] *= c1;
-          }
+            for (int e = 0; e < 2; ++e) {
+              float x = top[m][e];
+              x = fmaxf(x, __shfl_xor_sync(FULLW, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(FULLW, x, 2));
+              const float n = fmaxf(rr[m][e], x), N = fmaxf(RR[m][e], x + lv - K8_PBIAS), c = ex2(RR[m][e] - N);
+              ll[m][e] *= ex2(rr[m][e] - n);
+              rr[m][e] = n;
+              RR[m][e] = N;
+#pragma unroll
+              for (int d = 0; d < 16; ++d) {
+                O[m][d][2 * e] *= c;
+                O[m][d][2 * e + 1] *= c;
+              }
+            }
         }
-        uint32_t P[2][2];  // weights [8 keys][row gr, row gr + 8]
-        const float g0 = lv - R0, g1 = lv - R1;
+        uint32_t P[MT][2][2];  // weights [8 keys][row gr, row gr + 8]
+        bool far = false;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          l0 += ex2(fmaf(S[nt][0], f0, -r0)) + ex2(fmaf(S[nt][1], f0, -r0));
-          l1 += ex2(fmaf(S[nt][2], f1, -r1)) + ex2(fmaf(S[nt][3], f1, -r1));
-          P[nt][0] = pack_h2(ex2(fmaf(S[nt][0], f0, g0)), ex2(fmaf(S[nt][1], f0, g0)));
-          P[nt][1] = pack_h2(ex2(fmaf(S[nt][2], f1, g1)), ex2(fmaf(S[nt][3], f1, g1)));
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // exp2(score + lv - R) is exp2(score - r) times exp2 of this; where it is within 2^64 either way, a product that
+            // underflows is below fp16's least number all the same
+            const float h = lv - RR[m][e] + rr[m][e], w = ex2(h);
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const float x = S[m][nt][2 * e], y = S[m][nt][2 * e + 1];
+              const float a = ex2(fmaf(x, fs[m][e], -rr[m][e])), b = ex2(fmaf(y, fs[m][e], -rr[m][e]));
+              ll[m][e] += a + b;
+              P[m][nt][e] = pack_h2(a * w, b * w);
+            }
+            far |= !(fabsf(h) <= 64.f);
+          }
+        if (__any_sync(FULLW, far)) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+                P[m][nt][e] = pack_h2(ex2(fmaf(S[m][nt][2 * e], fs[m][e], lv - RR[m][e])),
+                                      ex2(fmaf(S[m][nt][2 * e + 1], fs[m][e], lv - RR[m][e])));
         }
         if (tail.z >> 16) {  // V rows that are not finite
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int k = 8 * nt + 2 * t;
-            const uint32_t nan = (k < left && (tail.z >> (16 + k) & 1) ? 0x7fffu : 0u) |
-                                 (k + 1 < left && (tail.z >> (17 + k) & 1) ? 0x7fff0000u : 0u);
-            P[nt][0] |= nan;
-            P[nt][1] |= nan;
-          }
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int k = 8 * (u >> 1) + 2 * t + (u & 1);
+                if ((tail.z >> (16 + k) & 1) && key0 + k < min(keys[m][e], key_hi)) P[m][u >> 1][e] |= u & 1 ? 0x7fff0000u : 0x7fffu;
+              }
         }
         // sums
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const uint4 v = lds128(sT + KV8_OFF_V + g * 512 + lane * 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16(O[4 * g + j], P[0][0], P[0][1], P[1][0], P[1][1], kv8_pair<0>(word(v, j)), kv8_pair<1>(word(v, j)));
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v0 = kv8_pair<0>(word(v, j)), v1 = kv8_pair<1>(word(v, j));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16(O[m][4 * g + j], P[m][0][0], P[m][0][1], P[m][1][0], P[m][1][1], v0, v1);
+          }
         }
         __syncwarp();  // the stage is read: the next copy into it may go out
       }
-      __syncthreads();  // all warps done with their stages: reuse them as the merge area
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        l0 += __shfl_xor_sync(FULLW, l0, o);
-        l1 += __shfl_xor_sync(FULLW, l1, o);
-      }
-      // numerators in the scores' reference (0 where no score was a number: the row will not be one)
-      const float m0 = r0 == K8_NONE ? 0.f : r0, m1 = r1 == K8_NONE ? 0.f : r1;
-      const float c0 = ex2(R0 - m0), c1 = ex2(R1 - m1);
-      if (t == 0) {
-        float *m = mml + warp * 32;
-        m[gr * 2] = any ? m0 : NEG_INF;
-        m[gr * 2 + 1] = l0;
-        m[(gr + 8) * 2] = any ? m1 : NEG_INF;
-        m[(gr + 8) * 2 + 1] = l1;
-      }
-      float *o = mo + warp * 16 * MO_STRIDE;
+      for (int m = 0; m < MT; ++m) {
+        __syncthreads();  // all warps done with their stages (or the merge area): (re)use them as the merge area
+        float *o = mo + warp * 16 * MO_STRIDE;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+        for (int e = 0; e < 2; ++e) {
+          float l = ll[m][e];
+          l += __shfl_xor_sync(FULLW, l, 1);
+          l += __shfl_xor_sync(FULLW, l, 2);
+          const float r = ref(rr[m][e], l), c = ex2(RR[m][e] - (r == NEG_INF ? 0.f : r));  // numerators in the scores' reference
+          if (t == 0) *reinterpret_cast<float2 *>(mml + warp * 32 + (gr + 8 * e) * 2) = make_float2(r, l);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float(*On)[4] = &O[4 * g];
-          const int d = 32 * g + 4 * (2 * t + c);
-          *reinterpret_cast<float4 *>(o + gr * MO_STRIDE + d) =
-              make_float4(On[0][c] * c0, On[1][c] * c0, On[2][c] * c0, On[3][c] * c0);
-          *reinterpret_cast<float4 *>(o + (gr + 8) * MO_STRIDE + d) =
-              make_float4(On[0][2 + c] * c1, On[1][2 + c] * c1, On[2][2 + c] * c1, On[3][2 + c] * c1);
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float(*On)[4] = &O[m][4 * g];
+              const int a = 2 * e + u;
+              *reinterpret_cast<float4 *>(o + (gr + 8 * e) * MO_STRIDE + 32 * g + 4 * (2 * t + u)) =
+                  make_float4(On[0][a] * c, On[1][a] * c, On[2][a] * c, On[3][a] * c);
+            }
         }
-    } else {
-      // a head's column: this lane has heads 2t and 2t + 1
-      const float crow0 = *reinterpret_cast<const float *>(smem + K8_OFF_ROW + 8 * t);
-      const float crow1 = *reinterpret_cast<const float *>(smem + K8_OFF_ROW + 8 * t + 4);
+        join(m);
+      }
+    };
+    // up to 8 query rows as columns; this lane has columns 2t and 2t + 1 (index e)
+    auto narrow = [&]() {
       uint2 qb[12];
 #pragma unroll
       for (int j = 0; j < 12; ++j) qb[j] = make_uint2(lds32(smem + j * 512 + lane * 16), lds32(smem + j * 512 + lane * 16 + 8));
-      float O[8][4];  // O[2g + j]: dims 32 g + 4 gr + 2 j (rows gr) and + 1 (rows gr + 8)
+      float f[2], O[8][4];  // O[2g + j]: dims 32 g + 4 gr + 2 j (rows gr) and + 1 (rows gr + 8)
+      float rr[2], RR[2], ll[2];
+      int keys[2], least = 0x7fffffff;
 #pragma unroll
       for (int n = 0; n < 8; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[e] = sFac[2 * t + e];
+        keys[e] = 2 * t + e < nq ? sKeys[2 * t + e] : 0x7fffffff;
+        least = min(least, keys[e]);
+        rr[e] = RR[e] = K8_NONE;
+        ll[e] = 0.f;
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(FULLW, least, o));
+      least = min(least, key_hi);
       for (int i = 0; i < run_n; ++i) {
         const uint8_t *sT = next_tile(i);
         if (!sT) {
           if (gave_up) break;
           continue;
         }
-        any = true;
-        // scores: rows keys gr and gr + 8, columns heads 2t, 2t + 1; two sums, as one chain of products waits for itself
+        // scores: rows keys gr and gr + 8 (index h); two sums, as one chain of products waits for itself
         float S[4] = {0.f, 0.f, 0.f, 0.f}, S2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
@@ -510,54 +654,60 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
                     kv8_pair<1>(word(kb, j)), qb[4 * g + j].x, qb[4 * g + j].y);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[e] += S2[e];
+        for (int u = 0; u < 4; ++u) S[u] += S2[u];
         const uint4 tail = lds128(sT + KV8_OFF_TAIL);
-        const int left = key_hi - (key_lo + K8_UNIT * (warp + i * K8_WARPS));
-        if (left < 16 || tail.z != 0) {
+        const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS);
+        if (!(key0 + 16 <= least && tail.z == 0)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = gr + 8 * e;
-            if (k >= left) S[2 * e] = S[2 * e + 1] = NEG_INF;
-            else if (tail.z >> k & 1) S[2 * e] = S[2 * e + 1] = __uint_as_float(0x7fffffffu);
+          for (int u = 0; u < 4; ++u) {
+            const int k = gr + 8 * (u >> 1);
+            if (key0 + k >= min(keys[u & 1], key_hi)) S[u] = NEG_INF;
+            else if (tail.z >> k & 1) S[u] = __uint_as_float(0x7fffffffu);
           }
         }
-        const float ks = __uint_as_float(tail.x), f0 = fmaf(ks, crow0, 0x1p-126f), f1 = fmaf(ks, crow1, 0x1p-126f);
+        const float ks = __uint_as_float(tail.x);
         const float lv = lg2(__uint_as_float(tail.y));
-        const float top0 = fmaxf(S[0], S[2]) * f0, top1 = fmaxf(S[1], S[3]) * f1;
-        const bool move = fmaxf(top0 - r0, top1 - r1) > K8_SLACK || lv + fmaxf(top0 - R0, top1 - R1) > K8_SLACK + K8_PBIAS;
-        if (__any_sync(FULLW, move)) {
-          float t0 = top0, t1 = top1;
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(FULLW, t0, o));
-            t1 = fmaxf(t1, __shfl_xor_sync(FULLW, t1, o));
-          }
-          const float n0 = fmaxf(r0, t0), n1 = fmaxf(r1, t1);
-          l0 *= ex2(r0 - n0);
-          l1 *= ex2(r1 - n1);
-          r0 = n0;
-          r1 = n1;
-          const float N0 = fmaxf(R0, t0 + lv - K8_PBIAS), N1 = fmaxf(R1, t1 + lv - K8_PBIAS);
-          const float c0 = ex2(R0 - N0), c1 = ex2(R1 - N1);
-          R0 = N0;
-          R1 = N1;
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            O[n][0] *= c0;
-            O[n][1] *= c1;
-            O[n][2] *= c0;
-            O[n][3] *= c1;
-          }
-        }
-        uint32_t P[2];  // weights: row head gr, columns keys 2t, 2t + 1 and + 8
-        const float g0 = lv - R0, g1 = lv - R1;
+        float fs[2], top[2];
+        bool move = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          l0 += ex2(fmaf(S[2 * e], f0, -r0));
-          l1 += ex2(fmaf(S[2 * e + 1], f1, -r1));
-          uint32_t pw = pack_h2(ex2(fmaf(S[2 * e], f0, g0)), ex2(fmaf(S[2 * e + 1], f1, g1)));
-          if (tail.z >> 16 && gr + 8 * e < left && (tail.z >> (16 + gr + 8 * e) & 1)) pw = 0x7fff7fffu;  // a V row that is not finite
-          P[e] = transpose8(pw);
+          fs[e] = fmaf(ks, f[e], 0x1p-126f);
+          top[e] = fmaxf(S[e], S[2 + e]) * fs[e];
+          move |= top[e] - rr[e] > K8_SLACK || lv + (top[e] - RR[e]) > K8_SLACK + K8_PBIAS;
+        }
+        if (__any_sync(FULLW, move)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(FULLW, x, o));
+            const float n = fmaxf(rr[e], x), N = fmaxf(RR[e], x + lv - K8_PBIAS), c = ex2(RR[e] - N);
+            ll[e] *= ex2(rr[e] - n);
+            rr[e] = n;
+            RR[e] = N;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              O[d][e] *= c;
+              O[d][2 + e] *= c;
+            }
+          }
+        }
+        uint32_t P[2];  // weights: row query row gr, columns keys 2t, 2t + 1 and + 8
+        const float h0 = lv - RR[0] + rr[0], h1 = lv - RR[1] + rr[1], w0 = ex2(h0), w1 = ex2(h1);
+        const bool far = __any_sync(FULLW, !(fmaxf(fabsf(h0), fabsf(h1)) <= 64.f));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = S[2 * h], y = S[2 * h + 1];
+          const float a = ex2(fmaf(x, fs[0], -rr[0])), b = ex2(fmaf(y, fs[1], -rr[1]));
+          ll[0] += a;
+          ll[1] += b;
+          uint32_t pw = pack_h2(a * w0, b * w1);
+          if (far) pw = pack_h2(ex2(fmaf(x, fs[0], lv - RR[0])), ex2(fmaf(y, fs[1], lv - RR[1])));
+          if (tail.z >> 16 && (tail.z >> (16 + gr + 8 * h) & 1)) {  // a V row that is not finite
+            const int k = key0 + gr + 8 * h;
+            pw |= (k < min(keys[0], key_hi) ? 0x7fffu : 0u) | (k < min(keys[1], key_hi) ? 0x7fff0000u : 0u);
+          }
+          P[h] = transpose8(pw);
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -568,75 +718,41 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
         __syncwarp();  // the stage is read: the next copy into it may go out
       }
       __syncthreads();  // all warps done with their stages: reuse them as the merge area
+      float c[2], r[2];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l0 += __shfl_xor_sync(FULLW, l0, o);
-        l1 += __shfl_xor_sync(FULLW, l1, o);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) ll[e] += __shfl_xor_sync(FULLW, ll[e], o);
+        r[e] = ref(rr[e], ll[e]);
+        c[e] = ex2(RR[e] - (r[e] == NEG_INF ? 0.f : r[e]));
       }
-      const float m0 = r0 == K8_NONE ? 0.f : r0, m1 = r1 == K8_NONE ? 0.f : r1;
-      const float c0 = ex2(R0 - m0), c1 = ex2(R1 - m1);
-      if (gr == 0)
-        *reinterpret_cast<float4 *>(mml + warp * 32 + 4 * t) = make_float4(any ? m0 : NEG_INF, l0, any ? m1 : NEG_INF, l1);
+      if (gr == 0) *reinterpret_cast<float4 *>(mml + warp * 32 + 4 * t) = make_float4(r[0], ll[0], r[1], ll[1]);
       float *o = mo + warp * 16 * MO_STRIDE + 2 * t * MO_STRIDE + 4 * gr;
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float k = c ? c1 : c0;
-          *reinterpret_cast<float4 *>(o + c * MO_STRIDE + 32 * g) =
-              make_float4(O[2 * g][c] * k, O[2 * g][2 + c] * k, O[2 * g + 1][c] * k, O[2 * g + 1][2 + c] * k);
-        }
-    }
-    __syncthreads();
-    float *fac = mo + K8_WARPS * 16 * MO_STRIDE;  // [4 warps][16 heads]
-    float *own_ml = fac + K8_WARPS * 16;          // DIRECT: the CTA's merged part, [16][2] and [16][128]
-    float *own_o = own_ml + 32;
-    if (tid < G) {
-      float M = NEG_INF;
-#pragma unroll
-      for (int ww = 0; ww < K8_WARPS; ++ww) M = fmaxf(M, mml[ww * 32 + tid * 2]);
-      const float base = M == NEG_INF ? 0.f : M;
-      float L = 0.f;
-#pragma unroll
-      for (int ww = 0; ww < K8_WARPS; ++ww) {
-        const float mw = mml[ww * 32 + tid * 2];
-        const float f = mw == NEG_INF ? 0.f : ex2(mw - base);
-        fac[ww * 16 + tid] = f;
-        L += mml[ww * 32 + tid * 2 + 1] * f;
-      }
-      float *pml = DIRECT ? own_ml : A.part_ml + (long long)w * G * 2;
-      pml[tid * 2] = M;
-      pml[tid * 2 + 1] = L;
-    }
-    __syncthreads();
-    for (int idx = tid; idx < G * (DV / 4); idx += blockDim.x) {
-      const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int ww = 0; ww < K8_WARPS; ++ww) {
-        const float f = fac[ww * 16 + g];
-        const float4 x = *reinterpret_cast<const float4 *>(mo + (ww * 16 + g) * MO_STRIDE + d4);
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
-      }
-      *reinterpret_cast<float4 *>(DIRECT ? own_o + g * DV + d4 : A.part_o + ((long long)w * G + g) * DV + d4) = acc;
-    }
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4 *>(o + e * MO_STRIDE + 32 * g) =
+              make_float4(O[2 * g][e] * c[e], O[2 * g][2 + e] * c[e], O[2 * g + 1][e] * c[e], O[2 * g + 1][2 + e] * c[e]);
+      join(0);
+    };
+    if (nq <= 8) narrow();
+    else if (K8_MT == 1 || nq <= 16) wide(std::integral_constant<int, 1>());
+    else wide(std::integral_constant<int, K8_MT>());
     if constexpr (DIRECT) {
       cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
       const int rank = (int)cl.block_rank();
       cl.sync();
-      for (int idx = rank * (K8_WARPS * 32) + tid; idx < G * (DV / 4); idx += A.cs * (K8_WARPS * 32)) {
-        const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
+      for (int idx = rank * (K8_WARPS * 32) + tid; idx < nq * (DV / 4); idx += A.cs * (K8_WARPS * 32)) {
+        const int r = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
         float M = NEG_INF, S = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = 0; c < A.cs; ++c) M = fmaxf(M, cl.map_shared_rank(own_ml, c)[2 * g]);
+        for (int c = 0; c < A.cs; ++c) M = fmaxf(M, cl.map_shared_rank(own_ml, c)[2 * r]);
         for (int c = 0; c < A.cs; ++c) {
-          const float2 ml = *reinterpret_cast<const float2 *>(cl.map_shared_rank(own_ml, c) + 2 * g);
+          const float2 ml = *reinterpret_cast<const float2 *>(cl.map_shared_rank(own_ml, c) + 2 * r);
           if (ml.x == NEG_INF) continue;
           const float f = ex2(ml.x - M);
-          const float4 o = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own_o, c) + g * DV + d4);
+          const float4 o = *reinterpret_cast<const float4 *>(cl.map_shared_rank(own_o, c) + r * DV + d4);
           S += ml.y * f;
           acc.x += o.x * f;
           acc.y += o.y * f;
@@ -644,7 +760,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           acc.w += o.w * f;
         }
         const float inv = S == 0.f ? 0.f : 1.f / S;
-        *reinterpret_cast<uint2 *>(A.out + ((long long)b * A.hq + (long long)kv * G + g) * DV + d4) =
+        const int c = (int)((uint32_t)r * A.g_mul >> 16);
+        *reinterpret_cast<uint2 *>(A.out + ((long long)(b + c) * A.hq + (long long)kv * G + (r - c * G)) * DV + d4) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       }
       cl.sync();  // no CTA leaves while another reads its part
@@ -667,7 +784,7 @@ bool one_launch(int B, int hkv, long long max_ctx) {
 
 size_t kv8_decode_workspace(int B, int hq, int hkv, long long max_ctx) {
   if (one_launch(B, hkv, max_ctx)) return 0;
-  return line_workspace<K8Line>(B, hq, hkv, max_ctx);
+  return line_workspace<K8Line>(B, hq, hkv, max_ctx, rows_together(hq / hkv));
 }
 
 cudaError_t launch_kv8_decode(const uint16_t *q, const int64_t *pos, const int32_t *seq, int B, int hq,
@@ -677,15 +794,15 @@ cudaError_t launch_kv8_decode(const uint16_t *q, const int64_t *pos, const int32
   const long long rows = (long long)B * hkv, units = (max_ctx + K8_UNIT - 1) / K8_UNIT;
   if (rows > 0x7ffffffLL) return cudaErrorInvalidValue;  // (its queries alone would fill the GPU)
   const bool direct = one_launch(B, hkv, max_ctx);
-  static void (*const kernels[2][3])(K8Args) = {
-      {kv8_decode_kernel<false, K8_LINE>, kv8_decode_kernel<false, K8_TURNS>, kv8_decode_kernel<false, K8_DIRECT>},
-      {kv8_decode_kernel<true, K8_LINE>, kv8_decode_kernel<true, K8_TURNS>, kv8_decode_kernel<true, K8_DIRECT>}};
+  static void (*const kernels[3])(K8Args) = {kv8_decode_kernel<K8_LINE>, kv8_decode_kernel<K8_TURNS>,
+                                             kv8_decode_kernel<K8_DIRECT>};
   const int form = direct ? K8_DIRECT : line_turns<K8Line>(B, hkv, max_ctx) > 1 ? K8_TURNS : K8_LINE;
-  void (*const kernel)(K8Args) = kernels[G <= 8][form];
-  cudaError_t e = ensure_smem_limit(24 + 3 * (G <= 8) + form, (const void *)kernel, K8_SMEM, true);
+  void (*const kernel)(K8Args) = kernels[form];
+  cudaError_t e = ensure_smem_limit(24 + form, (const void *)kernel, K8_SMEM, true);
   if (e != cudaSuccess) return e;
   K8Args A;
-  line_args<K8Line>(A, pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, ws, out);
+  line_args<K8Line>(A, pos, seq, B, hq, hkv, pool.num_seqs, max_pos, max_ctx, ws, out,
+                    rows_together(G));
   A.q = q;
   A.pool = pool;
   A.table = table;
@@ -694,6 +811,7 @@ cudaError_t launch_kv8_decode(const uint16_t *q, const int64_t *pos, const int32
   A.stall_ns = take_stall();
   const unsigned long long tpb = (unsigned long long)(pool.block_size >> 4);
   A.tpb_mul = ((1ull << 36) + tpb - 1) / tpb;
+  A.g_mul = (65536u + (uint32_t)G - 1) / (uint32_t)G;
   A.cs = 1;
   if (direct) {
     // as many CTAs a row as the longest row gives every warp a unit, as a

@@ -44,14 +44,13 @@ __device__ __forceinline__ bool unpack_unit(const Kv8View &src, const int32_t *_
                                             long long T, const int32_t *__restrict__ dst_seqs, const KvView &dst,
                                             long long unit, int h, unsigned *status) {
   const int lane = threadIdx.x & 31;
-  const int i = kv8_chunk(cu_rows, n, unit);
-  const int c0 = cu_rows[i], c1 = cu_rows[i + 1];
+  const Kv8Chunk C = kv8_chunk(cu_rows, lo, src_seqs, n, unit);
+  const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
   if (c0 < 0 || c1 < c0 || c1 > T) {
     if (lane == 0) flag(status, ST_BAD_ROWS);
     return i < n - 1;
   }
-  long long a = lo[i];
-  const int s = src_seqs[i];
+  long long a = C.pos;
   const bool mine = lane == 0 && h == 0;
   const long long u = unit - ((c0 >> 4) + 2LL * i);
   if (u < 0) return true;
@@ -148,7 +147,7 @@ __device__ __forceinline__ bool unpack_unit(const Kv8View &src, const int32_t *_
 }
 
 template <bool ROUND>
-__global__ void __launch_bounds__(K8U_WARPS * 32)
+__global__ void __launch_bounds__(K8U_WARPS * 32, ROUND ? 2 : 4)
     kv8_unpack_kernel(Kv8View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
                       const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
                       KvView dst, long long units, unsigned *status) {

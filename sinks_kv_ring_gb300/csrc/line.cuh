@@ -11,8 +11,13 @@
 // line is cut into a multiple of the CTAs' number of shares, and CTA c takes c,
 // c + CTAs, ...
 //
-// A kernel describes its line by a type LN with UNIT, ROW, MIN, MOST and CTAS
-// (the CTAs of an SM).
+// Neighbouring batch rows of one sequence (the draft tokens of a verification) may
+// go together (LN::SHARE): of every aligned block of `rmax` rows, those that follow
+// a row of the same sequence join it, the first one (the leader) has the line's
+// part for all of them, as long as the longest needs, and the others have none.
+//
+// A kernel describes its line by a type LN with UNIT, ROW, MIN, MOST, CTAS (the
+// CTAs of an SM) and SHARE.
 #pragma once
 
 #include "launch.h"
@@ -35,6 +40,7 @@ struct LineArgs {
   float *part_ml;
   float *part_o;
   uint16_t *out;
+  int rmax;  // rows that may go together: a power of two up to 4; 1 without LN::SHARE
 };
 
 // Units of keys of sequence b; 0 (flagged once) where its position or id is
@@ -49,6 +55,28 @@ __device__ __forceinline__ int line_units(long long p, int s, int num_seqs, int6
   }
   return (int)((p + LN::UNIT) / LN::UNIT);
 }
+
+// Which of a warp's rows (lane l: row l of 32, those of valid position and id
+// `valid`, of sequence s) join the row before them.
+__device__ __forceinline__ unsigned line_joined(bool valid, int s, int lane, int rmax) {
+  const unsigned ok = __ballot_sync(FULLW, valid);
+  const int before = __shfl_up_sync(FULLW, s, 1);
+  return __ballot_sync(FULLW, (lane & (rmax - 1)) != 0 && (ok >> lane & 1) && (ok >> (lane - 1) & 1) && s == before);
+}
+// Whether row lane + k goes with row lane.
+__device__ __forceinline__ bool line_follows(unsigned joined, int lane, int k) {
+  const unsigned m = ((1u << k) - 1u) << 1;  // (k < 4: rows lane + 1 .. lane + k)
+  return (joined >> lane & m) == m;
+}
+// What the plan says of a row with LN::SHARE: how far ahead of it its leader is, and
+// how many rows there are from the leader on.
+__device__ __forceinline__ uint8_t line_info(unsigned joined, int lane) {
+  const int lead = __clz(~(joined << (31 - lane)));  // ones from the row's bit down
+  const int more = __ffs(~(joined >> lane >> 1)) - 1;
+  return (uint8_t)(lead | (lead + 1 + more) << 4);
+}
+__device__ __forceinline__ int line_lead(uint8_t info) { return info & 15; }
+__device__ __forceinline__ int line_rows(uint8_t info) { return info >> 4; }
 
 // Units of a share for a line of `total` units.
 template <class LN>
@@ -65,20 +93,31 @@ __device__ __forceinline__ long long line_share(long long total, long long ctas)
 // by NT threads, `get(b, p, s)` giving sequence b's position and id; returns L.
 template <class LN, int NT, typename Get>
 __device__ __forceinline__ long long line_plan(Get get, int B, int hkv, int num_seqs, int64_t max_pos, long long max_ctx,
-                                               int ctas, int64_t *prefix, unsigned *status) {
+                                               int ctas, int64_t *prefix, unsigned *status, int rmax = 1,
+                                               uint8_t *info = nullptr) {
   __shared__ long long s_sum[NT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long base = 0;
   for (int b0 = 0; b0 < B; b0 += NT) {
     const int b = b0 + tid;
     long long x = 0;
+    int u = 0, q = 0;
     if (b < B) {
       long long p;
-      int q;
       get(b, p, q);
-      const int u = line_units<LN>(p, q, num_seqs, max_pos, max_ctx, status);
-      x = u ? (long long)hkv * (u + LN::ROW) : 0;
+      u = line_units<LN>(p, q, num_seqs, max_pos, max_ctx, status);
     }
+    if (LN::SHARE) {
+      const unsigned joined = line_joined(u > 0, q, lane, rmax);
+      int most = u;
+      for (int k = 1; k < rmax; ++k) {
+        const int y = __shfl_down_sync(FULLW, u, k);
+        if (line_follows(joined, lane, k)) most = max(most, y);
+      }
+      u = joined >> lane & 1 ? 0 : most;
+      if (b < B) info[b] = line_info(joined, lane);
+    }
+    x = u ? (long long)hkv * (u + LN::ROW) : 0;
     const long long mine = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,11 +156,12 @@ constexpr int LINE_PLAN_THREADS = 256;
 template <class LN>
 __global__ void __launch_bounds__(LINE_PLAN_THREADS)
     line_plan_kernel(const int64_t *__restrict__ pos, const int32_t *__restrict__ seq, int B, int hkv, int num_seqs,
-                     int64_t max_pos, long long max_ctx, int ctas, int64_t *__restrict__ plan, unsigned *status) {
+                     int64_t max_pos, long long max_ctx, int ctas, int64_t *__restrict__ plan, unsigned *status, int rmax) {
   pdl_wait();
   pdl_trigger();
   const auto get = [&](int b, long long &p, int &s) { p = pos[b], s = seq[b]; };
-  const long long L = line_plan<LN, LINE_PLAN_THREADS>(get, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + LINE_PLAN, status);
+  const long long L = line_plan<LN, LINE_PLAN_THREADS>(get, B, hkv, num_seqs, max_pos, max_ctx, ctas, plan + LINE_PLAN, status, rmax,
+                                                         reinterpret_cast<uint8_t *>(plan + LINE_PLAN + B + 1));
   if (threadIdx.x == 0) plan[0] = L;
 }
 
@@ -158,18 +198,23 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
   const long long row = (long long)blockIdx.x * (LINE_MERGE_WARPS / nw) + warp / nw;  // (b hkv + kv) G + g
   const bool have = row < (long long)A.B * A.hq;
   const int g = have ? (int)(row % G) : 0, pair = have ? (int)(row / G) : 0, b = pair / hkv, kv = pair - b * hkv;
+  __shared__ uint8_t s_info[LINE_INLINE_MAX];
+  int lead = 0;  // (a row that goes with one ahead of it has its pieces among that one's)
   // The plan, while the split kernel still runs: that kernel let this one start
   // after its own wait, so the batch (and the plan kernel's plan) are there.
   long long L, at, next;
   if (A.B <= LINE_INLINE_MAX) {
     const auto get = [&](int i, long long &p, int &s) { p = ld_early_s64(A.pos + i), s = ld_early_s32(A.seq + i); };
-    L = line_plan<LN, LINE_MERGE_WARPS * 32>(get, A.B, hkv, A.num_seqs, A.max_pos, A.max_ctx, ctas, s_prefix, nullptr);
-    at = s_prefix[b];
-    next = s_prefix[b + 1];
+    L = line_plan<LN, LINE_MERGE_WARPS * 32>(get, A.B, hkv, A.num_seqs, A.max_pos, A.max_ctx, ctas, s_prefix, nullptr, A.rmax,
+                                             s_info);
+    if (LN::SHARE) lead = line_lead(s_info[b]);
+    at = s_prefix[b - lead];
+    next = s_prefix[b - lead + 1];
   } else {
     L = ld_early_s64(A.plan);
-    at = ld_early_s64(A.plan + LINE_PLAN + b);
-    next = ld_early_s64(A.plan + LINE_PLAN + b + 1);
+    if (LN::SHARE) lead = line_lead(__ldcg(reinterpret_cast<const uint8_t *>(A.plan + LINE_PLAN + A.B + 1) + b));
+    at = ld_early_s64(A.plan + LINE_PLAN + b - lead);
+    next = ld_early_s64(A.plan + LINE_PLAN + b - lead + 1);
   }
   const long long len = have ? (next - at) / hkv : 0;  // 0: nothing to attend to
   long long c0 = 0;
@@ -191,7 +236,7 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
       ml[k] = make_float2(NEG_INF, 0.f);
       o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
-        const long long r = (c0 + i + pair) * G + g;
+        const long long r = (c0 + i + pair - lead * hkv) * (A.rmax * G) + lead * G + g;
         ml[k] = *reinterpret_cast<const float2 *>(A.part_ml + r * 2);
         o[k] = *reinterpret_cast<const float4 *>(A.part_o + r * DV + 4 * lane);
       }
@@ -251,7 +296,10 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
 }
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-inline size_t line_plan_bytes(int B) { return align256(((size_t)LINE_PLAN + B + 1) * 8); }
+template <class LN>
+size_t line_plan_bytes(int B) {
+  return align256(((size_t)LINE_PLAN + B + 1) * 8 + (LN::SHARE ? B : 0));
+}
 
 // CTAs: as many as the GPU holds at once and as can have a share (of LN::MIN units at least).
 template <class LN>
@@ -275,13 +323,13 @@ size_t line_pieces(int B, int hkv, long long max_ctx) {
 
 // Workspace of a call on the line, and its parts.
 template <class LN>
-size_t line_workspace(int B, int hq, int hkv, long long max_ctx) {
-  const size_t G = (size_t)(hq / hkv), n = line_pieces<LN>(B, hkv, max_ctx);
-  return line_plan_bytes(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
+size_t line_workspace(int B, int hq, int hkv, long long max_ctx, int rmax = 1) {
+  const size_t G = (size_t)(hq / hkv) * rmax, n = line_pieces<LN>(B, hkv, max_ctx);
+  return line_plan_bytes<LN>(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
 }
 template <class LN>
 void line_args(LineArgs &A, const int64_t *pos, const int32_t *seq, int B, int hq, int hkv, int num_seqs, int64_t max_pos,
-               long long max_ctx, void *ws, uint16_t *out) {
+               long long max_ctx, void *ws, uint16_t *out, int rmax = 1) {
   A.pos = pos;
   A.seq = seq;
   A.B = B;
@@ -292,10 +340,11 @@ void line_args(LineArgs &A, const int64_t *pos, const int32_t *seq, int B, int h
   A.max_pos = max_pos;
   A.max_ctx = max_ctx;
   A.plan = reinterpret_cast<int64_t *>(ws);
-  uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + line_plan_bytes(B);
+  uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + line_plan_bytes<LN>(B);
   A.part_ml = reinterpret_cast<float *>(w8);
-  A.part_o = reinterpret_cast<float *>(w8 + align256(line_pieces<LN>(B, hkv, max_ctx) * A.G * 2 * sizeof(float)));
+  A.part_o = reinterpret_cast<float *>(w8 + align256(line_pieces<LN>(B, hkv, max_ctx) * A.G * rmax * 2 * sizeof(float)));
   A.out = out;
+  A.rmax = rmax;
 }
 
 // The launches of a call on the line: the plan where the CTAs do not make it
@@ -306,7 +355,7 @@ cudaError_t line_launch(void (*kernel)(Args), int threads, size_t smem, const Ar
   cudaError_t e;
   if (A.B > LINE_INLINE_MAX) {
     e = launch_pdl(line_plan_kernel<LN>, dim3(1), dim3(LINE_PLAN_THREADS), 0, st, A.pos, A.seq, A.B, A.hkv, A.num_seqs,
-                   A.max_pos, A.max_ctx, ctas, A.plan, status);
+                   A.max_pos, A.max_ctx, ctas, A.plan, status, A.rmax);
     if (e != cudaSuccess) return e;
   }
   e = launch_pdl(kernel, dim3((unsigned)ctas), dim3((unsigned)threads), smem, st, A);

@@ -331,6 +331,60 @@ def test_decode_draft_rows_share_a_sequence(table):
     _check_decode(out, q, pos, seq, pool, table)
 
 
+@pytest.mark.parametrize("most", [1025, 9000])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 7, 8, 9, 16])
+def test_decode_rows_of_one_sequence_go_together(table, G, most):
+    """Neighbouring rows of one sequence are taken together, in aligned blocks of the batch: drafts of every length at
+    every place of a block, rows far apart or in any order, the same row twice, rows that cannot be served between, a
+    sequence that comes again later."""
+    gen = _gen(33 + G)
+    lens, hkv = [70, 300, 1025, 5, 16], 2
+    pool = _filled(gen, lens, hkv, 32, table, max_ctx=most)
+    rows = [(0, 66), (0, 67), (0, 68), (1, 299), (2, 1020), (2, 1021), (2, 1022), (2, 1023), (2, 1024), (2, 0), (2, 1024),
+            (2, 1024), (9, 5), (2, 512), (2, most), (2, 3), (3, 0), (3, 4), (4, 15), (-1, 0), (4, 14), (4, 14), (1, 16), (1, 15),
+            (1, 31), (0, 69), (0, 0), (2, 15), (2, 16), (2, 700), (2, 17)]
+    q = torch.randn(len(rows), hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    out = torch.full((len(rows), hkv * G, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    kvr.full_attn_decode_kv8(q, _ints([p for _, p in rows], torch.int64), _ints([s for s, _ in rows], torch.int32), pool, table,
+                             SCALE, most, out=out)
+    assert kvr.device_status() == kvr.DEV_BAD_POS | kvr.DEV_BAD_SEQ
+    bad = [i for i, (s, p) in enumerate(rows) if not 0 <= s < 5 or p >= most]
+    assert len(bad) == 3 and not out[bad].any()
+    good = [i for i in range(len(rows)) if i not in bad]
+    _check_decode(out[good], q[good], [rows[i][1] for i in good], [rows[i][0] for i in good], pool, table)
+    # a NaN in a key or value row reaches exactly the rows that see it, a NaN in a query its own head
+    k, v = _kv(gen, 1025 - 700, hkv)
+    k[0, 0, 100] = v[1, 1, 3] = float("nan")      # positions 700 and 701 of sequence 2
+    _append(pool, k, v, [2], [700], [325], table)
+    q[5, hkv * G - 1, 64] = float("inf")
+    out = kvr.full_attn_decode_kv8(q, _ints([p for _, p in rows], torch.int64), _ints([s for s, _ in rows], torch.int32), pool,
+                                   table, SCALE, most)
+    kvr.device_status()
+    want = torch.zeros_like(out, dtype=torch.bool)
+    for i, (s, p) in enumerate(rows):
+        if s == 2 and i not in bad:
+            want[i, :G] = p >= 700
+            want[i, G:] = p >= 701
+    want[5, -1] = True
+    assert torch.equal(torch.isnan(out), want)
+
+
+@pytest.mark.parametrize("C,G,B", [(2, 16, 9), (3, 8, 70), (4, 4, 40), (4, 16, 70)])
+def test_decode_drafts_of_long_contexts(table, C, G, B):
+    """Drafts of many sequences, on the work line, planned by the split kernel's CTAs or by a kernel of their own."""
+    gen = _gen(C * G + B)
+    hkv = 2
+    lens = torch.randint(C, 6000, (B,), generator=gen, device=DEV).tolist()
+    pool = _filled(gen, lens, hkv, 64, table, max_ctx=6000)
+    pos = [n - C + c for n in lens for c in range(C)]
+    seq = [s for s in range(B) for _ in range(C)]
+    q = torch.randn(B * C, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    out = kvr.full_attn_decode_kv8(q, _ints(pos, torch.int64), _ints(seq, torch.int32), pool, table, SCALE, 6000)
+    assert kvr.device_status() == 0
+    few = list(range(3 * C)) + list(range(B * C - 2 * C, B * C))
+    _check_decode(out[few], q[few], [pos[i] for i in few], [seq[i] for i in few], pool, table)
+
+
 @pytest.mark.parametrize("G", [8, 16])
 @pytest.mark.parametrize("vscales", [(1e-6,), (2e4,), (1.0, 1e-5, 3e3, 1e-2), (1e-3, 6e4), (1e-30, 1.0, 1e28), (0.0, 1.0)])
 def test_decode_value_scales_apart(table, vscales, G):
