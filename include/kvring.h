@@ -739,9 +739,6 @@ kvr_status kv_pages_fork(int32_t *block_table, int32_t num_seqs, int32_t max_blo
                          int32_t *free_count_out, int32_t free_cap, int32_t *copy_src, int32_t *copy_dst,
                          int32_t *copy_count, void *stream);
 
-/* Workspace bytes for kv_pages_compact (0 on bad arguments). */
-size_t kv_pages_compact_workspace_size(int32_t num_blocks);
-
 /*
  * kv_pages_compact: the pool's used blocks (those that are not in the free list)
  * are brought below `limit`, so that it can end there; limit = 0 means as low as
@@ -755,14 +752,12 @@ size_t kv_pages_compact_workspace_size(int32_t num_blocks);
  * the array it is made from.  A limit below the number of used blocks
  * (KVR_DEV_NO_BLOCKS), or a free list that names a block twice or none of the
  * pool's (KVR_DEV_BAD_BLOCK), moves nothing: the outputs are the inputs and
- * copy_count is 0.  workspace: kv_pages_compact_workspace_size(num_blocks) bytes,
- * 16-byte aligned, no initialisation.
+ * copy_count is 0.  num_blocks <= 2^20 (KVR_EUNSUPPORTED).
  */
 kvr_status kv_pages_compact(const int32_t *block_table, int32_t *block_table_out, int32_t num_seqs, int32_t max_blocks,
                             int32_t num_blocks, int32_t limit, const int32_t *refs, int32_t *refs_out,
                             const int32_t *free_ids, const int32_t *free_count, int32_t *free_ids_out, int32_t free_cap,
-                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *workspace,
-                            size_t workspace_bytes, void *stream);
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *stream);
 
 /*
  * kv_pages_copy: block copy_src[k] is copied to copy_dst[k] for k < min(*copy_count,

@@ -52,7 +52,7 @@ __all__ = [
     "Kv4Layout", "kv4_append_rope", "full_attn_decode_kv4", "full_attn_decode_kv4_workspace_size", "kv4_unpack",
     "kv_pages_grow",
     "Kv8Layout", "kv8_append_rope", "full_attn_decode_kv8", "full_attn_decode_kv8_workspace_size", "kv8_unpack",
-    "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_compact_workspace_size", "kv_pages_copy",
+    "kv_pages_fork", "kv_pages_free", "kv_pages_compact", "kv_pages_copy",
     "DQK", "DV", "DROT", "WINDOW",
 ]
 
@@ -175,11 +175,8 @@ def lib():
                 L.kv_pages_free.argtypes = [p, i32, i32, i32, i32, p, p, p, p, i32, p, p, i32, p]
                 L.kv_pages_fork.restype = ctypes.c_int
                 L.kv_pages_fork.argtypes = [p, i32, i32, i32, i32, p, p, p, p, i32, p, p, p, i32, p, p, p, p]
-                L.kv_pages_compact_workspace_size.restype = ctypes.c_size_t
-                L.kv_pages_compact_workspace_size.argtypes = [i32]
                 L.kv_pages_compact.restype = ctypes.c_int
-                L.kv_pages_compact.argtypes = [p, p, i32, i32, i32, i32, p, p, p, p, p, i32, p, p, p, p,
-                                               ctypes.c_size_t, p]
+                L.kv_pages_compact.argtypes = [p, p, i32, i32, i32, i32, p, p, p, p, p, i32, p, p, p, p]
                 L.kv_pages_copy.restype = ctypes.c_int
                 L.kv_pages_copy.argtypes = [p, p, i32, i32, p, p, p, i32, p]
                 _lib = L
@@ -940,12 +937,8 @@ def kv_pages_fork(block_table, num_blocks, block_size, refs, src_seqs, dst_seqs,
                                free_ids.shape[0], _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream)))
 
 
-def kv_pages_compact_workspace_size(num_blocks) -> int:
-    return int(lib().kv_pages_compact_workspace_size(int(num_blocks)))
-
-
 def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_src, copy_dst, copy_count, limit=0,
-                     table_out=None, refs_out=None, free_ids_out=None, workspace=None, stream=None):
+                     table_out=None, refs_out=None, free_ids_out=None, stream=None):
     """The pool's used blocks move below `limit` (0: as low as they fit): the
     copies to be made (kv_pages_copy) are copy_src[k] -> copy_dst[k] (int32,
     num_blocks // 2 entries), copy_count (int32 [1]) of them; block_table, refs
@@ -965,16 +958,11 @@ def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_s
             if t.shape != src.shape:
                 raise ValueError(f"{name} must have the shape {tuple(src.shape)}, got {tuple(t.shape)}")
         outs.append(t)
-    if workspace is None:
-        workspace = _empty(max(kv_pages_compact_workspace_size(num_blocks), 1), torch.uint8, refs, stream)
-    else:
-        _want(workspace, "workspace", torch.uint8, 1)
     S, mb = block_table.shape
-    _same_device(block_table, refs, free_ids, free_count, copy_src, copy_dst, copy_count, workspace, *outs)
+    _same_device(block_table, refs, free_ids, free_count, copy_src, copy_dst, copy_count, *outs)
     _check(lib().kv_pages_compact(_ptr(block_table), _ptr(outs[0]), S, mb, int(num_blocks), int(limit), _ptr(refs),
                                   _ptr(outs[1]), _ptr(free_ids), _ptr(free_count), _ptr(outs[2]), free_ids.shape[0],
-                                  _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)))
+                                  _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream)))
 
 
 def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):

@@ -864,29 +864,23 @@ kvr_status kv_pages_fork(int32_t *block_table, int32_t num_seqs, int32_t max_blo
   return ok();
 }
 
-size_t kv_pages_compact_workspace_size(int32_t num_blocks) { return num_blocks < 1 ? 0 : sizeof(int32_t) * (size_t)num_blocks; }
-
 kvr_status kv_pages_compact(const int32_t *block_table, int32_t *block_table_out, int32_t num_seqs, int32_t max_blocks,
                             int32_t num_blocks, int32_t limit, const int32_t *refs, int32_t *refs_out,
                             const int32_t *free_ids, const int32_t *free_count, int32_t *free_ids_out, int32_t free_cap,
-                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *workspace,
-                            size_t workspace_bytes, void *stream) {
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *stream) {
   const char *who = "kv_pages_compact";
   kvr_status s = check_pages(who, block_table, num_seqs, max_blocks, num_blocks, refs, free_ids, free_count, free_cap);
   if (s) return s;
+  if (num_blocks > kvr::COMPACT_MAX_BLOCKS) return fail(KVR_EUNSUPPORTED, "%s: num_blocks %d > 2^20", who, num_blocks);
   if (limit < 0) return fail(KVR_EINVAL, "%s: limit %d", who, limit);
   if (!block_table_out || !refs_out || !copy_src || !copy_dst || !copy_count || (free_cap > 0 && !free_ids_out))
     return fail(KVR_EINVAL, "%s: block_table_out/refs_out/free_ids_out/copy_src/copy_dst/copy_count is NULL", who);
-  const size_t need = kv_pages_compact_workspace_size(num_blocks);
-  if (!workspace || workspace_bytes < need)
-    return fail(KVR_EWORKSPACE, "workspace %zu bytes, need %zu", workspace ? workspace_bytes : (size_t)0, need);
-  if (!aligned16(workspace)) return fail(KVR_EINVAL, "workspace not 16-byte aligned");
   unsigned *st = nullptr;
   cudaError_t e = status_ptr(&st, stream);
   if (e != cudaSuccess) return state_fail(e, who);
   e = kvr::launch_pages_compact(block_table, block_table_out, (long long)num_seqs * max_blocks, num_blocks, limit, refs,
                                 refs_out, free_ids, free_count, free_ids_out, free_cap, copy_src, copy_dst, copy_count,
-                                static_cast<int32_t *>(workspace), st, as_stream(stream));
+                                st, as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_pages_compact launch");
   return ok();
 }

@@ -231,6 +231,7 @@ cudaError_t launch_kv8_unpack(const Kv8View &src, const int32_t *src_seqs, const
 // Shared pages (pages_share.cu) and the copies that follow (pages_copy.cu).
 constexpr int FORK_MAX_N = 8192;         // entries of one kv_pages_fork call (their places lie in shared memory)
 constexpr int PAGES_MAX_BLOCKS = 1 << 30;
+constexpr int COMPACT_MAX_BLOCKS = 1 << 20;  // of a pool that kv_pages_compact takes (its free blocks lie in shared memory)
 constexpr int PAGES_COPY_PLANES = 96;    // arrays of one copy launch (more take more launches)
 cudaError_t launch_pages_free(int32_t *table, int num_seqs, int max_blocks, int block_size, int num_blocks, int32_t *refs,
                               const int32_t *seqs, const int64_t *keep_lo, const int64_t *keep_hi, int n,
@@ -243,8 +244,7 @@ cudaError_t launch_pages_fork(int32_t *table, int num_seqs, int max_blocks, int 
 cudaError_t launch_pages_compact(const int32_t *table, int32_t *table_out, long long entries, int num_blocks, int limit,
                                  const int32_t *refs, int32_t *refs_out, const int32_t *free_ids,
                                  const int32_t *free_count, int32_t *free_out, int free_cap, int32_t *copy_src,
-                                 int32_t *copy_dst, int32_t *copy_count, int32_t *map, unsigned *status,
-                                 cudaStream_t st);
+                                 int32_t *copy_dst, int32_t *copy_count, unsigned *status, cudaStream_t st);
 cudaError_t launch_pages_copy(uint8_t *const *data, const long long *bytes, int planes, int num_blocks,
                               const int32_t *src, const int32_t *dst, const int32_t *count, int n, unsigned *status,
                               cudaStream_t st);

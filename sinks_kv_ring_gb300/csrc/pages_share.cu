@@ -10,9 +10,12 @@
 // blocks at -1, in ascending order, go to the free list -- an order that does not
 // hang on which holder came first, so atomics decide nothing.
 //
-// Each call is one cluster of SH_CTAS CTAs (the table entries that a call reads
-// may be spread over more of them first): the steps of a call wait for one
-// another, and a cluster's barrier is cheaper than a launch.
+// Each call is one cluster of CTAs (or one CTA, where there is little to do: its
+// barrier is cheaper): the steps of a call wait for one another, and a cluster's
+// barrier is cheaper than a launch.
+//
+// What bounds them: the latency of a launch and of a few dependent loads and
+// atomics, and a microsecond for each barrier of a cluster.
 #include <cooperative_groups.h>
 
 #include "launch.h"
@@ -22,9 +25,24 @@ namespace {
 
 constexpr int SH_CTAS = 8;
 constexpr int SH_THREADS = 1024;
-constexpr int SH_ALL = SH_CTAS * SH_THREADS;
 constexpr int SH_WARPS = SH_THREADS / 32;
+constexpr int SH_SMALL = 4;  // rounds of one CTA's threads up to which it does a call alone
 constexpr unsigned FULLW = 0xffffffffu;
+
+// Barrier of the call's CTAs: all that they wrote, to global memory too, is seen behind it.
+template <int CTAS>
+__device__ __forceinline__ void call_sync() {
+  if (CTAS == 1) {
+    __syncthreads();
+  } else {
+    __threadfence();
+    cooperative_groups::this_cluster().sync();
+  }
+}
+template <int CTAS>
+__device__ __forceinline__ int call_rank() {
+  return CTAS == 1 ? 0 : (int)cooperative_groups::this_cluster().block_rank();
+}
 
 // Exclusive prefix of x over the CTA's threads, in order; `total` is their sum.
 __device__ __forceinline__ int cta_prefix(int x, int &total) {
@@ -39,43 +57,34 @@ __device__ __forceinline__ int cta_prefix(int x, int &total) {
   __syncthreads();  // s_sum of the call before is read
   if (lane == 31) s_sum[warp] = y;
   __syncthreads();
-  int before = 0, all = s_sum[lane];
+  // every warp takes the sums' prefix
+  int z = s_sum[lane];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(FULLW, all, o);
-  for (int w = 0; w < warp; ++w) before += s_sum[w];
-  total = all;
-  return before + y - x;
-}
-
-// Sums of two counts of every CTA ahead of this one in the cluster, and of all of them.
-struct Two {
-  int a, b;
-};
-__device__ __forceinline__ void cluster_prefix(int a, int b, Two &before, Two &all) {
-  __shared__ Two s_mine;
-  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-  cl.sync();  // the counts of the call before are read
-  if (threadIdx.x == 0) s_mine = Two{a, b};
-  cl.sync();
-  before = all = Two{0, 0};
-  for (int r = 0; r < SH_CTAS; ++r) {
-    const Two x = *cl.map_shared_rank(&s_mine, r);
-    if (r < (int)cl.block_rank()) {
-      before.a += x.a;
-      before.b += x.b;
-    }
-    all.a += x.a;
-    all.b += x.b;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULLW, z, o);
+    if (lane >= o) z += v;
   }
-  cl.sync();  // (no CTA leaves while another reads its count)
+  total = __shfl_sync(FULLW, z, 31);
+  const int before = __shfl_sync(FULLW, z, (warp + 31) & 31);
+  return (warp ? before : 0) + y - x;
 }
-
-// This CTA's blocks: [lo, hi) of num_blocks, in the cluster's order.
-__device__ __forceinline__ void my_blocks(int num_blocks, int &lo, int &hi) {
-  const int rank = (int)cooperative_groups::this_cluster().block_rank();
-  const int each = (num_blocks + SH_CTAS - 1) / SH_CTAS;
-  lo = (int)min((long long)rank * each, (long long)num_blocks);
-  hi = (int)min((long long)lo + each, (long long)num_blocks);
+// The same for a truth value: two ballots in place of the shuffles.
+__device__ __forceinline__ int cta_rank(bool x, int &total) {
+  __shared__ int s_sum[SH_WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned m = __ballot_sync(FULLW, x);
+  __syncthreads();
+  if (lane == 0) s_sum[warp] = __popc(m);
+  __syncthreads();
+  int z = s_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULLW, z, o);
+    if (lane >= o) z += v;
+  }
+  total = __shfl_sync(FULLW, z, 31);
+  const int before = __shfl_sync(FULLW, z, (warp + 31) & 31);
+  return (warp ? before : 0) + __popc(m & ((1u << lane) - 1u));
 }
 
 struct FreeArgs {
@@ -124,43 +133,72 @@ __global__ void __launch_bounds__(SH_THREADS) pages_drop_kernel(FreeArgs A) {
   drop_entries(A, (long long)blockIdx.x * SH_THREADS + threadIdx.x, (long long)gridDim.x * SH_THREADS);
 }
 
-template <bool DROP>
-__global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pages_free_kernel(FreeArgs A) {
+template <int CTAS, bool DROP>
+__device__ __forceinline__ void pages_free_body(const FreeArgs &A) {
   pdl_wait();
   pdl_trigger();
-  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-  const int tid = threadIdx.x;
-  if (DROP) {
-    drop_entries(A, (long long)cl.block_rank() * SH_THREADS + tid, SH_ALL);
-    __threadfence();
-    cl.sync();
-  }
-  // blocks without a holder: counted, then listed in order
-  int lo, hi;
-  my_blocks(A.num_blocks, lo, hi);
-  int mine = 0;
-  for (int b0 = lo; b0 < hi; b0 += SH_THREADS) mine += __syncthreads_count(b0 + tid < hi && __ldcg(A.refs + b0 + tid) < 0);
+  const int tid = threadIdx.x, rank = call_rank<CTAS>();
   const int count = *A.free_count;
-  Two before, all;
-  cluster_prefix(mine, 0, before, all);  // (every CTA has read the count)
-  if (all.a == 0) return;
-  if (count < 0 || (long long)count + all.a > A.free_cap) {
-    if (cl.block_rank() == 0 && tid == 0) flag(A.status, ST_FREE_FULL);
-    return;
+  if (DROP) {
+    drop_entries(A, (long long)rank * SH_THREADS + tid, CTAS * SH_THREADS);
+    call_sync<CTAS>();
   }
-  int at = count + before.a;
+  // blocks without a holder: counted by the CTA that sees to them, then listed in order
+  const int each = (A.num_blocks + CTAS - 1) / CTAS;
+  const int lo = (int)min((long long)rank * each, (long long)A.num_blocks), hi = (int)min((long long)lo + each, (long long)A.num_blocks);
+  __shared__ int s_mine;
+  int before = 0, all = 0;
+  if (CTAS > 1) {
+    cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+    int mine = 0;
+    for (int b0 = lo; b0 < hi; b0 += 4 * SH_THREADS) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int b = b0 + u * SH_THREADS + tid;
+        mine += b < hi && __ldcg(A.refs + b) < 0;
+      }
+    }
+    int total;
+    cta_prefix(mine, total);
+    if (tid == 0) s_mine = total;
+    cl.sync();  // (and every CTA has read the count)
+    for (int r = 0; r < CTAS; ++r) {
+      const int x = *cl.map_shared_rank(&s_mine, r);
+      before += r < rank ? x : 0;
+      all += x;
+    }
+    cl.sync();  // (no CTA leaves while another reads its count)
+    if (all == 0) return;
+    if (count < 0 || (long long)count + all > A.free_cap) {
+      if (rank == 0 && tid == 0) flag(A.status, ST_FREE_FULL);
+      return;
+    }
+  } else {
+    for (int b0 = 0; b0 < hi; b0 += SH_THREADS) all += __syncthreads_count(b0 + tid < hi && __ldcg(A.refs + b0 + tid) < 0);
+    if (all == 0) return;
+    if (count < 0 || (long long)count + all > A.free_cap) {
+      if (tid == 0) flag(A.status, ST_FREE_FULL);
+      return;
+    }
+  }
+  int at = count + before;
   for (int b0 = lo; b0 < hi; b0 += SH_THREADS) {
     const bool dead = b0 + tid < hi && __ldcg(A.refs + b0 + tid) < 0;
     int total;
-    const int k = cta_prefix(dead ? 1 : 0, total);
+    const int k = cta_rank(dead, total);
     if (dead) {
       A.free_ids[at + k] = b0 + tid;
       A.refs[b0 + tid] = 0;
     }
     at += total;
   }
-  if (cl.block_rank() == 0 && tid == 0) *A.free_count = count + all.a;
+  if (rank == 0 && tid == 0) *A.free_count = count + all;
 }
+template <bool DROP>
+__global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pages_free_kernel(FreeArgs A) {
+  pages_free_body<SH_CTAS, DROP>(A);
+}
+__global__ void __launch_bounds__(SH_THREADS) pages_free_one_kernel(FreeArgs A) { pages_free_body<1, true>(A); }
 
 struct ForkArgs {
   int32_t *table;
@@ -176,12 +214,12 @@ struct ForkArgs {
   unsigned *status;
 };
 
-__global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pages_fork_kernel(ForkArgs A) {
+template <int CTAS>
+__device__ __forceinline__ void pages_fork_body(const ForkArgs &A) {
   extern __shared__ int32_t s_tail[];  // [n] entry i's new block: its number in the call, or -1 (none) or -2 (not served)
   pdl_wait();
   pdl_trigger();
-  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, rank = call_rank<CTAS>();
   const int count = *A.count_in;
   const long long cap_pos = (long long)A.max_blocks * A.block_size;
   int need = 0;
@@ -197,7 +235,7 @@ __global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pa
       else code = len % A.block_size ? 0 : -1;
     }
     int total;
-    const int k = cta_prefix(code == 0, total);
+    const int k = cta_rank(code == 0, total);
     if (i < A.n) s_tail[i] = code == 0 ? need + k : code;
     need += total;
   }
@@ -208,7 +246,7 @@ __global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pa
     if (tid == 0 && none) flag(A.status, ST_NO_BLOCKS);
   }
   if (!none) {
-    for (int i = rank * SH_WARPS + (tid >> 5); i < A.n; i += SH_CTAS * SH_WARPS) {  // a warp an entry
+    for (int i = rank * SH_WARPS + (tid >> 5); i < A.n; i += CTAS * SH_WARPS) {  // a warp an entry
       const int k = s_tail[i];
       if (k == -2) continue;
       const int32_t *from = A.table + (long long)A.src_seqs[i] * A.max_blocks;
@@ -236,14 +274,21 @@ __global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pa
       }
     }
   }
-  cl.sync();  // every CTA has read the free count
+  call_sync<CTAS>();  // every CTA has read the free count
   if (rank == 0 && tid == 0) {
     *A.copy_count = none ? 0 : need;
     *A.count_out = none ? count : count - need;
   }
 }
+__global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pages_fork_kernel(ForkArgs A) {
+  pages_fork_body<SH_CTAS>(A);
+}
+__global__ void __launch_bounds__(SH_THREADS) pages_fork_one_kernel(ForkArgs A) { pages_fork_body<1>(A); }
 
 struct CompactArgs {
+  const int32_t *table;
+  int32_t *table_out;
+  long long entries;
   int num_blocks, limit;
   const int32_t *refs;
   int32_t *refs_out;
@@ -251,100 +296,137 @@ struct CompactArgs {
   int32_t *free_out;
   int free_cap;
   int32_t *copy_src, *copy_dst, *copy_count;
-  int32_t *map;  // [num_blocks]: a block's id afterwards, -1 where it is free
   unsigned *status;
 };
 
+// The free blocks of a pool as bits in shared memory, and how many there are below
+// any id: per 32 words (1024 blocks) the total before them, per word the number
+// since those (16 bits).  Six bytes for 32 blocks.
+struct FreeSet {
+  uint32_t *bits;    // [groups * 32]
+  int *group;        // [groups + 1]
+  uint16_t *since;   // [groups * 32]
+  int groups;
+  __device__ __forceinline__ bool has(int b) const { return bits[b >> 5] >> (b & 31) & 1; }
+  __device__ __forceinline__ int below(int b) const {  // b < 1024 groups
+    return group[b >> 10] + since[b >> 5] + __popc(bits[b >> 5] & ((1u << (b & 31)) - 1u));
+  }
+  __device__ __forceinline__ int nth(int k) const {  // the k-th free block (k < their number)
+    int lo = 0, hi = groups;  // group[lo] <= k < group[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (group[mid] <= k) lo = mid; else hi = mid;
+    }
+    k -= group[lo];
+    int w = lo * 32;
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+      if (since[w + step] <= k) w += step;
+    k -= since[w];
+    uint32_t x = bits[w];
+    for (; k > 0; --k) x &= x - 1;
+    return w * 32 + __ffs(x) - 1;
+  }
+};
+
+// Every CTA makes the whole set of free blocks by itself, so where a block goes is
+// known everywhere without a word between the CTAs: the k-th used block at or past
+// the limit takes the k-th free place.  The one barrier stands between the last
+// read of the free list and its new form, which may be in place.
 __global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pages_compact_kernel(CompactArgs A) {
+  extern __shared__ uint32_t s_set[];
+  __shared__ int s_wrong;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, num = A.num_blocks;
+  FreeSet F;
+  F.groups = (num + 1023) >> 10;
+  F.bits = s_set;
+  F.group = reinterpret_cast<int *>(s_set + F.groups * 32);
+  F.since = reinterpret_cast<uint16_t *>(F.group + F.groups + 1);
+  for (int w = tid; w < F.groups * 32; w += SH_THREADS) F.bits[w] = 0;
+  if (tid == 0) s_wrong = 0;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cl.block_rank(), me = rank * SH_THREADS + tid, num = A.num_blocks;
+  const int me = call_rank<SH_CTAS>() * SH_THREADS + tid;
+  constexpr int ALL = SH_CTAS * SH_THREADS;
   const int count = *A.free_count;
   const bool sane = count >= 0 && count <= A.free_cap && count <= num;
-  for (long long b = me; b < num; b += SH_ALL) A.map[b] = (int)b;
-  __threadfence();
-  cl.sync();
-  if (sane)
-    for (int j = me; j < count; j += SH_ALL) {
+  // a free list that names a block twice, or none of the pool's, moves nothing
+  bool odd = !sane;
+  for (int j0 = tid; sane && j0 < count; j0 += 4 * SH_THREADS) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * SH_THREADS;
+      if (j >= count) break;
       const int id = A.free_ids[j];
-      if (id >= 0 && id < num) A.map[id] = -1;
+      if (id < 0 || id >= num) odd = true;
+      else odd |= atomicOr(F.bits + (id >> 5), 1u << (id & 31)) >> (id & 31) & 1;
     }
-  __threadfence();
-  cl.sync();
-  int lo, hi;
-  my_blocks(num, lo, hi);
-  int mine = 0;
-  for (int b0 = lo; b0 < hi; b0 += SH_THREADS) mine += __syncthreads_count(b0 + tid < hi && __ldcg(A.map + b0 + tid) < 0);
-  Two before, all;
-  cluster_prefix(mine, 0, before, all);
-  const int used = num - all.a, limit = A.limit > 0 ? min(A.limit, num) : used;
-  // a free list that names a block twice or none of the pool's, or a limit below what is used: nothing moves
-  const bool wrong = !sane || all.a != count, low = !wrong && limit < used, none = wrong || low;
+  }
+  if (odd) s_wrong = 1;
+  call_sync<SH_CTAS>();  // (every CTA has read the list)
+  for (int g = warp; g < F.groups; g += SH_WARPS) {
+    const int n = __popc(F.bits[g * 32 + lane]);
+    int y = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(FULLW, y, o);
+      if (lane >= o) y += z;
+    }
+    F.since[g * 32 + lane] = (uint16_t)(y - n);
+    if (lane == 31) F.group[g] = y;
+  }
+  __syncthreads();
+  int sum;  // (up to 1024 groups: one each)
+  const int mine = tid < F.groups ? F.group[tid] : 0, before = cta_prefix(mine, sum);
+  if (tid < F.groups) F.group[tid] = before;
+  if (tid == 0) F.group[F.groups] = sum;
+  __syncthreads();
+  const bool wrong = s_wrong != 0;
+  const int used = num - sum, limit = A.limit > 0 ? min(A.limit, num) : used;
+  const bool none = wrong || limit < used;
   if (me == 0 && none) flag(A.status, wrong ? ST_BAD_BLOCK : ST_NO_BLOCKS);
-  // holes below the limit, and used blocks at or past it, in order: the k-th of these goes to the k-th hole
-  int holes = 0, movers = 0;
-  for (int b0 = lo; b0 < hi; b0 += SH_THREADS) {
-    const int b = b0 + tid;
-    const bool gone = b < hi && __ldcg(A.map + b) < 0;
-    holes += __syncthreads_count(b < hi && gone && b < limit);
-    movers += __syncthreads_count(b < hi && !gone && b >= limit);
-  }
-  cluster_prefix(holes, movers, before, all);
-  const int M = none ? 0 : all.b, H = all.a;
-  int ha = before.a, ma = before.b;
-  for (int b0 = lo; b0 < hi; b0 += SH_THREADS) {
-    const int b = b0 + tid;
-    const bool gone = b < hi && __ldcg(A.map + b) < 0;
-    const bool hole = b < hi && gone && b < limit, mover = b < hi && !gone && b >= limit;
-    int th, tm;
-    const int kh = ha + cta_prefix(hole, th), km = ma + cta_prefix(mover, tm);
-    ha += th;
-    ma += tm;
-    if (!none) {
-      if (hole && kh < M) A.copy_dst[kh] = b;
-      if (mover) A.copy_src[km] = b;
-      // the free list afterwards, in descending order: the lowest ids are taken first
-      if (b < hi && b >= limit) A.free_out[num - 1 - b] = b;
-      if (hole && kh >= M) A.free_out[num - limit + H - 1 - kh] = b;
-      if (hole && kh >= M) A.refs_out[b] = 0;
-      if (mover) A.map[b] = -2 - km;  // (its place is looked up when all are known)
-      else if (b < hi && !gone) A.refs_out[b] = A.refs[b];
-      else if (b < hi && b >= limit) A.refs_out[b] = 0;
-    }
-  }
   if (none) {  // as it was
-    for (long long b = me; b < num; b += SH_ALL) {
+    for (long long b = me; b < num; b += ALL) {
       if (A.refs_out != A.refs) A.refs_out[b] = A.refs[b];
       if (A.free_out != A.free_ids && sane && b < count) A.free_out[b] = A.free_ids[b];
-      A.map[b] = (int)b;
+    }
+    if (A.table_out != A.table)
+      for (long long e = me; e < A.entries; e += ALL) A.table_out[e] = A.table[e];
+    if (me == 0) *A.copy_count = 0;
+    return;
+  }
+  const int H = limit < num ? F.below(limit) : sum, M = used - (limit - H);  // free places below the limit; blocks that move
+  for (long long bb = me; bb < num; bb += ALL) {
+    const int b = (int)bb, k = F.below(b);
+    const bool gone = F.has(b);
+    // the free list afterwards, in descending order: all from the limit on, then what is left below it
+    if (b >= limit) {
+      A.free_out[num - 1 - b] = b;
+      if (!gone) {
+        const int m = b - limit - (k - H), to = F.nth(m), r = A.refs[b];
+        A.copy_src[m] = b;
+        A.copy_dst[m] = to;
+        A.refs_out[to] = r;  // (nobody else writes a place that is taken)
+      }
+      A.refs_out[b] = 0;
+    } else if (!gone) {
+      if (A.refs_out != A.refs) A.refs_out[b] = A.refs[b];
+    } else if (k >= M) {
+      A.free_out[num - limit + H - 1 - k] = b;
+      A.refs_out[b] = 0;
     }
   }
-  __threadfence();
-  cl.sync();
-  for (int b = lo + tid; b < hi && M > 0; b += SH_THREADS) {
-    const int x = __ldcg(A.map + b);
-    if (x > -2) continue;
-    const int to = __ldcg(A.copy_dst + (-2 - x));
-    A.map[b] = to;
-    // (the hole's own thread wrote nothing there; in place, the old word is read ahead of its zero)
-    const int r = A.refs[b];
-    A.refs_out[to] = r;
-    A.refs_out[b] = 0;
+  // table entries after the move; one that names a free block names none
+  for (long long e = me; e < A.entries; e += ALL) {
+    int id = A.table[e];
+    if (id >= 0 && id < num) {
+      if (F.has(id)) id = -1;
+      else if (id >= limit) id = F.nth(id - limit - (F.below(id) - H));
+    }
+    A.table_out[e] = id;
   }
   if (me == 0) *A.copy_count = M;
-}
-
-// Table entries after the move; one that names a free block names none.
-__global__ void __launch_bounds__(256)
-    pages_remap_kernel(const int32_t *table, int32_t *table_out, long long entries, const int32_t *__restrict__ map, int num) {
-  pdl_wait();
-  pdl_trigger();
-  const long long step = (long long)gridDim.x * blockDim.x;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < entries; e += step) {
-    const int id = table[e];
-    table_out[e] = id >= 0 && id < num ? map[id] : id;
-  }
 }
 
 }  // namespace
@@ -354,8 +436,10 @@ cudaError_t launch_pages_free(int32_t *table, int num_seqs, int max_blocks, int 
                               int32_t *free_ids, int32_t *free_count, int free_cap, unsigned *status, cudaStream_t st) {
   const FreeArgs A{table, num_seqs, max_blocks, block_size, num_blocks, refs, seqs, keep_lo, keep_hi, n, free_ids,
                    free_count, free_cap, status};
-  // many entries: spread over the GPU by a launch of their own first
   const long long warps = (long long)n * ((max_blocks + 31) / 32), ctas = (warps + SH_WARPS - 1) / SH_WARPS;
+  if (ctas <= SH_SMALL && num_blocks <= SH_SMALL * SH_THREADS)
+    return launch_pdl(pages_free_one_kernel, dim3(1), dim3(SH_THREADS), 0, st, A);
+  // many entries: spread over the GPU by a launch of their own first
   if (ctas <= 4 * SH_CTAS) return launch_pdl(pages_free_kernel<true>, dim3(SH_CTAS), dim3(SH_THREADS), 0, st, A);
   const long long most = 2LL * num_sms();
   cudaError_t e = launch_pdl(pages_drop_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(SH_THREADS), 0, st, A);
@@ -370,21 +454,24 @@ cudaError_t launch_pages_fork(int32_t *table, int num_seqs, int max_blocks, int 
                               cudaStream_t st) {
   const ForkArgs A{table, num_seqs, max_blocks, block_size, num_blocks, refs, src_seqs, dst_seqs, lens, n, free_ids,
                    count_in, count_out, free_cap, copy_src, copy_dst, copy_count, status};
+  if ((long long)n * ((max_blocks + 31) / 32) <= SH_SMALL * SH_WARPS)
+    return launch_pdl(pages_fork_one_kernel, dim3(1), dim3(SH_THREADS), sizeof(int32_t) * (size_t)n, st, A);
   return launch_pdl(pages_fork_kernel, dim3(SH_CTAS), dim3(SH_THREADS), sizeof(int32_t) * (size_t)n, st, A);
 }
 
 cudaError_t launch_pages_compact(const int32_t *table, int32_t *table_out, long long entries, int num_blocks, int limit,
                                  const int32_t *refs, int32_t *refs_out, const int32_t *free_ids,
                                  const int32_t *free_count, int32_t *free_out, int free_cap, int32_t *copy_src,
-                                 int32_t *copy_dst, int32_t *copy_count, int32_t *map, unsigned *status,
-                                 cudaStream_t st) {
-  const CompactArgs A{num_blocks, limit, refs, refs_out, free_ids, free_count, free_out, free_cap, copy_src, copy_dst,
-                      copy_count, map, status};
-  cudaError_t e = launch_pdl(pages_compact_kernel, dim3(SH_CTAS), dim3(SH_THREADS), 0, st, A);
+                                 int32_t *copy_dst, int32_t *copy_count, unsigned *status, cudaStream_t st) {
+  const CompactArgs A{table, table_out, entries, num_blocks, limit, refs, refs_out, free_ids, free_count, free_out,
+                      free_cap, copy_src, copy_dst, copy_count, status};
+  auto bytes = [](int blocks) {
+    const size_t groups = ((size_t)blocks + 1023) / 1024;
+    return groups * 32 * 6 + (groups + 1) * 4;
+  };
+  cudaError_t e = ensure_smem_limit(23, (const void *)pages_compact_kernel, (int)bytes(COMPACT_MAX_BLOCKS));
   if (e != cudaSuccess) return e;
-  const long long blocks = (entries + 255) / 256, most = 8LL * num_sms();
-  return launch_pdl(pages_remap_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st, table,
-                    table_out, entries, static_cast<const int32_t *>(map), num_blocks);
+  return launch_pdl(pages_compact_kernel, dim3(SH_CTAS), dim3(SH_THREADS), bytes(num_blocks), st, A);
 }
 
 }  // namespace kvr

@@ -214,9 +214,8 @@ def test_shared_pages_host_validation_codes(L):
              c=P):
         return L.kv_pages_fork(table, S, mb, bs, nb, refs, src, dst, lens, n, ids, cin, cout, cap, a, b, c, None)
 
-    def comp(table=P, tout=P, S=4, mb=16, nb=64, limit=0, refs=P, rout=P, ids=P, count=P, iout=P, cap=8, a=P, b=P, c=P,
-             ws=P, wn=256):
-        return L.kv_pages_compact(table, tout, S, mb, nb, limit, refs, rout, ids, count, iout, cap, a, b, c, ws, wn, None)
+    def comp(table=P, tout=P, S=4, mb=16, nb=64, limit=0, refs=P, rout=P, ids=P, count=P, iout=P, cap=8, a=P, b=P, c=P):
+        return L.kv_pages_compact(table, tout, S, mb, nb, limit, refs, rout, ids, count, iout, cap, a, b, c, None)
 
     for call in (free, fork, comp):
         assert call(S=0) == -1 and call(mb=0) == -1 and call(nb=0) == -1 and call(cap=-1) == -1 and call(nb=(1 << 30) + 1) == -4
@@ -230,8 +229,7 @@ def test_shared_pages_host_validation_codes(L):
         assert fork(**{k: None}) == -1, k
     for k in ("tout", "rout", "count", "iout", "a", "b", "c"):
         assert comp(**{k: None}) == -1, k
-    assert comp(limit=-1) == -1 and comp(ws=None) == -3 and comp(wn=255) == -3 and comp(ws=ctypes.c_void_p(FAKE + 8)) == -1
-    assert L.kv_pages_compact_workspace_size(64) == 256 and L.kv_pages_compact_workspace_size(0) == 0
+    assert comp(limit=-1) == -1 and comp(nb=(1 << 20) + 1) == -4
 
     def copy(planes=(FAKE,), sizes=(64,), nb=8, a=P, b=P, c=P, n=3):
         pl = (ctypes.c_void_p * len(planes))(*planes) if planes else None
@@ -347,7 +345,6 @@ def test_binding_refuses_before_the_library(rec):
         lambda: kvr.kv_pages_compact(t, 12, refs, ids, count, _z(I32, 5), b, c),
         lambda: kvr.kv_pages_compact(t, 12, refs, ids, count, a, b, c, table_out=_z(I32, 3, 5)),
         lambda: kvr.kv_pages_compact(t, 12, refs, ids, count, a, b, c, refs_out=_z(I64, 12)),
-        lambda: kvr.kv_pages_compact(t, 12, refs, ids, count, a, b, c, workspace=_z(I32, 12)),
         lambda: kvr.kv_pages_copy([pool, lin], a, b, c),
         lambda: kvr.kv_pages_copy([pool, kvr.Kv8Layout.contiguous(2, 2, 100, block_size=32, device="cpu")], a, b, c),
         lambda: kvr.kv_pages_copy(pool, a.long(), b, c),
