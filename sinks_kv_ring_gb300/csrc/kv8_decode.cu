@@ -471,11 +471,13 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           continue;
         }
         // scores: columns keys 2t, 2t + 1 (nt = 0) and + 8
-        float S[MT][2][4];
+        float S[MT][2][4], S2[2][4];  // (one product a step: two sums, as one chain waits for itself)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) S[m][nt][0] = S[m][nt][1] = S[m][nt][2] = S[m][nt][3] = 0.f;
+          for (int m = 0; m < MT; ++m) S[m][nt][0] = S[m][nt][1] = S[m][nt][2] = S[m][nt][3] = 0.f;
+          S2[nt][0] = S2[nt][1] = S2[nt][2] = S2[nt][3] = 0.f;
+        }
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
           const uint4 ka = lds128(sT + g * 1024 + lane * 16), kb = lds128(sT + g * 1024 + 512 + lane * 16);
@@ -486,10 +488,16 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
               const uint4 q = lds128(smem + m * 12 * 512 + (g * 4 + j) * 512 + lane * 16);
-              mma_f16(S[m][0], q.x, q.y, q.z, q.w, a0, a1);
-              mma_f16(S[m][1], q.x, q.y, q.z, q.w, b0, b1);
+              mma_f16(MT == 1 && (j & 1) ? S2[0] : S[m][0], q.x, q.y, q.z, q.w, a0, a1);
+              mma_f16(MT == 1 && (j & 1) ? S2[1] : S[m][1], q.x, q.y, q.z, q.w, b0, b1);
             }
           }
+        }
+        if (MT == 1) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) S[0][nt][u] += S2[nt][u];
         }
         const uint4 tail = lds128(sT + KV8_OFF_TAIL);
         const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS);
@@ -773,11 +781,15 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
   for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K8_STAGES), (seen / K8_STAGES) & 1u, &never);
 }
 
-// Short contexts go by clusters in one launch, up to 2048 keys where the GPU
-// holds eight CTAs of every row at once, else up to 1024.
+// Short contexts go by clusters in one launch.  Measured at 16 query heads per KV
+// head (one launch against the work line's two): rows of 2048 keys, 1 x 4 KV heads
+// 8.6 us against 7.3, 4 x 4 10.5 / 10.3, 16 x 4 14.2 / 15.8, 64 x 4 37.3 / 40.5;
+// of 1024, 1 x 4 7.3 / 6.4, 4 x 4 8.4 / 9.6, 64 x 4 22.1 / 26.4; of 256, 1 x 4 6.1 /
+// 6.3, 64 x 4 10.8 / 16.0; of 4096, 4 x 4 14.0 / 12.1, 64 x 4 66.2 / 65.1.  A few rows
+// gain by the whole GPU's warps as soon as eight CTAs have more than a tile each.
 bool one_launch(int B, int hkv, long long max_ctx) {
-  const long long R = (long long)K8_CTAS * num_sms(), units = (max_ctx + K8_UNIT - 1) / K8_UNIT;
-  return units <= (8LL * B * hkv <= R ? 128 : 64);
+  const long long units = (max_ctx + K8_UNIT - 1) / K8_UNIT;
+  return units <= ((long long)B * hkv < 8 ? 32 : 128);
 }
 
 }  // namespace
