@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       }
     };
 #pragma unroll
-    for (int i = 0; i < K8_STAGES - 1; ++i)
+    for (int i = 0; i < K8_STAGES - 2; ++i)
       if (i < my_n) issue(i);
 
     kv8_query(Q[0], A.scale_log2, smem, reinterpret_cast<float *>(smem + K8_OFF_ROW), tid);
@@ -379,17 +379,48 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       gave_up = true;
       run_n = 0;
     }
-    // the tile of unit i, or null: no block of the pool, or (gave_up) not there in time
-    auto next_tile = [&](int i) -> const uint8_t * {
+    // Units go two at a time, for their latencies' sake.  Waits for units i and i + 1 (even i; the second may not be
+    // there) with the next two on their way; null where a unit is none or has no block of the pool.  False: not in time.
+    auto next_tiles = [&](int i, const uint8_t *(&T)[2]) {
       if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
-      if (i + K8_STAGES - 1 < my_n) issue(i + K8_STAGES - 1);
-      const uint32_t st = seen % K8_STAGES;
-      if (!__all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K8_STAGES) & 1u, abort_flag))) {
-        gave_up = true;
-        return nullptr;
+#pragma unroll
+      for (int u = K8_STAGES - 2; u < K8_STAGES; ++u)
+        if (i + u < my_n) issue(i + u);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        T[u] = nullptr;
+        if (i + u < run_n) {
+          const uint32_t st = seen % K8_STAGES;
+          if (!__all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K8_STAGES) & 1u, abort_flag))) {
+            gave_up = true;
+            return false;
+          }
+          ++seen;
+          if ((ok >> ((i + u) & 31)) & 1) T[u] = sStage + st * KV8_TILE;
+        }
       }
-      ++seen;
-      return (ok >> (i & 31)) & 1 ? sStage + st * KV8_TILE : nullptr;
+      return true;
+    };
+    // the units in turn: step(n, tiles, their first keys) takes one or two of them
+    auto units = [&](auto both, auto step) {
+      for (int i = 0; i < run_n; i += 2) {
+        const uint8_t *T[2];
+        if (!next_tiles(i, T)) break;
+        const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS), key1 = key0 + K8_UNIT * K8_WARPS;
+        if (decltype(both)::value && T[0] && T[1]) {
+          const uint8_t *const two[2] = {T[0], T[1]};
+          const int keys[2] = {key0, key1};
+          step(std::integral_constant<int, 2>(), two, keys);
+        } else {
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            const uint8_t *const one[1] = {u ? T[1] : T[0]};
+            const int keys[1] = {u ? key1 : key0};
+            if (one[0]) step(std::integral_constant<int, 1>(), one, keys);
+          }
+        }
+        __syncwarp();  // the stages are read: the next copies into them may go out
+      }
     };
     // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators,
     // of 16 rows at a time; behind it the CTA's merged part of all rows (DIRECT)
@@ -464,83 +495,98 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) least = min(least, __shfl_xor_sync(FULLW, least, o));
       least = min(least, key_hi);  // keys that every row sees
-      for (int i = 0; i < run_n; ++i) {
-        const uint8_t *sT = next_tile(i);
-        if (!sT) {
-          if (gave_up) break;
-          continue;
-        }
-        // scores: columns keys 2t, 2t + 1 (nt = 0) and + 8
-        float S[MT][2][4], S2[2][4];  // (one product a step: two sums, as one chain waits for itself)
+      units(std::integral_constant<bool, MT == 1>(), [&](auto nb, auto &T, auto &key0) {
+        constexpr int NB = decltype(nb)::value;
+        // scores: columns keys 2t, 2t + 1 (nt = 0) and + 8; where there is but one chain of products for each, two sums
+        constexpr bool SPLIT = MT == 1 && NB == 1;
+        float S[NB][MT][2][4], S2[2][4];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) S[m][nt][0] = S[m][nt][1] = S[m][nt][2] = S[m][nt][3] = 0.f;
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) S[n][m][nt][0] = S[n][m][nt][1] = S[n][m][nt][2] = S[n][m][nt][3] = 0.f;
           S2[nt][0] = S2[nt][1] = S2[nt][2] = S2[nt][3] = 0.f;
         }
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
-          const uint4 ka = lds128(sT + g * 1024 + lane * 16), kb = lds128(sT + g * 1024 + 512 + lane * 16);
+          uint4 ka[NB], kb[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) ka[n] = lds128(T[n] + g * 1024 + lane * 16), kb[n] = lds128(T[n] + g * 1024 + 512 + lane * 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = kv8_pair<0>(word(ka, j)), a1 = kv8_pair<1>(word(ka, j));
-            const uint32_t b0 = kv8_pair<0>(word(kb, j)), b1 = kv8_pair<1>(word(kb, j));
+            uint4 q[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const uint4 q = lds128(smem + m * 12 * 512 + (g * 4 + j) * 512 + lane * 16);
-              mma_f16(MT == 1 && (j & 1) ? S2[0] : S[m][0], q.x, q.y, q.z, q.w, a0, a1);
-              mma_f16(MT == 1 && (j & 1) ? S2[1] : S[m][1], q.x, q.y, q.z, q.w, b0, b1);
+            for (int m = 0; m < MT; ++m) q[m] = lds128(smem + m * 12 * 512 + (g * 4 + j) * 512 + lane * 16);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              const uint32_t a0 = kv8_pair<0>(word(ka[n], j)), a1 = kv8_pair<1>(word(ka[n], j));
+              const uint32_t b0 = kv8_pair<0>(word(kb[n], j)), b1 = kv8_pair<1>(word(kb[n], j));
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma_f16(SPLIT && (j & 1) ? S2[0] : S[n][m][0], q[m].x, q[m].y, q[m].z, q[m].w, a0, a1);
+                mma_f16(SPLIT && (j & 1) ? S2[1] : S[n][m][1], q[m].x, q[m].y, q[m].z, q[m].w, b0, b1);
+              }
             }
           }
         }
-        if (MT == 1) {
+        if (SPLIT) {
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) S[0][nt][u] += S2[nt][u];
+            for (int u = 0; u < 4; ++u) S[0][0][nt][u] += S2[nt][u];
         }
-        const uint4 tail = lds128(sT + KV8_OFF_TAIL);
-        const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS);
-        const bool plain = key0 + 16 <= least && tail.z == 0;  // every row sees all 16 keys, and all rows of the tile are finite
-        if (!plain) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int k = 8 * (u >> 1) + 2 * t + (u & 1);
-                float &x = S[m][u >> 1][2 * e + (u & 1)];
-                if (key0 + k >= min(keys[m][e], key_hi)) x = NEG_INF;
-                else if (tail.z >> k & 1) x = __uint_as_float(0x7fffffffu);  // a K row that is not finite
-              }
-        }
-        const float ks = __uint_as_float(tail.x);
-        const float lv = lg2(__uint_as_float(tail.y));  // -inf for a scale of 0: no weight
-        float fs[MT][2], top[MT][2];
+        uint4 tail[NB];
+        float lv[NB], fs[NB][MT][2], top[NB][MT][2];
         bool move = false;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NB; ++n) {
+          tail[n] = lds128(T[n] + KV8_OFF_TAIL);
+          if (!(key0[n] + 16 <= least && tail[n].z == 0)) {  // not every row sees all 16 keys, or some K row is not finite
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // (the least number keeps a factor of zero from making NaN of a masked score)
-            fs[m][e] = fmaf(ks, f[m][e], 0x1p-126f);
-            top[m][e] = fmaxf(fmax3(S[m][0][2 * e], S[m][0][2 * e + 1], S[m][1][2 * e]), S[m][1][2 * e + 1]) * fs[m][e];
-            move |= top[m][e] - rr[m][e] > K8_SLACK || lv + (top[m][e] - RR[m][e]) > K8_SLACK + K8_PBIAS;
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int k = 8 * (u >> 1) + 2 * t + (u & 1);
+                  float &x = S[n][m][u >> 1][2 * e + (u & 1)];
+                  if (key0[n] + k >= min(keys[m][e], key_hi)) x = NEG_INF;
+                  else if (tail[n].z >> k & 1) x = __uint_as_float(0x7fffffffu);
+                }
           }
-        if (__any_sync(FULLW, move)) {
-          // new references per row: the larger of the old one and this tile's maximum
+          const float ks = __uint_as_float(tail[n].x);
+          lv[n] = lg2(__uint_as_float(tail[n].y));  // -inf for a scale of 0: no weight
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = top[m][e];
-              x = fmaxf(x, __shfl_xor_sync(FULLW, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(FULLW, x, 2));
-              const float n = fmaxf(rr[m][e], x), N = fmaxf(RR[m][e], x + lv - K8_PBIAS), c = ex2(RR[m][e] - N);
-              ll[m][e] *= ex2(rr[m][e] - n);
-              rr[m][e] = n;
-              RR[m][e] = N;
+              // (the least number keeps a factor of zero from making NaN of a masked score)
+              fs[n][m][e] = fmaf(ks, f[m][e], 0x1p-126f);
+              const float(&x)[2][4] = S[n][m];
+              top[n][m][e] = fmaxf(fmax3(x[0][2 * e], x[0][2 * e + 1], x[1][2 * e]), x[1][2 * e + 1]) * fs[n][m][e];
+              move |= top[n][m][e] - rr[m][e] > K8_SLACK || lv[n] + (top[n][m][e] - RR[m][e]) > K8_SLACK + K8_PBIAS;
+            }
+        }
+        if (__any_sync(FULLW, move)) {
+          // new references per row: the larger of the old one and these tiles' maximum
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float r = rr[m][e], R = RR[m][e];
+#pragma unroll
+              for (int n = 0; n < NB; ++n) {
+                float x = top[n][m][e];
+                x = fmaxf(x, __shfl_xor_sync(FULLW, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(FULLW, x, 2));
+                r = fmaxf(r, x);
+                R = fmaxf(R, x + lv[n] - K8_PBIAS);
+              }
+              const float c = ex2(RR[m][e] - R);
+              ll[m][e] *= ex2(rr[m][e] - r);
+              rr[m][e] = r;
+              RR[m][e] = R;
 #pragma unroll
               for (int d = 0; d < 16; ++d) {
                 O[m][d][2 * e] *= c;
@@ -548,35 +594,41 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
               }
             }
         }
-        uint32_t P[MT][2][2];  // weights [8 keys][row gr, row gr + 8]
+        uint32_t P[NB][MT][2][2];  // weights [8 keys][row gr, row gr + 8]
         bool far = false;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // exp2(score + lv - R) is exp2(score - r) times exp2 of this; where it is within 2^64 either way, a product that
-            // underflows is below fp16's least number all the same
-            const float h = lv - RR[m][e] + rr[m][e], w = ex2(h);
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const float x = S[m][nt][2 * e], y = S[m][nt][2 * e + 1];
-              const float a = ex2(fmaf(x, fs[m][e], -rr[m][e])), b = ex2(fmaf(y, fs[m][e], -rr[m][e]));
-              ll[m][e] += a + b;
-              P[m][nt][e] = pack_h2(a * w, b * w);
-            }
-            far |= !(fabsf(h) <= 64.f);
-          }
-        if (__any_sync(FULLW, far)) {
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
+              // exp2(score + lv - R) is exp2(score - r) times exp2 of this; where it is within 2^64 either way, a product
+              // that underflows is below fp16's least number all the same
+              const float h = lv[n] - RR[m][e] + rr[m][e], w = ex2(h);
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt)
-                P[m][nt][e] = pack_h2(ex2(fmaf(S[m][nt][2 * e], fs[m][e], lv - RR[m][e])),
-                                      ex2(fmaf(S[m][nt][2 * e + 1], fs[m][e], lv - RR[m][e])));
+              for (int nt = 0; nt < 2; ++nt) {
+                const float x = S[n][m][nt][2 * e], y = S[n][m][nt][2 * e + 1];
+                const float a = ex2(fmaf(x, fs[n][m][e], -rr[m][e])), b = ex2(fmaf(y, fs[n][m][e], -rr[m][e]));
+                ll[m][e] += a + b;
+                P[n][m][nt][e] = pack_h2(a * w, b * w);
+              }
+              far |= !(fabsf(h) <= 64.f);
+            }
+        if (__any_sync(FULLW, far)) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+                  P[n][m][nt][e] = pack_h2(ex2(fmaf(S[n][m][nt][2 * e], fs[n][m][e], lv[n] - RR[m][e])),
+                                           ex2(fmaf(S[n][m][nt][2 * e + 1], fs[n][m][e], lv[n] - RR[m][e])));
         }
-        if (tail.z >> 16) {  // V rows that are not finite
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          if (!(tail[n].z >> 16)) continue;  // V rows that are not finite
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -584,22 +636,25 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 const int k = 8 * (u >> 1) + 2 * t + (u & 1);
-                if ((tail.z >> (16 + k) & 1) && key0 + k < min(keys[m][e], key_hi)) P[m][u >> 1][e] |= u & 1 ? 0x7fff0000u : 0x7fffu;
+                if ((tail[n].z >> (16 + k) & 1) && key0[n] + k < min(keys[m][e], key_hi))
+                  P[n][m][u >> 1][e] |= u & 1 ? 0x7fff0000u : 0x7fffu;
               }
         }
         // sums
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint4 v = lds128(sT + KV8_OFF_V + g * 512 + lane * 16);
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t v0 = kv8_pair<0>(word(v, j)), v1 = kv8_pair<1>(word(v, j));
+          for (int g = 0; g < 4; ++g) {
+            const uint4 v = lds128(T[n] + KV8_OFF_V + g * 512 + lane * 16);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma_f16(O[m][4 * g + j], P[m][0][0], P[m][0][1], P[m][1][0], P[m][1][1], v0, v1);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t v0 = kv8_pair<0>(word(v, j)), v1 = kv8_pair<1>(word(v, j));
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+                mma_f16(O[m][4 * g + j], P[n][m][0][0], P[n][m][0][1], P[n][m][1][0], P[n][m][1][1], v0, v1);
+            }
           }
-        }
-        __syncwarp();  // the stage is read: the next copy into it may go out
-      }
+      });
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         __syncthreads();  // all warps done with their stages (or the merge area): (re)use them as the merge area
@@ -645,54 +700,67 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(FULLW, least, o));
       least = min(least, key_hi);
-      for (int i = 0; i < run_n; ++i) {
-        const uint8_t *sT = next_tile(i);
-        if (!sT) {
-          if (gave_up) break;
-          continue;
-        }
+      units(std::integral_constant<bool, true>(), [&](auto nb, auto &T, auto &key0) {
+        constexpr int NB = decltype(nb)::value;
         // scores: rows keys gr and gr + 8 (index h); two sums, as one chain of products waits for itself
-        float S[4] = {0.f, 0.f, 0.f, 0.f}, S2[4] = {0.f, 0.f, 0.f, 0.f};
+        float S[NB][4], S2[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) S[n][u] = S2[n][u] = 0.f;
 #pragma unroll
         for (int g = 0; g < 3; ++g) {
-          const uint4 ka = lds128(sT + g * 1024 + lane * 16), kb = lds128(sT + g * 1024 + 512 + lane * 16);
+          uint4 ka[NB], kb[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) ka[n] = lds128(T[n] + g * 1024 + lane * 16), kb[n] = lds128(T[n] + g * 1024 + 512 + lane * 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_f16(j & 1 ? S2 : S, kv8_pair<0>(word(ka, j)), kv8_pair<0>(word(kb, j)), kv8_pair<1>(word(ka, j)),
-                    kv8_pair<1>(word(kb, j)), qb[4 * g + j].x, qb[4 * g + j].y);
-        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) S[u] += S2[u];
-        const uint4 tail = lds128(sT + KV8_OFF_TAIL);
-        const int key0 = key_lo + K8_UNIT * (warp + i * K8_WARPS);
-        if (!(key0 + 16 <= least && tail.z == 0)) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int k = gr + 8 * (u >> 1);
-            if (key0 + k >= min(keys[u & 1], key_hi)) S[u] = NEG_INF;
-            else if (tail.z >> k & 1) S[u] = __uint_as_float(0x7fffffffu);
-          }
+            for (int n = 0; n < NB; ++n)
+              mma_f16(j & 1 ? S2[n] : S[n], kv8_pair<0>(word(ka[n], j)), kv8_pair<0>(word(kb[n], j)), kv8_pair<1>(word(ka[n], j)),
+                      kv8_pair<1>(word(kb[n], j)), qb[4 * g + j].x, qb[4 * g + j].y);
         }
-        const float ks = __uint_as_float(tail.x);
-        const float lv = lg2(__uint_as_float(tail.y));
-        float fs[2], top[2];
+        uint4 tail[NB];
+        float lv[NB], fs[NB][2], top[NB][2];
         bool move = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          fs[e] = fmaf(ks, f[e], 0x1p-126f);
-          top[e] = fmaxf(S[e], S[2 + e]) * fs[e];
-          move |= top[e] - rr[e] > K8_SLACK || lv + (top[e] - RR[e]) > K8_SLACK + K8_PBIAS;
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) S[n][u] += S2[n][u];
+          tail[n] = lds128(T[n] + KV8_OFF_TAIL);
+          if (!(key0[n] + 16 <= least && tail[n].z == 0)) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int k = gr + 8 * (u >> 1);
+              if (key0[n] + k >= min(keys[u & 1], key_hi)) S[n][u] = NEG_INF;
+              else if (tail[n].z >> k & 1) S[n][u] = __uint_as_float(0x7fffffffu);
+            }
+          }
+          const float ks = __uint_as_float(tail[n].x);
+          lv[n] = lg2(__uint_as_float(tail[n].y));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            fs[n][e] = fmaf(ks, f[e], 0x1p-126f);
+            top[n][e] = fmaxf(S[n][e], S[n][2 + e]) * fs[n][e];
+            move |= top[n][e] - rr[e] > K8_SLACK || lv[n] + (top[n][e] - RR[e]) > K8_SLACK + K8_PBIAS;
+          }
         }
         if (__any_sync(FULLW, move)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = top[e];
+            float r = rr[e], R = RR[e];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(FULLW, x, o));
-            const float n = fmaxf(rr[e], x), N = fmaxf(RR[e], x + lv - K8_PBIAS), c = ex2(RR[e] - N);
-            ll[e] *= ex2(rr[e] - n);
-            rr[e] = n;
-            RR[e] = N;
+            for (int n = 0; n < NB; ++n) {
+              float x = top[n][e];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(FULLW, x, o));
+              r = fmaxf(r, x);
+              R = fmaxf(R, x + lv[n] - K8_PBIAS);
+            }
+            const float c = ex2(RR[e] - R);
+            ll[e] *= ex2(rr[e] - r);
+            rr[e] = r;
+            RR[e] = R;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
               O[d][e] *= c;
@@ -700,31 +768,43 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
             }
           }
         }
-        uint32_t P[2];  // weights: row query row gr, columns keys 2t, 2t + 1 and + 8
-        const float h0 = lv - RR[0] + rr[0], h1 = lv - RR[1] + rr[1], w0 = ex2(h0), w1 = ex2(h1);
-        const bool far = __any_sync(FULLW, !(fmaxf(fabsf(h0), fabsf(h1)) <= 64.f));
+        uint32_t P[NB][2];  // weights: row query row gr, columns keys 2t, 2t + 1 and + 8
+        float w[NB][2];
+        bool far = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float x = S[2 * h], y = S[2 * h + 1];
-          const float a = ex2(fmaf(x, fs[0], -rr[0])), b = ex2(fmaf(y, fs[1], -rr[1]));
-          ll[0] += a;
-          ll[1] += b;
-          uint32_t pw = pack_h2(a * w0, b * w1);
-          if (far) pw = pack_h2(ex2(fmaf(x, fs[0], lv - RR[0])), ex2(fmaf(y, fs[1], lv - RR[1])));
-          if (tail.z >> 16 && (tail.z >> (16 + gr + 8 * h) & 1)) {  // a V row that is not finite
-            const int k = key0 + gr + 8 * h;
-            pw |= (k < min(keys[0], key_hi) ? 0x7fffu : 0u) | (k < min(keys[1], key_hi) ? 0x7fff0000u : 0u);
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float h = lv[n] - RR[e] + rr[e];
+            w[n][e] = ex2(h);
+            far |= !(fabsf(h) <= 64.f);
           }
-          P[h] = transpose8(pw);
-        }
+        far = __any_sync(FULLW, far);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint4 v = lds128(sT + KV8_OFF_V + g * 512 + lane * 16);
-          mma_f16(O[2 * g], kv8_pair<0>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.x), kv8_pair<1>(v.y), P[0], P[1]);
-          mma_f16(O[2 * g + 1], kv8_pair<0>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.z), kv8_pair<1>(v.w), P[0], P[1]);
-        }
-        __syncwarp();  // the stage is read: the next copy into it may go out
-      }
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = S[n][2 * h], y = S[n][2 * h + 1];
+            const float a = ex2(fmaf(x, fs[n][0], -rr[0])), b = ex2(fmaf(y, fs[n][1], -rr[1]));
+            ll[0] += a;
+            ll[1] += b;
+            uint32_t pw = pack_h2(a * w[n][0], b * w[n][1]);
+            if (far) pw = pack_h2(ex2(fmaf(x, fs[n][0], lv[n] - RR[0])), ex2(fmaf(y, fs[n][1], lv[n] - RR[1])));
+            if (tail[n].z >> 16 && (tail[n].z >> (16 + gr + 8 * h) & 1)) {  // a V row that is not finite
+              const int k = key0[n] + gr + 8 * h;
+              pw |= (k < min(keys[0], key_hi) ? 0x7fffu : 0u) | (k < min(keys[1], key_hi) ? 0x7fff0000u : 0u);
+            }
+            P[n][h] = transpose8(pw);
+          }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint4 v = lds128(T[n] + KV8_OFF_V + g * 512 + lane * 16);
+            mma_f16(O[2 * g], kv8_pair<0>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.x), kv8_pair<1>(v.y), P[n][0], P[n][1]);
+            mma_f16(O[2 * g + 1], kv8_pair<0>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.z), kv8_pair<1>(v.w), P[n][0], P[n][1]);
+          }
+      });
       __syncthreads();  // all warps done with their stages: reuse them as the merge area
       float c[2], r[2];
 #pragma unroll
@@ -786,10 +866,11 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 // 8.6 us against 7.3, 4 x 4 10.5 / 10.3, 16 x 4 14.2 / 15.8, 64 x 4 37.3 / 40.5;
 // of 1024, 1 x 4 7.3 / 6.4, 4 x 4 8.4 / 9.6, 64 x 4 22.1 / 26.4; of 256, 1 x 4 6.1 /
 // 6.3, 64 x 4 10.8 / 16.0; of 4096, 4 x 4 14.0 / 12.1, 64 x 4 66.2 / 65.1.  A few rows
-// gain by the whole GPU's warps as soon as eight CTAs have more than a tile each.
+// gain by the whole GPU's warps once eight CTAs have a few tiles each; up to 1024
+// keys that is less than a second launch and a workspace cost the caller.
 bool one_launch(int B, int hkv, long long max_ctx) {
   const long long units = (max_ctx + K8_UNIT - 1) / K8_UNIT;
-  return units <= ((long long)B * hkv < 8 ? 32 : 128);
+  return units <= ((long long)B * hkv < 8 ? 64 : 128);
 }
 
 }  // namespace
