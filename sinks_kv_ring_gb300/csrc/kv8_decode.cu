@@ -40,7 +40,7 @@ constexpr unsigned ST_TIMEOUT = 8u;  // KVR_DEV_TIMEOUT
 constexpr int K8_WARPS = 4;
 constexpr int K8_CTAS = 2;           // per SM
 constexpr int K8_UNIT = 16;          // keys: one tile
-constexpr int K8_STAGES = 4;
+constexpr int K8_PAIRS = 2;           // of tiles in a warp's ring
 constexpr int K8_MT = 2;
 constexpr int K8_ROWS = 16 * K8_MT;  // query rows of a part: those of up to 4 batch rows of one sequence
 constexpr float K8_PBIAS = 11.f;     // weights are 2^11 where they equal the reference
@@ -60,15 +60,15 @@ int rows_together(int G) { return K8_ROWS / G >= 4 ? 4 : K8_ROWS / G >= 2 ? 2 : 
 constexpr int K8_OFF_ROW = K8_MT * 12 * 512;
 constexpr int K8_OFF_KEYS = K8_OFF_ROW + 4 * K8_ROWS;
 constexpr int K8_OFF_BAR = K8_OFF_KEYS + 4 * K8_ROWS;
-constexpr int K8_OFF_STALL = K8_OFF_BAR + 8 * K8_WARPS * K8_STAGES;  // a barrier that nothing completes (test hook)
+constexpr int K8_OFF_STALL = K8_OFF_BAR + 8 * K8_WARPS * K8_PAIRS;  // a barrier that nothing completes (test hook)
 constexpr int K8_OFF_ABORT = K8_OFF_STALL + 8;
 constexpr int K8_OFF_L = (K8_OFF_ABORT + 4 + 7) / 8 * 8;
 constexpr int K8_OFF_PLAN = (K8_OFF_L + 8 + 15) / 16 * 16;
 constexpr int K8_OFF_EARLY = K8_OFF_PLAN + (LINE_INLINE_MAX + 2) * 8;  // positions and ids of a batch of up to a row a thread
 constexpr int K8_OFF_INFO = K8_OFF_EARLY + K8_WARPS * 32 * 12;
 constexpr int K8_OFF_STAGE = (K8_OFF_INFO + LINE_INLINE_MAX + 127) / 128 * 128;
-constexpr int K8_SMEM = K8_OFF_STAGE + K8_WARPS * K8_STAGES * KV8_TILE;
-static_assert(K8_WARPS * K8_STAGES * KV8_TILE >=
+constexpr int K8_SMEM = K8_OFF_STAGE + K8_WARPS * K8_PAIRS * 2 * KV8_TILE;
+static_assert(K8_WARPS * K8_PAIRS * 2 * KV8_TILE >=
                   (K8_WARPS * 16 * (MO_STRIDE + 2) + K8_WARPS * 16 + K8_ROWS * (2 + DV)) * 4,
               "merge area");
 static_assert(K8_CTAS * (K8_SMEM + 1024) <= 228 * 1024, "CTAs per SM");
@@ -196,12 +196,12 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hkv = A.hkv, G = A.G;
   const uint32_t sBase = smem_u32(smem);
-  const uint32_t sBar = sBase + K8_OFF_BAR + 8 * K8_STAGES * warp;
+  const uint32_t sBar = sBase + K8_OFF_BAR + 8 * K8_PAIRS * warp;
   volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + K8_OFF_ABORT);
-  uint8_t *const sStage = smem + K8_OFF_STAGE + warp * K8_STAGES * KV8_TILE;
+  uint8_t *const sStage = smem + K8_OFF_STAGE + warp * K8_PAIRS * 2 * KV8_TILE;
   int64_t *sPrefix = reinterpret_cast<int64_t *>(smem + K8_OFF_PLAN);
   if (lane == 0) {
-    for (int j = 0; j < K8_STAGES; ++j) tc::mbar_init(sBar + 8 * j, 1);
+    for (int j = 0; j < K8_PAIRS; ++j) tc::mbar_init(sBar + 8 * j, 1);
     if (warp == 0) {
       tc::mbar_init(sBase + K8_OFF_STALL, 1);
       *abort_flag = 0;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
   int *const sKeys = reinterpret_cast<int *>(smem + K8_OFF_KEYS);
   const int tpb = A.pool.block_size >> 4;
   const int t = lane & 3, gr = lane >> 2;
-  uint32_t seen = 0;  // this warp's loads waited for so far: stage seen % K8_STAGES, phase (seen / K8_STAGES) & 1
+  uint32_t seen = 0;  // this warp's pairs waited for so far: slot seen % K8_PAIRS, phase (seen / K8_PAIRS) & 1
   uint32_t sent = 0;  // and issued
   bool gave_up = false;
 
@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
     tc::fence_proxy_async_smem();                   // the last piece's merge area lies over the stages:
     if (__syncthreads_or(*abort_flag != 0)) break;  // it is free again, its accesses ahead of the copies'
 
-    // Units go out 32 at a time: lane l looks up unit base + l's tile (a block
-    // that is none of the pool's gives -1) and issues its copy when its turn
-    // comes; `ok` has the warp's units that lie in the pool.
+    // Units go two at a time, for their latencies' sake: one barrier and one wait a pair.  They are looked up 32 at a
+    // time: lane l has unit base + l's tile (a block that is none of the pool's gives -1) and issues its copy when the
+    // pair's turn comes; `ok` has the warp's units that lie in the pool.
     int id = -1;
     uint32_t ok = 0, next_ok = 0;
     auto fetch_ids = [&](int base) {
@@ -356,20 +356,19 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       }
       next_ok = __ballot_sync(FULLW, id >= 0);
     };
-    auto issue = [&](int i) {
+    auto issue = [&](int i) {  // units i (even) and i + 1
       if ((i & 31) == 0) fetch_ids(i);
-      const uint32_t st = sent % K8_STAGES;
+      const uint32_t slot = sent % K8_PAIRS, bar = sBar + 8 * slot;
       ++sent;
-      if (lane == (i & 31)) {
-        const uint32_t bar = sBar + 8 * st;
-        tc::mbar_expect_tx(bar, id >= 0 ? KV8_TILE : 0);
-        if (id >= 0)
-          tc::bulk_load(smem_u32(sStage + st * KV8_TILE), A.pool.data + (long long)id * KV8_TILE, KV8_TILE, bar);
-      }
+      if ((lane ^ i) & 30) return;
+      if (!(lane & 1)) tc::mbar_expect_tx(bar, __popc(next_ok >> (i & 31) & 3u) * KV8_TILE);
+      if (id >= 0)
+        tc::bulk_load(smem_u32(sStage + (2 * slot + (lane & 1)) * KV8_TILE), A.pool.data + (long long)id * KV8_TILE, KV8_TILE,
+                      bar);
     };
 #pragma unroll
-    for (int i = 0; i < K8_STAGES - 2; ++i)
-      if (i < my_n) issue(i);
+    for (int i = 0; i < K8_PAIRS - 1; ++i)
+      if (2 * i < my_n) issue(2 * i);
 
     kv8_query(Q[0], A.scale_log2, smem, reinterpret_cast<float *>(smem + K8_OFF_ROW), tid);
     if (nq > 16) kv8_query(Q[K8_MT - 1], A.scale_log2, smem + 12 * 512, reinterpret_cast<float *>(smem + K8_OFF_ROW) + 16, tid);
@@ -379,26 +378,19 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       gave_up = true;
       run_n = 0;
     }
-    // Units go two at a time, for their latencies' sake.  Waits for units i and i + 1 (even i; the second may not be
-    // there) with the next two on their way; null where a unit is none or has no block of the pool.  False: not in time.
+    // Waits for units i (even) and i + 1, with the next pair on its way; null where a unit is none or has no block of the
+    // pool.  False: not in time.
     auto next_tiles = [&](int i, const uint8_t *(&T)[2]) {
       if ((i & 31) == 0) ok = next_ok;  // (the units of this round were looked up no later than with their first)
-#pragma unroll
-      for (int u = K8_STAGES - 2; u < K8_STAGES; ++u)
-        if (i + u < my_n) issue(i + u);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        T[u] = nullptr;
-        if (i + u < run_n) {
-          const uint32_t st = seen % K8_STAGES;
-          if (!__all_sync(FULLW, tc::mbar_wait(sBar + 8 * st, (seen / K8_STAGES) & 1u, abort_flag))) {
-            gave_up = true;
-            return false;
-          }
-          ++seen;
-          if ((ok >> ((i + u) & 31)) & 1) T[u] = sStage + st * KV8_TILE;
-        }
+      if (i + 2 * (K8_PAIRS - 1) < my_n) issue(i + 2 * (K8_PAIRS - 1));
+      const uint32_t slot = seen % K8_PAIRS;
+      if (!__all_sync(FULLW, tc::mbar_wait(sBar + 8 * slot, (seen / K8_PAIRS) & 1u, abort_flag))) {
+        gave_up = true;
+        return false;
       }
+      ++seen;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) T[u] = ok >> ((i + u) & 31) & 1 ? sStage + (2 * slot + u) * KV8_TILE : nullptr;
       return true;
     };
     // the units in turn: step(n, tiles, their first keys) takes one or two of them
@@ -419,7 +411,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
             if (one[0]) step(std::integral_constant<int, 1>(), one, keys);
           }
         }
-        __syncwarp();  // the stages are read: the next copies into them may go out
+        __syncwarp();  // the slot is read: the next pair into it may go out
       }
     };
     // merge area, over the stages once all warps are done with them: per warp, reference and sum per row, and numerators,
@@ -858,7 +850,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
   if (gave_up && lane == 0) flag(A.status, ST_TIMEOUT);
   // leave no copy in flight: only a wait that gave up left any (bounded again)
   uint32_t never = 0;
-  for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K8_STAGES), (seen / K8_STAGES) & 1u, &never);
+  for (; seen != sent; ++seen) tc::mbar_wait(sBar + 8 * (seen % K8_PAIRS), (seen / K8_PAIRS) & 1u, &never);
 }
 
 // Short contexts go by clusters in one launch.  Measured at 16 query heads per KV
