@@ -212,7 +212,13 @@ def _want(t, name, dtype, dim=None, cuda=True):
 
 
 # The C ABI takes bare pointers, so the sizes the kernels index by are
-# checked here, before any launch.
+# checked here, before any launch.  Calls of a few microseconds first ask in one
+# expression whether everything is as it should be (`fine`); the checks one by
+# one, which say what is not, cost half as much as such a call again.
+
+_BF, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_ODD = (AttributeError, TypeError, ValueError)  # what such an expression raises over something that is no tensor of its dims
+
 
 def _want_q(q):
     _want(q, "q", torch.bfloat16, 3)
@@ -765,24 +771,43 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
 
 def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_ctx, workspace, out, stream):
     _want_pool(pool, kind)
-    _want_q(q)
-    _want(pos, "pos", torch.int64, 1)
-    _want(seq, "seq", torch.int32, 1)
-    _want_table(table)
-    B, Hq, _ = q.shape
-    _want_len(pos, "pos", B)
-    _want_len(seq, "seq", B)
+    cur = torch.cuda.current_device()
+    try:
+        B, Hq, D = q.shape
+        P, half, two = table.shape
+        fine = (D == DQK and half == DROT // 2 and two == 2 and q.dtype is _BF and pos.dtype is _I64 and seq.dtype is _I32
+                and table.dtype is _F32 and pos.shape == (B,) and seq.shape == (B,) and q.is_contiguous()
+                and pos.is_contiguous() and seq.is_contiguous() and table.is_contiguous() and q.get_device() == cur
+                and pos.get_device() == cur and seq.get_device() == cur and table.get_device() == cur
+                and pool.data.get_device() == cur and pool.block_table.get_device() == cur)
+    except _ODD:
+        fine = False
+    if not fine:
+        _want_q(q)
+        _want(pos, "pos", torch.int64, 1)
+        _want(seq, "seq", torch.int32, 1)
+        _want_table(table)
+        B, Hq, _ = q.shape
+        P = table.shape[0]
+        _want_len(pos, "pos", B)
+        _want_len(seq, "seq", B)
+        _same_device(q, pos, seq, table, *pool.tensors())
     if workspace is None:
         n = size(B, Hq, pool.num_kv_heads, max_ctx)
         if n:  # (short contexts need none)
             workspace = _empty(n, torch.uint8, q, stream)
     else:
         _want(workspace, "workspace", torch.uint8, 1)
-    out = _out(out, B, Hq, q, stream)
-    _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
+        _same_device(q, workspace)
+    if out is None:
+        out = _empty((B, Hq, DV), _BF, q, stream)
+    else:
+        out = _out(out, B, Hq, q, stream)
+        _same_device(q, out)
     c = pool.c()
-    _check(fn(_ptr(q), _ptr(pos), _ptr(seq), B, Hq, ctypes.byref(c), _ptr(table), table.shape[0], float(softmax_scale),
-              int(max_ctx), _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(out), _stream(stream)))
+    _check(fn(q.data_ptr(), pos.data_ptr(), seq.data_ptr(), B, Hq, ctypes.byref(c), table.data_ptr(), P,
+              float(softmax_scale), int(max_ctx), None if workspace is None else workspace.data_ptr(),
+              0 if workspace is None else workspace.numel(), out.data_ptr(), _stream(stream)))
     return out
 
 
@@ -802,12 +827,6 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
 
 def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream):
     _want_pool(src, kind)
-    _want(src_seqs, "src_seqs", torch.int32, 1)
-    _want(lo, "lo", torch.int64, 1)
-    _want(cu_rows, "cu_rows", torch.int32, 1)
-    n = src_seqs.shape[0]
-    _want_len(lo, "lo", n)
-    _want_len(cu_rows, "cu_rows", n + 1)
     if isinstance(dst, LinearLayout):
         most = dst.num_rows
     elif isinstance(dst, PagedLayout):
@@ -816,14 +835,31 @@ def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream
         most = min(dst.num_seqs * dst.max_blocks * dst.block_size, 2 ** 31 - 1)
     else:
         raise TypeError("dst must be a PagedLayout or a LinearLayout")
+    cur = torch.cuda.current_device()
+    try:
+        n, = src_seqs.shape
+        fine = (dst_seqs is None and src_seqs.dtype is _I32 and lo.dtype is _I64 and cu_rows.dtype is _I32
+                and lo.shape == (n,) and cu_rows.shape == (n + 1,) and src_seqs.is_contiguous() and lo.is_contiguous()
+                and cu_rows.is_contiguous() and src_seqs.get_device() == cur and lo.get_device() == cur
+                and cu_rows.get_device() == cur and src.data.get_device() == cur and src.block_table.get_device() == cur
+                and dst.k.get_device() == cur and dst.v.get_device() == cur)
+    except _ODD:
+        fine = False
+    if not fine:
+        _want(src_seqs, "src_seqs", torch.int32, 1)
+        _want(lo, "lo", torch.int64, 1)
+        _want(cu_rows, "cu_rows", torch.int32, 1)
+        n = src_seqs.shape[0]
+        _want_len(lo, "lo", n)
+        _want_len(cu_rows, "cu_rows", n + 1)
+        if dst_seqs is not None:
+            _want(dst_seqs, "dst_seqs", torch.int32, 1)
+            _want_len(dst_seqs, "dst_seqs", n)
+        _same_device(src_seqs, lo, cu_rows, dst_seqs, *src.tensors(), *dst.tensors())
     T = most if T is None else int(T)
-    if dst_seqs is not None:
-        _want(dst_seqs, "dst_seqs", torch.int32, 1)
-        _want_len(dst_seqs, "dst_seqs", n)
-    _same_device(src_seqs, lo, cu_rows, dst_seqs, *src.tensors(), *dst.tensors())
     sc, dc = src.c(), dst.c()
-    _check(fn(ctypes.byref(sc), _ptr(src_seqs), _ptr(lo), _ptr(cu_rows), n, T, _ptr(dst_seqs), ctypes.byref(dc),
-              _stream(stream)))
+    _check(fn(ctypes.byref(sc), src_seqs.data_ptr(), lo.data_ptr(), cu_rows.data_ptr(), n, T, _ptr(dst_seqs),
+              ctypes.byref(dc), _stream(stream)))
 
 
 def kv8_append_rope(k, v, cu_rows, P0, seqs, table, value_scale, dst, stream=None):
@@ -833,22 +869,37 @@ def kv8_append_rope(k, v, cu_rows, P0, seqs, table, value_scale, dst, stream=Non
     written in order: those ahead of P0[i] in its tile of 16 are there already,
     those behind the chunk in its last tile mean nothing afterwards."""
     _want_pool(dst, Kv8Layout)
-    _want(k, "k", torch.bfloat16, 3)
-    _want(v, "v", torch.bfloat16, 3)
-    _want(cu_rows, "cu_rows", torch.int32, 1)
-    _want(P0, "P0", torch.int64, 1)
-    _want(seqs, "seqs", torch.int32, 1)
-    _want_table(table)
-    T, H = k.shape[:2]
-    n = seqs.shape[0]
-    if k.shape[2] != DQK or v.shape != (T, H, DV):
-        raise ValueError("k/v shapes disagree")
-    _want_len(cu_rows, "cu_rows", n + 1)
-    _want_len(P0, "P0", n)
-    _same_device(k, v, cu_rows, P0, seqs, table, *dst.tensors())
+    cur = torch.cuda.current_device()
+    try:
+        T, H, D = k.shape
+        n, = seqs.shape
+        P, half, two = table.shape
+        fine = (D == DQK and half == DROT // 2 and two == 2 and v.shape == (T, H, DV) and cu_rows.shape == (n + 1,)
+                and P0.shape == (n,) and k.dtype is _BF and v.dtype is _BF and cu_rows.dtype is _I32 and P0.dtype is _I64
+                and seqs.dtype is _I32 and table.dtype is _F32 and k.is_contiguous() and v.is_contiguous()
+                and cu_rows.is_contiguous() and P0.is_contiguous() and seqs.is_contiguous() and table.is_contiguous()
+                and k.get_device() == cur and v.get_device() == cur and cu_rows.get_device() == cur
+                and P0.get_device() == cur and seqs.get_device() == cur and table.get_device() == cur
+                and dst.data.get_device() == cur and dst.block_table.get_device() == cur)
+    except _ODD:
+        fine = False
+    if not fine:
+        _want(k, "k", torch.bfloat16, 3)
+        _want(v, "v", torch.bfloat16, 3)
+        _want(cu_rows, "cu_rows", torch.int32, 1)
+        _want(P0, "P0", torch.int64, 1)
+        _want(seqs, "seqs", torch.int32, 1)
+        _want_table(table)
+        T, H = k.shape[:2]
+        n, P = seqs.shape[0], table.shape[0]
+        if k.shape[2] != DQK or v.shape != (T, H, DV):
+            raise ValueError("k/v shapes disagree")
+        _want_len(cu_rows, "cu_rows", n + 1)
+        _want_len(P0, "P0", n)
+        _same_device(k, v, cu_rows, P0, seqs, table, *dst.tensors())
     c = dst.c()
-    _check(lib().kv8_append_rope(_ptr(k), _ptr(v), _ptr(cu_rows), _ptr(P0), _ptr(seqs), n, T, H, _ptr(table),
-                                 table.shape[0], float(value_scale), ctypes.byref(c), _stream(stream)))
+    _check(lib().kv8_append_rope(k.data_ptr(), v.data_ptr(), cu_rows.data_ptr(), P0.data_ptr(), seqs.data_ptr(), n, T, H,
+                                 table.data_ptr(), P, float(value_scale), ctypes.byref(c), _stream(stream)))
 
 
 def full_attn_decode_kv8_workspace_size(B, Hq, Hkv, max_ctx) -> int:
@@ -865,6 +916,20 @@ def full_attn_decode_kv8(q, pos, seq, pool, table, softmax_scale, max_ctx, works
 def kv8_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=None):
     """kv4_unpack from an 8-bit pool (Kv8Layout)."""
     _unpack_tiles(Kv8Layout, lib().kv8_unpack, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream)
+
+
+def _fine_ints(cur, *tensors):
+    """Whether all are contiguous int32 vectors on device cur."""
+    for t in tensors:
+        if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != cur:
+            return False
+    return True
+
+
+def _fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count):
+    return (block_table.dtype is _I32 and block_table.dim() == 2 and block_table.is_contiguous()
+            and block_table.get_device() == cur and refs.numel() == num_blocks and free_count.numel() == 1
+            and _fine_ints(cur, refs, free_ids, free_count))
 
 
 def _want_free_list(free_ids, free_count, refs, num_blocks):
@@ -892,19 +957,25 @@ def kv_pages_free(block_table, num_blocks, block_size, refs, seqs, free_ids, fre
     max_blocks]) become -1, refs (int32 [num_blocks], the holders of a block
     beyond the first) goes down, and the blocks that nobody holds are added to the
     free list (free_ids int32 [cap], free_count int32 [1]) in ascending order."""
-    _want(block_table, "block_table", torch.int32, 2)
-    _want(seqs, "seqs", torch.int32, 1)
-    _want_free_list(free_ids, free_count, refs, num_blocks)
+    cur = torch.cuda.current_device()
+    try:
+        fine = (keep_lo is None and keep_hi is None
+                and _fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and _fine_ints(cur, seqs))
+    except _ODD:
+        fine = False
+    if not fine:
+        _want(block_table, "block_table", torch.int32, 2)
+        _want(seqs, "seqs", torch.int32, 1)
+        _want_free_list(free_ids, free_count, refs, num_blocks)
+        for t, name in ((keep_lo, "keep_lo"), (keep_hi, "keep_hi")):
+            if t is not None:
+                _want(t, name, torch.int64, 1)
+                _want_len(t, name, seqs.shape[0])
+        _same_device(block_table, refs, seqs, free_ids, free_count, keep_lo, keep_hi)
     S, mb = block_table.shape
-    n = seqs.shape[0]
-    for t, name in ((keep_lo, "keep_lo"), (keep_hi, "keep_hi")):
-        if t is not None:
-            _want(t, name, torch.int64, 1)
-            _want_len(t, name, n)
-    _same_device(block_table, refs, seqs, free_ids, free_count, keep_lo, keep_hi)
-    _check(lib().kv_pages_free(_ptr(block_table), S, mb, int(block_size), int(num_blocks), _ptr(refs), _ptr(seqs),
-                               _ptr(keep_lo), _ptr(keep_hi), n, _ptr(free_ids), _ptr(free_count), free_ids.shape[0],
-                               _stream(stream)))
+    _check(lib().kv_pages_free(block_table.data_ptr(), S, mb, int(block_size), int(num_blocks), refs.data_ptr(),
+                               seqs.data_ptr(), _ptr(keep_lo), _ptr(keep_hi), seqs.shape[0], free_ids.data_ptr(),
+                               free_count.data_ptr(), free_ids.shape[0], _stream(stream)))
 
 
 def kv_pages_fork(block_table, num_blocks, block_size, refs, src_seqs, dst_seqs, lens, free_ids, free_count, copy_src,
@@ -916,25 +987,37 @@ def kv_pages_fork(block_table, num_blocks, block_size, refs, src_seqs, dst_seqs,
     entries), copy_count (int32 [1]) of them.  The remaining count goes to
     free_count_out (default: free_count itself).  Everything stays on the
     device."""
-    _want(block_table, "block_table", torch.int32, 2)
-    _want(src_seqs, "src_seqs", torch.int32, 1)
-    _want(dst_seqs, "dst_seqs", torch.int32, 1)
-    _want(lens, "lens", torch.int64, 1)
-    _want_free_list(free_ids, free_count, refs, num_blocks)
     if free_count_out is None:
         free_count_out = free_count
-    _want(free_count_out, "free_count_out", torch.int32, 1)
-    _want_len(free_count_out, "free_count_out", 1)
+    cur = torch.cuda.current_device()
+    try:
+        n, = src_seqs.shape
+        fine = (_fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and lens.dtype is _I64
+                and lens.shape == (n,) and lens.is_contiguous() and lens.get_device() == cur and dst_seqs.numel() == n
+                and free_count_out.numel() == 1 and copy_count.numel() == 1 and copy_src.numel() >= n
+                and copy_dst.numel() >= n
+                and _fine_ints(cur, src_seqs, dst_seqs, free_count_out, copy_src, copy_dst, copy_count))
+    except _ODD:
+        fine = False
+    if not fine:
+        _want(block_table, "block_table", torch.int32, 2)
+        _want(src_seqs, "src_seqs", torch.int32, 1)
+        _want(dst_seqs, "dst_seqs", torch.int32, 1)
+        _want(lens, "lens", torch.int64, 1)
+        _want_free_list(free_ids, free_count, refs, num_blocks)
+        _want(free_count_out, "free_count_out", torch.int32, 1)
+        _want_len(free_count_out, "free_count_out", 1)
+        n = src_seqs.shape[0]
+        _want_len(dst_seqs, "dst_seqs", n)
+        _want_len(lens, "lens", n)
+        _want_pairs(copy_src, copy_dst, copy_count, n)
+        _same_device(block_table, refs, src_seqs, dst_seqs, lens, free_ids, free_count, free_count_out, copy_src,
+                     copy_dst, copy_count)
     S, mb = block_table.shape
-    n = src_seqs.shape[0]
-    _want_len(dst_seqs, "dst_seqs", n)
-    _want_len(lens, "lens", n)
-    _want_pairs(copy_src, copy_dst, copy_count, n)
-    _same_device(block_table, refs, src_seqs, dst_seqs, lens, free_ids, free_count, free_count_out, copy_src, copy_dst,
-                 copy_count)
-    _check(lib().kv_pages_fork(_ptr(block_table), S, mb, int(block_size), int(num_blocks), _ptr(refs), _ptr(src_seqs),
-                               _ptr(dst_seqs), _ptr(lens), n, _ptr(free_ids), _ptr(free_count), _ptr(free_count_out),
-                               free_ids.shape[0], _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream)))
+    _check(lib().kv_pages_fork(block_table.data_ptr(), S, mb, int(block_size), int(num_blocks), refs.data_ptr(),
+                               src_seqs.data_ptr(), dst_seqs.data_ptr(), lens.data_ptr(), n, free_ids.data_ptr(),
+                               free_count.data_ptr(), free_count_out.data_ptr(), free_ids.shape[0], copy_src.data_ptr(),
+                               copy_dst.data_ptr(), copy_count.data_ptr(), _stream(stream)))
 
 
 def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_src, copy_dst, copy_count, limit=0,
@@ -945,24 +1028,34 @@ def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_s
     and the free list (then in descending order) name the new places, in
     table_out, refs_out and free_ids_out (default: the arrays themselves).
     Everything stays on the device."""
-    _want(block_table, "block_table", torch.int32, 2)
-    _want_free_list(free_ids, free_count, refs, num_blocks)
-    _want_pairs(copy_src, copy_dst, copy_count, int(num_blocks) // 2)
-    outs = []
-    for t, src, name in ((table_out, block_table, "table_out"), (refs_out, refs, "refs_out"),
-                         (free_ids_out, free_ids, "free_ids_out")):
-        if t is None:
-            t = src
-        else:
+    table_out = block_table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    free_ids_out = free_ids if free_ids_out is None else free_ids_out
+    cur = torch.cuda.current_device()
+    try:
+        fine = (_fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and table_out.dtype is _I32
+                and table_out.shape == block_table.shape and table_out.is_contiguous() and table_out.get_device() == cur
+                and refs_out.shape == refs.shape and free_ids_out.shape == free_ids.shape and copy_count.numel() == 1
+                and copy_src.numel() >= num_blocks // 2 and copy_dst.numel() >= num_blocks // 2
+                and _fine_ints(cur, refs_out, free_ids_out, copy_src, copy_dst, copy_count))
+    except _ODD:
+        fine = False
+    if not fine:
+        _want(block_table, "block_table", torch.int32, 2)
+        _want_free_list(free_ids, free_count, refs, num_blocks)
+        _want_pairs(copy_src, copy_dst, copy_count, int(num_blocks) // 2)
+        for t, src, name in ((table_out, block_table, "table_out"), (refs_out, refs, "refs_out"),
+                             (free_ids_out, free_ids, "free_ids_out")):
             _want(t, name, torch.int32, src.dim())
             if t.shape != src.shape:
                 raise ValueError(f"{name} must have the shape {tuple(src.shape)}, got {tuple(t.shape)}")
-        outs.append(t)
+        _same_device(block_table, refs, free_ids, free_count, copy_src, copy_dst, copy_count, table_out, refs_out,
+                     free_ids_out)
     S, mb = block_table.shape
-    _same_device(block_table, refs, free_ids, free_count, copy_src, copy_dst, copy_count, *outs)
-    _check(lib().kv_pages_compact(_ptr(block_table), _ptr(outs[0]), S, mb, int(num_blocks), int(limit), _ptr(refs),
-                                  _ptr(outs[1]), _ptr(free_ids), _ptr(free_count), _ptr(outs[2]), free_ids.shape[0],
-                                  _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count), _stream(stream)))
+    _check(lib().kv_pages_compact(block_table.data_ptr(), table_out.data_ptr(), S, mb, int(num_blocks), int(limit),
+                                  refs.data_ptr(), refs_out.data_ptr(), free_ids.data_ptr(), free_count.data_ptr(),
+                                  free_ids_out.data_ptr(), free_ids.shape[0], copy_src.data_ptr(), copy_dst.data_ptr(),
+                                  copy_count.data_ptr(), _stream(stream)))
 
 
 def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):
@@ -985,12 +1078,18 @@ def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):
     for t in planes:
         if t.shape[0] != nb:
             raise ValueError(f"the pools have {nb} and {t.shape[0]} blocks: they do not share a block table")
-    _want_pairs(copy_src, copy_dst, copy_count, 0)
+    cur = torch.cuda.current_device()
+    try:
+        fine = copy_count.numel() == 1 and _fine_ints(cur, copy_src, copy_dst, copy_count)
+    except _ODD:
+        fine = False
+    if not fine:
+        _want_pairs(copy_src, copy_dst, copy_count, 0)
     _same_device(copy_src, copy_dst, copy_count, *planes)
     n = len(planes)
     ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in planes])
     sizes = (ctypes.c_int64 * n)(*[t.stride(0) * t.element_size() for t in planes])
-    _check(lib().kv_pages_copy(ptrs, sizes, n, nb, _ptr(copy_src), _ptr(copy_dst), _ptr(copy_count),
+    _check(lib().kv_pages_copy(ptrs, sizes, n, nb, copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(),
                                min(copy_src.shape[0], copy_dst.shape[0]), _stream(stream)))
 
 
