@@ -69,8 +69,8 @@ struct Kv8Chunk {
 // onwards (rows [cu[i], cu[i+1]) touch at most rows / 16 + 2 tiles), so a unit
 // finds its chunk by a search over cu_rows and no plan is made first.  A round
 // narrows the chunks down by 32; the last 64 are read whole, with their positions
-// and sequences, so that small batches wait for one load where a binary search
-// waits for one a step (64 chunks of one token: 7.4 -> 5.2 us for the append).
+// and sequences, so that a batch of up to 64 waits for one load where a binary
+// search waits for one a step and then for the chunk's own.
 __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, const int64_t *__restrict__ pos,
                                               const int32_t *__restrict__ seqs, int n, long long unit) {
   const unsigned full = 0xffffffffu;

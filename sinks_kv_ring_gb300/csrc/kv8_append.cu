@@ -19,6 +19,17 @@
 // chunk that starts inside a tile finds the rows ahead of it there: their V
 // codes share 16 bytes with the new ones and are read in any case, their K codes
 // only where the scale grows.
+//
+// What bounds it: the latency of a warp's chain (its chunk, rows and RoPE rows,
+// largest magnitude, scale, stores) at the 20 warps an SM that its registers
+// leave, over the memory it moves: 37 x 1021 tokens of 8 KV heads take 59 us, 0.73
+// of what their 961 bytes each take at the copy rate, half of the issue slots
+// used; 8192 tokens of 4 KV heads 7.4 us, 64 tokens 3.6.  The first form took 145,
+// 17 and 7.4: quotients two to an instruction, all loads out before the block is
+// looked up, and one chunk search for all took the large case to 80; the rotary
+// group as pairs in one lane (no partner's loads, half the RoPE loads) and 32-byte
+// loads to 63, as the requests to L1 had bound it; CTAs of 4 warps at 96 registers
+// to 59 (at 80 registers, with spills: 67, at 124: 63).
 #include "kv8.cuh"
 #include "launch.h"
 

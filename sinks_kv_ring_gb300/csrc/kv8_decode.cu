@@ -23,9 +23,28 @@
 // Either reference moves (with a rescale of the sums) only when a sum passes it by
 // more than 4: the check is one vote a tile.
 //
-// Work.  Each warp streams its own tiles of 16 keys through its own ring of bulk
-// copies (one copy brings codes and scales), with no barrier between warps
-// inside a piece; 12 warps an SM, three CTAs, hold the sums in registers.
+// Work.  Each warp streams its own tiles of 16 keys, two at a time, through its own
+// ring of bulk copies (one copy brings codes and scales), with no barrier between
+// warps inside a piece; 8 warps an SM, two CTAs, hold the sums in registers.
+//
+// What bounds it.  321 bytes and 2 (192 + 128) flops a query row per key and KV
+// head.  Long contexts: HBM (batch 64 at 32769 keys, 4 KV heads: 394 us, 6.84 TB/s,
+// 1.0 of the copy rate, at 16 heads a group as at 8; one row of 2^20 keys 197 us).
+// With more query rows a key, the products: 64 x 4 drafts at 32772 keys take 563 us
+// at 8 heads a group (32 query rows a part) and 1108 at 16 (two parts each), where
+// the keys once would take 397; 16 x 2 at 16384 keys and 4 heads 56 us, 99 with each
+// row alone.  A warp needs about 1700 cycles for a tile at 16 query rows,
+// 650 of them the tensor pipe's for its two warps; so a batch that is neither is
+// bound by that and by the set-up of a part (2.4 us from the wait for the kernel
+// ahead to the first product) and the merge: one row of 32769 keys, 4 x 16 heads,
+// 14.2 us.
+//
+// Measured and left out (batch 64 at 32769, 16 heads, when the kernel took 401):
+// query operands in registers 420, three CTAs of 168 registers without the 32-row
+// form 410 (8 rows of 8192 keys: 19.8 against 21.8); the pair after the next one
+// requested behind the products instead of ahead of the wait, 1% slower throughout;
+// table entries, queries and RoPE rows brought into L1 ahead of the check of the
+// batch, no change.
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -46,7 +65,9 @@ constexpr int K8_ROWS = 16 * K8_MT;  // query rows of a part: those of up to 4 b
 constexpr float K8_PBIAS = 11.f;     // weights are 2^11 where they equal the reference
 constexpr float K8_SLACK = 4.f;      // how far a score or weight may pass its reference
 constexpr float K8_NONE = -1e30f;    // a reference before the first keys
-// The work line (line.cuh) in units of one tile.  The greatest share: the tensor
+// The work line (line.cuh) in units of one tile.  A row's set-up and merge, in units
+// (48 ragged rows at 8 heads a group: 24 -> 83.9 us, 36 -> 82.8, 56 -> 83.0; at 16:
+// 87.7, 89.4, 92.4; 12 x 4 drafts: 26.3, 27.2, 29.0).  The greatest share: the tensor
 // cores cut a sum off below its last bit at every product (2^-23 of it as
 // measured), one a tile for the values; at 2048 tiles a warp that is 2^-12 of the
 // sum at most, a sixteenth of the output's half step.

@@ -7,7 +7,11 @@
 // warp; which entry's it is comes from a search over cu_rows (kv8_chunk), and no
 // plan is made first.  A call of more than K8U_ONCE CTAs goes round with fewer of
 // them instead, and a warp stops behind the last entry's rows: a T far above the
-// rows there are (all that a block table spans) costs neither CTAs nor searches.
+// rows there are (all that a block table spans) costs neither CTAs nor searches
+// (1000 rows of 4 KV heads: 3.5 us with T = 1000, 23 with 2^19, 12 with 2^21 or 2^23).
+//
+// What bounds it: HBM, 321 bytes in and 640 out per (position, KV head): 122,880
+// positions of 4 KV heads take 72 us, 0.96 of the copy rate.
 #include "kv8.cuh"
 #include "launch.h"
 

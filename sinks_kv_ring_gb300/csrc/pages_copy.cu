@@ -7,6 +7,10 @@
 // a quantised one).  Pairs x planes x pieces of PC_PIECE bytes are laid on one
 // line, which the CTAs take in strides, so all layers go in one launch whatever
 // the count is (the host does not know it).
+//
+// What bounds it: HBM.  1440 blocks of 82 KB in each of three layers (710 MB read
+// and written) take 112 to 116 us, 0.90 to 0.93 of the copy rate; 4 loads in flight
+// a thread 123, four CTAs an SM 123, 32-byte loads 111 but 5% more on what L2 holds.
 #include "launch.h"
 
 namespace kvr {
