@@ -71,8 +71,9 @@ enum {
 #define KVR_DEV_BAD_BLOCK 4u  /* a block-table entry outside the pool, or a context past the table */
 #define KVR_DEV_TIMEOUT 8u    /* a kernel gave up waiting on its own pipeline (bounded wait) and returned */
 #define KVR_DEV_BAD_ROWS 16u  /* varlen: cu_rows not non-decreasing within [0, T]; that chunk is skipped */
-#define KVR_DEV_FREE_FULL 32u /* kv_pages_release_window: the free list could not take the released ids */
-#define KVR_DEV_NO_BLOCKS 64u /* kv_pages_grow: the free list holds fewer blocks than the step needs */
+#define KVR_DEV_FREE_FULL 32u /* kv_pages_release_window, kv_pages_free: the free list could not take the ids */
+#define KVR_DEV_NO_BLOCKS 64u /* kv_pages_grow, kv_pages_fork: the free list holds fewer blocks than the call needs;
+                                 kv_pages_compact: more blocks are used than the limit */
 
 /* KV storage kinds. */
 enum {
@@ -693,6 +694,12 @@ kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const 
  *   free_ids [free_cap], free_count [1] int32 (device): the free list, as
  *   kv_pages_grow takes from it.
  * num_blocks <= 2^30 (KVR_EUNSUPPORTED).
+ *
+ * Calls write only to blocks of their own sequence, so a block that is shared must
+ * not be appended to.  A fork sees to it: what it shares is full.  A sequence cut
+ * (kv_pages_free with keep_hi) inside a block that others still hold is forked to
+ * a new id at that length before it goes on, which copies the part.  Calls on one
+ * table, refs or free list are ordered by the caller (one stream).
  *
  * kv_pages_free gives up the blocks of sequences seqs[0..n-1] (int32, device):
  * all of them where keep_hi is NULL, else those that hold no position of

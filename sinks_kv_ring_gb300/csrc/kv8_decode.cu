@@ -7,7 +7,7 @@
 // so the tensor cores multiply codes and a scale costs one multiply a tile.  All
 // products are m16n8k16 f16 with fp32 accumulators; groups of more than 8 query
 // heads per KV head put the heads in the 16 rows, smaller ones in the 8 columns
-// (SMALL, below):
+// (kv8_decode_kernel, below):
 //   * Codes become fp16 numbers, exactly, by two instructions a pair (kv8_pair).
 //   * Queries are rotated, scaled by softmax_scale log2(e), brought by a power
 //     of two to a largest magnitude in [2^14, 2^15) per head, and rounded once to
@@ -21,7 +21,7 @@
 //     2^-11 of itself, an eighth of the output's own rounding.
 //   * sum p_j stays in fp32 beside it, under the running maximum of the scores.
 // Either reference moves (with a rescale of the sums) only when a sum passes it by
-// more than 4: the check is one vote a tile.
+// more than 4: the check is one vote a pair of tiles.
 //
 // Work.  Each warp streams its own tiles of 16 keys, two at a time, through its own
 // ring of bulk copies (one copy brings codes and scales), with no barrier between
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       line_end = min(x + L, total);
       ++turn;
     }
-    int w = 0, key_lo, key_hi, rows;  // rows: of the batch, from b on
+    long long w = 0;                  // the piece's first partial row
+    int key_lo, key_hi, rows;         // rows: of the batch, from b on
     long long at[4], top = -1;        // their positions, and the largest
     auto positions = [&]() {
 #pragma unroll
@@ -333,9 +334,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
       if (!ready) line_part<K8Line>(prefix, A.B, hkv, line_end, x, b, kv, lo, hi);
       ready = false;
       if (hi <= 0) continue;  // set-up alone: no piece
-      w = (int)blockIdx.x + b * hkv + kv;
-      if (TURNS) w += turn * (int)gridDim.x;
       rows = line_rows(info[b]);
+      w = line_at(A, (int)blockIdx.x + (TURNS ? turn * (int)gridDim.x : 0), b, kv, rows);
       positions();
       key_lo = lo * K8_UNIT;
       key_hi = (int)min((long long)hi * K8_UNIT, top + 1);
@@ -459,12 +459,12 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           fac[ww * 16 + tid] = f;
           L += mml[ww * 32 + tid * 2 + 1] * f;
         }
-        float *pml = DIRECT ? own_ml + 32 * m : A.part_ml + ((long long)w * (A.rmax * G) + 16 * m) * 2;
+        float *pml = DIRECT ? own_ml + 32 * m : A.part_ml + (w + 16 * m) * 2;
         pml[tid * 2] = M;
         pml[tid * 2 + 1] = L;
       }
       __syncthreads();
-      float *po = DIRECT ? own_o + 16 * m * DV : A.part_o + ((long long)w * (A.rmax * G) + 16 * m) * DV;
+      float *po = DIRECT ? own_o + 16 * m * DV : A.part_o + (w + 16 * m) * DV;
       for (int idx = tid; idx < n * (DV / 4); idx += blockDim.x) {
         const int g = idx / (DV / 4), d4 = 4 * (idx % (DV / 4));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -6,8 +6,8 @@
 // then its keys in units of UNIT; share c is units c L .. (c + 1) L - 1 of the
 // line, L = total / CTAs (at least MIN units), and CTA c takes it, so all CTAs
 // end together whatever the contexts are, and a row is cut only where a share
-// ends.  The part of row r in share c is piece c + r: no two pieces share a
-// number, and a row's are consecutive.  A share is at most MOST units: a longer
+// ends.  The part of row r in share c is piece c + r (line_at): no two pieces share
+// a number, and a row's are consecutive.  A share is at most MOST units: a longer
 // line is cut into a multiple of the CTAs' number of shares, and CTA c takes c,
 // c + CTAs, ...
 //
@@ -77,6 +77,15 @@ __device__ __forceinline__ uint8_t line_info(unsigned joined, int lane) {
 }
 __device__ __forceinline__ int line_lead(uint8_t info) { return info & 15; }
 __device__ __forceinline__ int line_rows(uint8_t info) { return info >> 4; }
+
+// First partial row (of one query row each) of the piece of batch rows b .. b + rows
+// - 1 and KV head kv in share c.  Along the line each next piece lies in the next
+// share, `rmax` G further, or is the next row's in the same share, `rows` G
+// further: no two overlap, and the pieces of all shares and rows fit in shares
+// rmax G + B hkv G.
+__device__ __forceinline__ long long line_at(const LineArgs &A, long long c, int b, int kv, int rows) {
+  return (c * A.rmax + (long long)b * A.hkv + (long long)kv * rows) * A.G;
+}
 
 // Units of a share for a line of `total` units.
 template <class LN>
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
   const bool have = row < (long long)A.B * A.hq;
   const int g = have ? (int)(row % G) : 0, pair = have ? (int)(row / G) : 0, b = pair / hkv, kv = pair - b * hkv;
   __shared__ uint8_t s_info[LINE_INLINE_MAX];
-  int lead = 0;  // (a row that goes with one ahead of it has its pieces among that one's)
+  int lead = 0, rows = 1;  // (a row that goes with one ahead of it has its pieces among that one's)
   // The plan, while the split kernel still runs: that kernel let this one start
   // after its own wait, so the batch (and the plan kernel's plan) are there.
   long long L, at, next;
@@ -207,12 +216,15 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
     const auto get = [&](int i, long long &p, int &s) { p = ld_early_s64(A.pos + i), s = ld_early_s32(A.seq + i); };
     L = line_plan<LN, LINE_MERGE_WARPS * 32>(get, A.B, hkv, A.num_seqs, A.max_pos, A.max_ctx, ctas, s_prefix, nullptr, A.rmax,
                                              s_info);
-    if (LN::SHARE) lead = line_lead(s_info[b]);
+    if (LN::SHARE) lead = line_lead(s_info[b]), rows = line_rows(s_info[b]);
     at = s_prefix[b - lead];
     next = s_prefix[b - lead + 1];
   } else {
     L = ld_early_s64(A.plan);
-    if (LN::SHARE) lead = line_lead(__ldcg(reinterpret_cast<const uint8_t *>(A.plan + LINE_PLAN + A.B + 1) + b));
+    if (LN::SHARE) {
+      const uint8_t info = __ldcg(reinterpret_cast<const uint8_t *>(A.plan + LINE_PLAN + A.B + 1) + b);
+      lead = line_lead(info), rows = line_rows(info);
+    }
     at = ld_early_s64(A.plan + LINE_PLAN + b - lead);
     next = ld_early_s64(A.plan + LINE_PLAN + b - lead + 1);
   }
@@ -236,7 +248,7 @@ __global__ void __launch_bounds__(LINE_MERGE_WARPS * 32)
       ml[k] = make_float2(NEG_INF, 0.f);
       o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < n) {
-        const long long r = (c0 + i + pair - lead * hkv) * (A.rmax * G) + lead * G + g;
+        const long long r = line_at(A, c0 + i, b - lead, kv, rows) + lead * G + g;
         ml[k] = *reinterpret_cast<const float2 *>(A.part_ml + r * 2);
         o[k] = *reinterpret_cast<const float4 *>(A.part_o + r * DV + 4 * lane);
       }
@@ -315,17 +327,17 @@ long long line_turns(int B, int hkv, long long max_ctx) {
   const long long most = (long long)line_ctas<LN>(B, hkv, max_ctx) * LN::MOST;
   return (units + most - 1) / most;
 }
-// Piece numbers: one per share of the longest line and one per row.
+// Partial rows of all pieces (line_at), on the longest line.
 template <class LN>
-size_t line_pieces(int B, int hkv, long long max_ctx) {
-  return (size_t)((long long)B * hkv + line_ctas<LN>(B, hkv, max_ctx) * line_turns<LN>(B, hkv, max_ctx));
+size_t line_partials(int B, int hkv, int G, long long max_ctx, int rmax) {
+  return (size_t)((long long)B * hkv + line_ctas<LN>(B, hkv, max_ctx) * line_turns<LN>(B, hkv, max_ctx) * rmax) * G;
 }
 
 // Workspace of a call on the line, and its parts.
 template <class LN>
 size_t line_workspace(int B, int hq, int hkv, long long max_ctx, int rmax = 1) {
-  const size_t G = (size_t)(hq / hkv) * rmax, n = line_pieces<LN>(B, hkv, max_ctx);
-  return line_plan_bytes<LN>(B) + align256(n * G * 2 * sizeof(float)) + align256(n * G * DV * sizeof(float));
+  const size_t n = line_partials<LN>(B, hkv, hq / hkv, max_ctx, rmax);
+  return line_plan_bytes<LN>(B) + align256(n * 2 * sizeof(float)) + align256(n * DV * sizeof(float));
 }
 template <class LN>
 void line_args(LineArgs &A, const int64_t *pos, const int32_t *seq, int B, int hq, int hkv, int num_seqs, int64_t max_pos,
@@ -342,7 +354,7 @@ void line_args(LineArgs &A, const int64_t *pos, const int32_t *seq, int B, int h
   A.plan = reinterpret_cast<int64_t *>(ws);
   uint8_t *w8 = reinterpret_cast<uint8_t *>(ws) + line_plan_bytes<LN>(B);
   A.part_ml = reinterpret_cast<float *>(w8);
-  A.part_o = reinterpret_cast<float *>(w8 + align256(line_pieces<LN>(B, hkv, max_ctx) * A.G * rmax * 2 * sizeof(float)));
+  A.part_o = reinterpret_cast<float *>(w8 + align256(line_partials<LN>(B, hkv, A.G, max_ctx, rmax) * 2 * sizeof(float)));
   A.out = out;
   A.rmax = rmax;
 }
