@@ -110,8 +110,8 @@ __device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_
 __device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  float y;  // (not .ftz: a tile's values may be so small that their scale is below the normal numbers)
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return half2_bits(__floats2half2_rn(lo, hi)); }
@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           float l = ll[m][e];
           l += __shfl_xor_sync(FULLW, l, 1);
           l += __shfl_xor_sync(FULLW, l, 2);
-          const float r = ref(rr[m][e], l), c = ex2(RR[m][e] - (r == NEG_INF ? 0.f : r));  // numerators in the scores' reference
+          // numerators in the scores' reference, by the root of the factor twice: scales near fp32's least number
+          const float r = ref(rr[m][e], l), c = ex2(0.5f * (RR[m][e] - (r == NEG_INF ? 0.f : r)));
           if (t == 0) *reinterpret_cast<float2 *>(mml + warp * 32 + (gr + 8 * e) * 2) = make_float2(r, l);
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
               const float(*On)[4] = &O[m][4 * g];
               const int a = 2 * e + u;
               *reinterpret_cast<float4 *>(o + (gr + 8 * e) * MO_STRIDE + 32 * g + 4 * (2 * t + u)) =
-                  make_float4(On[0][a] * c, On[1][a] * c, On[2][a] * c, On[3][a] * c);
+                  make_float4(On[0][a] * c * c, On[1][a] * c * c, On[2][a] * c * c, On[3][a] * c * c);
             }
         }
         join(m);
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) ll[e] += __shfl_xor_sync(FULLW, ll[e], o);
         r[e] = ref(rr[e], ll[e]);
-        c[e] = ex2(RR[e] - (r[e] == NEG_INF ? 0.f : r[e]));
+        c[e] = ex2(0.5f * (RR[e] - (r[e] == NEG_INF ? 0.f : r[e])));  // (twice, as above)
       }
       if (gr == 0) *reinterpret_cast<float4 *>(mml + warp * 32 + 4 * t) = make_float4(r[0], ll[0], r[1], ll[1]);
       float *o = mo + warp * 16 * MO_STRIDE + 2 * t * MO_STRIDE + 4 * gr;
@@ -834,7 +835,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<float4 *>(o + e * MO_STRIDE + 32 * g) =
-              make_float4(O[2 * g][e] * c[e], O[2 * g][2 + e] * c[e], O[2 * g + 1][e] * c[e], O[2 * g + 1][2 + e] * c[e]);
+              make_float4(O[2 * g][e] * c[e] * c[e], O[2 * g][2 + e] * c[e] * c[e], O[2 * g + 1][e] * c[e] * c[e],
+                          O[2 * g + 1][2 + e] * c[e] * c[e]);
       join(0);
     };
     if (nq <= 8) narrow();

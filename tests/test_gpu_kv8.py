@@ -233,7 +233,7 @@ def test_append_padding_and_flags(table):
 
 # -- decode --------------------------------------------------------------------------------------------------------------
 
-def _check_decode(got, q, pos, seq, pool, table, what="", rel_bar=True):
+def _check_decode(got, q, pos, seq, pool, table, what="", rel_bar=True, least=0.0):
     """Every row against fp64.  The output is rounded by half a bf16 step, 2^-8 |o| at most.  A score moves by at most
     2^-11 sum |q||k| for the rounding of the rotated q to fp16, and by less than as much again for what is held in fp32
     (12 products whose sums are cut off at 2^-23, the scale's factor): 2^-10 sum |q||k|, of which a weight and the sum
@@ -255,7 +255,7 @@ def _check_decode(got, q, pos, seq, pool, table, what="", rel_bar=True):
             err = np.abs(g[b, hs] - want)
             vmax = np.abs(V[:p + 1][ok[:p + 1]]).max() if ok[:p + 1].any() else 0.0
             move = np.exp(2 * 2.0 ** -10 * a[:, None]) - 1
-            tol = 2.0 ** -8 * np.abs(want) + move * (w + np.abs(want)) + 2.0 ** -10 * w + 2.0 ** -20 * vmax
+            tol = 2.0 ** -8 * np.abs(want) + move * (w + np.abs(want)) + 2.0 ** -10 * w + 2.0 ** -20 * vmax + least
             assert np.all(err <= tol), f"{what} row {b} head {h}: {np.max(err - tol):.3e} over"
             if rel_bar:
                 rel = np.sqrt((err ** 2).mean(1) / np.maximum((want ** 2).mean(1), 1e-300))
@@ -400,6 +400,23 @@ def test_decode_value_scales_apart(table, vscales, G):
         q = torch.randn(1, hkv * G, 192, generator=gen, device=DEV).bfloat16()
         out = kvr.full_attn_decode_kv8(q, _ints([n - 1], torch.int64), _ints([0], torch.int32), pool, table, SCALE, n)
         _check_decode(out, q, [n - 1], [0], pool, table, f"{vscales} {flip}")
+
+
+@pytest.mark.parametrize("G,rows", [(8, 1), (16, 1), (8, 4)])
+@pytest.mark.parametrize("n", [600, 9000])
+@pytest.mark.parametrize("mag", [1e-32, 1e-34, 1e-36, 1e-37])
+def test_decode_values_near_the_least_numbers(table, mag, n, G, rows):
+    """Scales down to the numbers below 2^-126.  Beside _check_decode's terms, an output below 2^-126 is rounded by half
+    of bf16's least step there, 2^-134."""
+    gen = _gen(43)
+    pool = _pool(gen, 1, 1, n, 64)
+    k, v = _kv(gen, n, 1)
+    _append(pool, k, (v.float() * mag).bfloat16(), [0], [0], [n], table)
+    q = torch.randn(rows, G, 192, generator=gen, device=DEV).bfloat16() * 3
+    pos = [n - rows + i for i in range(rows)]
+    out = kvr.full_attn_decode_kv8(q, _ints(pos, torch.int64), _ints([0] * rows, torch.int32), pool, table, SCALE, n)
+    _check_decode(out, q, pos, [0] * rows, pool, table, f"{mag}", rel_bar=False, least=2.0 ** -134)
+    assert torch.count_nonzero(out) > 0.9 * out.numel()
 
 
 @pytest.mark.parametrize("G", [8, 16])
@@ -628,6 +645,90 @@ def test_calls_on_another_stream(table):
     _check_decode(out, q, [n - 1], [0], pool, table)
     wk, wv = _want_unpacked(pool, 0, 0, n)
     assert torch.equal(rows.k.cpu(), wk) and torch.equal(rows.v.cpu(), wv)
+
+
+def test_two_streams_at_once(table):
+    """Two streams, each with a pool, rows and a workspace of its own, go on at the same time: as one after the other."""
+    hkv, G, n, steps = 2, 8, 2500, 12
+
+    def prepare(seed):
+        gen = _gen(seed)
+        lens = [n, 700, 1300]
+        pool = _filled(gen, lens, hkv, 64, table, max_ctx=n + 3 * steps)
+        kv = [_kv(gen, 6, hkv) for _ in range(steps)]
+        q = [torch.randn(6, hkv * G, 192, generator=gen, device=DEV).bfloat16() for _ in range(steps)]
+        most = pool.max_blocks * 64
+        ws = torch.empty(kvr.full_attn_decode_kv8_workspace_size(6, hkv * G, hkv, most), dtype=torch.uint8, device=DEV)
+        rows = kvr.LinearLayout.empty(sum(lens) + 3 * 3 * steps, hkv)
+        out = [torch.empty(6, hkv * G, 128, dtype=torch.bfloat16, device=DEV) for _ in range(steps)]
+        batch = []
+        for i in range(steps):
+            at = [x + 2 * i for x in lens]
+            batch.append((_ints([0, 2, 4, 6], torch.int32), _ints(at, torch.int64), _ints([a + j for a in at for j in (0, 1)], torch.int64)))
+        ids, each = _ints([0, 1, 2], torch.int32), _ints([0, 0, 1, 1, 2, 2], torch.int32)
+        end = _ints(np.concatenate([[0], np.cumsum([x + 2 * steps for x in lens])]).tolist(), torch.int32)
+        return pool, kv, q, ws, rows, out, batch, ids, each, end, _ints([0, 0, 0], torch.int64), most
+
+    def step(x, i, st):
+        pool, kv, q, ws, rows, out, batch, ids, each, end, zero, most = x
+        cu, at, pos = batch[i]
+        kvr.kv8_append_rope(*kv[i], cu, at, ids, table, VS, pool, stream=st)
+        kvr.full_attn_decode_kv8(q[i], pos, each, pool, table, SCALE, most, workspace=ws, out=out[i], stream=st)
+        if i + 1 == steps:
+            kvr.kv8_unpack(pool, ids, zero, end, rows, stream=st)
+
+    def results(x):
+        n = int(x[9][-1])
+        return [*x[5], x[4].k[:n], x[4].v[:n]]
+
+    alone = []
+    for seed in (81, 82):
+        x = prepare(seed)
+        for i in range(steps):
+            step(x, i, None)
+        torch.cuda.synchronize()
+        alone.append(results(x))
+    both, streams = [prepare(81), prepare(82)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for x, st in zip(both, streams):
+            step(x, i, st)
+    torch.cuda.synchronize()
+    assert kvr.device_status() == 0
+    for x, want in zip(both, alone):
+        for a, b in zip(results(x), want):
+            assert torch.equal(a, b)
+
+
+def test_arrays_that_start_16_bytes_off(table):
+    """Every array at the least alignment that the calls ask for: the same bytes as on aligned ones."""
+    gen = _gen(83)
+    n, hkv, G = 900, 3, 8
+    k, v = _kv(gen, n, hkv)
+    q = torch.randn(2, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+
+    def off(t):
+        words = 16 // t.element_size()
+        return torch.cat([t.new_zeros(words), t.reshape(-1)])[words:].view(t.shape)
+
+    def run(put):
+        pool = _pool(_gen(84), 1, hkv, n, 48, fill=0)
+        pool = kvr.Kv8Layout(put(pool.data), pool.block_table)
+        cs = put(table[:n].contiguous())
+        cu, zero, seq = _ints([0, 7, n], torch.int32), _ints([0, 7], torch.int64), _ints([0, 0], torch.int32)
+        kvr.kv8_append_rope(put(k[:7]), put(v[:7]), cu[:2].contiguous(), zero[:1].contiguous(), seq[:1].contiguous(), cs, VS, pool)
+        kvr.kv8_append_rope(put(k[7:]), put(v[7:]), _ints([0, n - 7], torch.int32), zero[1:].contiguous(), seq[:1].contiguous(),
+                            cs, VS, pool)
+        res = [pool.data]
+        res.append(kvr.full_attn_decode_kv8(put(q), _ints([n - 1, 400], torch.int64), seq, pool, cs, SCALE, n,
+                                            out=put(q.new_zeros(2, hkv * G, 128))))
+        rows = kvr.LinearLayout(put(k.new_zeros(n, hkv, 192)), put(k.new_zeros(n, hkv, 128)))
+        kvr.kv8_unpack(pool, seq[:1].contiguous(), zero[:1].contiguous(), _ints([0, n], torch.int32), rows)
+        return res + [rows.k, rows.v]
+
+    for a, b in zip(run(off), run(lambda t: t.clone())):
+        assert torch.equal(a, b)
+    assert kvr.device_status() == 0
 
 
 # -- long ----------------------------------------------------------------------------------------------------------------
