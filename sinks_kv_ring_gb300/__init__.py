@@ -1088,7 +1088,7 @@ def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):
     _same_device(copy_src, copy_dst, copy_count, *planes)
     n = len(planes)
     ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in planes])
-    sizes = (ctypes.c_int64 * n)(*[t.stride(0) * t.element_size() for t in planes])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() // max(nb, 1) * t.element_size() for t in planes])
     _check(lib().kv_pages_copy(ptrs, sizes, n, nb, copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(),
                                min(copy_src.shape[0], copy_dst.shape[0]), _stream(stream)))
 

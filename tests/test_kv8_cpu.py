@@ -303,6 +303,15 @@ def test_good_calls_reach_the_library(rec):
     assert n == 4 and list(sizes) == [2 * 2 * 5136, 2 * 32 * 384, 2 * 32 * 256, 2 * 2 * 2912]
 
 
+def test_copy_of_a_pool_of_one_block_cut_out_of_others(rec):
+    """The stride of an axis of one says nothing: the block is as large as its tensor."""
+    data = _z(U8, 5, 2, 2, 5136)[::5]
+    assert data.is_contiguous() and data.stride(0) == 5 * 2 * 2 * 5136
+    x = _page_args()
+    kvr.kv_pages_copy(kvr.Kv8Layout(data, _z(I32, 3, 4)), x["a"], x["b"], x["c"])
+    assert list(rec.calls[-1][1][1]) == [2 * 2 * 5136]
+
+
 def test_binding_refuses_before_the_library(rec):
     pool = kvr.Kv8Layout.contiguous(3, 2, 100, block_size=32, device="cpu")
     pool4 = kvr.Kv4Layout.contiguous(3, 2, 100, block_size=32, device="cpu")
