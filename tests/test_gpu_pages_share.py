@@ -220,6 +220,69 @@ def test_compact_edges():
             assert _compact(table, nb, refs, bad, c, 0, in_place) == kvr.DEV_BAD_BLOCK
 
 
+def test_the_largest_pool():
+    """2^20 blocks, the most that a compaction takes: the bit set at its full size."""
+    rng = np.random.default_rng(8)
+    nb, S, mb, bs = 1 << 20, 40, 60, 16
+    free, used = rng.permutation(nb).astype(np.int32), 0
+    table, refs = np.full((S, mb), -1, np.int32), np.zeros(nb, np.int32)
+    count = nb - 500
+    for s in range(20):
+        m = int(rng.integers(1, 25))
+        table[s, :m] = free[count + used:count + used + m]
+        used += m
+    refs[free[count:count + used]] = rng.integers(0, 3, used)
+    for limit in (0, 500, nb // 2, nb - 1, nb):
+        assert _compact(table, nb, refs, free, count, limit, False) == 0
+    assert _compact(table, nb, refs, free, count, 499) == kvr.DEV_NO_BLOCKS
+    assert _compact(table, nb, refs, free, count) == 0
+    refs[:] = 0
+    assert _free(table, bs, nb, refs, list(range(S)), free, count) == 0
+    assert _fork(table, bs, nb, refs, [0, 1, 0], [30, 31, 32], [16, 5, 9], free, count) == 0
+    nearly = np.arange(nb - 1, 0, -1, dtype=np.int32)                           # one block in use, the first; then the last
+    table[:] = -1
+    assert _compact(table, nb, refs, nearly, nb - 1) == 0
+    table[3, 2] = nb - 1
+    assert _compact(table, nb, refs, np.arange(nb, dtype=np.int32), nb - 1) == 0
+
+
+def test_two_streams_at_once():
+    """Two tables, each by a stream of its own, at the same time."""
+    S, mb, bs, nb = 60, 40, 16, 3000
+    runs = []
+    for seed in (41, 42):
+        rng = np.random.default_rng(seed)
+        table, refs, free, count, lens = _state(rng, S, mb, bs, nb, shared=0.0)
+        live = np.nonzero(lens)[0]
+        dst = np.nonzero(lens == 0)[0][:20]
+        src = rng.choice(live, len(dst))
+        cut = [int(rng.integers(0, lens[s] + 1)) for s in src]
+        runs.append(dict(t=_t(table), r=_t(refs), ids=_t(free), c=_t([count]), src=_t(src), dst=_t(dst), cut=_t(cut, torch.int64),
+                         a=_t([0] * nb), b=_t([0] * nb), k=_t([0]), was=(table, refs, free, count, src, dst, cut)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, st in zip(runs, streams):
+            kvr.kv_pages_free(x["t"], nb, bs, x["r"], x["dst"], x["ids"], x["c"], stream=st)
+        for x, st in zip(runs, streams):
+            kvr.kv_pages_fork(x["t"], nb, bs, x["r"], x["src"], x["dst"], x["cut"], x["ids"], x["c"], x["a"], x["b"], x["k"], stream=st)
+        for x, st in zip(runs, streams):
+            kvr.kv_pages_compact(x["t"], nb, x["r"], x["ids"], x["c"], x["a"], x["b"], x["k"], stream=st)
+    torch.cuda.synchronize()
+    assert kvr.device_status() == 0
+    for x in runs:
+        table, refs, free, count, src, dst, cut = x["was"]
+        free = list(free)
+        for _ in range(10):
+            table, refs, free, count, f = ops.free(table, bs, refs, dst, free, count)
+            table, refs, _, count, g = ops.fork(table, bs, refs, src, dst, cut, free, count)
+            table, refs, left, pairs, h = ops.compact(table, refs, free, count)
+            free[:count] = left
+            assert f == g == h == 0
+        assert np.array_equal(x["t"].cpu().numpy(), table) and np.array_equal(x["r"].cpu().numpy(), refs)
+        assert int(x["c"]) == count and x["ids"][:count].tolist() == left and int(x["k"]) == len(pairs)
+
+
 # -- copy ----------------------------------------------------------------------------------------------------------------
 
 def _pools(gen, nb, hkv, bs, kinds):
