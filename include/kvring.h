@@ -162,7 +162,7 @@ typedef struct kvr_kv4_layout {
  *   tile of 5136 bytes per 16 consecutive positions, position r of the tile
  *   (r = position % 16) at
  *     K codes   byte 1024 g + 64 r + i: dim 64 g + i (i < 64)
- *     V codes   byte 3072 + 512 g + 64 a + 16 ((r / 2) % 4) + 4 i + 2 (r / 8)
+ *     V codes   byte 16 * 192 + 512 g + 64 a + 16 ((r / 2) % 4) + 4 i + 2 (r / 8)
  *               + r % 2: dim 32 g + 4 a + i (i < 4)
  *     scales    fp32 at byte 5120 (K) and 5124 (V), bf16 numbers
  *     masks     16 bits at byte 5128 (K) and 5130 (V): bit r is set where the

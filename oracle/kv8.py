@@ -51,7 +51,7 @@ def rope_fp32(k, cs):
 def places(r):
     """Byte offsets of position r of a tile: K codes [192], V codes [128]."""
     d, e = np.arange(192), np.arange(128)
-    return 1024 * (d // 64) + 64 * r + d % 64, 3072 + 512 * (e // 32) + 64 * (e % 32 // 4) + 16 * (r // 2 % 4) + 4 * (e % 4) + 2 * (r // 8) + r % 2
+    return 1024 * (d // 64) + 64 * r + d % 64, 16 * 192 + 512 * (e // 32) + 64 * (e % 32 // 4) + 16 * (r // 2 % 4) + 4 * (e % 4) + 2 * (r // 8) + r % 2
 
 
 _PL = [places(r) for r in range(16)]

@@ -26,7 +26,7 @@
 
 namespace kvr {
 
-constexpr int KV8_OFF_V = 16 * DQK;                // 3072: V codes [4][8][4][4 dims][2][2]
+constexpr int KV8_OFF_V = 16 * DQK;                // V codes [4][8][4][4 dims][2][2]
 constexpr int KV8_OFF_TAIL = KV8_OFF_V + 16 * DV;  // 5120: K scale, V scale (fp32), K mask, V mask (16 bits), a zero word
 constexpr int KV8_TILE = KV8_OFF_TAIL + 16;        // 5136
 static_assert(KV8_TILE == 5136, "tile size of the pool format");
