@@ -155,6 +155,24 @@ def test_append_corner_rows(table):
     assert kvr.device_status() == 0
 
 
+def test_append_scales_over_the_whole_range(table):
+    """A tile per power of two from the least numbers to the greatest: quotients of 24-bit values (products with the value
+    scale, rotated pairs) by 8-bit scales, rounded as the oracle's division rounds them.  Two heads and five: one head a CTA,
+    and several."""
+    gen = _gen(19)
+    for hkv, reps in ((2, 1), (5, 6)):
+        e = torch.arange(-132, 125, device=DEV).repeat(reps)
+        T = 16 * len(e)
+        f = torch.ldexp(torch.ones(1, device=DEV, dtype=torch.float64), e).repeat_interleave(16)[:, None, None]
+        k, v = ((torch.randn(T, hkv, d, generator=gen, device=DEV).double().clamp(-3, 3) * f).bfloat16() for d in (192, 128))
+        pool = _pool(gen, 1, hkv, T, 64, fill=0)
+        want, bt, written = pool.data.cpu().numpy(), pool.block_table.cpu().numpy(), {}
+        _append(pool, k, v, [0], [0], [T], table)
+        _oracle_append(want, bt, k, v, [0], [0], [T], table, written=written)
+        assert o8.same(pool.data.cpu().numpy(), want, written)
+    assert kvr.device_status() == 0
+
+
 def test_append_halves_round_to_even(table):
     """Keys that lie exactly between two codes: bf16 values over a bf16 scale."""
     T = 16
