@@ -65,21 +65,27 @@ struct Kv8Chunk {
   int i, c0, c1, seq;
   long long pos;
 };
-// The chunk that owns unit `unit`, by a warp: chunk i owns units cu[i] / 16 + 2i
-// onwards (rows [cu[i], cu[i+1]) touch at most rows / 16 + 2 tiles), so a unit
-// finds its chunk by a search over cu_rows and no plan is made first.  A round
-// narrows the chunks down by 32; the last 64 are read whole, with their positions
-// and sequences, so that a batch of up to 64 waits for one load where a binary
-// search waits for one a step and then for the chunk's own.
+// Units of a call over chunks: chunk i owns units cu[i] / 16 + 2i onwards (rows [cu[i],
+// cu[i+1]) touch at most rows / 16 + 2 tiles), or, a unit a row, units cu[i] onwards
+// (rows touch no more tiles than there are rows).
+struct Kv8Units {
+  int shift, each;
+  __host__ __device__ __forceinline__ long long first(int cu, int i) const { return (cu >> shift) + (long long)each * i; }
+};
+constexpr Kv8Units KV8_BY_TILE{4, 2}, KV8_BY_ROW{0, 0};
+// The chunk that owns unit `unit`, by a warp: a search over cu_rows, and no plan is
+// made first.  A round narrows the chunks down by 32; the last 64 are read whole, with
+// their positions and sequences, so that a batch of up to 64 waits for one load where
+// a binary search waits for one a step and then for the chunk's own.
 __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, const int64_t *__restrict__ pos,
-                                              const int32_t *__restrict__ seqs, int n, long long unit) {
+                                              const int32_t *__restrict__ seqs, int n, Kv8Units units, long long unit) {
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;  // the chunk is in [lo, lo + len)
   while (len > 64) {
     const int step = (len + 31) >> 5, i = lo + lane * step;
     const bool in = lane * step < len;
-    const unsigned m = __ballot_sync(full, in && (long long)((in ? cu[i] : 0) >> 4) + 2LL * i <= unit);
+    const unsigned m = __ballot_sync(full, in && units.first(in ? cu[i] : 0, i) <= unit);
     const int last = 31 - __clz(m | 1u);  // (chunk 0 always counts)
     len = min(step, len - last * step);
     lo += last * step;
@@ -89,8 +95,8 @@ __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, co
   const int ca = in_a ? cu[ia] : 0, cb = in_b ? cu[ib] : 0, ce = cu[ie];
   const long long pa = in_a ? pos[ia] : 0, pb = in_b ? pos[ib] : 0;
   const int sa = in_a ? seqs[ia] : 0, sb = in_b ? seqs[ib] : 0;
-  const unsigned ma = __ballot_sync(full, in_a && (long long)(ca >> 4) + 2LL * ia <= unit);
-  const unsigned mb = __ballot_sync(full, in_b && (long long)(cb >> 4) + 2LL * ib <= unit);
+  const unsigned ma = __ballot_sync(full, in_a && units.first(ca, ia) <= unit);
+  const unsigned mb = __ballot_sync(full, in_b && units.first(cb, ib) <= unit);
   const int at = mb ? 63 - __clz(mb) : 31 - __clz(ma | 1u), l = at & 31, l1 = (at + 1) & 31;
   const int n_a = __shfl_sync(full, ca, l1), n_b = __shfl_sync(full, cb, l1);
   Kv8Chunk C;

@@ -24,13 +24,13 @@
 // codes only where the scale grows.  Large calls take up to four heads of a tile
 // one after the other (MANY), for one search and one look at the RoPE rows; where that
 // leaves fewer than 16 CTAs an SM, two rounds, a CTA has one head (64 tokens of 4 KV
-// heads: 3.2 us, by four heads 6.4; 8192: 7.5 and 8.1; 37 x 1021 of 8: 57.4 and 52.3).
+// heads: 3.0 us, by four heads 6.4; 8192: 7.5 and 8.1; 37 x 1021 of 8: 57.4 and 52.3).
 //
 // What bounds it: the latency of a warp's chain (rows, largest magnitude, scale,
 // stores) at the 32 warps an SM that its registers leave, over the memory it moves: 37
 // x 1021 tokens of 8 KV heads take 52 us, 0.82 of what their 961 bytes each take at the
 // copy rate; 30 x 4096 of 4, 82 us, 0.85; 8192 tokens of 4 KV heads 7.4 us, 64 tokens
-// 3.2.  The first form took 145, 17 and 7.4: quotients two to an instruction, all
+// 3.0.  The first form took 145, 17 and 7.4: quotients two to an instruction, all
 // loads out before the block is looked up, and one chunk search for all took the large
 // case to 80; the rotary group as pairs in one lane (no partner's loads, half the RoPE
 // loads) and 32-byte loads to 63, as the requests to L1 had bound it; a tile's K by one
@@ -140,6 +140,7 @@ struct Kv8Append {
   Kv8View dst;
   unsigned *status;
   int heads, per_tile;  // heads of a CTA, CTAs of a tile
+  Kv8Units units;
 };
 
 // Where a warp's tile lies and which of its rows are new.
@@ -410,14 +411,14 @@ __device__ __forceinline__ void kv8_append_v(const Kv8Append &A, const Kv8Item &
 
 // The tile of unit `unit` of the call, by a warp; false: none.
 __device__ __forceinline__ bool append_item(const Kv8Append &A, long long unit, bool say, Kv8Item &I, const int32_t *&entry) {
-  const Kv8Chunk C = kv8_chunk(A.cu_rows, A.P0, A.seqs, A.n, unit);
+  const Kv8Chunk C = kv8_chunk(A.cu_rows, A.P0, A.seqs, A.n, A.units, unit);
   const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
   const long long a = C.pos;
   if (c0 < 0 || c1 < c0 || c1 > A.T) {
     if (say) flag(A.status, ST_BAD_ROWS);
     return false;
   }
-  const long long u = unit - ((c0 >> 4) + 2LL * i);
+  const long long u = unit - A.units.first(c0, i);
   if (u < 0 || c1 == c0 || s == -1) return false;
   const bool bs = s < 0 || s >= A.dst.num_seqs;
   const long long most = min((long long)A.max_pos, (long long)A.dst.max_blocks * A.dst.block_size);
@@ -468,8 +469,9 @@ cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, const int32_
                               const int32_t *seqs, int n, long long T, const float *table, int64_t max_pos,
                               float value_scale, const Kv8View &dst, unsigned *status, cudaStream_t st) {
   if (dst.hkv > (1 << 24)) return cudaErrorInvalidValue;  // (a position alone would be 5 GB)
-  Kv8Append A{k, v, cu_rows, P0, seqs, n, T, table, max_pos, value_scale, dst, status, 1, dst.hkv};
-  const long long units = (T >> 4) + 2LL * n;  // tiles that the call could have
+  Kv8Append A{k, v, cu_rows, P0, seqs, n, T, table, max_pos, value_scale, dst, status, 1, dst.hkv, KV8_BY_TILE};
+  long long units = (T >> 4) + 2LL * n;  // tiles that the call could have: by row the fewer for chunks of one or two
+  if (T <= units) A.units = KV8_BY_ROW, units = T;  // (256 chunks of one row, 8 KV heads: 7.1 us, by tile 9.0)
   while (2 * A.heads <= K8A_HEADS && A.heads < dst.hkv &&
          units * ((dst.hkv + 2 * A.heads - 1) / (2 * A.heads)) >= 2LL * K8A_CTAS * num_sms())
     A.heads *= 2;

@@ -48,7 +48,8 @@ __device__ __forceinline__ bool unpack_unit(const Kv8View &src, const int32_t *_
                                             long long T, const int32_t *__restrict__ dst_seqs, const KvView &dst,
                                             long long unit, int h, unsigned *status) {
   const int lane = threadIdx.x & 31;
-  const Kv8Chunk C = kv8_chunk(cu_rows, lo, src_seqs, n, unit);
+  const Kv8Units units = KV8_BY_TILE;
+  const Kv8Chunk C = kv8_chunk(cu_rows, lo, src_seqs, n, units, unit);
   const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
   if (c0 < 0 || c1 < c0 || c1 > T) {
     if (lane == 0) flag(status, ST_BAD_ROWS);
@@ -56,7 +57,7 @@ __device__ __forceinline__ bool unpack_unit(const Kv8View &src, const int32_t *_
   }
   long long a = C.pos;
   const bool mine = lane == 0 && h == 0;
-  const long long u = unit - ((c0 >> 4) + 2LL * i);
+  const long long u = unit - units.first(c0, i);
   if (u < 0) return true;
   if (c1 == c0) return i < n - 1;
   // an entry that names no source has its rows written as zeros
