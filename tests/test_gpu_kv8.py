@@ -220,6 +220,35 @@ def test_append_many_chunks(table, n):
                 assert np.abs(got - ref).max() <= m * (1 + 2.0 ** -7) / 254 + 2.0 ** -8 * m, i
 
 
+@pytest.mark.parametrize("n,long", [(1, 1), (70, 60), (70, 0), (1500, 40), (1500, 0)])
+def test_append_short_chunks(table, n, long):
+    """Chunks of none to three rows behind what each sequence holds, over the ends of tiles, with padding between, and (as
+    long as the mean stays near one) a long one among them: the oracle's bytes."""
+    gen, rng = _gen(n + long), np.random.default_rng(n + long)
+    hkv = 2
+    first = rng.integers(0, 20, n)
+    rows = rng.choice([0, 1, 1, 1, 2, 3], n)
+    rows[n // 2] = max(long, 1)
+    cap = int((first + rows).max()) + 1
+    pool = _pool(gen, n, hkv, cap, 16, fill=0)
+    want, bt, written = pool.data.cpu().numpy(), pool.block_table.cpu().numpy(), {}
+    ids = rng.permutation(n)
+    gone = [i for i in range(n) if n > 1 and rng.random() < 0.1]
+    for lo, cnt in ((np.zeros(n, int), first), (first, rows)):
+        T = max(int(cnt.sum()), 1)
+        k, v = _kv(gen, T, hkv)
+        seqs = np.where(np.isin(np.arange(n), gone) & (cnt is rows), -1, ids)
+        _append(pool, k, v, seqs.tolist(), lo.tolist(), cnt.tolist(), table)
+        at = np.concatenate([[0], np.cumsum(cnt)])
+        for i in range(n):
+            if seqs[i] >= 0:
+                _oracle_append(want, bt, k[at[i]:at[i + 1]], v[at[i]:at[i + 1]], [int(seqs[i])], [int(lo[i])], [int(cnt[i])],
+                               table, written=written)
+    assert T <= T // 16 + 2 * n
+    assert kvr.device_status() == 0
+    assert o8.same(pool.data.cpu().numpy(), want, written)
+
+
 def test_append_padding_and_flags(table):
     gen = _gen(11)
     hkv, bs = 2, 32
@@ -385,6 +414,36 @@ def test_decode_rows_of_one_sequence_go_together(table, G, most):
             want[i, G:] = p >= 701
     want[5, -1] = True
     assert torch.equal(torch.isnan(out), want)
+
+
+@pytest.mark.parametrize("G,hkv,most", [(8, 2, 2300), (16, 1, 2300), (4, 1, 700)])
+def test_decode_thousands_of_rows(table, G, hkv, most):
+    """2600 rows, by a plan of their own: one to four neighbours of a sequence, and rows that cannot be served between."""
+    gen, rng = _gen(53), np.random.default_rng(53)
+    S, B = 40, 2600
+    lens = rng.integers(5, most, S).tolist()
+    pool = _filled(gen, lens, hkv, 32, table, max_ctx=most)
+    seq, pos = [], []
+    while len(seq) < B:
+        s = int(rng.integers(0, S))
+        for _ in range(int(rng.integers(1, 5))):
+            seq.append(s)
+            pos.append(int(rng.integers(0, lens[s])))
+        if rng.random() < 0.05:
+            seq[-1] = S if rng.random() < 0.5 else -1
+        elif rng.random() < 0.05:
+            pos[-1] = -1
+    seq, pos = seq[:B], pos[:B]
+    q = torch.randn(B, hkv * G, 192, generator=gen, device=DEV).bfloat16()
+    out = kvr.full_attn_decode_kv8(q, _ints(pos, torch.int64), _ints(seq, torch.int32), pool, table, SCALE, most)
+    assert kvr.device_status() == (kvr.DEV_BAD_SEQ | kvr.DEV_BAD_POS)
+    bad = [b for b in range(B) if not 0 <= seq[b] < S or pos[b] < 0]
+    assert len(bad) > 20 and not out[bad].any()
+    few = [b for b in range(B) if b not in set(bad)][::9]
+    _check_decode(out[few], q[few], [pos[b] for b in few], [seq[b] for b in few], pool, table)
+    again = kvr.full_attn_decode_kv8(q, _ints(pos, torch.int64), _ints(seq, torch.int32), pool, table, SCALE, most)
+    kvr.device_status()
+    assert torch.equal(out, again)
 
 
 @pytest.mark.parametrize("C,G,B", [(2, 16, 9), (3, 8, 70), (4, 4, 40), (4, 16, 70)])
