@@ -103,6 +103,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));

@@ -59,12 +59,6 @@ __device__ __forceinline__ float kv8_scale(float a) {
   return __uint_as_float(b);
 }
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-
 // What the quotients by a scale are made with.
 struct Kv8Div {
   uint64_t r, rest;  // the reciprocal in two numbers (0 for a scale of 0), in both halves

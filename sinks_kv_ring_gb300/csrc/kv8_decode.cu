@@ -14,6 +14,10 @@
 //     fp16 (2^-11 of a value, where the bf16 decode rounds to 2^-8).
 //   * The weights of the value product are p_j vs, taken as one power of two of
 //     score + log2(vs) less a reference of its own: the largest such sum so far.
+//     It is held as its distance d from the scores' reference r, and a weight's
+//     exponent is (score - r) + (log2(vs) - d): no value scale is ever added to a
+//     score, which may be so large (1e6 and more) that fp32 would cut the scale off.
+//     Scores are rounded once, ahead of their maximum, so the largest is r exactly.
 //     So a weight is at most 2^15 whatever the scales are, and one is lost to
 //     fp16's least number only where it is below 2^-35 of the largest share in
 //     the output, not of the largest probability: light keys with large values
@@ -65,6 +69,7 @@ constexpr int K8_ROWS = 16 * K8_MT;  // query rows of a part: those of up to 4 b
 constexpr float K8_PBIAS = 11.f;     // weights are 2^11 where they equal the reference
 constexpr float K8_SLACK = 4.f;      // how far a score or weight may pass its reference
 constexpr float K8_NONE = -1e30f;    // a reference before the first keys
+constexpr float K8_FAR = -512.f;     // least distance of the weights' reference: 2^-512 of the largest probability is no fp32 number
 // The work line (line.cuh) in units of one tile.  A row's set-up and merge, in units
 // (48 ragged rows at 8 heads a group: 24 -> 83.9 us, 36 -> 82.8, 56 -> 83.0; at 16:
 // 87.7, 89.4, 92.4; 12 x 4 drafts: 26.3, 27.2, 29.0).  The greatest share: the tensor
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
     auto wide = [&](auto mt) {
       constexpr int MT = decltype(mt)::value;
       float f[MT][2], O[MT][16][4];              // O[m][4g + i]: dims 32 g + 4 c + i of column c
-      float rr[MT][2], RR[MT][2], ll[MT][2];     // references of the scores and (less the bias) of the weights; sums
+      float rr[MT][2], dd[MT][2], ll[MT][2];     // the scores' reference, how far from it the weights' (less the bias) is; sums
       int keys[MT][2], least = 0x7fffffff;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -501,7 +506,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           f[m][e] = sFac[r];
           keys[m][e] = r < nq ? sKeys[r] : 0x7fffffff;
           least = min(least, keys[m][e]);
-          rr[m][e] = RR[m][e] = K8_NONE;
+          rr[m][e] = K8_NONE;
+          dd[m][e] = K8_FAR;
           ll[m][e] = 0.f;
         }
       }
@@ -550,11 +556,24 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
             for (int u = 0; u < 4; ++u) S[0][0][nt][u] += S2[nt][u];
         }
         uint4 tail[NB];
-        float lv[NB], fs[NB][MT][2], top[NB][MT][2];
+        float lv[NB], top[NB][MT][2];
         bool move = false;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           tail[n] = lds128(T[n] + KV8_OFF_TAIL);
+          const float ks = __uint_as_float(tail[n].x);
+          lv[n] = lg2(__uint_as_float(tail[n].y));  // -inf for a scale of 0: no weight
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float fs = ks * f[m][e];
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                float(&x)[4] = S[n][m][nt];
+                f32x2_split(mul_f32x2(f32x2(x[2 * e], x[2 * e + 1]), f32x2(fs, fs)), x[2 * e], x[2 * e + 1]);
+              }
+            }
           if (!(key0[n] + 16 <= least && tail[n].z == 0)) {  // not every row sees all 16 keys, or some K row is not finite
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -568,17 +587,14 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
                   else if (tail[n].z >> k & 1) x = __uint_as_float(0x7fffffffu);
                 }
           }
-          const float ks = __uint_as_float(tail[n].x);
-          lv[n] = lg2(__uint_as_float(tail[n].y));  // -inf for a scale of 0: no weight
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // (the least number keeps a factor of zero from making NaN of a masked score)
-              fs[n][m][e] = fmaf(ks, f[m][e], 0x1p-126f);
               const float(&x)[2][4] = S[n][m];
-              top[n][m][e] = fmaxf(fmax3(x[0][2 * e], x[0][2 * e + 1], x[1][2 * e]), x[1][2 * e + 1]) * fs[n][m][e];
-              move |= top[n][m][e] - rr[m][e] > K8_SLACK || lv[n] + (top[n][m][e] - RR[m][e]) > K8_SLACK + K8_PBIAS;
+              top[n][m][e] = fmaxf(fmax3(x[0][2 * e], x[0][2 * e + 1], x[1][2 * e]), x[1][2 * e + 1]);
+              const float by = top[n][m][e] - rr[m][e];
+              move |= by > K8_SLACK || (lv[n] - dd[m][e]) + by > K8_SLACK + K8_PBIAS;
             }
         }
         if (__any_sync(FULLW, move)) {
@@ -587,19 +603,22 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float r = rr[m][e], R = RR[m][e];
+              float r = rr[m][e], x[NB];
 #pragma unroll
               for (int n = 0; n < NB; ++n) {
-                float x = top[n][m][e];
-                x = fmaxf(x, __shfl_xor_sync(FULLW, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(FULLW, x, 2));
-                r = fmaxf(r, x);
-                R = fmaxf(R, x + lv[n] - K8_PBIAS);
+                x[n] = top[n][m][e];
+                x[n] = fmaxf(x[n], __shfl_xor_sync(FULLW, x[n], 1));
+                x[n] = fmaxf(x[n], __shfl_xor_sync(FULLW, x[n], 2));
+                r = fmaxf(r, x[n]);
               }
-              const float c = ex2(RR[m][e] - R);
-              ll[m][e] *= ex2(rr[m][e] - r);
+              const float by = rr[m][e] - r;
+              float d = fmaxf(dd[m][e] + by, K8_FAR);
+#pragma unroll
+              for (int n = 0; n < NB; ++n) d = fmaxf(d, (x[n] - r) + lv[n] - K8_PBIAS);
+              const float c = ex2((dd[m][e] - d) + by);
+              ll[m][e] *= ex2(by);
               rr[m][e] = r;
-              RR[m][e] = R;
+              dd[m][e] = d;
 #pragma unroll
               for (int d = 0; d < 16; ++d) {
                 O[m][d][2 * e] *= c;
@@ -615,13 +634,14 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // exp2(score + lv - R) is exp2(score - r) times exp2 of this; where it is within 2^64 either way, a product
-              // that underflows is below fp16's least number all the same
-              const float h = lv[n] - RR[m][e] + rr[m][e], w = ex2(h);
+              // a weight is exp2(score - r) times exp2 of this; where it is within 2^64 either way, a product that underflows
+              // is below fp16's least number all the same
+              const float h = lv[n] - dd[m][e], w = ex2(h);
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
-                const float x = S[n][m][nt][2 * e], y = S[n][m][nt][2 * e + 1];
-                const float a = ex2(fmaf(x, fs[n][m][e], -rr[m][e])), b = ex2(fmaf(y, fs[n][m][e], -rr[m][e]));
+                float &x = S[n][m][nt][2 * e], &y = S[n][m][nt][2 * e + 1];
+                f32x2_split(add_f32x2(f32x2(x, y), f32x2(-rr[m][e], -rr[m][e])), x, y);
+                const float a = ex2(x), b = ex2(y);
                 ll[m][e] += a + b;
                 P[n][m][nt][e] = pack_h2(a * w, b * w);
               }
@@ -636,8 +656,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
               for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
-                  P[n][m][nt][e] = pack_h2(ex2(fmaf(S[n][m][nt][2 * e], fs[n][m][e], lv[n] - RR[m][e])),
-                                           ex2(fmaf(S[n][m][nt][2 * e + 1], fs[n][m][e], lv[n] - RR[m][e])));
+                  P[n][m][nt][e] = pack_h2(ex2(S[n][m][nt][2 * e] + (lv[n] - dd[m][e])),
+                                           ex2(S[n][m][nt][2 * e + 1] + (lv[n] - dd[m][e])));
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -678,7 +698,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           l += __shfl_xor_sync(FULLW, l, 1);
           l += __shfl_xor_sync(FULLW, l, 2);
           // numerators in the scores' reference, by the root of the factor twice: scales near fp32's least number
-          const float r = ref(rr[m][e], l), c = ex2(0.5f * (RR[m][e] - (r == NEG_INF ? 0.f : r)));
+          const float r = ref(rr[m][e], l), c = ex2(0.5f * dd[m][e]);
           if (t == 0) *reinterpret_cast<float2 *>(mml + warp * 32 + (gr + 8 * e) * 2) = make_float2(r, l);
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -699,7 +719,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
       for (int j = 0; j < 12; ++j) qb[j] = make_uint2(lds32(smem + j * 512 + lane * 16), lds32(smem + j * 512 + lane * 16 + 8));
       float f[2], O[8][4];  // O[2g + j]: dims 32 g + 4 gr + 2 j (rows gr) and + 1 (rows gr + 8)
-      float rr[2], RR[2], ll[2];
+      float rr[2], dd[2], ll[2];
       int keys[2], least = 0x7fffffff;
 #pragma unroll
       for (int n = 0; n < 8; ++n) O[n][0] = O[n][1] = O[n][2] = O[n][3] = 0.f;
@@ -708,7 +728,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
         f[e] = sFac[2 * t + e];
         keys[e] = 2 * t + e < nq ? sKeys[2 * t + e] : 0x7fffffff;
         least = min(least, keys[e]);
-        rr[e] = RR[e] = K8_NONE;
+        rr[e] = K8_NONE;
+        dd[e] = K8_FAR;
         ll[e] = 0.f;
       }
 #pragma unroll
@@ -735,13 +756,17 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
                       kv8_pair<1>(word(kb[n], j)), qb[4 * g + j].x, qb[4 * g + j].y);
         }
         uint4 tail[NB];
-        float lv[NB], fs[NB][2], top[NB][2];
+        float lv[NB], top[NB][2];
         bool move = false;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) S[n][u] += S2[n][u];
           tail[n] = lds128(T[n] + KV8_OFF_TAIL);
+          const float ks = __uint_as_float(tail[n].x);
+          lv[n] = lg2(__uint_as_float(tail[n].y));
+          const uint64_t fs = mul_f32x2(f32x2(ks, ks), f32x2(f[0], f[1]));
+#pragma unroll
+          for (int h = 0; h < 4; h += 2)
+            f32x2_split(mul_f32x2(add_f32x2(f32x2(S[n][h], S[n][h + 1]), f32x2(S2[n][h], S2[n][h + 1])), fs), S[n][h], S[n][h + 1]);
           if (!(key0[n] + 16 <= least && tail[n].z == 0)) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -750,31 +775,32 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
               else if (tail[n].z >> k & 1) S[n][u] = __uint_as_float(0x7fffffffu);
             }
           }
-          const float ks = __uint_as_float(tail[n].x);
-          lv[n] = lg2(__uint_as_float(tail[n].y));
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            fs[n][e] = fmaf(ks, f[e], 0x1p-126f);
-            top[n][e] = fmaxf(S[n][e], S[n][2 + e]) * fs[n][e];
-            move |= top[n][e] - rr[e] > K8_SLACK || lv[n] + (top[n][e] - RR[e]) > K8_SLACK + K8_PBIAS;
+            top[n][e] = fmaxf(S[n][e], S[n][2 + e]);
+            const float by = top[n][e] - rr[e];
+            move |= by > K8_SLACK || (lv[n] - dd[e]) + by > K8_SLACK + K8_PBIAS;
           }
         }
         if (__any_sync(FULLW, move)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float r = rr[e], R = RR[e];
+            float r = rr[e], x[NB];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-              float x = top[n][e];
+              x[n] = top[n][e];
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(FULLW, x, o));
-              r = fmaxf(r, x);
-              R = fmaxf(R, x + lv[n] - K8_PBIAS);
+              for (int o = 4; o < 32; o <<= 1) x[n] = fmaxf(x[n], __shfl_xor_sync(FULLW, x[n], o));
+              r = fmaxf(r, x[n]);
             }
-            const float c = ex2(RR[e] - R);
-            ll[e] *= ex2(rr[e] - r);
+            const float by = rr[e] - r;
+            float d = fmaxf(dd[e] + by, K8_FAR);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) d = fmaxf(d, (x[n] - r) + lv[n] - K8_PBIAS);
+            const float c = ex2((dd[e] - d) + by);
+            ll[e] *= ex2(by);
             rr[e] = r;
-            RR[e] = R;
+            dd[e] = d;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
               O[d][e] *= c;
@@ -789,7 +815,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float h = lv[n] - RR[e] + rr[e];
+            const float h = lv[n] - dd[e];
             w[n][e] = ex2(h);
             far |= !(fabsf(h) <= 64.f);
           }
@@ -798,12 +824,13 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float x = S[n][2 * h], y = S[n][2 * h + 1];
-            const float a = ex2(fmaf(x, fs[n][0], -rr[0])), b = ex2(fmaf(y, fs[n][1], -rr[1]));
+            float x, y;
+            f32x2_split(add_f32x2(f32x2(S[n][2 * h], S[n][2 * h + 1]), f32x2(-rr[0], -rr[1])), x, y);
+            const float a = ex2(x), b = ex2(y);
             ll[0] += a;
             ll[1] += b;
             uint32_t pw = pack_h2(a * w[n][0], b * w[n][1]);
-            if (far) pw = pack_h2(ex2(fmaf(x, fs[n][0], lv[n] - RR[0])), ex2(fmaf(y, fs[n][1], lv[n] - RR[1])));
+            if (far) pw = pack_h2(ex2(x + (lv[n] - dd[0])), ex2(y + (lv[n] - dd[1])));
             if (tail[n].z >> 16 && (tail[n].z >> (16 + gr + 8 * h) & 1)) {  // a V row that is not finite
               const int k = key0[n] + gr + 8 * h;
               pw |= (k < min(keys[0], key_hi) ? 0x7fffu : 0u) | (k < min(keys[1], key_hi) ? 0x7fff0000u : 0u);
@@ -826,7 +853,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) ll[e] += __shfl_xor_sync(FULLW, ll[e], o);
         r[e] = ref(rr[e], ll[e]);
-        c[e] = ex2(0.5f * (RR[e] - (r[e] == NEG_INF ? 0.f : r[e])));  // (twice, as above)
+        c[e] = ex2(0.5f * dd[e]);  // (twice, as above)
       }
       if (gr == 0) *reinterpret_cast<float4 *>(mml + warp * 32 + 4 * t) = make_float4(r[0], ll[0], r[1], ll[1]);
       float *o = mo + warp * 16 * MO_STRIDE + 2 * t * MO_STRIDE + 4 * gr;
