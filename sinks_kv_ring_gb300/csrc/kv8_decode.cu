@@ -68,7 +68,7 @@ constexpr int K8_MT = 2;
 constexpr int K8_ROWS = 16 * K8_MT;  // query rows of a part: those of up to 4 batch rows of one sequence
 constexpr float K8_PBIAS = 11.f;     // weights are 2^11 where they equal the reference
 constexpr float K8_SLACK = 4.f;      // how far a score or weight may pass its reference
-constexpr float K8_NONE = -1e30f;    // a reference before the first keys
+constexpr float K8_NONE = -3.402823466e38f;  // a reference before the first keys: fp32's lowest finite number, so no score is below it
 constexpr float K8_FAR = -512.f;     // least distance of the weights' reference: 2^-512 of the largest probability is no fp32 number
 // The work line (line.cuh) in units of one tile.  A row's set-up and merge, in units
 // (48 ragged rows at 8 heads a group: 24 -> 83.9 us, 36 -> 82.8, 56 -> 83.0; at 16:
@@ -485,9 +485,9 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
         *reinterpret_cast<float4 *>(po + g * DV + d4) = acc;
       }
     };
-    // A warp's reference of a row for the merge: none (-inf) where it saw no key of the row's, 0 where no score was a
-    // number (the row will not be one either).
-    auto ref = [](float r, float l) { return r != K8_NONE ? r : l == 0.f ? NEG_INF : 0.f; };
+    // A warp's reference of a row for the merge: none (-inf) where it saw no key of the row's.  (The largest key adds 1 to
+    // the sum; where no score is a number the sum is none either, and makes the row's one, whatever the reference is.)
+    auto ref = [](float r, float l) { return l == 0.f ? NEG_INF : r; };
     const float *sFac = reinterpret_cast<const float *>(smem + K8_OFF_ROW);
 
     // MT x 16 query rows as rows of the products; this lane has rows gr and gr + 8 (index e) of each

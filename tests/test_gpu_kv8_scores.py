@@ -146,6 +146,14 @@ def test_scores_of_one_size(table, size, n, most, G, rows):
         _check_one_size(got, q, pos, pool, n, whole, f"{size} {vscales}")
 
 
+@pytest.mark.parametrize("G,rows", [(4, 1), (8, 1), (16, 1), (4, 4), (8, 4), (16, 4)])
+@pytest.mark.parametrize("n,most", [(1, 1), (20, 64), (600, 600), (9000, 9000)])
+@pytest.mark.parametrize("size", [1e30, 1e31, 1e32, 1e37])
+def test_scores_far_below_zero(table, size, n, most, G, rows):
+    """Rows whose scores all lie below -1e30, and as far above zero: no finite score stands for a row without keys."""
+    test_scores_of_one_size(table, size, n, most, G, rows)
+
+
 @pytest.mark.parametrize("G,rows", [(4, 1), (8, 1), (16, 1), (16, 4)])
 @pytest.mark.parametrize("n", [200, 9000])
 @pytest.mark.parametrize("mag", [1e-30, 1.0, 30.0, 300.0, 3e3])
