@@ -73,6 +73,15 @@ struct Kv8Units {
   __host__ __device__ __forceinline__ long long first(int cu, int i) const { return (cu >> shift) + (long long)each * i; }
 };
 constexpr Kv8Units KV8_BY_TILE{4, 2}, KV8_BY_ROW{0, 0};
+// Whether a chunk's rows are out of order, or not among the call's T.
+__device__ __forceinline__ bool kv8_rows_odd(int c0, int c1, long long T) { return c0 < 0 || c1 < c0 || c1 > T; }
+// Flags such chunks of a call.  The units may leave one out (no unit is its own, or the search
+// passes it by), so each is looked at by one thread of the grid: thread `me` of a CTA's `all`.
+__device__ __forceinline__ void kv8_rows_check(const int32_t *__restrict__ cu, int n, long long T, unsigned me, unsigned all,
+                                               unsigned *status) {
+  for (long long i = (long long)blockIdx.x * all + me; i < n; i += (long long)gridDim.x * all)
+    if (kv8_rows_odd(cu[i], cu[i + 1], T)) flag(status, ST_BAD_ROWS);
+}
 // The chunk that owns unit `unit`, by a warp: a search over cu_rows, and no plan is
 // made first.  A round narrows the chunks down by 32; the last 64 are read whole, with
 // their positions and sequences, so that a batch of up to 64 waits for one load where

@@ -19,7 +19,7 @@
 // A CTA takes one tile: two warps half of a head's K rows each, two half of its V
 // dims each, with 16 bytes of codes a lane and store; two of a kind exchange their
 // largest magnitudes through shared memory.  A first warp finds the tile's chunk and
-// rows for all.  A chunk that starts inside a tile finds the rows ahead of it there:
+// rows for all, while the others look at a part of cu_rows each CTA (kv8_rows_check).  A chunk that starts inside a tile finds the rows ahead of it there:
 // their V codes share 16 bytes with the new ones and are read in any case, their K
 // codes only where the scale grows.  Large calls take up to four heads of a tile
 // one after the other (MANY), for one search and one look at the RoPE rows; where that
@@ -408,10 +408,7 @@ __device__ __forceinline__ bool append_item(const Kv8Append &A, long long unit, 
   const Kv8Chunk C = kv8_chunk(A.cu_rows, A.P0, A.seqs, A.n, A.units, unit);
   const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
   const long long a = C.pos;
-  if (c0 < 0 || c1 < c0 || c1 > A.T) {
-    if (say) flag(A.status, ST_BAD_ROWS);
-    return false;
-  }
+  if (kv8_rows_odd(c0, c1, A.T)) return false;
   const long long u = unit - A.units.first(c0, i);
   if (u < 0 || c1 == c0 || s == -1) return false;
   const bool bs = s < 0 || s >= A.dst.num_seqs;
@@ -448,6 +445,8 @@ __global__ void __launch_bounds__(K8A_WARPS * 32, K8A_CTAS) kv8_append_kernel(Kv
     const int32_t *entry = nullptr;
     append_item(A, unit, say, I, entry);
     if (lane == 0) s_item = I, s_entry = entry;
+  } else {
+    kv8_rows_check(A.cu_rows, A.n, A.T, threadIdx.x - 32, 32 * (K8A_WARPS - 1), A.status);
   }
   __syncthreads();
   if (!s_entry) return;

@@ -1,0 +1,78 @@
+"""Batches of chunks of the 8-bit pool whose cu_rows is out of order, or runs past the
+rows that there are: the call says so, whatever form its units take."""
+import numpy as np
+import pytest
+import torch
+
+import sinks_kv_ring_gb300 as kvr
+from oracle import kv8 as o8
+
+from test_gpu_kv8 import DEV, VS, _append, _built, _gen, _ints, _kv, _oracle_append, _pool, table  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _filled(gen, n, first, hkv, cap, table):
+    pool = _pool(gen, n, hkv, cap, 16, fill=0x21)
+    T = int(sum(first))
+    k, v = _kv(gen, max(T, 1), hkv)
+    _append(pool, k, v, list(range(n)), [0] * n, list(first), table)
+    return pool
+
+
+def _check_append(pool, cu, T, first, hkv, gen, table, flags, served, seqs=None, lo=None, good=None):
+    """The first `good` chunks (all) are the oracle's, those of `served`, or as they were; the others are not looked at."""
+    n = len(cu) - 1
+    seqs = list(range(n)) if seqs is None else seqs
+    lo = list(first) if lo is None else lo
+    want, bt = pool.data.cpu().numpy(), pool.block_table.cpu().numpy()
+    k, v = _kv(gen, T, hkv)
+    kvr.kv8_append_rope(k, v, _ints(cu, torch.int32), _ints(lo, torch.int64), _ints(seqs, torch.int32), table, VS, pool)
+    said = kvr.device_status()
+    assert said == flags if good in (None, n) else said & flags
+    written = {}
+    for i in served:
+        _oracle_append(want, bt, k[cu[i]:cu[i + 1]], v[cu[i]:cu[i + 1]], [seqs[i]], [int(lo[i])], [cu[i + 1] - cu[i]], table,
+                       written=written)
+    got = pool.data.cpu().numpy()
+    for blk in bt[n if good is None else good:].flatten():
+        if 0 <= blk < len(got):
+            got[blk] = want[blk] = 0
+    assert o8.same(got, want, written)
+
+
+@pytest.mark.parametrize("n", [65, 500, 5000, 20000])
+def test_out_of_order_among_many(table, n):
+    """Told of any batch, wherever the place is; past 64 chunks, which of the others are written is not said."""
+    gen = _gen(n)
+    for at, to in ((n // 2, 7), (n, n + 1), (n - 1, -1), (0, -1), (1, n + 5)):
+        for each in (1, 20):
+            T = n * each
+            pool = _pool(gen, n, 1, 32, 16, fill=0x21)
+            k, v = _kv(gen, T, 1)
+            cu = torch.arange(n + 1, dtype=torch.int32, device=DEV) * each
+            cu[at] = to if to < n else to + T - n
+            P0, seqs = torch.zeros(n, dtype=torch.int64, device=DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+            kvr.kv8_append_rope(k, v, cu, P0, seqs, table, VS, pool)
+            assert kvr.device_status() & kvr.DEV_BAD_ROWS
+            kvr.kv8_unpack(pool, seqs, P0, cu, kvr.LinearLayout.empty(T, 1))
+            assert kvr.device_status() & kvr.DEV_BAD_ROWS
+
+
+@pytest.mark.parametrize("n", [8, 70])
+def test_single_rows_and_what_cannot_be_written(table, n):
+    """A decode step's chunks of one row: padding, ids, positions and blocks that are not there, beside good ones."""
+    gen, hkv = _gen(n), 2
+    first = [(5 * i) % 31 for i in range(n)]
+    pool = _filled(gen, n, first, hkv, 32, table)
+    pool.block_table[6, first[6] // 16] = pool.num_blocks
+    pool.block_table[2, first[2] // 16] = -1
+    cu = list(range(n + 1))
+    odd = {1: (n, None), 3: (None, 32), 4: (None, -1), 5: (-1, 1 << 60), 7: (-9, 0)}
+    seqs = [odd[i][0] if i in odd and odd[i][0] is not None else i for i in range(n)]
+    lo = [odd[i][1] if i in odd and odd[i][1] is not None else first[i] for i in range(n)]
+    served = [i for i in range(n) if i not in odd and i not in (2, 6)]
+    _check_append(pool, cu, n, first, hkv, gen, table, kvr.DEV_BAD_SEQ | kvr.DEV_BAD_POS | kvr.DEV_BAD_BLOCK, served, seqs, lo)
+    # and with the one in the middle past the rows that there are
+    cu[2 if n <= 64 else 70] = n + 1
+    _check_append(pool, cu, n, first, hkv, gen, table, kvr.DEV_BAD_ROWS, [0] if n <= 64 else [], seqs, lo, good=1 if n <= 64 else 0)
