@@ -646,7 +646,8 @@ kvr_status kv4_unpack(const kvr_kv4_layout *src, const int32_t *src_seqs, const 
  * head) holding a NaN or an infinity reads as NaN and counts for no scale.
  * cu_rows [n+1] int32, P0 [n] int64, seqs [n] int32 are device arrays; cu_rows
  * must be non-decreasing within [0, T] (an entry that is not is skipped with
- * KVR_DEV_BAD_ROWS, and entries after it may be skipped too).  seqs[i] = -1
+ * KVR_DEV_BAD_ROWS, and entries after it may be skipped too; in a call of more
+ * than 64 chunks any may be).  seqs[i] = -1
  * marks padding: the chunk is skipped and nothing is flagged.  A chunk with a
  * sequence id outside the layout (KVR_DEV_BAD_SEQ), or with P0 < 0 or rows past
  * the RoPE table or the block table (KVR_DEV_BAD_POS), is skipped; a tile whose
@@ -676,7 +677,8 @@ kvr_status full_attn_decode_kv8(const kvr_bf16 *q, const int64_t *pos, const int
 
 /*
  * Positions of an 8-bit pool as bf16 (one rounding of s * u), into pages or
- * rows.  Arguments, flags and results as kv4_unpack.
+ * rows.  Arguments, flags and results as kv4_unpack; of a cu_rows out of order
+ * as kv8_append_rope.
  */
 kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
                       int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);

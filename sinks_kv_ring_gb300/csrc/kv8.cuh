@@ -82,10 +82,16 @@ __device__ __forceinline__ void kv8_rows_check(const int32_t *__restrict__ cu, i
   for (long long i = (long long)blockIdx.x * all + me; i < n; i += (long long)gridDim.x * all)
     if (kv8_rows_odd(cu[i], cu[i + 1], T)) flag(status, ST_BAD_ROWS);
 }
+__device__ __forceinline__ int ones_from_below(unsigned m) { return __clz(__brev(~m)); }
 // The chunk that owns unit `unit`, by a warp: a search over cu_rows, and no plan is
 // made first.  A round narrows the chunks down by 32; the last 64 are read whole, with
 // their positions and sequences, so that a batch of up to 64 waits for one load where
 // a binary search waits for one a step and then for the chunk's own.
+//
+// It is the one ahead of the first that begins past the unit.  So where cu_rows is out of
+// order, a unit of a chunk ahead of the place finds its chunk all the same, up to 64
+// chunks: all from the first to its own begin no later, and the next one does.  (Of more,
+// the ones that a round looks at may lie behind the place.)
 __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, const int64_t *__restrict__ pos,
                                               const int32_t *__restrict__ seqs, int n, Kv8Units units, long long unit) {
   const unsigned full = 0xffffffffu;
@@ -95,7 +101,7 @@ __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, co
     const int step = (len + 31) >> 5, i = lo + lane * step;
     const bool in = lane * step < len;
     const unsigned m = __ballot_sync(full, in && units.first(in ? cu[i] : 0, i) <= unit);
-    const int last = 31 - __clz(m | 1u);  // (chunk 0 always counts)
+    const int last = max(ones_from_below(m), 1) - 1;  // (chunk 0 always counts)
     len = min(step, len - last * step);
     lo += last * step;
   }
@@ -106,7 +112,7 @@ __device__ __forceinline__ Kv8Chunk kv8_chunk(const int32_t *__restrict__ cu, co
   const int sa = in_a ? seqs[ia] : 0, sb = in_b ? seqs[ib] : 0;
   const unsigned ma = __ballot_sync(full, in_a && units.first(ca, ia) <= unit);
   const unsigned mb = __ballot_sync(full, in_b && units.first(cb, ib) <= unit);
-  const int at = mb ? 63 - __clz(mb) : 31 - __clz(ma | 1u), l = at & 31, l1 = (at + 1) & 31;
+  const int at = max(ma == full ? 32 + ones_from_below(mb) : ones_from_below(ma), 1) - 1, l = at & 31, l1 = (at + 1) & 31;
   const int n_a = __shfl_sync(full, ca, l1), n_b = __shfl_sync(full, cb, l1);
   Kv8Chunk C;
   C.i = lo + at;

@@ -1,5 +1,6 @@
 """Batches of chunks of the 8-bit pool whose cu_rows is out of order, or runs past the
-rows that there are: the call says so, whatever form its units take."""
+rows that there are: the call says so, whatever form its units take, and up to 64 chunks
+those ahead of the place are written as if there were no others."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +11,12 @@ from oracle import kv8 as o8
 from test_gpu_kv8 import DEV, VS, _append, _built, _gen, _ints, _kv, _oracle_append, _pool, table  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def _served(cu, T):
+    """How many chunks lie ahead of the first that is out of order."""
+    ok = [0 <= a <= b <= T for a, b in zip(cu, cu[1:])]
+    return ok.index(False) if False in ok else len(ok)
 
 
 def _filled(gen, n, first, hkv, cap, table):
@@ -39,6 +46,86 @@ def _check_append(pool, cu, T, first, hkv, gen, table, flags, served, seqs=None,
         if 0 <= blk < len(got):
             got[blk] = want[blk] = 0
     assert o8.same(got, want, written)
+
+
+def _check_unpack(pool, cu, T, hkv, flags, served, first=0):
+    n = len(cu) - 1
+    lo, seqs = [first] * n, list(range(n))
+    out = kvr.LinearLayout(torch.full((T, hkv, 192), 7.0, dtype=torch.bfloat16, device=DEV),
+                           torch.full((T, hkv, 128), 7.0, dtype=torch.bfloat16, device=DEV))
+    kvr.kv8_unpack(pool, _ints(seqs, torch.int32), _ints(lo, torch.int64), _ints(cu, torch.int32), out)
+    said = kvr.device_status()
+    assert said & flags if served < n else said == flags
+    data, bt = pool.data.cpu().numpy(), pool.block_table.cpu().numpy()
+    behind = np.zeros(T, bool)  # rows that a chunk behind the place names: its own, or the one's ahead
+    for a, b in zip(cu[served:], cu[served + 1:]):
+        behind[max(a, 0):max(b, 0)] = True
+    for i in range(served):
+        if cu[i] < cu[i + 1]:
+            for h in range(hkv):
+                keep = torch.from_numpy(~behind[cu[i]:cu[i + 1]])
+                K, V, _ = o8.sequence(data, bt[i], h, first + cu[i + 1] - cu[i])
+                for got, want in ((out.k, K), (out.v, V)):
+                    assert torch.equal(got[cu[i]:cu[i + 1], h].cpu()[keep], torch.from_numpy(want[first:]).bfloat16()[keep]), i
+    if served == n:
+        assert (out.k[max(cu[-1], 0):] == 7).all() and (out.v[max(cu[-1], 0):] == 7).all()
+
+
+ORDERS = {
+    "past the rows": ([*range(13)], 9),
+    "past the rows, by far": ([0, 1, 2, 3, 4, 5, 6, 7, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1], 9),
+    "a step back": ([0, 1, 2, 3, 4, 3, 4, 5, 6, 7, 8, 9, 10], 10),
+    "back to the first": ([0, 1, 0, 1], 1),
+    "negative first": ([-2, 0, 1], 1),
+    "negative first of many": ([-1, *range(1, 12)], 12),
+    "negative last": ([0, 1, 2, 3, 4, 5, 6, 7, 8, -4], 9),
+    "back by more than a tile's units": ([0, 100, 0, 100], 100),
+    "back behind a long one": ([0, 3, 90, 91, 20, 95, 100], 100),
+    "empty ahead of the place": ([0, 0, 0, 1, 1, 0, 1], 1),
+}
+
+
+@pytest.mark.parametrize("name", list(ORDERS))
+def test_out_of_order(table, name):
+    cu, T = ORDERS[name]
+    n, hkv, gen = len(cu) - 1, 2, _gen(len(name))
+    first = [3 * i % 17 for i in range(n)]
+    good = _served(cu, T)
+    assert good < n
+    most = max([1] + [cu[i + 1] - cu[i] for i in range(good)])
+    pool = _filled(gen, n, first, hkv, 32 + most, table)
+    _check_append(pool, cu, T, first, hkv, gen, table, kvr.DEV_BAD_ROWS, range(good), good=good)
+    whole = _filled(gen, n, [most + 16] * n, hkv, 32 + most, table)
+    _check_unpack(whole, cu, T, hkv, kvr.DEV_BAD_ROWS, good, first=5)
+
+
+@pytest.mark.parametrize("hkv", [1, 5])
+@pytest.mark.parametrize("n", [3, 33, 40, 64])
+@pytest.mark.parametrize("mean", [1, 12])
+def test_one_place_out_of_order(table, mean, n, hkv):
+    """Batches in order but for one entry, anywhere, or for none: by row and by tile, one head a CTA and several."""
+    rng, gen = np.random.default_rng(n + mean + hkv), _gen(n + mean + hkv)
+    for case in range(4):
+        rows = rng.integers(0, 2 * mean + 1, n)
+        cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int64)
+        T = max(int(cu[-1]), 1)
+        at = int(rng.integers(0, n + 1))
+        if case == 0:
+            cu[at] = -1 - int(rng.integers(0, 1000))
+        elif case == 1:
+            cu[at] = T + 1 + int(rng.integers(0, 1000))
+        elif case == 2:
+            cu[at] = int(rng.integers(0, T + 1))
+        cu = cu.tolist()
+        good = _served(cu, T)
+        flags = kvr.DEV_BAD_ROWS if good < n else 0
+        first = rng.integers(0, 20, n).tolist()
+        # (chunk `at` may have got longer, up to all rows, and be in order)
+        most = max([1] + [cu[i + 1] - cu[i] for i in range(good)])
+        pool = _filled(gen, n, first, hkv, 20 + most, table)
+        _check_append(pool, cu, T, first, hkv, gen, table, flags, range(good), good=good)
+        whole = _filled(gen, n, [most + 3] * n, hkv, 20 + most, table)
+        _check_unpack(whole, cu, T, hkv, flags, good, first=3)
 
 
 @pytest.mark.parametrize("n", [65, 500, 5000, 20000])
