@@ -391,10 +391,10 @@ __global__ void __cluster_dims__(SH_CTAS, 1, 1) __launch_bounds__(SH_THREADS) pa
   const bool none = wrong || limit < used;
   if (me == 0 && none) flag(A.status, wrong ? ST_BAD_BLOCK : ST_NO_BLOCKS);
   if (none) {  // as it was
-    for (long long b = me; b < num; b += ALL) {
-      if (A.refs_out != A.refs) A.refs_out[b] = A.refs[b];
-      if (A.free_out != A.free_ids && sane && b < count) A.free_out[b] = A.free_ids[b];
-    }
+    if (A.refs_out != A.refs)
+      for (long long b = me; b < num; b += ALL) A.refs_out[b] = A.refs[b];
+    if (A.free_out != A.free_ids)  // (a count that is none of the list's names all of it, or nothing)
+      for (long long j = me; j < min(count, A.free_cap); j += ALL) A.free_out[j] = A.free_ids[j];
     if (A.table_out != A.table)
       for (long long e = me; e < A.entries; e += ALL) A.table_out[e] = A.table[e];
     if (me == 0) *A.copy_count = 0;
