@@ -752,6 +752,7 @@ def kv4_append_rope(k, v, pos, seq, table, value_scale, dst, slots=None, stream=
     T, H = k.shape[:2]
     if k.shape[2] != DQK or v.shape != (T, H, DV) or pos.shape[0] != T:
         raise ValueError("k/v/pos shapes disagree")
+    _want_pool(dst, Kv4Layout)
     _same_device(k, v, pos, seq, slots, table, *dst.tensors())
     c = dst.c()
     _check(lib().kv4_append_rope(_ptr(k), _ptr(v), _ptr(pos), _ptr(seq), _ptr(slots), T, H, _ptr(table),
