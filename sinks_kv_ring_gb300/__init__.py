@@ -771,7 +771,6 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
 
 
 def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_ctx, workspace, out, stream):
-    _want_pool(pool, kind)
     cur = torch.cuda.current_device()
     try:
         B, Hq, D = q.shape
@@ -792,19 +791,19 @@ def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_c
         P = table.shape[0]
         _want_len(pos, "pos", B)
         _want_len(seq, "seq", B)
-        _same_device(q, pos, seq, table, *pool.tensors())
+    _want_pool(pool, kind)
+    given = workspace is not None or out is not None
     if workspace is None:
         n = size(B, Hq, pool.num_kv_heads, max_ctx)
         if n:  # (short contexts need none)
             workspace = _empty(n, torch.uint8, q, stream)
     else:
         _want(workspace, "workspace", torch.uint8, 1)
-        _same_device(q, workspace)
-    if out is None:
-        out = _empty((B, Hq, DV), _BF, q, stream)
-    else:
-        out = _out(out, B, Hq, q, stream)
-        _same_device(q, out)
+    out = _out(out, B, Hq, q, stream)
+    if not fine:
+        _same_device(q, pos, seq, table, workspace, out, *pool.tensors())
+    elif given:
+        _same_device(q, workspace, out)
     c = pool.c()
     _check(fn(q.data_ptr(), pos.data_ptr(), seq.data_ptr(), B, Hq, ctypes.byref(c), table.data_ptr(), P,
               float(softmax_scale), int(max_ctx), None if workspace is None else workspace.data_ptr(),
@@ -813,7 +812,12 @@ def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_c
 
 
 def _want_pool(pool, kind):
-    if getattr(pool, "TILE", None) != kind.TILE:  # (the layouts' structs look alike to the library)
+    """The quantised layouts' structs look alike to the library, so a pool says by TILE which it is; one of the caller's own
+    kind that does not say is a 4-bit one."""
+    tile = getattr(pool, "TILE", None)
+    if tile is None and not isinstance(pool, (RingLayout, PagedLayout, LinearLayout)):
+        tile = KV4_TILE
+    if tile != kind.TILE:
         raise TypeError(f"a {kind.__name__} is wanted, got {type(pool).__name__}")
 
 
@@ -827,15 +831,6 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
 
 
 def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream):
-    _want_pool(src, kind)
-    if isinstance(dst, LinearLayout):
-        most = dst.num_rows
-    elif isinstance(dst, PagedLayout):
-        if dst_seqs is None:
-            raise ValueError("dst_seqs names the sequences of a PagedLayout")
-        most = min(dst.num_seqs * dst.max_blocks * dst.block_size, 2 ** 31 - 1)
-    else:
-        raise TypeError("dst must be a PagedLayout or a LinearLayout")
     cur = torch.cuda.current_device()
     try:
         n, = src_seqs.shape
@@ -853,6 +848,16 @@ def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream
         n = src_seqs.shape[0]
         _want_len(lo, "lo", n)
         _want_len(cu_rows, "cu_rows", n + 1)
+    if isinstance(dst, LinearLayout):
+        most = dst.num_rows
+    elif isinstance(dst, PagedLayout):
+        if dst_seqs is None:
+            raise ValueError("dst_seqs names the sequences of a PagedLayout")
+        most = min(dst.num_seqs * dst.max_blocks * dst.block_size, 2 ** 31 - 1)
+    else:
+        raise TypeError("dst must be a PagedLayout or a LinearLayout")
+    _want_pool(src, kind)
+    if not fine:
         if dst_seqs is not None:
             _want(dst_seqs, "dst_seqs", torch.int32, 1)
             _want_len(dst_seqs, "dst_seqs", n)

@@ -45,3 +45,47 @@ def test_a_pool_of_other_bits_is_refused(rec, kind):  # noqa: F811
             with pytest.raises(TypeError):
                 call()
             assert not [name for name, _ in rec.calls[n:] if not name.endswith("workspace_size")]
+
+
+class _Pool4:
+    """A caller's own 4-bit pool: the struct and its tensors, and no more."""
+
+    def __init__(self):
+        self.inner = kvr.Kv4Layout.contiguous(3, 2, 100, block_size=32, device="cpu")
+        self.num_kv_heads = 2
+
+    def tensors(self):
+        return self.inner.tensors()
+
+    def c(self):
+        return self.inner.c()
+
+
+def test_a_callers_own_4_bit_pool_is_taken(rec):  # noqa: F811
+    for bits, call in _calls(_Pool4()):
+        if bits == 4:
+            call()
+        else:
+            with pytest.raises(TypeError):
+                call()
+    assert [n for n, _ in rec.calls if not n.endswith("workspace_size")] == ["kv4_append_rope", "kv4_append_rope",
+                                                                            "full_attn_decode_kv4", "kv4_unpack"]
+
+
+def test_the_first_wrong_argument_is_named(rec):  # noqa: F811
+    """Of several wrong arguments the refusal names the one that comes first in the call's checks: queries, positions,
+    lengths, the workspace, the output; entries ahead of the destination."""
+    pool, table = _pools()[4], _z(F32, 300, 32, 2)
+    q, pos, seq = _z(BF, 3, 16, 192), _z(I64, 3), _z(I32, 3)
+    ws, odd = _z(torch.uint8, 8192), _z(BF, 3, 16, 192)
+    for args, kw, name in (((q.float(), pos.int(), seq, pool, table), {}, "q must be"),
+                           ((q, pos.int(), seq, None, table), {}, "pos must be"),
+                           ((q, pos, _z(I32, 2), pool, table), dict(out=odd), "seq must have"),
+                           ((q, pos, seq, pool, table), dict(workspace=ws.int(), out=odd), "workspace must be"),
+                           ((q, pos, seq, pool, table), dict(workspace=ws, out=odd), "out must be")):
+        with pytest.raises((TypeError, ValueError), match=name):
+            kvr.full_attn_decode_kv4(*args, 0.1, 100, **kw)
+    with pytest.raises(TypeError, match="lo must be"):
+        kvr.kv4_unpack(pool, _z(I32, 2), _z(I32, 2), _z(I32, 3), None)
+    with pytest.raises(ValueError, match="cu_rows must have"):
+        kvr.kv4_unpack(pool, _z(I32, 2), _z(I64, 2), _z(I32, 2), None)
