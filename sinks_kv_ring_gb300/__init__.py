@@ -217,7 +217,8 @@ def _want(t, name, dtype, dim=None, cuda=True):
 # one, which say what is not, cost half as much as such a call again.
 
 _BF, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_ODD = (AttributeError, TypeError, ValueError)  # what such an expression raises over something that is no tensor of its dims
+# what such an expression raises over something that is no tensor of its dims, and where there is no GPU
+_ODD = (AttributeError, TypeError, ValueError, RuntimeError, AssertionError)
 
 
 def _want_q(q):
@@ -771,8 +772,8 @@ def full_attn_decode_kv4(q, pos, seq, pool, table, softmax_scale, max_ctx, works
 
 
 def _decode_tiles(kind, fn, size, q, pos, seq, pool, table, softmax_scale, max_ctx, workspace, out, stream):
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         B, Hq, D = q.shape
         P, half, two = table.shape
         fine = (D == DQK and half == DROT // 2 and two == 2 and q.dtype is _BF and pos.dtype is _I64 and seq.dtype is _I32
@@ -831,8 +832,8 @@ def kv4_unpack(src, src_seqs, lo, cu_rows, dst, dst_seqs=None, T=None, stream=No
 
 
 def _unpack_tiles(kind, fn, src, src_seqs, lo, cu_rows, dst, dst_seqs, T, stream):
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         n, = src_seqs.shape
         fine = (dst_seqs is None and src_seqs.dtype is _I32 and lo.dtype is _I64 and cu_rows.dtype is _I32
                 and lo.shape == (n,) and cu_rows.shape == (n + 1,) and src_seqs.is_contiguous() and lo.is_contiguous()
@@ -875,8 +876,8 @@ def kv8_append_rope(k, v, cu_rows, P0, seqs, table, value_scale, dst, stream=Non
     written in order: those ahead of P0[i] in its tile of 16 are there already,
     those behind the chunk in its last tile mean nothing afterwards."""
     _want_pool(dst, Kv8Layout)
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         T, H, D = k.shape
         n, = seqs.shape
         P, half, two = table.shape
@@ -963,8 +964,8 @@ def kv_pages_free(block_table, num_blocks, block_size, refs, seqs, free_ids, fre
     max_blocks]) become -1, refs (int32 [num_blocks], the holders of a block
     beyond the first) goes down, and the blocks that nobody holds are added to the
     free list (free_ids int32 [cap], free_count int32 [1]) in ascending order."""
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         fine = (keep_lo is None and keep_hi is None
                 and _fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and _fine_ints(cur, seqs))
     except _ODD:
@@ -995,8 +996,8 @@ def kv_pages_fork(block_table, num_blocks, block_size, refs, src_seqs, dst_seqs,
     device."""
     if free_count_out is None:
         free_count_out = free_count
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         n, = src_seqs.shape
         fine = (_fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and lens.dtype is _I64
                 and lens.shape == (n,) and lens.is_contiguous() and lens.get_device() == cur and dst_seqs.numel() == n
@@ -1037,8 +1038,8 @@ def kv_pages_compact(block_table, num_blocks, refs, free_ids, free_count, copy_s
     table_out = block_table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
     free_ids_out = free_ids if free_ids_out is None else free_ids_out
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         fine = (_fine_pages(cur, block_table, num_blocks, refs, free_ids, free_count) and table_out.dtype is _I32
                 and table_out.shape == block_table.shape and table_out.is_contiguous() and table_out.get_device() == cur
                 and refs_out.shape == refs.shape and free_ids_out.shape == free_ids.shape and copy_count.numel() == 1
@@ -1084,8 +1085,8 @@ def kv_pages_copy(pools, copy_src, copy_dst, copy_count, stream=None):
     for t in planes:
         if t.shape[0] != nb:
             raise ValueError(f"the pools have {nb} and {t.shape[0]} blocks: they do not share a block table")
-    cur = torch.cuda.current_device()
     try:
+        cur = torch.cuda.current_device()
         fine = copy_count.numel() == 1 and _fine_ints(cur, copy_src, copy_dst, copy_count)
     except _ODD:
         fine = False

@@ -89,3 +89,28 @@ def test_the_first_wrong_argument_is_named(rec):  # noqa: F811
         kvr.kv4_unpack(pool, _z(I32, 2), _z(I32, 2), _z(I32, 3), None)
     with pytest.raises(ValueError, match="cu_rows must have"):
         kvr.kv4_unpack(pool, _z(I32, 2), _z(I64, 2), _z(I32, 2), None)
+
+
+def test_cpu_tensors_are_refused_where_there_is_no_gpu():
+    """With the library itself, and whether or not a GPU is there: the tensor that is not on one is named."""
+    class Pool:
+        data = block_table = None
+        num_kv_heads = 2
+
+        def __init__(self, tile):
+            self.TILE = tile
+
+    p4, p8 = Pool(kvr.KV4_TILE), Pool(kvr.KV8_TILE)
+    table, k, v, q = _z(F32, 300, 32, 2), _z(BF, 5, 2, 192), _z(BF, 5, 2, 128), _z(BF, 3, 16, 192)
+    bt, refs, ids, one, pairs, two = _z(I32, 3, 4), _z(I32, 12), _z(I32, 12), _z(I32, 1), _z(I32, 12), _z(I32, 2)
+    for call, name in ((lambda: kvr.kv4_append_rope(k, v, _z(I64, 5), _z(I32, 5), table, 0.7, p4), "k"),
+                       (lambda: kvr.full_attn_decode_kv4(q, _z(I64, 3), _z(I32, 3), p4, table, 0.1, 100), "q"),
+                       (lambda: kvr.kv4_unpack(p4, two, _z(I64, 2), _z(I32, 3), None), "src_seqs"),
+                       (lambda: kvr.kv8_append_rope(k, v, _z(I32, 3), _z(I64, 2), two, table, 0.7, p8), "k"),
+                       (lambda: kvr.full_attn_decode_kv8(q, _z(I64, 3), _z(I32, 3), p8, table, 0.1, 100), "q"),
+                       (lambda: kvr.kv8_unpack(p8, two, _z(I64, 2), _z(I32, 3), None), "src_seqs"),
+                       (lambda: kvr.kv_pages_free(bt, 12, 32, refs, two, ids, one), "block_table"),
+                       (lambda: kvr.kv_pages_fork(bt, 12, 32, refs, two, two, _z(I64, 2), ids, one, pairs, pairs, one), "block_table"),
+                       (lambda: kvr.kv_pages_compact(bt, 12, refs, ids, one, pairs, pairs, one), "block_table")):
+        with pytest.raises(ValueError, match=f"^{name} must be a CUDA tensor"):
+            call()
