@@ -617,7 +617,7 @@ kvr_status full_attn_decode_kv4(const kvr_bf16 *q, const int64_t *pos, const int
  * src_seqs [n] int32, lo [n] int64, cu_rows [n+1] int32, dst_seqs [n] int32
  * are device arrays; cu_rows must be non-decreasing within [0, T] (an entry
  * that is not is skipped with KVR_DEV_BAD_ROWS, and entries after it may be
- * skipped too).  Positions that cannot be read (KVR_DEV_BAD_POS,
+ * skipped too; in a call of more than 64 entries any may be).  Positions that cannot be read (KVR_DEV_BAD_POS,
  * KVR_DEV_BAD_SEQ, KVR_DEV_BAD_BLOCK) are written as zeros, except that a
  * negative or too large lo writes no page; a destination that cannot be
  * addressed is flagged and not written.  n = 0 or T = 0 is a no-op.  T may be
@@ -677,8 +677,7 @@ kvr_status full_attn_decode_kv8(const kvr_bf16 *q, const int64_t *pos, const int
 
 /*
  * Positions of an 8-bit pool as bf16 (one rounding of s * u), into pages or
- * rows.  Arguments, flags and results as kv4_unpack; of a cu_rows out of order
- * as kv8_append_rope.
+ * rows.  Arguments, flags and results as kv4_unpack.
  */
 kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const int64_t *lo, const int32_t *cu_rows,
                       int32_t n, int64_t T, const int32_t *dst_seqs, const kvr_kv_layout *dst, void *stream);

@@ -5,9 +5,8 @@
 // Value = m + s * u: the product is exact in fp32, the sum is rounded once to
 // fp32 and once to bf16.  Entry i of the call is cu_rows[i+1] - cu_rows[i]
 // positions from lo[i] on.  A work unit is one tile of 16 positions of one KV
-// head, taken by one warp; entry i owns units cu_rows[i] / 16 + 2i onwards
-// (an entry of n rows touches at most n / 16 + 2 tiles), so a unit finds its
-// entry by a search over cu_rows and no plan is made first.  A call of more than
+// head, taken by one warp; which entry's it is comes from a search over cu_rows
+// (chunk_of), and no plan is made first.  A call of more than
 // K4U_ONCE CTAs goes round with fewer of them instead, and a warp stops behind
 // the last entry's rows: a T far above the rows there are (all that a block
 // table spans) costs neither CTAs nor searches.
@@ -16,6 +15,7 @@
 // long as every store fills its sectors: 122,880 positions of 4 KV heads take
 // 64 us (6.3 TB/s, 0.93 of the copy rate), 70 with K stored 16 bytes at a time
 // and 76 with codes converted by integer-to-float instructions.
+#include "chunks.cuh"
 #include "kv4.cuh"
 #include "launch.h"
 
@@ -56,30 +56,20 @@ __device__ __forceinline__ float kv4_half(uint32_t w, int hi) {
   return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w)));
 }
 
-// Unit `unit` of KV head h, by a warp.  False when it lies behind all rows of
-// the call, as every later one does: the entry found does not come earlier for
-// a later unit (even where cu_rows is out of order), and the last one's rows
-// have ended or are none.
-__device__ __forceinline__ bool unpack_unit(const Kv4View &src, const int32_t *__restrict__ src_seqs,
-                                            const int64_t *__restrict__ lo, const int32_t *__restrict__ cu_rows, int n,
-                                            long long T, const int32_t *__restrict__ dst_seqs, const KvView &dst,
-                                            long long unit, int h, unsigned *status) {
+// Unit `unit`, of entry C of the call's n, and KV head h, by a warp.  False when it lies
+// behind all rows of the call, as every later one does: the entry found does not
+// come earlier for a later unit (even where cu_rows is out of order), and the last
+// one's rows have ended or are none.
+__device__ __forceinline__ bool unpack_unit(const Kv4View &src, const Chunk &C, int n, long long T,
+                                            const int32_t *__restrict__ dst_seqs, const KvView &dst, long long unit, int h,
+                                            unsigned *status) {
   const int lane = threadIdx.x & 31;
-  // the last entry whose first unit is not past this one
-  int i = 0, hi = n;
-  while (hi - i > 1) {
-    const int mid = i + ((hi - i) >> 1);
-    if ((long long)(cu_rows[mid] >> 4) + 2LL * mid <= unit) i = mid; else hi = mid;
-  }
-  const int c0 = cu_rows[i], c1 = cu_rows[i + 1];
-  if (c0 < 0 || c1 < c0 || c1 > T) {
-    if (lane == 0) flag(status, ST_BAD_ROWS);
-    return i < n - 1;
-  }
-  long long a = lo[i];
-  const int s = src_seqs[i];
+  const ChunkUnits units = CHUNKS_BY_TILE;
+  const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
+  if (rows_odd(c0, c1, T)) return i < n - 1;
+  long long a = C.pos;
   const bool mine = lane == 0 && h == 0;
-  const long long u = unit - ((c0 >> 4) + 2LL * i);
+  const long long u = unit - units.first(c0, i);
   if (u < 0) return true;
   if (c1 == c0) return i < n - 1;
   // an entry that names no source has its rows written as zeros
@@ -192,10 +182,18 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
                       KvView dst, long long units, unsigned *status) {
   pdl_wait();
   pdl_trigger();
+  // rows_check, of one entry a thread (a call at once has 64 threads an entry or more): loaded ahead of the search, so
+  // that both wait once
+  const unsigned mine = blockIdx.x * (K4U_WARPS * 32) + threadIdx.x;
+  int c0 = 0, c1 = 0;
+  if (!ROUND && mine < (unsigned)n) c0 = cu_rows[mine], c1 = cu_rows[mine + 1];
   const unsigned w = blockIdx.x * K4U_WARPS + (threadIdx.x >> 5), first = w / (unsigned)src.hkv;
   int h = (int)(w - first * (unsigned)src.hkv);
+  Chunk C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, first);
+  if (!ROUND && rows_odd(c0, c1, T)) flag(status, ST_BAD_ROWS);
+  if (ROUND) rows_check(cu_rows, n, T, threadIdx.x, K4U_WARPS * 32, status);
   for (long long unit = first; unit < units;) {
-    if (!unpack_unit(src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
+    if (!unpack_unit(src, C, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
     // on by gridDim.x * K4U_WARPS (unit, head) pairs
     const unsigned step = gridDim.x * K4U_WARPS, su = step / (unsigned)src.hkv;
     unit += su;
@@ -204,6 +202,7 @@ __global__ void __launch_bounds__(K4U_WARPS * 32)
       h -= src.hkv;
       ++unit;
     }
+    C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, unit);
   }
 }
 

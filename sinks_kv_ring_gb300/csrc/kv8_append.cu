@@ -19,7 +19,7 @@
 // A CTA takes one tile: two warps half of a head's K rows each, two half of its V
 // dims each, with 16 bytes of codes a lane and store; two of a kind exchange their
 // largest magnitudes through shared memory.  A first warp finds the tile's chunk and
-// rows for all, while the others look at a part of cu_rows each CTA (kv8_rows_check).  A chunk that starts inside a tile finds the rows ahead of it there:
+// rows for all, while the others look at a part of cu_rows each CTA (rows_check).  A chunk that starts inside a tile finds the rows ahead of it there:
 // their V codes share 16 bytes with the new ones and are read in any case, their K
 // codes only where the scale grows.  Large calls take up to four heads of a tile
 // one after the other (MANY), for one search and one look at the RoPE rows; where that
@@ -134,7 +134,7 @@ struct Kv8Append {
   Kv8View dst;
   unsigned *status;
   int heads, per_tile;  // heads of a CTA, CTAs of a tile
-  Kv8Units units;
+  ChunkUnits units;
 };
 
 // Where a warp's tile lies and which of its rows are new.
@@ -405,10 +405,10 @@ __device__ __forceinline__ void kv8_append_v(const Kv8Append &A, const Kv8Item &
 
 // The tile of unit `unit` of the call, by a warp; false: none.
 __device__ __forceinline__ bool append_item(const Kv8Append &A, long long unit, bool say, Kv8Item &I, const int32_t *&entry) {
-  const Kv8Chunk C = kv8_chunk(A.cu_rows, A.P0, A.seqs, A.n, A.units, unit);
+  const Chunk C = chunk_of(A.cu_rows, A.P0, A.seqs, A.n, A.units, unit);
   const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
   const long long a = C.pos;
-  if (kv8_rows_odd(c0, c1, A.T)) return false;
+  if (rows_odd(c0, c1, A.T)) return false;
   const long long u = unit - A.units.first(c0, i);
   if (u < 0 || c1 == c0 || s == -1) return false;
   const bool bs = s < 0 || s >= A.dst.num_seqs;
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(K8A_WARPS * 32, K8A_CTAS) kv8_append_kernel(Kv
     append_item(A, unit, say, I, entry);
     if (lane == 0) s_item = I, s_entry = entry;
   } else {
-    kv8_rows_check(A.cu_rows, A.n, A.T, threadIdx.x - 32, 32 * (K8A_WARPS - 1), A.status);
+    rows_check(A.cu_rows, A.n, A.T, threadIdx.x - 32, 32 * (K8A_WARPS - 1), A.status);
   }
   __syncthreads();
   if (!s_entry) return;
@@ -462,9 +462,9 @@ cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, const int32_
                               const int32_t *seqs, int n, long long T, const float *table, int64_t max_pos,
                               float value_scale, const Kv8View &dst, unsigned *status, cudaStream_t st) {
   if (dst.hkv > (1 << 24)) return cudaErrorInvalidValue;  // (a position alone would be 5 GB)
-  Kv8Append A{k, v, cu_rows, P0, seqs, n, T, table, max_pos, value_scale, dst, status, 1, dst.hkv, KV8_BY_TILE};
+  Kv8Append A{k, v, cu_rows, P0, seqs, n, T, table, max_pos, value_scale, dst, status, 1, dst.hkv, CHUNKS_BY_TILE};
   long long units = (T >> 4) + 2LL * n;  // tiles that the call could have: by row the fewer for chunks of one or two
-  if (T <= units) A.units = KV8_BY_ROW, units = T;  // (256 chunks of one row, 8 KV heads: 7.1 us, by tile 9.0)
+  if (T <= units) A.units = CHUNKS_BY_ROW, units = T;  // (256 chunks of one row, 8 KV heads: 7.1 us, by tile 9.0)
   while (2 * A.heads <= K8A_HEADS && A.heads < dst.hkv &&
          units * ((dst.hkv + 2 * A.heads - 1) / (2 * A.heads)) >= 2LL * K8A_CTAS * num_sms())
     A.heads *= 2;

@@ -4,7 +4,7 @@
 // Value = s u: exact in fp32 (a code of 7 bits, a scale of 8), one rounding to
 // bf16.  Entry i of the call is cu_rows[i+1] - cu_rows[i] positions from lo[i]
 // on.  A work unit is one tile of 16 positions of one KV head, taken by one
-// warp; which entry's it is comes from a search over cu_rows (kv8_chunk), and no
+// warp; which entry's it is comes from a search over cu_rows (chunk_of), and no
 // plan is made first.  A call of more than K8U_ONCE CTAs goes round with fewer of
 // them instead, and a warp stops behind the last entry's rows: a T far above the
 // rows there are (all that a block table spans) costs neither CTAs nor searches
@@ -43,13 +43,13 @@ __device__ __forceinline__ void store32(uint16_t *p, const uint4 &a, const uint4
 // behind all rows of the call, as every later one does: the entry found does not
 // come earlier for a later unit (even where cu_rows is out of order), and the last
 // one's rows have ended or are none.
-__device__ __forceinline__ bool unpack_unit(const Kv8View &src, const Kv8Chunk &C, int n, long long T,
+__device__ __forceinline__ bool unpack_unit(const Kv8View &src, const Chunk &C, int n, long long T,
                                             const int32_t *__restrict__ dst_seqs, const KvView &dst, long long unit, int h,
                                             unsigned *status) {
   const int lane = threadIdx.x & 31;
-  const Kv8Units units = KV8_BY_TILE;
+  const ChunkUnits units = CHUNKS_BY_TILE;
   const int i = C.i, c0 = C.c0, c1 = C.c1, s = C.seq;
-  if (kv8_rows_odd(c0, c1, T)) return i < n - 1;
+  if (rows_odd(c0, c1, T)) return i < n - 1;
   long long a = C.pos;
   const bool mine = lane == 0 && h == 0;
   const long long u = unit - units.first(c0, i);
@@ -153,16 +153,16 @@ __global__ void __launch_bounds__(K8U_WARPS * 32, ROUND ? 2 : 4)
                       KvView dst, long long units, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  // kv8_rows_check, of one entry a thread (a call at once has 64 threads an entry or more): loaded ahead of the search, so
+  // rows_check, of one entry a thread (a call at once has 64 threads an entry or more): loaded ahead of the search, so
   // that both wait once (behind it: a call of one row 2.6 us for 2.2)
   const unsigned mine = blockIdx.x * (K8U_WARPS * 32) + threadIdx.x;
   int c0 = 0, c1 = 0;
   if (!ROUND && mine < (unsigned)n) c0 = cu_rows[mine], c1 = cu_rows[mine + 1];
   const unsigned w = blockIdx.x * K8U_WARPS + (threadIdx.x >> 5), first = w / (unsigned)src.hkv;
   int h = (int)(w - first * (unsigned)src.hkv);
-  Kv8Chunk C = kv8_chunk(cu_rows, lo, src_seqs, n, KV8_BY_TILE, first);
-  if (!ROUND && kv8_rows_odd(c0, c1, T)) flag(status, ST_BAD_ROWS);
-  if (ROUND) kv8_rows_check(cu_rows, n, T, threadIdx.x, K8U_WARPS * 32, status);
+  Chunk C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, first);
+  if (!ROUND && rows_odd(c0, c1, T)) flag(status, ST_BAD_ROWS);
+  if (ROUND) rows_check(cu_rows, n, T, threadIdx.x, K8U_WARPS * 32, status);
   for (long long unit = first; unit < units;) {
     if (!unpack_unit(src, C, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
     // on by gridDim.x * K8U_WARPS (unit, head) pairs
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(K8U_WARPS * 32, ROUND ? 2 : 4)
       h -= src.hkv;
       ++unit;
     }
-    C = kv8_chunk(cu_rows, lo, src_seqs, n, KV8_BY_TILE, unit);
+    C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, unit);
   }
 }
 
