@@ -119,6 +119,13 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A score's unit: the product of a K scale and a query's, held at fp32's greatest number, so that codes of 0 under large keys
+// and queries give 0 (a NaN, of a query that is not finite, stays one).
+__device__ __forceinline__ float score_unit(float ks, float f) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(ks * f), "f"(3.402823466e38f));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return half2_bits(__floats2half2_rn(lo, hi)); }
 
 // The query operands of 16 of a part's rows (row r is head r % G of batch row r / G
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float fs = ks * f[m][e];
+              const float fs = score_unit(ks, f[m][e]);
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
                 float(&x)[4] = S[n][m][nt];
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
           tail[n] = lds128(T[n] + KV8_OFF_TAIL);
           const float ks = __uint_as_float(tail[n].x);
           lv[n] = lg2(__uint_as_float(tail[n].y));
-          const uint64_t fs = mul_f32x2(f32x2(ks, ks), f32x2(f[0], f[1]));
+          const uint64_t fs = f32x2(score_unit(ks, f[0]), score_unit(ks, f[1]));
 #pragma unroll
           for (int h = 0; h < 4; h += 2)
             f32x2_split(mul_f32x2(add_f32x2(f32x2(S[n][h], S[n][h + 1]), f32x2(S2[n][h], S2[n][h + 1])), fs), S[n][h], S[n][h + 1]);

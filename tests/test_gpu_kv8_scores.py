@@ -188,3 +188,23 @@ def test_scores_rise_and_fall(table, n, G, rows):
         q = (torch.randn(rows, G, 192, generator=gen, device=DEV) * 0.1 + u * 14).bfloat16()
         pos = [n - rows + i for i in range(rows)]
         _check(_decode(q, pos, pool, table, n), q, pos, pool, n)
+
+
+@pytest.mark.parametrize("G,rows", [(4, 1), (8, 1), (16, 1), (16, 4)])
+@pytest.mark.parametrize("n,most", [(1, 1), (40, 64), (600, 600), (9000, 9000)])
+@pytest.mark.parametrize("key,query", [(3e38, 3e38), (3e38, 1e25), (1e20, 3e38)])
+def test_large_keys_beside_large_queries(table, key, query, n, most, G, rows):
+    """Keys and queries so large that the product of their scales is past fp32, in dims that do not meet: all scores are 0
+    and the output is the mean of the values."""
+    gen = _gen(n + G)
+    k = torch.zeros(n, 1, 192, device=DEV)
+    k[:, 0, 64:128] = torch.where(torch.rand(n, 64, generator=gen, device=DEV) < 0.5, -key, key)
+    q = torch.zeros(rows, G, 192, device=DEV)
+    q[..., 128:] = query
+    k, q = k.bfloat16(), q.bfloat16()
+    v = torch.randn(n, 1, 128, generator=gen, device=DEV).bfloat16()
+    pool = _pool(gen, k, v, table)
+    if most > n:
+        pool = kvr.Kv8Layout(pool.data, torch.nn.functional.pad(pool.block_table, (0, -(-most // 64) - 1), value=-1))
+    pos = [max(n - rows + i, 0) for i in range(rows)]
+    _check_one_size(_decode(q, pos, pool, table, most), torch.ones_like(q), pos, pool, n, np.ones(n, bool), f"{key} {query}")
