@@ -24,13 +24,20 @@ constexpr ChunkUnits CHUNKS_BY_TILE{4, 2}, CHUNKS_BY_ROW{0, 0};
 // Whether a chunk's rows are out of order, or not among the call's T.
 __device__ __forceinline__ bool rows_odd(int c0, int c1, long long T) { return c0 < 0 || c1 < c0 || c1 > T; }
 // Flags such chunks of a call.  The units may leave one out (no unit is its own, or the search
-// passes it by), so each is looked at by one thread of the grid: thread `me` of a CTA's `all`.
-__device__ __forceinline__ void rows_check(const int32_t *__restrict__ cu, int n, long long T, unsigned me, unsigned all,
-                                               unsigned *status) {
-  for (long long i = (long long)blockIdx.x * all + me; i < n; i += (long long)gridDim.x * all)
+// passes it by), so each is looked at once: by threads `me` of `all` of each of `ctas` CTAs.
+__device__ __forceinline__ void rows_check(const int32_t *__restrict__ cu, int n, long long T, unsigned cta, unsigned ctas,
+                                           unsigned me, unsigned all, unsigned *status) {
+  for (long long i = (long long)cta * all + me; i < n; i += (long long)ctas * all)
     if (rows_odd(cu[i], cu[i + 1], T)) flag(status, ST_BAD_ROWS);
 }
-__device__ __forceinline__ int ones_from_below(unsigned m) { return __clz(__brev(~m)); }
+// Whether unit `unit` lies behind all chunks, by a warp: none of the last 64 ends past it (so up to 64 chunks it holds of all of
+// them, in order or not).
+__device__ __forceinline__ bool behind_chunks(const int32_t *__restrict__ cu, int n, ChunkUnits units, long long unit) {
+  const int i = max(n - (int)(threadIdx.x & 31), 1), j = max(i - 32, 1);
+  return !__any_sync(0xffffffffu, units.first(cu[i], i) > unit || (n > 32 && units.first(cu[j], j) > unit));
+}
+constexpr int CHECK_CHUNKS = 1024;  // that a CTA looks at where CTAs do nothing else
+__device__ __forceinline__ int zeros_from_below(unsigned m) { return __clz(__brev(m)); }  // (32 of none)
 // The chunk that owns unit `unit`, by a warp: a search over cu_rows, and no plan is
 // made first.  A round narrows the chunks down by 32; the last 64 are read whole, with
 // their positions and sequences, so that a batch of up to 64 waits for one load where
@@ -48,8 +55,8 @@ __device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ cu, const 
   while (len > 64) {
     const int step = (len + 31) >> 5, i = lo + lane * step;
     const bool in = lane * step < len;
-    const unsigned m = __ballot_sync(full, in && units.first(in ? cu[i] : 0, i) <= unit);
-    const int last = max(ones_from_below(m), 1) - 1;  // (chunk 0 always counts)
+    const unsigned m = __ballot_sync(full, !(in && units.first(in ? cu[i] : 0, i) <= unit));
+    const int last = max(zeros_from_below(m), 1) - 1;  // (chunk 0 always counts)
     len = min(step, len - last * step);
     lo += last * step;
   }
@@ -58,9 +65,9 @@ __device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ cu, const 
   const int ca = in_a ? cu[ia] : 0, cb = in_b ? cu[ib] : 0, ce = cu[ie];
   const long long pa = in_a ? pos[ia] : 0, pb = in_b ? pos[ib] : 0;
   const int sa = in_a ? seqs[ia] : 0, sb = in_b ? seqs[ib] : 0;
-  const unsigned ma = __ballot_sync(full, in_a && units.first(ca, ia) <= unit);
-  const unsigned mb = __ballot_sync(full, in_b && units.first(cb, ib) <= unit);
-  const int at = max(ma == full ? 32 + ones_from_below(mb) : ones_from_below(ma), 1) - 1, l = at & 31, l1 = (at + 1) & 31;
+  const unsigned ma = __ballot_sync(full, !(in_a && units.first(ca, ia) <= unit));
+  const unsigned mb = __ballot_sync(full, !(in_b && units.first(cb, ib) <= unit));
+  const int at = max(ma ? zeros_from_below(ma) : 32 + zeros_from_below(mb), 1) - 1, l = at & 31, l1 = (at + 1) & 31;
   const int n_a = __shfl_sync(full, ca, l1), n_b = __shfl_sync(full, cb, l1);
   Chunk C;
   C.i = lo + at;

@@ -24,9 +24,12 @@ namespace {
 
 constexpr int K4U_WARPS = 8;
 // Going round takes 16 registers more a thread (600,002 positions of 4 KV heads:
-// 293 us at once, 300 in rounds).  1000 rows of 4 KV heads: 4.6 us with T = 1000,
-// 21 with T = 2^19 and 79 with 2^21 (empty CTAs), 9.5 beyond (in rounds).
+// 293 us at once, 296 in rounds).  1000 rows of 4 KV heads: 3.9 us with T = 1000,
+// 17 with T = 2^19 and 34 with 2^20 (empty CTAs), 5.8 beyond (in rounds).
 constexpr int K4U_ONCE = 1 << 16;
+// CTAs per SM past which a warp asks ahead of the search whether its unit lies behind all rows (1000 rows with T = 2^19 26 us
+// without it, 17 with it; fewer are a wave or two, which would wait for one load more).
+constexpr int K4U_MANY = 8;
 constexpr int K4U_CTAS = 32;  // CTAs per SM of a call that goes round
 
 // The values of a word of codes (dim i in nibble i) as bf16.  A code masked
@@ -179,23 +182,21 @@ template <bool ROUND>
 __global__ void __launch_bounds__(K4U_WARPS * 32)
     kv4_unpack_kernel(Kv4View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
                       const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
-                      KvView dst, long long units, unsigned *status) {
+                      KvView dst, long long units, unsigned ctas, unsigned many, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  // rows_check, of one entry a thread (a call at once has 64 threads an entry or more): loaded ahead of the search, so
-  // that both wait once
-  const unsigned mine = blockIdx.x * (K4U_WARPS * 32) + threadIdx.x;
-  int c0 = 0, c1 = 0;
-  if (!ROUND && mine < (unsigned)n) c0 = cu_rows[mine], c1 = cu_rows[mine + 1];
+  if (blockIdx.x >= ctas) {  // the grid's last CTAs look whether cu_rows is in order, and the others do not wait for it
+    rows_check(cu_rows, n, T, blockIdx.x - ctas, gridDim.x - ctas, threadIdx.x, K4U_WARPS * 32, status);
+    return;
+  }
   const unsigned w = blockIdx.x * K4U_WARPS + (threadIdx.x >> 5), first = w / (unsigned)src.hkv;
   int h = (int)(w - first * (unsigned)src.hkv);
+  if ((ROUND || ctas > many) && behind_chunks(cu_rows, n, CHUNKS_BY_TILE, first)) return;
   Chunk C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, first);
-  if (!ROUND && rows_odd(c0, c1, T)) flag(status, ST_BAD_ROWS);
-  if (ROUND) rows_check(cu_rows, n, T, threadIdx.x, K4U_WARPS * 32, status);
   for (long long unit = first; unit < units;) {
     if (!unpack_unit(src, C, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
-    // on by gridDim.x * K4U_WARPS (unit, head) pairs
-    const unsigned step = gridDim.x * K4U_WARPS, su = step / (unsigned)src.hkv;
+    // on by ctas * K4U_WARPS (unit, head) pairs
+    const unsigned step = ctas * K4U_WARPS, su = step / (unsigned)src.hkv;
     unit += su;
     h += (int)(step - su * (unsigned)src.hkv);
     if (h >= src.hkv) {
@@ -216,8 +217,10 @@ cudaError_t launch_kv4_unpack(const Kv4View &src, const int32_t *src_seqs, const
   if (src.hkv > (1 << 24)) return cudaErrorInvalidValue;  // (a position alone would be 3 GB)
   const bool round = blocks > K4U_ONCE;
   if (round) blocks = (long long)K4U_CTAS * num_sms();
-  return launch_pdl(round ? kv4_unpack_kernel<true> : kv4_unpack_kernel<false>, dim3((unsigned)blocks),
-                    dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, units, status);
+  const long long check = ((long long)n + CHECK_CHUNKS - 1) / CHECK_CHUNKS;
+  return launch_pdl(round ? kv4_unpack_kernel<true> : kv4_unpack_kernel<false>, dim3((unsigned)(blocks + check)),
+                    dim3(K4U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, units, (unsigned)blocks,
+                    (unsigned)(K4U_MANY * num_sms()), status);
 }
 
 }  // namespace kvr

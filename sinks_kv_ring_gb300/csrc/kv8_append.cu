@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(K8A_WARPS * 32, K8A_CTAS) kv8_append_kernel(Kv
     append_item(A, unit, say, I, entry);
     if (lane == 0) s_item = I, s_entry = entry;
   } else {
-    rows_check(A.cu_rows, A.n, A.T, threadIdx.x - 32, 32 * (K8A_WARPS - 1), A.status);
+    rows_check(A.cu_rows, A.n, A.T, blockIdx.x, gridDim.x, threadIdx.x - 32, 32 * (K8A_WARPS - 1), A.status);
   }
   __syncthreads();
   if (!s_entry) return;

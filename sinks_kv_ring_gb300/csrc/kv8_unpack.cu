@@ -8,7 +8,7 @@
 // plan is made first.  A call of more than K8U_ONCE CTAs goes round with fewer of
 // them instead, and a warp stops behind the last entry's rows: a T far above the
 // rows there are (all that a block table spans) costs neither CTAs nor searches
-// (1000 rows of 4 KV heads: 3.5 us with T = 1000, 23 with 2^19, 12 with 2^21 or 2^23).
+// (1000 rows of 4 KV heads: 3.6 us with T = 1000, 17 with 2^19, 7 with 2^21 or 2^23).
 //
 // What bounds it: HBM, 321 bytes in and 640 out per (position, KV head): 122,880
 // positions of 4 KV heads take 72 us, 0.96 of the copy rate.
@@ -20,6 +20,9 @@ namespace {
 
 constexpr int K8U_WARPS = 8;
 constexpr int K8U_ONCE = 1 << 16;
+// CTAs per SM past which a warp asks ahead of the search whether its unit lies behind all rows: 1000 rows with T = 2^19 27 us
+// without it, 17 with it.  A call of fewer is a wave or two, which would wait for one load more.
+constexpr int K8U_MANY = 8;
 constexpr int K8U_CTAS = 32;  // CTAs per SM of a call that goes round
 
 // Values of the four codes of a word, as bf16: (byte 0, 1) and (2, 3).
@@ -150,23 +153,21 @@ template <bool ROUND>
 __global__ void __launch_bounds__(K8U_WARPS * 32, ROUND ? 2 : 4)
     kv8_unpack_kernel(Kv8View src, const int32_t *__restrict__ src_seqs, const int64_t *__restrict__ lo,
                       const int32_t *__restrict__ cu_rows, int n, long long T, const int32_t *__restrict__ dst_seqs,
-                      KvView dst, long long units, unsigned *status) {
+                      KvView dst, long long units, unsigned ctas, unsigned many, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  // rows_check, of one entry a thread (a call at once has 64 threads an entry or more): loaded ahead of the search, so
-  // that both wait once (behind it: a call of one row 2.6 us for 2.2)
-  const unsigned mine = blockIdx.x * (K8U_WARPS * 32) + threadIdx.x;
-  int c0 = 0, c1 = 0;
-  if (!ROUND && mine < (unsigned)n) c0 = cu_rows[mine], c1 = cu_rows[mine + 1];
+  if (blockIdx.x >= ctas) {  // the grid's last CTAs look whether cu_rows is in order, and the others do not wait for it
+    rows_check(cu_rows, n, T, blockIdx.x - ctas, gridDim.x - ctas, threadIdx.x, K8U_WARPS * 32, status);
+    return;
+  }
   const unsigned w = blockIdx.x * K8U_WARPS + (threadIdx.x >> 5), first = w / (unsigned)src.hkv;
   int h = (int)(w - first * (unsigned)src.hkv);
+  if ((ROUND || ctas > many) && behind_chunks(cu_rows, n, CHUNKS_BY_TILE, first)) return;
   Chunk C = chunk_of(cu_rows, lo, src_seqs, n, CHUNKS_BY_TILE, first);
-  if (!ROUND && rows_odd(c0, c1, T)) flag(status, ST_BAD_ROWS);
-  if (ROUND) rows_check(cu_rows, n, T, threadIdx.x, K8U_WARPS * 32, status);
   for (long long unit = first; unit < units;) {
     if (!unpack_unit(src, C, n, T, dst_seqs, dst, unit, h, status) || !ROUND) return;
-    // on by gridDim.x * K8U_WARPS (unit, head) pairs
-    const unsigned step = gridDim.x * K8U_WARPS, su = step / (unsigned)src.hkv;
+    // on by ctas * K8U_WARPS (unit, head) pairs
+    const unsigned step = ctas * K8U_WARPS, su = step / (unsigned)src.hkv;
     unit += su;
     h += (int)(step - su * (unsigned)src.hkv);
     if (h >= src.hkv) {
@@ -187,8 +188,10 @@ cudaError_t launch_kv8_unpack(const Kv8View &src, const int32_t *src_seqs, const
   if (src.hkv > (1 << 24)) return cudaErrorInvalidValue;  // (a position alone would be 5 GB)
   const bool round = blocks > K8U_ONCE;
   if (round) blocks = (long long)K8U_CTAS * num_sms();
-  return launch_pdl(round ? kv8_unpack_kernel<true> : kv8_unpack_kernel<false>, dim3((unsigned)blocks),
-                    dim3(K8U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, units, status);
+  const long long check = ((long long)n + CHECK_CHUNKS - 1) / CHECK_CHUNKS;
+  return launch_pdl(round ? kv8_unpack_kernel<true> : kv8_unpack_kernel<false>, dim3((unsigned)(blocks + check)),
+                    dim3(K8U_WARPS * 32), 0, st, src, src_seqs, lo, cu_rows, n, T, dst_seqs, dst, units, (unsigned)blocks,
+                    (unsigned)(K8U_MANY * num_sms()), status);
 }
 
 }  // namespace kvr

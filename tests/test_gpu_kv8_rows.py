@@ -163,3 +163,33 @@ def test_single_rows_and_what_cannot_be_written(table, n):
     # and with the one in the middle past the rows that there are
     cu[2 if n <= 64 else 70] = n + 1
     _check_append(pool, cu, n, first, hkv, gen, table, kvr.DEV_BAD_ROWS, [0] if n <= 64 else [], seqs, lo, good=1 if n <= 64 else 0)
+
+
+@pytest.mark.parametrize("n,at", [(3, 1), (40, 30), (64, 20), (64, 63)])
+@pytest.mark.parametrize("T", [1 << 12, 1 << 19, (1 << 21) + 5])
+def test_out_of_order_with_far_more_rows_allowed(table, T, n, at):
+    """T far above the rows, and the entries behind the place all below those ahead of it: a unit ahead of it is not taken for
+    one behind all rows.  (At once, at once with most CTAs behind the rows, and in rounds; both quantised pools.)"""
+    gen, hkv, each = _gen(n + at), 4, 50
+    cu = [each * i for i in range(at + 1)] + [3 + i % 2 for i in range(n - at)]
+    good = _served(cu, T)
+    assert good == at
+    seqs = torch.arange(n, dtype=torch.int32, device=DEV)
+    lo = torch.zeros(n, dtype=torch.int64, device=DEV)
+    k, v = _kv(gen, each * n, hkv)
+    whole = torch.arange(n + 1, dtype=torch.int32, device=DEV) * each
+    p8, p4 = (cls.contiguous(n, hkv, 64, block_size=64) for cls in (kvr.Kv8Layout, kvr.Kv4Layout))
+    kvr.kv8_append_rope(k, v, whole, lo, seqs, table, VS, p8)
+    kvr.kv4_append_rope(k, v, torch.arange(each, device=DEV).repeat(n), seqs.repeat_interleave(each), table, VS, p4)
+    for pool, call in ((p8, kvr.kv8_unpack), (p4, kvr.kv4_unpack)):
+        pages = [kvr.PagedLayout.contiguous(n, hkv, 64, block_size=64) for _ in range(2)]
+        for p in pages:
+            p.k.fill_(7)
+            p.v.fill_(7)
+        call(pool, seqs, lo, whole, pages[0], dst_seqs=seqs, T=max(T, each * n))
+        assert kvr.device_status() == 0
+        call(pool, seqs, lo, _ints(cu, torch.int32), pages[1], dst_seqs=seqs, T=T)
+        assert kvr.device_status() & kvr.DEV_BAD_ROWS
+        for a, b in zip(pages[0].tensors()[:2], pages[1].tensors()[:2]):
+            assert torch.equal(a[:good], b[:good])
+        assert (pages[0].k[:, :, each:] == 7).all() and not (pages[0].k[:, :, :each] == 7).all(-1).any()
