@@ -669,6 +669,12 @@ size_t full_attn_decode_kv8_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, i
  * full_attn_decode over an 8-bit pool: the token at pos[b] of sequence seq[b]
  * attends positions 0..pos[b], whose values are the ones the codes stand for.
  * Arguments, bounds, flags, workspace and results as full_attn_decode_kv4.
+ * Neighbouring rows of one sequence (a draft's tokens) read its keys together, up
+ * to 32 query rows of a KV head (4 tokens of up to 8 q heads a KV head, 2 of 16).
+ * A verification of 3 or more tokens at 16 q heads a KV head over long contexts
+ * takes longer than full_attn_prefill_varlen does over bf16 pages (64 sequences of
+ * 4 tokens at 32772, 4 KV heads: 1117 us and 863): where that is the step that
+ * counts, keep the layer in bf16.
  */
 kvr_status full_attn_decode_kv8(const kvr_bf16 *q, const int64_t *pos, const int32_t *seq, int32_t B, int32_t Hq,
                                 const kvr_kv8_layout *pool, const float *rope_cos_sin, int64_t max_pos,
@@ -697,7 +703,9 @@ kvr_status kv8_unpack(const kvr_kv8_layout *src, const int32_t *src_seqs, const 
  * num_blocks <= 2^30 (KVR_EUNSUPPORTED).
  *
  * Calls write only to blocks of their own sequence, so a block that is shared must
- * not be appended to.  A fork sees to it: what it shares is full.  A sequence cut
+ * not be appended to: the appends do not look at refs, so one that did would write
+ * over the other holders' positions, and nothing would be flagged.  A fork sees to
+ * it: what it shares is full.  A sequence cut
  * (kv_pages_free with keep_hi) inside a block that others still hold is forked to
  * a new id at that length before it goes on, which copies the part.  Calls on one
  * table, refs or free list are ordered by the caller (one stream).

@@ -32,16 +32,18 @@
 // warps inside a piece; 8 warps an SM, two CTAs, hold the sums in registers.
 //
 // What bounds it.  321 bytes and 2 (192 + 128) flops a query row per key and KV
-// head.  Long contexts: HBM (batch 64 at 32769 keys, 4 KV heads: 394 us, 6.84 TB/s,
-// 1.0 of the copy rate, at 16 heads a group as at 8; one row of 2^20 keys 197 us).
-// With more query rows a key, the products: 64 x 4 drafts at 32772 keys take 563 us
-// at 8 heads a group (32 query rows a part) and 1108 at 16 (two parts each), where
-// the keys once would take 397; 16 x 2 at 16384 keys and 4 heads 56 us, 99 with each
-// row alone.  A warp needs about 1700 cycles for a tile at 16 query rows,
-// 650 of them the tensor pipe's for its two warps; so a batch that is neither is
-// bound by that and by the set-up of a part (2.4 us from the wait for the kernel
-// ahead to the first product) and the merge: one row of 32769 keys, 4 x 16 heads,
-// 14.2 us.
+// head.  Long contexts: HBM (batch 64 at 32769 keys, 4 KV heads: 387 to 396 us across
+// GPUs, 1.0 of the copy rate, at 16 heads a group as at 8; one row of 2^20 keys 194 to
+// 197 us).  With more query rows a key, a warp's own chain: 64 x 4 drafts at 32772
+// keys take 567 us at 8 heads a group (32 query rows a part) and 1117 at 16 (two
+// parts each), where the keys once would take 397 and the products alone 298 and 596
+// (8.2 cycles each on an SM quarter); two warps a scheduler at 255 registers do not
+// overlap them with the conversions and the softmax (tensor pipe 35%, issue slots
+// 34%).  16 x 2 at 16384 keys and 4 heads 56 us, 99 with each row alone.  A warp needs
+// about 1700 cycles for a tile at 16 query rows, 650 of them the tensor pipe's for its
+// two warps; so a batch that is neither is bound by that and by the set-up of a part
+// (2.4 us from the wait for the kernel ahead to the first product) and the merge: one
+// row of 32769 keys, 4 x 16 heads, 14.1 us.
 //
 // Measured and left out (batch 64 at 32769, 16 heads, when the kernel took 401):
 // query operands in registers 420, three CTAs of 168 registers without the 32-row
@@ -916,7 +918,8 @@ __global__ void __launch_bounds__(K8_WARPS * 32, K8_CTAS) kv8_decode_kernel(K8Ar
 // of 1024, 1 x 4 7.3 / 6.4, 4 x 4 8.4 / 9.6, 64 x 4 22.1 / 26.4; of 256, 1 x 4 6.1 /
 // 6.3, 64 x 4 10.8 / 16.0; of 4096, 4 x 4 14.0 / 12.1, 64 x 4 66.2 / 65.1.  A few rows
 // gain by the whole GPU's warps once eight CTAs have a few tiles each; up to 1024
-// keys that is less than a second launch and a workspace cost the caller.
+// keys that is less than a second launch and a workspace cost a caller from the host.
+// (A captured step does not pay those: 1 x 4 KV heads at 1024 keys costs it 0.9 us.)
 bool one_launch(int B, int hkv, long long max_ctx) {
   const long long units = (max_ctx + K8_UNIT - 1) / K8_UNIT;
   return units <= ((long long)B * hkv < 8 ? 64 : 128);

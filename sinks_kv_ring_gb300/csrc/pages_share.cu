@@ -18,7 +18,8 @@
 // atomics, and of a cluster's barriers.  Giving up 4 beams of 10 blocks and forking
 // them again takes 1.8 and 2.6 us (one CTA; with the cluster 9.3 in all), 128 of up
 // to 257 blocks 4.1 and 6.4 (a cluster of eight; of four 3.7 and 5.3, one CTA 15 and
-// 6.8); compacting 6000 blocks under 96 sequences 5.1, where a plan in global memory
+// 6.8: there four would do better, and all calls have eight, which compaction was
+// measured with and larger pools' counts are spread over); compacting 6000 blocks under 96 sequences 5.1, where a plan in global memory
 // with a barrier between its steps and a second launch for the tables took 13.2.
 #include <cooperative_groups.h>
 
