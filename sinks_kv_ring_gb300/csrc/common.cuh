@@ -88,8 +88,8 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// Packed pairs of fp32 (one instruction each on sm_100+): x * y + z and
-// x + y element-wise, round to nearest, as fmaf / + on each element.
+// Packed pairs of fp32 (one instruction each on sm_100+): x * y + z, x * y and
+// x + y element-wise, round to nearest, as fmaf / * / + on each element (never contracted).
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
